@@ -17,7 +17,9 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libqmm.so")
-SOURCES = ["qmm_api.cu", "qmm_b1.cu", "qmm_b2.cu", "qmm_noalloc.cu", "qmm_attn.cu"]
+SOURCES = ["qmm_api.cu", "qmm_b1.cu", "qmm_b2.cu", "qmm_noalloc.cu", "qmm_attn.cu",
+           "qmm_kv_attend.cu", "qmm_kv_attend_q8.cu", "qmm_kv_attend_f16.cu", "qmm_kv_attend_bf16.cu",
+           "qmm_kv_cache.cu", "qmm_logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -30,7 +32,7 @@ def nvcc() -> str:
 
 def _deps() -> list[str]:
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(INCLUDE, "qmm.h"))
+    files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     return files
 
 

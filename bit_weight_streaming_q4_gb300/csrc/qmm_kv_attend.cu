@@ -1,0 +1,329 @@
+// Attention of new tokens over the paged cache: the joining kernel and the C entries.
+//
+// The split kernel (qmm_kv_attend.cuh) leaves, per chunk and query, M_c, l_c and o_c.  A row's
+// result is out = sum_c w_c o_c / sum_c w_c l_c with w_c = 2^(M_c - max M), its lse the logarithm
+// of that denominator, and a token's weight the sum over queries of 2^(x_t - M) / l.
+#include <cudaTypedefs.h>
+
+#include "qmm_kv_attend.cuh"
+
+namespace qmm {
+namespace kv {
+
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kWeightTokens = 1024;  // slots per block of the weights' part
+
+// Denominator and reference of one query over its chunks: every lane of the warp returns them.
+// Chunks are taken in a fixed order (lane c % 32, then a butterfly), so the value depends on the
+// query alone.
+__device__ __forceinline__ float2 join_ml(const AttendParams& p, int64_t slot0, int n) {
+    const int lane = threadIdx.x & 31;
+    const float2* ml = reinterpret_cast<const float2*>(p.ml) + slot0;
+    float m = kNoMax;
+    for (int c = lane; c < n; c += 32) m = fmaxf(m, ml[static_cast<int64_t>(c) * p.qp].x);
+#pragma unroll
+    for (int k = 16; k >= 1; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+    const float ref = m == kNoMax ? 0.f : m;
+    float l = 0.f;
+    for (int c = lane; c < n; c += 32) {
+        const float2 v = ml[static_cast<int64_t>(c) * p.qp];
+        l = fmaf(v.y, exp2f(v.x - ref), l);
+    }
+#pragma unroll
+    for (int k = 16; k >= 1; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+    return make_float2(m, l);
+}
+
+// Blocks 0 .. rows * heads - 1: one (row, head) each, its chunks dealt to the warps in turn and
+// the warps' sums added in order.  The others: kWeightTokens slots of one (sequence, KV head)
+// each, taken in turn by however many blocks there are.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) attend_join(const AttendParams p, int out_blocks) {
+    extern __shared__ float jsm[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    griddep_wait();  // the split kernel has finished and its partials are visible
+    if (static_cast<int>(blockIdx.x) < out_blocks) {
+        constexpr int E = D / 32;
+        __shared__ int found;
+        const int h = blockIdx.x % p.heads, r = blockIdx.x / p.heads;
+        if (tid == 0) found = -1;
+        __syncthreads();
+        for (int a = tid; a < p.agents; a += kJoinThreads) {
+            const int4 i = p.info[a];
+            if (r >= i.y && r - i.y < i.z) found = i.x < 0 ? -2 : a;  // at most one sequence holds the row
+        }
+        __syncthreads();
+        const int a = found, g = h / p.group;
+        float m = kNoMax, l = 0.f, acc[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[i] = 0.f;
+        if (a == -1 && tid == 0 && h == 0) atomicOr(p.err, kErrRange);
+        if (a >= 0) {
+            const int n = (p.row_len[r] + p.chunk - 1) / p.chunk;
+            const int q = (r - p.info[a].y) * p.group + h % p.group;
+            const int64_t slot0 = static_cast<int64_t>(a * p.kv_heads + g) * p.chunks * p.qp + q;
+            const float2 t = join_ml(p, slot0, n);
+            m = t.x;
+            l = t.y;
+            const float ref = m == kNoMax ? 0.f : m;
+#pragma unroll 4
+            for (int c = warp; c < n; c += kJoinWarps) {
+                const int64_t s = slot0 + static_cast<int64_t>(c) * p.qp;
+                const float w = exp2f(p.ml[2 * s] - ref);
+                const float* o = p.o + s * D + lane * E;
+                float v[E];
+                if constexpr (E == 2) *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(o);
+                else
+#pragma unroll
+                    for (int i = 0; i < E; i += 4) *reinterpret_cast<float4*>(v + i) = *reinterpret_cast<const float4*>(o + i);
+                // (a chunk that the row does not see has w = 0 and o = 0)
+#pragma unroll
+                for (int i = 0; i < E; ++i) acc[i] = fmaf(v[i], w, acc[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < E; ++i) jsm[warp * D + lane * E + i] = acc[i];
+        __syncthreads();
+        if (tid < D) {
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < kJoinWarps; ++w) v += jsm[w * D + tid];
+            v = m == kNoMax ? 0.f : v / l;
+            const int64_t at = static_cast<int64_t>(blockIdx.x) * D + tid;
+            if (p.out_type == QMM_TYPE_F32) static_cast<float*>(p.out)[at] = v;
+            else if (p.out_type == QMM_TYPE_F16) static_cast<__half*>(p.out)[at] = __float2half_rn(v);
+            else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+        }
+        if (tid == 0 && p.lse) p.lse[blockIdx.x] = m == kNoMax ? kNoMax : (m - kShift + log2f(l)) * 0.6931471805599453f;
+        return;
+    }
+
+    // ---- weights: tokens by thread, queries in order
+    float* ref = jsm;           // [qp] M - kShift (the base-2 logarithm's part that l lacks)
+    float* inv = jsm + p.qp;    // [qp] 1 / l
+    const int per = (p.cap + kWeightTokens - 1) / kWeightTokens;
+    const int64_t all = static_cast<int64_t>(p.agents) * p.kv_heads * per;
+    for (int64_t b = blockIdx.x - out_blocks; b < all; b += gridDim.x - out_blocks) {
+        const int ag = static_cast<int>(b / per), t0 = static_cast<int>(b % per) * kWeightTokens;
+        const int4 info = p.info[ag / p.kv_heads];
+        if (t0 >= info.x) continue;  // past the sequence's longest row, or a refused sequence (-1)
+        const int nq = info.z * p.group;
+        __syncthreads();
+        for (int q = warp; q < nq; q += kJoinWarps) {
+            const int n = (p.row_len[info.y + q / p.group] + p.chunk - 1) / p.chunk;
+            const float2 t = join_ml(p, static_cast<int64_t>(ag) * p.chunks * p.qp + q, n);
+            if (lane == 0) {
+                ref[q] = t.x == kNoMax ? 0.f : t.x - kShift;
+                inv[q] = t.x == kNoMax ? 0.f : 1.f / t.y;
+            }
+        }
+        __syncthreads();
+        const int64_t base = static_cast<int64_t>(ag) * p.cap;
+        const float* x0 = p.scores + static_cast<int64_t>(ag) * p.chunks * p.chunk * p.qp;
+        for (int t = t0 + tid; t < t0 + kWeightTokens && t < info.x; t += kJoinThreads) {
+            const float* x = x0 + static_cast<int64_t>(t) * p.qp;
+            float sum = 0.f;
+            int q = 0;
+            for (; q + 4 <= nq; q += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(x + q);
+                sum = fmaf(ex2(v.x - ref[q]), inv[q], sum);
+                sum = fmaf(ex2(v.y - ref[q + 1]), inv[q + 1], sum);
+                sum = fmaf(ex2(v.z - ref[q + 2]), inv[q + 2], sum);
+                sum = fmaf(ex2(v.w - ref[q + 3]), inv[q + 3], sum);
+            }
+            for (; q < nq; ++q) sum = fmaf(ex2(x[q] - ref[q]), inv[q], sum);
+            p.weight_out[base + t] = p.weight_in ? p.weight_in[base + t] + sum : sum;
+        }
+    }
+}
+
+namespace {
+
+// Workers the split is planned for: 8 warps on each of a GB300's 152 SMs.
+constexpr int64_t kWorkers = 152 * kWarps;
+
+// Tokens per chunk, by the dims alone (so that a row's bits are those of any other call): the
+// longest of 1024 .. 64 that gives every worker two items when all sequences are full, and whose
+// pages one warp can hold (32).
+int32_t chunk_of(const qmm_kv_dims& d) {
+    const int64_t cap = int64_t{d.max_pages} * d.page_tokens;
+    for (int32_t c = 1024; c > 64; c >>= 1)
+        if (c <= 32 * d.page_tokens && (cap + c - 1) / c * d.agents * d.kv_heads >= 2 * kWorkers) return c;
+    return 64;
+}
+
+struct Layout {
+    int64_t info, ml, o, scores, bytes;
+    int32_t chunk, chunks, qp;
+};
+
+qmm_status layout(const qmm_kv_dims& d, bool weights, Layout* out) {
+    const int64_t group = d.heads / d.kv_heads;
+    const int64_t q = int64_t{d.max_agent_rows} * group;
+    if (q > kMaxGroupQ) return QMM_ERR_UNSUPPORTED_SHAPE;
+    Layout l = {};
+    l.chunk = chunk_of(d);
+    l.chunks = static_cast<int32_t>((int64_t{d.max_pages} * d.page_tokens + l.chunk - 1) / l.chunk);
+    l.qp = static_cast<int32_t>((q + 7) / 8 * 8);
+    const int64_t groups = int64_t{d.agents} * d.kv_heads;
+    // item numbers, and slots of partials, in 31 bits
+    if (groups * l.chunks > INT32_MAX / l.qp || groups > INT32_MAX / 8) return QMM_ERR_UNSUPPORTED_SHAPE;
+    auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
+    int64_t at = up(int64_t{d.agents} * 16);
+    l.ml = at;
+    at = up(at + groups * l.chunks * l.qp * 8);
+    l.o = at;
+    at = up(at + groups * l.chunks * l.qp * d.head_dim * 4);
+    l.scores = at;
+    if (weights) at = up(at + groups * l.chunks * l.chunk * l.qp * 4);
+    l.bytes = at;
+    *out = l;
+    return QMM_OK;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    }();
+    return fn;
+}
+
+// The pool as rows of head_dim 16-bit elements: boxes of 64 elements (128 bytes, swizzled) x the
+// rows of a tile that lie in one page.
+qmm_status make_map(const qmm_kv_dims& d, const void* pool, CUtensorMap* map) {
+    const int64_t rows = d.pool_pages * d.kv_heads * 2 * d.page_tokens;
+    if (rows > INT32_MAX) return QMM_ERR_UNSUPPORTED_SHAPE;
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+    if (!enc) return QMM_ERR_CUDA;
+    const int tile = 4096 / d.head_dim;
+    const cuuint64_t size[2] = {static_cast<cuuint64_t>(d.head_dim), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t stride[1] = {static_cast<cuuint64_t>(d.head_dim) * 2};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(tile < d.page_tokens ? tile : d.page_tokens)};
+    const cuuint32_t one[2] = {1, 1};
+    const CUresult r = enc(map, d.format == QMM_KV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                           const_cast<void*>(pool), size, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? QMM_OK : QMM_ERR_CUDA;
+}
+
+template <int D>
+cudaError_t launch_join(const AttendParams& p, int sms, cudaStream_t s) {
+    const int out_blocks = p.rows * p.heads;
+    int64_t weight_blocks = 0;
+    if (p.weight_out) {
+        weight_blocks = int64_t{p.agents} * p.kv_heads * ((p.cap + kWeightTokens - 1) / kWeightTokens);
+        if (weight_blocks > sms * 8) weight_blocks = sms * 8;
+    }
+    const int words = kJoinWarps * D > 2 * p.qp ? kJoinWarps * D : 2 * p.qp;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(out_blocks + weight_blocks));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(words) * 4;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attend_join<D>, p, out_blocks);
+}
+
+}  // namespace
+}  // namespace kv
+}  // namespace qmm
+
+extern "C" {
+
+qmm_status qmm_kv_attend_workspace_bytes(const qmm_kv_dims* dims, int32_t weights, int64_t* bytes) {
+    if (!bytes) return QMM_ERR_INVALID_ARG;
+    const qmm_status st = qmm::kv::check_dims(dims);
+    if (st != QMM_OK) return st;
+    qmm::kv::Layout l;
+    const qmm_status sl = qmm::kv::layout(*dims, weights != 0, &l);
+    if (sl == QMM_OK) *bytes = l.bytes;
+    return sl;
+}
+
+qmm_status qmm_kv_attend(const qmm_kv_dims* dims, const void* pool, const int32_t* page_table,
+                         const int32_t* agent_rows, const int32_t* row_len, const void* q, int64_t q_stride,
+                         int64_t rows, float scale, void* out, int32_t out_type, float* lse, const float* weight_in,
+                         float* weight_out, void* workspace, int64_t workspace_bytes, int* err_word, void* stream) {
+    using namespace qmm::kv;
+    qmm_status st = check_dims(dims);
+    if (st != QMM_OK) return st;
+    if (rows < 0 || (weight_in && !weight_out) || out_type < QMM_TYPE_F32 || out_type > QMM_TYPE_BF16)
+        return QMM_ERR_INVALID_ARG;
+    if (rows == 0) return QMM_OK;
+    if (!pool || !page_table || !agent_rows || !row_len || !q || !out || !workspace || !err_word ||
+        q_stride < int64_t{dims->heads} * dims->head_dim)
+        return QMM_ERR_INVALID_ARG;
+    if (rows > (1 << 24) / dims->heads) return QMM_ERR_UNSUPPORTED_SHAPE;
+    Layout l;
+    st = layout(*dims, weight_out != nullptr, &l);
+    if (st != QMM_OK) return st;
+    if (!aligned(pool, 16) || !aligned(q, 16) || q_stride % 8 != 0 || !aligned(out, 16) || !aligned(workspace, 16) ||
+        !aligned(page_table, 4) || !aligned(agent_rows, 4) || !aligned(row_len, 4) || !aligned(lse, 4) || !aligned(weight_in, 4) ||
+        !aligned(weight_out, 4) || !aligned(err_word, 4))
+        return QMM_ERR_MISALIGNED;
+    if (workspace_bytes < l.bytes) return QMM_ERR_SCRATCH_TOO_SMALL;
+    AttendLaunch a = {};
+    int dev = 0;
+    st = check_gpu(&dev, &a.sms);
+    if (st != QMM_OK) return st;
+    if (dims->format != QMM_KV_Q8_0) {
+        st = make_map(*dims, pool, &a.map);
+        if (st != QMM_OK) return st;
+    }
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    AttendParams& p = a.p;
+    p.pool = static_cast<const uint8_t*>(pool);
+    p.table = page_table;
+    p.agent_rows = agent_rows;
+    p.row_len = row_len;
+    p.q = static_cast<const uint16_t*>(q);
+    p.weight_in = weight_in;
+    p.weight_out = weight_out;
+    p.out = out;
+    p.lse = lse;
+    p.info = reinterpret_cast<int4*>(ws + l.info);
+    p.ml = reinterpret_cast<float*>(ws + l.ml);
+    p.o = reinterpret_cast<float*>(ws + l.o);
+    p.scores = weight_out ? reinterpret_cast<float*>(ws + l.scores) : nullptr;
+    p.err = err_word;
+    p.q_stride = q_stride;
+    p.max_pages = dims->max_pages;
+    p.pool_pages = static_cast<int32_t>(dims->pool_pages);
+    p.page_tokens = dims->page_tokens;
+    while ((1 << p.page_shift) < dims->page_tokens) ++p.page_shift;
+    p.heads = dims->heads;
+    p.kv_heads = dims->kv_heads;
+    p.group = dims->heads / dims->kv_heads;
+    p.agents = dims->agents;
+    p.rows = static_cast<int32_t>(rows);
+    p.max_agent_rows = dims->max_agent_rows;
+    p.chunk = l.chunk;
+    p.chunks = l.chunks;
+    p.qp = l.qp;
+    p.cap = dims->max_pages * dims->page_tokens;
+    p.out_type = out_type;
+    p.c2 = scale * 1.4426950408889634f;
+    a.head_dim = dims->head_dim;
+    a.max_q = dims->max_agent_rows * p.group;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = dims->format == QMM_KV_Q8_0  ? launch_attend_q8(a, s)
+                    : dims->format == QMM_KV_F16 ? launch_attend_f16(a, s)
+                                                 : launch_attend_bf16(a, s);
+    if (e == cudaSuccess)
+        e = dims->head_dim == 64    ? launch_join<64>(p, a.sms, s)
+            : dims->head_dim == 128 ? launch_join<128>(p, a.sms, s)
+                                    : launch_join<256>(p, a.sms, s);
+    return e == cudaSuccess ? QMM_OK : QMM_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,13 @@
+// The attention split kernel's instances for QMM_KV_Q8_0 pools (a translation unit of their own: they
+// compile in parallel).
+#include "qmm_kv_attend.cuh"
+
+namespace qmm {
+namespace kv {
+
+cudaError_t launch_attend_q8(const AttendLaunch& a, cudaStream_t s) {
+    return launch_attend_dim<QMM_KV_Q8_0, 128>(a, s);
+}
+
+}  // namespace kv
+}  // namespace qmm

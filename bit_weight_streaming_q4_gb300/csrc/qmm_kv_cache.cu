@@ -1,0 +1,585 @@
+// The paged cache's contents: appending new tokens' K and V, and eviction by accumulated
+// attention weight.
+#include <cooperative_groups.h>
+
+#include "qmm_kv.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace qmm {
+namespace kv {
+
+// ------------------------------------------------------------------------------ append
+// One block per 32 slots of a sequence (aligned in slot numbers, so that a q8_0 group lies in
+// one page) and KV head; a warp per token, lanes over the head dimension.  The rows' bytes bound
+// it (read once, written once); a decode step's few rows cost a launch and one chain of loads.
+// A q8_0 record keeps V dim-major: the block collects its tokens' V quants in shared memory and
+// writes each dim's 32 bytes at once where all 32 slots are new.
+constexpr int kAppendThreads = 256;
+
+struct AppendParams {
+    uint8_t* pool;
+    const int32_t* table;
+    const int32_t* agent_rows;
+    const int32_t* cache_len;
+    const void* src[2];  // K, V
+    int64_t stride[2];   // elements per row
+    float* weight;
+    int32_t* pos;
+    const int32_t* row_pos;
+    int* err;
+    int64_t rec_bytes;
+    int32_t rows, agents, kv_heads, max_pages, pool_pages, page_tokens, cap;
+    int32_t vec;  // rows can be read 4 elements at a time
+};
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+template <>
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// E elements from src, aligned to 4 elements if `vec` (E a multiple of 4) or 2 (E = 2).
+template <typename T, int E>
+__device__ __forceinline__ void load_row(const T* src, int vec, float (&v)[E]) {
+    constexpr int W = E < 4 ? E : 4;
+    if (vec) {
+#pragma unroll
+        for (int i = 0; i < E; i += W) {
+            alignas(sizeof(T) * W) T t[W];
+            if constexpr (sizeof(T) * W == 16) *reinterpret_cast<uint4*>(t) = *reinterpret_cast<const uint4*>(src + i);
+            else if constexpr (sizeof(T) * W == 8) *reinterpret_cast<uint2*>(t) = *reinterpret_cast<const uint2*>(src + i);
+            else *reinterpret_cast<uint32_t*>(t) = *reinterpret_cast<const uint32_t*>(src + i);
+#pragma unroll
+            for (int k = 0; k < W; ++k) v[i + k] = to_f32(t[k]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[i] = to_f32(src[i]);
+    }
+}
+
+template <int FMT>
+__device__ __forceinline__ uint16_t to_16(float v) {
+    if constexpr (FMT == QMM_KV_BF16) return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    else return __half_as_ushort(__float2half_rn(v));
+}
+
+// q8_0 of a 32-dim block held by 8 lanes, 4 dims each: the block's scale (all lanes) and the
+// lane's four quants.  All in fp32, rounded as the header says.
+__device__ __forceinline__ __half quantise(const float (&v)[4], uint32_t& q) {
+    float big = 0.f;
+    bool fine = true;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        big = fmaxf(big, fabsf(v[i]));
+        fine &= fabsf(v[i]) <= 3.4028235e38f;  // false for NaN and infinities
+    }
+#pragma unroll
+    for (int k = 1; k < 8; k <<= 1) {
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, k));
+        fine &= __shfl_xor_sync(0xffffffffu, fine ? 1 : 0, k) != 0;
+    }
+    if (!fine) {
+        q = 0;
+        return __ushort_as_half(0x7FFFu);
+    }
+    const __half d = __float2half_rn(fminf(__fdiv_rn(big, 127.f), 65504.f));
+    const float df = __half2float(d);
+    const float inv = df == 0.f ? 0.f : __frcp_rn(df);
+    q = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float r = fminf(fmaxf(rintf(__fmul_rn(v[i], inv)), -127.f), 127.f);
+        q |= (static_cast<uint32_t>(static_cast<int>(r)) & 0xFFu) << (8 * i);
+    }
+    return d;
+}
+
+template <int FMT, int D, typename T>
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendParams p) {
+    constexpr bool q8 = FMT == QMM_KV_Q8_0;
+    constexpr int E = D / 32;
+    __shared__ int tmp[33], mine[5];
+    __shared__ __align__(16) uint8_t vq[q8 ? 128 * 32 : 16];  // [dim][slot of the group]
+    __shared__ __half vs[q8 ? 4 * 32 : 8];                    // [block][slot]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = blockIdx.y;
+    // this block's sequence and group of slots
+    if (tid == 0) mine[0] = -1;
+    __syncthreads();
+    int before = 0;
+    for (int a0 = 0; a0 < p.agents; a0 += kAppendThreads) {
+        const int a = a0 + tid;
+        int n = 0, r0 = 0, nr = 0, len = 0;
+        if (a < p.agents) {
+            r0 = p.agent_rows[a];
+            nr = p.agent_rows[a + 1] - r0;
+            len = p.cache_len[a];
+            const bool ok = r0 >= 0 && nr >= 0 && nr <= p.rows - r0 && len >= 0 && len <= p.cap && nr <= p.cap - len;
+            if (!ok && blockIdx.x == 0 && g == 0) atomicOr(p.err, kErrRange);
+            if (ok && nr > 0) n = (len + nr - 1) / 32 - len / 32 + 1;
+        }
+        int sum;
+        const int at = before + block_exclusive(n, tmp, &sum);
+        const int i = static_cast<int>(blockIdx.x) - at;
+        if (i >= 0 && i < n) {
+            mine[0] = a;
+            mine[1] = (len / 32 + i) * 32;  // the group's first slot
+            mine[2] = len;
+            mine[3] = len + nr;
+            mine[4] = r0;
+        }
+        before += sum;
+    }
+    __syncthreads();
+    const int a = mine[0];
+    if (a < 0) return;
+    const int base = mine[1], lo = max(mine[2], base), hi = min(mine[3], base + 32), row0 = mine[4] - mine[2];
+
+    for (int t = lo + warp; t < hi; t += kAppendThreads / 32) {
+        const int r = row0 + t;
+        const int pg = p.table[static_cast<int64_t>(a) * p.max_pages + t / p.page_tokens];
+        const bool in = pg >= 0 && pg < p.pool_pages;
+        if (!in && lane == 0) atomicOr(p.err, kErrPage);
+        const int slot = t % p.page_tokens;
+        uint8_t* rec = p.pool + (static_cast<int64_t>(in ? pg : 0) * p.kv_heads + g) * p.rec_bytes;
+        float kv[2][E];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            load_row<T, E>(static_cast<const T*>(p.src[i]) + r * p.stride[i] + g * D + lane * E, p.vec, kv[i]);
+        if (in && lane == 0) {
+            const int64_t at = (static_cast<int64_t>(a) * p.kv_heads + g) * p.cap + t;
+            if (p.weight) p.weight[at] = 0.f;
+            if (p.pos && p.row_pos) p.pos[at] = p.row_pos[r];
+        }
+        if constexpr (q8) {
+            uint32_t q;
+            const __half dk = quantise(kv[0], q);
+            if (in) {
+                *reinterpret_cast<uint32_t*>(rec + slot * 128 + 16 * ((lane >> 2) ^ q8_key(slot)) + 4 * (lane & 3)) = q;
+                if ((lane & 7) == 0) *reinterpret_cast<__half*>(rec + 8192 + slot * 8 + (lane >> 3) * 2) = dk;
+            }
+            const __half dv = quantise(kv[1], q);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vq[(4 * lane + i) * 32 + t - base] = static_cast<uint8_t>(q >> (8 * i));
+            if ((lane & 7) == 0) vs[(lane >> 3) * 32 + t - base] = dv;
+        } else if (in) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint16_t* dst = reinterpret_cast<uint16_t*>(rec) + (i * p.page_tokens + slot) * D + lane * E;
+                alignas(16) uint16_t w[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e) w[e] = to_16<FMT>(kv[i][e]);
+                if constexpr (E == 2) *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<uint32_t*>(w);
+                else if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<uint2*>(w);
+                else *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<uint4*>(w);
+            }
+        }
+    }
+    if constexpr (q8) {
+        __syncthreads();
+        const int pg = p.table[static_cast<int64_t>(a) * p.max_pages + base / 64];  // one page holds the group
+        if (pg < 0 || pg >= p.pool_pages) return;
+        uint8_t* rec = p.pool + (static_cast<int64_t>(pg) * p.kv_heads + g) * p.rec_bytes;
+        const int at = base % 64;
+        if (hi - lo == 32) {
+            const int d = tid >> 1, part = tid & 1;
+            *reinterpret_cast<uint4*>(rec + 8704 + d * 64 + at + 16 * part) = *reinterpret_cast<const uint4*>(vq + d * 32 + 16 * part);
+        } else {
+            for (int i = tid; i < 128 * (hi - lo); i += kAppendThreads) {
+                const int d = i & 127, t = lo - base + (i >> 7);
+                rec[8704 + d * 64 + at + t] = vq[d * 32 + t];
+            }
+        }
+        for (int i = tid; i < 4 * (hi - lo); i += kAppendThreads) {
+            const int b = i & 3, t = lo - base + (i >> 2);
+            *reinterpret_cast<__half*>(rec + 16896 + (b * 64 + at + t) * 2) = vs[b * 32 + t];
+        }
+    }
+}
+
+template <int FMT, int D>
+cudaError_t launch_append(const AppendParams& p, int32_t type, cudaStream_t s) {
+    const dim3 grid(static_cast<unsigned>(p.rows / 32 + 2 * (p.agents < p.rows ? p.agents : p.rows)),
+                    static_cast<unsigned>(p.kv_heads));
+    if (type == QMM_TYPE_F32) kv_append_kernel<FMT, D, float><<<grid, kAppendThreads, 0, s>>>(p);
+    else if (type == QMM_TYPE_F16) kv_append_kernel<FMT, D, __half><<<grid, kAppendThreads, 0, s>>>(p);
+    else kv_append_kernel<FMT, D, __nv_bfloat16><<<grid, kAppendThreads, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <int FMT>
+cudaError_t launch_append_dim(const AppendParams& p, int32_t dim, int32_t type, cudaStream_t s) {
+    return dim == 64 ? launch_append<FMT, 64>(p, type, s) : dim == 128 ? launch_append<FMT, 128>(p, type, s) : launch_append<FMT, 256>(p, type, s);
+}
+
+// ------------------------------------------------------------------------------ evict
+// One cluster per (sequence, KV head), its slots cut evenly among the cluster's blocks.  The
+// keep-th largest key is found by a radix select over 11 + 11 + 10 bits: each pass counts the
+// digit of the keys that still match, the blocks add their counts through distributed shared
+// memory, and every block picks the same digit.  Then each block walks its slots in order: ties
+// at the threshold are kept from the lowest slot on, kept slots below the budget stay, freed ones
+// and kept ones past the budget go to two lists in slot order (positions by prefix sums over the
+// cluster), and the cluster moves the i-th of the second to the i-th of the first.  Reads are
+// the weights and positions (keys stay in shared memory while they fit), and each moved token
+// once; with the order of slots given up, nothing else has to move.
+constexpr int kEvictThreads = 512;
+constexpr int kBins = 2048;
+constexpr int kKeyCap = 16384;  // keys a block holds in shared memory
+
+struct EvictParams {
+    uint8_t* pool;
+    const int32_t* table;
+    const int32_t* cache_len;
+    const int32_t* keep;
+    const int32_t* protect_from;
+    const float* weight;
+    const int32_t* pos;
+    float* weight_out;
+    int32_t* pos_out;
+    int32_t* len_out;
+    int32_t* lists;  // [sequence][KV head][2][half]: freed slots, tokens to move into them
+    int* err;
+    int64_t rec_bytes, half;
+    int32_t sink, kv_heads, max_pages, pool_pages, page_tokens, cap, head_dim, key_cap;
+};
+
+// Keys in the order of eviction's preference: protected tokens above every weight, then the
+// weights (-0 as +0), NaN below every other.
+__device__ __forceinline__ uint32_t evict_key(float w, int32_t pos, int32_t sink, int32_t from) {
+    if (pos < sink || pos >= from) return 0xFFFFFFFFu;
+    if (w != w) return 0u;
+    const uint32_t u = __float_as_uint(w + 0.f);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+template <bool q8>
+__global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictParams p) {
+    extern __shared__ uint32_t keys[];  // [key_cap]
+    __shared__ int hist[kBins];
+    __shared__ int tmp[33], pick[2], counts[3];
+    cg::cluster_group cl = cg::this_cluster();
+    const int ranks = cl.num_blocks(), rank = cl.block_rank();
+    const int ag = blockIdx.x / ranks, a = ag / p.kv_heads, g = ag % p.kv_heads;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int len = p.cache_len[a], want = p.keep[a];
+    const bool ok = len >= 0 && len <= p.cap;
+    const int n = ok ? len : 0, budget = want >= 0 && want < n ? want : n;
+    if (rank == 0 && g == 0 && tid == 0) {
+        p.len_out[a] = ok ? budget : len;
+        if (!ok) atomicOr(p.err, kErrRange);
+    }
+    const int64_t base = static_cast<int64_t>(ag) * p.cap;
+    const int per = (n + ranks - 1) / ranks, s0 = min(n, rank * per), s1 = min(n, s0 + per);
+    if (budget == n) {  // nothing to evict (the whole cluster agrees)
+        for (int t = s0 + tid; t < s1; t += kEvictThreads) {
+            p.weight_out[base + t] = p.weight[base + t];
+            p.pos_out[base + t] = p.pos[base + t];
+        }
+        return;
+    }
+    if (budget == 0) return;  // everything goes
+    const int from = p.protect_from ? p.protect_from[a] : INT32_MAX;
+    const bool cached = per <= p.key_cap;
+    auto make = [&](int t) { return evict_key(p.weight[base + t], p.pos[base + t], p.sink, from); };
+    auto key = [&](int t) { return cached ? keys[t - s0] : make(t); };
+    if (cached)
+        for (int t = s0 + tid; t < s1; t += kEvictThreads) keys[t - s0] = make(t);
+
+    // ---- the threshold: the key of which `need` are kept, everything above it being kept too
+    uint32_t prefix = 0, mask = 0;
+    int need = budget;
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
+        for (int i = tid; i < kBins; i += kEvictThreads) hist[i] = 0;
+        __syncthreads();
+        for (int t = s0 + tid; t < s1; t += kEvictThreads) {
+            const uint32_t k = key(t);
+            if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1);
+        }
+        cl.sync();
+        // the thread's four bins, from the highest down
+        int c[4], mine = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int b = kBins - 1 - (4 * tid + i);
+            c[i] = 0;
+            for (int r = 0; r < ranks; ++r) c[i] += cl.map_shared_rank(hist, r)[b];
+            mine += c[i];
+        }
+        int total;
+        int above = block_exclusive(mine, tmp, &total);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (above < need && above + c[i] >= need) {  // one bin of the block's
+                pick[0] = kBins - 1 - (4 * tid + i);
+                pick[1] = need - above;
+            }
+            above += c[i];
+        }
+        cl.sync();  // (also: every block has read the counts before they are cleared)
+        prefix |= static_cast<uint32_t>(pick[0]) << shift;
+        mask |= static_cast<uint32_t>(bins - 1) << shift;
+        need = pick[1];
+        __syncthreads();
+    }
+    const uint32_t thr = prefix;
+
+    // ---- per block: ties, then (with the cluster's ties before it known) freed and moved slots
+    int ties = 0;
+    for (int t = s0 + tid; t < s1; t += kEvictThreads) ties += key(t) == thr;
+    int all;
+    block_exclusive(ties, tmp, &all);
+    if (tid == 0) counts[0] = all;
+    cl.sync();
+    int tie0 = 0;
+    for (int r = 0; r < rank; ++r) tie0 += cl.map_shared_rank(counts, r)[0];
+    int hole0 = 0, move0 = 0, moved = 0;
+    int32_t* holes = p.lists + static_cast<int64_t>(ag) * 2 * p.half;
+    int32_t* moves = holes + p.half;
+    for (int round = 0; round < 2; ++round) {  // counting, then writing
+        int tie = tie0, h = hole0, m = move0;
+        for (int t0 = s0; t0 < s1; t0 += kEvictThreads) {
+            const int t = t0 + tid;
+            const uint32_t k = t < s1 ? key(t) : 0u;
+            int sum;
+            const bool equal = t < s1 && k == thr;
+            const int before = tie + block_exclusive(equal, tmp, &sum);
+            tie += sum;
+            const bool kept = t < s1 && (k > thr || (equal && before < need));
+            const bool hole = t < s1 && t < budget && !kept, move = kept && t >= budget;
+            // holes and moves in one prefix sum: neither passes 512 in a step
+            const int at = block_exclusive((hole ? 1 : 0) | (move ? 1 << 16 : 0), tmp, &sum);
+            if (round == 1) {
+                if (hole) holes[h + (at & 0xFFFF)] = t;
+                if (move) moves[m + (at >> 16)] = t;
+                if (kept && t < budget) {
+                    p.weight_out[base + t] = p.weight[base + t];
+                    p.pos_out[base + t] = p.pos[base + t];
+                }
+            }
+            h += sum & 0xFFFF;
+            m += sum >> 16;
+        }
+        if (round == 0) {
+            if (tid == 0) {
+                counts[1] = h;
+                counts[2] = m;
+            }
+            cl.sync();
+            for (int r = 0; r < ranks; ++r) {
+                const int* c = cl.map_shared_rank(counts, r);
+                if (r < rank) {
+                    hole0 += c[1];
+                    move0 += c[2];
+                }
+                moved += c[2];
+            }
+        }
+    }
+    cl.sync();  // the lists are written, the arrays read, and no block's counts are needed any more
+
+    // ---- the moves: source slots >= budget > destination slots
+    const int step = ranks * kEvictThreads, first = rank * kEvictThreads + tid;
+    for (int i = first; i < moved; i += step) {
+        const int src = moves[i], dst = holes[i];
+        p.weight_out[base + dst] = p.weight[base + src];
+        p.pos_out[base + dst] = p.pos[base + src];
+    }
+    const int32_t* table = p.table + static_cast<int64_t>(a) * p.max_pages;
+    auto record = [&](int t) -> uint8_t* {
+        const int pg = table[t / p.page_tokens];
+        if (pg < 0 || pg >= p.pool_pages) {
+            atomicOr(p.err, kErrPage);
+            return nullptr;
+        }
+        return p.pool + (static_cast<int64_t>(pg) * p.kv_heads + g) * p.rec_bytes;
+    };
+    if constexpr (q8) {
+        // a warp moves 32 tokens at a time, a lane each: sources and destinations both rise with
+        // the lane, so the strided bytes of V share their sectors
+        for (int i0 = (first & ~31); i0 < moved; i0 += step) {
+            const int i = i0 + lane;
+            const bool in = i < moved;
+            const int src = in ? moves[i] : 0, dst = in ? holes[i] : 0;
+            const uint8_t* from_rec = in ? record(src) : nullptr;
+            uint8_t* to_rec = in ? record(dst) : nullptr;
+            if (!from_rec || !to_rec) continue;
+            const int ss = src & 63, ds = dst & 63;
+            uint4 row[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) row[c] = *reinterpret_cast<const uint4*>(from_rec + ss * 128 + 16 * (c ^ q8_key(ss)));
+#pragma unroll
+            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(to_rec + ds * 128 + 16 * (c ^ q8_key(ds))) = row[c];
+            *reinterpret_cast<uint2*>(to_rec + 8192 + ds * 8) = *reinterpret_cast<const uint2*>(from_rec + 8192 + ss * 8);
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                *reinterpret_cast<uint16_t*>(to_rec + 16896 + (b * 64 + ds) * 2) =
+                    *reinterpret_cast<const uint16_t*>(from_rec + 16896 + (b * 64 + ss) * 2);
+#pragma unroll 1
+            for (int d = 0; d < 128; d += 16) {
+                uint8_t v[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] = from_rec[8704 + (d + k) * 64 + ss];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) to_rec[8704 + (d + k) * 64 + ds] = v[k];
+            }
+        }
+    } else {
+        // 16-byte pieces of the tokens' K and V rows, consecutive pieces by consecutive threads
+        const int row = p.head_dim * 2, shift = p.head_dim == 64 ? 4 : p.head_dim == 128 ? 5 : 6, pieces = 1 << shift;
+        const int64_t work = static_cast<int64_t>(moved) << shift;
+#pragma unroll 4
+        for (int64_t i = first; i < work; i += step) {
+            const int tok = static_cast<int>(i >> shift), c = static_cast<int>(i & (pieces - 1));
+            const int src = moves[tok], dst = holes[tok];
+            const uint8_t* from_rec = record(src);
+            uint8_t* to_rec = record(dst);
+            if (!from_rec || !to_rec) continue;
+            const int half = c >= pieces / 2, off = (c - half * (pieces / 2)) * 16;
+            *reinterpret_cast<uint4*>(to_rec + (half * p.page_tokens + dst % p.page_tokens) * row + off) =
+                *reinterpret_cast<const uint4*>(from_rec + (half * p.page_tokens + src % p.page_tokens) * row + off);
+        }
+    }
+}
+
+namespace {
+
+int64_t list_half(const qmm_kv_dims& d) { return int64_t{d.max_pages} * d.page_tokens / 2 + 1; }
+
+}  // namespace
+}  // namespace kv
+}  // namespace qmm
+
+extern "C" {
+
+qmm_status qmm_kv_append(const qmm_kv_dims* dims, void* pool, const int32_t* page_table,
+                         const int32_t* agent_rows, const int32_t* cache_len, const void* k, int64_t k_stride,
+                         const void* v, int64_t v_stride, int32_t type, int64_t rows, float* weight, int32_t* pos,
+                         const int32_t* row_pos, int* err_word, void* stream) {
+    using namespace qmm::kv;
+    qmm_status st = check_dims(dims);
+    if (st != QMM_OK) return st;
+    if (rows < 0 || type < QMM_TYPE_F32 || type > QMM_TYPE_BF16) return QMM_ERR_INVALID_ARG;
+    if (rows == 0) return QMM_OK;
+    const int64_t width = int64_t{dims->kv_heads} * dims->head_dim;
+    if (!pool || !page_table || !agent_rows || !cache_len || !k || !v || !err_word || k_stride < width || v_stride < width)
+        return QMM_ERR_INVALID_ARG;
+    if (rows > (1 << 24)) return QMM_ERR_UNSUPPORTED_SHAPE;
+    const int size = type == QMM_TYPE_F32 ? 4 : 2;
+    if (!aligned(pool, 16) || !aligned(page_table, 4) || !aligned(agent_rows, 4) || !aligned(cache_len, 4) || !aligned(k, size) ||
+        !aligned(v, size) || !aligned(weight, 4) || !aligned(pos, 4) || !aligned(row_pos, 4) || !aligned(err_word, 4))
+        return QMM_ERR_MISALIGNED;
+    int dev = 0, sms = 0;
+    st = check_gpu(&dev, &sms);
+    if (st != QMM_OK) return st;
+    AppendParams p = {};
+    p.pool = static_cast<uint8_t*>(pool);
+    p.table = page_table;
+    p.agent_rows = agent_rows;
+    p.cache_len = cache_len;
+    p.src[0] = k;
+    p.src[1] = v;
+    p.stride[0] = k_stride;
+    p.stride[1] = v_stride;
+    p.weight = weight;
+    p.pos = pos;
+    p.row_pos = row_pos;
+    p.err = err_word;
+    p.rec_bytes = record_bytes(*dims);
+    p.rows = static_cast<int32_t>(rows);
+    p.agents = dims->agents;
+    p.kv_heads = dims->kv_heads;
+    p.max_pages = dims->max_pages;
+    p.pool_pages = static_cast<int32_t>(dims->pool_pages);
+    p.page_tokens = dims->page_tokens;
+    p.cap = dims->max_pages * dims->page_tokens;
+    p.vec = aligned(k, 16) && aligned(v, 16) && k_stride * size % 16 == 0 && v_stride * size % 16 == 0;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dims->format == QMM_KV_Q8_0  ? launch_append<QMM_KV_Q8_0, 128>(p, type, s)
+                          : dims->format == QMM_KV_F16 ? launch_append_dim<QMM_KV_F16>(p, dims->head_dim, type, s)
+                                                       : launch_append_dim<QMM_KV_BF16>(p, dims->head_dim, type, s);
+    return e == cudaSuccess ? QMM_OK : QMM_ERR_CUDA;
+}
+
+qmm_status qmm_kv_evict_workspace_bytes(const qmm_kv_dims* dims, int64_t* bytes) {
+    if (!bytes) return QMM_ERR_INVALID_ARG;
+    const qmm_status st = qmm::kv::check_dims(dims);
+    if (st != QMM_OK) return st;
+    *bytes = int64_t{dims->agents} * dims->kv_heads * 2 * qmm::kv::list_half(*dims) * 4;
+    return QMM_OK;
+}
+
+qmm_status qmm_kv_evict(const qmm_kv_dims* dims, void* pool, const int32_t* page_table, const int32_t* cache_len,
+                        const int32_t* keep, int32_t sink, const int32_t* protect_from, const float* weight,
+                        const int32_t* pos, float* weight_out, int32_t* pos_out, int32_t* len_out, void* workspace,
+                        int64_t workspace_bytes, int* err_word, void* stream) {
+    using namespace qmm::kv;
+    int64_t need = 0;
+    qmm_status st = qmm_kv_evict_workspace_bytes(dims, &need);
+    if (st != QMM_OK) return st;
+    if (!pool || !page_table || !cache_len || !keep || !weight || !pos || !weight_out || !pos_out || !len_out ||
+        len_out == cache_len || !workspace || !err_word)
+        return QMM_ERR_INVALID_ARG;
+    if (!aligned(pool, 16) || !aligned(workspace, 16) || !aligned(page_table, 4) || !aligned(cache_len, 4) || !aligned(keep, 4) ||
+        !aligned(protect_from, 4) || !aligned(weight, 4) || !aligned(pos, 4) || !aligned(weight_out, 4) || !aligned(pos_out, 4) ||
+        !aligned(len_out, 4) || !aligned(err_word, 4))
+        return QMM_ERR_MISALIGNED;
+    if (workspace_bytes < need) return QMM_ERR_SCRATCH_TOO_SMALL;
+    int dev = 0, sms = 0;
+    st = check_gpu(&dev, &sms);
+    if (st != QMM_OK) return st;
+    EvictParams p = {};
+    p.pool = static_cast<uint8_t*>(pool);
+    p.table = page_table;
+    p.cache_len = cache_len;
+    p.keep = keep;
+    p.protect_from = protect_from;
+    p.weight = weight;
+    p.pos = pos;
+    p.weight_out = weight_out;
+    p.pos_out = pos_out;
+    p.len_out = len_out;
+    p.lists = static_cast<int32_t*>(workspace);
+    p.err = err_word;
+    p.rec_bytes = record_bytes(*dims);
+    p.half = list_half(*dims);
+    p.sink = sink;
+    p.kv_heads = dims->kv_heads;
+    p.max_pages = dims->max_pages;
+    p.pool_pages = static_cast<int32_t>(dims->pool_pages);
+    p.page_tokens = dims->page_tokens;
+    p.cap = dims->max_pages * dims->page_tokens;
+    p.head_dim = dims->head_dim;
+    const int64_t groups = int64_t{dims->agents} * dims->kv_heads;
+    // blocks per cluster: as many as the longest sequence can use, up to 8 (the portable limit)
+    int ranks = 1;
+    while (ranks < 8 && p.cap > ranks * 512) ranks *= 2;
+    const int64_t per = (p.cap + ranks - 1) / ranks;
+    p.key_cap = static_cast<int32_t>(per < kKeyCap ? per : kKeyCap);
+    if (groups * ranks > INT32_MAX) return QMM_ERR_UNSUPPORTED_SHAPE;
+    const bool q8 = dims->format == QMM_KV_Q8_0;
+    cudaError_t e = q8 ? cudaFuncSetAttribute(kv_evict_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyCap * 4)
+                       : cudaFuncSetAttribute(kv_evict_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyCap * 4);
+    if (e == cudaSuccess) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(groups * ranks));
+        cfg.blockDim = dim3(kEvictThreads);
+        cfg.dynamicSmemBytes = static_cast<size_t>(p.key_cap) * 4;
+        cfg.stream = static_cast<cudaStream_t>(stream);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = q8 ? cudaLaunchKernelEx(&cfg, kv_evict_kernel<true>, p) : cudaLaunchKernelEx(&cfg, kv_evict_kernel<false>, p);
+    }
+    return e == cudaSuccess ? QMM_OK : QMM_ERR_CUDA;
+}
+
+}  // extern "C"
