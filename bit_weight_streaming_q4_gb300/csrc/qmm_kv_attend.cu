@@ -119,20 +119,18 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join(const AttendParams p
             }
         }
         __syncthreads();
-        const int64_t base = static_cast<int64_t>(ag) * p.cap;
-        const float* x0 = p.scores + static_cast<int64_t>(ag) * p.chunks * p.chunk * p.qp;
+        const int64_t base = static_cast<int64_t>(ag) * p.cap, plane = static_cast<int64_t>(p.chunks) * p.chunk;
+        const float4* x0 = reinterpret_cast<const float4*>(p.scores) + ag * (p.qp >> 2) * plane;
         for (int t = t0 + tid; t < t0 + kWeightTokens && t < info.x; t += kJoinThreads) {
-            const float* x = x0 + static_cast<int64_t>(t) * p.qp;
             float sum = 0.f;
-            int q = 0;
-            for (; q + 4 <= nq; q += 4) {
-                const float4 v = *reinterpret_cast<const float4*>(x + q);
+#pragma unroll 4
+            for (int q = 0; q < nq; q += 4) {
+                const float4 v = __ldcs(x0 + (q >> 2) * plane + t);
                 sum = fmaf(ex2(v.x - ref[q]), inv[q], sum);
-                sum = fmaf(ex2(v.y - ref[q + 1]), inv[q + 1], sum);
-                sum = fmaf(ex2(v.z - ref[q + 2]), inv[q + 2], sum);
-                sum = fmaf(ex2(v.w - ref[q + 3]), inv[q + 3], sum);
+                if (q + 1 < nq) sum = fmaf(ex2(v.y - ref[q + 1]), inv[q + 1], sum);
+                if (q + 2 < nq) sum = fmaf(ex2(v.z - ref[q + 2]), inv[q + 2], sum);
+                if (q + 3 < nq) sum = fmaf(ex2(v.w - ref[q + 3]), inv[q + 3], sum);
             }
-            for (; q < nq; ++q) sum = fmaf(ex2(x[q] - ref[q]), inv[q], sum);
             p.weight_out[base + t] = p.weight_in ? p.weight_in[base + t] + sum : sum;
         }
     }
@@ -140,8 +138,8 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join(const AttendParams p
 
 namespace {
 
-// Workers the split is planned for: 8 warps on each of a GB300's 152 SMs.
-constexpr int64_t kWorkers = 152 * kWarps;
+// Blocks the split is planned for: 4 on each of a GB300's 152 SMs.
+constexpr int64_t kWorkers = 152 * 4;
 
 // Tokens per chunk, by the dims alone (so that a row's bits are those of any other call): the
 // longest of 1024 .. 64 that gives every worker two items when all sequences are full, and whose
@@ -201,7 +199,7 @@ qmm_status make_map(const qmm_kv_dims& d, const void* pool, CUtensorMap* map) {
     if (rows > INT32_MAX) return QMM_ERR_UNSUPPORTED_SHAPE;
     const PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
     if (!enc) return QMM_ERR_CUDA;
-    const int tile = 4096 / d.head_dim;
+    const int tile = kTile;
     const cuuint64_t size[2] = {static_cast<cuuint64_t>(d.head_dim), static_cast<cuuint64_t>(rows)};
     const cuuint64_t stride[1] = {static_cast<cuuint64_t>(d.head_dim) * 2};
     const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(tile < d.page_tokens ? tile : d.page_tokens)};

@@ -4,12 +4,18 @@
 //   out = sum_t 2^(x_t - M) v_t / l,   l = sum_t 2^(x_t - M),   M = max_t x_t,   t < row_len[r].
 // A sequence's slots are cut into chunks of p.chunk tokens at fixed places, so what a row
 // gets never depends on the other rows of the call.  Each (sequence, chunk, KV head, tile of
-// 8 NT queries) is an item, and each warp of the persistent grid takes items on its own: it
-// streams the item's K and V tiles through a private ring of three half tiles (one K or V
-// part each), keeps a running maximum, denominator and output per query in registers, and
-// writes them as the item's partial.  Nothing is shared between warps but the table of
-// sequences, so no barrier stands in the loop, and the ring runs on across items: the next
-// item's first tiles are in flight while the last one is summed.
+// 8 NT queries) is an item; the blocks of a persistent grid take items in turn, keep running
+// maxima, denominators and outputs in registers, and write them as the item's partial.  All
+// queries of a tile share each K and V tile on chip, so the cache is read once for up to 48.
+//
+// A block's four warps work on tiles of 64 tokens: each forms the scores of 16 tokens for all
+// queries, the maxima meet in shared memory, the probabilities go there as the second
+// product's operand, and each warp then sums over all 64 tokens for a quarter of the dims.
+// So a thread holds the outputs of D / 4 dims only, and three or four blocks fit an SM: their
+// barriers (two a tile) and loads overlap.  K and V parts stream through a ring of half tiles by bulk copies; the
+// ring runs on across items.  (A first version gave every warp a ring and whole outputs of
+// its own, without barriers: at 24 queries it needed 255 registers, spilled, and with two
+// warps per scheduler waited on everything; 275 us for the case that takes %Q8% us now.)
 //
 // Both products run on mma.sync m16n8k16 with tokens (S^T = K Q^T) and then dims
 // (O^T = V^T P^T) as the 16 rows and queries as the 8 columns: one new token of a group of
@@ -20,8 +26,8 @@
 // since the cache's bytes bound it.  p carries a factor 2^kShift (the
 // denominator too), so that small probabilities stay clear of fp16's subnormals.
 //
-// 16-bit pools: a tile is 8 KB (64, 32 or 16 tokens), loaded by 2-D bulk tensor copies with
-// the 128-byte swizzle, which makes the ldmatrix reads conflict-free.  q8_0 pools: a tile is
+// 16-bit pools: half tiles are loaded by 2-D bulk tensor copies with the 128-byte swizzle,
+// which makes the ldmatrix reads conflict-free.  q8_0 pools: a tile is
 // one record; the K quants are exact in fp16, each 32-dim block's partial sum gets its scale
 // in fp32.  V's scale depends on token and block and so goes into P: a token's exponent
 // e_t = max over blocks of its scales' exponents joins the softmax's reference
@@ -37,8 +43,9 @@
 namespace qmm {
 namespace kv {
 
-constexpr int kWarps = 8;
-constexpr int kSlots = 3;            // half tiles in flight per warp
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kTile = 64;            // tokens per tile
 constexpr float kShift = 13.f;       // p's power of two: p^ <= 2^13, times a scale < 4 <= 2^15
 constexpr float kNoMax = -INFINITY;
 
@@ -54,7 +61,7 @@ struct AttendParams {
     float* lse;                 // [rows][heads] or null
     float* ml;                  // [sequence][KV head][chunk][qp][2]: M and l
     float* o;                   // [sequence][KV head][chunk][qp][D]
-    float* scores;              // [sequence][KV head][chunks * chunk][qp], x_t; null without weights
+    float* scores;              // [sequence][KV head][qp / 4][chunks * chunk][4], x_t; null without weights
     int4* info;                 // [agents]: longest row (-1: refused), first row, rows, 0
     int* err;
     int64_t q_stride;
@@ -68,22 +75,31 @@ struct AttendParams {
     float c2;                   // scale * log2(e)
 };
 
-template <int FMT, int D>
+template <int FMT, int D, int NT>
 struct Geo {
     static constexpr bool q8 = FMT == QMM_KV_Q8_0;
-    static constexpr int TT = q8 ? 64 : 4096 / D;         // tokens per tile
-    static constexpr int HB = q8 ? kQ8Half : TT * D * 2;  // bytes of a half tile
-    static constexpr int JB = TT >= 32 ? 2 : 1;           // blocks of 16 tokens per softmax step
-    static constexpr int SUB = TT / (16 * JB);            // softmax steps per tile
-    static constexpr int MT = D / 16;
-    static constexpr int max_nt = D == 256 ? 2 : 3;       // column tiles whose state fits the registers
+    static constexpr int QT = 8 * NT;                        // queries of a tile
+    static constexpr int HB = q8 ? kQ8Half : kTile * D * 2;  // bytes of a half tile (K or V)
+    static constexpr int slots = q8 ? 4 : 3;                 // half tiles in flight
+    static constexpr int KS = D / 16;
+    static constexpr int MW = D / 64;                        // m16 tiles of dims per warp
+    // halves per row of P and bytes per row of Q, for conflict-free reads: 8-byte (P) and 16-byte
+    // (Q) loads of the q8_0 layout, ldmatrix otherwise
+    static constexpr int PS = q8 ? kTile + 4 : kTile + 8;
+    static constexpr int QS = q8 ? 2 * D + 64 : 2 * D + 16;
+    // blocks per SM that the registers are limited for (D = 256: the ring alone takes 96 KB)
+    static constexpr int blocks = D == 256 ? 2 : NT == 6 ? 3 : 4;
+    // dynamic shared memory, after aligning to 1024: ring, Q, P (hi, lo), 2^-e, maxima, lengths, barriers
+    static constexpr int off_q = slots * HB;
+    static constexpr int off_p = off_q + QT * QS;
+    static constexpr int off_inv = off_p + 2 * QT * PS * 2;
+    static constexpr int off_red = off_inv + kTile * 2;
+    static constexpr int off_len = off_red + QT * 16;
+    static constexpr int off_bar = (off_len + QT * 4 + 15) / 16 * 16;
+    static constexpr int off_misc = off_bar + slots * 8 + 8;  // tmp[33], abort, miss[slots], odd[2][2]
+    static constexpr int off_seq = (off_misc + 48 * 4 + 15) / 16 * 16;
+    static constexpr int smem(int agents) { return 1024 + off_seq + (agents + 1) * 16; }
 };
-
-// Dynamic shared memory: the rings (1024-byte aligned), the barriers, the table of sequences.
-template <int FMT, int D>
-constexpr int attend_smem(int agents) {
-    return 1024 + kWarps * kSlots * Geo<FMT, D>::HB + kWarps * kSlots * 8 + 160 + (agents + 1) * 16;
-}
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -146,34 +162,42 @@ __device__ __forceinline__ void tma_load_2d_hint(void* smem_dst, const void* tma
 }
 
 template <int FMT, int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, 1)
+__global__ void __launch_bounds__(kThreads, (Geo<FMT, D, NT>::blocks))
     attend_partial(const __grid_constant__ CUtensorMap map, const __grid_constant__ AttendParams p) {
-    using G = Geo<FMT, D>;
+    using G = Geo<FMT, D, NT>;
     constexpr bool BF = FMT == QMM_KV_BF16;
-    constexpr int TT = G::TT, JB = G::JB, SUB = G::SUB, MT = G::MT, QT = 8 * NT;
+    constexpr int QT = G::QT, MW = G::MW, PS = G::PS, QS = G::QS;
     extern __shared__ uint8_t sm_raw[];
     griddep_launch_dependents();  // the joining kernel waits for this grid's end before it reads
     uint8_t* sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kWarps * kSlots * G::HB);
-    int* tmp = reinterpret_cast<int*>(bars + kWarps * kSlots);  // 33 ints; [36]: abort flag
-    int4* seq = reinterpret_cast<int4*>(tmp + 40);  // [agents + 1]: first item, longest row, shortest row, first row
+    uint16_t* Ph = reinterpret_cast<uint16_t*>(sm + G::off_p);  // [QT][PS]
+    uint16_t* Pl = Ph + QT * PS;
+    uint16_t* inv_e = reinterpret_cast<uint16_t*>(sm + G::off_inv);  // [64], q8_0: 2^-e_t
+    float* red = reinterpret_cast<float*>(sm + G::off_red);          // [QT][4 warps]
+    int* qlen_sm = reinterpret_cast<int*>(sm + G::off_len);          // [QT]
+    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + G::off_bar);
+    int* tmp = reinterpret_cast<int*>(sm + G::off_misc);
+    volatile int* abort_flag = tmp + 33;
+    volatile int* miss_sm = tmp + 34;                                // [slots]: a page of the half tile is outside the pool
+    uint32_t* odd_sm = reinterpret_cast<uint32_t*>(tmp + 40);        // [2][2]: rows of V to be taken query by query
+    int4* seq = reinterpret_cast<int4*>(sm + G::off_seq);  // [agents + 1]: first item, longest row, shortest row, first row
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g8 = lane >> 2, t4 = lane & 3;
-    volatile int* abort_flag = tmp + 36;
 
-    // ---- the table of sequences: every CTA forms the same one
-    if (tid < kWarps * kSlots) mbar_init(bars + tid, 1);
+    // ---- the table of sequences: every block forms the same one
     if (tid == 0) {
+        for (int i = 0; i < G::slots; ++i) mbar_init(bar + i, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
-    for (int a = tid; a <= p.agents; a += kWarps * 32) {
+    if (tid < 4) odd_sm[tid] = 0;
+    for (int a = tid; a <= p.agents; a += kThreads) {
         const int r0 = p.agent_rows[a], r1 = a < p.agents ? p.agent_rows[a + 1] : r0;
         const bool ok = r0 >= 0 && r1 >= r0 && r1 <= p.rows && r1 - r0 <= p.max_agent_rows;
         seq[a] = make_int4(ok ? 0 : -1, 0, INT32_MAX, r0);
     }
     __syncthreads();
-    for (int r = tid; r < p.rows; r += kWarps * 32) {
+    for (int r = tid; r < p.rows; r += kThreads) {
         int lo = 0, hi = p.agents;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -190,7 +214,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     }
     __syncthreads();
     int total = 0;
-    for (int a0 = 0; a0 < p.agents; a0 += kWarps * 32) {
+    for (int a0 = 0; a0 < p.agents; a0 += kThreads) {
         const int a = a0 + tid;
         int n = 0;
         if (a < p.agents) {
@@ -209,12 +233,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         total += sum;
     }
     __syncthreads();
-
-    // ---- this warp's items: w, w + stride, ...
-    const int stride = gridDim.x * kWarps;
-    uint8_t* ring = sm + warp * kSlots * G::HB;
-    uint64_t* bar = bars + warp * kSlots;
-    const uint64_t policy = l2_policy_evict_first();
 
     struct Item {
         int a, g, tile, tok0, end;
@@ -238,8 +256,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         it.end = min(it.tok0 + p.chunk, s.y);
         return it;
     };
-    // lane l: the item's l-th page (an item spans at most 32), -1 if the table points outside
-    // the pool
+
+    // ---- the producer (warp 0): the item whose half tiles are being requested, and the one after
+    // it, whose pages are already on their way.  Lane l holds an item's l-th page (an item spans
+    // at most 32), -1 if the table points outside the pool.
+    Item pi = {}, ni = {};
+    int ppages = 0, npages = 0, ptok = 0, phalf = 0, pslot = 0, nitem = blockIdx.x, issued = 0;
     auto load_pages = [&](const Item& it) {
         const int first = it.tok0 >> p.page_shift;
         int pg = 0;
@@ -252,16 +274,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         }
         return pg;
     };
-    // the producer's place: the item whose tiles are being requested, and the one after it,
-    // whose pages are already known by then
-    Item pi = {}, ni = {};
-    int ppages = 0, npages = 0, ptok = 0, phalf = 0, pslot = 0, nitem = warp * gridDim.x + blockIdx.x;
-    uint32_t bad = 0;  // bit s: the half tile in slot s has a page outside the pool
-    int issued = 0, taken = 0;
-    if (nitem < total) {
-        ni = decode(nitem);
-        npages = load_pages(ni);
-    }
     auto issue = [&]() {
         if (ptok >= pi.end) {
             if (nitem >= total) return;
@@ -269,493 +281,466 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             ppages = npages;
             ptok = pi.tok0;
             phalf = 0;
-            nitem += stride;
+            nitem += gridDim.x;
             if (nitem < total) {
                 ni = decode(nitem);
                 npages = load_pages(ni);
             }
         }
-        uint8_t* dst = ring + pslot * G::HB;
+        uint8_t* dst = sm + pslot * G::HB;
         uint64_t* b = bar + pslot;
         const int first = pi.tok0 >> p.page_shift;
-        if (lane == 0) fence_proxy_async_smem();  // the slot's generic accesses, before the copy
         if constexpr (G::q8) {
             const int pg = __shfl_sync(0xffffffffu, ppages, (ptok >> 6) - first);
-            bad = pg < 0 ? bad | (1u << pslot) : bad & ~(1u << pslot);
             if (lane == 0) {
+                miss_sm[pslot] = pg < 0;
                 if (pg < 0) mbar_arrive(b);
                 else {
                     mbar_arrive_expect_tx(b, kQ8Half);
                     bulk_g2s(dst, p.pool + (static_cast<int64_t>(pg) * p.kv_heads + pi.g) * kQ8Rec + phalf * kQ8Half, kQ8Half,
-                             b, policy);
+                             b, l2_policy_evict_first());
                 }
             }
         } else {
-            // pieces of min(TT, page_tokens) tokens, those with tokens before the item's end
-            const int br = min(TT, p.page_tokens);
-            int pg[TT / 16];
+            // pieces of min(64, page_tokens) tokens, those with tokens before the item's end
+            const int br = min(kTile, p.page_tokens);
+            int pg[kTile / 16];
             uint32_t bytes = 0;
             bool miss = false;
 #pragma unroll
-            for (int k = 0; k < TT / 16; ++k) {
+            for (int k = 0; k < kTile / 16; ++k) {
                 const int tok = ptok + k * br;
-                const bool in = k * br < TT && tok < pi.end;
+                const bool in = k * br < kTile && tok < pi.end;
                 const int x = __shfl_sync(0xffffffffu, ppages, in ? (tok >> p.page_shift) - first : 0);
                 pg[k] = in ? x : -1;
-                if (in && x < 0) miss = true;
+                miss |= in && x < 0;
                 if (pg[k] >= 0) bytes += br * D * 2;
             }
-            bad = miss ? bad | (1u << pslot) : bad & ~(1u << pslot);
             if (lane == 0) {
+                miss_sm[pslot] = miss;
                 if (bytes == 0) mbar_arrive(b);
                 else mbar_arrive_expect_tx(b, bytes);
+                const uint64_t policy = l2_policy_evict_first();
 #pragma unroll
-                for (int k = 0; k < TT / 16; ++k) {
+                for (int k = 0; k < kTile / 16; ++k) {
                     if (pg[k] < 0) continue;
                     const int y = ((pg[k] * p.kv_heads + pi.g) * 2 + phalf) * p.page_tokens + ((ptok + k * br) & (p.page_tokens - 1));
 #pragma unroll
                     for (int x = 0; x < D / 64; ++x)
-                        tma_load_2d_hint(dst + x * TT * 128 + k * br * 128, &map, 64 * x, y, b, policy);
+                        tma_load_2d_hint(dst + x * kTile * 128 + k * br * 128, &map, 64 * x, y, b, policy);
                 }
             }
         }
         ++issued;
-        pslot = pslot == kSlots - 1 ? 0 : pslot + 1;
+        pslot = pslot == G::slots - 1 ? 0 : pslot + 1;
         phalf ^= 1;
-        if (phalf == 0) ptok += TT;
+        if (phalf == 0) ptok += kTile;
     };
-    for (int i = 0; i < kSlots; ++i) issue();
+    if (warp == 0) {
+        if (nitem < total) {
+            ni = decode(nitem);
+            npages = load_pages(ni);
+        }
+        for (int i = 0; i < G::slots; ++i) issue();
+    }
 
     bool live = true;
-    int slot = 0, phase = 0;  // the consumer's slot and its barrier's phase
-    auto await = [&]() {
-        const bool ok = mbar_wait_bounded(bar + slot, phase, abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) live = false;
-    };
-    auto advance = [&]() {  // the slot is read: refill it
-        __syncwarp();
-        ++taken;
-        if (++slot == kSlots) {
+    int slot = 0, phase = 0;  // of the next half tile to be read, and its barrier's phase
+    int freed = 0;            // half tiles read that have not been refilled
+    int taken = 0;
+    uint32_t parity = 0;      // of the tile: which pair of odd_sm it uses
+    auto next = [&]() {
+        if (++slot == G::slots) {
             slot = 0;
             phase ^= 1;
         }
-        issue();
+        ++taken;
     };
 
-    for (int item = warp * gridDim.x + blockIdx.x; item < total && live; item += stride) {
+    for (int item = blockIdx.x; item < total && live; item += gridDim.x) {
         const Item it = decode(item);
         const int r0 = seq[it.a].w, nq = (seq[it.a + 1].w - r0) * p.group, q0 = it.tile * QT;
         const int minlen = seq[it.a].z;
         const int nnt = min(NT, (nq - q0 + 7) >> 3);
-
-        // Q^T's B fragments; k-slots of a q8_0 block are permuted so that a thread's eight dims
-        // are contiguous (slots 2t, 2t+1, 2t+8, 2t+9 of step k2: dims 8t + 4 k2 + 0 .. 3)
-        uint32_t qb[NT][MT][2];
-        int qlen[NT][2], qlen_t[NT];  // tokens seen by the queries of the accumulators' columns, and of g8
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int qa = q0 + 8 * nt + g8;
-            const uint16_t* row = nullptr;
-            qlen_t[nt] = 0;
-            if (qa < nq) {
-                const int r = r0 + qa / p.group;
-                qlen_t[nt] = p.row_len[r];
-                row = p.q + r * p.q_stride + static_cast<int64_t>(it.g * p.group + qa % p.group) * D;
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) qlen[nt][e] = __shfl_sync(0xffffffffu, qlen_t[nt], (2 * t4 + e) << 2);
-            if constexpr (G::q8) {
-#pragma unroll
-                for (int blk = 0; blk < 4; ++blk) {
-                    const uint4 v = row ? *reinterpret_cast<const uint4*>(row + 32 * blk + 8 * t4) : make_uint4(0, 0, 0, 0);
-                    qb[nt][2 * blk][0] = v.x;
-                    qb[nt][2 * blk][1] = v.y;
-                    qb[nt][2 * blk + 1][0] = v.z;
-                    qb[nt][2 * blk + 1][1] = v.w;
-                }
-            } else {
-#pragma unroll
-                for (int ks = 0; ks < MT; ++ks)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        qb[nt][ks][e] = row ? *reinterpret_cast<const uint32_t*>(row + 16 * ks + 2 * t4 + 8 * e) : 0u;
-            }
+        __syncthreads();  // the previous item's queries, lengths and sums are read
+        for (int i = tid; i < QT * (D / 8); i += kThreads) {
+            const int qi = i / (D / 8), c = i % (D / 8), qa = q0 + qi;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (qa < nq)
+                v = *reinterpret_cast<const uint4*>(p.q + (r0 + qa / p.group) * p.q_stride +
+                                                    static_cast<int64_t>(it.g * p.group + qa % p.group) * D + 8 * c);
+            *reinterpret_cast<uint4*>(sm + G::off_q + qi * QS + 16 * c) = v;
         }
+        if (tid < QT) qlen_sm[tid] = q0 + tid < nq ? p.row_len[r0 + (q0 + tid) / p.group] : 0;
+        __syncthreads();
 
-        float mx[NT][2], l[NT][2], o[MT][NT][4];
+        float mx[NT][2], l[NT][2], o[MW][NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             mx[nt][0] = mx[nt][1] = kNoMax;
             l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int mt = 0; mt < MW; ++mt)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) o[mt][nt][c] = 0.f;
         }
-        float* srow = p.scores ? p.scores + (static_cast<int64_t>(it.a * p.kv_heads + it.g) * p.chunks * p.chunk) * p.qp : nullptr;
+        // scores, for the weights: four queries of consecutive tokens side by side
+        const int64_t plane = static_cast<int64_t>(p.chunks) * p.chunk * 4;
+        float* sbase = p.scores ? p.scores + static_cast<int64_t>(it.a * p.kv_heads + it.g) * (p.qp >> 2) * plane : nullptr;
 
-        for (int tb = it.tok0; tb < it.end && live; tb += TT) {
-            await();
-            const uint8_t* kt = ring + slot * G::HB;
-            const int vslot = slot == kSlots - 1 ? 0 : slot + 1;
-            uint8_t* vt = ring + vslot * G::HB;
-            const bool miss = (bad >> slot) & 1;
-            if constexpr (G::q8) {  // V's scales join the softmax
-                const bool ok = mbar_wait_bounded(bar + vslot, vslot == 0 ? phase ^ 1 : phase, abort_flag);
-                if (!__all_sync(0xffffffffu, ok)) live = false;
-            }
-            if (!live) break;
-            const bool edge = miss || tb + TT > minlen;  // some query does not see some token of the tile
+        for (int tb = it.tok0; tb < it.end; tb += kTile) {
+            const uint8_t* kt = sm + slot * G::HB;
+            bool ok = mbar_wait_bounded(bar + slot, phase, abort_flag);
+            const bool miss = miss_sm[slot] != 0;
+            const bool edge = miss || tb + kTile > minlen;  // some query does not see some token of the tile
+            next();
+            uint8_t* vt = sm + slot * G::HB;
+
+            // ---- scores of tokens 16 warp + g8 (c0, c1) and + 8 (c2, c3), queries 8 nt + 2 t4 + {0, 1}
+            const int ta = 16 * warp + g8;
+            float s[NT][4];
 #pragma unroll
-            for (int sub = 0; sub < SUB; ++sub) {
-                // ---- scores: s[jj][nt][c], c0/c1: token A, queries 2t4, 2t4 + 1; c2/c3: token B
-                float s[JB][NT][4];
-                int ta[JB], tB[JB];  // the thread's tokens within the tile
-                uint32_t dv[JB][4][2], dinv[JB][2];  // q8_0: V scales of tokens 16 t4 + 4 j + 0 .. 3 by block
-                float ea[JB], eb[JB];                // q8_0: exponents of tokens A and B
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int jj = 0; jj < JB; ++jj) {
-                    const int j = sub * JB + jj;
+                for (int c = 0; c < 4; ++c) s[nt][c] = 0.f;
+            if constexpr (G::q8) {
+                // k-slots are permuted so that a thread's eight dims of a block are contiguous (slots
+                // 2t, 2t+1, 2t+8, 2t+9 of step k2: dims 8t + 4 k2 + 0 .. 3)
+                const int key = q8_key(g8);
+                const uint2 sca = *reinterpret_cast<const uint2*>(kt + 8192 + ta * 8);
+                const uint2 scb = *reinterpret_cast<const uint2*>(kt + 8192 + (ta + 8) * 8);
+#pragma unroll
+                for (int blk = 0; blk < 4; ++blk) {
+                    const uint8_t* ka = kt + ta * 128 + 16 * ((2 * blk + (t4 >> 1)) ^ key) + 8 * (t4 & 1);
+                    uint2 va = *reinterpret_cast<const uint2*>(ka), vb = *reinterpret_cast<const uint2*>(ka + 8 * 128);
+                    va.x ^= 0x80808080u, va.y ^= 0x80808080u, vb.x ^= 0x80808080u, vb.y ^= 0x80808080u;
+                    const uint32_t a0 = i8_to_h2(va.x, 0x4140u), a1 = i8_to_h2(vb.x, 0x4140u), a2 = i8_to_h2(va.x, 0x4342u),
+                                   a3 = i8_to_h2(vb.x, 0x4342u);
+                    const uint32_t b0 = i8_to_h2(va.y, 0x4140u), b1 = i8_to_h2(vb.y, 0x4140u), b2 = i8_to_h2(va.y, 0x4342u),
+                                   b3 = i8_to_h2(vb.y, 0x4342u);
+                    const __half2 pa = as_h2(blk < 2 ? sca.x : sca.y), pb = as_h2(blk < 2 ? scb.x : scb.y);
+                    const float fa = (blk & 1) ? __high2float(pa) : __low2float(pa);
+                    const float fb = (blk & 1) ? __high2float(pb) : __low2float(pb);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) s[jj][nt][c] = 0.f;
-                    if constexpr (G::q8) {
-                        // row g8 of block j is token 16 (g8 / 2) + 4 j + g8 % 2, row g8 + 8 two on: the
-                        // thread's P^T slots are then tokens 16 t4 + 4 j + 0 .. 3, contiguous in V
-                        ta[jj] = 16 * (g8 >> 1) + 4 * j + (g8 & 1);
-                        tB[jj] = ta[jj] + 2;
-                        const int key = 2 * (g8 & 1) + (j & 1);
-                        const uint2 sca = *reinterpret_cast<const uint2*>(kt + 8192 + ta[jj] * 8);
-                        const uint2 scb = *reinterpret_cast<const uint2*>(kt + 8192 + tB[jj] * 8);
-#pragma unroll
-                        for (int blk = 0; blk < 4; ++blk) {
-                            const uint8_t* ka = kt + ta[jj] * 128 + 16 * ((2 * blk + (t4 >> 1)) ^ key) + 8 * (t4 & 1);
-                            const uint8_t* kb = kt + tB[jj] * 128 + 16 * ((2 * blk + (t4 >> 1)) ^ (key + 4)) + 8 * (t4 & 1);
-                            uint2 va = *reinterpret_cast<const uint2*>(ka), vb = *reinterpret_cast<const uint2*>(kb);
-                            va.x ^= 0x80808080u, va.y ^= 0x80808080u, vb.x ^= 0x80808080u, vb.y ^= 0x80808080u;
-                            const __half2 pa = as_h2(blk < 2 ? sca.x : sca.y), pb = as_h2(blk < 2 ? scb.x : scb.y);
-                            const float fa = (blk & 1) ? __high2float(pa) : __low2float(pa);
-                            const float fb = (blk & 1) ? __high2float(pb) : __low2float(pb);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                if (nt < nnt) {
-                                    float d[4] = {0.f, 0.f, 0.f, 0.f};
-                                    mma_m16n8k16(d, i8_to_h2(va.x, 0x4140u), i8_to_h2(vb.x, 0x4140u), i8_to_h2(va.x, 0x4342u),
-                                                 i8_to_h2(vb.x, 0x4342u), qb[nt][2 * blk][0], qb[nt][2 * blk][1]);
-                                    mma_m16n8k16(d, i8_to_h2(va.y, 0x4140u), i8_to_h2(vb.y, 0x4140u), i8_to_h2(va.y, 0x4342u),
-                                                 i8_to_h2(vb.y, 0x4342u), qb[nt][2 * blk + 1][0], qb[nt][2 * blk + 1][1]);
-                                    s[jj][nt][0] = fmaf(d[0], fa, s[jj][nt][0]);
-                                    s[jj][nt][1] = fmaf(d[1], fa, s[jj][nt][1]);
-                                    s[jj][nt][2] = fmaf(d[2], fb, s[jj][nt][2]);
-                                    s[jj][nt][3] = fmaf(d[3], fb, s[jj][nt][3]);
-                                }
+                        if (nt < nnt) {
+                            const uint4 q = lds128(sm + G::off_q + (8 * nt + g8) * QS + 64 * blk + 16 * t4);
+                            float d[4] = {0.f, 0.f, 0.f, 0.f};
+                            mma_m16n8k16(d, a0, a1, a2, a3, q.x, q.y);
+                            mma_m16n8k16(d, b0, b1, b2, b3, q.z, q.w);
+                            s[nt][0] = fmaf(d[0], fa, s[nt][0]);
+                            s[nt][1] = fmaf(d[1], fa, s[nt][1]);
+                            s[nt][2] = fmaf(d[2], fb, s[nt][2]);
+                            s[nt][3] = fmaf(d[3], fb, s[nt][3]);
                         }
-                        // the tokens' exponents (of the largest scale, in -14 .. 14) and normalised scales
-                        uint32_t top0 = 0, top1 = 0;
-#pragma unroll
-                        for (int blk = 0; blk < 4; ++blk) {
-                            const uint2 w = *reinterpret_cast<const uint2*>(vt + 8192 + (blk * 64 + 16 * t4 + 4 * j) * 2);
-                            dv[jj][blk][0] = w.x;
-                            dv[jj][blk][1] = w.y;
-                            top0 = as_u32(__hmax2(as_h2(top0), as_h2(w.x & 0x7FFF7FFFu)));
-                            top1 = as_u32(__hmax2(as_h2(top1), as_h2(w.y & 0x7FFF7FFFu)));
-                        }
-                        const __half2 least = as_h2(0x04000400u), most = as_h2(0x74007400u);
-                        top0 = as_u32(__hmin2(__hmax2(as_h2(top0 & 0x7C007C00u), least), most));
-                        top1 = as_u32(__hmin2(__hmax2(as_h2(top1 & 0x7C007C00u), least), most));
-                        dinv[jj][0] = 0x78007800u - top0;  // 2^-e
-                        dinv[jj][1] = 0x78007800u - top1;
-                        const int sh = 16 * (g8 & 1) + 10;
-                        ea[jj] = static_cast<float>(static_cast<int>((__shfl_sync(0xffffffffu, top0, g8 >> 1) >> sh) & 31u) - 15);
-                        eb[jj] = static_cast<float>(static_cast<int>((__shfl_sync(0xffffffffu, top1, g8 >> 1) >> sh) & 31u) - 15);
-                    } else {
-                        ta[jj] = 16 * j + g8;
-                        tB[jj] = ta[jj] + 8;
-                        const uint32_t base = smem_u32(kt) + (16 * j + (lane & 15)) * 128;
-#pragma unroll
-                        for (int ks = 0; ks < MT; ++ks) {
-                            const int ch = 2 * ks + (lane >> 4);
-                            uint32_t a[4];
-                            ldmatrix_x4(a, base + (ch >> 3) * (TT * 128) + (((ch & 7) ^ (lane & 7)) << 4));
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                if (nt < nnt) mma16<BF>(s[jj][nt], a[0], a[1], a[2], a[3], qb[nt][ks][0], qb[nt][ks][1]);
-                        }
-                    }
                 }
-                // ---- base-2 scores, masks, the weights' copy, the step's maxima
+            } else {
+                const uint32_t base = smem_u32(kt) + (16 * warp + (lane & 15)) * 128;
+                const uint32_t qbase = smem_u32(sm + G::off_q) + (lane & 7) * QS + (lane >> 3) * 16;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    if (nt >= nnt) continue;
-                    float step[2] = {kNoMax, kNoMax};
-#pragma unroll
-                    for (int jj = 0; jj < JB; ++jj) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) s[jj][nt][c] *= p.c2;
-                        if (edge) {
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                if (miss || tb + ta[jj] >= qlen[nt][e]) s[jj][nt][e] = kNoMax;
-                                if (miss || tb + tB[jj] >= qlen[nt][e]) s[jj][nt][2 + e] = kNoMax;
-                            }
-                        }
-                        if (srow && q0 + 8 * nt < p.qp) {
-                            float* at = srow + static_cast<int64_t>(tb) * p.qp + q0 + 8 * nt + 2 * t4;
-                            *reinterpret_cast<float2*>(at + ta[jj] * p.qp) = make_float2(s[jj][nt][0], s[jj][nt][1]);
-                            *reinterpret_cast<float2*>(at + tB[jj] * p.qp) = make_float2(s[jj][nt][2], s[jj][nt][3]);
-                        }
-                        if constexpr (G::q8) {
-                            s[jj][nt][0] += ea[jj];
-                            s[jj][nt][1] += ea[jj];
-                            s[jj][nt][2] += eb[jj];
-                            s[jj][nt][3] += eb[jj];
-                        }
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) step[e] = fmaxf(step[e], fmaxf(s[jj][nt][e], s[jj][nt][2 + e]));
-                    }
-                    float alpha[2];
+                for (int ks = 0; ks < G::KS; ks += 2) {
+                    uint32_t a[2][4];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float m = step[e];
+                        const int ch = 2 * (ks + e) + (lane >> 4);
+                        ldmatrix_x4(a[e], base + (ch >> 3) * (kTile * 128) + (((ch & 7) ^ (lane & 7)) << 4));
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        if (nt < nnt) {
+                            uint32_t q[4];
+                            ldmatrix_x4(q, qbase + nt * 8 * QS + ks * 32);
+                            mma16<BF>(s[nt], a[0][0], a[0][1], a[0][2], a[0][3], q[0], q[1]);
+                            mma16<BF>(s[nt], a[1][0], a[1][1], a[1][2], a[1][3], q[2], q[3]);
+                        }
+                }
+            }
+            ok &= mbar_wait_bounded(bar + slot, phase, abort_flag);  // V
+            next();
+            float ea = 0.f, eb = 0.f;
+            uint16_t two_e = 0;
+            if constexpr (G::q8) {
+                // lane l < 16: the exponent of token 16 warp + l's largest V scale, in -14 .. 14
+                const int t = 16 * warp + (lane & 15);
+                uint32_t top = 0;
+#pragma unroll
+                for (int blk = 0; blk < 4; ++blk) {
+                    const uint32_t w = *reinterpret_cast<const uint16_t*>(vt + 8192 + (blk * 64 + t) * 2) & 0x7FFFu;
+                    top = w > 0x7C00u ? top : max(top, w);  // (NaN scales do not count)
+                }
+                const int e = min(max(static_cast<int>(top >> 10), 1), 29);
+                two_e = static_cast<uint16_t>((30 - e) << 10);  // 2^-e
+                ea = static_cast<float>(__shfl_sync(0xffffffffu, e, g8) - 15);
+                eb = static_cast<float>(__shfl_sync(0xffffffffu, e, g8 + 8) - 15);
+            }
+            // ---- base-2 scores, masks, the weights' copy, the warp's maxima
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                if (nt < nnt) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) s[nt][c] *= p.c2;
+                    if (edge) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int n = miss ? 0 : qlen_sm[8 * nt + 2 * t4 + e];
+                            if (tb + ta >= n) s[nt][e] = kNoMax;
+                            if (tb + ta + 8 >= n) s[nt][2 + e] = kNoMax;
+                        }
+                    }
+                    if (sbase && q0 + 8 * nt < p.qp) {
+                        float* at = sbase + ((q0 >> 2) + 2 * nt + (t4 >> 1)) * plane + (tb + ta) * 4 + 2 * (t4 & 1);
+                        *reinterpret_cast<float2*>(at) = make_float2(s[nt][0], s[nt][1]);
+                        *reinterpret_cast<float2*>(at + 32) = make_float2(s[nt][2], s[nt][3]);
+                    }
+                    if constexpr (G::q8) {
+                        s[nt][0] += ea;
+                        s[nt][1] += ea;
+                        s[nt][2] += eb;
+                        s[nt][3] += eb;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float m = fmaxf(s[nt][e], s[nt][2 + e]);
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                        m = fmaxf(m, mx[nt][e]);
+                        if (g8 == 0) red[(8 * nt + 2 * t4 + e) * 4 + warp] = m;
+                    }
+                }
+            // every warp is past this tile's K and the last tile's V and P; one decision for all
+            if (__syncthreads_or(!ok)) {
+                live = false;
+                break;
+            }
+            if (warp == 0) {
+                if (lane == 0) fence_proxy_async_smem();  // the slots' generic accesses, before the copies
+                for (freed += 1; freed > 0; --freed) issue();
+            }
+            freed = 1;  // this tile's V, at the next tile's barrier
+            if (tid < 2) odd_sm[2 * (parity ^ 1) + tid] = 0;
+            if (G::q8 && lane < 16) inv_e[16 * warp + lane] = two_e;
+
+            // ---- new maxima, rescaling, probabilities to shared memory
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                if (nt < nnt) {
+                    float alpha[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float4 r = *reinterpret_cast<const float4*>(red + (8 * nt + 2 * t4 + e) * 4);
+                        const float m = fmaxf(fmaxf(fmaxf(r.x, r.y), fmaxf(r.z, r.w)), mx[nt][e]);
                         // (nothing seen so far: any finite reference gives 2^-inf = 0)
                         const float ref = m == kNoMax ? 0.f : m;
                         alpha[e] = mx[nt][e] == m ? 1.f : ex2(mx[nt][e] - ref);
                         mx[nt][e] = m;
-                        float sum = 0.f;
-#pragma unroll
-                        for (int jj = 0; jj < JB; ++jj) {
-                            const float pa = ex2(s[jj][nt][e] - ref + kShift), pb = ex2(s[jj][nt][2 + e] - ref + kShift);
-                            s[jj][nt][e] = pa;
-                            s[jj][nt][2 + e] = pb;
-                            if constexpr (G::q8)
-                                sum += pa * __int_as_float((127 - static_cast<int>(ea[jj])) << 23) +
-                                       pb * __int_as_float((127 - static_cast<int>(eb[jj])) << 23);
-                            else
-                                sum += pa + pb;
-                        }
+                        const float pa = ex2(s[nt][e] - ref + kShift), pb = ex2(s[nt][2 + e] - ref + kShift);
+                        s[nt][e] = pa;
+                        s[nt][2 + e] = pb;
+                        float sum = pa + pb;
+                        if constexpr (G::q8)
+                            sum = pa * __int_as_float((127 - static_cast<int>(ea)) << 23) +
+                                  pb * __int_as_float((127 - static_cast<int>(eb)) << 23);
                         l[nt][e] = fmaf(l[nt][e], alpha[e], sum);
                     }
                     if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt)
+                        for (int mt = 0; mt < MW; ++mt)
 #pragma unroll
                             for (int c = 0; c < 4; ++c) o[mt][nt][c] *= alpha[c & 1];
                     }
-                }
-                if (sub == SUB - 1) {
-                    advance();  // K is read
-                    if constexpr (!G::q8) {
-                        if (SUB == 1) await();
-                    }
-                } else if constexpr (!G::q8) {
-                    // V's first use in a tile of two steps; its slot follows K's
-                    const bool ok = mbar_wait_bounded(bar + vslot, vslot == 0 ? phase ^ 1 : phase, abort_flag);
-                    if (!__all_sync(0xffffffffu, ok)) live = false;
-                }
-                if (!live) break;
-
-                if constexpr (!G::q8) {
-                    if (edge) {
-                        // Rows of V that some query does not see.  Past the sequence's end (and in
-                        // tiles with a missing page) they hold anything and become zero.  A row that
-                        // some queries see is looked at: if it holds a NaN or infinity, its
-                        // contribution is added query by query, and zero takes its place.
-                        const int lo = 16 * JB * sub, hi = lo + 16 * JB;
-                        const int first = miss ? lo : max(lo, minlen - tb), last = miss ? lo : it.end - tb;
-                        for (int t = first; t < hi; ++t) {
-                            // lane's share of the row: D / 32 elements from dim lane * D / 32
-                            constexpr int E = D / 64;  // 32-bit words
-                            uint32_t* w = reinterpret_cast<uint32_t*>(vt + ((lane * E) >> 5) * (TT * 128) + t * 128 +
-                                                                      (((((lane * E) & 31) >> 2) ^ (t & 7)) << 4) + ((lane * E) & 3) * 4);
-                            bool odd = t >= last;
-                            if (!odd) {
-                                bool here = false;
-                                constexpr uint32_t ex = BF ? 0x7F80u : 0x7C00u;
 #pragma unroll
-                                for (int i = 0; i < E; ++i)
-                                    here |= (w[i] & ex) == ex || ((w[i] >> 16) & ex) == ex;
-                                odd = __any_sync(0xffffffffu, here);
-                                if (odd) {
-                                    const int src = ((t & 7) << 2) | t4;
-#pragma unroll
-                                    for (int jj = 0; jj < JB; ++jj) {
-                                        if ((t - lo) >> 4 != jj) continue;
-                                        const bool up = t & 8;
-#pragma unroll
-                                        for (int nt = 0; nt < NT; ++nt) {
-                                            if (nt >= nnt) continue;
-                                            float pt[2];
-#pragma unroll
-                                            for (int e = 0; e < 2; ++e) {
-                                                const float x = __shfl_sync(0xffffffffu, s[jj][nt][e], src);
-                                                const float y = __shfl_sync(0xffffffffu, s[jj][nt][2 + e], src);
-                                                pt[e] = up ? y : x;
-                                            }
-#pragma unroll
-                                            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                                                for (int c = 0; c < 4; ++c) {
-                                                    const int d = 16 * mt + g8 + 8 * (c >> 1);
-                                                    const uint16_t u = *reinterpret_cast<const uint16_t*>(
-                                                        vt + (d >> 6) * (TT * 128) + t * 128 + ((((d & 63) >> 3) ^ (t & 7)) << 4) + (d & 7) * 2);
-                                                    const float v = BF ? __uint_as_float(static_cast<uint32_t>(u) << 16)
-                                                                       : __half2float(__ushort_as_half(u));
-                                                    if (tb + t < qlen[nt][c & 1]) o[mt][nt][c] = fmaf(pt[c & 1], v, o[mt][nt][c]);
-                                                }
-                                        }
-                                    }
-                                }
-                            }
-                            __syncwarp();
-                            if (odd)
-#pragma unroll
-                                for (int i = 0; i < E; ++i) w[i] = 0u;
-                        }
-                        __syncwarp();
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t hi, lo;
+                        split2<BF>(s[nt][2 * h], s[nt][2 * h + 1], hi, lo);
+                        const int at = (8 * nt + g8) * PS + 16 * warp + 8 * h + 2 * t4;
+                        *reinterpret_cast<uint32_t*>(Ph + at) = movmatrix_trans(hi);
+                        *reinterpret_cast<uint32_t*>(Pl + at) = movmatrix_trans(lo);
                     }
                 }
-
-                // ---- P^T as B fragments (hi, lo), and O^T += V^T P^T
-                if constexpr (G::q8) {
-                    uint32_t bh[JB][NT][2], bl[JB][NT][2];
+            if constexpr (!G::q8) {
+                if (edge) {
+                    // The warp's rows of V that some query does not see.  Past the sequence's end (and
+                    // in tiles with a missing page) they hold anything and become zero.  One that
+                    // some queries see and that holds a NaN or infinity is marked.
+                    const int last = miss ? 0 : it.end - tb;
+                    for (int t = max(16 * warp, miss ? 0 : minlen - tb); t < 16 * warp + 16; ++t) {
+                        uint32_t* w = reinterpret_cast<uint32_t*>(vt + ((lane * MW) >> 5) * (kTile * 128) + t * 128 +
+                                                                  (((((lane * MW) & 31) >> 2) ^ (t & 7)) << 4) + ((lane * MW) & 3) * 4);
+                        if (t >= last) {
 #pragma unroll
-                    for (int jj = 0; jj < JB; ++jj)
+                            for (int i = 0; i < MW; ++i) w[i] = 0u;
+                        } else {
+                            bool here = false;
+                            constexpr uint32_t ex = BF ? 0x7F80u : 0x7C00u;
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            if (nt < nnt) {
-#pragma unroll
-                                for (int h = 0; h < 2; ++h) {
-                                    uint32_t hi, lo;
-                                    split2<false>(s[jj][nt][2 * h], s[jj][nt][2 * h + 1], hi, lo);
-                                    bh[jj][nt][h] = movmatrix_trans(hi);
-                                    bl[jj][nt][h] = movmatrix_trans(lo);
-                                }
-                            }
-#pragma unroll
-                    for (int blk = 0; blk < 4; ++blk) {
-                        uint2 w[2][2];  // V quants of the step's tokens: [m16 tile][row g8, g8 + 8]
-#pragma unroll
-                        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                w[mt][h] = *reinterpret_cast<const uint2*>(vt + (32 * blk + 16 * mt + 8 * h + g8) * 64 + 16 * t4 + 8 * sub);
-                                w[mt][h].x ^= 0x80808080u;
-                                w[mt][h].y ^= 0x80808080u;
-                            }
-#pragma unroll
-                        for (int jj = 0; jj < JB; ++jj) {
-                            const __half2 d0 = __hmul2(as_h2(dv[jj][blk][0]), as_h2(dinv[jj][0]));
-                            const __half2 d1 = __hmul2(as_h2(dv[jj][blk][1]), as_h2(dinv[jj][1]));
-                            uint32_t a[2][4];
-#pragma unroll
-                            for (int mt = 0; mt < 2; ++mt) {
-                                const uint32_t w0 = jj ? w[mt][0].y : w[mt][0].x, w1 = jj ? w[mt][1].y : w[mt][1].x;
-                                a[mt][0] = i8_to_h2(w0, 0x4140u);
-                                a[mt][1] = i8_to_h2(w1, 0x4140u);
-                                a[mt][2] = i8_to_h2(w0, 0x4342u);
-                                a[mt][3] = i8_to_h2(w1, 0x4342u);
-                            }
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                if (nt < nnt) {
-                                    // (hi + lo) * scale = ph + pl: the product's rounding error comes back by fma
-                                    __half2 ph0 = __hmul2(as_h2(bh[jj][nt][0]), d0), ph1 = __hmul2(as_h2(bh[jj][nt][1]), d1);
-                                    __half2 pl0 = __hfma2(as_h2(bl[jj][nt][0]), d0, __hfma2(as_h2(bh[jj][nt][0]), d0, __hneg2(ph0)));
-                                    __half2 pl1 = __hfma2(as_h2(bl[jj][nt][1]), d1, __hfma2(as_h2(bh[jj][nt][1]), d1, __hneg2(ph1)));
-                                    uint32_t uh0 = as_u32(ph0), uh1 = as_u32(ph1), ul0 = as_u32(pl0), ul1 = as_u32(pl1);
-                                    if (edge) {  // a scale that is NaN or infinite has no effect on rows that do not see it
-                                        const int t = tb + 16 * t4 + 4 * (sub * JB + jj), n = miss ? 0 : qlen_t[nt];
-                                        const uint32_t m0 = (t < n ? 0xFFFFu : 0u) | (t + 1 < n ? 0xFFFF0000u : 0u);
-                                        const uint32_t m1 = (t + 2 < n ? 0xFFFFu : 0u) | (t + 3 < n ? 0xFFFF0000u : 0u);
-                                        uh0 &= m0, ul0 &= m0, uh1 &= m1, ul1 &= m1;
-                                    }
-#pragma unroll
-                                    for (int mt = 0; mt < 2; ++mt) {
-                                        mma_m16n8k16(o[2 * blk + mt][nt], a[mt][0], a[mt][1], a[mt][2], a[mt][3], uh0, uh1);
-                                        mma_m16n8k16(o[2 * blk + mt][nt], a[mt][0], a[mt][1], a[mt][2], a[mt][3], ul0, ul1);
-                                    }
-                                }
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int jj = 0; jj < JB; ++jj) {
-                        const int j = sub * JB + jj;
-                        uint32_t bh[NT][2], bl[NT][2];
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            if (nt < nnt) {
-#pragma unroll
-                                for (int h = 0; h < 2; ++h) {
-                                    uint32_t hi, lo;
-                                    split2<BF>(s[jj][nt][2 * h], s[jj][nt][2 * h + 1], hi, lo);
-                                    bh[nt][h] = movmatrix_trans(hi);
-                                    bl[nt][h] = movmatrix_trans(lo);
-                                }
-                            }
-                        const int t = 16 * j + (lane & 7) + ((lane >> 4) << 3);
-                        const uint32_t base = smem_u32(vt) + t * 128;
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            const int ch = 2 * mt + ((lane >> 3) & 1);
-                            uint32_t a[4];
-                            ldmatrix_x4_trans(a, base + (ch >> 3) * (TT * 128) + (((ch & 7) ^ (lane & 7)) << 4));
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                if (nt < nnt) {
-                                    mma16<BF>(o[mt][nt], a[0], a[1], a[2], a[3], bh[nt][0], bh[nt][1]);
-                                    mma16<BF>(o[mt][nt], a[0], a[1], a[2], a[3], bl[nt][0], bl[nt][1]);
-                                }
+                            for (int i = 0; i < MW; ++i) here |= (w[i] & ex) == ex || ((w[i] >> 16) & ex) == ex;
+                            if (__any_sync(0xffffffffu, here) && lane == 0) atomicOr(odd_sm + 2 * parity + (t >> 5), 1u << (t & 31));
                         }
                     }
                 }
             }
-            if (!live) break;
-            advance();  // V is read
+            __syncthreads();  // P is complete
+            if constexpr (!G::q8) {
+                if (edge && (odd_sm[2 * parity] | odd_sm[2 * parity + 1])) {
+                    // marked rows: added query by query, to those that see them; then zero in the product
+#pragma unroll 1
+                    for (int t = 0; t < kTile; ++t) {
+                        if (!((odd_sm[2 * parity + (t >> 5)] >> (t & 31)) & 1)) continue;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                const int q = 8 * nt + 2 * t4 + (c & 1);
+                                if (nt >= nnt || tb + t >= qlen_sm[q]) continue;
+                                const uint32_t h = Ph[q * PS + t], u = Pl[q * PS + t];
+                                const float pt = BF ? __uint_as_float(h << 16) + __uint_as_float(u << 16)
+                                                    : __half2float(__ushort_as_half(h)) + __half2float(__ushort_as_half(u));
+#pragma unroll
+                                for (int mt = 0; mt < MW; ++mt) {
+                                    const int d = 16 * (warp * MW + mt) + g8 + 8 * (c >> 1);
+                                    const uint32_t v = *reinterpret_cast<const uint16_t*>(
+                                        vt + (d >> 6) * (kTile * 128) + t * 128 + ((((d & 63) >> 3) ^ (t & 7)) << 4) + (d & 7) * 2);
+                                    o[mt][nt][c] = fmaf(pt, BF ? __uint_as_float(v << 16) : __half2float(__ushort_as_half(v)), o[mt][nt][c]);
+                                }
+                            }
+                    }
+                    __syncthreads();
+                    for (int t = warp; t < kTile; t += kWarps)
+                        if ((odd_sm[2 * parity + (t >> 5)] >> (t & 31)) & 1)
+                            for (int i = lane; i < D / 2; i += 32)
+                                *reinterpret_cast<uint32_t*>(vt + (i >> 5) * (kTile * 128) + t * 128 + (i & 31) * 4) = 0u;
+                    __syncthreads();
+                }
+            }
+
+            // ---- O^T += V^T P^T for dims D / 4 * warp ..
+            if constexpr (G::q8) {
+                // (D / 4 = 32: one block of scales.)  Tokens of step ks: 16 t4 + 4 ks + 0 .. 3 are the thread's
+                // k-slots 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9, so that its sixteen V bytes are contiguous
+                uint4 w[2][2];
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        w[mt][h] = *reinterpret_cast<const uint4*>(vt + (32 * warp + 16 * mt + 8 * h + g8) * 64 + 16 * t4);
+                        w[mt][h].x ^= 0x80808080u, w[mt][h].y ^= 0x80808080u, w[mt][h].z ^= 0x80808080u, w[mt][h].w ^= 0x80808080u;
+                    }
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) {
+                    const int tok = 16 * t4 + 4 * ks;
+                    const uint2 dv = *reinterpret_cast<const uint2*>(vt + 8192 + (warp * 64 + tok) * 2);
+                    const uint2 di = *reinterpret_cast<const uint2*>(inv_e + tok);
+                    const __half2 d0 = __hmul2(as_h2(dv.x), as_h2(di.x)), d1 = __hmul2(as_h2(dv.y), as_h2(di.y));
+                    uint32_t a[2][4];
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt) {
+                        const uint32_t w0 = ks == 0 ? w[mt][0].x : ks == 1 ? w[mt][0].y : ks == 2 ? w[mt][0].z : w[mt][0].w;
+                        const uint32_t w1 = ks == 0 ? w[mt][1].x : ks == 1 ? w[mt][1].y : ks == 2 ? w[mt][1].z : w[mt][1].w;
+                        a[mt][0] = i8_to_h2(w0, 0x4140u);
+                        a[mt][1] = i8_to_h2(w1, 0x4140u);
+                        a[mt][2] = i8_to_h2(w0, 0x4342u);
+                        a[mt][3] = i8_to_h2(w1, 0x4342u);
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        if (nt < nnt) {
+                            const uint2 bh = *reinterpret_cast<const uint2*>(Ph + (8 * nt + g8) * PS + tok);
+                            const uint2 bl = *reinterpret_cast<const uint2*>(Pl + (8 * nt + g8) * PS + tok);
+                            // (hi + lo) * scale = ph + pl: the product's rounding error comes back by fma
+                            const __half2 ph0 = __hmul2(as_h2(bh.x), d0), ph1 = __hmul2(as_h2(bh.y), d1);
+                            const __half2 pl0 = __hfma2(as_h2(bl.x), d0, __hfma2(as_h2(bh.x), d0, __hneg2(ph0)));
+                            const __half2 pl1 = __hfma2(as_h2(bl.y), d1, __hfma2(as_h2(bh.y), d1, __hneg2(ph1)));
+                            uint32_t uh0 = as_u32(ph0), uh1 = as_u32(ph1), ul0 = as_u32(pl0), ul1 = as_u32(pl1);
+                            if (edge) {  // a scale that is NaN or infinite has no effect on rows that do not see it
+                                const int n = miss ? 0 : qlen_sm[8 * nt + g8] - tb - tok;
+                                const uint32_t m0 = (n > 0 ? 0xFFFFu : 0u) | (n > 1 ? 0xFFFF0000u : 0u);
+                                const uint32_t m1 = (n > 2 ? 0xFFFFu : 0u) | (n > 3 ? 0xFFFF0000u : 0u);
+                                uh0 &= m0, ul0 &= m0, uh1 &= m1, ul1 &= m1;
+                            }
+#pragma unroll
+                            for (int mt = 0; mt < 2; ++mt) {
+                                mma_m16n8k16(o[mt][nt], a[mt][0], a[mt][1], a[mt][2], a[mt][3], uh0, uh1);
+                                mma_m16n8k16(o[mt][nt], a[mt][0], a[mt][1], a[mt][2], a[mt][3], ul0, ul1);
+                            }
+                        }
+                }
+            } else {
+                const uint32_t pbase = smem_u32(Ph) + ((lane & 7) * PS + (lane >> 3) * 8) * 2;
+                const uint32_t vbase = smem_u32(vt) + ((lane & 7) + ((lane >> 4) << 3)) * 128;
+#pragma unroll
+                for (int ks = 0; ks < 4; ks += 2) {
+                    uint32_t a[2][MW][4];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int mt = 0; mt < MW; ++mt) {
+                            const int ch = 2 * (warp * MW + mt) + ((lane >> 3) & 1);
+                            ldmatrix_x4_trans(a[e][mt], vbase + (ch >> 3) * (kTile * 128) + (ks + e) * 16 * 128 +
+                                                            (((ch & 7) ^ (lane & 7)) << 4));
+                        }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        if (nt < nnt) {
+                            uint32_t bh[4], bl[4];
+                            ldmatrix_x4(bh, pbase + (nt * 8 * PS + ks * 16) * 2);
+                            ldmatrix_x4(bl, pbase + (QT * PS + nt * 8 * PS + ks * 16) * 2);
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                                for (int mt = 0; mt < MW; ++mt) {
+                                    mma16<BF>(o[mt][nt], a[e][mt][0], a[e][mt][1], a[e][mt][2], a[e][mt][3], bh[2 * e], bh[2 * e + 1]);
+                                    mma16<BF>(o[mt][nt], a[e][mt][0], a[e][mt][1], a[e][mt][2], a[e][mt][3], bl[2 * e], bl[2 * e + 1]);
+                                }
+                        }
+                }
+            }
+            parity ^= 1;
         }
         if (!live) break;
 
         // ---- the item's partial
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float sum = l[nt][e];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                l[nt][e] = sum;
+            }
+        __syncthreads();  // (the maxima in `red` are read)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (g8 == 0) red[(8 * nt + 2 * t4 + e) * 4 + warp] = l[nt][e];
+        __syncthreads();
         const int64_t slot0 = (static_cast<int64_t>(it.a * p.kv_heads + it.g) * p.chunks + it.tok0 / p.chunk) * p.qp + q0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int qi = 8 * nt + 2 * t4 + e;
-                float sum = l[nt][e];
-                sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 16);
                 if (q0 + qi >= nq) continue;
-                float* po = p.o + (slot0 + qi) * D;
+                float* po = p.o + (slot0 + qi) * D + 16 * warp * MW;
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
+                for (int mt = 0; mt < MW; ++mt) {
                     po[16 * mt + g8] = o[mt][nt][e];
                     po[16 * mt + g8 + 8] = o[mt][nt][2 + e];
                 }
-                if (g8 == 0) *reinterpret_cast<float2*>(p.ml + (slot0 + qi) * 2) = make_float2(mx[nt][e], sum);
-            }
-    }
-    if (!live) {
-        if (lane == 0) {
-            *abort_flag = 1;
-            atomicOr(p.err, kErrTimeout);
-            // let every copy still in flight land before the CTA exits
-            volatile int go_on = 0;
-            for (; taken < issued; ++taken) {
-                mbar_wait_bounded(bar + slot, phase, &go_on);
-                if (++slot == kSlots) {
-                    slot = 0;
-                    phase ^= 1;
+                if (warp == 0 && g8 == 0) {
+                    const float4 r = *reinterpret_cast<const float4*>(red + qi * 4);
+                    *reinterpret_cast<float2*>(p.ml + (slot0 + qi) * 2) = make_float2(mx[nt][e], (r.x + r.y) + (r.z + r.w));
                 }
             }
-        }
-        __syncwarp();
+    }
+    if (!live && warp == 0 && lane == 0) {
+        *abort_flag = 1;
+        atomicOr(p.err, kErrTimeout);
+        // let every copy still in flight land before the block exits
+        volatile int go_on = 0;
+        for (; taken < issued; next()) mbar_wait_bounded(bar + slot, phase, &go_on);
     }
 }
 
@@ -773,18 +758,24 @@ cudaError_t launch_attend_bf16(const AttendLaunch& a, cudaStream_t s);
 
 template <int FMT, int D, int NT>
 cudaError_t launch_attend_one(const AttendLaunch& a, cudaStream_t s) {
-    const int bytes = attend_smem<FMT, D>(a.p.agents);
+    const int bytes = Geo<FMT, D, NT>::smem(a.p.agents);
     cudaError_t e = cudaFuncSetAttribute(attend_partial<FMT, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    int per_sm = 0;
+    if (e == cudaSuccess)
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attend_partial<FMT, D, NT>, kThreads, bytes);
     if (e != cudaSuccess) return e;
-    attend_partial<FMT, D, NT><<<a.sms, kWarps * 32, bytes, s>>>(a.map, a.p);
+    if (per_sm < 1) return cudaErrorInvalidConfiguration;
+    attend_partial<FMT, D, NT><<<a.sms * per_sm, kThreads, bytes, s>>>(a.map, a.p);
     return cudaGetLastError();
 }
 
-// One column tile of queries, or the most that the registers hold.  (With 8 queries or fewer the
-// wide form would carry the registers of empty column tiles.)
+// The fewest column tiles that take all queries of a sequence, up to the most whose state fits
+// the registers of three blocks per SM (two at D = 256); a wider instance would carry empty tiles.
 template <int FMT, int D>
 cudaError_t launch_attend_dim(const AttendLaunch& a, cudaStream_t s) {
-    return a.max_q <= 8 ? launch_attend_one<FMT, D, 1>(a, s) : launch_attend_one<FMT, D, Geo<FMT, D>::max_nt>(a, s);
+    if (a.max_q <= 8) return launch_attend_one<FMT, D, 1>(a, s);
+    if (a.max_q <= 24 || D == 256) return launch_attend_one<FMT, D, 3>(a, s);
+    return launch_attend_one<FMT, D, D == 256 ? 3 : 6>(a, s);
 }
 
 }  // namespace kv
