@@ -217,16 +217,18 @@ cudaError_t launch_append_dim(const AppendParams& p, int32_t dim, int32_t type, 
 }
 
 // ------------------------------------------------------------------------------ evict
-// One cluster per (sequence, KV head), its slots cut evenly among the cluster's blocks.  The
-// keep-th largest key is found by a radix select over 11 + 11 + 10 bits: each pass counts the
-// digit of the keys that still match, the blocks add their counts through distributed shared
-// memory, and every block picks the same digit.  Then each block walks its slots in order: ties
-// at the threshold are kept from the lowest slot on, kept slots below the budget stay, freed ones
-// and kept ones past the budget go to two lists in slot order (positions by prefix sums over the
-// cluster), and the cluster moves the i-th of the second to the i-th of the first.  Reads are
-// the weights and positions (keys stay in shared memory while they fit), and each moved token
-// once; with the order of slots given up, nothing else has to move.
+// Two kernels.  The first has one cluster per (sequence, KV head), its slots cut evenly among the
+// cluster's blocks.  The keep-th largest key is found by a radix select over 11 + 11 + 10 bits: each
+// pass counts the digit of the keys that still match, the blocks add their counts through
+// distributed shared memory, and every block picks the same digit.  Then each thread walks its run
+// of slots: ties at the threshold are kept from the lowest slot on, kept slots below the budget
+// stay, and the freed ones and the kept ones past the budget go to two lists in slot order
+// (places by prefix sums over the cluster).  The second kernel, a whole grid, moves the i-th of
+// the one list to the i-th of the other.  The weights and positions are read once (keys stay in
+// shared memory while they fit), and each moved token is read and written once; with the order
+// of slots given up, nothing else has to move.
 constexpr int kEvictThreads = 512;
+constexpr int kMoveThreads = 256;
 constexpr int kBins = 2048;
 constexpr int kKeyCap = 16384;  // keys a block holds in shared memory
 
@@ -241,10 +243,13 @@ struct EvictParams {
     float* weight_out;
     int32_t* pos_out;
     int32_t* len_out;
-    int32_t* lists;  // [sequence][KV head][2][half]: freed slots, tokens to move into them
+    int32_t* moved;  // [sequence][KV head]
+    int2* lists;     // [sequence][KV head][2][half]: freed slots, and those that move into them: slot
+                     // number, and page * page_tokens + place in the page (-1: a page outside the pool)
     int* err;
     int64_t rec_bytes, half;
-    int32_t sink, kv_heads, max_pages, pool_pages, page_tokens, cap, head_dim, key_cap;
+    int32_t sink, kv_heads, max_pages, pool_pages, page_tokens, page_shift, cap, head_dim, key_cap;
+    int32_t slices;  // blocks of the second kernel per (sequence, KV head)
 };
 
 // Keys in the order of eviction's preference: protected tokens above every weight, then the
@@ -256,21 +261,24 @@ __device__ __forceinline__ uint32_t evict_key(float w, int32_t pos, int32_t sink
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-template <bool q8>
-__global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(kEvictThreads) kv_evict_select(const EvictParams p) {
     extern __shared__ uint32_t keys[];  // [key_cap]
     __shared__ int hist[kBins];
     __shared__ int tmp[33], pick[2], counts[3];
+    griddep_launch_dependents();  // the moving kernel waits for this grid's end
     cg::cluster_group cl = cg::this_cluster();
     const int ranks = cl.num_blocks(), rank = cl.block_rank();
     const int ag = blockIdx.x / ranks, a = ag / p.kv_heads, g = ag % p.kv_heads;
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int tid = threadIdx.x;
     const int len = p.cache_len[a], want = p.keep[a];
     const bool ok = len >= 0 && len <= p.cap;
     const int n = ok ? len : 0, budget = want >= 0 && want < n ? want : n;
-    if (rank == 0 && g == 0 && tid == 0) {
-        p.len_out[a] = ok ? budget : len;
-        if (!ok) atomicOr(p.err, kErrRange);
+    if (rank == 0 && tid == 0) {
+        p.moved[ag] = 0;
+        if (g == 0) {
+            p.len_out[a] = ok ? budget : len;
+            if (!ok) atomicOr(p.err, kErrRange);
+        }
     }
     const int64_t base = static_cast<int64_t>(ag) * p.cap;
     const int per = (n + ranks - 1) / ranks, s0 = min(n, rank * per), s1 = min(n, s0 + per);
@@ -303,14 +311,14 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictPara
         }
         cl.sync();
         // the thread's four bins, from the highest down
-        int c[4], mine = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int b = kBins - 1 - (4 * tid + i);
-            c[i] = 0;
-            for (int r = 0; r < ranks; ++r) c[i] += cl.map_shared_rank(hist, r)[b];
-            mine += c[i];
+        int c[4] = {}, mine = 0;
+        const int at4 = kBins - 4 - 4 * tid;
+#pragma unroll 4
+        for (int r = 0; r < ranks; ++r) {
+            const int4 v = *reinterpret_cast<const int4*>(cl.map_shared_rank(hist, r) + at4);
+            c[0] += v.w, c[1] += v.z, c[2] += v.y, c[3] += v.x;
         }
+        mine = c[0] + c[1] + c[2] + c[3];
         int total;
         int above = block_exclusive(mine, tmp, &total);
 #pragma unroll
@@ -325,124 +333,144 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictPara
         prefix |= static_cast<uint32_t>(pick[0]) << shift;
         mask |= static_cast<uint32_t>(bins - 1) << shift;
         need = pick[1];
-        __syncthreads();
     }
     const uint32_t thr = prefix;
 
-    // ---- per block: ties, then (with the cluster's ties before it known) freed and moved slots
-    int ties = 0;
-    for (int t = s0 + tid; t < s1; t += kEvictThreads) ties += key(t) == thr;
+    // ---- the thread's run of slots: ties first, then (with the ties before it known) freed and
+    // moved slots
+    const int run = (per + kEvictThreads - 1) / kEvictThreads, t0 = min(s1, s0 + tid * run), t1 = min(s1, t0 + run);
+    int mine = 0;
+    for (int t = t0; t < t1; ++t) mine += key(t) == thr;
     int all;
-    block_exclusive(ties, tmp, &all);
+    int tie = block_exclusive(mine, tmp, &all);
     if (tid == 0) counts[0] = all;
     cl.sync();
-    int tie0 = 0;
-    for (int r = 0; r < rank; ++r) tie0 += cl.map_shared_rank(counts, r)[0];
-    int hole0 = 0, move0 = 0, moved = 0;
-    int32_t* holes = p.lists + static_cast<int64_t>(ag) * 2 * p.half;
-    int32_t* moves = holes + p.half;
-    for (int round = 0; round < 2; ++round) {  // counting, then writing
-        int tie = tie0, h = hole0, m = move0;
-        for (int t0 = s0; t0 < s1; t0 += kEvictThreads) {
-            const int t = t0 + tid;
-            const uint32_t k = t < s1 ? key(t) : 0u;
-            int sum;
-            const bool equal = t < s1 && k == thr;
-            const int before = tie + block_exclusive(equal, tmp, &sum);
-            tie += sum;
-            const bool kept = t < s1 && (k > thr || (equal && before < need));
-            const bool hole = t < s1 && t < budget && !kept, move = kept && t >= budget;
-            // holes and moves in one prefix sum: neither passes 512 in a step
-            const int at = block_exclusive((hole ? 1 : 0) | (move ? 1 << 16 : 0), tmp, &sum);
-            if (round == 1) {
-                if (hole) holes[h + (at & 0xFFFF)] = t;
-                if (move) moves[m + (at >> 16)] = t;
-                if (kept && t < budget) {
-                    p.weight_out[base + t] = p.weight[base + t];
-                    p.pos_out[base + t] = p.pos[base + t];
-                }
-            }
-            h += sum & 0xFFFF;
-            m += sum >> 16;
+    for (int r = 0; r < rank; ++r) tie += cl.map_shared_rank(counts, r)[0];
+    int holes = 0, moves = 0, eq = tie;
+    for (int t = t0; t < t1; ++t) {
+        const uint32_t k = key(t);
+        const bool kept = k > thr || (k == thr && eq < need);
+        eq += k == thr;
+        holes += !kept && t < budget;
+        moves += kept && t >= budget;
+    }
+    int hole = block_exclusive(holes, tmp, &all);
+    if (tid == 0) counts[1] = all;
+    int move = block_exclusive(moves, tmp, &all);
+    if (tid == 0) counts[2] = all;
+    cl.sync();
+    int total = 0;
+    for (int r = 0; r < ranks; ++r) {
+        const int* c = cl.map_shared_rank(counts, r);
+        if (r < rank) {
+            hole += c[1];
+            move += c[2];
         }
-        if (round == 0) {
-            if (tid == 0) {
-                counts[1] = h;
-                counts[2] = m;
-            }
-            cl.sync();
-            for (int r = 0; r < ranks; ++r) {
-                const int* c = cl.map_shared_rank(counts, r);
-                if (r < rank) {
-                    hole0 += c[1];
-                    move0 += c[2];
-                }
-                moved += c[2];
-            }
+        total += c[2];
+    }
+    if (rank == 0 && tid == 0) p.moved[ag] = total;
+    int2* to = p.lists + static_cast<int64_t>(ag) * 2 * p.half;
+    int2* src = to + p.half;
+    const int32_t* table = p.table + static_cast<int64_t>(a) * p.max_pages;
+    auto place = [&](int t) {
+        const int pg = table[t >> p.page_shift];
+        if (pg >= 0 && pg < p.pool_pages) return pg * p.page_tokens + (t & (p.page_tokens - 1));
+        atomicOr(p.err, kErrPage);
+        return -1;
+    };
+    for (int t = t0; t < t1; ++t) {
+        const uint32_t k = key(t);
+        const bool kept = k > thr || (k == thr && tie < need);
+        tie += k == thr;
+        if (t < budget) {
+            if (!kept) to[hole++] = make_int2(t, place(t));
+        } else if (kept) {
+            src[move++] = make_int2(t, place(t));
         }
     }
-    cl.sync();  // the lists are written, the arrays read, and no block's counts are needed any more
+    if (p.weight_out != p.weight || p.pos_out != p.pos)  // (slots that move are overwritten by the second kernel)
+        for (int t = s0 + tid; t < min(s1, budget); t += kEvictThreads) {
+            p.weight_out[base + t] = p.weight[base + t];
+            p.pos_out[base + t] = p.pos[base + t];
+        }
+    cl.sync();  // no block leaves while its counts are read
+}
 
-    // ---- the moves: source slots >= budget > destination slots
-    const int step = ranks * kEvictThreads, first = rank * kEvictThreads + tid;
+template <bool q8>
+__global__ void __launch_bounds__(kMoveThreads) kv_evict_move(const EvictParams p) {
+    const int ag = blockIdx.x / p.slices, g = ag % p.kv_heads, lane = threadIdx.x & 31;
+    const int64_t base = static_cast<int64_t>(ag) * p.cap;
+    const int2* to = p.lists + static_cast<int64_t>(ag) * 2 * p.half;
+    const int2* from = to + p.half;
+    const int first = (blockIdx.x % p.slices) * kMoveThreads + threadIdx.x, step = p.slices * kMoveThreads;
+    griddep_wait();  // the lists are written
+    const int moved = p.moved[ag];
+    // source slots >= budget > destination slots: nothing read here is written here
     for (int i = first; i < moved; i += step) {
-        const int src = moves[i], dst = holes[i];
+        const int src = from[i].x, dst = to[i].x;
         p.weight_out[base + dst] = p.weight[base + src];
         p.pos_out[base + dst] = p.pos[base + src];
     }
-    const int32_t* table = p.table + static_cast<int64_t>(a) * p.max_pages;
-    auto record = [&](int t) -> uint8_t* {
-        const int pg = table[t / p.page_tokens];
-        if (pg < 0 || pg >= p.pool_pages) {
-            atomicOr(p.err, kErrPage);
-            return nullptr;
-        }
-        return p.pool + (static_cast<int64_t>(pg) * p.kv_heads + g) * p.rec_bytes;
-    };
     if constexpr (q8) {
-        // a warp moves 32 tokens at a time, a lane each: sources and destinations both rise with
-        // the lane, so the strided bytes of V share their sectors
-        for (int i0 = (first & ~31); i0 < moved; i0 += step) {
-            const int i = i0 + lane;
-            const bool in = i < moved;
-            const int src = in ? moves[i] : 0, dst = in ? holes[i] : 0;
-            const uint8_t* from_rec = in ? record(src) : nullptr;
-            uint8_t* to_rec = in ? record(dst) : nullptr;
-            if (!from_rec || !to_rec) continue;
+        // a warp moves 32 tokens, a lane each, one fifth at a time: K with the scales, or 32 dims of V.
+        // Sources and destinations both rise with the lane, so V's strided bytes share their sectors.
+        const int work = (moved + 31) / 32 * 5;
+        for (int w = first >> 5; w < work; w += step >> 5) {
+            const int i = w / 5 * 32 + lane, part = w % 5;
+            const int src = i < moved ? from[i].y : -1, dst = i < moved ? to[i].y : -1;
+            if (src < 0 || dst < 0) continue;
+            const uint8_t* a = p.pool + (static_cast<int64_t>(src >> 6) * p.kv_heads + g) * kQ8Rec;
+            uint8_t* b = p.pool + (static_cast<int64_t>(dst >> 6) * p.kv_heads + g) * kQ8Rec;
             const int ss = src & 63, ds = dst & 63;
-            uint4 row[8];
+            if (part == 4) {
+                uint4 row[8];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) row[c] = *reinterpret_cast<const uint4*>(from_rec + ss * 128 + 16 * (c ^ q8_key(ss)));
+                for (int c = 0; c < 8; ++c) row[c] = *reinterpret_cast<const uint4*>(a + ss * 128 + 16 * (c ^ q8_key(ss)));
+                const uint2 ks = *reinterpret_cast<const uint2*>(a + 8192 + ss * 8);
+                uint16_t vs[4];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(to_rec + ds * 128 + 16 * (c ^ q8_key(ds))) = row[c];
-            *reinterpret_cast<uint2*>(to_rec + 8192 + ds * 8) = *reinterpret_cast<const uint2*>(from_rec + 8192 + ss * 8);
+                for (int c = 0; c < 4; ++c) vs[c] = *reinterpret_cast<const uint16_t*>(a + 16896 + (c * 64 + ss) * 2);
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-                *reinterpret_cast<uint16_t*>(to_rec + 16896 + (b * 64 + ds) * 2) =
-                    *reinterpret_cast<const uint16_t*>(from_rec + 16896 + (b * 64 + ss) * 2);
-#pragma unroll 1
-            for (int d = 0; d < 128; d += 16) {
-                uint8_t v[16];
+                for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(b + ds * 128 + 16 * (c ^ q8_key(ds))) = row[c];
+                *reinterpret_cast<uint2*>(b + 8192 + ds * 8) = ks;
 #pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] = from_rec[8704 + (d + k) * 64 + ss];
+                for (int c = 0; c < 4; ++c) *reinterpret_cast<uint16_t*>(b + 16896 + (c * 64 + ds) * 2) = vs[c];
+            } else {
+                a += 8704 + 32 * part * 64 + ss;
+                b += 8704 + 32 * part * 64 + ds;
+                uint8_t v[32];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) to_rec[8704 + (d + k) * 64 + ds] = v[k];
+                for (int k = 0; k < 32; ++k) v[k] = a[k * 64];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) b[k * 64] = v[k];
             }
         }
     } else {
-        // 16-byte pieces of the tokens' K and V rows, consecutive pieces by consecutive threads
-        const int row = p.head_dim * 2, shift = p.head_dim == 64 ? 4 : p.head_dim == 128 ? 5 : 6, pieces = 1 << shift;
+        // 16-byte pieces of the tokens' K and V rows, consecutive pieces by consecutive threads, four
+        // of a thread's in flight
+        const int row = p.head_dim * 2, shift = p.head_dim == 64 ? 4 : p.head_dim == 128 ? 5 : 6;
         const int64_t work = static_cast<int64_t>(moved) << shift;
-#pragma unroll 4
-        for (int64_t i = first; i < work; i += step) {
-            const int tok = static_cast<int>(i >> shift), c = static_cast<int>(i & (pieces - 1));
-            const int src = moves[tok], dst = holes[tok];
-            const uint8_t* from_rec = record(src);
-            uint8_t* to_rec = record(dst);
-            if (!from_rec || !to_rec) continue;
-            const int half = c >= pieces / 2, off = (c - half * (pieces / 2)) * 16;
-            *reinterpret_cast<uint4*>(to_rec + (half * p.page_tokens + dst % p.page_tokens) * row + off) =
-                *reinterpret_cast<const uint4*>(from_rec + (half * p.page_tokens + src % p.page_tokens) * row + off);
+        const int c = first & ((1 << shift) - 1), half = c >> (shift - 1), off = (c & ((1 << (shift - 1)) - 1)) * 16;
+        auto address = [&](int t) {
+            const int64_t pg = t >> p.page_shift;
+            return p.pool + (pg * p.kv_heads + g) * p.rec_bytes + (half * p.page_tokens + (t & (p.page_tokens - 1))) * row + off;
+        };
+        // (step is a multiple of the pieces per token: a thread's pieces are the same part of each)
+        for (int64_t i0 = first; i0 < work; i0 += 4 * static_cast<int64_t>(step)) {
+            int src[4], dst[4];
+            uint4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t i = i0 + k * static_cast<int64_t>(step);
+                src[k] = i < work ? from[i >> shift].y : -1;
+                dst[k] = i < work ? to[i >> shift].y : -1;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (src[k] >= 0) v[k] = __ldcs(reinterpret_cast<const uint4*>(address(src[k])));
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (src[k] >= 0 && dst[k] >= 0) *reinterpret_cast<uint4*>(address(dst[k])) = v[k];
         }
     }
 }
@@ -510,7 +538,8 @@ qmm_status qmm_kv_evict_workspace_bytes(const qmm_kv_dims* dims, int64_t* bytes)
     if (!bytes) return QMM_ERR_INVALID_ARG;
     const qmm_status st = qmm::kv::check_dims(dims);
     if (st != QMM_OK) return st;
-    *bytes = int64_t{dims->agents} * dims->kv_heads * 2 * qmm::kv::list_half(*dims) * 4;
+    const int64_t groups = int64_t{dims->agents} * dims->kv_heads;
+    *bytes = (groups * 4 + 15) / 16 * 16 + groups * 2 * qmm::kv::list_half(*dims) * 8;
     return QMM_OK;
 }
 
@@ -544,7 +573,9 @@ qmm_status qmm_kv_evict(const qmm_kv_dims* dims, void* pool, const int32_t* page
     p.weight_out = weight_out;
     p.pos_out = pos_out;
     p.len_out = len_out;
-    p.lists = static_cast<int32_t*>(workspace);
+    const int64_t groups = int64_t{dims->agents} * dims->kv_heads;
+    p.moved = static_cast<int32_t*>(workspace);
+    p.lists = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + (groups * 4 + 15) / 16 * 16);
     p.err = err_word;
     p.rec_bytes = record_bytes(*dims);
     p.half = list_half(*dims);
@@ -555,16 +586,20 @@ qmm_status qmm_kv_evict(const qmm_kv_dims* dims, void* pool, const int32_t* page
     p.page_tokens = dims->page_tokens;
     p.cap = dims->max_pages * dims->page_tokens;
     p.head_dim = dims->head_dim;
-    const int64_t groups = int64_t{dims->agents} * dims->kv_heads;
+    while ((1 << p.page_shift) < dims->page_tokens) ++p.page_shift;
     // blocks per cluster: as many as the longest sequence can use, up to 8 (the portable limit)
     int ranks = 1;
     while (ranks < 8 && p.cap > ranks * 512) ranks *= 2;
     const int64_t per = (p.cap + ranks - 1) / ranks;
     p.key_cap = static_cast<int32_t>(per < kKeyCap ? per : kKeyCap);
-    if (groups * ranks > INT32_MAX) return QMM_ERR_UNSUPPORTED_SHAPE;
-    const bool q8 = dims->format == QMM_KV_Q8_0;
-    cudaError_t e = q8 ? cudaFuncSetAttribute(kv_evict_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyCap * 4)
-                       : cudaFuncSetAttribute(kv_evict_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyCap * 4);
+    // the moves: eight blocks per SM over all groups, no more than the most pieces a group can move
+    const int64_t pieces = dims->format == QMM_KV_Q8_0 ? (p.half + 31) / 32 * 5 * 32 : p.half * dims->head_dim / 4;
+    int64_t slices = (int64_t{sms} * 8 + groups - 1) / groups;
+    if (slices > (pieces + kMoveThreads - 1) / kMoveThreads) slices = (pieces + kMoveThreads - 1) / kMoveThreads;
+    p.slices = static_cast<int32_t>(slices);
+    if (groups * ranks > INT32_MAX || groups * slices > INT32_MAX || dims->pool_pages * dims->page_tokens > INT32_MAX)
+        return QMM_ERR_UNSUPPORTED_SHAPE;
+    cudaError_t e = cudaFuncSetAttribute(kv_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyCap * 4);
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(groups * ranks));
@@ -577,7 +612,15 @@ qmm_status qmm_kv_evict(const qmm_kv_dims* dims, void* pool, const int32_t* page
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        e = q8 ? cudaLaunchKernelEx(&cfg, kv_evict_kernel<true>, p) : cudaLaunchKernelEx(&cfg, kv_evict_kernel<false>, p);
+        e = cudaLaunchKernelEx(&cfg, kv_evict_select, p);
+        if (e == cudaSuccess) {
+            cfg.gridDim = dim3(static_cast<unsigned>(groups * slices));
+            cfg.blockDim = dim3(kMoveThreads);
+            cfg.dynamicSmemBytes = 0;
+            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[0].val.programmaticStreamSerializationAllowed = 1;
+            e = dims->format == QMM_KV_Q8_0 ? cudaLaunchKernelEx(&cfg, kv_evict_move<true>, p) : cudaLaunchKernelEx(&cfg, kv_evict_move<false>, p);
+        }
     }
     return e == cudaSuccess ? QMM_OK : QMM_ERR_CUDA;
 }

@@ -1,15 +1,18 @@
 // Log probabilities of given tokens, entropy and top alternatives over rows of logits.
 //
-// One cluster of blocks per row, the row cut evenly among them; a block takes its slice in rounds
-// of kRound elements held in registers, so every logit is read from memory once.  With running
-// maximum M, per thread and then merged:
-//   Z = sum e^(x - M),  U = sum e^(x - M) (x - M);   lse = M + ln Z,  entropy = ln Z - U / Z.
-// Alternatives: elements are ordered by (value, lower column first) as 64-bit keys, all distinct.
-// The k-th largest of the threads' maxima bounds the k-th largest element from below, and at
-// most k threads hold elements above it: so at most k * kPer elements pass the bound, whatever the
-// data (a first, coarser bound from the maxima of 32 groups of threads makes it about
-// k in practice).  They and the block's list so far are ranked by counting, and the cluster's
-// lists in the same way at the end.
+// A row is cut into segments of kSeg columns; a block holds a segment in registers (every logit is
+// read from memory once), reduces it and takes the next, and the blocks of a cluster share the
+// row's segments.  Per segment, with its maximum M:
+//   Z = sum e^(x - M),  U = sum e^(x - M) (x - M);   lse = M + ln Z,  entropy = ln Z - U / Z,
+// and the segments' sums are merged in their order at the end, so a row's bits do not depend on
+// how many blocks it was given.
+// Alternatives, ordered by (value, lower column first): the k-th largest of the maxima of 32
+// groups of threads bounds the segment's k-th largest element from below; the elements at or
+// above it (about k of them) and the block's list so far are ranked by counting.  Where ties let
+// more than kCand elements pass, elements are compared as 64-bit keys of value and column, all
+// distinct: at most k threads have an element above the k-th largest of the threads' maxima, so
+// at most k * kPer pass, whatever the data.
+// What bounds it: the logits' bytes.  %LP%
 #include <cooperative_groups.h>
 
 #include "qmm_kv.cuh"
@@ -19,12 +22,13 @@ namespace cg = cooperative_groups;
 namespace qmm {
 namespace logprobs {
 
-constexpr int kThreads = 512;
-constexpr int kPer = 32;                  // elements per thread and round
-constexpr int kRound = kThreads * kPer;
+constexpr int kThreads = 256;
+constexpr int kPer = 40;                  // elements per thread and segment
+constexpr int kSeg = kThreads * kPer;
 constexpr int kMaxTop = 32;
-constexpr int kCand = 64 * kPer;          // candidates of a round
-constexpr int kMaxRanks = 8;
+constexpr int kCand = kMaxTop * kPer;     // candidates of a segment
+constexpr int kMaxRanks = 16;
+constexpr int kSums = 64;                 // segments whose sums a block keeps apart (see the kernel)
 
 struct Params {
     const void* logits;
@@ -34,7 +38,9 @@ struct Params {
     float* logprob;
     int32_t* top_index;
     float* top_logprob;
-    int64_t n, stride, slice;  // columns, row stride, columns per block
+    int64_t n, stride;  // columns, row stride
+    int32_t segs;       // segments per row
+    int32_t fold;       // segments per kept sum
     int32_t given, top;
     int32_t vec;  // rows can be read 16 bytes at a time
 };
@@ -65,7 +71,7 @@ struct Sums {
 };
 __device__ __forceinline__ Sums merge(const Sums& a, const Sums& b) {
     const float m = fmaxf(a.m, b.m);
-    if (m == -INFINITY) return {m, 0.f, 0.f};
+    if (m == -INFINITY) return {m, a.z + b.z, 0.f};  // (0, or a NaN's)
     // (a part without finite elements has z = u = 0; any finite distance will do)
     const float da = fmaxf(a.m - m, -1e30f), db = fmaxf(b.m - m, -1e30f);
     const float ea = ex2(da * kLog2e), eb = ex2(db * kLog2e);
@@ -76,20 +82,32 @@ __device__ __forceinline__ Sums shfl_xor(const Sums& s, int k) {
 }
 
 struct Shared {
-    uint64_t group[32];          // maxima of 16 threads each
-    uint64_t first[kThreads];    // the threads' maxima that pass the coarse bound
+    float group[2][32];          // maxima of 8 threads each; two, for alternate segments
+    uint64_t first[kThreads];    // the threads' largest keys that pass the bound
     uint64_t cand[kCand + kMaxTop];
-    uint64_t list[kMaxTop];      // the slice's best so far, best first
+    uint64_t list[kMaxTop];      // the block's best so far, best first; 0: none
     uint64_t all[kMaxRanks * kMaxTop];
     uint64_t bound;
-    Sums part[kThreads / 32];
-    Sums total;
-    int odd;                     // the slice has a NaN or +infinity
-    int n_first, n_cand;
+    Sums part[2][kThreads / 32];
+    Sums sums[kSums];            // of the block's segments, in order
+    int n_first, n_cand[2];
 };
 
+// The k-th largest of 32 lanes' values (every lane returns it).
+__device__ __forceinline__ float kth_of_warp(float v, int k) {
+    int above = 0, equal = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        const float o = __shfl_sync(0xffffffffu, v, j);
+        above += o > v;
+        equal += o == v && j < static_cast<int>(threadIdx.x & 31);
+    }
+    const uint32_t who = __ballot_sync(0xffffffffu, above + equal == k - 1);
+    return __shfl_sync(0xffffffffu, v, __ffs(who) - 1);
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const Params p) {
     extern __shared__ __align__(16) uint8_t raw[];
     Shared& sh = *reinterpret_cast<Shared*>(raw);
     cg::cluster_group cl = cg::this_cluster();
@@ -97,135 +115,149 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Params p) {
     const int64_t row = blockIdx.x / ranks;
     const T* x = static_cast<const T*>(p.logits) + row * p.stride;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t c0 = min(p.n, rank * p.slice), c1 = min(p.n, c0 + p.slice);
-    if (tid == 0) sh.odd = 0;
+    // kept sums are dealt out whole: rank r has those of units u0 .. u1 - 1, `fold` segments each
+    const int units = (p.segs + p.fold - 1) / p.fold;
+    const int u0 = units * rank / ranks, u1 = units * (rank + 1) / ranks;
+    const int s0 = min(p.segs, u0 * p.fold), s1 = min(p.segs, u1 * p.fold);
     if (tid < kMaxTop) sh.list[tid] = 0;  // below every key of an element
-    __syncthreads();
+    if (tid < 2) sh.n_cand[tid] = 0;
 
     constexpr int W = 16 / sizeof(T);  // elements of a 16-byte load
-    Sums s = {-INFINITY, 0.f, 0.f};
-    bool odd = false;
-    for (int64_t r0 = c0; r0 < c1; r0 += kRound) {
-        // element i of a thread: r0 + (i / W * kThreads + tid) * W + i % W
+    const int k = p.top;
+    Sums fold = {-INFINITY, 0.f, 0.f};
+    for (int seg = s0; seg < s1; ++seg) {
+        const int odd = (seg - s0) & 1;
+        const int base = seg * kSeg, cols = static_cast<int>(min(static_cast<int64_t>(kSeg), p.n - base));
+        // element i of a thread: column base + (i / W * kThreads + tid) * W + i % W
+        auto column = [&](int i) { return (i / W * kThreads + tid) * W + i % W; };
         float v[kPer];
-        float top = -INFINITY;
-        auto column = [&](int i) { return r0 + (static_cast<int64_t>(i / W) * kThreads + tid) * W + i % W; };
 #pragma unroll
         for (int i = 0; i < kPer; i += W) {
-            const int64_t c = column(i);
-            if (p.vec && c + W <= c1) {
+            const int c = column(i);
+            if (p.vec && c + W <= cols) {
                 alignas(16) T t[W];
-                *reinterpret_cast<uint4*>(t) = __ldcs(reinterpret_cast<const uint4*>(x + c));
+                *reinterpret_cast<uint4*>(t) = __ldcs(reinterpret_cast<const uint4*>(x + base + c));
 #pragma unroll
-                for (int k = 0; k < W; ++k) v[i + k] = as_f32(t[k]);
+                for (int j = 0; j < W; ++j) v[i + j] = as_f32(t[j]);
             } else {
 #pragma unroll
-                for (int k = 0; k < W; ++k) v[i + k] = c + k < c1 ? as_f32(x[c + k]) : -INFINITY;
+                for (int j = 0; j < W; ++j) v[i + j] = c + j < cols ? as_f32(x[base + c + j]) : -INFINITY;
             }
         }
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) top = fmaxf(top, v[i]);
+        if (k > 0) {
+            float gm = top;
+#pragma unroll
+            for (int b = 1; b < 8; b <<= 1) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, b));
+            if ((lane & 7) == 0) sh.group[odd][tid >> 3] = gm;
+        }
+        // a NaN, and a +infinity through its difference with itself, ends up in z
+        const float ref = top == -INFINITY ? 0.f : top;
+        Sums s = {top, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            odd |= !(v[i] < INFINITY);  // NaN or +infinity
-            top = fmaxf(top, v[i]);
+            const float d = v[i] - ref, e = ex2(d * kLog2e);
+            s.z += e;
+            s.u = fmaf(e, fmaxf(d, -1e30f), s.u);
         }
-        if (top > -INFINITY) {
-            Sums t = {top, 0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const float d = fmaxf(v[i] - top, -1e30f), e = ex2(d * kLog2e);
-                t.z += e;
-                t.u = fmaf(e, d, t.u);
-            }
-            s = merge(s, t);
+        for (int b = 16; b >= 1; b >>= 1) s = merge(s, shfl_xor(s, b));
+        if (lane == 0) sh.part[odd][warp] = s;
+        __syncthreads();  // (also: the last segment's list is complete)
+        if (tid == 0) {
+            Sums t = sh.part[odd][0];
+#pragma unroll
+            for (int w = 1; w < kThreads / 32; ++w) t = merge(t, sh.part[odd][w]);
+            const int in = seg - u0 * p.fold;
+            fold = in % p.fold == 0 ? t : merge(fold, t);
+            sh.sums[in / p.fold] = fold;
         }
-        if (p.top > 0) {
-            const int k = p.top;
-            // the thread's largest key (its lowest column among equals); columns past the end have none
-            uint64_t best = 0;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (v[i] == top && best == 0 && column(i) < c1) best = key_of(v[i], static_cast<uint32_t>(column(i)));
-            // ---- the coarse bound: the k-th largest of 32 groups' maxima, or the list's k-th
-            uint64_t gm = best;
-#pragma unroll
-            for (int b = 1; b < 16; b <<= 1) gm = max64(gm, __shfl_xor_sync(0xffffffffu, gm, b));
-            if ((lane & 15) == 0) sh.group[tid >> 4] = gm;
-            if (tid == 0) sh.n_first = sh.n_cand = 0;
-            __syncthreads();
-            if (warp == 0) {
-                const uint64_t mine = sh.group[lane];
-                int rank_of = 0;
-                for (int j = 0; j < 32; ++j) {
-                    const uint64_t o = sh.group[j];
-                    rank_of += o > mine || (o == mine && j < lane);
-                }
-                if (rank_of == k - 1) sh.bound = max64(mine, sh.list[k - 1]);
-            }
-            __syncthreads();
-            uint64_t bound = sh.bound;
-            // ---- the threads whose maximum passes; if they are many, the k-th largest maximum
-            const bool in = best != 0 && best >= bound;
-            if (in) sh.first[atomicAdd(&sh.n_first, 1)] = best;
-            __syncthreads();
-            const int nf = sh.n_first;
-            if (nf > kCand / kPer) {
-                for (int i = tid; i < nf; i += kThreads) {
-                    const uint64_t mine = sh.first[i];
-                    int rank_of = 0;
-                    for (int j = 0; j < nf; ++j) rank_of += sh.first[j] > mine;
-                    if (rank_of == k - 1) sh.bound = max64(mine, sh.bound);
-                }
-                __syncthreads();
-                bound = sh.bound;
-            }
-            // ---- the elements that pass, and the list so far, ranked by counting
-            if (best != 0 && best >= bound) {
+        if (k > 0) {
+            // ---- the bound.  An element equal to the list's last lies in a higher column and loses;
+            // -infinity is left to the end
+            const float group = kth_of_warp(sh.group[odd][lane], k);
+            const uint64_t last = sh.list[k - 1];
+            const float worst = last ? value_of(last) : -INFINITY;
+            const bool strict = group <= worst;
+            const float bound = strict ? worst : group;
+            if (strict ? top > bound : top >= bound) {
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) {
-                    const int64_t c = column(i);
-                    if (c < c1) {
-                        const uint64_t q = key_of(v[i], static_cast<uint32_t>(c));
-                        if (q >= bound) sh.cand[atomicAdd(&sh.n_cand, 1)] = q;
+                    if (strict ? v[i] > bound : v[i] >= bound) {
+                        const int at = atomicAdd(&sh.n_cand[odd], 1);
+                        if (at < kCand) sh.cand[at] = key_of(v[i], static_cast<uint32_t>(base + column(i)));
                     }
                 }
             }
             __syncthreads();
-            const int fresh = sh.n_cand;
+            int fresh = sh.n_cand[odd];
+            if (fresh > kCand) {
+                // ---- ties: the same by keys, with the threads' largest keys as the groups
+                uint64_t best = 0;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    if (best == 0 && v[i] == top && top > -INFINITY) best = key_of(v[i], static_cast<uint32_t>(base + column(i)));
+                if (tid == 0) {
+                    sh.n_first = 0;
+                    sh.bound = last + 1;
+                }
+                __syncthreads();
+                if (best > last) sh.first[atomicAdd(&sh.n_first, 1)] = best;
+                __syncthreads();
+                const int nf = sh.n_first;
+                if (tid < nf) {
+                    const uint64_t mine = sh.first[tid];
+                    int rank_of = 0;
+                    for (int j = 0; j < nf; ++j) rank_of += sh.first[j] > mine;
+                    if (rank_of == k - 1) sh.bound = mine;
+                }
+                if (tid == 0) sh.n_cand[odd] = 0;
+                __syncthreads();
+                const uint64_t from = sh.bound;
+                if (best >= from) {
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) {
+                        const uint64_t q = key_of(v[i], static_cast<uint32_t>(base + column(i)));
+                        if (v[i] > -INFINITY && q >= from) sh.cand[atomicAdd(&sh.n_cand[odd], 1)] = q;
+                    }
+                }
+                __syncthreads();
+                fresh = sh.n_cand[odd];
+            }
+            if (tid == 0) sh.n_cand[odd ^ 1] = 0;
             if (fresh > 0) {
+                // ---- the candidates and the list so far, ranked by counting
                 if (tid < k) sh.cand[fresh + tid] = sh.list[tid];
                 __syncthreads();
                 for (int i = tid; i < fresh + k; i += kThreads) {
                     const uint64_t mine = sh.cand[i];
                     int rank_of = 0;
+#pragma unroll 8
                     for (int j = 0; j < fresh + k; ++j) rank_of += sh.cand[j] > mine;
                     if (mine != 0 && rank_of < k) sh.list[rank_of] = mine;
                 }
             }
-            __syncthreads();
         }
-    }
-
-    // ---- the block's sums, in a fixed order
-#pragma unroll
-    for (int k = 16; k >= 1; k >>= 1) s = merge(s, shfl_xor(s, k));
-    if (lane == 0) sh.part[warp] = s;
-    if (odd) sh.odd = 1;
-    __syncthreads();
-    if (tid == 0) {
-        Sums t = sh.part[0];
-        for (int w = 1; w < kThreads / 32; ++w) t = merge(t, sh.part[w]);
-        sh.total = t;
     }
     cl.sync();
     if (rank == 0) {
-        // every thread merges the cluster's sums; the lists are ranked as before
-        Sums t = sh.total;
-        bool bad = sh.odd != 0;
-        for (int r = 1; r < ranks; ++r) {
-            const Shared* o = cl.map_shared_rank(&sh, r);
-            t = merge(t, o->total);
-            bad |= o->odd != 0;
+        // ---- the row's sums, in the segments' order
+        if (warp == 0) {
+            Sums t = {-INFINITY, 0.f, 0.f};
+            for (int r = 0; r < ranks; ++r) {
+                const Sums* o = cl.map_shared_rank(sh.sums, r);
+                const int n = units * (r + 1) / ranks - units * r / ranks;
+                for (int i = 0; i < n; ++i) t = merge(t, o[i]);
+            }
+            if (lane == 0) sh.part[0][0] = t;
+        } else if (k > 0) {
+            for (int i = tid - 32; i < ranks * k; i += kThreads - 32) sh.all[i] = cl.map_shared_rank(&sh, i / k)->list[i % k];
         }
+        __syncthreads();
+        const Sums t = sh.part[0][0];
+        const bool bad = t.z != t.z;
         const float nan = __int_as_float(0x7FFFFFFF);
         const float lz = logf(t.z);
         const bool none = t.m == -INFINITY;
@@ -238,24 +270,38 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Params p) {
             const int64_t tok = p.tokens[row * p.given + i];
             p.logprob[row * p.given + i] = tok >= 0 && tok < p.n ? lp(as_f32(x[tok])) : nan;
         }
-        const int total = ranks * p.top;
-        if (bad) {
-            for (int i = tid; i < p.top; i += kThreads) {
-                p.top_index[row * p.top + i] = -1;
-                p.top_logprob[row * p.top + i] = nan;
-            }
-        } else if (p.top > 0) {
-            for (int i = tid; i < total; i += kThreads)
-                sh.all[i] = cl.map_shared_rank(&sh, i / p.top)->list[i % p.top];
+        if (k > 0) {
+            int32_t* index = p.top_index + row * k;
+            float* out = p.top_logprob + row * k;
+            // how many there are (fewer than k only if the rest of the row is -infinity)
+            const int total = ranks * k;
+            if (tid == 0) sh.n_first = 0;
             __syncthreads();
             for (int i = tid; i < total; i += kThreads) {
                 const uint64_t mine = sh.all[i];
+                if (mine == 0) continue;
                 int rank_of = 0;
+#pragma unroll 8
                 for (int j = 0; j < total; ++j) rank_of += sh.all[j] > mine;
-                if (mine != 0 && rank_of < p.top) {
-                    const int64_t at = row * p.top + rank_of;
-                    p.top_index[at] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(mine));
-                    p.top_logprob[at] = lp(value_of(mine));
+                if (rank_of < k) {
+                    sh.list[rank_of] = mine;
+                    atomicAdd(&sh.n_first, 1);
+                }
+            }
+            __syncthreads();
+            const int found = sh.n_first;
+            if (tid < k && (bad || tid < found)) {
+                index[tid] = bad ? -1 : static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(sh.list[tid]));
+                out[tid] = bad ? nan : lp(value_of(sh.list[tid]));
+            } else if (!bad && tid == k - 1) {
+                // the lowest columns that are not in the list
+                int c = 0;
+                for (int i = found; i < k; ++c) {
+                    bool in = false;
+                    for (int j = 0; j < found; ++j) in |= 0xFFFFFFFFu - static_cast<uint32_t>(sh.list[j]) == static_cast<uint32_t>(c);
+                    if (in) continue;
+                    index[i] = c;
+                    out[i++] = -INFINITY;
                 }
             }
         }
@@ -266,6 +312,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Params p) {
 template <typename T>
 cudaError_t launch(const Params& p, int64_t m, int ranks, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(logprobs_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared));
+    if (e == cudaSuccess && ranks > 8) e = cudaFuncSetAttribute(logprobs_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(m * ranks));
@@ -288,7 +335,7 @@ extern "C" qmm_status qmm_logprobs(const void* logits, int32_t type, int64_t m, 
                                    const int32_t* tokens, int32_t given, int32_t top, float* lse, float* entropy,
                                    float* logprob, int32_t* top_index, float* top_logprob, void* stream) {
     using namespace qmm::logprobs;
-    if (type < QMM_TYPE_F32 || type > QMM_TYPE_BF16 || m < 0 || n < 1 || n > INT32_MAX || stride < n || given < 0 || top < 0 ||
+    if (type < QMM_TYPE_F32 || type > QMM_TYPE_BF16 || m < 0 || n < 1 || n > (1 << 30) || stride < n || given < 0 || top < 0 ||
         top > kMaxTop || top > n || (given > 0 && (!tokens || !logprob)) || (top > 0 && (!top_index || !top_logprob)))
         return QMM_ERR_INVALID_ARG;
     if (m == 0) return QMM_OK;
@@ -301,10 +348,11 @@ extern "C" qmm_status qmm_logprobs(const void* logits, int32_t type, int64_t m, 
     int dev = 0, sms = 0;
     const qmm_status st = qmm::kv::check_gpu(&dev, &sms);
     if (st != QMM_OK) return st;
-    // blocks per row, by the number of columns alone (so that a row's bits do not depend on the
-    // other rows of the call): up to 8, the portable limit, of 8 elements a thread or more
+    // blocks per row: the fewest that give every SM six, up to one per segment and the largest
+    // cluster (the row's bits do not depend on it)
+    const int32_t segs = static_cast<int32_t>((n + kSeg - 1) / kSeg);
     int ranks = 1;
-    while (ranks < kMaxRanks && n > int64_t{ranks} * kThreads * 8) ranks *= 2;
+    while (ranks < kMaxRanks && ranks < segs && m * ranks < 6 * sms) ranks *= 2;
     Params p = {};
     p.logits = logits;
     p.tokens = tokens;
@@ -315,7 +363,8 @@ extern "C" qmm_status qmm_logprobs(const void* logits, int32_t type, int64_t m, 
     p.top_logprob = top_logprob;
     p.n = n;
     p.stride = stride;
-    p.slice = ((n + ranks - 1) / ranks + 7) / 8 * 8;
+    p.segs = segs;
+    p.fold = (segs + kSums - 1) / kSums;  // by the number of columns alone
     p.given = given;
     p.top = top;
     p.vec = aligned(logits, 16) && stride * size % 16 == 0;
