@@ -7,12 +7,17 @@
 // and the segments' sums are merged in their order at the end, so a row's bits do not depend on
 // how many blocks it was given.
 // Alternatives, ordered by (value, lower column first): the k-th largest of the maxima of 32
-// groups of threads bounds the segment's k-th largest element from below; the elements at or
-// above it (about k of them) and the block's list so far are ranked by counting.  Where ties let
-// more than kCand elements pass, elements are compared as 64-bit keys of value and column, all
-// distinct: at most k threads have an element above the k-th largest of the threads' maxima, so
-// at most k * kPer pass, whatever the data.
-// What bounds it: the logits' bytes.  %LP%
+// groups of threads bounds the segment's k-th largest element from below, and with it the row's;
+// elements at or above the highest such bound so far (about k of the first segment, fewer of each
+// later one) are collected and ranked by counting at the end.  Where ties let more than kCand
+// elements pass, what is held is ranked at once and the segment is read again and compared as 64-bit
+// keys of value and column, all distinct: at most k threads have an element above the k-th
+// largest of the threads' largest keys, so at most k * kPer pass, whatever the data.
+// What bounds it: at hundreds of rows the logits' bytes (524 x 151,936 fp32: 53 us without
+// alternatives, 5.9 TB/s; 68 us with 5, whose bound and collection lengthen every segment's
+// chain of barriers); at a few rows that chain and the cluster's two barriers, about 9 us.  Four
+// blocks of 256 threads per SM, 40 elements a thread: 512 threads, or 32 or 24 elements, took
+// 4 to 40 % longer, three blocks 20 %.
 #include <cooperative_groups.h>
 
 #include "qmm_kv.cuh"
@@ -26,7 +31,8 @@ constexpr int kThreads = 256;
 constexpr int kPer = 40;                  // elements per thread and segment
 constexpr int kSeg = kThreads * kPer;
 constexpr int kMaxTop = 32;
-constexpr int kCand = kMaxTop * kPer;     // candidates of a segment
+constexpr int kPerSm = 4;                 // blocks that an SM holds (registers and shared memory)
+constexpr int kCand = kMaxTop * (kPer + 1);  // candidates a block holds
 constexpr int kMaxRanks = 16;
 constexpr int kSums = 64;                 // segments whose sums a block keeps apart (see the kernel)
 
@@ -45,20 +51,24 @@ struct Params {
     int32_t vec;  // rows can be read 16 bytes at a time
 };
 
-__device__ __forceinline__ uint64_t key_of(float v, uint32_t column) {
+// A float's bits in an order that integers compare (-0 counts as +0).
+__device__ __forceinline__ uint32_t order_of(float v) {
     const uint32_t u = __float_as_uint(v + 0.0f);
-    return (static_cast<uint64_t>((u & 0x80000000u) ? ~u : (u | 0x80000000u)) << 32) | (0xFFFFFFFFu - column);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
-__device__ __forceinline__ float value_of(uint64_t k) {
-    const uint32_t o = static_cast<uint32_t>(k >> 32);
-    return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
+__device__ __forceinline__ float from_order(uint32_t o) { return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o); }
+
+__device__ __forceinline__ uint64_t key_of(float v, uint32_t column) {
+    return (static_cast<uint64_t>(order_of(v)) << 32) | (0xFFFFFFFFu - column);
 }
+__device__ __forceinline__ float value_of(uint64_t k) { return from_order(static_cast<uint32_t>(k >> 32)); }
 __device__ __forceinline__ uint64_t max64(uint64_t a, uint64_t b) { return a > b ? a : b; }
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+constexpr float kLeast = -3.402823466e38f;  // the least finite value
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float as_f32(float v) { return v; }
@@ -82,34 +92,117 @@ __device__ __forceinline__ Sums shfl_xor(const Sums& s, int k) {
 }
 
 struct Shared {
-    float group[2][32];          // maxima of 8 threads each; two, for alternate segments
+    uint64_t bar;
+    alignas(16) float group[2][32];  // maxima of 8 threads each; two, for alternate segments
     uint64_t first[kThreads];    // the threads' largest keys that pass the bound
-    uint64_t cand[kCand + kMaxTop];
-    uint64_t list[kMaxTop];      // the block's best so far, best first; 0: none
-    uint64_t all[kMaxRanks * kMaxTop];
+    uint64_t cand[kCand];        // (at the end, in the cluster's first block: the lists' entries)
+    uint64_t list[kMaxTop];      // the block's best, best first; 0, below every element's key: none
+    uint64_t best[kMaxTop];
     uint64_t bound;
-    Sums part[2][kThreads / 32];
+    float2 part[2][kThreads / 32];
+    Sums total;
     Sums sums[kSums];            // of the block's segments, in order
-    int n_first, n_cand[2];
+    float raise[2];              // bounds found by one warp for the segments after
+    int n_first, n_all, n_cand;
 };
 
-// The k-th largest of 32 lanes' values (every lane returns it).
-__device__ __forceinline__ float kth_of_warp(float v, int k) {
-    int above = 0, equal = 0;
+// The k-th largest of 32 values in shared memory, `mine` being the lane's: the least of those with
+// fewer than k above them.
+__device__ __forceinline__ float kth_of_32(const float* all, float mine, int k) {
+    int above = 0;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        const float o = __shfl_sync(0xffffffffu, v, j);
-        above += o > v;
-        equal += o == v && j < static_cast<int>(threadIdx.x & 31);
+    for (int j = 0; j < 32; j += 4) {
+        const float4 o = *reinterpret_cast<const float4*>(all + j);
+        above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
     }
-    const uint32_t who = __ballot_sync(0xffffffffu, above + equal == k - 1);
-    return __shfl_sync(0xffffffffu, v, __ffs(who) - 1);
+    return from_order(__reduce_min_sync(0xffffffffu, above < k ? order_of(mine) : 0xFFFFFFFFu));
+}
+
+// Ranks cand[0 .. n) by counting and leaves the best k, in order, in `list` (0 past the last) and at
+// the front of cand; returns their number.  Only values that are not below the floor can be among them.
+// The whole block takes part.
+__device__ __noinline__ int rank_candidates(Shared& sh, int n, int k, float floor) {
+    const int tid = threadIdx.x;
+    if (tid < kMaxTop) sh.list[tid] = 0;
+    if (tid == 0) sh.n_first = 0;
+    __syncthreads();
+    const uint64_t* from = sh.cand;
+    if (n > 64) {
+        for (int i = tid; i < n; i += kThreads)
+            if (value_of(sh.cand[i]) >= floor) {
+                const int at = atomicAdd(&sh.n_first, 1);
+                if (at < kThreads) sh.first[at] = sh.cand[i];
+            }
+        __syncthreads();
+        if (sh.n_first <= kThreads) {
+            from = sh.first;
+            n = sh.n_first;
+        }
+    }
+    for (int i = tid; i < n; i += kThreads) {
+        const uint64_t mine = from[i];
+        int rank_of = 0;
+#pragma unroll 8
+        for (int j = 0; j < n; ++j) rank_of += from[j] > mine;
+        if (rank_of < k) sh.list[rank_of] = mine;
+    }
+    __syncthreads();
+    const int left = min(n, k);
+    if (tid < left) sh.cand[tid] = sh.list[tid];
+    __syncthreads();
+    return left;
+}
+
+// A segment (cols columns from x, the first of them column `base`) let too many elements pass:
+// ties.  The `before` candidates held when it began are cut to the best k, and the segment is read
+// again and compared by keys: at most k threads have an element above the k-th largest of the
+// threads' largest keys.  Returns the candidates then held, the best k.
+template <typename T>
+__device__ __noinline__ int redo_by_keys(Shared& sh, const T* x, int base, int cols, int before, int k, float floor) {
+    const int tid = threadIdx.x;
+    before = rank_candidates(sh, before, k, floor);
+    const uint64_t last = sh.list[k - 1];  // 0 unless there are k
+    uint64_t best = 0;
+#pragma unroll 4
+    for (int c = tid; c < cols; c += kThreads) {
+        const float v = as_f32(x[c]);
+        if (v >= kLeast) best = max64(best, key_of(v, static_cast<uint32_t>(base + c)));
+    }
+    if (tid == 0) {
+        sh.n_first = 0;
+        sh.bound = last + 1;
+        sh.n_cand = before;
+    }
+    __syncthreads();
+    if (best > last) sh.first[atomicAdd(&sh.n_first, 1)] = best;
+    __syncthreads();
+    const int nf = sh.n_first;
+    if (tid < nf) {
+        const uint64_t mine = sh.first[tid];
+        int rank_of = 0;
+        for (int j = 0; j < nf; ++j) rank_of += sh.first[j] > mine;
+        if (rank_of == k - 1) sh.bound = mine;
+    }
+    __syncthreads();
+    const uint64_t least = sh.bound;
+    if (best >= least)
+        for (int c = tid; c < cols; c += kThreads) {
+            const float v = as_f32(x[c]);
+            const uint64_t q = key_of(v, static_cast<uint32_t>(base + c));
+            if (v >= kLeast && q >= least) sh.cand[atomicAdd(&sh.n_cand, 1)] = q;
+        }
+    __syncthreads();
+    const int left = rank_candidates(sh, sh.n_cand, k, floor);
+    if (tid == 0) sh.n_cand = left;
+    __syncthreads();
+    return left;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, kPerSm) logprobs_kernel(const Params p) {
     extern __shared__ __align__(16) uint8_t raw[];
-    Shared& sh = *reinterpret_cast<Shared*>(raw);
+    T* buffer = reinterpret_cast<T*>(raw);  // [kSeg]
+    Shared& sh = *reinterpret_cast<Shared*>(raw + kSeg * sizeof(T));
     cg::cluster_group cl = cg::this_cluster();
     const int ranks = cl.num_blocks(), rank = cl.block_rank();
     const int64_t row = blockIdx.x / ranks;
@@ -119,22 +212,54 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const Params p) {
     const int units = (p.segs + p.fold - 1) / p.fold;
     const int u0 = units * rank / ranks, u1 = units * (rank + 1) / ranks;
     const int s0 = min(p.segs, u0 * p.fold), s1 = min(p.segs, u1 * p.fold);
-    if (tid < kMaxTop) sh.list[tid] = 0;  // below every key of an element
-    if (tid < 2) sh.n_cand[tid] = 0;
+    if (tid == 0) sh.n_cand = 0;
+    if (tid < 2) sh.raise[tid] = kLeast;
 
     constexpr int W = 16 / sizeof(T);  // elements of a 16-byte load
     const int k = p.top;
     Sums fold = {-INFINITY, 0.f, 0.f};
+    float bound = kLeast;  // elements below it are not collected (they are not among the k largest, or -infinity)
+    float floor = kLeast;  // a value that the k-th largest element so far is not below
+    int held = 0;          // candidates so far
+
+    // a segment whose bytes are whole 16-byte pieces comes by a bulk copy into shared memory, asked for
+    // as soon as the one before it is in registers
+    auto in_bulk = [&](int seg) { return p.vec && (min(static_cast<int64_t>(kSeg), p.n - seg * kSeg) * sizeof(T)) % 16 == 0; };
+    auto fetch = [&](int seg) {
+        if (!in_bulk(seg)) return;
+        const uint32_t bytes = static_cast<uint32_t>(min(static_cast<int64_t>(kSeg), p.n - seg * kSeg) * sizeof(T));
+        fence_proxy_async_smem();  // the buffer's reads, before the copy
+        mbar_arrive_expect_tx(&sh.bar, bytes);
+        bulk_g2s(buffer, x + seg * kSeg, bytes, &sh.bar, l2_policy_evict_first());
+    };
+    uint32_t phase = 0;
+    bool late = false;  // a copy did not arrive in time: the row becomes NaN
+    volatile int never = 0;
+    if (tid == 0) {
+        mbar_init(&sh.bar, 1);
+        fence_mbar_init();
+        if (s0 < s1) fetch(s0);
+    }
+    __syncthreads();
+
     for (int seg = s0; seg < s1; ++seg) {
         const int odd = (seg - s0) & 1;
         const int base = seg * kSeg, cols = static_cast<int>(min(static_cast<int64_t>(kSeg), p.n - base));
         // element i of a thread: column base + (i / W * kThreads + tid) * W + i % W
         auto column = [&](int i) { return (i / W * kThreads + tid) * W + i % W; };
+        const bool bulk = !late && in_bulk(seg);
+        if (bulk) late |= !mbar_wait_bounded(&sh.bar, phase, &never);
+        phase ^= bulk;
         float v[kPer];
 #pragma unroll
         for (int i = 0; i < kPer; i += W) {
             const int c = column(i);
-            if (p.vec && c + W <= cols) {
+            if (bulk) {
+                alignas(16) T t[W];
+                *reinterpret_cast<uint4*>(t) = *reinterpret_cast<const uint4*>(buffer + c);
+#pragma unroll
+                for (int j = 0; j < W; ++j) v[i + j] = c < cols ? as_f32(t[j]) : -INFINITY;
+            } else if (p.vec && c + W <= cols) {
                 alignas(16) T t[W];
                 *reinterpret_cast<uint4*>(t) = __ldcs(reinterpret_cast<const uint4*>(x + base + c));
 #pragma unroll
@@ -144,119 +269,133 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const Params p) {
                 for (int j = 0; j < W; ++j) v[i + j] = c + j < cols ? as_f32(x[base + c + j]) : -INFINITY;
             }
         }
-        float top = -INFINITY;
+        float top8[kPer / 8], top = -INFINITY;  // the thread's maxima
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) top = fmaxf(top, v[i]);
-        if (k > 0) {
-            float gm = top;
+        for (int i = 0; i < kPer; i += 8) {
+            float a = v[i];
 #pragma unroll
-            for (int b = 1; b < 8; b <<= 1) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, b));
-            if ((lane & 7) == 0) sh.group[odd][tid >> 3] = gm;
+            for (int j = 1; j < 8; ++j) a = fmaxf(a, v[i + j]);
+            top8[i / 8] = a;
+            top = fmaxf(top, a);
         }
+        float gm = top;
+#pragma unroll
+        for (int b = 1; b < 8; b <<= 1) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, b));
+        if ((lane & 7) == 0) sh.group[odd][tid >> 3] = gm;
+        late = __syncthreads_or(late);  // (also: the buffer is read)
+        if (tid == 0 && seg + 1 < s1 && !late) fetch(seg + 1);
+        const float group = sh.group[odd][lane];
+        if (k > 0) {
+            const float b = sh.raise[odd ^ 1];
+            bound = fmaxf(bound, b);
+            floor = fmaxf(floor, b);
+        }
+        const float m = from_order(__reduce_max_sync(0xffffffffu, order_of(group)));
         // a NaN, and a +infinity through its difference with itself, ends up in z
-        const float ref = top == -INFINITY ? 0.f : top;
-        Sums s = {top, 0.f, 0.f};
+        const float ref = m == -INFINITY ? 0.f : m;
+        float z = late ? __int_as_float(0x7FFFFFFF) : 0.f, u = 0.f;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const float d = v[i] - ref, e = ex2(d * kLog2e);
-            s.z += e;
-            s.u = fmaf(e, fmaxf(d, -1e30f), s.u);
+            z += e;
+            u = fmaf(e, fmaxf(d, -1e30f), u);
         }
 #pragma unroll
-        for (int b = 16; b >= 1; b >>= 1) s = merge(s, shfl_xor(s, b));
-        if (lane == 0) sh.part[odd][warp] = s;
-        __syncthreads();  // (also: the last segment's list is complete)
-        if (tid == 0) {
-            Sums t = sh.part[odd][0];
+        for (int b = 16; b >= 1; b >>= 1) {
+            z += __shfl_xor_sync(0xffffffffu, z, b);
+            u += __shfl_xor_sync(0xffffffffu, u, b);
+        }
+        if (lane == 0) sh.part[odd][warp] = make_float2(z, u);
+        if (k > 0 && m >= bound) {
+            if (seg == s0 || warp == (seg & 7)) {  // one warp in turn, for the segments after
+                const float b = kth_of_32(sh.group[odd], group, k);
+                if (seg == s0) bound = floor = fmaxf(bound, b);
+                else if (lane == 0) sh.raise[odd] = b;
+            }
+            // (a warp whose lanes hold none skips the elements; one atomic per lane that holds some)
+            if (__any_sync(0xffffffffu, top >= bound)) {
+                int mine = 0;
 #pragma unroll
-            for (int w = 1; w < kThreads / 32; ++w) t = merge(t, sh.part[odd][w]);
+                for (int i = 0; i < kPer; i += 8)
+                    if (__any_sync(0xffffffffu, top8[i / 8] >= bound)) {
+#pragma unroll
+                        for (int j = i; j < i + 8; ++j) mine += v[j] >= bound;
+                    }
+                int at = mine ? atomicAdd(&sh.n_cand, mine) : 0;
+#pragma unroll
+                for (int i = 0; i < kPer; i += 8)
+                    if (__any_sync(0xffffffffu, top8[i / 8] >= bound)) {
+#pragma unroll
+                        for (int j = i; j < i + 8; ++j)
+                            if (v[j] >= bound) {
+                                if (at < kCand) sh.cand[at] = key_of(v[j], static_cast<uint32_t>(base + column(j)));
+                                ++at;
+                            }
+                    }
+            }
+        }
+        __syncthreads();
+        if (tid == kThreads - 1) {
+            float2 s = sh.part[odd][0];
+#pragma unroll
+            for (int w = 1; w < kThreads / 32; ++w) {
+                s.x += sh.part[odd][w].x;
+                s.y += sh.part[odd][w].y;
+            }
             const int in = seg - u0 * p.fold;
-            fold = in % p.fold == 0 ? t : merge(fold, t);
+            fold = in % p.fold == 0 ? Sums{m, s.x, s.y} : merge(fold, Sums{m, s.x, s.y});
             sh.sums[in / p.fold] = fold;
         }
         if (k > 0) {
-            // ---- the bound.  An element equal to the list's last lies in a higher column and loses;
-            // -infinity is left to the end
-            const float group = kth_of_warp(sh.group[odd][lane], k);
-            const uint64_t last = sh.list[k - 1];
-            const float worst = last ? value_of(last) : -INFINITY;
-            const bool strict = group <= worst;
-            const float bound = strict ? worst : group;
-            if (strict ? top > bound : top >= bound) {
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    if (strict ? v[i] > bound : v[i] >= bound) {
-                        const int at = atomicAdd(&sh.n_cand[odd], 1);
-                        if (at < kCand) sh.cand[at] = key_of(v[i], static_cast<uint32_t>(base + column(i)));
-                    }
-                }
-            }
-            __syncthreads();
-            int fresh = sh.n_cand[odd];
-            if (fresh > kCand) {
-                // ---- ties: the same by keys, with the threads' largest keys as the groups
-                uint64_t best = 0;
-#pragma unroll
-                for (int i = 0; i < kPer; ++i)
-                    if (best == 0 && v[i] == top && top > -INFINITY) best = key_of(v[i], static_cast<uint32_t>(base + column(i)));
-                if (tid == 0) {
-                    sh.n_first = 0;
-                    sh.bound = last + 1;
-                }
-                __syncthreads();
-                if (best > last) sh.first[atomicAdd(&sh.n_first, 1)] = best;
-                __syncthreads();
-                const int nf = sh.n_first;
-                if (tid < nf) {
-                    const uint64_t mine = sh.first[tid];
-                    int rank_of = 0;
-                    for (int j = 0; j < nf; ++j) rank_of += sh.first[j] > mine;
-                    if (rank_of == k - 1) sh.bound = mine;
-                }
-                if (tid == 0) sh.n_cand[odd] = 0;
-                __syncthreads();
-                const uint64_t from = sh.bound;
-                if (best >= from) {
-#pragma unroll
-                    for (int i = 0; i < kPer; ++i) {
-                        const uint64_t q = key_of(v[i], static_cast<uint32_t>(base + column(i)));
-                        if (v[i] > -INFINITY && q >= from) sh.cand[atomicAdd(&sh.n_cand[odd], 1)] = q;
-                    }
-                }
-                __syncthreads();
-                fresh = sh.n_cand[odd];
-            }
-            if (tid == 0) sh.n_cand[odd ^ 1] = 0;
-            if (fresh > 0) {
-                // ---- the candidates and the list so far, ranked by counting
-                if (tid < k) sh.cand[fresh + tid] = sh.list[tid];
-                __syncthreads();
-                for (int i = tid; i < fresh + k; i += kThreads) {
-                    const uint64_t mine = sh.cand[i];
-                    int rank_of = 0;
-#pragma unroll 8
-                    for (int j = 0; j < fresh + k; ++j) rank_of += sh.cand[j] > mine;
-                    if (mine != 0 && rank_of < k) sh.list[rank_of] = mine;
+            const int now = sh.n_cand;
+            if (now <= kCand) {
+                held = now;
+            } else {
+                held = redo_by_keys(sh, x + base, base, cols, held, k, floor);
+                if (held == k) {
+                    // a later element equal to the k-th best lies in a higher column and loses
+                    const float w = value_of(sh.list[k - 1]);
+                    floor = fmaxf(floor, w);
+                    bound = fmaxf(bound, nextafterf(w, INFINITY));
                 }
             }
         }
     }
+    if (k > 0) {
+        __syncthreads();
+        rank_candidates(sh, held, k, floor);
+    }
+    if (late && tid == 0) mbar_wait_bounded(&sh.bar, phase ^ 1, &never);  // let the copy land before the block exits
     cl.sync();
     if (rank == 0) {
-        // ---- the row's sums, in the segments' order
+        // ---- the row's sums, as a tree over the units (a fixed one); of the lists, what is not below
+        // another list's last
         if (warp == 0) {
             Sums t = {-INFINITY, 0.f, 0.f};
-            for (int r = 0; r < ranks; ++r) {
-                const Sums* o = cl.map_shared_rank(sh.sums, r);
-                const int n = units * (r + 1) / ranks - units * r / ranks;
-                for (int i = 0; i < n; ++i) t = merge(t, o[i]);
+            for (int i = lane; i < units; i += 32) {
+                int r = static_cast<int>(static_cast<int64_t>(i) * ranks / units);  // the rank that has unit i
+                while (units * (r + 1) / ranks <= i) ++r;
+                t = merge(t, cl.map_shared_rank(sh.sums, r)[i - units * r / ranks]);
             }
-            if (lane == 0) sh.part[0][0] = t;
-        } else if (k > 0) {
-            for (int i = tid - 32; i < ranks * k; i += kThreads - 32) sh.all[i] = cl.map_shared_rank(&sh, i / k)->list[i % k];
+#pragma unroll
+            for (int b = 16; b >= 1; b >>= 1) t = merge(t, shfl_xor(t, b));
+            if (lane == 0) sh.total = t;
+        } else if (warp == 1 && k > 0) {
+            uint64_t bound = lane < ranks ? cl.map_shared_rank(&sh, lane)->list[k - 1] : 0;
+#pragma unroll
+            for (int b = 16; b >= 1; b >>= 1) bound = max64(bound, __shfl_xor_sync(0xffffffffu, bound, b));
+            if (lane == 0) {
+                sh.bound = bound;
+                sh.n_first = sh.n_all = 0;
+            }
         }
         __syncthreads();
-        const Sums t = sh.part[0][0];
+        for (int i = tid; i < ranks * k; i += kThreads) {
+            const uint64_t mine = cl.map_shared_rank(&sh, i / k)->list[i % k];
+            if (mine != 0 && mine >= sh.bound) sh.cand[atomicAdd(&sh.n_all, 1)] = mine;
+        }
+        __syncthreads();
+        const Sums t = sh.total;
         const bool bad = t.z != t.z;
         const float nan = __int_as_float(0x7FFFFFFF);
         const float lz = logf(t.z);
@@ -274,31 +413,28 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const Params p) {
             int32_t* index = p.top_index + row * k;
             float* out = p.top_logprob + row * k;
             // how many there are (fewer than k only if the rest of the row is -infinity)
-            const int total = ranks * k;
-            if (tid == 0) sh.n_first = 0;
-            __syncthreads();
+            const int total = sh.n_all;
             for (int i = tid; i < total; i += kThreads) {
-                const uint64_t mine = sh.all[i];
-                if (mine == 0) continue;
+                const uint64_t mine = sh.cand[i];
                 int rank_of = 0;
 #pragma unroll 8
-                for (int j = 0; j < total; ++j) rank_of += sh.all[j] > mine;
+                for (int j = 0; j < total; ++j) rank_of += sh.cand[j] > mine;
                 if (rank_of < k) {
-                    sh.list[rank_of] = mine;
+                    sh.best[rank_of] = mine;
                     atomicAdd(&sh.n_first, 1);
                 }
             }
             __syncthreads();
             const int found = sh.n_first;
             if (tid < k && (bad || tid < found)) {
-                index[tid] = bad ? -1 : static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(sh.list[tid]));
-                out[tid] = bad ? nan : lp(value_of(sh.list[tid]));
+                index[tid] = bad ? -1 : static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(sh.best[tid]));
+                out[tid] = bad ? nan : lp(value_of(sh.best[tid]));
             } else if (!bad && tid == k - 1) {
                 // the lowest columns that are not in the list
                 int c = 0;
                 for (int i = found; i < k; ++c) {
                     bool in = false;
-                    for (int j = 0; j < found; ++j) in |= 0xFFFFFFFFu - static_cast<uint32_t>(sh.list[j]) == static_cast<uint32_t>(c);
+                    for (int j = 0; j < found; ++j) in |= 0xFFFFFFFFu - static_cast<uint32_t>(sh.best[j]) == static_cast<uint32_t>(c);
                     if (in) continue;
                     index[i] = c;
                     out[i++] = -INFINITY;
@@ -310,14 +446,19 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const Params p) {
 }
 
 template <typename T>
+constexpr int shared_bytes() { return kSeg * static_cast<int>(sizeof(T)) + static_cast<int>(sizeof(Shared)); }
+
+static_assert(kPerSm * (shared_bytes<float>() + 1024) <= 228 * 1024, "the blocks' shared memory");
+
+template <typename T>
 cudaError_t launch(const Params& p, int64_t m, int ranks, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(logprobs_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared));
+    cudaError_t e = cudaFuncSetAttribute(logprobs_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, shared_bytes<T>());
     if (e == cudaSuccess && ranks > 8) e = cudaFuncSetAttribute(logprobs_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(m * ranks));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = sizeof(Shared);
+    cfg.dynamicSmemBytes = shared_bytes<T>();
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -348,11 +489,18 @@ extern "C" qmm_status qmm_logprobs(const void* logits, int32_t type, int64_t m, 
     int dev = 0, sms = 0;
     const qmm_status st = qmm::kv::check_gpu(&dev, &sms);
     if (st != QMM_OK) return st;
-    // blocks per row: the fewest that give every SM six, up to one per segment and the largest
-    // cluster (the row's bits do not depend on it)
+    // blocks per row: what makes the fewest waves of the shortest blocks, in segments' times, a block's
+    // start and end counting as two (the row's bits do not depend on it)
     const int32_t segs = static_cast<int32_t>((n + kSeg - 1) / kSeg);
     int ranks = 1;
-    while (ranks < kMaxRanks && ranks < segs && m * ranks < 6 * sms) ranks *= 2;
+    int64_t least = INT64_MAX;
+    for (int r = 1; r <= kMaxRanks && (r == 1 || r < 2 * segs); r *= 2) {
+        const int64_t cost = (m * r + kPerSm * sms - 1) / (kPerSm * sms) * ((segs + r - 1) / r + 2);
+        if (cost < least) {
+            least = cost;
+            ranks = r;
+        }
+    }
     Params p = {};
     p.logits = logits;
     p.tokens = tokens;
