@@ -217,20 +217,30 @@ cudaError_t launch_append_dim(const AppendParams& p, int32_t dim, int32_t type, 
 }
 
 // ------------------------------------------------------------------------------ evict
-// Two kernels.  The first has one cluster per (sequence, KV head), its slots cut evenly among the
-// cluster's blocks.  The keep-th largest key is found by a radix select over 11 + 11 + 10 bits: each
-// pass counts the digit of the keys that still match, the blocks add their counts through
-// distributed shared memory, and every block picks the same digit.  Then each thread walks its run
+// Two kernels.  The first has a block, or a cluster of blocks with an even share of the slots
+// each, per (sequence, KV head).  The keep-th largest
+// key is found by a radix select from the top, 13 bits a pass (11 in clusters): count the digit of the keys that
+// still match, add the blocks' counts through distributed shared memory, pick a digit; once at
+// most kFew keys match they are ranked by counting.  Then each warp walks its run
 // of slots: ties at the threshold are kept from the lowest slot on, kept slots below the budget
 // stay, and the freed ones and the kept ones past the budget go to two lists in slot order
-// (places by prefix sums over the cluster).  The second kernel, a whole grid, moves the i-th of
+// (places by prefix sums over the warps).  The second kernel, a whole grid, moves the i-th of
 // the one list to the i-th of the other.  The weights and positions are read once (keys stay in
 // shared memory while they fit), and each moved token is read and written once; with the order
 // of slots given up, nothing else has to move.
-constexpr int kEvictThreads = 512;
+// What bounds it: 4 x 23,003 fp16 tokens cut to 11,500 take 58 us, 34 of them the moves (188 MB, 5.5
+// TB/s) and the rest the select's chain of barriers on few SMs.  A q8_0 record keeps V
+// dim-major, so moving half of a page's tokens touches all of its sectors: the destinations are
+// read and written whole, and 8 ragged caches (60 MB of moved tokens, 218 MB of sectors) take 37 us.
+constexpr int kEvictThreads = 1024;
 constexpr int kMoveThreads = 256;
-constexpr int kBins = 2048;
-constexpr int kKeyCap = 16384;  // keys a block holds in shared memory
+// Bits of a pass: 13 take fewer passes and collide less than 11, but in a cluster every block reads
+// every block's counts (8 x 32 KB took 20 us of 131,071 keys in eight blocks).
+template <bool multi>
+constexpr int kDigit = multi ? 11 : 13;
+constexpr int kBins = 1 << 13;
+constexpr int kKeyCap = 24576;  // keys a block holds in shared memory
+constexpr int kFew = 256;       // keys that are ranked by counting
 
 struct EvictParams {
     uint8_t* pool;
@@ -249,6 +259,7 @@ struct EvictParams {
     int* err;
     int64_t rec_bytes, half;
     int32_t sink, kv_heads, max_pages, pool_pages, page_tokens, page_shift, cap, head_dim, key_cap;
+    int32_t vec;     // weight, pos and their outputs are 16-byte aligned
     int32_t slices;  // blocks of the second kernel per (sequence, KV head)
 };
 
@@ -261,10 +272,14 @@ __device__ __forceinline__ uint32_t evict_key(float w, int32_t pos, int32_t sink
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+template <bool multi>
 __global__ void __launch_bounds__(kEvictThreads) kv_evict_select(const EvictParams p) {
-    extern __shared__ uint32_t keys[];  // [key_cap]
-    __shared__ int hist[kBins];
-    __shared__ int tmp[33], pick[2], counts[3];
+    extern __shared__ __align__(16) int hist[];  // [kBins], then the keys, [key_cap]
+    uint32_t* keys = reinterpret_cast<uint32_t*>(hist + kBins);
+    __shared__ uint32_t few[kFew];
+    __shared__ __align__(16) uint32_t all_few[kFew];
+    __shared__ int tmp[33], pick[3], counts[3], n_few;
+    __shared__ int4 warp_counts[kEvictThreads / 32];
     griddep_launch_dependents();  // the moving kernel waits for this grid's end
     cg::cluster_group cl = cg::this_cluster();
     const int ranks = cl.num_blocks(), rank = cl.block_rank();
@@ -281,7 +296,7 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_select(const EvictPara
         }
     }
     const int64_t base = static_cast<int64_t>(ag) * p.cap;
-    const int per = (n + ranks - 1) / ranks, s0 = min(n, rank * per), s1 = min(n, s0 + per);
+    const int per = ((n + ranks - 1) / ranks + 31) / 32 * 32, s0 = min(n, rank * per), s1 = min(n, s0 + per);
     if (budget == n) {  // nothing to evict (the whole cluster agrees)
         for (int t = s0 + tid; t < s1; t += kEvictThreads) {
             p.weight_out[base + t] = p.weight[base + t];
@@ -294,70 +309,198 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_select(const EvictPara
     const bool cached = per <= p.key_cap;
     auto make = [&](int t) { return evict_key(p.weight[base + t], p.pos[base + t], p.sink, from); };
     auto key = [&](int t) { return cached ? keys[t - s0] : make(t); };
-    if (cached)
-        for (int t = s0 + tid; t < s1; t += kEvictThreads) keys[t - s0] = make(t);
+    // The arrays' slots below the budget go out as they are; the second kernel overwrites the freed
+    // ones.  (In place, nothing is written.)
+    const bool copy = p.weight_out != p.weight || p.pos_out != p.pos;
+    auto put = [&](int t, float w, int32_t q) {
+        if (t >= budget) return;
+        p.weight_out[base + t] = w;
+        p.pos_out[base + t] = q;
+    };
+    if (cached) {
+        int t = s0 + 4 * tid;
+        if (p.vec)  // four slots by 16-byte loads, four such in flight
+            for (; t + 12 * kEvictThreads + 3 < s1; t += 16 * kEvictThreads) {
+                float4 w[4];
+                int4 q[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    w[i] = *reinterpret_cast<const float4*>(p.weight + base + t + 4 * i * kEvictThreads);
+                    q[i] = *reinterpret_cast<const int4*>(p.pos + base + t + 4 * i * kEvictThreads);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int at = t + 4 * i * kEvictThreads;
+                    if (copy && at + 3 < budget) {
+                        *reinterpret_cast<float4*>(p.weight_out + base + at) = w[i];
+                        *reinterpret_cast<int4*>(p.pos_out + base + at) = q[i];
+                    } else if (copy) {
+                        put(at, w[i].x, q[i].x), put(at + 1, w[i].y, q[i].y), put(at + 2, w[i].z, q[i].z);
+                    }
+                    *reinterpret_cast<uint4*>(keys + t - s0 + 4 * i * kEvictThreads) =
+                        make_uint4(evict_key(w[i].x, q[i].x, p.sink, from), evict_key(w[i].y, q[i].y, p.sink, from),
+                                   evict_key(w[i].z, q[i].z, p.sink, from), evict_key(w[i].w, q[i].w, p.sink, from));
+                }
+            }
+        for (; t < s1; t += 4 * kEvictThreads) {
+            float w[4];
+            int q[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                w[i] = t + i < s1 ? p.weight[base + t + i] : 0.f;
+                q[i] = t + i < s1 ? p.pos[base + t + i] : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (t + i < s1) {
+                    if (copy) put(t + i, w[i], q[i]);
+                    keys[t - s0 + i] = evict_key(w[i], q[i], p.sink, from);
+                }
+        }
+    } else if (copy) {
+        for (int t = s0 + tid; t < min(s1, budget); t += kEvictThreads) put(t, p.weight[base + t], p.pos[base + t]);
+    }
 
     // ---- the threshold: the key of which `need` are kept, everything above it being kept too
-    uint32_t prefix = 0, mask = 0;
-    int need = budget;
+    uint32_t thr = 0, mask = 0;
+    int need = budget, match = n, shift = 32;
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
-        for (int i = tid; i < kBins; i += kEvictThreads) hist[i] = 0;
+    while (match > kFew && shift > 0) {
+        const int bits = shift > kDigit<multi> ? kDigit<multi> : shift, bins = 1 << bits;
+        shift -= bits;
+        for (int i = tid; i < 1 << kDigit<multi>; i += kEvictThreads) hist[i] = 0;
+        __syncthreads();
+#pragma unroll 4
+        for (int t = s0 + tid; t < s1; t += kEvictThreads) {
+            const uint32_t k = key(t);
+            // (protected keys are many and equal: one addition per warp)
+            const uint32_t top = __ballot_sync(__activemask(), k == 0xFFFFFFFFu);
+            if (k == 0xFFFFFFFFu) {
+                if (mask == thr && (tid & 31) == __ffs(top) - 1) atomicAdd(&hist[bins - 1], __popc(top));
+            } else if ((k & mask) == thr) {
+                atomicAdd(&hist[(k >> shift) & (bins - 1)], 1);
+            }
+        }
+        cl.sync();
+        // the thread's bins, from the highest down
+        constexpr int B = (1 << kDigit<multi>) / kEvictThreads;
+        const int first = (1 << kDigit<multi>) - B - B * tid;
+        int c[B] = {}, mine = 0;
+        for (int r = 0; r < ranks; ++r) {
+            const int2* v = reinterpret_cast<const int2*>(cl.map_shared_rank(hist, r) + first);
+#pragma unroll
+            for (int i = 0; i < B / 2; ++i) {
+                const int2 x = v[B / 2 - 1 - i];
+                c[2 * i] += x.y, c[2 * i + 1] += x.x;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < B; ++i) mine += c[i];
+        int total;
+        int above = block_exclusive(mine, tmp, &total);
+        if (above < need && above + mine >= need) {  // one thread of the block's
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                if (above < need && above + c[i] >= need) {
+                    pick[0] = first + B - 1 - i;
+                    pick[1] = need - above;
+                    pick[2] = c[i];
+                }
+                above += c[i];
+            }
+        }
+        cl.sync();  // (also: every block has read the counts before they are cleared)
+        thr |= static_cast<uint32_t>(pick[0]) << shift;
+        mask |= static_cast<uint32_t>(bins - 1) << shift;
+        need = pick[1];
+        match = pick[2];
+    }
+    if (shift > 0) {
+        // few keys match: every block ranks all of them
+        if (tid == 0) n_few = 0;
         __syncthreads();
         for (int t = s0 + tid; t < s1; t += kEvictThreads) {
             const uint32_t k = key(t);
-            if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1);
+            if ((k & mask) == thr) few[atomicAdd(&n_few, 1)] = k;
         }
         cl.sync();
-        // the thread's four bins, from the highest down
-        int c[4] = {}, mine = 0;
-        const int at4 = kBins - 4 - 4 * tid;
-#pragma unroll 4
-        for (int r = 0; r < ranks; ++r) {
-            const int4 v = *reinterpret_cast<const int4*>(cl.map_shared_rank(hist, r) + at4);
-            c[0] += v.w, c[1] += v.z, c[2] += v.y, c[3] += v.x;
+        for (int r = 0, at = 0; r < ranks; ++r) {
+            const int c = *cl.map_shared_rank(&n_few, r);
+            const uint32_t* from_few = cl.map_shared_rank(few, r);
+            for (int i = tid; i < c; i += kEvictThreads) all_few[at + i] = from_few[i];
+            at += c;
         }
-        mine = c[0] + c[1] + c[2] + c[3];
-        int total;
-        int above = block_exclusive(mine, tmp, &total);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (above < need && above + c[i] >= need) {  // one bin of the block's
-                pick[0] = kBins - 1 - (4 * tid + i);
+        __syncthreads();
+        if (tid < match) {
+            const uint32_t mine = all_few[tid];
+            int above = 0, same = 0, i = 0;
+#pragma unroll 4
+            for (; i + 4 <= match; i += 4) {
+                const uint4 o = *reinterpret_cast<const uint4*>(all_few + i);
+                above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+                same += (o.x == mine) + (o.y == mine) + (o.z == mine) + (o.w == mine);
+            }
+            for (; i < match; ++i) {
+                above += all_few[i] > mine;
+                same += all_few[i] == mine;
+            }
+            if (above < need && above + same >= need) {  // (equal keys write equal values)
+                pick[0] = static_cast<int>(mine);
                 pick[1] = need - above;
             }
-            above += c[i];
         }
-        cl.sync();  // (also: every block has read the counts before they are cleared)
-        prefix |= static_cast<uint32_t>(pick[0]) << shift;
-        mask |= static_cast<uint32_t>(bins - 1) << shift;
+        cl.sync();
+        thr = static_cast<uint32_t>(pick[0]);
         need = pick[1];
     }
-    const uint32_t thr = prefix;
 
-    // ---- the thread's run of slots: ties first, then (with the ties before it known) freed and
-    // moved slots
-    const int run = (per + kEvictThreads - 1) / kEvictThreads, t0 = min(s1, s0 + tid * run), t1 = min(s1, t0 + run);
-    int mine = 0;
-    for (int t = t0; t < t1; ++t) mine += key(t) == thr;
-    int all;
-    int tie = block_exclusive(mine, tmp, &all);
-    if (tid == 0) counts[0] = all;
-    cl.sync();
-    for (int r = 0; r < rank; ++r) tie += cl.map_shared_rank(counts, r)[0];
-    int holes = 0, moves = 0, eq = tie;
-    for (int t = t0; t < t1; ++t) {
+    // ---- the warp's run of slots, counted: above and at the threshold, below and past the budget
+    const int warp = tid >> 5, lane = tid & 31;
+    const int run = (per / 32 + kEvictThreads / 32 - 1) / (kEvictThreads / 32) * 32;
+    const int t0 = min(s1, s0 + warp * run), t1 = min(s1, t0 + run);
+    int4 n4 = make_int4(0, 0, 0, 0);
+#pragma unroll 4
+    for (int t = t0 + lane; t < t1; t += 32) {
         const uint32_t k = key(t);
-        const bool kept = k > thr || (k == thr && eq < need);
-        eq += k == thr;
-        holes += !kept && t < budget;
-        moves += kept && t >= budget;
+        if (t < budget) n4.x += k > thr, n4.y += k == thr;
+        else n4.z += k > thr, n4.w += k == thr;
     }
-    int hole = block_exclusive(holes, tmp, &all);
-    if (tid == 0) counts[1] = all;
-    int move = block_exclusive(moves, tmp, &all);
-    if (tid == 0) counts[2] = all;
+    n4.x = __reduce_add_sync(0xffffffffu, n4.x), n4.y = __reduce_add_sync(0xffffffffu, n4.y);
+    n4.z = __reduce_add_sync(0xffffffffu, n4.z), n4.w = __reduce_add_sync(0xffffffffu, n4.w);
+    if (lane == 0) warp_counts[warp] = n4;
+    __syncthreads();
+    // ties before the warp's run: those of the block's earlier warps, and of earlier blocks
+    const int4 w4 = warp_counts[lane];
+    const int block_ties = __reduce_add_sync(0xffffffffu, w4.y + w4.w);
+    if (tid == 0) counts[0] = block_ties;
+    cl.sync();
+    int tie_block = 0;
+    for (int r = 0; r < rank; ++r) tie_block += cl.map_shared_rank(counts, r)[0];
+    // (lane l: what warp l keeps on either side of the budget)
+    int tie_lane = w4.y + w4.w;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, tie_lane, k);
+        if (lane >= k) tie_lane += o;
+    }
+    tie_lane += tie_block - w4.y - w4.w;
+    const int a0 = min(s1, s0 + lane * run), a1 = min(s1, a0 + run);  // warp l's run
+    const int below = max(0, min(a1, budget) - a0);
+    const int kept_below = w4.x + min(w4.y, max(0, need - tie_lane));
+    const int kept_past = w4.z + min(w4.w, max(0, need - tie_lane - w4.y));
+    int hole_lane = below - kept_below, move_lane = kept_past;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, hole_lane, k), q = __shfl_up_sync(0xffffffffu, move_lane, k);
+        if (lane >= k) hole_lane += o, move_lane += q;
+    }
+    if (tid == 31) {
+        counts[1] = hole_lane;
+        counts[2] = move_lane;
+    }
+    int tie = __shfl_sync(0xffffffffu, tie_lane, warp);
+    int hole = __shfl_sync(0xffffffffu, hole_lane - (below - kept_below), warp);
+    int move = __shfl_sync(0xffffffffu, move_lane - kept_past, warp);
     cl.sync();
     int total = 0;
     for (int r = 0; r < ranks; ++r) {
@@ -369,30 +512,38 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_select(const EvictPara
         total += c[2];
     }
     if (rank == 0 && tid == 0) p.moved[ag] = total;
+
+    // ---- the lists
     int2* to = p.lists + static_cast<int64_t>(ag) * 2 * p.half;
     int2* src = to + p.half;
     const int32_t* table = p.table + static_cast<int64_t>(a) * p.max_pages;
-    auto place = [&](int t) {
-        const int pg = table[t >> p.page_shift];
-        if (pg >= 0 && pg < p.pool_pages) return pg * p.page_tokens + (t & (p.page_tokens - 1));
-        atomicOr(p.err, kErrPage);
-        return -1;
-    };
-    for (int t = t0; t < t1; ++t) {
-        const uint32_t k = key(t);
-        const bool kept = k > thr || (k == thr && tie < need);
-        tie += k == thr;
-        if (t < budget) {
-            if (!kept) to[hole++] = make_int2(t, place(t));
-        } else if (kept) {
-            src[move++] = make_int2(t, place(t));
+    const uint32_t before = (1u << lane) - 1;
+    // the pages of the warp's run, a lane each, if they are at most 32
+    const int page0 = t0 >> p.page_shift;
+    const bool held = ((t1 - 1) >> p.page_shift) - page0 < 32;
+    int pages = -1;
+    if (held && ((page0 + lane) << p.page_shift) < t1) pages = table[page0 + lane];
+#pragma unroll 4
+    for (int t = t0 + lane; t - lane < t1; t += 32) {
+        const bool in = t < t1;
+        const uint32_t k = in ? key(t) : 0u;
+        const uint32_t equal = __ballot_sync(0xffffffffu, in && k == thr);
+        const bool kept = in && (k > thr || (k == thr && tie + __popc(equal & before) < need));
+        const bool free = in && !kept && t < budget, late = kept && t >= budget;
+        const uint32_t frees = __ballot_sync(0xffffffffu, free), lates = __ballot_sync(0xffffffffu, late);
+        int pg = __shfl_sync(0xffffffffu, pages, ((t >> p.page_shift) - page0) & 31);
+        if (free || late) {
+            if (!held) pg = table[t >> p.page_shift];
+            int place = -1;
+            if (pg >= 0 && pg < p.pool_pages) place = pg * p.page_tokens + (t & (p.page_tokens - 1));
+            else atomicOr(p.err, kErrPage);
+            if (free) to[hole + __popc(frees & before)] = make_int2(t, place);
+            else src[move + __popc(lates & before)] = make_int2(t, place);
         }
+        tie += __popc(equal);
+        hole += __popc(frees);
+        move += __popc(lates);
     }
-    if (p.weight_out != p.weight || p.pos_out != p.pos)  // (slots that move are overwritten by the second kernel)
-        for (int t = s0 + tid; t < min(s1, budget); t += kEvictThreads) {
-            p.weight_out[base + t] = p.weight[base + t];
-            p.pos_out[base + t] = p.pos[base + t];
-        }
     cl.sync();  // no block leaves while its counts are read
 }
 
@@ -587,10 +738,13 @@ qmm_status qmm_kv_evict(const qmm_kv_dims* dims, void* pool, const int32_t* page
     p.cap = dims->max_pages * dims->page_tokens;
     p.head_dim = dims->head_dim;
     while ((1 << p.page_shift) < dims->page_tokens) ++p.page_shift;
-    // blocks per cluster: as many as the longest sequence can use, up to 8 (the portable limit)
+    // blocks per cluster, up to 8 (the portable limit): as many as the longest sequence's keys need,
+    // and up to one per 8,192 slots while every block has an SM to itself (4 x 8 groups of 23,040
+    // slots: 66 us with one block each, 58 with four; with eight, which take two waves, 96)
     int ranks = 1;
-    while (ranks < 8 && p.cap > ranks * 512) ranks *= 2;
-    const int64_t per = (p.cap + ranks - 1) / ranks;
+    while (ranks < 8 && (p.cap > ranks * kKeyCap || (p.cap > ranks * 8192 && groups * ranks * 2 <= sms))) ranks *= 2;
+    const int64_t per = ((p.cap + ranks - 1) / ranks + 31) / 32 * 32;
+    p.vec = aligned(weight, 16) && aligned(pos, 16) && aligned(weight_out, 16) && aligned(pos_out, 16);
     p.key_cap = static_cast<int32_t>(per < kKeyCap ? per : kKeyCap);
     // the moves: eight blocks per SM over all groups, no more than the most pieces a group can move
     const int64_t pieces = dims->format == QMM_KV_Q8_0 ? (p.half + 31) / 32 * 5 * 32 : p.half * dims->head_dim / 4;
@@ -599,12 +753,13 @@ qmm_status qmm_kv_evict(const qmm_kv_dims* dims, void* pool, const int32_t* page
     p.slices = static_cast<int32_t>(slices);
     if (groups * ranks > INT32_MAX || groups * slices > INT32_MAX || dims->pool_pages * dims->page_tokens > INT32_MAX)
         return QMM_ERR_UNSUPPORTED_SHAPE;
-    cudaError_t e = cudaFuncSetAttribute(kv_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyCap * 4);
+    const auto select = ranks > 1 ? kv_evict_select<true> : kv_evict_select<false>;
+    cudaError_t e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, (kBins + kKeyCap) * 4);
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(groups * ranks));
         cfg.blockDim = dim3(kEvictThreads);
-        cfg.dynamicSmemBytes = static_cast<size_t>(p.key_cap) * 4;
+        cfg.dynamicSmemBytes = static_cast<size_t>(kBins + p.key_cap) * 4;
         cfg.stream = static_cast<cudaStream_t>(stream);
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -612,7 +767,7 @@ qmm_status qmm_kv_evict(const qmm_kv_dims* dims, void* pool, const int32_t* page
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, kv_evict_select, p);
+        e = cudaLaunchKernelEx(&cfg, select, p);
         if (e == cudaSuccess) {
             cfg.gridDim = dim3(static_cast<unsigned>(groups * slices));
             cfg.blockDim = dim3(kMoveThreads);

@@ -236,15 +236,17 @@ def test_evict_long(fmt, dim, page, n):
     check_evict(c, *slots(c, seed=3, kind="few"), keep=[n // 3, 3], sink=4, protect=[n - 500, 9])
 
 
-def test_evict_longer_than_the_keys_that_a_block_holds():
-    """Keys are formed again from memory where a block's share passes its shared memory."""
+@pytest.mark.parametrize("n", [33001, 140001, 270001])
+def test_evict_longer_than_the_keys_that_a_block_holds(n):
+    """Clusters of two and eight blocks, and keys formed again from memory where a block's share passes
+    its shared memory."""
     t = torch_cuda()
-    n = 140001
     c = Cache("f16", (n,), 1, 64, 256, seed=24)
     w, pos = slots(c, seed=4)
-    pool, wo, po, m, err = evict(c, w, pos, [60000], 4, [n - 1000])
-    assert err == 0 and m == [60000]
-    budget, moves = evict_ref(w[0, 0], pos[0, 0], n, 60000, 4, n - 1000)
+    keep = n * 3 // 7
+    pool, wo, po, m, err = evict(c, w, pos, [keep], 4, [n - 1000])
+    assert err == 0 and m == [keep]
+    budget, moves = evict_ref(w[0, 0], pos[0, 0], n, keep, 4, n - 1000)
     ww, pp = w[0, 0].copy(), pos[0, 0].copy()
     src, dst = np.array(moves).T
     ww[dst], pp[dst] = w[0, 0, src], pos[0, 0, src]
