@@ -138,17 +138,16 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join(const AttendParams p
 
 namespace {
 
-// Blocks the split is planned for: 4 on each of a GB300's 152 SMs.
-constexpr int64_t kWorkers = 152 * 4;
-
 // Tokens per chunk, by the dims alone (so that a row's bits are those of any other call): the
-// longest of 1024 .. 64 that gives every worker two items when all sequences are full, and whose
-// pages one warp can hold (32).
+// longest of 1024 .. a tile that gives every block of a GB300's grid two items (one block per SM at
+// head dimension 128, four otherwise) when all sequences are full, and whose pages one warp can
+// hold (32).
 int32_t chunk_of(const qmm_kv_dims& d) {
-    const int64_t cap = int64_t{d.max_pages} * d.page_tokens;
-    for (int32_t c = 1024; c > 64; c >>= 1)
-        if (c <= 32 * d.page_tokens && (cap + c - 1) / c * d.agents * d.kv_heads >= 2 * kWorkers) return c;
-    return 64;
+    const int64_t cap = int64_t{d.max_pages} * d.page_tokens, blocks = d.head_dim == 128 ? 152 : 608;
+    const int32_t least = d.head_dim == 128 ? kTcTile : kTile;
+    for (int32_t c = 1024; c > least; c >>= 1)
+        if (c <= 32 * d.page_tokens && (cap + c - 1) / c * d.agents * d.kv_heads >= 2 * blocks) return c;
+    return least;
 }
 
 struct Layout {
@@ -199,7 +198,7 @@ qmm_status make_map(const qmm_kv_dims& d, const void* pool, CUtensorMap* map) {
     if (rows > INT32_MAX) return QMM_ERR_UNSUPPORTED_SHAPE;
     const PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
     if (!enc) return QMM_ERR_CUDA;
-    const int tile = kTile;
+    const int tile = d.head_dim == 128 ? kTcTile : kTile;
     const cuuint64_t size[2] = {static_cast<cuuint64_t>(d.head_dim), static_cast<cuuint64_t>(rows)};
     const cuuint64_t stride[1] = {static_cast<cuuint64_t>(d.head_dim) * 2};
     const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(tile < d.page_tokens ? tile : d.page_tokens)};

@@ -46,6 +46,7 @@ namespace kv {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 64;            // tokens per tile
+constexpr int kTcTile = 128;         // tokens per tile of the tensor core kernel (head dimension 128)
 constexpr float kShift = 13.f;       // p's power of two: p^ <= 2^13, times a scale < 4 <= 2^15
 constexpr float kNoMax = -INFINITY;
 
@@ -161,6 +162,94 @@ __device__ __forceinline__ void tma_load_2d_hint(void* smem_dst, const void* tma
         : "memory");
 }
 
+// The table of sequences, in shared memory: every block forms the same one.  seq[a] = (first item,
+// longest row, shortest row, first row), one more entry at the end; returns the number of items.
+// Block 0 also writes it out for the joining kernel.  tmp: 33 ints.  The whole block takes part.
+__device__ __forceinline__ int form_table(const AttendParams& p, int4* seq, int* tmp, int qt) {
+    const int tid = threadIdx.x, n_threads = blockDim.x;
+    for (int a = tid; a <= p.agents; a += n_threads) {
+        const int r0 = p.agent_rows[a], r1 = a < p.agents ? p.agent_rows[a + 1] : r0;
+        const bool ok = r0 >= 0 && r1 >= r0 && r1 <= p.rows && r1 - r0 <= p.max_agent_rows;
+        seq[a] = make_int4(ok ? 0 : -1, 0, INT32_MAX, r0);
+    }
+    __syncthreads();
+    for (int r = tid; r < p.rows; r += n_threads) {
+        int lo = 0, hi = p.agents;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (seq[mid].w <= r) lo = mid;
+            else hi = mid;
+        }
+        if (r < seq[lo].w || r >= seq[lo + 1].w) continue;  // a row of no sequence
+        const int len = p.row_len[r];
+        if (len < 0 || len > p.cap) atomicExch(&seq[lo].x, -1);
+        else {
+            atomicMax(&seq[lo].y, len);
+            atomicMin(&seq[lo].z, len);
+        }
+    }
+    __syncthreads();
+    int total = 0;
+    for (int a0 = 0; a0 < p.agents; a0 += n_threads) {
+        const int a = a0 + tid;
+        int n = 0;
+        if (a < p.agents) {
+            const int4 s = seq[a];
+            const int nr = seq[a + 1].w - s.w;
+            if (s.x >= 0 && nr > 0) n = (s.y + p.chunk - 1) / p.chunk * p.kv_heads * ((nr * p.group + qt - 1) / qt);
+            if (blockIdx.x == 0) {
+                p.info[a] = make_int4(s.x < 0 ? -1 : s.y, s.w, nr, 0);
+                if (s.x < 0) atomicOr(p.err, kErrRange);
+            }
+        }
+        int sum;
+        const int at = block_exclusive(n, tmp, &sum);
+        if (a < p.agents) seq[a].x = total + at;
+        total += sum;
+    }
+    __syncthreads();
+    return total;
+}
+
+// Item `item` of the table: chunk tok0 .. end - 1 of sequence a for KV head g and its tile-th tile of
+// qt queries.  Tiles of the same chunk, and KV heads of the same pages, follow one another.
+struct Item {
+    int a, g, tile, tok0, end;
+};
+__device__ __forceinline__ Item decode_item(const AttendParams& p, const int4* seq, int item, int qt) {
+    int lo = 0, hi = p.agents;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (seq[mid].x <= item) lo = mid;
+        else hi = mid;
+    }
+    const int4 s = seq[lo];
+    const int tiles = ((seq[lo + 1].w - s.w) * p.group + qt - 1) / qt;
+    int rest = item - s.x;
+    Item it;
+    it.a = lo;
+    it.tile = rest % tiles;
+    rest /= tiles;
+    it.g = rest % p.kv_heads;
+    it.tok0 = rest / p.kv_heads * p.chunk;
+    it.end = min(it.tok0 + p.chunk, s.y);
+    return it;
+}
+
+// Lane l: the item's l-th page (an item spans at most 32), -1 if the table points outside the pool.
+__device__ __forceinline__ int load_item_pages(const AttendParams& p, const Item& it) {
+    const int first = it.tok0 >> p.page_shift, lane = threadIdx.x & 31;
+    int pg = 0;
+    if (((first + lane) << p.page_shift) < it.end) {
+        pg = p.table[static_cast<int64_t>(it.a) * p.max_pages + first + lane];
+        if (pg < 0 || pg >= p.pool_pages) {
+            atomicOr(p.err, kErrPage);
+            pg = -1;
+        }
+    }
+    return pg;
+}
+
 template <int FMT, int D, int NT>
 __global__ void __launch_bounds__(kThreads, (Geo<FMT, D, NT>::blocks))
     attend_partial(const __grid_constant__ CUtensorMap map, const __grid_constant__ AttendParams p) {
@@ -191,89 +280,16 @@ __global__ void __launch_bounds__(kThreads, (Geo<FMT, D, NT>::blocks))
         fence_mbar_init();
     }
     if (tid < 4) odd_sm[tid] = 0;
-    for (int a = tid; a <= p.agents; a += kThreads) {
-        const int r0 = p.agent_rows[a], r1 = a < p.agents ? p.agent_rows[a + 1] : r0;
-        const bool ok = r0 >= 0 && r1 >= r0 && r1 <= p.rows && r1 - r0 <= p.max_agent_rows;
-        seq[a] = make_int4(ok ? 0 : -1, 0, INT32_MAX, r0);
-    }
-    __syncthreads();
-    for (int r = tid; r < p.rows; r += kThreads) {
-        int lo = 0, hi = p.agents;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (seq[mid].w <= r) lo = mid;
-            else hi = mid;
-        }
-        if (r < seq[lo].w || r >= seq[lo + 1].w) continue;  // a row of no sequence
-        const int len = p.row_len[r];
-        if (len < 0 || len > p.cap) atomicExch(&seq[lo].x, -1);
-        else {
-            atomicMax(&seq[lo].y, len);
-            atomicMin(&seq[lo].z, len);
-        }
-    }
-    __syncthreads();
-    int total = 0;
-    for (int a0 = 0; a0 < p.agents; a0 += kThreads) {
-        const int a = a0 + tid;
-        int n = 0;
-        if (a < p.agents) {
-            const int4 s = seq[a];
-            const int nr = seq[a + 1].w - s.w;
-            if (s.x >= 0 && nr > 0)
-                n = (s.y + p.chunk - 1) / p.chunk * p.kv_heads * ((nr * p.group + QT - 1) / QT);
-            if (blockIdx.x == 0) {
-                p.info[a] = make_int4(s.x < 0 ? -1 : s.y, s.w, nr, 0);
-                if (s.x < 0) atomicOr(p.err, kErrRange);
-            }
-        }
-        int sum;
-        const int at = block_exclusive(n, tmp, &sum);
-        if (a < p.agents) seq[a].x = total + at;
-        total += sum;
-    }
-    __syncthreads();
+    const int total = form_table(p, seq, tmp, QT);
 
-    struct Item {
-        int a, g, tile, tok0, end;
-    };
-    auto decode = [&](int item) {
-        int lo = 0, hi = p.agents;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (seq[mid].x <= item) lo = mid;
-            else hi = mid;
-        }
-        const int4 s = seq[lo];
-        const int tiles = ((seq[lo + 1].w - s.w) * p.group + QT - 1) / QT;
-        int rest = item - s.x;
-        Item it;
-        it.a = lo;
-        it.tile = rest % tiles;
-        rest /= tiles;
-        it.g = rest % p.kv_heads;
-        it.tok0 = rest / p.kv_heads * p.chunk;
-        it.end = min(it.tok0 + p.chunk, s.y);
-        return it;
-    };
+    auto decode = [&](int item) { return decode_item(p, seq, item, QT); };
 
     // ---- the producer (warp 0): the item whose half tiles are being requested, and the one after
     // it, whose pages are already on their way.  Lane l holds an item's l-th page (an item spans
     // at most 32), -1 if the table points outside the pool.
     Item pi = {}, ni = {};
     int ppages = 0, npages = 0, ptok = 0, phalf = 0, pslot = 0, nitem = blockIdx.x, issued = 0;
-    auto load_pages = [&](const Item& it) {
-        const int first = it.tok0 >> p.page_shift;
-        int pg = 0;
-        if (((first + lane) << p.page_shift) < it.end) {
-            pg = p.table[static_cast<int64_t>(it.a) * p.max_pages + first + lane];
-            if (pg < 0 || pg >= p.pool_pages) {
-                atomicOr(p.err, kErrPage);
-                pg = -1;
-            }
-        }
-        return pg;
-    };
+    auto load_pages = [&](const Item& it) { return load_item_pages(p, it); };
     auto issue = [&]() {
         if (ptok >= pi.end) {
             if (nitem >= total) return;

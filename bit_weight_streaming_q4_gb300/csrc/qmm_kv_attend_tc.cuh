@@ -1,0 +1,813 @@
+// Attention of new tokens over the paged cache: the split kernel for head dimension 128, on the
+// 5th-generation tensor cores.
+//
+// The mathematics, the items and the partials are those of qmm_kv_attend.cuh.  A block (one per SM,
+// persistent) works on tiles of 128 tokens:
+//   S^T[token][query] = K Q^T      M = 128 tokens, N = 16, 32 or 48 queries, K = the dims
+//   O^T[dim][query]  += V^T P^T    M = 128 dims, K = the tokens
+// with the accumulators in tensor memory, so a thread of the softmax warps owns a token's row of
+// scores and needs no exchange to form its probabilities, and the outputs cost no registers.
+//   warp 0      asks for K and V tiles (bulk copies into two rings)
+//   warp 1      issues the products: S of tile t + 1 goes before O of tile t, so that it overlaps
+//               the softmax
+//   warps 2, 3  bring the next item: its numbers and its queries
+//   warps 4-11  softmax, two groups of four, half of the queries each: scores from tensor memory,
+//               probabilities into shared memory as the second product's B operand, in two
+//               16-bit parts (two products)
+//   warps 12-15 q8_0 only: K and V quants to fp16 in tensor memory, as A operands
+// 16-bit pools: the swizzled tiles are A operands as they come, K by rows and V transposed
+// (M-contiguous).  q8_0: K's quants are exact in fp16, one accumulator per 32-dim block takes its
+// scale in fp32; V's element, quant times normalised scale (see qmm_kv_attend.cuh), is split into
+// two fp16 parts without error, and three of the four products of parts count.
+//
+// A query's reference is its first tile's maximum and moves only when a score passes it by more than
+// 2^kSlack (a vote per tile; then the warps form the tile's maxima and rescale what they
+// hold).  Each query decides for itself, so its bits depend on nothing but its own tokens.
+#pragma once
+
+#include "qmm_kv_attend.cuh"
+
+namespace qmm {
+namespace kv {
+
+constexpr float kSlack = 2.f;     // p <= 2^(kShift + kSlack)
+
+template <int FMT, int N>
+struct TcGeo {
+    static constexpr bool q8 = FMT == QMM_KV_Q8_0;
+    static constexpr int threads = q8 ? 512 : 384;
+    static constexpr int W = N / 2;                                // queries of a softmax group
+    static constexpr int half = q8 ? 2 * kQ8Half : kTcTile * 256;  // bytes of a tile's K or V
+    static constexpr int k_slots = q8 ? 4 : 3, v_slots = q8 ? 4 : 2;
+    static constexpr int opnd = N * 256;                           // bytes of a B operand: N rows of 128 16-bit values
+    // tensor memory columns: scores (one set per 32-dim block of a q8_0 pool), outputs, and the A operands
+    static constexpr int col_s = 0, col_o = q8 ? 4 * N : 64, col_k = 240, col_vh = 304, col_vl = 368;
+    static constexpr int cols = q8 ? 512 : 128;
+    // shared memory, after aligning to 1024
+    static constexpr int off_v = k_slots * half;
+    static constexpr int off_q = (off_v + v_slots * half + 1023) / 1024 * 1024;  // two
+    static constexpr int off_p = off_q + 2 * opnd;                              // hi, lo
+    static constexpr int off_dv = off_p + 2 * opnd;                             // q8_0: normalised V scales [4][128] fp16
+    static constexpr int off_len = off_dv + (q8 ? 4 * kTcTile * 2 : 0);         // [2][N] tokens that a query sees
+    static constexpr int off_lim = off_len + 2 * N * 4;                         // [N] reference + slack
+    static constexpr int off_sub = off_lim + N * 4;                             // [N] reference - kShift
+    static constexpr int off_alpha = off_sub + N * 4;                           // [N]
+    static constexpr int off_red = off_alpha + N * 4;                           // [8 warps][32]
+    static constexpr int off_odd = off_red + 8 * 32 * 4;                        // [4] tokens to be taken query by query
+    static constexpr int off_bar = off_odd + 16;
+    static constexpr int bars = 2 * k_slots + 2 * v_slots + 4 + 4 + 4 + 2;
+    static constexpr int off_item = (off_bar + bars * 8 + 15) / 16 * 16;        // [2] of ItemRec
+    static constexpr int off_misc = off_item + 2 * 32;                          // tmp[33], abort, accumulate, tmem, miss[v_slots]
+    static constexpr int off_seq = (off_misc + 48 * 4 + 15) / 16 * 16;
+    static constexpr int smem(int agents) { return 1024 + off_seq + (agents + 1) * 16; }
+};
+
+// Shared-memory descriptor of an M-contiguous operand in the 128-byte swizzle: atoms of 64 elements
+// (128 bytes) x 8 rows; `lead` bytes to the next 64 elements, 1024 to the next 8 rows.
+__device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t saddr, uint32_t lead) {
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+
+__device__ __forceinline__ uint32_t order_bits(float v) {
+    const uint32_t u = __float_as_uint(v);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float from_order_bits(uint32_t o) { return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o); }
+
+// 8 consecutive columns of the thread's tensor memory lane (to be waited for with tc_wait_ld).
+__device__ __forceinline__ void tmem_load8(uint32_t taddr, float (&v)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_store8(uint32_t taddr, const float (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "f"(v[0]),
+                 "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
+
+// The products, issued by the thread whose `one` is set while its whole warp computes the operands
+// (which then stay in uniform registers; inside a branch of one lane each issue took about 100 clocks).
+__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 q, %0, 0;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%1], %2, %3, %4, p;\n\t}" ::"r"(one),
+        "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 q, %0, 0;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], %3, %4, p;\n\t}" ::"r"(one),
+        "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t one, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %0, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(one),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+
+// v[c] of W <= 32 columns reduced over the warp's lanes by f: lane c returns column c's.  At each
+// step a lane keeps half of its columns and hands the other half to its partner.
+template <int W, typename F>
+__device__ __forceinline__ float reduce_columns(const float (&v)[W], float none, F f) {
+    float u[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) u[i] = i < W ? v[i < W ? i : 0] : none;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = 16; h >= 1; h >>= 1) {
+        const bool up = lane & h;
+#pragma unroll
+        for (int i = 0; i < h; ++i) {
+            if (i >= W) continue;  // (columns that nobody has)
+            const float mine = up ? u[i + h] : u[i], other = up ? u[i] : u[i + h];
+            u[i] = f(mine, __shfl_xor_sync(0xffffffffu, other, h));
+        }
+    }
+    return u[0];
+}
+
+// What the roles need to know of an item, formed once by the warps that bring its queries.
+struct alignas(16) ItemRec {
+    int a, g, tok0, end;
+    int q0, nq, minlen, r0;  // first query, queries of the sequence and KV head, the sequence's shortest row and first row
+};
+
+template <int FMT, int N>
+__global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
+    attend_partial_tc(const __grid_constant__ CUtensorMap map, const __grid_constant__ AttendParams p) {
+    using G = TcGeo<FMT, N>;
+    constexpr bool BF = FMT == QMM_KV_BF16;
+    constexpr int D = 128;
+    extern __shared__ uint8_t sm_raw[];
+    griddep_launch_dependents();  // the joining kernel waits for this grid's end before it reads
+    uint8_t* sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
+    int* qlen_sm = reinterpret_cast<int*>(sm + G::off_len);
+    float* lim_sm = reinterpret_cast<float*>(sm + G::off_lim);
+    float* sub_sm = reinterpret_cast<float*>(sm + G::off_sub);
+    float* alpha_sm = reinterpret_cast<float*>(sm + G::off_alpha);
+    float* red_sm = reinterpret_cast<float*>(sm + G::off_red);
+    ItemRec* item_sm = reinterpret_cast<ItemRec*>(sm + G::off_item);
+    volatile uint32_t* odd_sm = reinterpret_cast<uint32_t*>(sm + G::off_odd);
+    uint64_t* kfull = reinterpret_cast<uint64_t*>(sm + G::off_bar);
+    uint64_t* kempty = kfull + G::k_slots;
+    uint64_t* vfull = kempty + G::k_slots;
+    uint64_t* vempty = vfull + G::v_slots;
+    uint64_t *qfull = vempty + G::v_slots, *qempty = qfull + 2;                          // two each
+    uint64_t *sfull = qempty + 2, *sempty = sfull + 1, *pfull = sfull + 2, *odone = sfull + 3;
+    uint64_t *akfull = sfull + 4, *akfree = sfull + 5, *avfull = sfull + 6, *avfree = sfull + 7, *drained = sfull + 8,
+             *oddread = sfull + 9;
+    int* tmp = reinterpret_cast<int*>(sm + G::off_misc);
+    volatile int* abort_flag = tmp + 33;
+    volatile int* accum_sm = tmp + 34;  // the outputs hold something that the next product adds to
+    uint32_t* tmem_sm = reinterpret_cast<uint32_t*>(tmp + 35);
+    volatile int* vmiss = tmp + 36;     // [v_slots]: a page of the tile is outside the pool
+    int4* seq = reinterpret_cast<int4*>(sm + G::off_seq);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int i = 0; i < G::k_slots; ++i) {
+            mbar_init(kfull + i, 1);
+            mbar_init(kempty + i, G::q8 ? 12 : 1);
+        }
+        for (int i = 0; i < G::v_slots; ++i) {
+            mbar_init(vfull + i, 1);
+            mbar_init(vempty + i, G::q8 ? 12 : 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(qfull + i, 2);
+            mbar_init(qempty + i, G::q8 ? 13 : 9);
+        }
+        mbar_init(sfull, 1);
+        mbar_init(sempty, 8);
+        mbar_init(pfull, 8);
+        mbar_init(odone, 1);
+        mbar_init(akfull, 4);
+        mbar_init(akfree, 1);
+        mbar_init(avfull, 4);
+        mbar_init(avfree, 1);
+        mbar_init(drained, 1);
+        mbar_init(oddread, 8);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (tid < 4) odd_sm[tid] = 0;
+    if (warp == 1) {
+        tmem_alloc(tmem_sm, G::cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    const int total = form_table(p, seq, tmp, N);
+    tc_fence_after();
+    const uint32_t tmem = *tmem_sm;
+
+    // A wait of one of the roles.  Once one has run out, everything that follows runs dry.
+    bool live = true;
+    auto await = [&](uint64_t* b, uint32_t parity) {
+        if (live && !mbar_wait_bounded(b, parity, abort_flag)) {
+            live = false;
+            *abort_flag = 1;
+        }
+        __syncwarp();
+    };
+    // the same, with one answer for the warp
+    auto await_warp = [&](uint64_t* b, uint32_t parity) {
+        await(b, parity);
+        live = __all_sync(0xffffffffu, live);
+    };
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- producer
+        const uint64_t policy = l2_policy_evict_first();
+        int nitem = blockIdx.x, t = 0;
+        Item ni = {};
+        int npages = 0;
+        if (nitem < total) {
+            ni = decode_item(p, seq, nitem, N);
+            npages = load_item_pages(p, ni);
+        }
+        while (nitem < total && live) {
+            const Item it = ni;
+            const int pages = npages, first = it.tok0 >> p.page_shift;
+            nitem += gridDim.x;
+            if (nitem < total) {
+                ni = decode_item(p, seq, nitem, N);
+                npages = load_item_pages(p, ni);
+            }
+            for (int tb = it.tok0; tb < it.end && live; tb += kTcTile, ++t) {
+                // pieces of at most a page, those with tokens before the item's end
+                constexpr int kPieces = G::q8 ? 2 : kTcTile / 16;
+                const int br = min(kTcTile, p.page_tokens);
+                int pg[kPieces];
+                int n_pieces = 0;
+                bool miss = false;
+#pragma unroll
+                for (int k = 0; k < kPieces; ++k) {
+                    const int tok = tb + k * br;
+                    const bool in = k * br < kTcTile && tok < it.end;
+                    const int x = __shfl_sync(0xffffffffu, pages, in ? (tok >> p.page_shift) - first : 0);
+                    pg[k] = in ? x : -1;
+                    miss |= in && x < 0;
+                    n_pieces += pg[k] >= 0;
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int slots = h ? G::v_slots : G::k_slots, s = t % slots, round = t / slots;
+                    uint64_t* full = (h ? vfull : kfull) + s;
+                    if (round > 0) await_warp((h ? vempty : kempty) + s, (round - 1) & 1);
+                    if (!live) break;
+                    if (lane == 0) {
+                        fence_proxy_async_smem();  // the slot's generic accesses, before the copies
+                        if (h) vmiss[s] = miss;
+                        uint8_t* dst = sm + (h ? G::off_v : 0) + s * G::half;
+                        if (n_pieces == 0) mbar_arrive(full);
+                        else mbar_arrive_expect_tx(full, n_pieces * (G::q8 ? kQ8Half : br * D * 2));
+#pragma unroll
+                        for (int k = 0; k < kPieces; ++k) {
+                            if (pg[k] < 0) continue;
+                            if constexpr (G::q8) {
+                                bulk_g2s(dst + k * kQ8Half, p.pool + (static_cast<int64_t>(pg[k]) * p.kv_heads + it.g) * kQ8Rec + h * kQ8Half,
+                                         kQ8Half, full, policy);
+                            } else {
+                                const int y = ((pg[k] * p.kv_heads + it.g) * 2 + h) * p.page_tokens + ((tb + k * br) & (p.page_tokens - 1));
+#pragma unroll
+                                for (int x = 0; x < D / 64; ++x)
+                                    tma_load_2d_hint(dst + x * kTcTile * 128 + k * br * 128, &map, 64 * x, y, full, policy);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+        if (!live && lane == 0) {
+            // let every copy still in flight land before the block exits: the last of each slot
+            volatile int go_on = 0;
+            for (int h = 0; h < 2; ++h) {
+                const int slots = h ? G::v_slots : G::k_slots;
+                for (int i = max(0, t - slots); i <= t; ++i) mbar_wait_bounded((h ? vfull : kfull) + i % slots, (i / slots) & 1, &go_on, 100000000ull);
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- products
+        constexpr uint32_t kType = BF ? (1u << 7) | (1u << 10) : 0u;
+        constexpr uint32_t kIdescS = idesc_f16_f32(128, N) | kType;
+        constexpr uint32_t kIdescO = kIdescS | (G::q8 ? 0u : 1u << 15);  // 16-bit pools: A is M-contiguous
+        int t = 0, k = 0;  // tiles and items so far
+        const uint32_t one = lane == 0;
+        const uint32_t ph = smem_u32(sm + G::off_p);
+        auto product_o = [&](int i) {
+            await_warp(pfull, i & 1);
+            const int vs = i % G::v_slots;
+            if constexpr (G::q8) await_warp(avfull, i & 1);
+            else await_warp(vfull + vs, (i / G::v_slots) & 1);
+            if (!live) return;
+            tc_fence_after();
+            const uint64_t bh = smem_desc_sw128(ph), bl = smem_desc_sw128(ph + G::opnd);
+            const uint64_t av = smem_desc_sw128_mn(smem_u32(sm + G::off_v) + vs * G::half, kTcTile * 128);
+            uint32_t acc = *accum_sm != 0;
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+                const uint64_t at = ((ks >> 2) * (N * 128) + (ks & 3) * 32) >> 4;
+                if constexpr (G::q8) {
+                    mma_ts(one, tmem + G::col_o, tmem + G::col_vh + 8 * ks, bh + at, kIdescO, acc);
+                    mma_ts(one, tmem + G::col_o, tmem + G::col_vh + 8 * ks, bl + at, kIdescO, 1);
+                    mma_ts(one, tmem + G::col_o, tmem + G::col_vl + 8 * ks, bh + at, kIdescO, 1);
+                } else {
+                    mma_ss(one, tmem + G::col_o, av + ks * (2048 >> 4), bh + at, kIdescO, acc);
+                    mma_ss(one, tmem + G::col_o, av + ks * (2048 >> 4), bl + at, kIdescO, 1);
+                }
+                acc = 1;
+            }
+            mma_commit(one, odone);
+            mma_commit(one, G::q8 ? avfree : vempty + vs);
+        };
+        for (int item = blockIdx.x; item < total && live; item += gridDim.x, ++k) {
+            await_warp(qfull + (k & 1), (k >> 1) & 1);
+            const int tok0 = item_sm[k & 1].tok0, end = item_sm[k & 1].end;
+            const uint64_t bq = smem_desc_sw128(smem_u32(sm + G::off_q) + (k & 1) * G::opnd);
+            for (int tb = tok0; tb < end && live; tb += kTcTile, ++t) {
+                const int s = t % G::k_slots;
+                if constexpr (G::q8) await_warp(akfull, t & 1);
+                else await_warp(kfull + s, (t / G::k_slots) & 1);
+                if (t > 0) await_warp(sempty, (t - 1) & 1);
+                if (!live) break;
+                tc_fence_after();
+                const uint64_t ak = smem_desc_sw128(smem_u32(sm) + s * G::half);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) {
+                    const uint64_t at = ((ks >> 2) * (N * 128) + (ks & 3) * 32) >> 4;
+                    if constexpr (G::q8)
+                        mma_ts(one, tmem + G::col_s + (ks >> 1) * N, tmem + G::col_k + 8 * ks, bq + at, kIdescS, ks & 1);
+                    else
+                        mma_ss(one, tmem + G::col_s, ak + (((ks >> 2) * (kTcTile * 128) + (ks & 3) * 32) >> 4), bq + at, kIdescS, ks > 0);
+                }
+                mma_commit(one, sfull);
+                mma_commit(one, G::q8 ? akfree : kempty + s);
+                if (tb + kTcTile >= end) mma_commit(one, qempty + (k & 1));
+                if (t > 0) product_o(t - 1);
+            }
+        }
+        if (t > 0 && live) product_o(t - 1);
+        // every product issued has finished before the tensor memory is released
+        if (lane == 0) {
+            tc_commit(drained);
+            volatile int go_on = 0;
+            mbar_wait_bounded(drained, 0, &go_on, 10000000000ull);
+        }
+        __syncwarp();
+    } else if (warp < 4) {
+        // ---------------------------------------------------------------- the next item: numbers and queries, half a warp per row
+        int k = 0;
+        for (int item = blockIdx.x; item < total && live; item += gridDim.x, ++k) {
+            const Item it = decode_item(p, seq, item, N);
+            const int r0 = seq[it.a].w, nq = (seq[it.a + 1].w - r0) * p.group, q0 = it.tile * N;
+            const int buf = k & 1, c = lane & 15;
+            int qi = 2 * (warp - 2) + (lane >> 4), r = r0 + (q0 + qi) / p.group, h = (q0 + qi) % p.group;
+            if (k > 1) await_warp(qempty + buf, ((k >> 1) - 1) & 1);
+            if (!live) break;
+            if (warp == 2 && lane == 0) {
+                ItemRec rec = {it.a, it.g, it.tok0, it.end, q0, nq, seq[it.a].z, r0};
+                item_sm[buf] = rec;
+            }
+            uint8_t* dst = sm + G::off_q + buf * G::opnd + (c >> 3) * (N * 128);
+#pragma unroll 4
+            for (int i = 0; i < N / 4; ++i) {  // 16-byte pieces, swizzled as the copies do
+                const bool in = q0 + qi < nq;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                int len = 0;
+                if (in) {
+                    v = *reinterpret_cast<const uint4*>(p.q + r * p.q_stride + static_cast<int64_t>(it.g * p.group + h) * D + 8 * c);
+                    if (c == 0) len = p.row_len[r];
+                }
+                *reinterpret_cast<uint4*>(dst + qi * 128 + (((c & 7) ^ (qi & 7)) << 4)) = v;
+                if (c == 0) qlen_sm[buf * N + qi] = len;
+                qi += 4;
+                for (h += 4; h >= p.group; h -= p.group) ++r;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(qfull + buf);
+        }
+    } else if (warp < 12) {
+        // ---------------------------------------------------------------- softmax: a token per thread, then a dim
+        constexpr int W = G::W;
+        const int grp = (warp - 4) >> 2, me = (tid - 128) & 127, w4 = warp & 3;
+        const uint32_t bar_id = 1 + grp;       // the group's barrier
+        const int c0 = grp * W;                // the group's first query of the tile
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * w4) << 16);
+        float* lim = lim_sm + c0;
+        float* sub = sub_sm + c0;
+        float* alpha = alpha_sm + c0;
+        float* red = red_sm + grp * 128;       // [4][32]
+        int t = 0, k = 0;
+        uint32_t odds = 0;                     // tiles with marked tokens so far
+        // (what ends the loops is voted on, so that the warps always meet at the same barriers)
+        for (int item = blockIdx.x; item < total; item += gridDim.x, ++k) {
+            await(qfull + (k & 1), (k >> 1) & 1);
+            const ItemRec it = item_sm[k & 1];
+            const int* qlen = qlen_sm + (k & 1) * N + c0;
+            const int q0 = it.q0 + c0;
+            float l[W];
+#pragma unroll
+            for (int q = 0; q < W; ++q) l[q] = 0.f;
+            if (me < W) {
+                lim[me] = kNoMax;
+                sub[me] = -kShift;
+            }
+            named_bar_sync(bar_id, 128);
+            const int64_t plane = static_cast<int64_t>(p.chunks) * p.chunk * 4;
+            float* sbase = p.scores ? p.scores + (static_cast<int64_t>(it.a * p.kv_heads + it.g) * (p.qp >> 2) + (q0 >> 2)) * plane : nullptr;
+            const int planes = (p.qp - q0) >> 2;
+
+            bool stop = false;
+            for (int tb = it.tok0; tb < it.end; tb += kTcTile, ++t) {
+                const int tok = tb + me;
+                const int vs = t % G::v_slots;
+                uint8_t* vt = sm + G::off_v + vs * G::half;
+                float e = 0.f, f[4];
+                if constexpr (G::q8) {
+                    // the token's K scales and the exponent of its largest V scale
+                    const int ksl = t % G::k_slots;
+                    await(kfull + ksl, (t / G::k_slots) & 1);
+                    const uint2 sc = *reinterpret_cast<const uint2*>(sm + ksl * G::half + (me >> 6) * kQ8Half + 8192 + (me & 63) * 8);
+                    f[0] = __low2float(as_h2(sc.x)), f[1] = __high2float(as_h2(sc.x));
+                    f[2] = __low2float(as_h2(sc.y)), f[3] = __high2float(as_h2(sc.y));
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(kempty + ksl);
+                }
+                await(vfull + vs, (t / G::v_slots) & 1);
+                bool miss = vmiss[vs] != 0;  // a page of the tile is outside the pool
+                if constexpr (G::q8) {
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const uint32_t w = *reinterpret_cast<const uint16_t*>(vt + (me >> 6) * kQ8Half + 8192 + (b * 64 + (me & 63)) * 2) & 0x7FFFu;
+                        top = w > 0x7C00u ? top : max(top, w);  // (NaN scales do not count)
+                    }
+                    e = static_cast<float>(min(max(static_cast<int>(top >> 10), 1), 29) - 15);
+                }
+                await(sfull, t & 1);
+                tc_fence_after();
+                // ---- base-2 scores, masked; a query's first tile, or one that passes its reference by more
+                // than the slack, takes the long way
+                float x[W];
+                if constexpr (G::q8) {
+#pragma unroll
+                    for (int c = 0; c < W; c += 8) {
+                        float v[4][8];
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) tmem_load8(lanes + G::col_s + b * N + c0 + c, v[b]);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            x[c + i] = fmaf(v[3][i], f[3], fmaf(v[2][i], f[2], fmaf(v[1][i], f[1], v[0][i] * f[0]))) * p.c2;
+                    }
+                } else {
+                    float v[W / 8][8];
+#pragma unroll
+                    for (int c = 0; c < W / 8; ++c) tmem_load8(lanes + G::col_s + c0 + 8 * c, v[c]);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int q = 0; q < W; ++q) x[q] = v[q / 8][q % 8] * p.c2;
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sempty);
+                if (miss || tb + kTcTile > it.minlen) {  // some query does not see some token of the tile
+#pragma unroll
+                    for (int q = 0; q < W; ++q)
+                        if (miss || tok >= qlen[q]) x[q] = kNoMax;
+                }
+                if (sbase) {
+                    float* at = sbase + static_cast<int64_t>(tok) * 4;
+#pragma unroll
+                    for (int q = 0; q < W; q += 4)
+                        if ((q >> 2) < planes) *reinterpret_cast<float4*>(at + (q >> 2) * plane) = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
+                }
+                bool over = !live || miss;
+#pragma unroll
+                for (int q = 0; q < W; q += 4) {
+                    const float4 m = *reinterpret_cast<const float4*>(lim + q);
+                    if constexpr (G::q8) x[q] += e, x[q + 1] += e, x[q + 2] += e, x[q + 3] += e;
+                    over |= x[q] > m.x || x[q + 1] > m.y || x[q + 2] > m.z || x[q + 3] > m.w;
+                }
+                bool moved = false;  // some reference moves
+                if (bar_or(bar_id, 128, over)) {
+                    if (bar_or(bar_id, 128, !live)) {
+                        stop = true;
+                        break;
+                    }
+                    miss = bar_or(bar_id, 128, miss);
+                    // (a NaN is no maximum: fmaxf passes it over)
+                    red[w4 * 32 + lane] = reduce_columns<W>(x, kNoMax, [](float a, float b) { return fmaxf(a, b); });
+                    named_bar_sync(bar_id, 128);
+                    if (me < W) {
+                        float m = fmaxf(fmaxf(red[me], red[32 + me]), fmaxf(red[64 + me], red[96 + me]));
+                        if (fabsf(m) < 1e6f) m = ceilf(m * 16.f) * 0.0625f;  // (sums with the constants are then exact)
+                        const bool passed = m > lim[me];
+                        alpha[me] = passed ? ex2(lim[me] - kSlack - m) : 1.f;  // (2^-inf = 0 the first time)
+                        if (passed) {
+                            lim[me] = m + kSlack;
+                            sub[me] = m - kShift;
+                        }
+                    }
+                    named_bar_sync(bar_id, 128);
+#pragma unroll
+                    for (int q = 0; q < W; ++q) {
+                        const float a = alpha[q];
+                        l[q] *= a;
+                        moved |= a != 1.f;
+                    }
+                }
+                const bool edge = miss || tb + kTcTile > it.minlen;
+                const bool fresh = tb == it.tok0;  // the outputs hold nothing yet
+                if (t > 0) {
+                    await(odone, (t - 1) & 1);  // the last tile's P is read and its outputs are summed
+                    tc_fence_after();
+                }
+                if (moved && !fresh) {
+#pragma unroll
+                    for (int c = 0; c < W; c += 8) {
+                        float v[8];
+                        tmem_load8(lanes + G::col_o + c0 + c, v);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] *= alpha[c + i];
+                        tmem_store8(lanes + G::col_o + c0 + c, v);
+                    }
+                    tc_wait_st();
+                }
+                // ---- probabilities, as rows of the B operand (tokens contiguous, swizzled)
+                const float inv = G::q8 ? __int_as_float((127 - static_cast<int>(e)) << 23) : 1.f;  // 2^-e
+                uint8_t* pbase = sm + G::off_p + (me >> 6) * (N * 128) + c0 * 128 + (me & 7) * 2;
+                const int chunk = (me & 63) >> 3;
+#pragma unroll
+                for (int q = 0; q < W; q += 2) {
+                    const float2 m = *reinterpret_cast<const float2*>(sub + q);
+                    const float pa = ex2(x[q] - m.x), pb = ex2(x[q + 1] - m.y);
+                    l[q] = G::q8 ? fmaf(pa, inv, l[q]) : l[q] + pa;
+                    l[q + 1] = G::q8 ? fmaf(pb, inv, l[q + 1]) : l[q + 1] + pb;
+                    uint32_t hi, lo;
+                    split2<BF>(pa, pb, hi, lo);
+                    uint8_t* at = pbase + q * 128 + ((chunk ^ (q & 7)) << 4);  // (c0 is a multiple of 8)
+                    uint8_t* bt = pbase + (q + 1) * 128 + ((chunk ^ ((q + 1) & 7)) << 4);
+                    *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(hi);
+                    *reinterpret_cast<uint16_t*>(bt) = static_cast<uint16_t>(hi >> 16);
+                    *reinterpret_cast<uint16_t*>(at + G::opnd) = static_cast<uint16_t>(lo);
+                    *reinterpret_cast<uint16_t*>(bt + G::opnd) = static_cast<uint16_t>(lo >> 16);
+                }
+                bool holds = !fresh;
+                if (edge) {
+                    // Tokens that some query does not see.  Past the sequence's end (and in tiles with a
+                    // missing page) V holds anything and becomes zero (q8_0: its scales do, in the
+                    // converting warps).  One that some queries see and whose V (q8_0: a scale) is
+                    // not finite is added query by query, to those that see it, and is zero in the
+                    // product.  (Both groups come to the same answers.)
+                    bool odd = false;
+                    const bool gone = miss || tok >= it.end;
+                    auto piece = [&](int c) { return reinterpret_cast<uint4*>(vt + (c >> 3) * (kTcTile * 128) + me * 128 + (((c & 7) ^ (me & 7)) << 4)); };
+                    if (!gone && tok >= it.minlen) {
+                        if constexpr (G::q8) {
+#pragma unroll
+                            for (int b = 0; b < 4; ++b)
+                                odd |= (*reinterpret_cast<const uint16_t*>(vt + (me >> 6) * kQ8Half + 8192 + (b * 64 + (me & 63)) * 2) & 0x7C00u) == 0x7C00u;
+                        } else {
+                            constexpr uint32_t ex = BF ? 0x7F80u : 0x7C00u;
+                            auto bad = [&](uint32_t w) { return (w & ex) == ex || ((w >> 16) & ex) == ex; };
+                            for (int c = 0; c < 16; ++c) {
+                                const uint4 v = *piece(c);
+                                odd |= bad(v.x) || bad(v.y) || bad(v.z) || bad(v.w);
+                            }
+                        }
+                    }
+                    const bool any = bar_or(bar_id, 128, odd);  // (also: P is written)
+                    if (any) {
+                        const uint32_t who = __ballot_sync(0xffffffffu, odd);
+                        if (lane == 0) odd_sm[w4] = who;  // (both groups write the same)
+                        named_bar_sync(bar_id, 128);
+                        const uint16_t* P = reinterpret_cast<const uint16_t*>(sm + G::off_p);
+#pragma unroll 1
+                        for (int c = 0; c < W; c += 8) {
+                            float v[8];
+                            if (holds) {
+                                tmem_load8(lanes + G::col_o + c0 + c, v);
+                                tc_wait_ld();
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) v[i] = 0.f;
+                            }
+#pragma unroll 1
+                            for (int j = 0; j < kTcTile; ++j) {
+                                if (!((odd_sm[j >> 5] >> (j & 31)) & 1)) continue;
+                                float y;  // V of token j, dim me (q8_0: by its normalised scale)
+                                if constexpr (G::q8) {
+                                    const uint8_t* rec = vt + (j >> 6) * kQ8Half;
+                                    const float d = __half2float(*reinterpret_cast<const __half*>(rec + 8192 + ((me >> 5) * 64 + (j & 63)) * 2));
+                                    uint32_t top = 0;
+                                    for (int b = 0; b < 4; ++b) {
+                                        const uint32_t w = *reinterpret_cast<const uint16_t*>(rec + 8192 + (b * 64 + (j & 63)) * 2) & 0x7FFFu;
+                                        top = w > 0x7C00u ? top : max(top, w);
+                                    }
+                                    const int ej = min(max(static_cast<int>(top >> 10), 1), 29) - 15;
+                                    y = static_cast<float>(static_cast<int8_t>(rec[me * 64 + (j & 63)])) * (d * __int_as_float((127 - ej) << 23));
+                                } else {
+                                    const uint32_t u = *reinterpret_cast<const uint16_t*>(
+                                        vt + (me >> 6) * (kTcTile * 128) + j * 128 + ((((me & 63) >> 3) ^ (j & 7)) << 4) + (me & 7) * 2);
+                                    y = BF ? __uint_as_float(u << 16) : __half2float(__ushort_as_half(static_cast<uint16_t>(u)));
+                                }
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const int q = c + i, at = (j >> 6) * (N * 64) + (c0 + q) * 64 + ((((j & 63) >> 3) ^ (q & 7)) << 3) + (j & 7);
+                                    const uint32_t h = P[at], u = P[at + G::opnd / 2];
+                                    const float pr = BF ? __uint_as_float(h << 16) + __uint_as_float(u << 16)
+                                                        : __half2float(__ushort_as_half(static_cast<uint16_t>(h))) +
+                                                              __half2float(__ushort_as_half(static_cast<uint16_t>(u)));
+                                    if (tb + j < qlen[q]) v[i] = fmaf(pr, y, v[i]);
+                                }
+                            }
+                            tmem_store8(lanes + G::col_o + c0 + c, v);
+                        }
+                        tc_wait_st();
+                        holds = true;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(oddread);
+                        await(oddread, odds++ & 1);  // V's rows are read by both groups
+                    }
+                    if constexpr (!G::q8) {
+                        if (grp == 0 && (gone || odd))
+                            for (int c = 0; c < 16; ++c) *piece(c) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+                if (me == 0 && grp == 0) *accum_sm = holds;
+                fence_proxy_async_smem();  // P and V, before the tensor cores read them
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(pfull);
+                    if constexpr (G::q8) mbar_arrive(vempty + vs);
+                }
+            }
+            if (stop) break;
+
+            // ---- the item's partial: a dim per thread
+            await(odone, (t - 1) & 1);
+            tc_fence_after();
+            const int64_t slot0 = (static_cast<int64_t>(it.a * p.kv_heads + it.g) * p.chunks + it.tok0 / p.chunk) * p.qp + q0;
+            float v[W / 8][8];
+#pragma unroll
+            for (int c = 0; c < W / 8; ++c) tmem_load8(lanes + G::col_o + c0 + 8 * c, v[c]);
+            tc_wait_ld();
+            tc_fence_before();
+            float* po = p.o + slot0 * D + me;
+#pragma unroll
+            for (int q = 0; q < W; ++q)
+                if (q0 + q < it.nq) po[q * D] = v[q / 8][q % 8];
+            red[w4 * 32 + lane] = reduce_columns<W>(l, 0.f, [](float a, float b) { return a + b; });
+            named_bar_sync(bar_id, 128);
+            if (me < W && q0 + me < it.nq) {
+                const float m = lim[me] == kNoMax ? kNoMax : sub[me] + kShift;
+                const float s = (red[me] + red[32 + me]) + (red[64 + me] + red[96 + me]);
+                *reinterpret_cast<float2*>(p.ml + (slot0 + me) * 2) = make_float2(m, s);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(qempty + (k & 1));
+            named_bar_sync(bar_id, 128);  // (the sums and references are read)
+        }
+        if (!live && me == 0) atomicOr(p.err, kErrTimeout);
+    } else if (G::q8) {
+        // ---------------------------------------------------------------- q8_0 to fp16: a token per thread, then a dim
+        constexpr uint32_t kBar = 3;
+        const int me = tid - 384, w4 = warp - 12;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * w4) << 16);
+        __half* dv = reinterpret_cast<__half*>(sm + G::off_dv);  // [4][128]
+        int t = 0, k = 0;
+        bool go = true;
+        for (int item = blockIdx.x; item < total && go; item += gridDim.x, ++k) {
+            await(qfull + (k & 1), (k >> 1) & 1);
+            const ItemRec it = item_sm[k & 1];
+            for (int tb = it.tok0; tb < it.end; tb += kTcTile, ++t) {
+                const int ks = t % G::k_slots, vs = t % G::v_slots;
+                await(kfull + ks, (t / G::k_slots) & 1);
+                if (t > 0) await(akfree, (t - 1) & 1);
+                tc_fence_after();
+                const int slot = me & 63;
+                const uint8_t* kt = sm + ks * G::half + (me >> 6) * kQ8Half + slot * 128;
+                const int key = q8_key(slot & 7);
+#pragma unroll
+                for (int c = 0; c < 8; c += 2) {
+                    uint32_t out[16];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(kt + 16 * ((c + j) ^ key));
+                        const uint32_t u[4] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u, w.z ^ 0x80808080u, w.w ^ 0x80808080u};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            out[8 * j + 2 * i] = i8_to_h2(u[i], 0x4140u);
+                            out[8 * j + 2 * i + 1] = i8_to_h2(u[i], 0x4342u);
+                        }
+                    }
+                    tmem_st16(lanes + G::col_k + 8 * c, out);
+                }
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(akfull);
+                    mbar_arrive(kempty + ks);
+                }
+                // ---- V: normalised scales by token, then elements by dim
+                await(vfull + vs, (t / G::v_slots) & 1);
+                const uint8_t* vt = sm + G::off_v + vs * G::half;
+                {
+                    const int tok = tb + me;
+                    const uint8_t* sc = vt + (me >> 6) * kQ8Half + 8192 + slot * 2;
+                    uint32_t d[4], top = 0;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        d[b] = *reinterpret_cast<const uint16_t*>(sc + b * 128);
+                        const uint32_t w = d[b] & 0x7FFFu;
+                        top = w > 0x7C00u ? top : max(top, w);
+                    }
+                    const __half inv = __ushort_as_half(static_cast<uint16_t>((30 - min(max(static_cast<int>(top >> 10), 1), 29)) << 10));
+                    bool odd = false;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) odd |= (d[b] & 0x7C00u) == 0x7C00u;
+                    const bool none = vmiss[vs] != 0 || tok >= it.end || (odd && tok >= it.minlen);
+                    named_bar_sync(kBar, 128);  // the last tile's scales are read
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+                        dv[b * kTcTile + me] = none ? __ushort_as_half(0) : __hmul(__ushort_as_half(static_cast<uint16_t>(d[b])), inv);
+                }
+                if (t > 0) await(avfree, (t - 1) & 1);
+                if (bar_or(kBar, 128, !live)) {
+                    go = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {  // 16 tokens
+                    const uint4 w = *reinterpret_cast<const uint4*>(vt + (c >> 2) * kQ8Half + me * 64 + 16 * (c & 3));
+                    const uint4 s0 = *reinterpret_cast<const uint4*>(dv + w4 * kTcTile + 16 * c);
+                    const uint4 s1 = *reinterpret_cast<const uint4*>(dv + w4 * kTcTile + 16 * c + 8);
+                    const uint32_t u[4] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u, w.z ^ 0x80808080u, w.w ^ 0x80808080u};
+                    const uint32_t s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const __half2 v = as_h2(i8_to_h2(u[i >> 1], (i & 1) ? 0x4342u : 0x4140u));
+                        const __half2 h = __hmul2(v, as_h2(s[i]));
+                        hi[i] = as_u32(h);
+                        lo[i] = as_u32(__hfma2(v, as_h2(s[i]), __hneg2(h)));
+                    }
+                    tmem_st8(lanes + G::col_vh + 8 * c, hi);
+                    tmem_st8(lanes + G::col_vl + 8 * c, lo);
+                }
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(avfull);
+                    mbar_arrive(vempty + vs);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(qempty + (k & 1));
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, G::cols);
+}
+
+template <int FMT, int N>
+cudaError_t launch_attend_tc_one(const AttendLaunch& a, cudaStream_t s) {
+    const int bytes = TcGeo<FMT, N>::smem(a.p.agents);
+    cudaError_t e = cudaFuncSetAttribute(attend_partial_tc<FMT, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    attend_partial_tc<FMT, N><<<a.sms, TcGeo<FMT, N>::threads, bytes, s>>>(a.map, a.p);
+    return cudaGetLastError();
+}
+
+// The fewest columns that take all queries of a sequence, up to 48.
+template <int FMT>
+cudaError_t launch_attend_tc(const AttendLaunch& a, cudaStream_t s) {
+    return a.max_q <= 16   ? launch_attend_tc_one<FMT, 16>(a, s)
+           : a.max_q <= 32 ? launch_attend_tc_one<FMT, 32>(a, s)
+                           : launch_attend_tc_one<FMT, 48>(a, s);
+}
+
+}  // namespace kv
+}  // namespace qmm
