@@ -38,15 +38,16 @@ struct TcGeo {
     static constexpr int threads = q8 ? 512 : 384;
     static constexpr int W = N / 2;                                // queries of a softmax group
     static constexpr int half = q8 ? 2 * kQ8Half : kTcTile * 256;  // bytes of a tile's K or V
-    static constexpr int k_slots = q8 ? 4 : 3, v_slots = q8 ? 4 : 2;
+    static constexpr int k_slots = q8 ? 4 : 3, v_slots = q8 ? 4 : N == 16 ? 3 : 2;
     static constexpr int opnd = N * 256;                           // bytes of a B operand: N rows of 128 16-bit values
-    // tensor memory columns: scores (one set per 32-dim block of a q8_0 pool), outputs, and the A operands
-    static constexpr int col_s = 0, col_o = q8 ? 4 * N : 64, col_k = 240, col_vh = 304, col_vl = 368;
-    static constexpr int cols = q8 ? 512 : 128;
+    // tensor memory columns: scores (one set per 32-dim block of a q8_0 pool), outputs (2 N: those of P's
+    // high and of its low parts), and the A operands
+    static constexpr int col_s = 0, col_o = q8 ? 4 * N : 64, col_k = 288, col_vh = 352, col_vl = 416;
+    static constexpr int cols = q8 ? 512 : 256;
     // shared memory, after aligning to 1024
     static constexpr int off_v = k_slots * half;
     static constexpr int off_q = (off_v + v_slots * half + 1023) / 1024 * 1024;  // two
-    static constexpr int off_p = off_q + 2 * opnd;                              // hi, lo
+    static constexpr int off_p = off_q + 2 * opnd;                              // per 64 tokens: N rows of high parts, N of low ones
     static constexpr int off_dv = off_p + 2 * opnd;                             // q8_0: normalised V scales [4][128] fp16
     static constexpr int off_len = off_dv + (q8 ? 4 * kTcTile * 2 : 0);         // [2][N] tokens that a query sees
     static constexpr int off_lim = off_len + 2 * N * 4;                         // [N] reference + slack
@@ -88,33 +89,17 @@ __device__ __forceinline__ void tmem_store8(uint32_t taddr, const float (&v)[8])
                  : "memory");
 }
 
-// The products, issued by the thread whose `one` is set while its whole warp computes the operands
-// (which then stay in uniform registers; inside a branch of one lane each issue took about 100 clocks).
-__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// One lane of a converged warp.  (The products' operands stay in uniform registers inside its branch; by
+// `lane == 0` an issue took 49 clocks and by a predicate on the instruction 68, against the 40 that the
+// smallest product itself takes.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 q, %0, 0;\n\t"
-        "setp.ne.b32 p, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%1], %2, %3, %4, p;\n\t}" ::"r"(one),
-        "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 q, %0, 0;\n\t"
-        "setp.ne.b32 p, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], %3, %4, p;\n\t}" ::"r"(one),
-        "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
-}
-__device__ __forceinline__ void mma_commit(uint32_t one, uint64_t* bar) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %0, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(one),
-        "r"(smem_u32(bar))
-        : "memory");
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
 }
 
 // v[c] of W <= 32 columns reduced over the warp's lanes by f: lane c returns column c's.  At each
@@ -303,10 +288,10 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
         // ---------------------------------------------------------------- products
         constexpr uint32_t kType = BF ? (1u << 7) | (1u << 10) : 0u;
         constexpr uint32_t kIdescS = idesc_f16_f32(128, N) | kType;
-        constexpr uint32_t kIdescO = kIdescS | (G::q8 ? 0u : 1u << 15);  // 16-bit pools: A is M-contiguous
+        // (both parts of P at once: 2 N columns; 16-bit pools: A is M-contiguous)
+        constexpr uint32_t kIdescO = idesc_f16_f32(128, 2 * N) | kType | (G::q8 ? 0u : 1u << 15);
         int t = 0, k = 0;  // tiles and items so far
-        const uint32_t one = lane == 0;
-        const uint32_t ph = smem_u32(sm + G::off_p);
+        const uint64_t bp = smem_desc_sw128(smem_u32(sm + G::off_p));
         auto product_o = [&](int i) {
             await_warp(pfull, i & 1);
             const int vs = i % G::v_slots;
@@ -314,24 +299,23 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
             else await_warp(vfull + vs, (i / G::v_slots) & 1);
             if (!live) return;
             tc_fence_after();
-            const uint64_t bh = smem_desc_sw128(ph), bl = smem_desc_sw128(ph + G::opnd);
             const uint64_t av = smem_desc_sw128_mn(smem_u32(sm + G::off_v) + vs * G::half, kTcTile * 128);
-            uint32_t acc = *accum_sm != 0;
+            const uint32_t acc = *accum_sm != 0;
+            if (elect_one()) {
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-                const uint64_t at = ((ks >> 2) * (N * 128) + (ks & 3) * 32) >> 4;
-                if constexpr (G::q8) {
-                    mma_ts(one, tmem + G::col_o, tmem + G::col_vh + 8 * ks, bh + at, kIdescO, acc);
-                    mma_ts(one, tmem + G::col_o, tmem + G::col_vh + 8 * ks, bl + at, kIdescO, 1);
-                    mma_ts(one, tmem + G::col_o, tmem + G::col_vl + 8 * ks, bh + at, kIdescO, 1);
-                } else {
-                    mma_ss(one, tmem + G::col_o, av + ks * (2048 >> 4), bh + at, kIdescO, acc);
-                    mma_ss(one, tmem + G::col_o, av + ks * (2048 >> 4), bl + at, kIdescO, 1);
+                for (int ks = 0; ks < 8; ++ks) {
+                    const uint64_t b = bp + (((ks >> 2) * (2 * N * 128) + (ks & 3) * 32) >> 4);
+                    if constexpr (G::q8) {
+                        tc_mma_f16_ts(tmem + G::col_o, tmem + G::col_vh + 8 * ks, b, kIdescO, ks ? 1 : acc);
+                        tc_mma_f16_ts(tmem + G::col_o, tmem + G::col_vl + 8 * ks, b, kIdescS, 1);  // (by the high parts only)
+                    } else {
+                        tc_mma_f16_ss(tmem + G::col_o, av + ks * (2048 >> 4), b, kIdescO, ks ? 1 : acc);
+                    }
                 }
-                acc = 1;
+                tc_commit(odone);
+                tc_commit(G::q8 ? avfree : vempty + vs);
             }
-            mma_commit(one, odone);
-            mma_commit(one, G::q8 ? avfree : vempty + vs);
+            __syncwarp();
         };
         for (int item = blockIdx.x; item < total && live; item += gridDim.x, ++k) {
             await_warp(qfull + (k & 1), (k >> 1) & 1);
@@ -345,27 +329,29 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                 if (!live) break;
                 tc_fence_after();
                 const uint64_t ak = smem_desc_sw128(smem_u32(sm) + s * G::half);
+                const bool last = tb + kTcTile >= end;
+                if (elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {
-                    const uint64_t at = ((ks >> 2) * (N * 128) + (ks & 3) * 32) >> 4;
-                    if constexpr (G::q8)
-                        mma_ts(one, tmem + G::col_s + (ks >> 1) * N, tmem + G::col_k + 8 * ks, bq + at, kIdescS, ks & 1);
-                    else
-                        mma_ss(one, tmem + G::col_s, ak + (((ks >> 2) * (kTcTile * 128) + (ks & 3) * 32) >> 4), bq + at, kIdescS, ks > 0);
+                    for (int ks = 0; ks < 8; ++ks) {
+                        const uint64_t b = bq + (((ks >> 2) * (N * 128) + (ks & 3) * 32) >> 4);
+                        if constexpr (G::q8)
+                            tc_mma_f16_ts(tmem + G::col_s + (ks >> 1) * N, tmem + G::col_k + 8 * ks, b, kIdescS, ks & 1);
+                        else
+                            tc_mma_f16_ss(tmem + G::col_s, ak + (((ks >> 2) * (kTcTile * 128) + (ks & 3) * 32) >> 4), b, kIdescS, ks > 0);
+                    }
+                    tc_commit(sfull);
+                    tc_commit(G::q8 ? akfree : kempty + s);
+                    if (last) tc_commit(qempty + (k & 1));
                 }
-                mma_commit(one, sfull);
-                mma_commit(one, G::q8 ? akfree : kempty + s);
-                if (tb + kTcTile >= end) mma_commit(one, qempty + (k & 1));
+                __syncwarp();
                 if (t > 0) product_o(t - 1);
             }
         }
         if (t > 0 && live) product_o(t - 1);
         // every product issued has finished before the tensor memory is released
-        if (lane == 0) {
-            tc_commit(drained);
-            volatile int go_on = 0;
-            mbar_wait_bounded(drained, 0, &go_on, 10000000000ull);
-        }
+        if (elect_one()) tc_commit(drained);
+        volatile int go_on = 0;
+        mbar_wait_bounded(drained, 0, &go_on, 10000000000ull);
         __syncwarp();
     } else if (warp < 4) {
         // ---------------------------------------------------------------- the next item: numbers and queries, half a warp per row
@@ -540,18 +526,20 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                 if (moved && !fresh) {
 #pragma unroll
                     for (int c = 0; c < W; c += 8) {
-                        float v[8];
-                        tmem_load8(lanes + G::col_o + c0 + c, v);
+                        float v[2][8];
+                        tmem_load8(lanes + G::col_o + c0 + c, v[0]);
+                        tmem_load8(lanes + G::col_o + N + c0 + c, v[1]);
                         tc_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] *= alpha[c + i];
-                        tmem_store8(lanes + G::col_o + c0 + c, v);
+                        for (int i = 0; i < 8; ++i) v[0][i] *= alpha[c + i], v[1][i] *= alpha[c + i];
+                        tmem_store8(lanes + G::col_o + c0 + c, v[0]);
+                        tmem_store8(lanes + G::col_o + N + c0 + c, v[1]);
                     }
                     tc_wait_st();
                 }
                 // ---- probabilities, as rows of the B operand (tokens contiguous, swizzled)
                 const float inv = G::q8 ? __int_as_float((127 - static_cast<int>(e)) << 23) : 1.f;  // 2^-e
-                uint8_t* pbase = sm + G::off_p + (me >> 6) * (N * 128) + c0 * 128 + (me & 7) * 2;
+                uint8_t* pbase = sm + G::off_p + (me >> 6) * (2 * N * 128) + c0 * 128 + (me & 7) * 2;
                 const int chunk = (me & 63) >> 3;
 #pragma unroll
                 for (int q = 0; q < W; q += 2) {
@@ -565,8 +553,8 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                     uint8_t* bt = pbase + (q + 1) * 128 + ((chunk ^ ((q + 1) & 7)) << 4);
                     *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(hi);
                     *reinterpret_cast<uint16_t*>(bt) = static_cast<uint16_t>(hi >> 16);
-                    *reinterpret_cast<uint16_t*>(at + G::opnd) = static_cast<uint16_t>(lo);
-                    *reinterpret_cast<uint16_t*>(bt + G::opnd) = static_cast<uint16_t>(lo >> 16);
+                    *reinterpret_cast<uint16_t*>(at + N * 128) = static_cast<uint16_t>(lo);
+                    *reinterpret_cast<uint16_t*>(bt + N * 128) = static_cast<uint16_t>(lo >> 16);
                 }
                 bool holds = !fresh;
                 if (edge) {
@@ -629,8 +617,8 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                                 }
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) {
-                                    const int q = c + i, at = (j >> 6) * (N * 64) + (c0 + q) * 64 + ((((j & 63) >> 3) ^ (q & 7)) << 3) + (j & 7);
-                                    const uint32_t h = P[at], u = P[at + G::opnd / 2];
+                                    const int q = c + i, at = (j >> 6) * (2 * N * 64) + (c0 + q) * 64 + ((((j & 63) >> 3) ^ (q & 7)) << 3) + (j & 7);
+                                    const uint32_t h = P[at], u = P[at + N * 64];
                                     const float pr = BF ? __uint_as_float(h << 16) + __uint_as_float(u << 16)
                                                         : __half2float(__ushort_as_half(static_cast<uint16_t>(h))) +
                                                               __half2float(__ushort_as_half(static_cast<uint16_t>(u)));
@@ -638,6 +626,10 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                                 }
                             }
                             tmem_store8(lanes + G::col_o + c0 + c, v);
+                            if (!holds) {
+                                const float zero[8] = {};
+                                tmem_store8(lanes + G::col_o + N + c0 + c, zero);
+                            }
                         }
                         tc_wait_st();
                         holds = true;
@@ -665,15 +657,18 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
             await(odone, (t - 1) & 1);
             tc_fence_after();
             const int64_t slot0 = (static_cast<int64_t>(it.a * p.kv_heads + it.g) * p.chunks + it.tok0 / p.chunk) * p.qp + q0;
-            float v[W / 8][8];
-#pragma unroll
-            for (int c = 0; c < W / 8; ++c) tmem_load8(lanes + G::col_o + c0 + 8 * c, v[c]);
-            tc_wait_ld();
-            tc_fence_before();
             float* po = p.o + slot0 * D + me;
 #pragma unroll
-            for (int q = 0; q < W; ++q)
-                if (q0 + q < it.nq) po[q * D] = v[q / 8][q % 8];
+            for (int c = 0; c < W; c += 8) {
+                float v[2][8];
+                tmem_load8(lanes + G::col_o + c0 + c, v[0]);
+                tmem_load8(lanes + G::col_o + N + c0 + c, v[1]);
+                tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (q0 + c + i < it.nq) po[(c + i) * D] = v[0][i] + v[1][i];
+            }
+            tc_fence_before();
             red[w4 * 32 + lane] = reduce_columns<W>(l, 0.f, [](float a, float b) { return a + b; });
             named_bar_sync(bar_id, 128);
             if (me < W && q0 + me < it.nq) {
