@@ -6,6 +6,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "qmm_ptx.cuh"
 #include "qmm_serve.h"
 
@@ -14,7 +16,8 @@ namespace kv {
 
 constexpr int kQ8Rec = 17408;   // bytes of a q8_0 record (64 tokens, one KV head)
 constexpr int kQ8Half = 8704;   // its K part, and its V part
-constexpr int kMaxAgents = 1024;
+constexpr int kMaxAgents = 960;      // (the table of sequences shares an SM's memory with the tiles)
+constexpr int kMaxShared = 227 * 1024;  // dynamic shared memory of a block
 constexpr int kMaxGroupQ = 4096;  // queries of one sequence per KV head in a call
 constexpr int kErrTimeout = 1, kErrPage = 2, kErrRange = 4;
 
@@ -47,16 +50,41 @@ inline qmm_status check_dims(const qmm_kv_dims* d) {
     return QMM_OK;
 }
 
-// The current device, which has to be an sm_103 one, and its number of SMs.
+// The current device, which has to be an sm_103 one, and its number of SMs (looked up once per device).
 inline qmm_status check_gpu(int* dev, int* sms) {
-    int major = 0, minor = 0;
-    if (cudaGetDevice(dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, *dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, *dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev) != cudaSuccess)
-        return QMM_ERR_NO_DEVICE;
-    return major == 10 && minor == 3 ? QMM_OK : QMM_ERR_NO_DEVICE;
+    static std::atomic<int> known[64];  // SMs + 1; 1: not an sm_103 device; 0: not looked up
+    if (cudaGetDevice(dev) != cudaSuccess) return QMM_ERR_NO_DEVICE;
+    int k = *dev >= 0 && *dev < 64 ? known[*dev].load(std::memory_order_relaxed) : 0;
+    if (k == 0) {
+        int major = 0, minor = 0, n = 0;
+        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, *dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, *dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, *dev) != cudaSuccess)
+            return QMM_ERR_NO_DEVICE;
+        k = major == 10 && minor == 3 ? n + 1 : 1;
+        if (*dev >= 0 && *dev < 64) known[*dev].store(k, std::memory_order_relaxed);
+    }
+    *sms = k - 1;
+    return k > 1 ? QMM_OK : QMM_ERR_NO_DEVICE;
 }
+
+// A kernel's attributes, set once per device.
+class Once {
+    std::atomic<uint64_t> done{0};
+
+public:
+    // all the dynamic shared memory that a block without static shared memory, or with `fixed` bytes
+    // of it, can have
+    template <typename K>
+    cudaError_t allow_shared(K kernel, int dev, int fixed = 0, bool big_cluster = false) {
+        const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t{1} << dev : 0;
+        if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared - fixed);
+        if (e == cudaSuccess && big_cluster) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+        return e;
+    }
+};
 
 // Exclusive prefix of `v` over the block's threads (blockDim.x a multiple of 32, at most 1024)
 // and the block's total.  `tmp`: 33 ints of shared memory; every thread takes part, and the

@@ -110,12 +110,28 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join(const AttendParams p
         if (t0 >= info.x) continue;  // past the sequence's longest row, or a refused sequence (-1)
         const int nq = info.z * p.group;
         __syncthreads();
-        for (int q = warp; q < nq; q += kJoinWarps) {
-            const int n = (p.row_len[info.y + q / p.group] + p.chunk - 1) / p.chunk;
-            const float2 t = join_ml(p, static_cast<int64_t>(ag) * p.chunks * p.qp + q, n);
-            if (lane == 0) {
-                ref[q] = t.x == kNoMax ? 0.f : t.x - kShift;
-                inv[q] = t.x == kNoMax ? 0.f : 1.f / t.y;
+        // several threads per query, chunks dealt out among them (consecutive queries lie side by side)
+        const int per_q = nq <= 8 ? 32 : nq <= 32 ? 8 : nq <= 64 ? 4 : 1;
+        for (int q0 = 0; q0 < nq; q0 += kJoinThreads / per_q) {
+            const int q = q0 + tid / per_q, part = tid % per_q;
+            const int n = q < nq ? (p.row_len[info.y + q / p.group] + p.chunk - 1) / p.chunk : 0;
+            const float2* ml = reinterpret_cast<const float2*>(p.ml) + static_cast<int64_t>(ag) * p.chunks * p.qp + q;
+            float m = kNoMax, l = 0.f;
+#pragma unroll 4
+            for (int c = part; c < n; c += per_q) {
+                const float2 v = ml[static_cast<int64_t>(c) * p.qp];
+                if (v.x > m) l *= exp2f(m - v.x), m = v.x;
+                if (v.x > kNoMax) l = fmaf(v.y, exp2f(v.x - m), l);
+            }
+            for (int k = per_q >> 1; k >= 1; k >>= 1) {
+                const float mo = __shfl_xor_sync(0xffffffffu, m, k), lo = __shfl_xor_sync(0xffffffffu, l, k);
+                const float mn = fmaxf(m, mo), r = mn == kNoMax ? 0.f : mn;
+                l = l * exp2f(m - r) + lo * exp2f(mo - r);
+                m = mn;
+            }
+            if (part == 0 && q < nq) {
+                ref[q] = m == kNoMax ? 0.f : m - kShift;
+                inv[q] = m == kNoMax ? 0.f : 1.f / l;
             }
         }
         __syncthreads();
@@ -139,14 +155,14 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join(const AttendParams p
 namespace {
 
 // Tokens per chunk, by the dims alone (so that a row's bits are those of any other call): the
-// longest of 1024 .. a tile that gives every block of a GB300's grid two items (one block per SM at
-// head dimension 128, four otherwise) when all sequences are full, and whose pages one warp can
-// hold (32).
+// longest of 1024 .. a tile that gives every block of a GB300's grid two items at head dimension 128
+// (one block per SM), and six otherwise (four), when all sequences are full, and whose pages one
+// warp can hold (32).  At head dimension 64, 61 ragged sequences: 104 us at 1,024, 92 at 512, 93 at 256.
 int32_t chunk_of(const qmm_kv_dims& d) {
-    const int64_t cap = int64_t{d.max_pages} * d.page_tokens, blocks = d.head_dim == 128 ? 152 : 608;
+    const int64_t cap = int64_t{d.max_pages} * d.page_tokens, items = d.head_dim == 128 ? 2 * 152 : 6 * 608;
     const int32_t least = d.head_dim == 128 ? kTcTile : kTile;
     for (int32_t c = 1024; c > least; c >>= 1)
-        if (c <= 32 * d.page_tokens && (cap + c - 1) / c * d.agents * d.kv_heads >= 2 * blocks) return c;
+        if (c <= 32 * d.page_tokens && (cap + c - 1) / c * d.agents * d.kv_heads >= items) return c;
     return least;
 }
 
@@ -270,8 +286,7 @@ qmm_status qmm_kv_attend(const qmm_kv_dims* dims, const void* pool, const int32_
         return QMM_ERR_MISALIGNED;
     if (workspace_bytes < l.bytes) return QMM_ERR_SCRATCH_TOO_SMALL;
     AttendLaunch a = {};
-    int dev = 0;
-    st = check_gpu(&dev, &a.sms);
+    st = check_gpu(&a.device, &a.sms);
     if (st != QMM_OK) return st;
     if (dims->format != QMM_KV_Q8_0) {
         st = make_map(*dims, pool, &a.map);

@@ -766,7 +766,7 @@ struct AttendLaunch {
     CUtensorMap map;
     int32_t head_dim;
     int32_t max_q;  // most queries of one sequence per KV head
-    int32_t sms;
+    int32_t device, sms;
 };
 cudaError_t launch_attend_q8(const AttendLaunch& a, cudaStream_t s);
 cudaError_t launch_attend_f16(const AttendLaunch& a, cudaStream_t s);
@@ -774,13 +774,14 @@ cudaError_t launch_attend_bf16(const AttendLaunch& a, cudaStream_t s);
 
 template <int FMT, int D, int NT>
 cudaError_t launch_attend_one(const AttendLaunch& a, cudaStream_t s) {
+    static_assert(Geo<FMT, D, NT>::smem(kMaxAgents) <= kMaxShared);
     const int bytes = Geo<FMT, D, NT>::smem(a.p.agents);
-    cudaError_t e = cudaFuncSetAttribute(attend_partial<FMT, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    int per_sm = 0;
-    if (e == cudaSuccess)
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attend_partial<FMT, D, NT>, kThreads, bytes);
+    static Once once;
+    const cudaError_t e = once.allow_shared(attend_partial<FMT, D, NT>, a.device);
     if (e != cudaSuccess) return e;
-    if (per_sm < 1) return cudaErrorInvalidConfiguration;
+    // blocks per SM: what the registers were limited for, or what shared memory holds
+    int per_sm = (228 * 1024) / (bytes + 1024);
+    if (per_sm > Geo<FMT, D, NT>::blocks) per_sm = Geo<FMT, D, NT>::blocks;
     attend_partial<FMT, D, NT><<<a.sms * per_sm, kThreads, bytes, s>>>(a.map, a.p);
     return cudaGetLastError();
 }

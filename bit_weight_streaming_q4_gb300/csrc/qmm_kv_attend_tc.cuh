@@ -7,14 +7,15 @@
 //   O^T[dim][query]  += V^T P^T    M = 128 dims, K = the tokens
 // with the accumulators in tensor memory, so a thread of the softmax warps owns a token's row of
 // scores and needs no exchange to form its probabilities, and the outputs cost no registers.
-//   warp 0      asks for K and V tiles (bulk copies into two rings)
+//   warps 0, 3  ask for K tiles and V tiles (bulk copies into two rings; one warp for both would hold K
+//               back while V's slots are in use)
 //   warp 1      issues the products: S of tile t + 1 goes before O of tile t, so that it overlaps
 //               the softmax
-//   warps 2, 3  bring the next item: its numbers and its queries
-//   warps 4-11  softmax, two groups of four, half of the queries each: scores from tensor memory,
-//               probabilities into shared memory as the second product's B operand, in two
-//               16-bit parts (two products)
-//   warps 12-15 q8_0 only: K and V quants to fp16 in tensor memory, as A operands
+//   warp 2      brings the next item: its numbers and its queries
+//   warps 4 ..  softmax, two or three groups of four, a share of the queries each: scores from
+//               tensor memory, probabilities into shared memory as the second product's B operand,
+//               in two 16-bit parts
+//   last four   q8_0 only: K and V quants to fp16 in tensor memory, as A operands
 // 16-bit pools: the swizzled tiles are A operands as they come, K by rows and V transposed
 // (M-contiguous).  q8_0: K's quants are exact in fp16, one accumulator per 32-dim block takes its
 // scale in fp32; V's element, quant times normalised scale (see qmm_kv_attend.cuh), is split into
@@ -30,15 +31,19 @@
 namespace qmm {
 namespace kv {
 
-constexpr float kSlack = 2.f;     // p <= 2^(kShift + kSlack)
+constexpr float kTcShift = 9.f;   // p's power of two ..
+constexpr float kSlack = 6.f;     // .. and how far a score may pass its reference: p <= 2^15
+constexpr float kLowScale = 2048.f;  // p's low part is kept times this (its products have columns of their
+                                     // own), so that 22 bits of p count down to 2^-33 of the reference's
 
 template <int FMT, int N>
 struct TcGeo {
     static constexpr bool q8 = FMT == QMM_KV_Q8_0;
-    static constexpr int threads = q8 ? 512 : 384;
-    static constexpr int W = N / 2;                                // queries of a softmax group
+    static constexpr int groups = N == 48 ? 3 : 2;                 // softmax groups of four warps
+    static constexpr int W = N / groups;                           // queries of a group
+    static constexpr int threads = 128 * (1 + groups + (q8 ? 1 : 0));
     static constexpr int half = q8 ? 2 * kQ8Half : kTcTile * 256;  // bytes of a tile's K or V
-    static constexpr int k_slots = q8 ? 4 : 3, v_slots = q8 ? 4 : N == 16 ? 3 : 2;
+    static constexpr int k_slots = q8 ? 4 : 2, v_slots = q8 ? 4 : 3;  // (K's are free again once S is formed)
     static constexpr int opnd = N * 256;                           // bytes of a B operand: N rows of 128 16-bit values
     // tensor memory columns: scores (one set per 32-dim block of a q8_0 pool), outputs (2 N: those of P's
     // high and of its low parts), and the A operands
@@ -48,17 +53,17 @@ struct TcGeo {
     static constexpr int off_v = k_slots * half;
     static constexpr int off_q = (off_v + v_slots * half + 1023) / 1024 * 1024;  // two
     static constexpr int off_p = off_q + 2 * opnd;                              // per 64 tokens: N rows of high parts, N of low ones
-    static constexpr int off_dv = off_p + 2 * opnd;                             // q8_0: normalised V scales [4][128] fp16
-    static constexpr int off_len = off_dv + (q8 ? 4 * kTcTile * 2 : 0);         // [2][N] tokens that a query sees
+    static constexpr int off_dv = off_p + 2 * opnd;                             // q8_0: normalised V scales [2][4][128] fp16
+    static constexpr int off_len = off_dv + (q8 ? 2 * 4 * kTcTile * 2 : 0);         // [2][N] tokens that a query sees
     static constexpr int off_lim = off_len + 2 * N * 4;                         // [N] reference + slack
-    static constexpr int off_sub = off_lim + N * 4;                             // [N] reference - kShift
+    static constexpr int off_sub = off_lim + N * 4;                             // [N] reference - kTcShift
     static constexpr int off_alpha = off_sub + N * 4;                           // [N]
-    static constexpr int off_red = off_alpha + N * 4;                           // [8 warps][32]
-    static constexpr int off_odd = off_red + 8 * 32 * 4;                        // [4] tokens to be taken query by query
+    static constexpr int off_red = off_alpha + N * 4;                           // [softmax warps][32]
+    static constexpr int off_odd = off_red + 4 * groups * 32 * 4;               // [4] tokens to be taken query by query
     static constexpr int off_bar = off_odd + 16;
     static constexpr int bars = 2 * k_slots + 2 * v_slots + 4 + 4 + 4 + 2;
     static constexpr int off_item = (off_bar + bars * 8 + 15) / 16 * 16;        // [2] of ItemRec
-    static constexpr int off_misc = off_item + 2 * 32;                          // tmp[33], abort, accumulate, tmem, miss[v_slots]
+    static constexpr int off_misc = off_item + 2 * 32;                          // tmp[33], abort, accumulate, tmem, miss[v_slots], dead and missed by group
     static constexpr int off_seq = (off_misc + 48 * 4 + 15) / 16 * 16;
     static constexpr int smem(int agents) { return 1024 + off_seq + (agents + 1) * 16; }
 };
@@ -100,6 +105,20 @@ __device__ __forceinline__ bool elect_one() {
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(one));
     return one != 0;
+}
+
+// (hi, lo) 16-bit pairs of two fp32 values: value = hi + lo / kLowScale.
+template <bool BF>
+__device__ __forceinline__ void split2_scaled(float a, float b, uint32_t& hi, uint32_t& lo) {
+    if constexpr (BF) {
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(b), "f"(a));
+        const float ra = a - __uint_as_float(hi << 16), rb = b - __uint_as_float(hi & 0xFFFF0000u);
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(rb * kLowScale), "f"(ra * kLowScale));
+    } else {
+        const __half2 h = __floats2half2_rn(a, b);
+        hi = as_u32(h);
+        lo = as_u32(__floats2half2_rn((a - __low2float(h)) * kLowScale, (b - __high2float(h)) * kLowScale));
+    }
 }
 
 // v[c] of W <= 32 columns reduced over the warp's lanes by f: lane c returns column c's.  At each
@@ -164,30 +183,31 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
     if (tid == 0) {
         for (int i = 0; i < G::k_slots; ++i) {
             mbar_init(kfull + i, 1);
-            mbar_init(kempty + i, G::q8 ? 12 : 1);
+            mbar_init(kempty + i, G::q8 ? 4 + 4 * G::groups : 1);
         }
         for (int i = 0; i < G::v_slots; ++i) {
             mbar_init(vfull + i, 1);
-            mbar_init(vempty + i, G::q8 ? 12 : 1);
+            mbar_init(vempty + i, G::q8 ? 4 + 4 * G::groups : 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(qfull + i, 2);
-            mbar_init(qempty + i, G::q8 ? 13 : 9);
+            mbar_init(qfull + i, 1);
+            mbar_init(qempty + i, 1 + 4 * G::groups + (G::q8 ? 4 : 0));
         }
         mbar_init(sfull, 1);
-        mbar_init(sempty, 8);
-        mbar_init(pfull, 8);
+        mbar_init(sempty, 4 * G::groups);
+        mbar_init(pfull, 4 * G::groups);
         mbar_init(odone, 1);
         mbar_init(akfull, 4);
         mbar_init(akfree, 1);
         mbar_init(avfull, 4);
         mbar_init(avfree, 1);
         mbar_init(drained, 1);
-        mbar_init(oddread, 8);
+        mbar_init(oddread, 4 * G::groups);
         *abort_flag = 0;
         fence_mbar_init();
     }
     if (tid < 4) odd_sm[tid] = 0;
+    if (tid < 6) tmp[40 + tid] = -(tid & 1);
     if (warp == 1) {
         tmem_alloc(tmem_sm, G::cols);
         tmem_relinquish();
@@ -212,8 +232,13 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
         live = __all_sync(0xffffffffu, live);
     };
 
-    if (warp == 0) {
-        // ---------------------------------------------------------------- producer
+    if (warp == 0 || warp == 3) {
+        // ---------------------------------------------------------------- producers
+        const int h = warp == 3;  // 0: K, 1: V
+        const int slots = h ? G::v_slots : G::k_slots;
+        uint64_t* full = h ? vfull : kfull;
+        uint64_t* empty = h ? vempty : kempty;
+        uint8_t* ring = sm + (h ? G::off_v : 0);
         const uint64_t policy = l2_policy_evict_first();
         int nitem = blockIdx.x, t = 0;
         Item ni = {};
@@ -246,43 +271,36 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                     miss |= in && x < 0;
                     n_pieces += pg[k] >= 0;
                 }
+                const int s = t % slots, round = t / slots;
+                if (round > 0) await_warp(empty + s, (round - 1) & 1);
+                if (!live) break;
+                if (lane == 0) {
+                    fence_proxy_async_smem();  // the slot's generic accesses, before the copies
+                    if (h) vmiss[s] = miss;
+                    uint8_t* dst = ring + s * G::half;
+                    if (n_pieces == 0) mbar_arrive(full + s);
+                    else mbar_arrive_expect_tx(full + s, n_pieces * (G::q8 ? kQ8Half : br * D * 2));
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int slots = h ? G::v_slots : G::k_slots, s = t % slots, round = t / slots;
-                    uint64_t* full = (h ? vfull : kfull) + s;
-                    if (round > 0) await_warp((h ? vempty : kempty) + s, (round - 1) & 1);
-                    if (!live) break;
-                    if (lane == 0) {
-                        fence_proxy_async_smem();  // the slot's generic accesses, before the copies
-                        if (h) vmiss[s] = miss;
-                        uint8_t* dst = sm + (h ? G::off_v : 0) + s * G::half;
-                        if (n_pieces == 0) mbar_arrive(full);
-                        else mbar_arrive_expect_tx(full, n_pieces * (G::q8 ? kQ8Half : br * D * 2));
+                    for (int k = 0; k < kPieces; ++k) {
+                        if (pg[k] < 0) continue;
+                        if constexpr (G::q8) {
+                            bulk_g2s(dst + k * kQ8Half, p.pool + (static_cast<int64_t>(pg[k]) * p.kv_heads + it.g) * kQ8Rec + h * kQ8Half, kQ8Half,
+                                     full + s, policy);
+                        } else {
+                            const int y = ((pg[k] * p.kv_heads + it.g) * 2 + h) * p.page_tokens + ((tb + k * br) & (p.page_tokens - 1));
 #pragma unroll
-                        for (int k = 0; k < kPieces; ++k) {
-                            if (pg[k] < 0) continue;
-                            if constexpr (G::q8) {
-                                bulk_g2s(dst + k * kQ8Half, p.pool + (static_cast<int64_t>(pg[k]) * p.kv_heads + it.g) * kQ8Rec + h * kQ8Half,
-                                         kQ8Half, full, policy);
-                            } else {
-                                const int y = ((pg[k] * p.kv_heads + it.g) * 2 + h) * p.page_tokens + ((tb + k * br) & (p.page_tokens - 1));
-#pragma unroll
-                                for (int x = 0; x < D / 64; ++x)
-                                    tma_load_2d_hint(dst + x * kTcTile * 128 + k * br * 128, &map, 64 * x, y, full, policy);
-                            }
+                            for (int x = 0; x < D / 64; ++x)
+                                tma_load_2d_hint(dst + x * kTcTile * 128 + k * br * 128, &map, 64 * x, y, full + s, policy);
                         }
                     }
-                    __syncwarp();
                 }
+                __syncwarp();
             }
         }
         if (!live && lane == 0) {
             // let every copy still in flight land before the block exits: the last of each slot
             volatile int go_on = 0;
-            for (int h = 0; h < 2; ++h) {
-                const int slots = h ? G::v_slots : G::k_slots;
-                for (int i = max(0, t - slots); i <= t; ++i) mbar_wait_bounded((h ? vfull : kfull) + i % slots, (i / slots) & 1, &go_on, 100000000ull);
-            }
+            for (int i = max(0, t - slots); i < t; ++i) mbar_wait_bounded(full + i % slots, (i / slots) & 1, &go_on, 100000000ull);
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- products
@@ -353,23 +371,23 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
         volatile int go_on = 0;
         mbar_wait_bounded(drained, 0, &go_on, 10000000000ull);
         __syncwarp();
-    } else if (warp < 4) {
+    } else if (warp == 2) {
         // ---------------------------------------------------------------- the next item: numbers and queries, half a warp per row
         int k = 0;
         for (int item = blockIdx.x; item < total && live; item += gridDim.x, ++k) {
             const Item it = decode_item(p, seq, item, N);
             const int r0 = seq[it.a].w, nq = (seq[it.a + 1].w - r0) * p.group, q0 = it.tile * N;
             const int buf = k & 1, c = lane & 15;
-            int qi = 2 * (warp - 2) + (lane >> 4), r = r0 + (q0 + qi) / p.group, h = (q0 + qi) % p.group;
+            int qi = lane >> 4, r = r0 + (q0 + qi) / p.group, h = (q0 + qi) % p.group;
             if (k > 1) await_warp(qempty + buf, ((k >> 1) - 1) & 1);
             if (!live) break;
-            if (warp == 2 && lane == 0) {
+            if (lane == 0) {
                 ItemRec rec = {it.a, it.g, it.tok0, it.end, q0, nq, seq[it.a].z, r0};
                 item_sm[buf] = rec;
             }
             uint8_t* dst = sm + G::off_q + buf * G::opnd + (c >> 3) * (N * 128);
-#pragma unroll 4
-            for (int i = 0; i < N / 4; ++i) {  // 16-byte pieces, swizzled as the copies do
+#pragma unroll 8
+            for (int i = 0; i < N / 2; ++i) {  // 16-byte pieces, swizzled as the copies do
                 const bool in = q0 + qi < nq;
                 uint4 v = make_uint4(0, 0, 0, 0);
                 int len = 0;
@@ -379,14 +397,14 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                 }
                 *reinterpret_cast<uint4*>(dst + qi * 128 + (((c & 7) ^ (qi & 7)) << 4)) = v;
                 if (c == 0) qlen_sm[buf * N + qi] = len;
-                qi += 4;
-                for (h += 4; h >= p.group; h -= p.group) ++r;
+                qi += 2;
+                for (h += 2; h >= p.group; h -= p.group) ++r;
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(qfull + buf);
         }
-    } else if (warp < 12) {
+    } else if (warp < 4 + 4 * G::groups) {
         // ---------------------------------------------------------------- softmax: a token per thread, then a dim
         constexpr int W = G::W;
         const int grp = (warp - 4) >> 2, me = (tid - 128) & 127, w4 = warp & 3;
@@ -397,6 +415,8 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
         float* sub = sub_sm + c0;
         float* alpha = alpha_sm + c0;
         float* red = red_sm + grp * 128;       // [4][32]
+        volatile int* dead = tmp + 40 + 2 * grp;    // some thread's wait ran out
+        volatile int* missed = dead + 1;            // the last tile with a missing page
         int t = 0, k = 0;
         uint32_t odds = 0;                     // tiles with marked tokens so far
         // (what ends the loops is voted on, so that the warps always meet at the same barriers)
@@ -410,12 +430,12 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
             for (int q = 0; q < W; ++q) l[q] = 0.f;
             if (me < W) {
                 lim[me] = kNoMax;
-                sub[me] = -kShift;
+                sub[me] = -kTcShift;
             }
             named_bar_sync(bar_id, 128);
             const int64_t plane = static_cast<int64_t>(p.chunks) * p.chunk * 4;
             float* sbase = p.scores ? p.scores + (static_cast<int64_t>(it.a * p.kv_heads + it.g) * (p.qp >> 2) + (q0 >> 2)) * plane : nullptr;
-            const int planes = (p.qp - q0) >> 2;
+            const int planes = (it.nq - q0 + 3) >> 2;
 
             bool stop = false;
             for (int tb = it.tok0; tb < it.end; tb += kTcTile, ++t) {
@@ -490,12 +510,14 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                     over |= x[q] > m.x || x[q + 1] > m.y || x[q + 2] > m.z || x[q + 3] > m.w;
                 }
                 bool moved = false;  // some reference moves
+                if (!live) *dead = 1;
+                if (miss) *missed = t;
                 if (bar_or(bar_id, 128, over)) {
-                    if (bar_or(bar_id, 128, !live)) {
+                    if (*dead) {
                         stop = true;
                         break;
                     }
-                    miss = bar_or(bar_id, 128, miss);
+                    miss = *missed == t;
                     // (a NaN is no maximum: fmaxf passes it over)
                     red[w4 * 32 + lane] = reduce_columns<W>(x, kNoMax, [](float a, float b) { return fmaxf(a, b); });
                     named_bar_sync(bar_id, 128);
@@ -506,7 +528,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                         alpha[me] = passed ? ex2(lim[me] - kSlack - m) : 1.f;  // (2^-inf = 0 the first time)
                         if (passed) {
                             lim[me] = m + kSlack;
-                            sub[me] = m - kShift;
+                            sub[me] = m - kTcShift;
                         }
                     }
                     named_bar_sync(bar_id, 128);
@@ -541,14 +563,19 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                 const float inv = G::q8 ? __int_as_float((127 - static_cast<int>(e)) << 23) : 1.f;  // 2^-e
                 uint8_t* pbase = sm + G::off_p + (me >> 6) * (2 * N * 128) + c0 * 128 + (me & 7) * 2;
                 const int chunk = (me & 63) >> 3;
+                // (all of them before the first store, which the compiler may not load past)
+#pragma unroll
+                for (int q = 0; q < W; q += 4) {
+                    const float4 m = *reinterpret_cast<const float4*>(sub + q);
+                    x[q] = ex2(x[q] - m.x), x[q + 1] = ex2(x[q + 1] - m.y);
+                    x[q + 2] = ex2(x[q + 2] - m.z), x[q + 3] = ex2(x[q + 3] - m.w);
+                }
 #pragma unroll
                 for (int q = 0; q < W; q += 2) {
-                    const float2 m = *reinterpret_cast<const float2*>(sub + q);
-                    const float pa = ex2(x[q] - m.x), pb = ex2(x[q + 1] - m.y);
-                    l[q] = G::q8 ? fmaf(pa, inv, l[q]) : l[q] + pa;
-                    l[q + 1] = G::q8 ? fmaf(pb, inv, l[q + 1]) : l[q + 1] + pb;
+                    l[q] = G::q8 ? fmaf(x[q], inv, l[q]) : l[q] + x[q];
+                    l[q + 1] = G::q8 ? fmaf(x[q + 1], inv, l[q + 1]) : l[q + 1] + x[q + 1];
                     uint32_t hi, lo;
-                    split2<BF>(pa, pb, hi, lo);
+                    split2_scaled<BF>(x[q], x[q + 1], hi, lo);
                     uint8_t* at = pbase + q * 128 + ((chunk ^ (q & 7)) << 4);  // (c0 is a multiple of 8)
                     uint8_t* bt = pbase + (q + 1) * 128 + ((chunk ^ ((q + 1) & 7)) << 4);
                     *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(hi);
@@ -562,7 +589,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                     // missing page) V holds anything and becomes zero (q8_0: its scales do, in the
                     // converting warps).  One that some queries see and whose V (q8_0: a scale) is
                     // not finite is added query by query, to those that see it, and is zero in the
-                    // product.  (Both groups come to the same answers.)
+                    // product.  (All groups come to the same answers.)
                     bool odd = false;
                     const bool gone = miss || tok >= it.end;
                     auto piece = [&](int c) { return reinterpret_cast<uint4*>(vt + (c >> 3) * (kTcTile * 128) + me * 128 + (((c & 7) ^ (me & 7)) << 4)); };
@@ -583,7 +610,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                     const bool any = bar_or(bar_id, 128, odd);  // (also: P is written)
                     if (any) {
                         const uint32_t who = __ballot_sync(0xffffffffu, odd);
-                        if (lane == 0) odd_sm[w4] = who;  // (both groups write the same)
+                        if (lane == 0) odd_sm[w4] = who;  // (all groups write the same)
                         named_bar_sync(bar_id, 128);
                         const uint16_t* P = reinterpret_cast<const uint16_t*>(sm + G::off_p);
 #pragma unroll 1
@@ -619,9 +646,9 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                                 for (int i = 0; i < 8; ++i) {
                                     const int q = c + i, at = (j >> 6) * (2 * N * 64) + (c0 + q) * 64 + ((((j & 63) >> 3) ^ (q & 7)) << 3) + (j & 7);
                                     const uint32_t h = P[at], u = P[at + N * 64];
-                                    const float pr = BF ? __uint_as_float(h << 16) + __uint_as_float(u << 16)
-                                                        : __half2float(__ushort_as_half(static_cast<uint16_t>(h))) +
-                                                              __half2float(__ushort_as_half(static_cast<uint16_t>(u)));
+                                    const float ph = BF ? __uint_as_float(h << 16) : __half2float(__ushort_as_half(static_cast<uint16_t>(h)));
+                                    const float pl = BF ? __uint_as_float(u << 16) : __half2float(__ushort_as_half(static_cast<uint16_t>(u)));
+                                    const float pr = fmaf(pl, 1.f / kLowScale, ph);
                                     if (tb + j < qlen[q]) v[i] = fmaf(pr, y, v[i]);
                                 }
                             }
@@ -635,7 +662,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                         holds = true;
                         __syncwarp();
                         if (lane == 0) mbar_arrive(oddread);
-                        await(oddread, odds++ & 1);  // V's rows are read by both groups
+                        await(oddread, odds++ & 1);  // V's rows are read by every group
                     }
                     if constexpr (!G::q8) {
                         if (grp == 0 && (gone || odd))
@@ -666,7 +693,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                 tc_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (q0 + c + i < it.nq) po[(c + i) * D] = v[0][i] + v[1][i];
+                    if (q0 + c + i < it.nq) po[(c + i) * D] = fmaf(v[1][i], 1.f / kLowScale, v[0][i]);
             }
             tc_fence_before();
             red[w4 * 32 + lane] = reduce_columns<W>(l, 0.f, [](float a, float b) { return a + b; });
@@ -683,79 +710,88 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
         if (!live && me == 0) atomicOr(p.err, kErrTimeout);
     } else if (G::q8) {
         // ---------------------------------------------------------------- q8_0 to fp16: a token per thread, then a dim
-        constexpr uint32_t kBar = 3;
-        const int me = tid - 384, w4 = warp - 12;
+        constexpr uint32_t kBar = 4;
+        const int me = tid & 127, w4 = warp & 3;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * w4) << 16);
-        __half* dv = reinterpret_cast<__half*>(sm + G::off_dv);  // [4][128]
+        __half* dv = reinterpret_cast<__half*>(sm + G::off_dv);  // [2][4][128]
+        const int slot = me & 63, key = q8_key(slot & 7);
+        // K of tile i: a token per thread
+        auto convert_k = [&](int i) {
+            const int ks = i % G::k_slots;
+            await(kfull + ks, (i / G::k_slots) & 1);
+            if (i > 0) await(akfree, (i - 1) & 1);
+            tc_fence_after();
+            const uint8_t* kt = sm + ks * G::half + (me >> 6) * kQ8Half + slot * 128;
+            uint4 row[8];  // (loaded before the first store to tensor memory, which the compiler may not load past)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) row[c] = *reinterpret_cast<const uint4*>(kt + 16 * (c ^ key));
+#pragma unroll
+            for (int c = 0; c < 8; c += 2) {
+                uint32_t out[16];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint4 w = row[c + j];
+                    const uint32_t u[4] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u, w.z ^ 0x80808080u, w.w ^ 0x80808080u};
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        out[8 * j + 2 * n] = i8_to_h2(u[n], 0x4140u);
+                        out[8 * j + 2 * n + 1] = i8_to_h2(u[n], 0x4342u);
+                    }
+                }
+                tmem_st16(lanes + G::col_k + 8 * c, out);
+            }
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(akfull);
+                mbar_arrive(kempty + ks);
+            }
+        };
         int t = 0, k = 0;
         bool go = true;
         for (int item = blockIdx.x; item < total && go; item += gridDim.x, ++k) {
             await(qfull + (k & 1), (k >> 1) & 1);
             const ItemRec it = item_sm[k & 1];
+            if (k == 0) convert_k(0);
             for (int tb = it.tok0; tb < it.end; tb += kTcTile, ++t) {
-                const int ks = t % G::k_slots, vs = t % G::v_slots;
-                await(kfull + ks, (t / G::k_slots) & 1);
-                if (t > 0) await(akfree, (t - 1) & 1);
-                tc_fence_after();
-                const int slot = me & 63;
-                const uint8_t* kt = sm + ks * G::half + (me >> 6) * kQ8Half + slot * 128;
-                const int key = q8_key(slot & 7);
-#pragma unroll
-                for (int c = 0; c < 8; c += 2) {
-                    uint32_t out[16];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint4 w = *reinterpret_cast<const uint4*>(kt + 16 * ((c + j) ^ key));
-                        const uint32_t u[4] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u, w.z ^ 0x80808080u, w.w ^ 0x80808080u};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            out[8 * j + 2 * i] = i8_to_h2(u[i], 0x4140u);
-                            out[8 * j + 2 * i + 1] = i8_to_h2(u[i], 0x4342u);
-                        }
-                    }
-                    tmem_st16(lanes + G::col_k + 8 * c, out);
-                }
-                tc_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(akfull);
-                    mbar_arrive(kempty + ks);
-                }
-                // ---- V: normalised scales by token, then elements by dim
+                // the next tile's K goes first: it is free to, while V waits for the last products
+                if (tb + kTcTile < it.end || item + gridDim.x < total) convert_k(t + 1);
+                const int vs = t % G::v_slots;
                 await(vfull + vs, (t / G::v_slots) & 1);
                 const uint8_t* vt = sm + G::off_v + vs * G::half;
-                {
-                    const int tok = tb + me;
-                    const uint8_t* sc = vt + (me >> 6) * kQ8Half + 8192 + slot * 2;
-                    uint32_t d[4], top = 0;
+                // ---- V: normalised scales by token, then elements by dim
+                const int tok = tb + me;
+                const uint8_t* sc = vt + (me >> 6) * kQ8Half + 8192 + slot * 2;
+                uint32_t d[4], top = 0;
+                bool odd = false;
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        d[b] = *reinterpret_cast<const uint16_t*>(sc + b * 128);
-                        const uint32_t w = d[b] & 0x7FFFu;
-                        top = w > 0x7C00u ? top : max(top, w);
-                    }
-                    const __half inv = __ushort_as_half(static_cast<uint16_t>((30 - min(max(static_cast<int>(top >> 10), 1), 29)) << 10));
-                    bool odd = false;
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) odd |= (d[b] & 0x7C00u) == 0x7C00u;
-                    const bool none = vmiss[vs] != 0 || tok >= it.end || (odd && tok >= it.minlen);
-                    named_bar_sync(kBar, 128);  // the last tile's scales are read
-#pragma unroll
-                    for (int b = 0; b < 4; ++b)
-                        dv[b * kTcTile + me] = none ? __ushort_as_half(0) : __hmul(__ushort_as_half(static_cast<uint16_t>(d[b])), inv);
+                for (int b = 0; b < 4; ++b) {
+                    d[b] = *reinterpret_cast<const uint16_t*>(sc + b * 128);
+                    const uint32_t w = d[b] & 0x7FFFu;
+                    top = w > 0x7C00u ? top : max(top, w);
+                    odd |= (d[b] & 0x7C00u) == 0x7C00u;
                 }
+                const __half inv = __ushort_as_half(static_cast<uint16_t>((30 - min(max(static_cast<int>(top >> 10), 1), 29)) << 10));
+                const bool none = vmiss[vs] != 0 || tok >= it.end || (odd && tok >= it.minlen);
+                __half* dt = dv + (t & 1) * 4 * kTcTile;
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    dt[b * kTcTile + me] = none ? __ushort_as_half(0) : __hmul(__ushort_as_half(static_cast<uint16_t>(d[b])), inv);
+                uint4 row[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) row[c] = *reinterpret_cast<const uint4*>(vt + (c >> 2) * kQ8Half + me * 64 + 16 * (c & 3));
                 if (t > 0) await(avfree, (t - 1) & 1);
-                if (bar_or(kBar, 128, !live)) {
+                if (bar_or(kBar, 128, !live)) {  // (also: the scales are written)
                     go = false;
                     break;
                 }
                 tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {  // 16 tokens
-                    const uint4 w = *reinterpret_cast<const uint4*>(vt + (c >> 2) * kQ8Half + me * 64 + 16 * (c & 3));
-                    const uint4 s0 = *reinterpret_cast<const uint4*>(dv + w4 * kTcTile + 16 * c);
-                    const uint4 s1 = *reinterpret_cast<const uint4*>(dv + w4 * kTcTile + 16 * c + 8);
+                    const uint4 w = row[c];
+                    const uint4 s0 = *reinterpret_cast<const uint4*>(dt + w4 * kTcTile + 16 * c);
+                    const uint4 s1 = *reinterpret_cast<const uint4*>(dt + w4 * kTcTile + 16 * c + 8);
                     const uint32_t u[4] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u, w.z ^ 0x80808080u, w.w ^ 0x80808080u};
                     const uint32_t s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
                     uint32_t hi[8], lo[8];
@@ -789,8 +825,10 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
 
 template <int FMT, int N>
 cudaError_t launch_attend_tc_one(const AttendLaunch& a, cudaStream_t s) {
+    static_assert(TcGeo<FMT, N>::smem(kMaxAgents) <= kMaxShared);
     const int bytes = TcGeo<FMT, N>::smem(a.p.agents);
-    cudaError_t e = cudaFuncSetAttribute(attend_partial_tc<FMT, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    static Once once;
+    const cudaError_t e = once.allow_shared(attend_partial_tc<FMT, N>, a.device);
     if (e != cudaSuccess) return e;
     attend_partial_tc<FMT, N><<<a.sms, TcGeo<FMT, N>::threads, bytes, s>>>(a.map, a.p);
     return cudaGetLastError();

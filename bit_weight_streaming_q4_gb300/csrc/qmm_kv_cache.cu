@@ -241,6 +241,7 @@ constexpr int kDigit = multi ? 11 : 13;
 constexpr int kBins = 1 << 13;
 constexpr int kKeyCap = 24576;  // keys a block holds in shared memory
 constexpr int kFew = 256;       // keys that are ranked by counting
+constexpr int kSelectStatic = 4096;  // more than the selecting kernel's static shared memory
 
 struct EvictParams {
     uint8_t* pool;
@@ -754,7 +755,9 @@ qmm_status qmm_kv_evict(const qmm_kv_dims* dims, void* pool, const int32_t* page
     if (groups * ranks > INT32_MAX || groups * slices > INT32_MAX || dims->pool_pages * dims->page_tokens > INT32_MAX)
         return QMM_ERR_UNSUPPORTED_SHAPE;
     const auto select = ranks > 1 ? kv_evict_select<true> : kv_evict_select<false>;
-    cudaError_t e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, (kBins + kKeyCap) * 4);
+    static_assert((kBins + kKeyCap) * 4 <= kMaxShared - kSelectStatic);
+    static Once once[2];
+    cudaError_t e = once[ranks > 1].allow_shared(select, dev, kSelectStatic);
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(groups * ranks));

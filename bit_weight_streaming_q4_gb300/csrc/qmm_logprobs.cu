@@ -451,9 +451,9 @@ constexpr int shared_bytes() { return kSeg * static_cast<int>(sizeof(T)) + stati
 static_assert(kPerSm * (shared_bytes<float>() + 1024) <= 228 * 1024, "the blocks' shared memory");
 
 template <typename T>
-cudaError_t launch(const Params& p, int64_t m, int ranks, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(logprobs_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, shared_bytes<T>());
-    if (e == cudaSuccess && ranks > 8) e = cudaFuncSetAttribute(logprobs_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+cudaError_t launch(const Params& p, int64_t m, int ranks, int dev, cudaStream_t s) {
+    static kv::Once once;
+    const cudaError_t e = once.allow_shared(logprobs_kernel<T>, dev, 0, true);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(m * ranks));
@@ -517,8 +517,8 @@ extern "C" qmm_status qmm_logprobs(const void* logits, int32_t type, int64_t m, 
     p.top = top;
     p.vec = aligned(logits, 16) && stride * size % 16 == 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = type == QMM_TYPE_F32   ? launch<float>(p, m, ranks, s)
-                          : type == QMM_TYPE_F16 ? launch<__half>(p, m, ranks, s)
-                                                 : launch<__nv_bfloat16>(p, m, ranks, s);
+    const cudaError_t e = type == QMM_TYPE_F32   ? launch<float>(p, m, ranks, dev, s)
+                          : type == QMM_TYPE_F16 ? launch<__half>(p, m, ranks, dev, s)
+                                                 : launch<__nv_bfloat16>(p, m, ranks, dev, s);
     return e == cudaSuccess ? QMM_OK : QMM_ERR_CUDA;
 }

@@ -5,7 +5,10 @@ table, the workspace and the error word -- and appends to the cache, attends ove
 from it; ``logprobs`` reads the lm_head's output.  As in ``qmm``, every step runs in the library's
 CUDA kernels, there is no fallback, and PyTorch supplies only device memory and streams.  Calls go
 to the current stream unless ``stream`` is given; a tensor last written on another stream has to be
-ordered before them by the caller."""
+ordered before them by the caller.
+
+A small call takes about as long here as on the GPU, so the checks below are plain comparisons and
+form their messages only to raise them."""
 from __future__ import annotations
 
 import ctypes
@@ -56,26 +59,34 @@ def load():
     return _lib
 
 
-_types = None
+_torch = _f32 = _i32 = _types = _raw = None
 
 
-def _type_of(t) -> int:
-    global _types
-    if _types is None:
-        import torch
-        _types = {torch.float32: TYPE_F32, torch.float16: TYPE_F16, torch.bfloat16: TYPE_BF16}
-    if t.dtype not in _types:
-        raise TypeError(f"fp32, fp16 or bf16 expected, got {t.dtype}")
-    return _types[t.dtype]
+def _setup():
+    """torch and its types, looked up at the first use (the module imports without torch)."""
+    global _torch, _f32, _i32, _types, _raw
+    import torch
+    # (the handle alone, without the Stream object around it: 0.1 us instead of 3)
+    _raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+    _f32, _i32 = torch.float32, torch.int32
+    _types = {torch.float32: TYPE_F32, torch.float16: TYPE_F16, torch.bfloat16: TYPE_BF16}
+    _torch = torch
 
 
-def _opt(t) -> int:
-    return 0 if t is None else t.data_ptr()
+def _stream(t) -> int:
+    """The current stream of tensor t's device."""
+    return _raw(t.get_device())
 
 
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
+def _refuse(name, what):
+    raise ValueError(f"{name}: {what}")
+
+
+def _vector(name, t, dtype, n):
+    """Address of a contiguous CUDA tensor of n elements."""
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
+        _refuse(name, f"a contiguous {dtype} CUDA tensor of {n} elements")
+    return t.data_ptr()
 
 
 class KvPlan:
@@ -91,22 +102,29 @@ class KvPlan:
 
     def __init__(self, page_table, *, format: str, heads: int, kv_heads: int, head_dim: int, page_tokens: int,
                  pool_pages: int, max_rows: int, max_agent_rows: int | None = None):
-        import torch
-        _need(page_table.dtype == torch.int32 and page_table.dim() == 2 and page_table.is_contiguous() and page_table.is_cuda,
-              "page_table: a contiguous int32 CUDA tensor [agents, max_pages]")
-        _need(format in FORMATS, f"format: one of {', '.join(FORMATS)}")
+        if _torch is None:
+            _setup()
+        if page_table.dtype is not _i32 or page_table.dim() != 2 or not page_table.is_contiguous() or not page_table.is_cuda:
+            _refuse("page_table", "a contiguous int32 CUDA tensor [agents, max_pages]")
+        if format not in FORMATS:
+            _refuse("format", f"one of {', '.join(FORMATS)}")
         agents, max_pages = page_table.shape
         self.page_table, self.format, self.max_rows = page_table, format, int(max_rows)
         self.dims = KvDims(FORMATS[format], heads, kv_heads, head_dim, page_tokens, agents, max_pages,
                            int(max_agent_rows or max_rows), pool_pages)
-        self._ref = ctypes.byref(self.dims)
+        self.agents, self.heads, self.kv_heads, self.head_dim = agents, heads, kv_heads, head_dim
         self.cap = max_pages * page_tokens
-        self._pool_dtype = {"q8_0": torch.uint8, "f16": torch.float16, "bf16": torch.bfloat16}[format]
-        self._q_dtype = torch.bfloat16 if format == "bf16" else torch.float16
+        self._slots = agents * kv_heads * self.cap
+        self._ref = ctypes.byref(self.dims)
+        self._pool_dtype = {"q8_0": _torch.uint8, "f16": _torch.float16, "bf16": _torch.bfloat16}[format]
+        self._q_dtype = _torch.bfloat16 if format == "bf16" else _torch.float16
         self._pool_size = pool_pages * kv_heads * (17408 if format == "q8_0" else 2 * page_tokens * head_dim)
-        self._i32, self._f32 = torch.int32, torch.float32
-        self.error_word = torch.zeros(1, dtype=torch.int32, device=page_table.device)
+        self._scale = head_dim ** -0.5
+        self.error_word = _torch.zeros(1, dtype=_i32, device=page_table.device)
+        self._err, self._table = self.error_word.data_ptr(), page_table.data_ptr()
         self._workspace = {}
+        lib = load()
+        self._append, self._attend, self._evict = lib.qmm_kv_append, lib.qmm_kv_attend, lib.qmm_kv_evict
         self._bytes("qmm_kv_evict_workspace_bytes")  # refuses dims that no call takes
 
     def _bytes(self, name, *args) -> int:
@@ -115,27 +133,30 @@ class KvPlan:
         return n.value
 
     def _space(self, kind: str):
-        """The workspace of a kind of call, allocated at its first use and kept."""
-        t = self._workspace.get(kind)
-        if t is None:
-            import torch
+        """Address and bytes of a kind of call's workspace, allocated at its first use and kept."""
+        w = self._workspace.get(kind)
+        if w is None:
             n = self._bytes("qmm_kv_evict_workspace_bytes") if kind == "evict" else \
                 self._bytes("qmm_kv_attend_workspace_bytes", int(kind == "weights"))
-            t = self._workspace[kind] = torch.empty(n, dtype=torch.uint8, device=self.page_table.device)
-        return t
+            t = _torch.empty(n, dtype=_torch.uint8, device=self.page_table.device)
+            w = self._workspace[kind] = (t.data_ptr(), n, t)
+        return w
 
-    def _check_pool(self, pool):
-        _need(pool.dtype == self._pool_dtype and pool.numel() == self._pool_size and pool.is_contiguous() and pool.is_cuda,
-              f"pool: a contiguous {self._pool_dtype} CUDA tensor of {self._pool_size} elements")
+    def _pool(self, pool) -> int:
+        if pool.dtype is not self._pool_dtype or pool.numel() != self._pool_size or not pool.is_contiguous() or not pool.is_cuda:
+            _refuse("pool", f"a contiguous {self._pool_dtype} CUDA tensor of {self._pool_size} elements")
+        return pool.data_ptr()
 
-    def _check_slots(self, name, t, dtype):
-        _need(t is None or (t.dtype == dtype and t.is_contiguous() and t.is_cuda and
-                            t.numel() == self.dims.agents * self.dims.kv_heads * self.cap),
-              f"{name}: a contiguous {dtype} CUDA tensor [agents, kv_heads, {self.cap}]")
-
-    def _check_ints(self, name, t, n):
-        _need(t.dtype == self._i32 and t.numel() == n and t.is_contiguous() and t.is_cuda,
-              f"{name}: a contiguous int32 CUDA tensor of {n} elements")
+    def _rows_of(self, name, t, dtype, heads):
+        """Address and row stride of [rows, heads, head_dim] with any row stride."""
+        s = t.shape
+        if len(s) != 3 or s[1] != heads or s[2] != self.head_dim or t.dtype is not dtype or not t.is_cuda:
+            _refuse(name, f"a {dtype} CUDA tensor [rows, {heads}, {self.head_dim}]")
+        st = t.stride()
+        if s[0] > 0 and (st[2] != 1 or (heads > 1 and st[1] != self.head_dim)):
+            _refuse(name, "contiguous but for the row stride")
+        # (a single row's stride says nothing)
+        return t.data_ptr(), st[0] if s[0] > 1 else heads * self.head_dim
 
     def append(self, pool, agent_rows, cache_len, k, v, *, weight=None, pos=None, row_pos=None, stream: int | None = None) -> None:
         """Write K and V of new rows behind the sequences' cached tokens (qmm_kv_append).
@@ -144,26 +165,22 @@ class KvPlan:
         projection's output are taken in place).  cache_len: int32 [agents], tokens cached
         before the call (not changed).  weight / pos: the slots' arrays, whose new entries become
         0 and row_pos."""
-        d = self.dims
+        kind = _types.get(k.dtype)
+        if kind is None:
+            _refuse("k", "fp32, fp16 or bf16")
+        kp, ks = self._rows_of("k", k, k.dtype, self.kv_heads)
+        vp, vs = self._rows_of("v", v, k.dtype, self.kv_heads)
         rows = k.shape[0]
-        self._check_pool(pool)
-        for name, t in (("k", k), ("v", v)):
-            _need(t.shape == (rows, d.kv_heads, d.head_dim) and t.is_cuda and t.dtype == k.dtype and
-                  (rows == 0 or t.stride()[1:] == (d.head_dim, 1)),
-                  f"{name}: a CUDA tensor [rows, {d.kv_heads}, {d.head_dim}], contiguous but for the row stride")
-        self._check_ints("agent_rows", agent_rows, d.agents + 1)
-        self._check_ints("cache_len", cache_len, d.agents)
-        self._check_slots("weight", weight, self._f32)
-        self._check_slots("pos", pos, self._i32)
-        if row_pos is not None:
-            self._check_ints("row_pos", row_pos, rows)
-        width = d.kv_heads * d.head_dim
-        # (a single row's stride says nothing)
-        ks, vs = (k.stride(0), v.stride(0)) if rows > 1 else (width, width)
-        st = _q.current_stream() if stream is None else stream
-        _q._check(load().qmm_kv_append(self._ref, pool.data_ptr(), self.page_table.data_ptr(), agent_rows.data_ptr(),
-                                       cache_len.data_ptr(), k.data_ptr(), ks, v.data_ptr(), vs, _type_of(k), rows, _opt(weight),
-                                       _opt(pos), _opt(row_pos), self.error_word.data_ptr(), st), "qmm_kv_append")
+        if v.shape[0] != rows:
+            _refuse("v", f"{rows} rows, as k")
+        st = self._append(
+            self._ref, self._pool(pool), self._table, _vector("agent_rows", agent_rows, _i32, self.agents + 1),
+            _vector("cache_len", cache_len, _i32, self.agents), kp, ks, vp, vs, kind, rows,
+            0 if weight is None else _vector("weight", weight, _f32, self._slots),
+            0 if pos is None else _vector("pos", pos, _i32, self._slots),
+            0 if row_pos is None else _vector("row_pos", row_pos, _i32, rows), self._err, _stream(pool) if stream is None else stream)
+        if st:
+            raise _q.QmmError(st, "qmm_kv_append")
 
     def attend(self, pool, agent_rows, row_len, q, out, *, lse=None, weight_in=None, weight_out=None,
                scale: float | None = None, stream: int | None = None) -> None:
@@ -174,27 +191,23 @@ class KvPlan:
         that the row sees; lse: fp32 [rows, heads]; weight_in / weight_out: the slots' accumulated
         weights before and after (weight_in may be weight_out, or None for zeros); scale: None
         for 1 / sqrt(head_dim)."""
-        d = self.dims
+        qp, qs = self._rows_of("q", q, self._q_dtype, self.heads)
         rows = q.shape[0]
-        self._check_pool(pool)
-        shape = (rows, d.heads, d.head_dim)
-        _need(q.shape == shape and q.dtype == self._q_dtype and q.is_cuda and (rows == 0 or q.stride()[1:] == (d.head_dim, 1)),
-              f"q: a {self._q_dtype} CUDA tensor [rows, {d.heads}, {d.head_dim}], contiguous but for the row stride")
-        _need(out.shape == shape and out.is_contiguous() and out.is_cuda, f"out: a contiguous CUDA tensor [rows, {d.heads}, {d.head_dim}]")
-        _need(rows <= self.max_rows, f"q: at most {self.max_rows} rows (the plan's max_rows)")
-        self._check_ints("agent_rows", agent_rows, d.agents + 1)
-        self._check_ints("row_len", row_len, rows)
-        _need(lse is None or (lse.dtype == self._f32 and lse.numel() == rows * d.heads and lse.is_contiguous() and lse.is_cuda),
-              f"lse: a contiguous fp32 CUDA tensor [rows, {d.heads}]")
-        self._check_slots("weight_in", weight_in, self._f32)
-        self._check_slots("weight_out", weight_out, self._f32)
-        ws = self._space("weights" if weight_out is not None else "attend")
-        st = _q.current_stream() if stream is None else stream
-        _q._check(load().qmm_kv_attend(self._ref, pool.data_ptr(), self.page_table.data_ptr(), agent_rows.data_ptr(),
-                                       row_len.data_ptr(), q.data_ptr(), q.stride(0) if rows > 1 else d.heads * d.head_dim, rows,
-                                       d.head_dim ** -0.5 if scale is None else scale, out.data_ptr(), _type_of(out), _opt(lse),
-                                       _opt(weight_in), _opt(weight_out), ws.data_ptr(), ws.numel(), self.error_word.data_ptr(), st),
-                  "qmm_kv_attend")
+        if rows > self.max_rows:
+            _refuse("q", f"at most {self.max_rows} rows (the plan's max_rows)")
+        kind = _types.get(out.dtype)
+        if kind is None or out.shape != q.shape or not out.is_contiguous() or not out.is_cuda:
+            _refuse("out", f"a contiguous fp32, fp16 or bf16 CUDA tensor [{rows}, {self.heads}, {self.head_dim}]")
+        ws, ws_bytes, _ = self._space("attend" if weight_out is None else "weights")
+        st = self._attend(
+            self._ref, self._pool(pool), self._table, _vector("agent_rows", agent_rows, _i32, self.agents + 1),
+            _vector("row_len", row_len, _i32, rows), qp, qs, rows, self._scale if scale is None else scale, out.data_ptr(), kind,
+            0 if lse is None else _vector("lse", lse, _f32, rows * self.heads),
+            0 if weight_in is None else _vector("weight_in", weight_in, _f32, self._slots),
+            0 if weight_out is None else _vector("weight_out", weight_out, _f32, self._slots), ws, ws_bytes, self._err,
+            _stream(pool) if stream is None else stream)
+        if st:
+            raise _q.QmmError(st, "qmm_kv_attend")
 
     def evict(self, pool, cache_len, keep, weight, pos, *, weight_out, pos_out, len_out, sink: int = 0, protect_from=None,
               stream: int | None = None) -> None:
@@ -203,23 +216,16 @@ class KvPlan:
         cache_len, keep, len_out: int32 [agents] (keep < 0: no limit); protect_from: int32
         [agents] or None; weight_out and pos_out may be weight and pos.  Slots from len_out on
         are free afterwards."""
-        d = self.dims
-        self._check_pool(pool)
-        self._check_ints("cache_len", cache_len, d.agents)
-        self._check_ints("keep", keep, d.agents)
-        self._check_ints("len_out", len_out, d.agents)
-        if protect_from is not None:
-            self._check_ints("protect_from", protect_from, d.agents)
-        for name, t, dt in (("weight", weight, self._f32), ("weight_out", weight_out, self._f32), ("pos", pos, self._i32),
-                            ("pos_out", pos_out, self._i32)):
-            _need(t is not None, f"{name}: needed")
-            self._check_slots(name, t, dt)
-        ws = self._space("evict")
-        st = _q.current_stream() if stream is None else stream
-        _q._check(load().qmm_kv_evict(self._ref, pool.data_ptr(), self.page_table.data_ptr(), cache_len.data_ptr(), keep.data_ptr(),
-                                      sink, _opt(protect_from), weight.data_ptr(), pos.data_ptr(), weight_out.data_ptr(),
-                                      pos_out.data_ptr(), len_out.data_ptr(), ws.data_ptr(), ws.numel(), self.error_word.data_ptr(),
-                                      st), "qmm_kv_evict")
+        ws, ws_bytes, _ = self._space("evict")
+        st = self._evict(
+            self._ref, self._pool(pool), self._table, _vector("cache_len", cache_len, _i32, self.agents),
+            _vector("keep", keep, _i32, self.agents), sink,
+            0 if protect_from is None else _vector("protect_from", protect_from, _i32, self.agents),
+            _vector("weight", weight, _f32, self._slots), _vector("pos", pos, _i32, self._slots),
+            _vector("weight_out", weight_out, _f32, self._slots), _vector("pos_out", pos_out, _i32, self._slots),
+            _vector("len_out", len_out, _i32, self.agents), ws, ws_bytes, self._err, _stream(pool) if stream is None else stream)
+        if st:
+            raise _q.QmmError(st, "qmm_kv_evict")
 
     def error(self) -> int:
         """The error word (synchronises): 0, or 1 (a wait ran out) | 2 (page table) | 4 (rows or lengths)."""
@@ -233,27 +239,27 @@ def logprobs(logits, tokens=None, lse=None, logprob=None, entropy=None, top_inde
     logits: fp32, fp16 or bf16 [m, n], any row stride.  tokens: int32 [m, given] with logprob
     fp32 [m, given]; lse, entropy: fp32 [m]; top_index: int32 [m, top] with top_logprob fp32
     [m, top], top <= 32.  Outputs left out are not computed."""
-    import torch
-    _need(logits.dim() == 2 and logits.is_cuda and (logits.shape[0] == 0 or logits.stride(1) == 1 or logits.shape[1] == 1),
-          "logits: a CUDA tensor [m, n], contiguous but for the row stride")
+    if _torch is None:
+        _setup()
+    kind = _types.get(logits.dtype)
+    if kind is None or logits.dim() != 2 or not logits.is_cuda:
+        _refuse("logits", "an fp32, fp16 or bf16 CUDA tensor [m, n]")
     m, n = logits.shape
-    _need((tokens is None) == (logprob is None) and (top_index is None) == (top_logprob is None),
-          "tokens and logprob, top_index and top_logprob: given together")
-
-    def two(name, t, dtype):
-        if t is None:
-            return 0
-        _need(t.dtype == dtype and t.dim() == 2 and t.shape[0] == m and t.is_contiguous() and t.is_cuda,
-              f"{name}: a contiguous {dtype} CUDA tensor [{m}, ..]")
-        return t.shape[1]
-
-    given, top = two("tokens", tokens, torch.int32), two("top_index", top_index, torch.int32)
-    _need(two("logprob", logprob, torch.float32) == given, "logprob: as many columns as tokens")
-    _need(two("top_logprob", top_logprob, torch.float32) == top, "top_logprob: as many columns as top_index")
-    for name, t in (("lse", lse), ("entropy", entropy)):
-        _need(t is None or (t.dtype == torch.float32 and t.numel() == m and t.is_contiguous() and t.is_cuda),
-              f"{name}: a contiguous fp32 CUDA tensor [{m}]")
-    st = _q.current_stream() if stream is None else stream
-    _q._check(load().qmm_logprobs(logits.data_ptr(), _type_of(logits), m, n, logits.stride(0) if m > 1 else n, _opt(tokens), given,
-                                  top, _opt(lse), _opt(entropy), _opt(logprob), _opt(top_index), _opt(top_logprob), st),
-              "qmm_logprobs")
+    st = logits.stride()
+    if m > 0 and n > 1 and st[1] != 1:
+        _refuse("logits", "contiguous but for the row stride")
+    if (tokens is None) != (logprob is None) or (top_index is None) != (top_logprob is None):
+        _refuse("tokens and logprob, top_index and top_logprob", "given together")
+    given = top = tp = lp = ip = vp = 0
+    if tokens is not None:
+        given = tokens.shape[1]
+        tp, lp = _vector("tokens", tokens, _i32, m * given), _vector("logprob", logprob, _f32, m * given)
+    if top_index is not None:
+        top = top_index.shape[1]
+        ip, vp = _vector("top_index", top_index, _i32, m * top), _vector("top_logprob", top_logprob, _f32, m * top)
+    status = load().qmm_logprobs(logits.data_ptr(), kind, m, n, st[0] if m > 1 else n, tp, given, top,
+                                 0 if lse is None else _vector("lse", lse, _f32, m),
+                                 0 if entropy is None else _vector("entropy", entropy, _f32, m), lp, ip, vp,
+                                 _stream(logits) if stream is None else stream)
+    if status:
+        raise _q.QmmError(status, "qmm_logprobs")

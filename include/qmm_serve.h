@@ -38,7 +38,7 @@ typedef struct {
     int32_t kv_heads;
     int32_t head_dim;
     int32_t page_tokens;
-    int32_t agents;         /* sequences: rows of page_table, at most 1024 */
+    int32_t agents;         /* sequences: rows of page_table, at most 960 */
     int32_t max_pages;      /* columns of page_table */
     int32_t max_agent_rows; /* qmm_kv_attend: upper bound on one sequence's rows in a call, >= 1
                                (max_agent_rows * heads / kv_heads <= 4096); a sequence above

@@ -69,7 +69,7 @@ def test_header_and_exports(lib):
     (dict(kv_heads=0), INVALID), (dict(agents=0), INVALID), (dict(max_pages=0), INVALID), (dict(pool_pages=0), INVALID),
     (dict(pool_pages=1 << 31), INVALID), (dict(max_agent_rows=0), INVALID), (dict(head_dim=96), SHAPE), (dict(page_tokens=48), SHAPE),
     (dict(page_tokens=512), SHAPE), (dict(format=0, head_dim=64), SHAPE), (dict(format=0, page_tokens=32), SHAPE),
-    (dict(agents=1025), SHAPE), (dict(max_pages=1 << 30), SHAPE)])
+    (dict(agents=961), SHAPE), (dict(max_pages=1 << 30), SHAPE)])
 def test_dims_are_checked(lib, call, kw, status):
     assert call(lib, dims(**kw)) == status
     assert call(lib, None) == INVALID
