@@ -157,7 +157,9 @@ namespace {
 // Tokens per chunk, by the dims alone (so that a row's bits are those of any other call): the
 // longest of 1024 .. a tile that gives every block of a GB300's grid two items at head dimension 128
 // (one block per SM), and six otherwise (four), when all sequences are full, and whose pages one
-// warp can hold (32).  At head dimension 64, 61 ragged sequences: 104 us at 1,024, 92 at 512, 93 at 256.
+// warp can hold (32).  At head dimension 64, 61 ragged sequences: 104 us at 1,024, 92 at 512, 93 at 256.  At 128,
+// calls with weights at 1,024 and 2,048: 109 and 112 us for a sequence of 131,071 (fp16), 184 and 189 for
+// 8 x 16,000 at 8 rows (bf16), 108 and 115 for 4 x 23,000 (q8_0).
 int32_t chunk_of(const qmm_kv_dims& d) {
     const int64_t cap = int64_t{d.max_pages} * d.page_tokens, items = d.head_dim == 128 ? 2 * 152 : 6 * 608;
     const int32_t least = d.head_dim == 128 ? kTcTile : kTile;

@@ -1,39 +1,34 @@
-// Attention of new tokens over the paged cache: the split kernel.
+// Attention of new tokens over the paged cache: what the split kernels share, and the one for head
+// dimensions 64 and 256.
 //
 // For query (row r of sequence a, head h of KV head g's group) and x_t = scale log2(e) q . k_t:
 //   out = sum_t 2^(x_t - M) v_t / l,   l = sum_t 2^(x_t - M),   M = max_t x_t,   t < row_len[r].
 // A sequence's slots are cut into chunks of p.chunk tokens at fixed places, so what a row
 // gets never depends on the other rows of the call.  Each (sequence, chunk, KV head, tile of
-// 8 NT queries) is an item; the blocks of a persistent grid take items in turn, keep running
-// maxima, denominators and outputs in registers, and write them as the item's partial.  All
-// queries of a tile share each K and V tile on chip, so the cache is read once for up to 48.
+// queries) is an item; the blocks of a persistent grid take items in turn and write M, l and the
+// unnormalised output as the item's partial, which the joining kernel adds up.  All queries of a
+// tile share each K and V tile on chip, so the cache is read once for up to 48.
 //
-// A block's four warps work on tiles of 64 tokens: each forms the scores of 16 tokens for all
-// queries, the maxima meet in shared memory, the probabilities go there as the second
-// product's operand, and each warp then sums over all 64 tokens for a quarter of the dims.
-// So a thread holds the outputs of D / 4 dims only, and three or four blocks fit an SM: their
-// barriers (two a tile) and loads overlap.  K and V parts stream through a ring of half tiles by bulk copies; the
-// ring runs on across items.  (A first version gave every warp a ring and whole outputs of
-// its own, without barriers: at 24 queries it needed 255 registers, spilled, and with two
-// warps per scheduler waited on everything; 275 us for the case that takes %Q8% us now.)
+// This kernel (16-bit pools).  A block's four warps work on tiles of 64 tokens: each forms the scores
+// of 16 tokens for all queries, the maxima meet in shared memory, the probabilities go there as the
+// second product's operand, and each warp then sums over all 64 tokens for a quarter of the dims.
+// So a thread holds the outputs of D / 4 dims only, and up to four blocks fit an SM: their barriers
+// (two a tile) and loads overlap.  K and V parts stream through a ring of half tiles by 2-D bulk
+// tensor copies with the 128-byte swizzle, which makes the ldmatrix reads conflict-free; the ring
+// runs on across items.  (A first version gave every warp a ring and whole outputs of its own,
+// without barriers: 61 ragged bf16 sequences at D = 64 took 118 us, 90 now.)
 //
 // Both products run on mma.sync m16n8k16 with tokens (S^T = K Q^T) and then dims
 // (O^T = V^T P^T) as the 16 rows and queries as the 8 columns: one new token of a group of
 // up to 8 heads fills one column tile, where queries as rows would pad them to 16.  S^T's
 // accumulators become P^T's operands by an 8x8 transpose in registers (movmatrix).
-// p enters the second product as two 16-bit parts (hi = round(p), lo = round(p - hi)),
-// which keeps fp32's accuracy for the price of a second product; the kernel has the room,
-// since the cache's bytes bound it.  p carries a factor 2^kShift (the
-// denominator too), so that small probabilities stay clear of fp16's subnormals.
+// p enters the second product as two 16-bit parts (hi = round(p), lo = round(p - hi)), which keeps
+// fp32's accuracy for the price of a second product.  It carries a factor 2^kShift (the denominator
+// too), so that small probabilities stay clear of fp16's subnormals.
 //
-// 16-bit pools: half tiles are loaded by 2-D bulk tensor copies with the 128-byte swizzle,
-// which makes the ldmatrix reads conflict-free.  q8_0 pools: a tile is
-// one record; the K quants are exact in fp16, each 32-dim block's partial sum gets its scale
-// in fp32.  V's scale depends on token and block and so goes into P: a token's exponent
-// e_t = max over blocks of its scales' exponents joins the softmax's reference
-// (y_t = x_t + e_t, M = max y_t), p^ = 2^(y_t - M) <= 1 is split, and p^ times the
-// normalised scale (scale 2^-e_t) is formed error-free in half2 (product, its error by fma).
-// No scale of the format can then overflow or vanish.
+// What bounds it: at D = 64 the chain of barriers and waits of a 16 KB tile, not the bytes (61 ragged
+// sequences, 250 MB: 63 us, 4.0 TB/s, and 27 for the join and the weights).  An M = 128 tensor core
+// product would be half empty at D = 64, and D = 256 leaves it no room for two tiles.
 #pragma once
 
 #include <cuda.h>
@@ -47,7 +42,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 64;            // tokens per tile
 constexpr int kTcTile = 128;         // tokens per tile of the tensor core kernel (head dimension 128)
-constexpr float kShift = 13.f;       // p's power of two: p^ <= 2^13, times a scale < 4 <= 2^15
+constexpr float kShift = 13.f;       // p's power of two in the partials: l = sum 2^(x - M + kShift)
 constexpr float kNoMax = -INFINITY;
 
 struct AttendParams {
@@ -78,23 +73,19 @@ struct AttendParams {
 
 template <int FMT, int D, int NT>
 struct Geo {
-    static constexpr bool q8 = FMT == QMM_KV_Q8_0;
-    static constexpr int QT = 8 * NT;                        // queries of a tile
-    static constexpr int HB = q8 ? kQ8Half : kTile * D * 2;  // bytes of a half tile (K or V)
-    static constexpr int slots = q8 ? 4 : 3;                 // half tiles in flight
+    static constexpr int QT = 8 * NT;             // queries of a tile
+    static constexpr int HB = kTile * D * 2;      // bytes of a half tile (K or V)
+    static constexpr int slots = 3;               // half tiles in flight
     static constexpr int KS = D / 16;
-    static constexpr int MW = D / 64;                        // m16 tiles of dims per warp
-    // halves per row of P and bytes per row of Q, for conflict-free reads: 8-byte (P) and 16-byte
-    // (Q) loads of the q8_0 layout, ldmatrix otherwise
-    static constexpr int PS = q8 ? kTile + 4 : kTile + 8;
-    static constexpr int QS = q8 ? 2 * D + 64 : 2 * D + 16;
+    static constexpr int MW = D / 64;             // m16 tiles of dims per warp
+    static constexpr int PS = kTile + 8;          // halves per row of P, and bytes per row of Q: the padding
+    static constexpr int QS = 2 * D + 16;         // keeps ldmatrix free of bank conflicts
     // blocks per SM that the registers are limited for (D = 256: the ring alone takes 96 KB)
     static constexpr int blocks = D == 256 ? 2 : NT == 6 ? 3 : 4;
-    // dynamic shared memory, after aligning to 1024: ring, Q, P (hi, lo), 2^-e, maxima, lengths, barriers
+    // dynamic shared memory, after aligning to 1024: ring, Q, P (hi, lo), maxima, lengths, barriers
     static constexpr int off_q = slots * HB;
     static constexpr int off_p = off_q + QT * QS;
-    static constexpr int off_inv = off_p + 2 * QT * PS * 2;
-    static constexpr int off_red = off_inv + kTile * 2;
+    static constexpr int off_red = off_p + 2 * QT * PS * 2;
     static constexpr int off_len = off_red + QT * 16;
     static constexpr int off_bar = (off_len + QT * 4 + 15) / 16 * 16;
     static constexpr int off_misc = off_bar + slots * 8 + 8;  // tmp[33], abort, miss[slots], odd[2][2]
@@ -261,7 +252,6 @@ __global__ void __launch_bounds__(kThreads, (Geo<FMT, D, NT>::blocks))
     uint8_t* sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
     uint16_t* Ph = reinterpret_cast<uint16_t*>(sm + G::off_p);  // [QT][PS]
     uint16_t* Pl = Ph + QT * PS;
-    uint16_t* inv_e = reinterpret_cast<uint16_t*>(sm + G::off_inv);  // [64], q8_0: 2^-e_t
     float* red = reinterpret_cast<float*>(sm + G::off_red);          // [QT][4 warps]
     int* qlen_sm = reinterpret_cast<int*>(sm + G::off_len);          // [QT]
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + G::off_bar);
@@ -306,45 +296,32 @@ __global__ void __launch_bounds__(kThreads, (Geo<FMT, D, NT>::blocks))
         uint8_t* dst = sm + pslot * G::HB;
         uint64_t* b = bar + pslot;
         const int first = pi.tok0 >> p.page_shift;
-        if constexpr (G::q8) {
-            const int pg = __shfl_sync(0xffffffffu, ppages, (ptok >> 6) - first);
-            if (lane == 0) {
-                miss_sm[pslot] = pg < 0;
-                if (pg < 0) mbar_arrive(b);
-                else {
-                    mbar_arrive_expect_tx(b, kQ8Half);
-                    bulk_g2s(dst, p.pool + (static_cast<int64_t>(pg) * p.kv_heads + pi.g) * kQ8Rec + phalf * kQ8Half, kQ8Half,
-                             b, l2_policy_evict_first());
-                }
-            }
-        } else {
-            // pieces of min(64, page_tokens) tokens, those with tokens before the item's end
-            const int br = min(kTile, p.page_tokens);
-            int pg[kTile / 16];
-            uint32_t bytes = 0;
-            bool miss = false;
+        // pieces of min(64, page_tokens) tokens, those with tokens before the item's end
+        const int br = min(kTile, p.page_tokens);
+        int pg[kTile / 16];
+        uint32_t bytes = 0;
+        bool miss = false;
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k) {
+            const int tok = ptok + k * br;
+            const bool in = k * br < kTile && tok < pi.end;
+            const int x = __shfl_sync(0xffffffffu, ppages, in ? (tok >> p.page_shift) - first : 0);
+            pg[k] = in ? x : -1;
+            miss |= in && x < 0;
+            if (pg[k] >= 0) bytes += br * D * 2;
+        }
+        if (lane == 0) {
+            miss_sm[pslot] = miss;
+            if (bytes == 0) mbar_arrive(b);
+            else mbar_arrive_expect_tx(b, bytes);
+            const uint64_t policy = l2_policy_evict_first();
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k) {
-                const int tok = ptok + k * br;
-                const bool in = k * br < kTile && tok < pi.end;
-                const int x = __shfl_sync(0xffffffffu, ppages, in ? (tok >> p.page_shift) - first : 0);
-                pg[k] = in ? x : -1;
-                miss |= in && x < 0;
-                if (pg[k] >= 0) bytes += br * D * 2;
-            }
-            if (lane == 0) {
-                miss_sm[pslot] = miss;
-                if (bytes == 0) mbar_arrive(b);
-                else mbar_arrive_expect_tx(b, bytes);
-                const uint64_t policy = l2_policy_evict_first();
+                if (pg[k] < 0) continue;
+                const int y = ((pg[k] * p.kv_heads + pi.g) * 2 + phalf) * p.page_tokens + ((ptok + k * br) & (p.page_tokens - 1));
 #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k) {
-                    if (pg[k] < 0) continue;
-                    const int y = ((pg[k] * p.kv_heads + pi.g) * 2 + phalf) * p.page_tokens + ((ptok + k * br) & (p.page_tokens - 1));
-#pragma unroll
-                    for (int x = 0; x < D / 64; ++x)
-                        tma_load_2d_hint(dst + x * kTile * 128 + k * br * 128, &map, 64 * x, y, b, policy);
-                }
+                for (int x = 0; x < D / 64; ++x)
+                    tma_load_2d_hint(dst + x * kTile * 128 + k * br * 128, &map, 64 * x, y, b, policy);
             }
         }
         ++issued;
@@ -419,76 +396,27 @@ __global__ void __launch_bounds__(kThreads, (Geo<FMT, D, NT>::blocks))
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) s[nt][c] = 0.f;
-            if constexpr (G::q8) {
-                // k-slots are permuted so that a thread's eight dims of a block are contiguous (slots
-                // 2t, 2t+1, 2t+8, 2t+9 of step k2: dims 8t + 4 k2 + 0 .. 3)
-                const int key = q8_key(g8);
-                const uint2 sca = *reinterpret_cast<const uint2*>(kt + 8192 + ta * 8);
-                const uint2 scb = *reinterpret_cast<const uint2*>(kt + 8192 + (ta + 8) * 8);
+            const uint32_t base = smem_u32(kt) + (16 * warp + (lane & 15)) * 128;
+            const uint32_t qbase = smem_u32(sm + G::off_q) + (lane & 7) * QS + (lane >> 3) * 16;
 #pragma unroll
-                for (int blk = 0; blk < 4; ++blk) {
-                    const uint8_t* ka = kt + ta * 128 + 16 * ((2 * blk + (t4 >> 1)) ^ key) + 8 * (t4 & 1);
-                    uint2 va = *reinterpret_cast<const uint2*>(ka), vb = *reinterpret_cast<const uint2*>(ka + 8 * 128);
-                    va.x ^= 0x80808080u, va.y ^= 0x80808080u, vb.x ^= 0x80808080u, vb.y ^= 0x80808080u;
-                    const uint32_t a0 = i8_to_h2(va.x, 0x4140u), a1 = i8_to_h2(vb.x, 0x4140u), a2 = i8_to_h2(va.x, 0x4342u),
-                                   a3 = i8_to_h2(vb.x, 0x4342u);
-                    const uint32_t b0 = i8_to_h2(va.y, 0x4140u), b1 = i8_to_h2(vb.y, 0x4140u), b2 = i8_to_h2(va.y, 0x4342u),
-                                   b3 = i8_to_h2(vb.y, 0x4342u);
-                    const __half2 pa = as_h2(blk < 2 ? sca.x : sca.y), pb = as_h2(blk < 2 ? scb.x : scb.y);
-                    const float fa = (blk & 1) ? __high2float(pa) : __low2float(pa);
-                    const float fb = (blk & 1) ? __high2float(pb) : __low2float(pb);
+            for (int ks = 0; ks < G::KS; ks += 2) {
+                uint32_t a[2][4];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        if (nt < nnt) {
-                            const uint4 q = lds128(sm + G::off_q + (8 * nt + g8) * QS + 64 * blk + 16 * t4);
-                            float d[4] = {0.f, 0.f, 0.f, 0.f};
-                            mma_m16n8k16(d, a0, a1, a2, a3, q.x, q.y);
-                            mma_m16n8k16(d, b0, b1, b2, b3, q.z, q.w);
-                            s[nt][0] = fmaf(d[0], fa, s[nt][0]);
-                            s[nt][1] = fmaf(d[1], fa, s[nt][1]);
-                            s[nt][2] = fmaf(d[2], fb, s[nt][2]);
-                            s[nt][3] = fmaf(d[3], fb, s[nt][3]);
-                        }
+                for (int e = 0; e < 2; ++e) {
+                    const int ch = 2 * (ks + e) + (lane >> 4);
+                    ldmatrix_x4(a[e], base + (ch >> 3) * (kTile * 128) + (((ch & 7) ^ (lane & 7)) << 4));
                 }
-            } else {
-                const uint32_t base = smem_u32(kt) + (16 * warp + (lane & 15)) * 128;
-                const uint32_t qbase = smem_u32(sm + G::off_q) + (lane & 7) * QS + (lane >> 3) * 16;
 #pragma unroll
-                for (int ks = 0; ks < G::KS; ks += 2) {
-                    uint32_t a[2][4];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int ch = 2 * (ks + e) + (lane >> 4);
-                        ldmatrix_x4(a[e], base + (ch >> 3) * (kTile * 128) + (((ch & 7) ^ (lane & 7)) << 4));
+                for (int nt = 0; nt < NT; ++nt)
+                    if (nt < nnt) {
+                        uint32_t q[4];
+                        ldmatrix_x4(q, qbase + nt * 8 * QS + ks * 32);
+                        mma16<BF>(s[nt], a[0][0], a[0][1], a[0][2], a[0][3], q[0], q[1]);
+                        mma16<BF>(s[nt], a[1][0], a[1][1], a[1][2], a[1][3], q[2], q[3]);
                     }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        if (nt < nnt) {
-                            uint32_t q[4];
-                            ldmatrix_x4(q, qbase + nt * 8 * QS + ks * 32);
-                            mma16<BF>(s[nt], a[0][0], a[0][1], a[0][2], a[0][3], q[0], q[1]);
-                            mma16<BF>(s[nt], a[1][0], a[1][1], a[1][2], a[1][3], q[2], q[3]);
-                        }
-                }
             }
             ok &= mbar_wait_bounded(bar + slot, phase, abort_flag);  // V
             next();
-            float ea = 0.f, eb = 0.f;
-            uint16_t two_e = 0;
-            if constexpr (G::q8) {
-                // lane l < 16: the exponent of token 16 warp + l's largest V scale, in -14 .. 14
-                const int t = 16 * warp + (lane & 15);
-                uint32_t top = 0;
-#pragma unroll
-                for (int blk = 0; blk < 4; ++blk) {
-                    const uint32_t w = *reinterpret_cast<const uint16_t*>(vt + 8192 + (blk * 64 + t) * 2) & 0x7FFFu;
-                    top = w > 0x7C00u ? top : max(top, w);  // (NaN scales do not count)
-                }
-                const int e = min(max(static_cast<int>(top >> 10), 1), 29);
-                two_e = static_cast<uint16_t>((30 - e) << 10);  // 2^-e
-                ea = static_cast<float>(__shfl_sync(0xffffffffu, e, g8) - 15);
-                eb = static_cast<float>(__shfl_sync(0xffffffffu, e, g8 + 8) - 15);
-            }
             // ---- base-2 scores, masks, the weights' copy, the warp's maxima
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -507,12 +435,6 @@ __global__ void __launch_bounds__(kThreads, (Geo<FMT, D, NT>::blocks))
                         float* at = sbase + ((q0 >> 2) + 2 * nt + (t4 >> 1)) * plane + (tb + ta) * 4 + 2 * (t4 & 1);
                         *reinterpret_cast<float2*>(at) = make_float2(s[nt][0], s[nt][1]);
                         *reinterpret_cast<float2*>(at + 32) = make_float2(s[nt][2], s[nt][3]);
-                    }
-                    if constexpr (G::q8) {
-                        s[nt][0] += ea;
-                        s[nt][1] += ea;
-                        s[nt][2] += eb;
-                        s[nt][3] += eb;
                     }
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -534,7 +456,6 @@ __global__ void __launch_bounds__(kThreads, (Geo<FMT, D, NT>::blocks))
             }
             freed = 1;  // this tile's V, at the next tile's barrier
             if (tid < 2) odd_sm[2 * (parity ^ 1) + tid] = 0;
-            if (G::q8 && lane < 16) inv_e[16 * warp + lane] = two_e;
 
             // ---- new maxima, rescaling, probabilities to shared memory
 #pragma unroll
@@ -553,9 +474,6 @@ __global__ void __launch_bounds__(kThreads, (Geo<FMT, D, NT>::blocks))
                         s[nt][e] = pa;
                         s[nt][2 + e] = pb;
                         float sum = pa + pb;
-                        if constexpr (G::q8)
-                            sum = pa * __int_as_float((127 - static_cast<int>(ea)) << 23) +
-                                  pb * __int_as_float((127 - static_cast<int>(eb)) << 23);
                         l[nt][e] = fmaf(l[nt][e], alpha[e], sum);
                     }
                     if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
@@ -573,142 +491,86 @@ __global__ void __launch_bounds__(kThreads, (Geo<FMT, D, NT>::blocks))
                         *reinterpret_cast<uint32_t*>(Pl + at) = movmatrix_trans(lo);
                     }
                 }
-            if constexpr (!G::q8) {
-                if (edge) {
-                    // The warp's rows of V that some query does not see.  Past the sequence's end (and
-                    // in tiles with a missing page) they hold anything and become zero.  One that
-                    // some queries see and that holds a NaN or infinity is marked.
-                    const int last = miss ? 0 : it.end - tb;
-                    for (int t = max(16 * warp, miss ? 0 : minlen - tb); t < 16 * warp + 16; ++t) {
-                        uint32_t* w = reinterpret_cast<uint32_t*>(vt + ((lane * MW) >> 5) * (kTile * 128) + t * 128 +
-                                                                  (((((lane * MW) & 31) >> 2) ^ (t & 7)) << 4) + ((lane * MW) & 3) * 4);
-                        if (t >= last) {
+            if (edge) {
+                // The warp's rows of V that some query does not see.  Past the sequence's end (and
+                // in tiles with a missing page) they hold anything and become zero.  One that
+                // some queries see and that holds a NaN or infinity is marked.
+                const int last = miss ? 0 : it.end - tb;
+                for (int t = max(16 * warp, miss ? 0 : minlen - tb); t < 16 * warp + 16; ++t) {
+                    uint32_t* w = reinterpret_cast<uint32_t*>(vt + ((lane * MW) >> 5) * (kTile * 128) + t * 128 +
+                                                              (((((lane * MW) & 31) >> 2) ^ (t & 7)) << 4) + ((lane * MW) & 3) * 4);
+                    if (t >= last) {
 #pragma unroll
-                            for (int i = 0; i < MW; ++i) w[i] = 0u;
-                        } else {
-                            bool here = false;
-                            constexpr uint32_t ex = BF ? 0x7F80u : 0x7C00u;
+                        for (int i = 0; i < MW; ++i) w[i] = 0u;
+                    } else {
+                        bool here = false;
+                        constexpr uint32_t ex = BF ? 0x7F80u : 0x7C00u;
 #pragma unroll
-                            for (int i = 0; i < MW; ++i) here |= (w[i] & ex) == ex || ((w[i] >> 16) & ex) == ex;
-                            if (__any_sync(0xffffffffu, here) && lane == 0) atomicOr(odd_sm + 2 * parity + (t >> 5), 1u << (t & 31));
-                        }
+                        for (int i = 0; i < MW; ++i) here |= (w[i] & ex) == ex || ((w[i] >> 16) & ex) == ex;
+                        if (__any_sync(0xffffffffu, here) && lane == 0) atomicOr(odd_sm + 2 * parity + (t >> 5), 1u << (t & 31));
                     }
                 }
             }
             __syncthreads();  // P is complete
-            if constexpr (!G::q8) {
-                if (edge && (odd_sm[2 * parity] | odd_sm[2 * parity + 1])) {
-                    // marked rows: added query by query, to those that see them; then zero in the product
+            if (edge && (odd_sm[2 * parity] | odd_sm[2 * parity + 1])) {
+                // marked rows: added query by query, to those that see them; then zero in the product
 #pragma unroll 1
-                    for (int t = 0; t < kTile; ++t) {
-                        if (!((odd_sm[2 * parity + (t >> 5)] >> (t & 31)) & 1)) continue;
+                for (int t = 0; t < kTile; ++t) {
+                    if (!((odd_sm[2 * parity + (t >> 5)] >> (t & 31)) & 1)) continue;
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                const int q = 8 * nt + 2 * t4 + (c & 1);
-                                if (nt >= nnt || tb + t >= qlen_sm[q]) continue;
-                                const uint32_t h = Ph[q * PS + t], u = Pl[q * PS + t];
-                                const float pt = BF ? __uint_as_float(h << 16) + __uint_as_float(u << 16)
-                                                    : __half2float(__ushort_as_half(h)) + __half2float(__ushort_as_half(u));
+                        for (int c = 0; c < 4; ++c) {
+                            const int q = 8 * nt + 2 * t4 + (c & 1);
+                            if (nt >= nnt || tb + t >= qlen_sm[q]) continue;
+                            const uint32_t h = Ph[q * PS + t], u = Pl[q * PS + t];
+                            const float pt = BF ? __uint_as_float(h << 16) + __uint_as_float(u << 16)
+                                                : __half2float(__ushort_as_half(h)) + __half2float(__ushort_as_half(u));
 #pragma unroll
-                                for (int mt = 0; mt < MW; ++mt) {
-                                    const int d = 16 * (warp * MW + mt) + g8 + 8 * (c >> 1);
-                                    const uint32_t v = *reinterpret_cast<const uint16_t*>(
-                                        vt + (d >> 6) * (kTile * 128) + t * 128 + ((((d & 63) >> 3) ^ (t & 7)) << 4) + (d & 7) * 2);
-                                    o[mt][nt][c] = fmaf(pt, BF ? __uint_as_float(v << 16) : __half2float(__ushort_as_half(v)), o[mt][nt][c]);
-                                }
+                            for (int mt = 0; mt < MW; ++mt) {
+                                const int d = 16 * (warp * MW + mt) + g8 + 8 * (c >> 1);
+                                const uint32_t v = *reinterpret_cast<const uint16_t*>(
+                                    vt + (d >> 6) * (kTile * 128) + t * 128 + ((((d & 63) >> 3) ^ (t & 7)) << 4) + (d & 7) * 2);
+                                o[mt][nt][c] = fmaf(pt, BF ? __uint_as_float(v << 16) : __half2float(__ushort_as_half(v)), o[mt][nt][c]);
                             }
-                    }
-                    __syncthreads();
-                    for (int t = warp; t < kTile; t += kWarps)
-                        if ((odd_sm[2 * parity + (t >> 5)] >> (t & 31)) & 1)
-                            for (int i = lane; i < D / 2; i += 32)
-                                *reinterpret_cast<uint32_t*>(vt + (i >> 5) * (kTile * 128) + t * 128 + (i & 31) * 4) = 0u;
-                    __syncthreads();
+                        }
                 }
+                __syncthreads();
+                for (int t = warp; t < kTile; t += kWarps)
+                    if ((odd_sm[2 * parity + (t >> 5)] >> (t & 31)) & 1)
+                        for (int i = lane; i < D / 2; i += 32)
+                            *reinterpret_cast<uint32_t*>(vt + (i >> 5) * (kTile * 128) + t * 128 + (i & 31) * 4) = 0u;
+                __syncthreads();
             }
 
             // ---- O^T += V^T P^T for dims D / 4 * warp ..
-            if constexpr (G::q8) {
-                // (D / 4 = 32: one block of scales.)  Tokens of step ks: 16 t4 + 4 ks + 0 .. 3 are the thread's
-                // k-slots 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9, so that its sixteen V bytes are contiguous
-                uint4 w[2][2];
+            const uint32_t pbase = smem_u32(Ph) + ((lane & 7) * PS + (lane >> 3) * 8) * 2;
+            const uint32_t vbase = smem_u32(vt) + ((lane & 7) + ((lane >> 4) << 3)) * 128;
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
+            for (int ks = 0; ks < 4; ks += 2) {
+                uint32_t a[2][MW][4];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        w[mt][h] = *reinterpret_cast<const uint4*>(vt + (32 * warp + 16 * mt + 8 * h + g8) * 64 + 16 * t4);
-                        w[mt][h].x ^= 0x80808080u, w[mt][h].y ^= 0x80808080u, w[mt][h].z ^= 0x80808080u, w[mt][h].w ^= 0x80808080u;
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int mt = 0; mt < MW; ++mt) {
+                        const int ch = 2 * (warp * MW + mt) + ((lane >> 3) & 1);
+                        ldmatrix_x4_trans(a[e][mt], vbase + (ch >> 3) * (kTile * 128) + (ks + e) * 16 * 128 +
+                                                        (((ch & 7) ^ (lane & 7)) << 4));
                     }
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) {
-                    const int tok = 16 * t4 + 4 * ks;
-                    const uint2 dv = *reinterpret_cast<const uint2*>(vt + 8192 + (warp * 64 + tok) * 2);
-                    const uint2 di = *reinterpret_cast<const uint2*>(inv_e + tok);
-                    const __half2 d0 = __hmul2(as_h2(dv.x), as_h2(di.x)), d1 = __hmul2(as_h2(dv.y), as_h2(di.y));
-                    uint32_t a[2][4];
+                for (int nt = 0; nt < NT; ++nt)
+                    if (nt < nnt) {
+                        uint32_t bh[4], bl[4];
+                        ldmatrix_x4(bh, pbase + (nt * 8 * PS + ks * 16) * 2);
+                        ldmatrix_x4(bl, pbase + (QT * PS + nt * 8 * PS + ks * 16) * 2);
 #pragma unroll
-                    for (int mt = 0; mt < 2; ++mt) {
-                        const uint32_t w0 = ks == 0 ? w[mt][0].x : ks == 1 ? w[mt][0].y : ks == 2 ? w[mt][0].z : w[mt][0].w;
-                        const uint32_t w1 = ks == 0 ? w[mt][1].x : ks == 1 ? w[mt][1].y : ks == 2 ? w[mt][1].z : w[mt][1].w;
-                        a[mt][0] = i8_to_h2(w0, 0x4140u);
-                        a[mt][1] = i8_to_h2(w1, 0x4140u);
-                        a[mt][2] = i8_to_h2(w0, 0x4342u);
-                        a[mt][3] = i8_to_h2(w1, 0x4342u);
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int mt = 0; mt < MW; ++mt) {
+                                mma16<BF>(o[mt][nt], a[e][mt][0], a[e][mt][1], a[e][mt][2], a[e][mt][3], bh[2 * e], bh[2 * e + 1]);
+                                mma16<BF>(o[mt][nt], a[e][mt][0], a[e][mt][1], a[e][mt][2], a[e][mt][3], bl[2 * e], bl[2 * e + 1]);
+                            }
                     }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        if (nt < nnt) {
-                            const uint2 bh = *reinterpret_cast<const uint2*>(Ph + (8 * nt + g8) * PS + tok);
-                            const uint2 bl = *reinterpret_cast<const uint2*>(Pl + (8 * nt + g8) * PS + tok);
-                            // (hi + lo) * scale = ph + pl: the product's rounding error comes back by fma
-                            const __half2 ph0 = __hmul2(as_h2(bh.x), d0), ph1 = __hmul2(as_h2(bh.y), d1);
-                            const __half2 pl0 = __hfma2(as_h2(bl.x), d0, __hfma2(as_h2(bh.x), d0, __hneg2(ph0)));
-                            const __half2 pl1 = __hfma2(as_h2(bl.y), d1, __hfma2(as_h2(bh.y), d1, __hneg2(ph1)));
-                            uint32_t uh0 = as_u32(ph0), uh1 = as_u32(ph1), ul0 = as_u32(pl0), ul1 = as_u32(pl1);
-                            if (edge) {  // a scale that is NaN or infinite has no effect on rows that do not see it
-                                const int n = miss ? 0 : qlen_sm[8 * nt + g8] - tb - tok;
-                                const uint32_t m0 = (n > 0 ? 0xFFFFu : 0u) | (n > 1 ? 0xFFFF0000u : 0u);
-                                const uint32_t m1 = (n > 2 ? 0xFFFFu : 0u) | (n > 3 ? 0xFFFF0000u : 0u);
-                                uh0 &= m0, ul0 &= m0, uh1 &= m1, ul1 &= m1;
-                            }
-#pragma unroll
-                            for (int mt = 0; mt < 2; ++mt) {
-                                mma_m16n8k16(o[mt][nt], a[mt][0], a[mt][1], a[mt][2], a[mt][3], uh0, uh1);
-                                mma_m16n8k16(o[mt][nt], a[mt][0], a[mt][1], a[mt][2], a[mt][3], ul0, ul1);
-                            }
-                        }
-                }
-            } else {
-                const uint32_t pbase = smem_u32(Ph) + ((lane & 7) * PS + (lane >> 3) * 8) * 2;
-                const uint32_t vbase = smem_u32(vt) + ((lane & 7) + ((lane >> 4) << 3)) * 128;
-#pragma unroll
-                for (int ks = 0; ks < 4; ks += 2) {
-                    uint32_t a[2][MW][4];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-#pragma unroll
-                        for (int mt = 0; mt < MW; ++mt) {
-                            const int ch = 2 * (warp * MW + mt) + ((lane >> 3) & 1);
-                            ldmatrix_x4_trans(a[e][mt], vbase + (ch >> 3) * (kTile * 128) + (ks + e) * 16 * 128 +
-                                                            (((ch & 7) ^ (lane & 7)) << 4));
-                        }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        if (nt < nnt) {
-                            uint32_t bh[4], bl[4];
-                            ldmatrix_x4(bh, pbase + (nt * 8 * PS + ks * 16) * 2);
-                            ldmatrix_x4(bl, pbase + (QT * PS + nt * 8 * PS + ks * 16) * 2);
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                                for (int mt = 0; mt < MW; ++mt) {
-                                    mma16<BF>(o[mt][nt], a[e][mt][0], a[e][mt][1], a[e][mt][2], a[e][mt][3], bh[2 * e], bh[2 * e + 1]);
-                                    mma16<BF>(o[mt][nt], a[e][mt][0], a[e][mt][1], a[e][mt][2], a[e][mt][3], bl[2 * e], bl[2 * e + 1]);
-                                }
-                        }
-                }
             }
             parity ^= 1;
         }

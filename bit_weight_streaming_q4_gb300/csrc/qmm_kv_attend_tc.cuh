@@ -18,12 +18,25 @@
 //   last four   q8_0 only: K and V quants to fp16 in tensor memory, as A operands
 // 16-bit pools: the swizzled tiles are A operands as they come, K by rows and V transposed
 // (M-contiguous).  q8_0: K's quants are exact in fp16, one accumulator per 32-dim block takes its
-// scale in fp32; V's element, quant times normalised scale (see qmm_kv_attend.cuh), is split into
-// two fp16 parts without error, and three of the four products of parts count.
+// scale in fp32.  V's scale depends on token and block: a token's exponent e_t = max over blocks of
+// its scales' exponents joins the softmax's reference (y_t = x_t + e_t, M = max y_t), so that
+// p^ = 2^(y_t - M) <= 1 whatever the scales, and V's element, quant times normalised scale
+// (scale 2^-e_t), is split into two fp16 parts without error (product, its error by fma); three of
+// the four products of parts count.  No scale of the format can then overflow or vanish.
 //
 // A query's reference is its first tile's maximum and moves only when a score passes it by more than
-// 2^kSlack (a vote per tile; then the warps form the tile's maxima and rescale what they
-// hold).  Each query decides for itself, so its bits depend on nothing but its own tokens.
+// 2^kSlack (a vote per tile; then the group forms the tile's maxima and rescales what it
+// holds).  Each query decides for itself, so its bits depend on nothing but its own tokens.
+//
+// What it measured (this kernel alone, without weights; in brackets the call, whose join comes after):
+// fp16, one sequence of 131,071, 1 row: 81 us (88), 6.6 TB/s, the bytes.  bf16, 8 x 16,000, 8 rows
+// (48 queries a head): 99 us (114), 5.3 TB/s.  q8_0, 4 x 23,000, 3 rows (18 queries): 90 us (96), 2.2 TB/s.
+// The last two are bound by the chain from a tile's scores to its probabilities: by clock readings in
+// a copy of the kernel a softmax group takes about 3,700 and 3,900 clocks a tile, fp16 at one row 2,700.
+// Not kept, this kernel's time against its time then: groups that take whole tiles in turn, with
+// outputs of their own (q8_0 125 us for 90, bf16 144 for 110: each thread then does all queries); four
+// groups of 8 queries at q8_0 (97 for 90); K and V converted by warps of their own (98 for 90).
+// On mma.sync with the outputs in registers the three cases took 86, 300 and 113 us.
 #pragma once
 
 #include "qmm_kv_attend.cuh"
@@ -58,8 +71,8 @@ struct TcGeo {
     static constexpr int off_lim = off_len + 2 * N * 4;                         // [N] reference + slack
     static constexpr int off_sub = off_lim + N * 4;                             // [N] reference - kTcShift
     static constexpr int off_alpha = off_sub + N * 4;                           // [N]
-    static constexpr int off_red = off_alpha + N * 4;                           // [softmax warps][32]
-    static constexpr int off_odd = off_red + 4 * groups * 32 * 4;               // [4] tokens to be taken query by query
+    static constexpr int off_red = off_alpha + N * 4;                           // [group][4 warps][W]
+    static constexpr int off_odd = off_red + 4 * N * 4;                         // [4] tokens to be taken query by query
     static constexpr int off_bar = off_odd + 16;
     static constexpr int bars = 2 * k_slots + 2 * v_slots + 4 + 4 + 4 + 2;
     static constexpr int off_item = (off_bar + bars * 8 + 15) / 16 * 16;        // [2] of ItemRec
@@ -378,7 +391,6 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
             const Item it = decode_item(p, seq, item, N);
             const int r0 = seq[it.a].w, nq = (seq[it.a + 1].w - r0) * p.group, q0 = it.tile * N;
             const int buf = k & 1, c = lane & 15;
-            int qi = lane >> 4, r = r0 + (q0 + qi) / p.group, h = (q0 + qi) % p.group;
             if (k > 1) await_warp(qempty + buf, ((k >> 1) - 1) & 1);
             if (!live) break;
             if (lane == 0) {
@@ -386,19 +398,27 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                 item_sm[buf] = rec;
             }
             uint8_t* dst = sm + G::off_q + buf * G::opnd + (c >> 3) * (N * 128);
-#pragma unroll 8
-            for (int i = 0; i < N / 2; ++i) {  // 16-byte pieces, swizzled as the copies do
-                const bool in = q0 + qi < nq;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                int len = 0;
-                if (in) {
-                    v = *reinterpret_cast<const uint4*>(p.q + r * p.q_stride + static_cast<int64_t>(it.g * p.group + h) * D + 8 * c);
-                    if (c == 0) len = p.row_len[r];
+            for (int i0 = 0; i0 < N; i0 += 16) {
+                // eight rows' 16-byte pieces on their way at once, then stored, swizzled as the copies do
+                uint4 v[8];
+                int len[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int qa = q0 + i0 + 2 * j + (lane >> 4);
+                    v[j] = make_uint4(0, 0, 0, 0);
+                    len[j] = 0;
+                    if (qa < nq) {
+                        const int r = r0 + qa / p.group, h = qa % p.group;
+                        v[j] = *reinterpret_cast<const uint4*>(p.q + r * p.q_stride + static_cast<int64_t>(it.g * p.group + h) * D + 8 * c);
+                        len[j] = p.row_len[r];
+                    }
                 }
-                *reinterpret_cast<uint4*>(dst + qi * 128 + (((c & 7) ^ (qi & 7)) << 4)) = v;
-                if (c == 0) qlen_sm[buf * N + qi] = len;
-                qi += 2;
-                for (h += 2; h >= p.group; h -= p.group) ++r;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int qi = i0 + 2 * j + (lane >> 4);
+                    *reinterpret_cast<uint4*>(dst + qi * 128 + (((c & 7) ^ (qi & 7)) << 4)) = v[j];
+                    if (c == 0) qlen_sm[buf * N + qi] = len[j];
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -414,7 +434,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
         float* lim = lim_sm + c0;
         float* sub = sub_sm + c0;
         float* alpha = alpha_sm + c0;
-        float* red = red_sm + grp * 128;       // [4][32]
+        float* red = red_sm + grp * 4 * W;     // [4][W]
         volatile int* dead = tmp + 40 + 2 * grp;    // some thread's wait ran out
         volatile int* missed = dead + 1;            // the last tile with a missing page
         int t = 0, k = 0;
@@ -519,10 +539,11 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                     }
                     miss = *missed == t;
                     // (a NaN is no maximum: fmaxf passes it over)
-                    red[w4 * 32 + lane] = reduce_columns<W>(x, kNoMax, [](float a, float b) { return fmaxf(a, b); });
+                    const float r = reduce_columns<W>(x, kNoMax, [](float a, float b) { return fmaxf(a, b); });
+                    if (lane < W) red[w4 * W + lane] = r;
                     named_bar_sync(bar_id, 128);
                     if (me < W) {
-                        float m = fmaxf(fmaxf(red[me], red[32 + me]), fmaxf(red[64 + me], red[96 + me]));
+                        float m = fmaxf(fmaxf(red[me], red[W + me]), fmaxf(red[2 * W + me], red[3 * W + me]));
                         if (fabsf(m) < 1e6f) m = ceilf(m * 16.f) * 0.0625f;  // (sums with the constants are then exact)
                         const bool passed = m > lim[me];
                         alpha[me] = passed ? ex2(lim[me] - kSlack - m) : 1.f;  // (2^-inf = 0 the first time)
@@ -696,11 +717,12 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                     if (q0 + c + i < it.nq) po[(c + i) * D] = fmaf(v[1][i], 1.f / kLowScale, v[0][i]);
             }
             tc_fence_before();
-            red[w4 * 32 + lane] = reduce_columns<W>(l, 0.f, [](float a, float b) { return a + b; });
+            const float r = reduce_columns<W>(l, 0.f, [](float a, float b) { return a + b; });
+            if (lane < W) red[w4 * W + lane] = r;
             named_bar_sync(bar_id, 128);
             if (me < W && q0 + me < it.nq) {
                 const float m = lim[me] == kNoMax ? kNoMax : sub[me] + kShift;
-                const float s = (red[me] + red[32 + me]) + (red[64 + me] + red[96 + me]);
+                const float s = (red[me] + red[W + me]) + (red[2 * W + me] + red[3 * W + me]);
                 *reinterpret_cast<float2*>(p.ml + (slot0 + me) * 2) = make_float2(m, s);
             }
             __syncwarp();
