@@ -35,18 +35,20 @@ __device__ __forceinline__ float2 join_ml(const AttendParams& p, int64_t slot0, 
     return make_float2(m, l);
 }
 
-// Blocks 0 .. rows * heads - 1: one (row, head) each, its chunks dealt to the warps in turn and
-// the warps' sums added in order.  The others: kWeightTokens slots of one (sequence, KV head)
-// each, taken in turn by however many blocks there are.
+// The first weight_blocks blocks: kWeightTokens slots of one (sequence, KV head) each, taken in turn by
+// however many blocks there are.  They are the long ones, so they start first and the others fill
+// in beside them.  The others: one (row, head) each, its chunks dealt to the warps in turn and the
+// warps' sums added in order.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) attend_join(const AttendParams p, int out_blocks) {
+__global__ void __launch_bounds__(kJoinThreads) attend_join(const AttendParams p, int weight_blocks) {
     extern __shared__ float jsm[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     griddep_wait();  // the split kernel has finished and its partials are visible
-    if (static_cast<int>(blockIdx.x) < out_blocks) {
+    if (static_cast<int>(blockIdx.x) >= weight_blocks) {
+        const int block = blockIdx.x - weight_blocks;
         constexpr int E = D / 32;
         __shared__ int found;
-        const int h = blockIdx.x % p.heads, r = blockIdx.x / p.heads;
+        const int h = block % p.heads, r = block / p.heads;
         if (tid == 0) found = -1;
         __syncthreads();
         for (int a = tid; a < p.agents; a += kJoinThreads) {
@@ -90,12 +92,12 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join(const AttendParams p
 #pragma unroll
             for (int w = 0; w < kJoinWarps; ++w) v += jsm[w * D + tid];
             v = m == kNoMax ? 0.f : v / l;
-            const int64_t at = static_cast<int64_t>(blockIdx.x) * D + tid;
+            const int64_t at = static_cast<int64_t>(block) * D + tid;
             if (p.out_type == QMM_TYPE_F32) static_cast<float*>(p.out)[at] = v;
             else if (p.out_type == QMM_TYPE_F16) static_cast<__half*>(p.out)[at] = __float2half_rn(v);
             else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
         }
-        if (tid == 0 && p.lse) p.lse[blockIdx.x] = m == kNoMax ? kNoMax : (m - kShift + log2f(l)) * 0.6931471805599453f;
+        if (tid == 0 && p.lse) p.lse[block] = m == kNoMax ? kNoMax : (m - kShift + log2f(l)) * 0.6931471805599453f;
         return;
     }
 
@@ -104,7 +106,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join(const AttendParams p
     float* inv = jsm + p.qp;    // [qp] 1 / l
     const int per = (p.cap + kWeightTokens - 1) / kWeightTokens;
     const int64_t all = static_cast<int64_t>(p.agents) * p.kv_heads * per;
-    for (int64_t b = blockIdx.x - out_blocks; b < all; b += gridDim.x - out_blocks) {
+    for (int64_t b = blockIdx.x; b < all; b += weight_blocks) {
         const int ag = static_cast<int>(b / per), t0 = static_cast<int>(b % per) * kWeightTokens;
         const int4 info = p.info[ag / p.kv_heads];
         if (t0 >= info.x) continue;  // past the sequence's longest row, or a refused sequence (-1)
@@ -137,17 +139,47 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join(const AttendParams p
         __syncthreads();
         const int64_t base = static_cast<int64_t>(ag) * p.cap, plane = static_cast<int64_t>(p.chunks) * p.chunk;
         const float4* x0 = reinterpret_cast<const float4*>(p.scores) + ag * (p.qp >> 2) * plane;
-        for (int t = t0 + tid; t < t0 + kWeightTokens && t < info.x; t += kJoinThreads) {
-            float sum = 0.f;
-#pragma unroll 4
-            for (int q = 0; q < nq; q += 4) {
-                const float4 v = __ldcs(x0 + (q >> 2) * plane + t);
-                sum = fmaf(ex2(v.x - ref[q]), inv[q], sum);
-                if (q + 1 < nq) sum = fmaf(ex2(v.y - ref[q + 1]), inv[q + 1], sum);
-                if (q + 2 < nq) sum = fmaf(ex2(v.z - ref[q + 2]), inv[q + 2], sum);
-                if (q + 3 < nq) sum = fmaf(ex2(v.w - ref[q + 3]), inv[q + 3], sum);
+        // kWeightTokens / kJoinThreads tokens a thread at once: their loads are in flight together and share
+        // the queries' numbers.  (A token past info.x takes the last one's scores and stores nothing.)
+        constexpr int T = kWeightTokens / kJoinThreads;
+        const float4* x[T];
+        float sum[T];
+#pragma unroll
+        for (int i = 0; i < T; ++i) {
+            const int t = t0 + tid + i * kJoinThreads;
+            x[i] = x0 + (t < info.x ? t : info.x - 1);
+            sum[i] = 0.f;
+        }
+#pragma unroll 2
+        for (int q = 0; q < (nq & ~3); q += 4) {
+            const float4 r = *reinterpret_cast<const float4*>(ref + q), w = *reinterpret_cast<const float4*>(inv + q);
+            float4 v[T];
+#pragma unroll
+            for (int i = 0; i < T; ++i) v[i] = __ldcs(x[i] + (q >> 2) * plane);
+#pragma unroll
+            for (int i = 0; i < T; ++i) {
+                sum[i] = fmaf(ex2(v[i].x - r.x), w.x, sum[i]);
+                sum[i] = fmaf(ex2(v[i].y - r.y), w.y, sum[i]);
+                sum[i] = fmaf(ex2(v[i].z - r.z), w.z, sum[i]);
+                sum[i] = fmaf(ex2(v[i].w - r.w), w.w, sum[i]);
             }
-            p.weight_out[base + t] = p.weight_in ? p.weight_in[base + t] + sum : sum;
+        }
+        if (nq & 3) {
+            const int q = nq & ~3;
+            float4 v[T];
+#pragma unroll
+            for (int i = 0; i < T; ++i) v[i] = __ldcs(x[i] + (q >> 2) * plane);
+#pragma unroll
+            for (int i = 0; i < T; ++i) {
+                sum[i] = fmaf(ex2(v[i].x - ref[q]), inv[q], sum[i]);
+                if ((nq & 3) > 1) sum[i] = fmaf(ex2(v[i].y - ref[q + 1]), inv[q + 1], sum[i]);
+                if ((nq & 3) > 2) sum[i] = fmaf(ex2(v[i].z - ref[q + 2]), inv[q + 2], sum[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < T; ++i) {
+            const int t = t0 + tid + i * kJoinThreads;
+            if (t < info.x) p.weight_out[base + t] = p.weight_in ? p.weight_in[base + t] + sum[i] : sum[i];
         }
     }
 }
@@ -246,7 +278,7 @@ cudaError_t launch_join(const AttendParams& p, int sms, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attend_join<D>, p, out_blocks);
+    return cudaLaunchKernelEx(&cfg, attend_join<D>, p, static_cast<int>(weight_blocks));
 }
 
 }  // namespace
