@@ -57,6 +57,7 @@ struct TcGeo {
     static constexpr int threads = 128 * (1 + groups + (q8 ? 1 : 0));
     static constexpr int half = q8 ? 2 * kQ8Half : kTcTile * 256;  // bytes of a tile's K or V
     static constexpr int k_slots = q8 ? 4 : 2, v_slots = q8 ? 4 : 3;  // (K's are free again once S is formed)
+    static constexpr int p_bufs = N == 48 ? 1 : 2;                 // (no room for two beside three V tiles: bf16 8 x 16,000 101 us with V's third, 106 with P's second)
     static constexpr int opnd = N * 256;                           // bytes of a B operand: N rows of 128 16-bit values
     // tensor memory columns: scores (one set per 32-dim block of a q8_0 pool), outputs (2 N: those of P's
     // high and of its low parts), and the A operands
@@ -65,8 +66,8 @@ struct TcGeo {
     // shared memory, after aligning to 1024
     static constexpr int off_v = k_slots * half;
     static constexpr int off_q = (off_v + v_slots * half + 1023) / 1024 * 1024;  // two
-    static constexpr int off_p = off_q + 2 * opnd;                              // per 64 tokens: N rows of high parts, N of low ones
-    static constexpr int off_dv = off_p + 2 * opnd;                             // q8_0: normalised V scales [2][4][128] fp16
+    static constexpr int off_p = off_q + 2 * opnd;                              // p_bufs, each 2 N / 32 blocks of [token][32 queries]: high parts, then low ones
+    static constexpr int off_dv = off_p + p_bufs * 2 * opnd;                             // q8_0: normalised V scales [2][4][128] fp16
     static constexpr int off_len = off_dv + (q8 ? 2 * 4 * kTcTile * 2 : 0);         // [2][N] tokens that a query sees
     static constexpr int off_lim = off_len + 2 * N * 4;                         // [N] reference + slack
     static constexpr int off_sub = off_lim + N * 4;                             // [N] reference - kTcShift
@@ -74,9 +75,9 @@ struct TcGeo {
     static constexpr int off_red = off_alpha + N * 4;                           // [group][4 warps][W]
     static constexpr int off_odd = off_red + 4 * N * 4;                         // [4] tokens to be taken query by query
     static constexpr int off_bar = off_odd + 16;
-    static constexpr int bars = 2 * k_slots + 2 * v_slots + 4 + 4 + 4 + 2;
+    static constexpr int bars = 2 * k_slots + 2 * v_slots + 4 + 6 + 4 + 2;
     static constexpr int off_item = (off_bar + bars * 8 + 15) / 16 * 16;        // [2] of ItemRec
-    static constexpr int off_misc = off_item + 2 * 32;                          // tmp[33], abort, accumulate, tmem, miss[v_slots], dead and missed by group
+    static constexpr int off_misc = off_item + 2 * 32;                          // tmp[33], abort, accumulate[2], tmem, miss[v_slots], dead and missed by group
     static constexpr int off_seq = (off_misc + 48 * 4 + 15) / 16 * 16;
     static constexpr int smem(int agents) { return 1024 + off_seq + (agents + 1) * 16; }
 };
@@ -86,6 +87,15 @@ struct TcGeo {
 __device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t saddr, uint32_t lead) {
     return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
            (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+// The same of one in the 64-byte swizzle: atoms of 32 elements (64 bytes) x 8 rows, 512 to the next 8 rows.
+__device__ __forceinline__ uint64_t smem_desc_sw64_mn(uint32_t saddr, uint32_t lead) {
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
+           (static_cast<uint64_t>(512 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(4) << 61);
+}
+// Byte of (token, column) of P: 64-byte rows by token, in blocks of 32 columns.
+__device__ __forceinline__ int p_byte(int token, int col) {
+    return (col >> 5) * (kTcTile * 64) + token * 64 + ((((col >> 3) & 3) ^ ((token >> 1) & 3)) << 4) + (col & 7) * 2;
 }
 
 __device__ __forceinline__ uint32_t order_bits(float v) {
@@ -182,14 +192,14 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
     uint64_t* vfull = kempty + G::k_slots;
     uint64_t* vempty = vfull + G::v_slots;
     uint64_t *qfull = vempty + G::v_slots, *qempty = qfull + 2;                          // two each
-    uint64_t *sfull = qempty + 2, *sempty = sfull + 1, *pfull = sfull + 2, *odone = sfull + 3;
-    uint64_t *akfull = sfull + 4, *akfree = sfull + 5, *avfull = sfull + 6, *avfree = sfull + 7, *drained = sfull + 8,
-             *oddread = sfull + 9;
+    uint64_t *sfull = qempty + 2, *sempty = sfull + 1, *pfull = sfull + 2, *odone = sfull + 4;  // (pfull and odone: two each)
+    uint64_t *akfull = sfull + 6, *akfree = sfull + 7, *avfull = sfull + 8, *avfree = sfull + 9, *drained = sfull + 10,
+             *oddread = sfull + 11;
     int* tmp = reinterpret_cast<int*>(sm + G::off_misc);
     volatile int* abort_flag = tmp + 33;
-    volatile int* accum_sm = tmp + 34;  // the outputs hold something that the next product adds to
-    uint32_t* tmem_sm = reinterpret_cast<uint32_t*>(tmp + 35);
-    volatile int* vmiss = tmp + 36;     // [v_slots]: a page of the tile is outside the pool
+    volatile int* accum_sm = tmp + 34;  // [2]: the outputs hold something that P's product adds to
+    uint32_t* tmem_sm = reinterpret_cast<uint32_t*>(tmp + 36);
+    volatile int* vmiss = tmp + 37;     // [v_slots <= 4]: a page of the tile is outside the pool
     int4* seq = reinterpret_cast<int4*>(sm + G::off_seq);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -208,8 +218,10 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
         }
         mbar_init(sfull, 1);
         mbar_init(sempty, 4 * G::groups);
-        mbar_init(pfull, 4 * G::groups);
-        mbar_init(odone, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(pfull + i, 4 * G::groups);
+            mbar_init(odone + i, 1);
+        }
         mbar_init(akfull, 4);
         mbar_init(akfree, 1);
         mbar_init(avfull, 4);
@@ -220,7 +232,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
         fence_mbar_init();
     }
     if (tid < 4) odd_sm[tid] = 0;
-    if (tid < 6) tmp[40 + tid] = -(tid & 1);
+    if (tid < 6) tmp[41 + tid] = -(tid & 1);
     if (warp == 1) {
         tmem_alloc(tmem_sm, G::cols);
         tmem_relinquish();
@@ -319,31 +331,33 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
         // ---------------------------------------------------------------- products
         constexpr uint32_t kType = BF ? (1u << 7) | (1u << 10) : 0u;
         constexpr uint32_t kIdescS = idesc_f16_f32(128, N) | kType;
-        // (both parts of P at once: 2 N columns; 16-bit pools: A is M-contiguous)
-        constexpr uint32_t kIdescO = idesc_f16_f32(128, 2 * N) | kType | (G::q8 ? 0u : 1u << 15);
+        // (both parts of P at once: 2 N columns; B is N-contiguous and, of 16-bit pools, A M-contiguous)
+        constexpr uint32_t kIdescO = idesc_f16_f32(128, 2 * N) | kType | 1u << 16 | (G::q8 ? 0u : 1u << 15);
+        constexpr uint32_t kIdescL = idesc_f16_f32(128, N) | kType | 1u << 16;
         int t = 0, k = 0;  // tiles and items so far
-        const uint64_t bp = smem_desc_sw128(smem_u32(sm + G::off_p));
+        const uint64_t bp = smem_desc_sw64_mn(smem_u32(sm + G::off_p), kTcTile * 64);
         auto product_o = [&](int i) {
-            await_warp(pfull, i & 1);
+            await_warp(pfull + i % G::p_bufs, (i / G::p_bufs) & 1);
             const int vs = i % G::v_slots;
             if constexpr (G::q8) await_warp(avfull, i & 1);
             else await_warp(vfull + vs, (i / G::v_slots) & 1);
             if (!live) return;
             tc_fence_after();
             const uint64_t av = smem_desc_sw128_mn(smem_u32(sm + G::off_v) + vs * G::half, kTcTile * 128);
-            const uint32_t acc = *accum_sm != 0;
+            const uint32_t acc = accum_sm[i % G::p_bufs] != 0;
+            const uint64_t bi = bp + i % G::p_bufs * (2 * G::opnd >> 4);
             if (elect_one()) {
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks) {
-                    const uint64_t b = bp + (((ks >> 2) * (2 * N * 128) + (ks & 3) * 32) >> 4);
+                    const uint64_t b = bi + (ks * 1024 >> 4);
                     if constexpr (G::q8) {
                         tc_mma_f16_ts(tmem + G::col_o, tmem + G::col_vh + 8 * ks, b, kIdescO, ks ? 1 : acc);
-                        tc_mma_f16_ts(tmem + G::col_o, tmem + G::col_vl + 8 * ks, b, kIdescS, 1);  // (by the high parts only)
+                        tc_mma_f16_ts(tmem + G::col_o, tmem + G::col_vl + 8 * ks, b, kIdescL, 1);  // (by the high parts only)
                     } else {
                         tc_mma_f16_ss(tmem + G::col_o, av + ks * (2048 >> 4), b, kIdescO, ks ? 1 : acc);
                     }
                 }
-                tc_commit(odone);
+                tc_commit(odone + i % G::p_bufs);
                 tc_commit(G::q8 ? avfree : vempty + vs);
             }
             __syncwarp();
@@ -435,7 +449,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
         float* sub = sub_sm + c0;
         float* alpha = alpha_sm + c0;
         float* red = red_sm + grp * 4 * W;     // [4][W]
-        volatile int* dead = tmp + 40 + 2 * grp;    // some thread's wait ran out
+        volatile int* dead = tmp + 41 + 2 * grp;    // some thread's wait ran out
         volatile int* missed = dead + 1;            // the last tile with a missing page
         int t = 0, k = 0;
         uint32_t odds = 0;                     // tiles with marked tokens so far
@@ -562,11 +576,14 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                 }
                 const bool edge = miss || tb + kTcTile > it.minlen;
                 const bool fresh = tb == it.tok0;  // the outputs hold nothing yet
-                if (t > 0) {
-                    await(odone, (t - 1) & 1);  // the last tile's P is read and its outputs are summed
+                // (the last product's outputs: only a new reference or a marked token has to wait for them)
+                auto outputs = [&] {
+                    await(odone + (t - 1) % G::p_bufs, ((t - 1) / G::p_bufs) & 1);
                     tc_fence_after();
-                }
+                };
+                if (t >= G::p_bufs) await(odone + t % G::p_bufs, (t / G::p_bufs - 1) & 1);  // this buffer's last P is read
                 if (moved && !fresh) {
+                    outputs();
 #pragma unroll
                     for (int c = 0; c < W; c += 8) {
                         float v[2][8];
@@ -580,10 +597,10 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                     }
                     tc_wait_st();
                 }
-                // ---- probabilities, as rows of the B operand (tokens contiguous, swizzled)
+                // ---- probabilities, as the token's rows of the B operand (queries contiguous, swizzled): 16-byte
+                // stores; with tokens contiguous they were 2-byte ones, 32 of a q8_0 thread's
                 const float inv = G::q8 ? __int_as_float((127 - static_cast<int>(e)) << 23) : 1.f;  // 2^-e
-                uint8_t* pbase = sm + G::off_p + (me >> 6) * (2 * N * 128) + c0 * 128 + (me & 7) * 2;
-                const int chunk = (me & 63) >> 3;
+                uint8_t* pt = sm + G::off_p + t % G::p_bufs * (2 * G::opnd);
                 // (all of them before the first store, which the compiler may not load past)
 #pragma unroll
                 for (int q = 0; q < W; q += 4) {
@@ -592,17 +609,14 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                     x[q + 2] = ex2(x[q + 2] - m.z), x[q + 3] = ex2(x[q + 3] - m.w);
                 }
 #pragma unroll
-                for (int q = 0; q < W; q += 2) {
-                    l[q] = G::q8 ? fmaf(x[q], inv, l[q]) : l[q] + x[q];
-                    l[q + 1] = G::q8 ? fmaf(x[q + 1], inv, l[q + 1]) : l[q + 1] + x[q + 1];
-                    uint32_t hi, lo;
-                    split2_scaled<BF>(x[q], x[q + 1], hi, lo);
-                    uint8_t* at = pbase + q * 128 + ((chunk ^ (q & 7)) << 4);  // (c0 is a multiple of 8)
-                    uint8_t* bt = pbase + (q + 1) * 128 + ((chunk ^ ((q + 1) & 7)) << 4);
-                    *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(hi);
-                    *reinterpret_cast<uint16_t*>(bt) = static_cast<uint16_t>(hi >> 16);
-                    *reinterpret_cast<uint16_t*>(at + N * 128) = static_cast<uint16_t>(lo);
-                    *reinterpret_cast<uint16_t*>(bt + N * 128) = static_cast<uint16_t>(lo >> 16);
+                for (int q = 0; q < W; q += 8) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) l[q + i] = G::q8 ? fmaf(x[q + i], inv, l[q + i]) : l[q + i] + x[q + i];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) split2_scaled<BF>(x[q + 2 * i], x[q + 2 * i + 1], hi[i], lo[i]);
+                    *reinterpret_cast<uint4*>(pt + p_byte(me, c0 + q)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(pt + p_byte(me, N + c0 + q)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
                 bool holds = !fresh;
                 if (edge) {
@@ -633,7 +647,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                         const uint32_t who = __ballot_sync(0xffffffffu, odd);
                         if (lane == 0) odd_sm[w4] = who;  // (all groups write the same)
                         named_bar_sync(bar_id, 128);
-                        const uint16_t* P = reinterpret_cast<const uint16_t*>(sm + G::off_p);
+                        if (holds) outputs();
 #pragma unroll 1
                         for (int c = 0; c < W; c += 8) {
                             float v[8];
@@ -665,8 +679,9 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                                 }
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) {
-                                    const int q = c + i, at = (j >> 6) * (2 * N * 64) + (c0 + q) * 64 + ((((j & 63) >> 3) ^ (q & 7)) << 3) + (j & 7);
-                                    const uint32_t h = P[at], u = P[at + N * 64];
+                                    const int q = c + i;
+                                    const uint32_t h = *reinterpret_cast<const uint16_t*>(pt + p_byte(j, c0 + q));
+                                    const uint32_t u = *reinterpret_cast<const uint16_t*>(pt + p_byte(j, N + c0 + q));
                                     const float ph = BF ? __uint_as_float(h << 16) : __half2float(__ushort_as_half(static_cast<uint16_t>(h)));
                                     const float pl = BF ? __uint_as_float(u << 16) : __half2float(__ushort_as_half(static_cast<uint16_t>(u)));
                                     const float pr = fmaf(pl, 1.f / kLowScale, ph);
@@ -690,19 +705,19 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                             for (int c = 0; c < 16; ++c) *piece(c) = make_uint4(0, 0, 0, 0);
                     }
                 }
-                if (me == 0 && grp == 0) *accum_sm = holds;
+                if (me == 0 && grp == 0) accum_sm[t % G::p_bufs] = holds;
                 fence_proxy_async_smem();  // P and V, before the tensor cores read them
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(pfull);
+                    mbar_arrive(pfull + t % G::p_bufs);
                     if constexpr (G::q8) mbar_arrive(vempty + vs);
                 }
             }
             if (stop) break;
 
             // ---- the item's partial: a dim per thread
-            await(odone, (t - 1) & 1);
+            await(odone + (t - 1) % G::p_bufs, ((t - 1) / G::p_bufs) & 1);
             tc_fence_after();
             const int64_t slot0 = (static_cast<int64_t>(it.a * p.kv_heads + it.g) * p.chunks + it.tok0 / p.chunk) * p.qp + q0;
             float* po = p.o + slot0 * D + me;
