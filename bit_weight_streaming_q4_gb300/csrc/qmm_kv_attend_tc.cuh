@@ -60,7 +60,8 @@ struct TcGeo {
     static constexpr int p_bufs = N == 48 ? 1 : 2;                 // (no room for two beside three V tiles: bf16 8 x 16,000 101 us with V's third, 106 with P's second)
     static constexpr int opnd = N * 256;                           // bytes of a B operand: N rows of 128 16-bit values
     // tensor memory columns: scores (one set per 32-dim block of a q8_0 pool), outputs (2 N: those of P's
-    // high and of its low parts), and the A operands
+    // high and of its low parts; of 16-bit pools two sets, items in turn), and the A operands
+    static constexpr int o_bufs = q8 ? 1 : 2;
     static constexpr int col_s = 0, col_o = q8 ? 4 * N : 64, col_k = 288, col_vh = 352, col_vl = 416;
     static constexpr int cols = q8 ? 512 : 256;
     // shared memory, after aligning to 1024
@@ -171,8 +172,10 @@ struct alignas(16) ItemRec {
     int q0, nq, minlen, r0;  // first query, queries of the sequence and KV head, the sequence's shortest row and first row
 };
 
+// (512: at most 128 registers, so that with 384 threads a block of the joining kernel, 48 registers by 256
+// threads, fits beside and has begun when the partials are there; without room it cost 2 us a call)
 template <int FMT, int N>
-__global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
+__global__ void __launch_bounds__((TcGeo<FMT, N>::threads > 512 ? TcGeo<FMT, N>::threads : 512), 1)
     attend_partial_tc(const __grid_constant__ CUtensorMap map, const __grid_constant__ AttendParams p) {
     using G = TcGeo<FMT, N>;
     constexpr bool BF = FMT == QMM_KV_BF16;
@@ -336,7 +339,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
         constexpr uint32_t kIdescL = idesc_f16_f32(128, N) | kType | 1u << 16;
         int t = 0, k = 0;  // tiles and items so far
         const uint64_t bp = smem_desc_sw64_mn(smem_u32(sm + G::off_p), kTcTile * 64);
-        auto product_o = [&](int i) {
+        auto product_o = [&](int i, int item_no) {
             await_warp(pfull + i % G::p_bufs, (i / G::p_bufs) & 1);
             const int vs = i % G::v_slots;
             if constexpr (G::q8) await_warp(avfull, i & 1);
@@ -345,16 +348,17 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
             tc_fence_after();
             const uint64_t av = smem_desc_sw128_mn(smem_u32(sm + G::off_v) + vs * G::half, kTcTile * 128);
             const uint32_t acc = accum_sm[i % G::p_bufs] != 0;
+            const uint32_t o = tmem + G::col_o + item_no % G::o_bufs * (2 * N);
             const uint64_t bi = bp + i % G::p_bufs * (2 * G::opnd >> 4);
             if (elect_one()) {
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks) {
                     const uint64_t b = bi + (ks * 1024 >> 4);
                     if constexpr (G::q8) {
-                        tc_mma_f16_ts(tmem + G::col_o, tmem + G::col_vh + 8 * ks, b, kIdescO, ks ? 1 : acc);
-                        tc_mma_f16_ts(tmem + G::col_o, tmem + G::col_vl + 8 * ks, b, kIdescL, 1);  // (by the high parts only)
+                        tc_mma_f16_ts(o, tmem + G::col_vh + 8 * ks, b, kIdescO, ks ? 1 : acc);
+                        tc_mma_f16_ts(o, tmem + G::col_vl + 8 * ks, b, kIdescL, 1);  // (by the high parts only)
                     } else {
-                        tc_mma_f16_ss(tmem + G::col_o, av + ks * (2048 >> 4), b, kIdescO, ks ? 1 : acc);
+                        tc_mma_f16_ss(o, av + ks * (2048 >> 4), b, kIdescO, ks ? 1 : acc);
                     }
                 }
                 tc_commit(odone + i % G::p_bufs);
@@ -389,10 +393,10 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                     if (last) tc_commit(qempty + (k & 1));
                 }
                 __syncwarp();
-                if (t > 0) product_o(t - 1);
+                if (t > 0) product_o(t - 1, tb == tok0 ? k - 1 : k);
             }
         }
-        if (t > 0 && live) product_o(t - 1);
+        if (t > 0 && live) product_o(t - 1, k - 1);
         // every product issued has finished before the tensor memory is released
         if (elect_one()) tc_commit(drained);
         volatile int go_on = 0;
@@ -453,12 +457,32 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
         volatile int* missed = dead + 1;            // the last tile with a missing page
         int t = 0, k = 0;
         uint32_t odds = 0;                     // tiles with marked tokens so far
+        auto last_product = [&] { await(odone + (t - 1) % G::p_bufs, ((t - 1) / G::p_bufs) & 1); };  // of tile t - 1
+        // The outputs of an item as its partial, a dim per thread.  With two sets of them that waits until the
+        // next item's first probabilities are out, so that the tensor cores have work meanwhile.
+        float* po = nullptr;                   // where they go, or null
+        int left = 0;                          // queries from c0 on
+        auto drain = [&](uint32_t cols) {
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < W; c += 8) {
+                float v[2][8];
+                tmem_load8(cols + c, v[0]);
+                tmem_load8(cols + N + c, v[1]);
+                tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (c + i < left) po[(c + i) * D] = fmaf(v[1][i], 1.f / kLowScale, v[0][i]);
+            }
+            po = nullptr;
+        };
         // (what ends the loops is voted on, so that the warps always meet at the same barriers)
         for (int item = blockIdx.x; item < total; item += gridDim.x, ++k) {
             await(qfull + (k & 1), (k >> 1) & 1);
             const ItemRec it = item_sm[k & 1];
             const int* qlen = qlen_sm + (k & 1) * N + c0;
             const int q0 = it.q0 + c0;
+            const uint32_t ocol = lanes + G::col_o + k % G::o_bufs * (2 * N) + c0;  // the item's outputs
             float l[W];
 #pragma unroll
             for (int q = 0; q < W; ++q) l[q] = 0.f;
@@ -549,6 +573,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                 if (bar_or(bar_id, 128, over)) {
                     if (*dead) {
                         stop = true;
+                        po = nullptr;
                         break;
                     }
                     miss = *missed == t;
@@ -576,24 +601,20 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                 }
                 const bool edge = miss || tb + kTcTile > it.minlen;
                 const bool fresh = tb == it.tok0;  // the outputs hold nothing yet
-                // (the last product's outputs: only a new reference or a marked token has to wait for them)
-                auto outputs = [&] {
-                    await(odone + (t - 1) % G::p_bufs, ((t - 1) / G::p_bufs) & 1);
-                    tc_fence_after();
-                };
                 if (t >= G::p_bufs) await(odone + t % G::p_bufs, (t / G::p_bufs - 1) & 1);  // this buffer's last P is read
                 if (moved && !fresh) {
-                    outputs();
+                    last_product();  // (only a new reference or a marked token needs its outputs)
+                    tc_fence_after();
 #pragma unroll
                     for (int c = 0; c < W; c += 8) {
                         float v[2][8];
-                        tmem_load8(lanes + G::col_o + c0 + c, v[0]);
-                        tmem_load8(lanes + G::col_o + N + c0 + c, v[1]);
+                        tmem_load8(ocol + c, v[0]);
+                        tmem_load8(ocol + N + c, v[1]);
                         tc_wait_ld();
 #pragma unroll
                         for (int i = 0; i < 8; ++i) v[0][i] *= alpha[c + i], v[1][i] *= alpha[c + i];
-                        tmem_store8(lanes + G::col_o + c0 + c, v[0]);
-                        tmem_store8(lanes + G::col_o + N + c0 + c, v[1]);
+                        tmem_store8(ocol + c, v[0]);
+                        tmem_store8(ocol + N + c, v[1]);
                     }
                     tc_wait_st();
                 }
@@ -647,12 +668,15 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                         const uint32_t who = __ballot_sync(0xffffffffu, odd);
                         if (lane == 0) odd_sm[w4] = who;  // (all groups write the same)
                         named_bar_sync(bar_id, 128);
-                        if (holds) outputs();
+                        if (holds) {
+                            last_product();
+                            tc_fence_after();
+                        }
 #pragma unroll 1
                         for (int c = 0; c < W; c += 8) {
                             float v[8];
                             if (holds) {
-                                tmem_load8(lanes + G::col_o + c0 + c, v);
+                                tmem_load8(ocol + c, v);
                                 tc_wait_ld();
                             } else {
 #pragma unroll
@@ -688,10 +712,10 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                                     if (tb + j < qlen[q]) v[i] = fmaf(pr, y, v[i]);
                                 }
                             }
-                            tmem_store8(lanes + G::col_o + c0 + c, v);
+                            tmem_store8(ocol + c, v);
                             if (!holds) {
                                 const float zero[8] = {};
-                                tmem_store8(lanes + G::col_o + N + c0 + c, zero);
+                                tmem_store8(ocol + N + c, zero);
                             }
                         }
                         tc_wait_st();
@@ -713,23 +737,20 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
                     mbar_arrive(pfull + t % G::p_bufs);
                     if constexpr (G::q8) mbar_arrive(vempty + vs);
                 }
+                if (G::o_bufs == 2 && po) {  // the last item's outputs (with one buffer of P its products are waited for above)
+                    if (G::p_bufs == 2) last_product();
+                    drain(lanes + G::col_o + (k - 1) % 2 * (2 * N) + c0);
+                }
             }
             if (stop) break;
 
-            // ---- the item's partial: a dim per thread
-            await(odone + (t - 1) % G::p_bufs, ((t - 1) / G::p_bufs) & 1);
-            tc_fence_after();
+            // ---- the item's partial
             const int64_t slot0 = (static_cast<int64_t>(it.a * p.kv_heads + it.g) * p.chunks + it.tok0 / p.chunk) * p.qp + q0;
-            float* po = p.o + slot0 * D + me;
-#pragma unroll
-            for (int c = 0; c < W; c += 8) {
-                float v[2][8];
-                tmem_load8(lanes + G::col_o + c0 + c, v[0]);
-                tmem_load8(lanes + G::col_o + N + c0 + c, v[1]);
-                tc_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (q0 + c + i < it.nq) po[(c + i) * D] = fmaf(v[1][i], 1.f / kLowScale, v[0][i]);
+            po = p.o + slot0 * D + me;
+            left = it.nq - q0;
+            if (G::o_bufs == 1) {
+                last_product();
+                drain(ocol);
             }
             tc_fence_before();
             const float r = reduce_columns<W>(l, 0.f, [](float a, float b) { return a + b; });
@@ -743,6 +764,10 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads), 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(qempty + (k & 1));
             named_bar_sync(bar_id, 128);  // (the sums and references are read)
+        }
+        if (po) {
+            last_product();
+            if (__all_sync(0xffffffffu, live)) drain(lanes + G::col_o + (k - 1) % 2 * (2 * N) + c0);
         }
         if (!live && me == 0) atomicOr(p.err, kErrTimeout);
     } else if (G::q8) {
