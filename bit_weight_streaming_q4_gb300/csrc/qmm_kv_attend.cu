@@ -167,8 +167,17 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join(const AttendParams p
         if (nq & 3) {
             const int q = nq & ~3;
             float4 v[T];
+            if ((nq & 3) == 3) {
 #pragma unroll
-            for (int i = 0; i < T; ++i) v[i] = __ldcs(x[i] + (q >> 2) * plane);
+                for (int i = 0; i < T; ++i) v[i] = __ldcs(x[i] + (q >> 2) * plane);
+            } else {  // (two a token)
+                const float2* x2 = reinterpret_cast<const float2*>(x0 + (q >> 2) * plane);
+#pragma unroll
+                for (int i = 0; i < T; ++i) {
+                    const float2 u = __ldcs(x2 + (x[i] - x0));
+                    v[i] = make_float4(u.x, u.y, 0.f, 0.f);
+                }
+            }
 #pragma unroll
             for (int i = 0; i < T; ++i) {
                 sum[i] = fmaf(ex2(v[i].x - ref[q]), inv[q], sum[i]);

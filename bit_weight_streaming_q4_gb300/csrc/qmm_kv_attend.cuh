@@ -57,7 +57,8 @@ struct AttendParams {
     float* lse;                 // [rows][heads] or null
     float* ml;                  // [sequence][KV head][chunk][qp][2]: M and l
     float* o;                   // [sequence][KV head][chunk][qp][D]
-    float* scores;              // [sequence][KV head][qp / 4][chunks * chunk][4], x_t; null without weights
+    float* scores;              // [sequence][KV head][qp / 4][chunks * chunk][4] x_t, or null without weights;
+                                // [..][2] in the last four if the sequence has at most two queries there
     int4* info;                 // [agents]: longest row (-1: refused), first row, rows, 0
     int* err;
     int64_t q_stride;
@@ -431,10 +432,12 @@ __global__ void __launch_bounds__(kThreads, (Geo<FMT, D, NT>::blocks))
                             if (tb + ta + 8 >= n) s[nt][2 + e] = kNoMax;
                         }
                     }
-                    if (sbase && q0 + 8 * nt < p.qp) {
-                        float* at = sbase + ((q0 >> 2) + 2 * nt + (t4 >> 1)) * plane + (tb + ta) * 4 + 2 * (t4 & 1);
+                    const int qi = q0 + 8 * nt + 2 * t4;
+                    if (sbase && qi < nq) {
+                        const int n = nq - (qi & ~3) > 2 ? 4 : 2;
+                        float* at = sbase + (qi >> 2) * plane + (tb + ta) * n + (qi & (n - 1));
                         *reinterpret_cast<float2*>(at) = make_float2(s[nt][0], s[nt][1]);
-                        *reinterpret_cast<float2*>(at + 32) = make_float2(s[nt][2], s[nt][3]);
+                        *reinterpret_cast<float2*>(at + 8 * n) = make_float2(s[nt][2], s[nt][3]);
                     }
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {

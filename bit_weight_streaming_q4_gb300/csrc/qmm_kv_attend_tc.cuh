@@ -493,7 +493,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads > 512 ? TcGeo<FMT, N>:
             named_bar_sync(bar_id, 128);
             const int64_t plane = static_cast<int64_t>(p.chunks) * p.chunk * 4;
             float* sbase = p.scores ? p.scores + (static_cast<int64_t>(it.a * p.kv_heads + it.g) * (p.qp >> 2) + (q0 >> 2)) * plane : nullptr;
-            const int planes = (it.nq - q0 + 3) >> 2;
+            const int mine = it.nq - q0;  // queries from c0 on
 
             bool stop = false;
             for (int tb = it.tok0; tb < it.end; tb += kTcTile, ++t) {
@@ -557,8 +557,10 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads > 512 ? TcGeo<FMT, N>:
                 if (sbase) {
                     float* at = sbase + static_cast<int64_t>(tok) * 4;
 #pragma unroll
-                    for (int q = 0; q < W; q += 4)
-                        if ((q >> 2) < planes) *reinterpret_cast<float4*>(at + (q >> 2) * plane) = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
+                    for (int q = 0; q < W; q += 4) {
+                        if (q + 2 < mine) *reinterpret_cast<float4*>(at + (q >> 2) * plane) = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
+                        else if (q < mine) *reinterpret_cast<float2*>(at + (q >> 2) * plane - 2 * tok) = make_float2(x[q], x[q + 1]);
+                    }
                 }
                 bool over = !live || miss;
 #pragma unroll
