@@ -49,11 +49,12 @@ constexpr float kSlack = 6.f;     // .. and how far a score may pass its referen
 constexpr float kLowScale = 2048.f;  // p's low part is kept times this (its products have columns of their
                                      // own), so that 22 bits of p count down to 2^-33 of the reference's
 
-template <int FMT, int N>
+// Q: queries of a tile, of N columns.
+template <int FMT, int N, int Q>
 struct TcGeo {
     static constexpr bool q8 = FMT == QMM_KV_Q8_0;
     static constexpr int groups = N == 48 ? 3 : 2;                 // softmax groups of four warps
-    static constexpr int W = N / groups;                           // queries of a group
+    static constexpr int W = Q / groups, B = W % 8 ? W : 8;        // queries of a group, and of a read of tensor memory
     static constexpr int threads = 128 * (1 + groups + (q8 ? 1 : 0));
     static constexpr int half = q8 ? 2 * kQ8Half : kTcTile * 256;  // bytes of a tile's K or V
     static constexpr int k_slots = q8 ? 4 : 2, v_slots = q8 ? 4 : 3;  // (K's are free again once S is formed)
@@ -106,16 +107,37 @@ __device__ __forceinline__ uint32_t order_bits(float v) {
 __device__ __forceinline__ float from_order_bits(uint32_t o) { return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o); }
 
 // 8 consecutive columns of the thread's tensor memory lane (to be waited for with tc_wait_ld).
-__device__ __forceinline__ void tmem_load8(uint32_t taddr, float (&v)[8]) {
+__device__ __forceinline__ void tmem_load8(uint32_t taddr, float* v) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
                  : "r"(taddr)
                  : "memory");
 }
-__device__ __forceinline__ void tmem_store8(uint32_t taddr, const float (&v)[8]) {
+__device__ __forceinline__ void tmem_load4(uint32_t taddr, float* v) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                 : "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_store8(uint32_t taddr, const float* v) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "f"(v[0]),
                  "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                  : "memory");
+}
+__device__ __forceinline__ void tmem_store4(uint32_t taddr, const float* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3])
+                 : "memory");
+}
+template <int B>
+__device__ __forceinline__ void tmem_load_n(uint32_t taddr, float (&v)[B]) {
+    static_assert(B == 8 || B == 12);
+    tmem_load8(taddr, v);
+    if constexpr (B == 12) tmem_load4(taddr + 8, v + 8);
+}
+template <int B>
+__device__ __forceinline__ void tmem_store_n(uint32_t taddr, const float (&v)[B]) {
+    tmem_store8(taddr, v);
+    if constexpr (B == 12) tmem_store4(taddr + 8, v + 8);
 }
 
 // One lane of a converged warp.  (The products' operands stay in uniform registers inside its branch; by
@@ -174,10 +196,10 @@ struct alignas(16) ItemRec {
 
 // (512: at most 128 registers, so that with 384 threads a block of the joining kernel, 48 registers by 256
 // threads, fits beside and has begun when the partials are there; without room it cost 2 us a call)
-template <int FMT, int N>
-__global__ void __launch_bounds__((TcGeo<FMT, N>::threads > 512 ? TcGeo<FMT, N>::threads : 512), 1)
+template <int FMT, int N, int Q>
+__global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, N, Q>::threads : 512), 1)
     attend_partial_tc(const __grid_constant__ CUtensorMap map, const __grid_constant__ AttendParams p) {
-    using G = TcGeo<FMT, N>;
+    using G = TcGeo<FMT, N, Q>;
     constexpr bool BF = FMT == QMM_KV_BF16;
     constexpr int D = 128;
     extern __shared__ uint8_t sm_raw[];
@@ -241,7 +263,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads > 512 ? TcGeo<FMT, N>:
         tmem_relinquish();
     }
     tc_fence_before();
-    const int total = form_table(p, seq, tmp, N);
+    const int total = form_table(p, seq, tmp, Q);
     tc_fence_after();
     const uint32_t tmem = *tmem_sm;
 
@@ -272,7 +294,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads > 512 ? TcGeo<FMT, N>:
         Item ni = {};
         int npages = 0;
         if (nitem < total) {
-            ni = decode_item(p, seq, nitem, N);
+            ni = decode_item(p, seq, nitem, Q);
             npages = load_item_pages(p, ni);
         }
         while (nitem < total && live) {
@@ -280,7 +302,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads > 512 ? TcGeo<FMT, N>:
             const int pages = npages, first = it.tok0 >> p.page_shift;
             nitem += gridDim.x;
             if (nitem < total) {
-                ni = decode_item(p, seq, nitem, N);
+                ni = decode_item(p, seq, nitem, Q);
                 npages = load_item_pages(p, ni);
             }
             for (int tb = it.tok0; tb < it.end && live; tb += kTcTile, ++t) {
@@ -406,8 +428,8 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads > 512 ? TcGeo<FMT, N>:
         // ---------------------------------------------------------------- the next item: numbers and queries, half a warp per row
         int k = 0;
         for (int item = blockIdx.x; item < total && live; item += gridDim.x, ++k) {
-            const Item it = decode_item(p, seq, item, N);
-            const int r0 = seq[it.a].w, nq = (seq[it.a + 1].w - r0) * p.group, q0 = it.tile * N;
+            const Item it = decode_item(p, seq, item, Q);
+            const int r0 = seq[it.a].w, nq = (seq[it.a + 1].w - r0) * p.group, q0 = it.tile * Q;
             const int buf = k & 1, c = lane & 15;
             if (k > 1) await_warp(qempty + buf, ((k >> 1) - 1) & 1);
             if (!live) break;
@@ -444,7 +466,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads > 512 ? TcGeo<FMT, N>:
         }
     } else if (warp < 4 + 4 * G::groups) {
         // ---------------------------------------------------------------- softmax: a token per thread, then a dim
-        constexpr int W = G::W;
+        constexpr int W = G::W, B = G::B;
         const int grp = (warp - 4) >> 2, me = (tid - 128) & 127, w4 = warp & 3;
         const uint32_t bar_id = 1 + grp;       // the group's barrier
         const int c0 = grp * W;                // the group's first query of the tile
@@ -465,13 +487,13 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads > 512 ? TcGeo<FMT, N>:
         auto drain = [&](uint32_t cols) {
             tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < W; c += 8) {
-                float v[2][8];
-                tmem_load8(cols + c, v[0]);
-                tmem_load8(cols + N + c, v[1]);
+            for (int c = 0; c < W; c += B) {
+                float v[2][B];
+                tmem_load_n<B>(cols + c, v[0]);
+                tmem_load_n<B>(cols + N + c, v[1]);
                 tc_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
+                for (int i = 0; i < B; ++i)
                     if (c + i < left) po[(c + i) * D] = fmaf(v[1][i], 1.f / kLowScale, v[0][i]);
             }
             po = nullptr;
@@ -529,22 +551,22 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads > 512 ? TcGeo<FMT, N>:
                 float x[W];
                 if constexpr (G::q8) {
 #pragma unroll
-                    for (int c = 0; c < W; c += 8) {
-                        float v[4][8];
+                    for (int c = 0; c < W; c += B) {
+                        float v[4][B];
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) tmem_load8(lanes + G::col_s + b * N + c0 + c, v[b]);
+                        for (int b = 0; b < 4; ++b) tmem_load_n<B>(lanes + G::col_s + b * N + c0 + c, v[b]);
                         tc_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
+                        for (int i = 0; i < B; ++i)
                             x[c + i] = fmaf(v[3][i], f[3], fmaf(v[2][i], f[2], fmaf(v[1][i], f[1], v[0][i] * f[0]))) * p.c2;
                     }
                 } else {
-                    float v[W / 8][8];
+                    float v[W / B][B];
 #pragma unroll
-                    for (int c = 0; c < W / 8; ++c) tmem_load8(lanes + G::col_s + c0 + 8 * c, v[c]);
+                    for (int c = 0; c < W / B; ++c) tmem_load_n<B>(lanes + G::col_s + c0 + B * c, v[c]);
                     tc_wait_ld();
 #pragma unroll
-                    for (int q = 0; q < W; ++q) x[q] = v[q / 8][q % 8] * p.c2;
+                    for (int q = 0; q < W; ++q) x[q] = v[q / B][q % B] * p.c2;
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -608,15 +630,15 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads > 512 ? TcGeo<FMT, N>:
                     last_product();  // (only a new reference or a marked token needs its outputs)
                     tc_fence_after();
 #pragma unroll
-                    for (int c = 0; c < W; c += 8) {
-                        float v[2][8];
-                        tmem_load8(ocol + c, v[0]);
-                        tmem_load8(ocol + N + c, v[1]);
+                    for (int c = 0; c < W; c += B) {
+                        float v[2][B];
+                        tmem_load_n<B>(ocol + c, v[0]);
+                        tmem_load_n<B>(ocol + N + c, v[1]);
                         tc_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) v[0][i] *= alpha[c + i], v[1][i] *= alpha[c + i];
-                        tmem_store8(ocol + c, v[0]);
-                        tmem_store8(ocol + N + c, v[1]);
+                        for (int i = 0; i < B; ++i) v[0][i] *= alpha[c + i], v[1][i] *= alpha[c + i];
+                        tmem_store_n<B>(ocol + c, v[0]);
+                        tmem_store_n<B>(ocol + N + c, v[1]);
                     }
                     tc_wait_st();
                 }
@@ -632,14 +654,21 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads > 512 ? TcGeo<FMT, N>:
                     x[q + 2] = ex2(x[q + 2] - m.z), x[q + 3] = ex2(x[q + 3] - m.w);
                 }
 #pragma unroll
-                for (int q = 0; q < W; q += 8) {
-                    uint32_t hi[4], lo[4];
+                for (int q = 0; q < W; q += B == 8 ? 8 : 4) {
+                    constexpr int S = B == 8 ? 4 : 2;  // (12 columns begin in the middle of 16 bytes)
+                    uint32_t hi[S], lo[S];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) l[q + i] = G::q8 ? fmaf(x[q + i], inv, l[q + i]) : l[q + i] + x[q + i];
+                    for (int i = 0; i < 2 * S; ++i) l[q + i] = G::q8 ? fmaf(x[q + i], inv, l[q + i]) : l[q + i] + x[q + i];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) split2_scaled<BF>(x[q + 2 * i], x[q + 2 * i + 1], hi[i], lo[i]);
-                    *reinterpret_cast<uint4*>(pt + p_byte(me, c0 + q)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(pt + p_byte(me, N + c0 + q)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    for (int i = 0; i < S; ++i) split2_scaled<BF>(x[q + 2 * i], x[q + 2 * i + 1], hi[i], lo[i]);
+                    uint8_t *ph = pt + p_byte(me, c0 + q), *pl = pt + p_byte(me, N + c0 + q);
+                    if constexpr (S == 4) {
+                        *reinterpret_cast<uint4*>(ph) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4*>(pl) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    } else {
+                        *reinterpret_cast<uint2*>(ph) = make_uint2(hi[0], hi[1]);
+                        *reinterpret_cast<uint2*>(pl) = make_uint2(lo[0], lo[1]);
+                    }
                 }
                 bool holds = !fresh;
                 if (edge) {
@@ -675,14 +704,14 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads > 512 ? TcGeo<FMT, N>:
                             tc_fence_after();
                         }
 #pragma unroll 1
-                        for (int c = 0; c < W; c += 8) {
-                            float v[8];
+                        for (int c = 0; c < W; c += B) {
+                            float v[B];
                             if (holds) {
-                                tmem_load8(ocol + c, v);
+                                tmem_load_n<B>(ocol + c, v);
                                 tc_wait_ld();
                             } else {
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) v[i] = 0.f;
+                                for (int i = 0; i < B; ++i) v[i] = 0.f;
                             }
 #pragma unroll 1
                             for (int j = 0; j < kTcTile; ++j) {
@@ -704,7 +733,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads > 512 ? TcGeo<FMT, N>:
                                     y = BF ? __uint_as_float(u << 16) : __half2float(__ushort_as_half(static_cast<uint16_t>(u)));
                                 }
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) {
+                                for (int i = 0; i < B; ++i) {
                                     const int q = c + i;
                                     const uint32_t h = *reinterpret_cast<const uint16_t*>(pt + p_byte(j, c0 + q));
                                     const uint32_t u = *reinterpret_cast<const uint16_t*>(pt + p_byte(j, N + c0 + q));
@@ -714,10 +743,10 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads > 512 ? TcGeo<FMT, N>:
                                     if (tb + j < qlen[q]) v[i] = fmaf(pr, y, v[i]);
                                 }
                             }
-                            tmem_store8(ocol + c, v);
+                            tmem_store_n<B>(ocol + c, v);
                             if (!holds) {
-                                const float zero[8] = {};
-                                tmem_store8(ocol + N + c, zero);
+                                const float zero[B] = {};
+                                tmem_store_n<B>(ocol + N + c, zero);
                             }
                         }
                         tc_wait_st();
@@ -887,23 +916,24 @@ __global__ void __launch_bounds__((TcGeo<FMT, N>::threads > 512 ? TcGeo<FMT, N>:
     if (warp == 1) tmem_dealloc(tmem, G::cols);
 }
 
-template <int FMT, int N>
+template <int FMT, int N, int Q>
 cudaError_t launch_attend_tc_one(const AttendLaunch& a, cudaStream_t s) {
-    static_assert(TcGeo<FMT, N>::smem(kMaxAgents) <= kMaxShared);
-    const int bytes = TcGeo<FMT, N>::smem(a.p.agents);
+    using G = TcGeo<FMT, N, Q>;
+    static_assert(G::smem(kMaxAgents) <= kMaxShared);
     static Once once;
-    const cudaError_t e = once.allow_shared(attend_partial_tc<FMT, N>, a.device);
+    const cudaError_t e = once.allow_shared(attend_partial_tc<FMT, N, Q>, a.device);
     if (e != cudaSuccess) return e;
-    attend_partial_tc<FMT, N><<<a.sms, TcGeo<FMT, N>::threads, bytes, s>>>(a.map, a.p);
+    attend_partial_tc<FMT, N, Q><<<a.sms, G::threads, G::smem(a.p.agents), s>>>(a.map, a.p);
     return cudaGetLastError();
 }
 
-// The fewest columns that take all queries of a sequence, up to 48.
+// The fewest queries a tile that take all of a sequence's, up to 48.
 template <int FMT>
 cudaError_t launch_attend_tc(const AttendLaunch& a, cudaStream_t s) {
-    return a.max_q <= 16   ? launch_attend_tc_one<FMT, 16>(a, s)
-           : a.max_q <= 32 ? launch_attend_tc_one<FMT, 32>(a, s)
-                           : launch_attend_tc_one<FMT, 48>(a, s);
+    return a.max_q <= 16   ? launch_attend_tc_one<FMT, 16, 16>(a, s)
+           : a.max_q <= 24 ? launch_attend_tc_one<FMT, 32, 24>(a, s)
+           : a.max_q <= 32 ? launch_attend_tc_one<FMT, 32, 32>(a, s)
+                           : launch_attend_tc_one<FMT, 48, 48>(a, s);
 }
 
 }  // namespace kv
