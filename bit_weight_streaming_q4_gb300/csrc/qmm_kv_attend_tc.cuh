@@ -15,7 +15,7 @@
 //   warps 4 ..  softmax, two or three groups of four, a share of the queries each: scores from
 //               tensor memory, probabilities into shared memory as the second product's B operand,
 //               in two 16-bit parts
-//   last four   q8_0 only: K and V quants to fp16 in tensor memory, as A operands
+//   last four   q8_0 only: K and V quants to fp16 in tensor memory, as A operands (or eight, four for each)
 // 16-bit pools: the swizzled tiles are A operands as they come, K by rows and V transposed
 // (M-contiguous).  q8_0: K's quants are exact in fp16, one accumulator per 32-dim block takes its
 // scale in fp32.  V's scale depends on token and block: a token's exponent e_t = max over blocks of
@@ -55,7 +55,12 @@ struct TcGeo {
     static constexpr bool q8 = FMT == QMM_KV_Q8_0;
     static constexpr int groups = N == 48 ? 3 : 2;                 // softmax groups of four warps
     static constexpr int W = Q / groups, B = W % 8 ? W : 8;        // queries of a group, and of a read of tensor memory
-    static constexpr int threads = 128 * (1 + groups + (q8 ? 1 : 0));
+    // q8_0, few queries: K and V converted by warps of their own, waits asked for at once and references read
+    // early.  4 x 23,000 tokens with weights: 1 row 84 -> 82 us, 3 rows 98 -> 94.  At 32 and 48 queries, whose
+    // threads have too few registers for it, 5 rows would go from 108 to 125 and 8 from 136 to 158.
+    static constexpr bool eager = q8 && Q <= 24;
+    static constexpr int converters = !q8 ? 0 : eager ? 2 : 1;     // groups of four warps
+    static constexpr int threads = 128 * (1 + groups + converters);
     static constexpr int half = q8 ? 2 * kQ8Half : kTcTile * 256;  // bytes of a tile's K or V
     static constexpr int k_slots = q8 ? 4 : 2, v_slots = q8 ? 4 : 3;  // (K's are free again once S is formed)
     static constexpr int p_bufs = N == 48 ? 1 : 2;                 // (no room for two beside three V tiles: bf16 8 x 16,000 101 us with V's third, 106 with P's second)
@@ -138,6 +143,19 @@ template <int B>
 __device__ __forceinline__ void tmem_store_n(uint32_t taddr, const float (&v)[B]) {
     tmem_store8(taddr, v);
     if constexpr (B == 12) tmem_store4(taddr + 8, v + 8);
+}
+
+// Whether a wait would be over now.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 // One lane of a converged warp.  (The products' operands stay in uniform registers inside its branch; by
@@ -239,7 +257,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(qfull + i, 1);
-            mbar_init(qempty + i, 1 + 4 * G::groups + (G::q8 ? 4 : 0));
+            mbar_init(qempty + i, 1 + 4 * G::groups + 4 * G::converters);
         }
         mbar_init(sfull, 1);
         mbar_init(sempty, 4 * G::groups);
@@ -522,39 +540,53 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
                 const int tok = tb + me;
                 const int vs = t % G::v_slots;
                 uint8_t* vt = sm + G::off_v + vs * G::half;
-                float e = 0.f, f[4];
-                if constexpr (G::q8) {
-                    // the token's K scales and the exponent of its largest V scale
-                    const int ksl = t % G::k_slots;
-                    await(kfull + ksl, (t / G::k_slots) & 1);
-                    const uint2 sc = *reinterpret_cast<const uint2*>(sm + ksl * G::half + (me >> 6) * kQ8Half + 8192 + (me & 63) * 8);
-                    f[0] = __low2float(as_h2(sc.x)), f[1] = __high2float(as_h2(sc.x));
-                    f[2] = __low2float(as_h2(sc.y)), f[3] = __high2float(as_h2(sc.y));
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(kempty + ksl);
+                const int ksl = t % G::k_slots;
+                bool ready = false, p_free = t < G::p_bufs;  // P's buffer is read
+                if constexpr (G::eager) {
+                    // (those that are over already, which they mostly are: one after the other each costs some 100 clocks)
+                    ready = mbar_test(vfull + vs, (t / G::v_slots) & 1) & mbar_test(sfull, t & 1) &
+                            mbar_test(kfull + ksl, (t / G::k_slots) & 1);
+                    p_free = p_free || mbar_test(odone + t % G::p_bufs, (t / G::p_bufs - 1) & 1);
+                    ready = __all_sync(0xffffffffu, ready);
+                    p_free = __all_sync(0xffffffffu, p_free);
                 }
-                await(vfull + vs, (t / G::v_slots) & 1);
-                bool miss = vmiss[vs] != 0;  // a page of the tile is outside the pool
-                if constexpr (G::q8) {
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        const uint32_t w = *reinterpret_cast<const uint16_t*>(vt + (me >> 6) * kQ8Half + 8192 + (b * 64 + (me & 63)) * 2) & 0x7FFFu;
-                        top = w > 0x7C00u ? top : max(top, w);  // (NaN scales do not count)
-                    }
-                    e = static_cast<float>(min(max(static_cast<int>(top >> 10), 1), 29) - 15);
+                if (!ready) {
+                    if constexpr (G::q8) await(kfull + ksl, (t / G::k_slots) & 1);
+                    await(vfull + vs, (t / G::v_slots) & 1);
+                    await(sfull, t & 1);
                 }
-                await(sfull, t & 1);
                 tc_fence_after();
                 // ---- base-2 scores, masked; a query's first tile, or one that passes its reference by more
                 // than the slack, takes the long way
-                float x[W];
+                float x[W], e = 0.f;
+                float4 limit[W / 4];
+                bool miss;
+                auto limits = [&] {
+#pragma unroll
+                    for (int q = 0; q < W; q += 4) limit[q / 4] = *reinterpret_cast<const float4*>(lim + q);
+                };
                 if constexpr (G::q8) {
+                    float f[4];
 #pragma unroll
                     for (int c = 0; c < W; c += B) {
                         float v[4][B];
 #pragma unroll
                         for (int b = 0; b < 4; ++b) tmem_load_n<B>(lanes + G::col_s + b * N + c0 + c, v[b]);
+                        if (c == 0) {
+                            // the token's K scales and the exponent of its largest V scale
+                            const uint2 sc = *reinterpret_cast<const uint2*>(sm + ksl * G::half + (me >> 6) * kQ8Half + 8192 + (me & 63) * 8);
+                            uint32_t w[4], top = 0;
+#pragma unroll
+                            for (int b = 0; b < 4; ++b)
+                                w[b] = *reinterpret_cast<const uint16_t*>(vt + (me >> 6) * kQ8Half + 8192 + (b * 64 + (me & 63)) * 2) & 0x7FFFu;
+                            miss = vmiss[vs] != 0;  // a page of the tile is outside the pool
+                            if constexpr (G::eager) limits();
+                            f[0] = __low2float(as_h2(sc.x)), f[1] = __high2float(as_h2(sc.x));
+                            f[2] = __low2float(as_h2(sc.y)), f[3] = __high2float(as_h2(sc.y));
+#pragma unroll
+                            for (int b = 0; b < 4; ++b) top = w[b] > 0x7C00u ? top : max(top, w[b]);  // (NaN scales do not count)
+                            e = static_cast<float>(min(max(static_cast<int>(top >> 10), 1), 29) - 15);
+                        }
                         tc_wait_ld();
 #pragma unroll
                         for (int i = 0; i < B; ++i)
@@ -564,13 +596,17 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
                     float v[W / B][B];
 #pragma unroll
                     for (int c = 0; c < W / B; ++c) tmem_load_n<B>(lanes + G::col_s + c0 + B * c, v[c]);
+                    miss = vmiss[vs] != 0;
                     tc_wait_ld();
 #pragma unroll
                     for (int q = 0; q < W; ++q) x[q] = v[q / B][q % B] * p.c2;
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(sempty);
+                if (lane == 0) {
+                    mbar_arrive(sempty);
+                    if constexpr (G::q8) mbar_arrive(kempty + ksl);
+                }
                 if (miss || tb + kTcTile > it.minlen) {  // some query does not see some token of the tile
 #pragma unroll
                     for (int q = 0; q < W; ++q)
@@ -585,13 +621,20 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
                     }
                 }
                 bool over = !live || miss;
+                if constexpr (!G::eager) limits();
 #pragma unroll
                 for (int q = 0; q < W; q += 4) {
-                    const float4 m = *reinterpret_cast<const float4*>(lim + q);
+                    const float4 m = limit[q / 4];
                     if constexpr (G::q8) x[q] += e, x[q + 1] += e, x[q + 2] += e, x[q + 3] += e;
                     over |= x[q] > m.x || x[q + 1] > m.y || x[q + 2] > m.z || x[q + 3] > m.w;
                 }
                 bool moved = false;  // some reference moves
+                float4 base[W / 4];  // the references, as P takes them
+                auto bases = [&] {
+#pragma unroll
+                    for (int q = 0; q < W; q += 4) base[q / 4] = *reinterpret_cast<const float4*>(sub + q);
+                };
+                if constexpr (G::eager) bases();
                 if (!live) *dead = 1;
                 if (miss) *missed = t;
                 if (bar_or(bar_id, 128, over)) {
@@ -622,10 +665,11 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
                         l[q] *= a;
                         moved |= a != 1.f;
                     }
+                    if constexpr (G::eager) bases();
                 }
                 const bool edge = miss || tb + kTcTile > it.minlen;
                 const bool fresh = tb == it.tok0;  // the outputs hold nothing yet
-                if (t >= G::p_bufs) await(odone + t % G::p_bufs, (t / G::p_bufs - 1) & 1);  // this buffer's last P is read
+                if (!p_free) await(odone + t % G::p_bufs, (t / G::p_bufs - 1) & 1);
                 if (moved && !fresh) {
                     last_product();  // (only a new reference or a marked token needs its outputs)
                     tc_fence_after();
@@ -646,10 +690,10 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
                 // stores; with tokens contiguous they were 2-byte ones, 32 of a q8_0 thread's
                 const float inv = G::q8 ? __int_as_float((127 - static_cast<int>(e)) << 23) : 1.f;  // 2^-e
                 uint8_t* pt = sm + G::off_p + t % G::p_bufs * (2 * G::opnd);
-                // (all of them before the first store, which the compiler may not load past)
+                if constexpr (!G::eager) bases();
 #pragma unroll
                 for (int q = 0; q < W; q += 4) {
-                    const float4 m = *reinterpret_cast<const float4*>(sub + q);
+                    const float4 m = base[q / 4];
                     x[q] = ex2(x[q] - m.x), x[q + 1] = ex2(x[q + 1] - m.y);
                     x[q + 2] = ex2(x[q + 2] - m.z), x[q + 3] = ex2(x[q + 3] - m.w);
                 }
@@ -811,8 +855,8 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
         // K of tile i: a token per thread
         auto convert_k = [&](int i) {
             const int ks = i % G::k_slots;
-            await(kfull + ks, (i / G::k_slots) & 1);
-            if (i > 0) await(akfree, (i - 1) & 1);
+            await_warp(kfull + ks, (i / G::k_slots) & 1);
+            if (i > 0) await_warp(akfree, (i - 1) & 1);
             tc_fence_after();
             const uint8_t* kt = sm + ks * G::half + (me >> 6) * kQ8Half + slot * 128;
             uint4 row[8];  // (loaded before the first store to tensor memory, which the compiler may not load past)
@@ -843,13 +887,23 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
         };
         int t = 0, k = 0;
         bool go = true;
+        if (G::converters == 2 && warp < G::threads / 32 - 4) {  // K only
+            for (int item = blockIdx.x; item < total && live; item += gridDim.x, ++k) {
+                await_warp(qfull + (k & 1), (k >> 1) & 1);
+                const int tok0 = item_sm[k & 1].tok0, end = item_sm[k & 1].end;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(qempty + (k & 1));
+                for (int tb = tok0; tb < end && live; tb += kTcTile, ++t) convert_k(t);
+            }
+            go = false;
+        }
         for (int item = blockIdx.x; item < total && go; item += gridDim.x, ++k) {
             await(qfull + (k & 1), (k >> 1) & 1);
             const ItemRec it = item_sm[k & 1];
-            if (k == 0) convert_k(0);
+            if (G::converters == 1 && k == 0) convert_k(0);
             for (int tb = it.tok0; tb < it.end; tb += kTcTile, ++t) {
                 // the next tile's K goes first: it is free to, while V waits for the last products
-                if (tb + kTcTile < it.end || item + gridDim.x < total) convert_k(t + 1);
+                if (G::converters == 1 && (tb + kTcTile < it.end || item + gridDim.x < total)) convert_k(t + 1);
                 const int vs = t % G::v_slots;
                 await(vfull + vs, (t / G::v_slots) & 1);
                 const uint8_t* vt = sm + G::off_v + vs * G::half;
