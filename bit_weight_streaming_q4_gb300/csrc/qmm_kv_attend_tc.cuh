@@ -29,14 +29,16 @@
 // holds).  Each query decides for itself, so its bits depend on nothing but its own tokens.
 //
 // What it measured (this kernel alone, without weights; in brackets the call, whose join comes after):
-// fp16, one sequence of 131,071, 1 row: 81 us (88), 6.6 TB/s, the bytes.  bf16, 8 x 16,000, 8 rows
-// (48 queries a head): 99 us (114), 5.3 TB/s.  q8_0, 4 x 23,000, 3 rows (18 queries): 90 us (96), 2.2 TB/s.
-// The last two are bound by the chain from a tile's scores to its probabilities: by clock readings in
-// a copy of the kernel a softmax group takes about 3,700 and 3,900 clocks a tile, fp16 at one row 2,700.
+// fp16, one sequence of 131,071, 1 row: 80 us (87), 6.7 TB/s, the bytes.  bf16, 8 x 16,000, 8 rows
+// (48 queries a head): 93 us (107), 5.6 TB/s.  q8_0, 4 x 23,000, 3 rows (18 queries): 80 us (87), 2.5 TB/s.
+// The second is bound by the chain from a tile's scores to its probabilities, some 3,500 clocks a tile
+// in a softmax group (by clock readings in a copy of the kernel); q8_0 by the conversion of V as well:
+// without three quarters of it, 66 us for 85.  With weights the scores' way through L2 costs 10 to 33 us.
 // Not kept, this kernel's time against its time then: groups that take whole tiles in turn, with
 // outputs of their own (q8_0 125 us for 90, bf16 144 for 110: each thread then does all queries); four
-// groups of 8 queries at q8_0 (97 for 90); K and V converted by warps of their own (98 for 90).
-// On mma.sync with the outputs in registers the three cases took 86, 300 and 113 us.
+// groups of 8 queries at q8_0 (97 for 90); registers dealt out anew between the roles (85 for 81).
+// On mma.sync with the outputs in registers the three cases took 86, 300 and 113 us.  (qmm_attn_decode's
+// kernel does the q8_0 case in 52 us, with p rounded to 16 bits once and without the weights.)
 #pragma once
 
 #include "qmm_kv_attend.cuh"
@@ -63,7 +65,7 @@ struct TcGeo {
     static constexpr int threads = 128 * (1 + groups + converters);
     static constexpr int half = q8 ? 2 * kQ8Half : kTcTile * 256;  // bytes of a tile's K or V
     static constexpr int k_slots = q8 ? 4 : 2, v_slots = q8 ? 4 : 3;  // (K's are free again once S is formed)
-    static constexpr int p_bufs = N == 48 ? 1 : 2;                 // (no room for two beside three V tiles: bf16 8 x 16,000 101 us with V's third, 106 with P's second)
+    static constexpr int p_bufs = N == 48 ? 1 : 2;                 // (no room for two beside three V tiles: bf16 8 x 16,000: this kernel 101 us with V's third, 106 with P's second)
     static constexpr int opnd = N * 256;                           // bytes of a B operand: N rows of 128 16-bit values
     // tensor memory columns: scores (one set per 32-dim block of a q8_0 pool), outputs (2 N: those of P's
     // high and of its low parts; of 16-bit pools two sets, items in turn), and the A operands
