@@ -14,40 +14,96 @@ constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kWeightTokens = 1024;  // slots per block of the weights' part
 
-// Denominator and reference of one query over its chunks: every lane of the warp returns them.
-// Chunks are taken in a fixed order (lane c % 32, then a butterfly), so the value depends on the
-// query alone.
-__device__ __forceinline__ float2 join_ml(const AttendParams& p, int64_t slot0, int n) {
-    const int lane = threadIdx.x & 31;
+// Reference and denominator of one query over its chunks, by the whole block: every thread returns
+// them.  Up to 32 chunks every warp does alone; more are taken in a fixed order (thread
+// c % kJoinThreads, a butterfly, the warps in turn), so the value depends on the query alone.
+__device__ __forceinline__ float2 join_ml(const AttendParams& p, int64_t slot0, int n, float* tmp) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const float2* ml = reinterpret_cast<const float2*>(p.ml) + slot0;
     float m = kNoMax;
-    for (int c = lane; c < n; c += 32) m = fmaxf(m, ml[static_cast<int64_t>(c) * p.qp].x);
+    if (n <= 32) {
+        float2 v = make_float2(kNoMax, 0.f);
+        if (lane < n) v = ml[static_cast<int64_t>(lane) * p.qp];
+        m = v.x;
+#pragma unroll
+        for (int k = 16; k >= 1; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+        float l = v.y * exp2f(v.x - (m == kNoMax ? 0.f : m));
+#pragma unroll
+        for (int k = 16; k >= 1; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+        return make_float2(m, l);
+    }
+#pragma unroll 4
+    for (int c = tid; c < n; c += kJoinThreads) m = fmaxf(m, ml[static_cast<int64_t>(c) * p.qp].x);
 #pragma unroll
     for (int k = 16; k >= 1; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+    if (lane == 0) tmp[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, tmp[w]);
     const float ref = m == kNoMax ? 0.f : m;
     float l = 0.f;
-    for (int c = lane; c < n; c += 32) {
+#pragma unroll 4
+    for (int c = tid; c < n; c += kJoinThreads) {
         const float2 v = ml[static_cast<int64_t>(c) * p.qp];
         l = fmaf(v.y, exp2f(v.x - ref), l);
     }
 #pragma unroll
     for (int k = 16; k >= 1; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+    if (lane == 0) tmp[kJoinWarps + warp] = l;
+    __syncthreads();
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) l += tmp[kJoinWarps + w];
     return make_float2(m, l);
+}
+
+// sum_c 2^(M_c - ref) o_c over the chunks of one query, E consecutive dims a lane: chunks dealt to the warps in
+// turn, the warps' sums in order.  Thread i < 32 E returns dim i of the warps' common range.
+template <int E>
+__device__ __forceinline__ float join_sum(const AttendParams& p, int64_t slot0, int n, float ref, const float* o0, int d, float* jsm) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    float acc[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) acc[i] = 0.f;
+#pragma unroll(E == 1 ? 8 : 4)
+    for (int c = warp; c < n; c += kJoinWarps) {
+        const int64_t s = slot0 + static_cast<int64_t>(c) * p.qp;
+        const float w = exp2f(p.ml[2 * s] - ref);
+        const float* o = o0 + s * d + lane * E;
+        float v[E];
+        if constexpr (E == 1) v[0] = *o;
+        else if constexpr (E == 2) *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(o);
+        else
+#pragma unroll
+            for (int i = 0; i < E; i += 4) *reinterpret_cast<float4*>(v + i) = *reinterpret_cast<const float4*>(o + i);
+        // (a chunk that the row does not see has w = 0 and o = 0)
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[i] = fmaf(v[i], w, acc[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) jsm[(warp * 32 + lane) * E + i] = acc[i];
+    __syncthreads();
+    float v = 0.f;
+    if (tid < 32 * E) {
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) v += jsm[w * 32 * E + tid];
+    }
+    return v;
 }
 
 // The first weight_blocks blocks: kWeightTokens slots of one (sequence, KV head) each, taken in turn by
 // however many blocks there are.  They are the long ones, so they start first and the others fill
-// in beside them.  The others: one (row, head) each, its chunks dealt to the warps in turn and the
-// warps' sums added in order.
+// in beside them.  The others: one (row, head) each, or 32 dims of one where that makes few blocks (a
+// sequence of 118,000 tokens, D = 256, 3 rows of 2 heads: 1,842 chunks a query).  The bits are the same.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads, 6) attend_join(const AttendParams p, int weight_blocks) {
+__global__ void __launch_bounds__(kJoinThreads, 6) attend_join(const AttendParams p, int weight_blocks, int slices) {
     extern __shared__ float jsm[];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x;
     griddep_wait();  // the split kernel has finished and its partials are visible
     if (static_cast<int>(blockIdx.x) >= weight_blocks) {
-        const int block = blockIdx.x - weight_blocks;
-        constexpr int E = D / 32;
+        const int block = (blockIdx.x - weight_blocks) / slices, slice = (blockIdx.x - weight_blocks) % slices;
         __shared__ int found;
+        __shared__ float tmp[2 * kJoinWarps];
         const int h = block % p.heads, r = block / p.heads;
         if (tid == 0) found = -1;
         __syncthreads();
@@ -57,47 +113,27 @@ __global__ void __launch_bounds__(kJoinThreads, 6) attend_join(const AttendParam
         }
         __syncthreads();
         const int a = found, g = h / p.group;
-        float m = kNoMax, l = 0.f, acc[E];
-#pragma unroll
-        for (int i = 0; i < E; ++i) acc[i] = 0.f;
-        if (a == -1 && tid == 0 && h == 0) atomicOr(p.err, kErrRange);
+        const int width = slices == 1 ? D : 32;  // dims of the block
+        float m = kNoMax, l = 0.f, v = 0.f;
+        if (a == -1 && tid == 0 && h == 0 && slice == 0) atomicOr(p.err, kErrRange);
         if (a >= 0) {
             const int n = (p.row_len[r] + p.chunk - 1) / p.chunk;
             const int q = (r - p.info[a].y) * p.group + h % p.group;
             const int64_t slot0 = static_cast<int64_t>(a * p.kv_heads + g) * p.chunks * p.qp + q;
-            const float2 t = join_ml(p, slot0, n);
+            const float2 t = join_ml(p, slot0, n, tmp);
             m = t.x;
             l = t.y;
             const float ref = m == kNoMax ? 0.f : m;
-#pragma unroll 4
-            for (int c = warp; c < n; c += kJoinWarps) {
-                const int64_t s = slot0 + static_cast<int64_t>(c) * p.qp;
-                const float w = exp2f(p.ml[2 * s] - ref);
-                const float* o = p.o + s * D + lane * E;
-                float v[E];
-                if constexpr (E == 2) *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(o);
-                else
-#pragma unroll
-                    for (int i = 0; i < E; i += 4) *reinterpret_cast<float4*>(v + i) = *reinterpret_cast<const float4*>(o + i);
-                // (a chunk that the row does not see has w = 0 and o = 0)
-#pragma unroll
-                for (int i = 0; i < E; ++i) acc[i] = fmaf(v[i], w, acc[i]);
-            }
+            v = slices == 1 ? join_sum<D / 32>(p, slot0, n, ref, p.o, D, jsm) : join_sum<1>(p, slot0, n, ref, p.o + 32 * slice, D, jsm);
         }
-#pragma unroll
-        for (int i = 0; i < E; ++i) jsm[warp * D + lane * E + i] = acc[i];
-        __syncthreads();
-        if (tid < D) {
-            float v = 0.f;
-#pragma unroll
-            for (int w = 0; w < kJoinWarps; ++w) v += jsm[w * D + tid];
+        if (tid < width) {
             v = m == kNoMax ? 0.f : v / l;
-            const int64_t at = static_cast<int64_t>(block) * D + tid;
+            const int64_t at = static_cast<int64_t>(block) * D + slice * 32 + tid;
             if (p.out_type == QMM_TYPE_F32) static_cast<float*>(p.out)[at] = v;
             else if (p.out_type == QMM_TYPE_F16) static_cast<__half*>(p.out)[at] = __float2half_rn(v);
             else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
         }
-        if (tid == 0 && p.lse) p.lse[block] = m == kNoMax ? kNoMax : (m - kShift + log2f(l)) * 0.6931471805599453f;
+        if (tid == 0 && slice == 0 && p.lse) p.lse[block] = m == kNoMax ? kNoMax : (m - kShift + log2f(l)) * 0.6931471805599453f;
         return;
     }
 
@@ -197,18 +233,27 @@ __global__ void __launch_bounds__(kJoinThreads, 6) attend_join(const AttendParam
 
 namespace {
 
-// Tokens per chunk, by the dims alone (so that a row's bits are those of any other call): the
-// longest of 1024 .. a tile that gives every block of a GB300's grid two items at head dimension 128
-// (one block per SM), and six otherwise (four), when all sequences are full, and whose pages one
-// warp can hold (32).  At head dimension 64, 61 ragged sequences: 104 us at 1,024, 92 at 512, 93 at 256.  At 128,
+// Tokens per chunk, by the dims alone (so that a row's bits are those of any other call): of 1024 ..
+// a tile, with pages that one warp can hold (32), the one whose rounds of a GB300's grid (152
+// blocks at head dimension 128, 608 otherwise) take the least when all sequences are full, an item being
+// its tiles and kItem tiles' time for its start and end.  At head dimension 64, 61 ragged sequences: 104 us at 1,024, 92 at 512, 93 at 256.  At 128,
 // calls with weights at 1,024 and 2,048: 109 and 112 us for a sequence of 131,071 (fp16), 184 and 189 for
 // 8 x 16,000 at 8 rows (bf16), 108 and 115 for 4 x 23,000 (q8_0).
 int32_t chunk_of(const qmm_kv_dims& d) {
-    const int64_t cap = int64_t{d.max_pages} * d.page_tokens, items = d.head_dim == 128 ? 2 * 152 : 6 * 608;
-    const int32_t least = d.head_dim == 128 ? kTcTile : kTile;
-    for (int32_t c = 1024; c > least; c >>= 1)
-        if (c <= 32 * d.page_tokens && (cap + c - 1) / c * d.agents * d.kv_heads >= items) return c;
-    return least;
+    constexpr double kItem = 1.5;
+    const int64_t cap = int64_t{d.max_pages} * d.page_tokens, blocks = d.head_dim == 128 ? 152 : 608;
+    const int32_t tile = d.head_dim == 128 ? kTcTile : kTile;
+    int32_t best = tile;
+    double least = 0;
+    for (int32_t c = tile; c <= 1024 && (c == tile || c <= 32 * d.page_tokens); c *= 2) {
+        const int64_t items = (cap + c - 1) / c * d.agents * d.kv_heads;
+        const double time = static_cast<double>((items + blocks - 1) / blocks) * (c / tile + kItem);
+        if (c == tile || time <= least) {
+            best = c;
+            least = time;
+        }
+    }
+    return best;
 }
 
 struct Layout {
@@ -272,7 +317,8 @@ qmm_status make_map(const qmm_kv_dims& d, const void* pool, CUtensorMap* map) {
 
 template <int D>
 cudaError_t launch_join(const AttendParams& p, int sms, cudaStream_t s) {
-    const int out_blocks = p.rows * p.heads;
+    const int slices = int64_t{p.rows} * p.heads * (D / 32) <= 4 * sms ? D / 32 : 1;
+    const int out_blocks = p.rows * p.heads * slices;
     int64_t weight_blocks = 0;
     if (p.weight_out) {
         weight_blocks = int64_t{p.agents} * p.kv_heads * ((p.cap + kWeightTokens - 1) / kWeightTokens);
@@ -289,7 +335,7 @@ cudaError_t launch_join(const AttendParams& p, int sms, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attend_join<D>, p, static_cast<int>(weight_blocks));
+    return cudaLaunchKernelEx(&cfg, attend_join<D>, p, static_cast<int>(weight_blocks), slices);
 }
 
 }  // namespace
