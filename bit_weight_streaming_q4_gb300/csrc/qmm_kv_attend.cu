@@ -234,14 +234,14 @@ __global__ void __launch_bounds__(kJoinThreads, 6) attend_join(const AttendParam
 namespace {
 
 // Tokens per chunk, by the dims alone (so that a row's bits are those of any other call): of 1024 ..
-// a tile, with pages that one warp can hold (32), the one whose rounds of a GB300's grid (152
-// blocks at head dimension 128, 608 otherwise) take the least when all sequences are full, an item being
+// a tile, with pages that one warp can hold (32), the one whose rounds of a GB300's grid (608
+// blocks at head dimension 64, 152 at 128, 304 at 256) take the least when all sequences are full, an item being
 // its tiles and kItem tiles' time for its start and end.  At head dimension 64, 61 ragged sequences: 104 us at 1,024, 92 at 512, 93 at 256.  At 128,
 // calls with weights at 1,024 and 2,048: 109 and 112 us for a sequence of 131,071 (fp16), 184 and 189 for
 // 8 x 16,000 at 8 rows (bf16), 108 and 115 for 4 x 23,000 (q8_0).
 int32_t chunk_of(const qmm_kv_dims& d) {
     constexpr double kItem = 1.5;
-    const int64_t cap = int64_t{d.max_pages} * d.page_tokens, blocks = d.head_dim == 128 ? 152 : 608;
+    const int64_t cap = int64_t{d.max_pages} * d.page_tokens, blocks = d.head_dim == 64 ? 608 : d.head_dim == 128 ? 152 : 304;
     const int32_t tile = d.head_dim == 128 ? kTcTile : kTile;
     int32_t best = tile;
     double least = 0;

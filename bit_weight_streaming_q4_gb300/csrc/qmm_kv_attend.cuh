@@ -7,7 +7,7 @@
 // gets never depends on the other rows of the call.  Each (sequence, chunk, KV head, tile of
 // queries) is an item; the blocks of a persistent grid take items in turn and write M, l and the
 // unnormalised output as the item's partial, which the joining kernel adds up.  All queries of a
-// tile share each K and V tile on chip, so the cache is read once for up to 48.
+// tile share each K and V tile on chip, so the cache is read once for as many queries as a tile has.
 //
 // This kernel (16-bit pools).  A block's four warps work on tiles of 64 tokens: each forms the scores
 // of 16 tokens for all queries, the maxima meet in shared memory, the probabilities go there as the
@@ -82,7 +82,7 @@ struct Geo {
     static constexpr int PS = kTile + 8;          // halves per row of P, and bytes per row of Q: the padding
     static constexpr int QS = 2 * D + 16;         // keeps ldmatrix free of bank conflicts
     // blocks per SM that the registers are limited for (D = 256: the ring alone takes 96 KB)
-    static constexpr int blocks = D == 256 ? 2 : NT == 6 ? 3 : 4;
+    static constexpr int blocks = D == 256 ? 2 : 4;
     // dynamic shared memory, after aligning to 1024: ring, Q, P (hi, lo), maxima, lengths, barriers
     static constexpr int off_q = slots * HB;
     static constexpr int off_p = off_q + QT * QS;
@@ -651,13 +651,17 @@ cudaError_t launch_attend_one(const AttendLaunch& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-// The fewest column tiles that take all queries of a sequence, up to the most whose state fits
-// the registers of three blocks per SM (two at D = 256); a wider instance would carry empty tiles.
+// Column tiles of 8 queries that an item takes.  D = 64: the fewest items per chunk, and of 3 and 4 column
+// tiles the fewer where the items are as many (5 x 24,000 tokens, 4 KV heads: 18 queries 61 us by 3 and 85 by
+// 2; 30: 77 by 4, 107 by 3; 48: 110 by 3, 131 by 4, 154 by 6, whose registers leave three blocks an SM;
+// 64: 135 by 4, 153 by 3).  D = 256: 2, the most of which two blocks fit an SM (18 queries 212 us, 235 by 3;
+// 30: 215, 292 by 4; 48: 283, 408 by 3).
 template <int FMT, int D>
 cudaError_t launch_attend_dim(const AttendLaunch& a, cudaStream_t s) {
     if (a.max_q <= 8) return launch_attend_one<FMT, D, 1>(a, s);
-    if (a.max_q <= 24 || D == 256) return launch_attend_one<FMT, D, 3>(a, s);
-    return launch_attend_one<FMT, D, D == 256 ? 3 : 6>(a, s);
+    if (D == 256 || a.max_q <= 16) return launch_attend_one<FMT, D, 2>(a, s);
+    return (a.max_q + 31) / 32 < (a.max_q + 23) / 24 ? launch_attend_one<FMT, D, D == 256 ? 2 : 4>(a, s)
+                                                     : launch_attend_one<FMT, D, D == 256 ? 2 : 3>(a, s);
 }
 
 }  // namespace kv
