@@ -103,6 +103,8 @@ struct Shared {
     Sums total;
     Sums sums[kSums];            // of the block's segments, in order
     float raise[2];              // bounds found by one warp for the segments after
+    alignas(16) float most[kThreads];  // the threads' largest candidates
+    uint32_t least;
     int n_first, n_all, n_cand;
 };
 
@@ -124,7 +126,28 @@ __device__ __forceinline__ float kth_of_32(const float* all, float mine, int k) 
 __device__ __noinline__ int rank_candidates(Shared& sh, int n, int k, float floor) {
     const int tid = threadIdx.x;
     if (tid < kMaxTop) sh.list[tid] = 0;
-    if (tid == 0) sh.n_first = 0;
+    if (tid == 0) {
+        sh.n_first = 0;
+        sh.least = 0xFFFFFFFFu;
+    }
+    if (n > kThreads) {
+        // many (600 at 31 alternatives of 151,936 columns): the k-th largest of the threads' largest is a floor
+        // that few more than k pass.  (200 rows: 50 us; 84 with all ranked against all.)
+        float top = -INFINITY;
+        for (int i = tid; i < n; i += kThreads) top = fmaxf(top, value_of(sh.cand[i]));
+        sh.most[tid] = top;
+        __syncthreads();
+        int above = 0;
+#pragma unroll 8
+        for (int j = 0; j < kThreads; j += 4) {
+            const float4 o = *reinterpret_cast<const float4*>(sh.most + j);
+            above += (o.x > top) + (o.y > top) + (o.z > top) + (o.w > top);
+        }
+        const uint32_t least = __reduce_min_sync(0xffffffffu, above < k ? order_of(top) : 0xFFFFFFFFu);
+        if ((tid & 31) == 0) atomicMin(&sh.least, least);
+        __syncthreads();
+        floor = fmaxf(floor, from_order(sh.least));
+    }
     __syncthreads();
     const uint64_t* from = sh.cand;
     if (n > 64) {
