@@ -105,7 +105,10 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
     constexpr bool q8 = FMT == QMM_KV_Q8_0;
     constexpr int E = D / 32;
     __shared__ int tmp[33], mine[5];
-    __shared__ __align__(16) uint8_t vq[q8 ? 128 * 32 : 16];  // [dim][slot of the group]
+    // [dim][slot of the group], a word further every four dims: a warp's lanes, four dims apart, then store to
+    // 32 different banks
+    __shared__ __align__(16) uint8_t vq[q8 ? 128 * 32 + 32 * 4 : 16];
+    auto vq_at = [](int d) { return d * 32 + (d >> 2) * 4; };
     __shared__ __half vs[q8 ? 4 * 32 : 8];                    // [block][slot]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = blockIdx.y;
     // this block's sequence and group of slots
@@ -173,7 +176,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
                 }
                 const __half dv = quantise(kv[k][1], q);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) vq[(4 * lane + i) * 32 + t - base] = static_cast<uint8_t>(q >> (8 * i));
+                for (int i = 0; i < 4; ++i) vq[vq_at(4 * lane + i) + t - base] = static_cast<uint8_t>(q >> (8 * i));
                 if ((lane & 7) == 0) vs[(lane >> 3) * 32 + t - base] = dv;
             } else if (in) {
 #pragma unroll
@@ -205,11 +208,21 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
         const int at = base % 64;
         if (hi - lo == 32) {
             const int d = tid >> 1, part = tid & 1;
-            *reinterpret_cast<uint4*>(rec + 8704 + d * 64 + at + 16 * part) = *reinterpret_cast<const uint4*>(vq + d * 32 + 16 * part);
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(vq + vq_at(d) + 16 * part);
+            *reinterpret_cast<uint4*>(rec + 8704 + d * 64 + at + 16 * part) = make_uint4(w[0], w[1], w[2], w[3]);
         } else {
-            for (int i = tid; i < 128 * (hi - lo); i += kAppendThreads) {
-                const int d = i & 127, t = lo - base + (i >> 7);
-                rec[8704 + d * 64 + at + t] = vq[d * 32 + t];
+            const int first = lo - base, last = hi - base;
+            for (int i = tid; i < 128 * 8; i += kAppendThreads) {  // four slots of a dim
+                const int d = i >> 3, t0 = 4 * (i & 7);
+                uint8_t* to = rec + 8704 + d * 64 + at + t0;
+                const uint8_t* from = vq + vq_at(d) + t0;
+                if (t0 >= first && t0 + 4 <= last) {
+                    *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(from);
+                } else {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        if (t0 + t >= first && t0 + t < last) to[t] = from[t];
+                }
             }
         }
         for (int i = tid; i < 4 * (hi - lo); i += kAppendThreads) {
