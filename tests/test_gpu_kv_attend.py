@@ -312,3 +312,27 @@ def test_attend_reports_bad_pages_rows_and_lengths(fmt):
     assert err == 4 and (out[0] == 0).all() and np.array_equal(out[1], good[0][1])
     out, lse, _, err = run(c, 4, [0, 2, 2], [200, 200], q, plan=c.plan(4, 2, 1))
     assert err == 4 and (out == 0).all()
+
+
+@pytest.mark.parametrize("fmt,dim", [("q8_0", 128), ("f16", 64), ("bf16", 64), ("f16", 128), ("bf16", 128), ("f16", 256), ("bf16", 256)])
+@pytest.mark.parametrize("heads", [8, 9, 16, 17, 24, 25, 32, 33, 48, 49, 65, 73])
+def test_attend_numbers_of_queries_around_the_tiles(fmt, dim, heads):
+    check(Cache(fmt, (333, 66), 1, dim, 32 if fmt != "q8_0" else 64, seed=heads), heads, 1)
+
+
+@pytest.mark.parametrize("fmt,dim,page,n", [("q8_0", 128, 64, 5003), ("f16", 64, 16, 5003), ("bf16", 256, 32, 5003), ("f16", 128, 64, 40001)])
+def test_attend_more_chunks_than_a_warp_has_lanes(fmt, dim, page, n):
+    check(Cache(fmt, (n, 70), 1, dim, page, seed=13), 3, 2)
+
+
+@pytest.mark.parametrize("fmt,dim,page", [("f16", 64, 16), ("q8_0", 128, 64), ("bf16", 256, 32)])
+def test_attend_bits_of_a_row_in_a_small_and_a_large_call(fmt, dim, page):
+    """A row alone, and beside the 39 rows of another sequence: how the join is split differs."""
+    c = Cache(fmt, (5003, 300), 1, dim, page, seed=14)
+    q = queries(c, 40, 16)
+    plan = c.plan(16, 40, 39)
+    few = run(c, 16, [0, 1, 1], [5003], q[:1], plan=plan)
+    many = run(c, 16, [0, 1, 40], [5003] + [300 - i for i in range(39)], q, plan=plan)
+    assert few[3] == 0 and many[3] == 0
+    assert np.array_equal(few[0][0], many[0][0]) and np.array_equal(few[1][0], many[1][0])
+    assert np.array_equal(few[2][0], many[2][0])

@@ -162,3 +162,14 @@ def test_logprobs_none_of_the_outputs_and_no_rows():
     serve.logprobs(x, lse=lse)
     t.cuda.synchronize()
     assert np.allclose(lse.cpu().numpy(), t.logsumexp(x.double(), -1).cpu().numpy(), atol=2.0 ** -16)
+
+
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_logprobs_many_candidates_per_block(kind):
+    """Hundreds of rows: a block has many segments, and 32 alternatives let some 80 elements of each pass."""
+    t = torch_cuda()
+    g = t.Generator(device="cuda").manual_seed(2)
+    x = (t.randn(320, 151936, generator=g, device="cuda") * 2.5).to(kind)
+    got = run(x, top=32)
+    order = t.sort(x.float(), dim=-1, descending=True, stable=True).indices[:, :32].cpu().numpy()
+    assert np.array_equal(got["top_index"], order)
