@@ -12,7 +12,6 @@ namespace kv {
 
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
-constexpr int kWeightTokens = 1024;  // slots per block of the weights' part
 
 // Reference and denominator of one query over its chunks, by the whole block: every thread returns
 // them.  Up to 32 chunks every warp does alone; more are taken in a fixed order (thread
@@ -73,9 +72,10 @@ __device__ __forceinline__ float join_sum(const AttendParams& p, int64_t slot0, 
         float v[E];
         if constexpr (E == 1) v[0] = *o;
         else if constexpr (E == 2) *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(o);
-        else
+        else {
 #pragma unroll
             for (int i = 0; i < E; i += 4) *reinterpret_cast<float4*>(v + i) = *reinterpret_cast<const float4*>(o + i);
+        }
         // (a chunk that the row does not see has w = 0 and o = 0)
 #pragma unroll
         for (int i = 0; i < E; ++i) acc[i] = fmaf(v[i], w, acc[i]);
@@ -91,11 +91,11 @@ __device__ __forceinline__ float join_sum(const AttendParams& p, int64_t slot0, 
     return v;
 }
 
-// The first weight_blocks blocks: kWeightTokens slots of one (sequence, KV head) each, taken in turn by
+// The first weight_blocks blocks: T slots a thread of one (sequence, KV head) each, taken in turn by
 // however many blocks there are.  They are the long ones, so they start first and the others fill
 // in beside them.  The others: one (row, head) each, or 32 dims of one where that makes few blocks (a
 // sequence of 118,000 tokens, D = 256, 3 rows of 2 heads: 1,842 chunks a query).  The bits are the same.
-template <int D>
+template <int D, int T>
 __global__ void __launch_bounds__(kJoinThreads, 6) attend_join(const AttendParams p, int weight_blocks, int slices) {
     extern __shared__ float jsm[];
     const int tid = threadIdx.x;
@@ -140,10 +140,11 @@ __global__ void __launch_bounds__(kJoinThreads, 6) attend_join(const AttendParam
     // ---- weights: tokens by thread, queries in order
     float* ref = jsm;           // [qp] M - kShift (the base-2 logarithm's part that l lacks)
     float* inv = jsm + p.qp;    // [qp] 1 / l
-    const int per = (p.cap + kWeightTokens - 1) / kWeightTokens;
+    constexpr int kSlots = T * kJoinThreads;
+    const int per = (p.cap + kSlots - 1) / kSlots;
     const int64_t all = static_cast<int64_t>(p.agents) * p.kv_heads * per;
     for (int64_t b = blockIdx.x; b < all; b += weight_blocks) {
-        const int ag = static_cast<int>(b / per), t0 = static_cast<int>(b % per) * kWeightTokens;
+        const int ag = static_cast<int>(b / per), t0 = static_cast<int>(b % per) * kSlots;
         const int4 info = p.info[ag / p.kv_heads];
         if (t0 >= info.x) continue;  // past the sequence's longest row, or a refused sequence (-1)
         const int nq = info.z * p.group;
@@ -177,9 +178,8 @@ __global__ void __launch_bounds__(kJoinThreads, 6) attend_join(const AttendParam
         const float4* x0 = reinterpret_cast<const float4*>(p.scores) + ag * (p.qp >> 2) * plane;
         // (Blocks beside each other hide the latency better than a thread's own loads: 8 x 16,000 bf16 at 8 rows, whole
         // calls: 169 us by six blocks an SM, 174 by five with the loop unrolled twice, 184 with the next four prefetched.)
-        // kWeightTokens / kJoinThreads tokens a thread at once: their loads are in flight together and share
+        // T tokens a thread at once: their loads are in flight together and share
         // the queries' numbers.  (A token past info.x takes the last one's scores and stores nothing.)
-        constexpr int T = kWeightTokens / kJoinThreads;
         const float4* x[T];
         float sum[T];
 #pragma unroll
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kJoinThreads, 6) attend_join(const AttendParam
             x[i] = x0 + (t < info.x ? t : info.x - 1);
             sum[i] = 0.f;
         }
-#pragma unroll 1
+#pragma unroll(T == 1 ? 4 : 1)
         for (int q = 0; q < (nq & ~3); q += 4) {
             const float4 r = *reinterpret_cast<const float4*>(ref + q), w = *reinterpret_cast<const float4*>(inv + q);
             float4 v[T];
@@ -319,9 +319,16 @@ template <int D>
 cudaError_t launch_join(const AttendParams& p, int sms, cudaStream_t s) {
     const int slices = int64_t{p.rows} * p.heads * (D / 32) <= 4 * sms ? D / 32 : 1;
     const int out_blocks = p.rows * p.heads * slices;
+    // slots a thread of the weights' part: four share a block's start; one where that leaves few blocks
+    // with many queries, whose time is the latency of their loads (a call of 3 x 20,619 tokens, one KV head, 48
+    // queries: 26 us by one, 36 by four; 85,205 tokens and 4 queries: 19 and 18)
     int64_t weight_blocks = 0;
+    bool narrow = false;
     if (p.weight_out) {
-        weight_blocks = int64_t{p.agents} * p.kv_heads * ((p.cap + kWeightTokens - 1) / kWeightTokens);
+        const int64_t groups = int64_t{p.agents} * p.kv_heads;
+        weight_blocks = groups * ((p.cap + 4 * kJoinThreads - 1) / (4 * kJoinThreads));
+        narrow = weight_blocks < 2 * sms && p.qp > 8;
+        if (narrow) weight_blocks = groups * ((p.cap + kJoinThreads - 1) / kJoinThreads);
         if (weight_blocks > sms * 8) weight_blocks = sms * 8;
     }
     const int words = kJoinWarps * D > 2 * p.qp ? kJoinWarps * D : 2 * p.qp;
@@ -335,7 +342,7 @@ cudaError_t launch_join(const AttendParams& p, int sms, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attend_join<D>, p, static_cast<int>(weight_blocks), slices);
+    return cudaLaunchKernelEx(&cfg, narrow ? attend_join<D, 1> : attend_join<D, 4>, p, static_cast<int>(weight_blocks), slices);
 }
 
 }  // namespace
