@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kJoinThreads, 6) attend_join(const AttendParam
         float m = kNoMax, l = 0.f, v = 0.f;
         if (a == -1 && tid == 0 && h == 0 && slice == 0) atomicOr(p.err, kErrRange);
         if (a >= 0) {
-            const int n = (p.row_len[r] + p.chunk - 1) / p.chunk;
+            const int n = (min(p.row_len[r], p.info[a].x) + p.chunk - 1) / p.chunk;  // (the partials that there are)
             const int q = (r - p.info[a].y) * p.group + h % p.group;
             const int64_t slot0 = static_cast<int64_t>(a * p.kv_heads + g) * p.chunks * p.qp + q;
             const float2 t = join_ml(p, slot0, n, tmp);
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kJoinThreads, 6) attend_join(const AttendParam
         const int per_q = nq <= 8 ? 32 : nq <= 32 ? 8 : nq <= 64 ? 4 : 1;
         for (int q0 = 0; q0 < nq; q0 += kJoinThreads / per_q) {
             const int q = q0 + tid / per_q, part = tid % per_q;
-            const int n = q < nq ? (p.row_len[info.y + q / p.group] + p.chunk - 1) / p.chunk : 0;
+            const int n = q < nq ? (min(p.row_len[info.y + q / p.group], info.x) + p.chunk - 1) / p.chunk : 0;
             const float2* ml = reinterpret_cast<const float2*>(p.ml) + static_cast<int64_t>(ag) * p.chunks * p.qp + q;
             float m = kNoMax, l = 0.f;
 #pragma unroll 4

@@ -157,14 +157,19 @@ __device__ __forceinline__ void tma_load_2d_hint(void* smem_dst, const void* tma
 // The table of sequences, in shared memory: every block forms the same one.  seq[a] = (first item,
 // longest row, shortest row, first row), one more entry at the end; returns the number of items.
 // Block 0 also writes it out for the joining kernel.  tmp: 33 ints.  The whole block takes part.
+// Where agent_rows falls anywhere, every sequence is refused: the search below needs it sorted, and so does
+// the joining kernel, which takes a row's length as checked if its sequence is not refused.
 __device__ __forceinline__ int form_table(const AttendParams& p, int4* seq, int* tmp, int qt) {
     const int tid = threadIdx.x, n_threads = blockDim.x;
+    bool falls = false;
     for (int a = tid; a <= p.agents; a += n_threads) {
         const int r0 = p.agent_rows[a], r1 = a < p.agents ? p.agent_rows[a + 1] : r0;
         const bool ok = r0 >= 0 && r1 >= r0 && r1 <= p.rows && r1 - r0 <= p.max_agent_rows;
         seq[a] = make_int4(ok ? 0 : -1, 0, INT32_MAX, r0);
+        falls |= r1 < r0;
     }
-    __syncthreads();
+    if (__syncthreads_or(falls))
+        for (int a = tid; a <= p.agents; a += n_threads) seq[a].x = -1;
     for (int r = tid; r < p.rows; r += n_threads) {
         int lo = 0, hi = p.agents;
         while (hi - lo > 1) {

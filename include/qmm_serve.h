@@ -81,7 +81,9 @@ qmm_status qmm_kv_append(const qmm_kv_dims* dims, void* pool, const int32_t* pag
  *                           sequence's rows and the heads of group g.
  * A row with row_len 0 sees nothing: its out is 0 and its lse -infinity.  What lies in slots
  * that a row does not see has no effect on it, NaN and infinity included.
- *  agent_rows: int32 [agents + 1], non-decreasing; a sequence may have no rows.
+ *  agent_rows: int32 [agents + 1], non-decreasing (else *err_word |= 4, and no sequence of the call
+ *              is attended to: every row is written as one that sees nothing, no weight is
+ *              written); a sequence may have no rows.
  *  row_len:    int32 [rows], 0 <= row_len[r] <= max_pages * page_tokens.
  *  q:          [rows][heads][head_dim], fp16 (bf16 with a BF16 pool), row r at r * q_stride
  *              elements; 16-byte aligned, q_stride a multiple of 8.
