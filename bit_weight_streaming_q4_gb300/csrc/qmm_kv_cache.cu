@@ -114,15 +114,19 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
     // this block's sequence and group of slots
     if (tid == 0) mine[0] = -1;
     __syncthreads();
+    // (where agent_rows falls anywhere, sequences could share rows, and be more than the grid holds: none is taken)
     int before = 0;
+    bool falls = false;
     for (int a0 = 0; a0 < p.agents; a0 += kAppendThreads) {
         const int a = a0 + tid;
         int n = 0, r0 = 0, nr = 0, len = 0;
         if (a < p.agents) {
             r0 = p.agent_rows[a];
-            nr = p.agent_rows[a + 1] - r0;
+            const int r1 = p.agent_rows[a + 1];
+            falls |= r1 < r0;
+            nr = r0 >= 0 && r1 >= r0 ? r1 - r0 : -1;
             len = p.cache_len[a];
-            const bool ok = r0 >= 0 && nr >= 0 && nr <= p.rows - r0 && len >= 0 && len <= p.cap && nr <= p.cap - len;
+            const bool ok = nr >= 0 && nr <= p.rows - r0 && len >= 0 && len <= p.cap && nr <= p.cap - len;
             if (!ok && blockIdx.x == 0 && g == 0) atomicOr(p.err, kErrRange);
             if (ok && nr > 0) n = (len + nr - 1) / 32 - len / 32 + 1;
         }
@@ -138,7 +142,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
         }
         before += sum;
     }
-    __syncthreads();
+    if (__syncthreads_or(falls)) return;
     const int a = mine[0];
     if (a < 0) return;
     const int base = mine[1], lo = max(mine[2], base), hi = min(mine[3], base + 32), row0 = mine[4] - mine[2];

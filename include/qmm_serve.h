@@ -59,7 +59,8 @@ typedef struct {
  *  k, v:       [rows][kv_heads][head_dim] of `type`, row r at r * k_stride (v_stride) elements:
  *              columns of a wider matrix, such as qmm_run's y, are taken in place.  Aligned
  *              to their element; 16-byte aligned rows are read faster.
- *  agent_rows: int32 [agents + 1], non-decreasing.  cache_len: int32 [agents], not changed.
+ *  agent_rows: int32 [agents + 1], non-decreasing (else *err_word |= 4, and nothing is appended).
+ *  cache_len:  int32 [agents], not changed.
  *  weight, pos: as above, or null.  The new slots' weight becomes 0 and, with row_pos
  *              (int32 [rows], or null) given, their pos row_pos[r].
  * F16 and BF16 pools take each value rounded once.  Q8_0, per 32 dims: d = fp16(max|x| / 127),
