@@ -126,14 +126,17 @@ __global__ void __launch_bounds__(kJoinThreads, 6) attend_join(const AttendParam
             const float ref = m == kNoMax ? 0.f : m;
             v = slices == 1 ? join_sum<D / 32>(p, slot0, n, ref, p.o, D, jsm) : join_sum<1>(p, slot0, n, ref, p.o + 32 * slice, D, jsm);
         }
+        // Nothing seen: no maximum, and no denominator either.  (A NaN is no maximum, but it is in l: a row whose
+        // scores are all NaN comes here with M = -infinity and l = NaN, and divides by it.)
+        const bool none = m == kNoMax && l == 0.f;
         if (tid < width) {
-            v = m == kNoMax ? 0.f : v / l;
+            v = none ? 0.f : v / l;
             const int64_t at = static_cast<int64_t>(block) * D + slice * 32 + tid;
             if (p.out_type == QMM_TYPE_F32) static_cast<float*>(p.out)[at] = v;
             else if (p.out_type == QMM_TYPE_F16) static_cast<__half*>(p.out)[at] = __float2half_rn(v);
             else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
         }
-        if (tid == 0 && slice == 0 && p.lse) p.lse[block] = m == kNoMax ? kNoMax : (m - kShift + log2f(l)) * 0.6931471805599453f;
+        if (tid == 0 && slice == 0 && p.lse) p.lse[block] = none ? kNoMax : (m - kShift + log2f(l)) * 0.6931471805599453f;
         return;
     }
 

@@ -81,7 +81,8 @@ qmm_status qmm_kv_append(const qmm_kv_dims* dims, void* pool, const int32_t* pag
  *     weight_out[a][g][t] = weight_in[a][g][t] + the sum of the softmax's t-th entries over the
  *                           sequence's rows and the heads of group g.
  * A row with row_len 0 sees nothing: its out is 0 and its lse -infinity.  What lies in slots
- * that a row does not see has no effect on it, NaN and infinity included.
+ * that a row does not see has no effect on it, NaN and infinity included; a row that sees a score that is
+ * NaN has NaN throughout out and lse.
  *  agent_rows: int32 [agents + 1], non-decreasing (else *err_word |= 4, and no sequence of the call
  *              is attended to: every row is written as one that sees nothing, no weight is
  *              written); a sequence may have no rows.
