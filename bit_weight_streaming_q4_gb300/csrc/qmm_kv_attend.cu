@@ -163,7 +163,8 @@ __global__ void __launch_bounds__(kJoinThreads, 6) attend_join(const AttendParam
             for (int c = part; c < n; c += per_q) {
                 const float2 v = ml[static_cast<int64_t>(c) * p.qp];
                 if (v.x > m) l *= exp2f(m - v.x), m = v.x;
-                if (v.x > kNoMax) l = fmaf(v.y, exp2f(v.x - m), l);
+                // (without a maximum v.y is 0, or the NaN of a chunk whose scores are all NaN)
+                l = v.x > kNoMax ? fmaf(v.y, exp2f(v.x - m), l) : l + v.y;
             }
             for (int k = per_q >> 1; k >= 1; k >>= 1) {
                 const float mo = __shfl_xor_sync(0xffffffffu, m, k), lo = __shfl_xor_sync(0xffffffffu, l, k);
@@ -172,8 +173,11 @@ __global__ void __launch_bounds__(kJoinThreads, 6) attend_join(const AttendParam
                 m = mn;
             }
             if (part == 0 && q < nq) {
-                ref[q] = m == kNoMax ? 0.f : m - kShift;
-                inv[q] = m == kNoMax ? 0.f : 1.f / l;
+                // A query whose denominator is NaN: every score that it sees has to give NaN, and a slot that it does not
+                // see (-infinity) nothing.  2^(x + 3.4e38) is infinity for the ones and 0 for the others; times 0.
+                const bool nan = l != l;
+                ref[q] = nan ? -3.402823466e38f : m == kNoMax ? 0.f : m - kShift;
+                inv[q] = nan || m == kNoMax ? 0.f : 1.f / l;
             }
         }
         __syncthreads();

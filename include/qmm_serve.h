@@ -82,7 +82,7 @@ qmm_status qmm_kv_append(const qmm_kv_dims* dims, void* pool, const int32_t* pag
  *                           sequence's rows and the heads of group g.
  * A row with row_len 0 sees nothing: its out is 0 and its lse -infinity.  What lies in slots
  * that a row does not see has no effect on it, NaN and infinity included; a row that sees a score that is
- * NaN has NaN throughout out and lse.
+ * NaN has NaN throughout out and lse, and makes the weights of the slots that it sees NaN.
  *  agent_rows: int32 [agents + 1], non-decreasing (else *err_word |= 4, and no sequence of the call
  *              is attended to: every row is written as one that sees nothing, no weight is
  *              written); a sequence may have no rows.
