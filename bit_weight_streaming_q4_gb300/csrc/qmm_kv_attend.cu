@@ -136,12 +136,12 @@ __global__ void __launch_bounds__(kJoinThreads, 6) attend_join(const AttendParam
             else if (p.out_type == QMM_TYPE_F16) static_cast<__half*>(p.out)[at] = __float2half_rn(v);
             else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
         }
-        if (tid == 0 && slice == 0 && p.lse) p.lse[block] = none ? kNoMax : (m - kShift + log2f(l)) * 0.6931471805599453f;
+        if (tid == 0 && slice == 0 && p.lse) p.lse[block] = none ? kNoMax : (m + log2f(l)) * 0.6931471805599453f;
         return;
     }
 
     // ---- weights: tokens by thread, queries in order
-    float* ref = jsm;           // [qp] M - kShift (the base-2 logarithm's part that l lacks)
+    float* ref = jsm;           // [qp] M
     float* inv = jsm + p.qp;    // [qp] 1 / l
     constexpr int kSlots = T * kJoinThreads;
     const int per = (p.cap + kSlots - 1) / kSlots;
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kJoinThreads, 6) attend_join(const AttendParam
                 // A query whose denominator is NaN: every score that it sees has to give NaN, and a slot that it does not
                 // see (-infinity) nothing.  2^(x + 3.4e38) is infinity for the ones and 0 for the others; times 0.
                 const bool nan = l != l;
-                ref[q] = nan ? -3.402823466e38f : m == kNoMax ? 0.f : m - kShift;
+                ref[q] = nan ? -3.402823466e38f : m == kNoMax ? 0.f : m;
                 inv[q] = nan || m == kNoMax ? 0.f : 1.f / l;
             }
         }

@@ -42,7 +42,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 64;            // tokens per tile
 constexpr int kTcTile = 128;         // tokens per tile of the tensor core kernel (head dimension 128)
-constexpr float kShift = 13.f;       // p's power of two in the partials: l = sum 2^(x - M + kShift)
+constexpr float kShift = 13.f;       // p's power of two at head dimensions 64 and 256; off again in the partials
 constexpr float kNoMax = -INFINITY;
 
 struct AttendParams {
@@ -55,8 +55,8 @@ struct AttendParams {
     float* weight_out;
     void* out;
     float* lse;                 // [rows][heads] or null
-    float* ml;                  // [sequence][KV head][chunk][qp][2]: M and l
-    float* o;                   // [sequence][KV head][chunk][qp][D]
+    float* ml;                  // [sequence][KV head][chunk][qp][2]: a reference M and l = sum 2^(x - M)
+    float* o;                   // [sequence][KV head][chunk][qp][D]: sum 2^(x - M) v
     float* scores;              // [sequence][KV head][qp / 4][chunks * chunk][4] x_t, or null without weights;
                                 // [..][2] in the last four if the sequence has at most two queries there
     int4* info;                 // [agents]: longest row (-1: refused), first row, rows, 0
@@ -584,7 +584,8 @@ __global__ void __launch_bounds__(kThreads, (Geo<FMT, D, NT>::blocks))
         }
         if (!live) break;
 
-        // ---- the item's partial
+        // ---- the item's partial (the shift comes off the sums: taken off M, it could be lost to a large M's spacing)
+        constexpr float kUnshift = 1.f / (1 << static_cast<int>(kShift));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -612,12 +613,12 @@ __global__ void __launch_bounds__(kThreads, (Geo<FMT, D, NT>::blocks))
                 float* po = p.o + (slot0 + qi) * D + 16 * warp * MW;
 #pragma unroll
                 for (int mt = 0; mt < MW; ++mt) {
-                    po[16 * mt + g8] = o[mt][nt][e];
-                    po[16 * mt + g8 + 8] = o[mt][nt][2 + e];
+                    po[16 * mt + g8] = o[mt][nt][e] * kUnshift;
+                    po[16 * mt + g8 + 8] = o[mt][nt][2 + e] * kUnshift;
                 }
                 if (warp == 0 && g8 == 0) {
                     const float4 r = *reinterpret_cast<const float4*>(red + qi * 4);
-                    *reinterpret_cast<float2*>(p.ml + (slot0 + qi) * 2) = make_float2(mx[nt][e], (r.x + r.y) + (r.z + r.w));
+                    *reinterpret_cast<float2*>(p.ml + (slot0 + qi) * 2) = make_float2(mx[nt][e], ((r.x + r.y) + (r.z + r.w)) * kUnshift);
                 }
             }
     }

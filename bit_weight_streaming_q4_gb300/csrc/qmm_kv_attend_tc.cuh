@@ -48,6 +48,8 @@ namespace kv {
 
 constexpr float kTcShift = 9.f;   // p's power of two ..
 constexpr float kSlack = 6.f;     // .. and how far a score may pass its reference: p <= 2^15
+constexpr float kFine = 4194304.f;  // 2^22: references below it hold sums with the two (fp32 is spaced by 1/4 at most
+                                    // there); a larger one stands alone, without shift and slack: p <= 1
 constexpr float kLowScale = 2048.f;  // p's low part is kept times this (its products have columns of their
                                      // own), so that 22 bits of p count down to 2^-33 of the reference's
 
@@ -79,7 +81,7 @@ struct TcGeo {
     static constexpr int off_dv = off_p + p_bufs * 2 * opnd;                             // q8_0: normalised V scales [2][4][128] fp16
     static constexpr int off_len = off_dv + (q8 ? 2 * 4 * kTcTile * 2 : 0);         // [2][N] tokens that a query sees
     static constexpr int off_lim = off_len + 2 * N * 4;                         // [N] reference + slack
-    static constexpr int off_sub = off_lim + N * 4;                             // [N] reference - kTcShift
+    static constexpr int off_sub = off_lim + N * 4;                             // [N] what comes off the scores: reference - kTcShift
     static constexpr int off_alpha = off_sub + N * 4;                           // [N]
     static constexpr int off_red = off_alpha + N * 4;                           // [group][4 warps][W]
     static constexpr int off_odd = off_red + 4 * N * 4;                         // [4] tokens to be taken query by query
@@ -583,8 +585,8 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
                                 w[b] = *reinterpret_cast<const uint16_t*>(vt + (me >> 6) * kQ8Half + 8192 + (b * 64 + (me & 63)) * 2) & 0x7FFFu;
                             miss = vmiss[vs] != 0;  // a page of the tile is outside the pool
                             if constexpr (G::eager) limits();
-                            f[0] = __low2float(as_h2(sc.x)), f[1] = __high2float(as_h2(sc.x));
-                            f[2] = __low2float(as_h2(sc.y)), f[3] = __high2float(as_h2(sc.y));
+                            f[0] = __low2float(as_h2(sc.x)) * p.c2, f[1] = __high2float(as_h2(sc.x)) * p.c2;
+                            f[2] = __low2float(as_h2(sc.y)) * p.c2, f[3] = __high2float(as_h2(sc.y)) * p.c2;
 #pragma unroll
                             for (int b = 0; b < 4; ++b) top = w[b] > 0x7C00u ? top : max(top, w[b]);  // (NaN scales do not count)
                             e = static_cast<float>(min(max(static_cast<int>(top >> 10), 1), 29) - 15);
@@ -592,7 +594,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
                         tc_wait_ld();
 #pragma unroll
                         for (int i = 0; i < B; ++i)
-                            x[c + i] = fmaf(v[3][i], f[3], fmaf(v[2][i], f[2], fmaf(v[1][i], f[1], v[0][i] * f[0]))) * p.c2;
+                            x[c + i] = fmaf(v[3][i], f[3], fmaf(v[2][i], f[2], fmaf(v[1][i], f[1], v[0][i] * f[0])));
                     }
                 } else {
                     float v[W / B][B];
@@ -627,8 +629,8 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
 #pragma unroll
                 for (int q = 0; q < W; q += 4) {
                     const float4 m = limit[q / 4];
-                    if constexpr (G::q8) x[q] += e, x[q + 1] += e, x[q + 2] += e, x[q + 3] += e;
-                    over |= x[q] > m.x || x[q + 1] > m.y || x[q + 2] > m.z || x[q + 3] > m.w;
+                    if constexpr (G::q8) over |= x[q] + e > m.x || x[q + 1] + e > m.y || x[q + 2] + e > m.z || x[q + 3] + e > m.w;
+                    else over |= x[q] > m.x || x[q + 1] > m.y || x[q + 2] > m.z || x[q + 3] > m.w;
                 }
                 bool moved = false;  // some reference moves
                 float4 base[W / 4];  // the references, as P takes them
@@ -647,17 +649,23 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
                     }
                     miss = *missed == t;
                     // (a NaN is no maximum: fmaxf passes it over)
-                    const float r = reduce_columns<W>(x, kNoMax, [](float a, float b) { return fmaxf(a, b); });
+                    float y[W];
+#pragma unroll
+                    for (int q = 0; q < W; ++q) y[q] = G::q8 ? x[q] + e : x[q];
+                    const float r = reduce_columns<W>(y, kNoMax, [](float a, float b) { return fmaxf(a, b); });
                     if (lane < W) red[w4 * W + lane] = r;
                     named_bar_sync(bar_id, 128);
                     if (me < W) {
                         float m = fmaxf(fmaxf(red[me], red[W + me]), fmaxf(red[2 * W + me], red[3 * W + me]));
                         if (fabsf(m) < 1e6f) m = ceilf(m * 16.f) * 0.0625f;  // (sums with the constants are then exact)
                         const bool passed = m > lim[me];
-                        alpha[me] = passed ? ex2(lim[me] - kSlack - m) : 1.f;  // (2^-inf = 0 the first time)
+                        const bool fine = fabsf(m) < kFine;
+                        const float base = fine ? m - kTcShift : m;
+                        // (what was formed with the old reference, by the difference of what was taken off; 0 the first time)
+                        alpha[me] = !passed ? 1.f : lim[me] == kNoMax ? 0.f : ex2(sub[me] - base);
                         if (passed) {
-                            lim[me] = m + kSlack;
-                            sub[me] = m - kTcShift;
+                            lim[me] = fine ? m + kSlack : m;
+                            sub[me] = base;
                         }
                     }
                     named_bar_sync(bar_id, 128);
@@ -696,8 +704,10 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
 #pragma unroll
                 for (int q = 0; q < W; q += 4) {
                     const float4 m = base[q / 4];
-                    x[q] = ex2(x[q] - m.x), x[q + 1] = ex2(x[q + 1] - m.y);
-                    x[q + 2] = ex2(x[q + 2] - m.z), x[q + 3] = ex2(x[q + 3] - m.w);
+                    x[q] -= m.x, x[q + 1] -= m.y, x[q + 2] -= m.z, x[q + 3] -= m.w;
+                    // (e after the reference is off: a large score's spacing could swallow it)
+                    if constexpr (G::q8) x[q] += e, x[q + 1] += e, x[q + 2] += e, x[q + 3] += e;
+                    x[q] = ex2(x[q]), x[q + 1] = ex2(x[q + 1]), x[q + 2] = ex2(x[q + 2]), x[q + 3] = ex2(x[q + 3]);
                 }
 #pragma unroll
                 for (int q = 0; q < W; q += B == 8 ? 8 : 4) {
@@ -834,7 +844,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
             if (lane < W) red[w4 * W + lane] = r;
             named_bar_sync(bar_id, 128);
             if (me < W && q0 + me < it.nq) {
-                const float m = lim[me] == kNoMax ? kNoMax : sub[me] + kShift;
+                const float m = lim[me] == kNoMax ? kNoMax : sub[me];  // (as it was taken off, so that parts meet exactly)
                 const float s = (red[me] + red[W + me]) + (red[2 * W + me] + red[3 * W + me]);
                 *reinterpret_cast<float2*>(p.ml + (slot0 + me) * 2) = make_float2(m, s);
             }
