@@ -18,11 +18,13 @@
 //   last four   q8_0 only: K and V quants to fp16 in tensor memory, as A operands (or eight, four for each)
 // 16-bit pools: the swizzled tiles are A operands as they come, K by rows and V transposed
 // (M-contiguous).  q8_0: K's quants are exact in fp16, one accumulator per 32-dim block takes its
-// scale in fp32.  V's scale depends on token and block: a token's exponent e_t = max over blocks of
-// its scales' exponents joins the softmax's reference (y_t = x_t + e_t, M = max y_t), so that
+// scale in fp32.  V's scale depends on token and block: the exponent of a token's largest scale (-7 at least)
+// is its e_t and joins the softmax's reference (y_t = x_t + e_t, M = max y_t), so that
 // p^ = 2^(y_t - M) <= 1 whatever the scales, and V's element, quant times normalised scale
-// (scale 2^-e_t), is split into two fp16 parts without error (product, its error by fma); three of
-// the four products of parts count.  No scale of the format can then overflow or vanish.
+// (scale 2^(8 - e_t), below 2^9: the product is at most 65,504), is split into two fp16 parts without error
+// (product, its error by fma); three of the four products of parts count.  That holds while none of the
+// token's scales other than 0 has an exponent more than 22 below the largest's, which takes one of 512 or more;
+// what the product lacks of other tokens is added one by one in fp32.
 //
 // A query's reference is its first tile's maximum and moves only when a score passes it by more than
 // 2^kSlack (a vote per tile; then the group forms the tile's maxima and rescales what it
@@ -49,7 +51,9 @@ namespace kv {
 constexpr float kTcShift = 9.f;   // p's power of two ..
 constexpr float kSlack = 6.f;     // .. and how far a score may pass its reference: p <= 2^15
 constexpr float kFine = 4194304.f;  // 2^22: references below it hold sums with the two (fp32 is spaced by 1/4 at most
-                                    // there); a larger one stands alone, without shift and slack: p <= 1
+                                    // there); a larger one stands alone, without shift and slack: p <= 1 (q8_0, whose
+                                    // exponent in -7 .. 15 a large score may round away: 2^15)
+constexpr int kVShift = 8;        // q8_0: V's power of two, off again where the outputs are read
 constexpr float kLowScale = 2048.f;  // p's low part is kept times this (its products have columns of their
                                      // own), so that 22 bits of p count down to 2^-33 of the reference's
 
@@ -88,8 +92,8 @@ struct TcGeo {
     static constexpr int off_bar = off_odd + 16;
     static constexpr int bars = 2 * k_slots + 2 * v_slots + 4 + 6 + 4 + 2;
     static constexpr int off_item = (off_bar + bars * 8 + 15) / 16 * 16;        // [2] of ItemRec
-    static constexpr int off_misc = off_item + 2 * 32;                          // tmp[33], abort, accumulate[2], tmem, miss[v_slots], dead and missed by group
-    static constexpr int off_seq = (off_misc + 48 * 4 + 15) / 16 * 16;
+    static constexpr int off_misc = off_item + 2 * 32;                          // tmp[33], abort, accumulate[2], tmem, miss[v_slots], dead and missed by group, wide by group
+    static constexpr int off_seq = (off_misc + 52 * 4 + 15) / 16 * 16;
     static constexpr int smem(int agents) { return 1024 + off_seq + (agents + 1) * 16; }
 };
 
@@ -103,6 +107,26 @@ __device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t saddr, uint32_t 
 __device__ __forceinline__ uint64_t smem_desc_sw64_mn(uint32_t saddr, uint32_t lead) {
     return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
            (static_cast<uint64_t>(512 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(4) << 61);
+}
+// V's scales of a q8_0 token, their signs off: the largest (NaN does not count); its biased exponent, which comes off
+// the scales (that of 2^-7 at least: its inverse times 2^kVShift is then one fp16 number, and smaller scales
+// need no more room; infinity as 65,504); and whether some scale other than 0 is then below what fp16 holds
+// exactly, its own exponent (counted from 1) being more than 22 below.  A token whose largest is below kWide never is.
+constexpr uint32_t kWide = 24u << 10;  // 512
+__device__ __forceinline__ uint32_t largest_scale(const uint32_t (&w)[4]) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) top = w[b] > 0x7C00u ? top : max(top, w[b]);
+    return top;
+}
+__device__ __forceinline__ int scale_exponent(uint32_t top) { return min(max(static_cast<int>(top >> 10), 8), 30); }
+__device__ __forceinline__ __half scale_inverse(int exponent) { return __ushort_as_half(static_cast<uint16_t>((30 + kVShift - exponent) << 10)); }
+__device__ __forceinline__ bool scales_far_apart(const uint32_t (&w)[4]) {
+    const int top = scale_exponent(largest_scale(w));
+    bool apart = false;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) apart |= w[b] != 0 && max(static_cast<int>(w[b] >> 10), 1) + 22 < top;
+    return apart;
 }
 // Byte of (token, column) of P: 64-byte rows by token, in blocks of 32 columns.
 __device__ __forceinline__ int p_byte(int token, int col) {
@@ -139,13 +163,15 @@ __device__ __forceinline__ void tmem_store4(uint32_t taddr, const float* v) {
 }
 template <int B>
 __device__ __forceinline__ void tmem_load_n(uint32_t taddr, float (&v)[B]) {
-    static_assert(B == 8 || B == 12);
-    tmem_load8(taddr, v);
+    static_assert(B == 4 || B == 8 || B == 12);
+    if constexpr (B == 4) tmem_load4(taddr, v);
+    else tmem_load8(taddr, v);
     if constexpr (B == 12) tmem_load4(taddr + 8, v + 8);
 }
 template <int B>
 __device__ __forceinline__ void tmem_store_n(uint32_t taddr, const float (&v)[B]) {
-    tmem_store8(taddr, v);
+    if constexpr (B == 4) tmem_store4(taddr, v);
+    else tmem_store8(taddr, v);
     if constexpr (B == 12) tmem_store4(taddr + 8, v + 8);
 }
 
@@ -279,7 +305,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
         fence_mbar_init();
     }
     if (tid < 4) odd_sm[tid] = 0;
-    if (tid < 6) tmp[41 + tid] = -(tid & 1);
+    if (tid < 9) tmp[41 + tid] = tid < 6 ? -(tid & 1) : -1;
     if (warp == 1) {
         tmem_alloc(tmem_sm, G::cols);
         tmem_relinquish();
@@ -499,6 +525,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
         float* red = red_sm + grp * 4 * W;     // [4][W]
         volatile int* dead = tmp + 41 + 2 * grp;    // some thread's wait ran out
         volatile int* missed = dead + 1;            // the last tile with a missing page
+        volatile int* wide_sm = tmp + 47 + grp;     // q8_0: the last tile with a token whose scales may lie far apart
         int t = 0, k = 0;
         uint32_t odds = 0;                     // tiles with marked tokens so far
         auto last_product = [&] { await(odone + (t - 1) % G::p_bufs, ((t - 1) / G::p_bufs) & 1); };  // of tile t - 1
@@ -507,6 +534,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
         float* po = nullptr;                   // where they go, or null
         int left = 0;                          // queries from c0 on
         auto drain = [&](uint32_t cols) {
+            constexpr float kBack = G::q8 ? 1.f / (1 << kVShift) : 1.f;
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < W; c += B) {
@@ -516,7 +544,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
                 tc_wait_ld();
 #pragma unroll
                 for (int i = 0; i < B; ++i)
-                    if (c + i < left) po[(c + i) * D] = fmaf(v[1][i], 1.f / kLowScale, v[0][i]);
+                    if (c + i < left) po[(c + i) * D] = fmaf(v[1][i], kBack / kLowScale, v[0][i] * kBack);
             }
             po = nullptr;
         };
@@ -564,7 +592,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
                 // than the slack, takes the long way
                 float x[W], e = 0.f;
                 float4 limit[W / 4];
-                bool miss;
+                bool miss, wide = false;  // (q8_0: the token's V scales may lie far apart)
                 auto limits = [&] {
 #pragma unroll
                     for (int q = 0; q < W; q += 4) limit[q / 4] = *reinterpret_cast<const float4*>(lim + q);
@@ -579,7 +607,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
                         if (c == 0) {
                             // the token's K scales and the exponent of its largest V scale
                             const uint2 sc = *reinterpret_cast<const uint2*>(sm + ksl * G::half + (me >> 6) * kQ8Half + 8192 + (me & 63) * 8);
-                            uint32_t w[4], top = 0;
+                            uint32_t w[4];
 #pragma unroll
                             for (int b = 0; b < 4; ++b)
                                 w[b] = *reinterpret_cast<const uint16_t*>(vt + (me >> 6) * kQ8Half + 8192 + (b * 64 + (me & 63)) * 2) & 0x7FFFu;
@@ -587,9 +615,9 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
                             if constexpr (G::eager) limits();
                             f[0] = __low2float(as_h2(sc.x)) * p.c2, f[1] = __high2float(as_h2(sc.x)) * p.c2;
                             f[2] = __low2float(as_h2(sc.y)) * p.c2, f[3] = __high2float(as_h2(sc.y)) * p.c2;
-#pragma unroll
-                            for (int b = 0; b < 4; ++b) top = w[b] > 0x7C00u ? top : max(top, w[b]);  // (NaN scales do not count)
-                            e = static_cast<float>(min(max(static_cast<int>(top >> 10), 1), 29) - 15);
+                            const uint32_t top = largest_scale(w);
+                            wide = top >= kWide;
+                            e = static_cast<float>(scale_exponent(top) - 15);
                         }
                         tc_wait_ld();
 #pragma unroll
@@ -624,7 +652,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
                         else if (q < mine) *reinterpret_cast<float2*>(at + (q >> 2) * plane - 2 * tok) = make_float2(x[q], x[q + 1]);
                     }
                 }
-                bool over = !live || miss;
+                bool over = !live || miss || wide;
                 if constexpr (!G::eager) limits();
 #pragma unroll
                 for (int q = 0; q < W; q += 4) {
@@ -641,6 +669,8 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
                 if constexpr (G::eager) bases();
                 if (!live) *dead = 1;
                 if (miss) *missed = t;
+                if (G::q8 && wide) *wide_sm = t;
+                bool some_wide = false;
                 if (bar_or(bar_id, 128, over)) {
                     if (*dead) {
                         stop = true;
@@ -648,6 +678,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
                         break;
                     }
                     miss = *missed == t;
+                    some_wide = G::q8 && *wide_sm == t;
                     // (a NaN is no maximum: fmaxf passes it over)
                     float y[W];
 #pragma unroll
@@ -677,7 +708,7 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
                     }
                     if constexpr (G::eager) bases();
                 }
-                const bool edge = miss || tb + kTcTile > it.minlen;
+                const bool edge = miss || some_wide || tb + kTcTile > it.minlen;
                 const bool fresh = tb == it.tok0;  // the outputs hold nothing yet
                 if (!p_free) await(odone + t % G::p_bufs, (t / G::p_bufs - 1) & 1);
                 if (moved && !fresh) {
@@ -732,15 +763,20 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
                     // missing page) V holds anything and becomes zero (q8_0: its scales do, in the
                     // converting warps).  One that some queries see and whose V (q8_0: a scale) is
                     // not finite is added query by query, to those that see it, and is zero in the
-                    // product.  (All groups come to the same answers.)
-                    bool odd = false;
+                    // product.  So is, to all, what the product lacks of a q8_0 token whose scales lie far
+                    // apart.  (All groups come to the same answers.)
                     const bool gone = miss || tok >= it.end;
+                    bool odd = false;
                     auto piece = [&](int c) { return reinterpret_cast<uint4*>(vt + (c >> 3) * (kTcTile * 128) + me * 128 + (((c & 7) ^ (me & 7)) << 4)); };
-                    if (!gone && tok >= it.minlen) {
+                    if (!gone && (G::q8 || tok >= it.minlen)) {
                         if constexpr (G::q8) {
+                            uint32_t w[4];
 #pragma unroll
                             for (int b = 0; b < 4; ++b)
-                                odd |= (*reinterpret_cast<const uint16_t*>(vt + (me >> 6) * kQ8Half + 8192 + (b * 64 + (me & 63)) * 2) & 0x7C00u) == 0x7C00u;
+                                w[b] = *reinterpret_cast<const uint16_t*>(vt + (me >> 6) * kQ8Half + 8192 + (b * 64 + (me & 63)) * 2) & 0x7FFFu;
+                            odd = scales_far_apart(w);
+#pragma unroll
+                            for (int b = 0; b < 4; ++b) odd |= tok >= it.minlen && w[b] >= 0x7C00u;
                         } else {
                             constexpr uint32_t ex = BF ? 0x7F80u : 0x7C00u;
                             auto bad = [&](uint32_t w) { return (w & ex) == ex || ((w >> 16) & ex) == ex; };
@@ -759,15 +795,16 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
                             last_product();
                             tc_fence_after();
                         }
+                        constexpr int S = 4;  // (few registers: this is rare, and the loop around it has none to spare)
 #pragma unroll 1
-                        for (int c = 0; c < W; c += B) {
-                            float v[B];
+                        for (int c = 0; c < W; c += S) {
+                            float v[S];
                             if (holds) {
-                                tmem_load_n<B>(ocol + c, v);
+                                tmem_load_n<S>(ocol + c, v);
                                 tc_wait_ld();
                             } else {
 #pragma unroll
-                                for (int i = 0; i < B; ++i) v[i] = 0.f;
+                                for (int i = 0; i < S; ++i) v[i] = 0.f;
                             }
 #pragma unroll 1
                             for (int j = 0; j < kTcTile; ++j) {
@@ -775,21 +812,29 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
                                 float y;  // V of token j, dim me (q8_0: by its normalised scale)
                                 if constexpr (G::q8) {
                                     const uint8_t* rec = vt + (j >> 6) * kQ8Half;
-                                    const float d = __half2float(*reinterpret_cast<const __half*>(rec + 8192 + ((me >> 5) * 64 + (j & 63)) * 2));
-                                    uint32_t top = 0;
+                                    const __half d = *reinterpret_cast<const __half*>(rec + 8192 + ((me >> 5) * 64 + (j & 63)) * 2);
+                                    uint32_t w[4];
+                                    bool zeroed = false;  // (not finite: the converting warps took zeros)
+#pragma unroll
                                     for (int b = 0; b < 4; ++b) {
-                                        const uint32_t w = *reinterpret_cast<const uint16_t*>(rec + 8192 + (b * 64 + (j & 63)) * 2) & 0x7FFFu;
-                                        top = w > 0x7C00u ? top : max(top, w);
+                                        w[b] = *reinterpret_cast<const uint16_t*>(rec + 8192 + (b * 64 + (j & 63)) * 2) & 0x7FFFu;
+                                        zeroed |= tb + j >= it.minlen && w[b] >= 0x7C00u;
                                     }
-                                    const int ej = min(max(static_cast<int>(top >> 10), 1), 29) - 15;
-                                    y = static_cast<float>(static_cast<int8_t>(rec[me * 64 + (j & 63)])) * (d * __int_as_float((127 - ej) << 23));
+                                    const int ej = scale_exponent(largest_scale(w));
+                                    const float quant = static_cast<float>(static_cast<int8_t>(rec[me * 64 + (j & 63)]));
+                                    y = quant * (__half2float(d) * __int_as_float((142 + kVShift - ej) << 23));
+                                    if (!zeroed) {  // scales far apart: what the product lacks
+                                        const __half n = __hmul(d, scale_inverse(ej)), z = __float2half_rn(quant), hi = __hmul(z, n);
+                                        // (an infinite one is in it already)
+                                        y = isfinite(y) ? y - (__half2float(hi) + __half2float(__hfma(z, n, __hneg(hi)))) : 0.f;
+                                    }
                                 } else {
                                     const uint32_t u = *reinterpret_cast<const uint16_t*>(
                                         vt + (me >> 6) * (kTcTile * 128) + j * 128 + ((((me & 63) >> 3) ^ (j & 7)) << 4) + (me & 7) * 2);
                                     y = BF ? __uint_as_float(u << 16) : __half2float(__ushort_as_half(static_cast<uint16_t>(u)));
                                 }
 #pragma unroll
-                                for (int i = 0; i < B; ++i) {
+                                for (int i = 0; i < S; ++i) {
                                     const int q = c + i;
                                     const uint32_t h = *reinterpret_cast<const uint16_t*>(pt + p_byte(j, c0 + q));
                                     const uint32_t u = *reinterpret_cast<const uint16_t*>(pt + p_byte(j, N + c0 + q));
@@ -799,10 +844,10 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
                                     if (tb + j < qlen[q]) v[i] = fmaf(pr, y, v[i]);
                                 }
                             }
-                            tmem_store_n<B>(ocol + c, v);
+                            tmem_store_n<S>(ocol + c, v);
                             if (!holds) {
-                                const float zero[B] = {};
-                                tmem_store_n<B>(ocol + N + c, zero);
+                                const float zero[S] = {};
+                                tmem_store_n<S>(ocol + N + c, zero);
                             }
                         }
                         tc_wait_st();
@@ -922,16 +967,15 @@ __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, 
                 // ---- V: normalised scales by token, then elements by dim
                 const int tok = tb + me;
                 const uint8_t* sc = vt + (me >> 6) * kQ8Half + 8192 + slot * 2;
-                uint32_t d[4], top = 0;
+                uint32_t d[4], w[4];
                 bool odd = false;
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     d[b] = *reinterpret_cast<const uint16_t*>(sc + b * 128);
-                    const uint32_t w = d[b] & 0x7FFFu;
-                    top = w > 0x7C00u ? top : max(top, w);
+                    w[b] = d[b] & 0x7FFFu;
                     odd |= (d[b] & 0x7C00u) == 0x7C00u;
                 }
-                const __half inv = __ushort_as_half(static_cast<uint16_t>((30 - min(max(static_cast<int>(top >> 10), 1), 29)) << 10));
+                const __half inv = scale_inverse(scale_exponent(largest_scale(w)));
                 const bool none = vmiss[vs] != 0 || tok >= it.end || (odd && tok >= it.minlen);
                 __half* dt = dv + (t & 1) * 4 * kTcTile;
 #pragma unroll

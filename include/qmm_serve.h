@@ -96,7 +96,9 @@ qmm_status qmm_kv_append(const qmm_kv_dims* dims, void* pool, const int32_t* pag
  *              call's kernels finish.
  * A row's out and lse are bit-identical whatever the other rows and sequences of the call.
  * Scores, softmax and sums are fp32; the probabilities enter the product with V as the sum of
- * two 16-bit parts (relative error 2^-22; 2^-17 with BF16).
+ * two 16-bit parts (relative error 2^-22, or 2^-38 of the row's largest one where that is more;
+ * 2^-17 with BF16).  With Q8_0 the same holds of a probability times its token's largest V scale,
+ * and V's elements are exact whatever the scales of a token's blocks.
  * Rows of no sequence set *err_word |= 4 and are written as rows that see nothing.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, SCRATCH_TOO_SMALL, NO_DEVICE, CUDA.
  */
