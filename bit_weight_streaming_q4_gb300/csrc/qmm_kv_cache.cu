@@ -594,9 +594,10 @@ __global__ void __launch_bounds__(kMoveThreads) kv_evict_move(const EvictParams 
     const int moved = p.moved[ag];
     // source slots >= budget > destination slots: nothing read here is written here
     for (int i = first; i < moved; i += step) {
-        const int src = from[i].x, dst = to[i].x;
-        p.weight_out[base + dst] = p.weight[base + src];
-        p.pos_out[base + dst] = p.pos[base + src];
+        const int2 src = from[i], dst = to[i];
+        if (src.y < 0 || dst.y < 0) continue;  // (K and V stay: so do the slots' numbers)
+        p.weight_out[base + dst.x] = p.weight[base + src.x];
+        p.pos_out[base + dst.x] = p.pos[base + src.x];
     }
     if constexpr (q8) {
         // a warp moves 32 tokens, a lane each, one fifth at a time: K with the scales, or 32 dims of V.

@@ -123,7 +123,8 @@ qmm_status qmm_kv_attend(const qmm_kv_dims* dims, const void* pool, const int32_
  *              below len_out[a] only; may be weight and pos themselves.
  *  len_out:    int32 [agents] = min(cache_len[a], keep[a]); must not be cache_len.
  *  workspace:  16-byte aligned, at least qmm_kv_evict_workspace_bytes bytes.
- * A page table entry outside the pool leaves the tokens concerned unmoved.
+ * A page table entry outside the pool leaves the tokens concerned unmoved, with their weight and pos: the
+ * slots that they would have left and entered keep what they hold.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, SCRATCH_TOO_SMALL, NO_DEVICE, CUDA.
  */
 qmm_status qmm_kv_evict_workspace_bytes(const qmm_kv_dims* dims, int64_t* bytes);
