@@ -98,7 +98,10 @@ class KvPlan:
     call, so that layers can share a plan: a uint8 tensor of pool_pages * kv_heads * 17,408 bytes,
     or a 16-bit one of pool_pages * kv_heads * 2 * page_tokens * head_dim elements.
     max_rows / max_agent_rows bound the rows of an attend call, and those of one sequence.
-    Calls of one plan share its workspace: order them on one stream."""
+    Calls of one plan share its workspace: those on different streams have to be ordered by the caller.
+    A workspace is allocated at the first call that needs it, as memory of that call's stream, and
+    goes back to the allocator behind the work of every stream that calls went to; a stream that is
+    handed to a call has to outlive the plan."""
 
     def __init__(self, page_table, *, format: str, heads: int, kv_heads: int, head_dim: int, page_tokens: int,
                  pool_pages: int, max_rows: int, max_agent_rows: int | None = None):
@@ -120,9 +123,11 @@ class KvPlan:
         self._q_dtype = _torch.bfloat16 if format == "bf16" else _torch.float16
         self._pool_size = pool_pages * kv_heads * (17408 if format == "q8_0" else 2 * page_tokens * head_dim)
         self._scale = head_dim ** -0.5
-        self.error_word = _torch.zeros(1, dtype=_i32, device=page_table.device)
+        # (a copy from the host: it is there, on any stream, when the constructor returns)
+        self.error_word = _torch.tensor([0], dtype=_i32, device=page_table.device)
         self._err, self._table = self.error_word.data_ptr(), page_table.data_ptr()
         self._workspace = {}
+        self._streams = {}  # handles of the calls' streams, and the streams as torch knows them
         lib = load()
         self._append, self._attend, self._evict = lib.qmm_kv_append, lib.qmm_kv_attend, lib.qmm_kv_evict
         self._bytes("qmm_kv_evict_workspace_bytes")  # refuses dims that no call takes
@@ -132,13 +137,29 @@ class KvPlan:
         _q._check(getattr(load(), name)(self._ref, *args, ctypes.byref(n)), name)
         return n.value
 
-    def _space(self, kind: str):
-        """Address and bytes of a kind of call's workspace, allocated at its first use and kept."""
+    def _on(self, pool, stream: int | None) -> int:
+        """The call's stream, of which the allocator is told at its first call."""
+        if stream is None:
+            stream = _stream(pool)
+        if stream not in self._streams:
+            device = self.page_table.device
+            s = _torch.cuda.ExternalStream(stream, device) if stream else _torch.cuda.default_stream(device)
+            for t in [self.error_word] + [w[2] for w in self._workspace.values()]:
+                t.record_stream(s)
+            self._streams[stream] = s
+        return stream
+
+    def _space(self, kind: str, stream: int):
+        """Address and bytes of a kind of call's workspace, allocated for the stream of its first use and kept."""
         w = self._workspace.get(kind)
         if w is None:
             n = self._bytes("qmm_kv_evict_workspace_bytes") if kind == "evict" else \
                 self._bytes("qmm_kv_attend_workspace_bytes", int(kind == "weights"))
-            t = _torch.empty(n, dtype=_torch.uint8, device=self.page_table.device)
+            # (not for torch's current stream, whose pending work may still use the block that it gets)
+            with _torch.cuda.stream(self._streams[stream]):
+                t = _torch.empty(n, dtype=_torch.uint8, device=self.page_table.device)
+            for s in self._streams.values():
+                t.record_stream(s)
             w = self._workspace[kind] = (t.data_ptr(), n, t)
         return w
 
@@ -178,7 +199,7 @@ class KvPlan:
             _vector("cache_len", cache_len, _i32, self.agents), kp, ks, vp, vs, kind, rows,
             0 if weight is None else _vector("weight", weight, _f32, self._slots),
             0 if pos is None else _vector("pos", pos, _i32, self._slots),
-            0 if row_pos is None else _vector("row_pos", row_pos, _i32, rows), self._err, _stream(pool) if stream is None else stream)
+            0 if row_pos is None else _vector("row_pos", row_pos, _i32, rows), self._err, self._on(pool, stream))
         if st:
             raise _q.QmmError(st, "qmm_kv_append")
 
@@ -198,14 +219,14 @@ class KvPlan:
         kind = _types.get(out.dtype)
         if kind is None or out.shape != q.shape or not out.is_contiguous() or not out.is_cuda:
             _refuse("out", f"a contiguous fp32, fp16 or bf16 CUDA tensor [{rows}, {self.heads}, {self.head_dim}]")
-        ws, ws_bytes, _ = self._space("attend" if weight_out is None else "weights")
+        stream = self._on(pool, stream)
+        ws, ws_bytes, _ = self._space("attend" if weight_out is None else "weights", stream)
         st = self._attend(
             self._ref, self._pool(pool), self._table, _vector("agent_rows", agent_rows, _i32, self.agents + 1),
             _vector("row_len", row_len, _i32, rows), qp, qs, rows, self._scale if scale is None else scale, out.data_ptr(), kind,
             0 if lse is None else _vector("lse", lse, _f32, rows * self.heads),
             0 if weight_in is None else _vector("weight_in", weight_in, _f32, self._slots),
-            0 if weight_out is None else _vector("weight_out", weight_out, _f32, self._slots), ws, ws_bytes, self._err,
-            _stream(pool) if stream is None else stream)
+            0 if weight_out is None else _vector("weight_out", weight_out, _f32, self._slots), ws, ws_bytes, self._err, stream)
         if st:
             raise _q.QmmError(st, "qmm_kv_attend")
 
@@ -216,14 +237,15 @@ class KvPlan:
         cache_len, keep, len_out: int32 [agents] (keep < 0: no limit); protect_from: int32
         [agents] or None; weight_out and pos_out may be weight and pos.  Slots from len_out on
         are free afterwards."""
-        ws, ws_bytes, _ = self._space("evict")
+        stream = self._on(pool, stream)
+        ws, ws_bytes, _ = self._space("evict", stream)
         st = self._evict(
             self._ref, self._pool(pool), self._table, _vector("cache_len", cache_len, _i32, self.agents),
             _vector("keep", keep, _i32, self.agents), sink,
             0 if protect_from is None else _vector("protect_from", protect_from, _i32, self.agents),
             _vector("weight", weight, _f32, self._slots), _vector("pos", pos, _i32, self._slots),
             _vector("weight_out", weight_out, _f32, self._slots), _vector("pos_out", pos_out, _i32, self._slots),
-            _vector("len_out", len_out, _i32, self.agents), ws, ws_bytes, self._err, _stream(pool) if stream is None else stream)
+            _vector("len_out", len_out, _i32, self.agents), ws, ws_bytes, self._err, stream)
         if st:
             raise _q.QmmError(st, "qmm_kv_evict")
 
