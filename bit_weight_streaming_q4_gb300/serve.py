@@ -5,7 +5,7 @@ table, the workspace and the error word -- and appends to the cache, attends ove
 from it; ``logprobs`` reads the lm_head's output.  As in ``qmm``, every step runs in the library's
 CUDA kernels, there is no fallback, and PyTorch supplies only device memory and streams.  Calls go
 to the current stream unless ``stream`` is given; a tensor last written on another stream has to be
-ordered before them by the caller.
+ordered before them by the caller.  All tensors of a call are on one device, the current one.
 
 A small call takes about as long here as on the GPU, so the checks below are plain comparisons and
 form their messages only to raise them."""
@@ -59,34 +59,36 @@ def load():
     return _lib
 
 
-_torch = _f32 = _i32 = _types = _raw = None
+_torch = _f32 = _i32 = _types = _raw = _here = None
 
 
 def _setup():
     """torch and its types, looked up at the first use (the module imports without torch)."""
-    global _torch, _f32, _i32, _types, _raw
+    global _torch, _f32, _i32, _types, _raw, _here
     import torch
     # (the handle alone, without the Stream object around it: 0.1 us instead of 3)
     _raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+    _here = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _f32, _i32 = torch.float32, torch.int32
     _types = {torch.float32: TYPE_F32, torch.float16: TYPE_F16, torch.bfloat16: TYPE_BF16}
     _torch = torch
-
-
-def _stream(t) -> int:
-    """The current stream of tensor t's device."""
-    return _raw(t.get_device())
 
 
 def _refuse(name, what):
     raise ValueError(f"{name}: {what}")
 
 
-def _vector(name, t, dtype, n):
-    """Address of a contiguous CUDA tensor of n elements."""
-    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
-        _refuse(name, f"a contiguous {dtype} CUDA tensor of {n} elements")
+def _vector(name, t, dtype, n, device):
+    """Address of a contiguous CUDA tensor of n elements on a device."""
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != device:
+        _refuse(name, f"a contiguous {dtype} CUDA tensor of {n} elements on device {device}")
     return t.data_ptr()
+
+
+def _current(device):
+    """The library launches on the current device: it has to be the tensors'."""
+    if _here() != device:
+        _refuse("device", f"the tensors are on {device}, the current device is {_here()}")
 
 
 class KvPlan:
@@ -116,6 +118,7 @@ class KvPlan:
         self.dims = KvDims(FORMATS[format], heads, kv_heads, head_dim, page_tokens, agents, max_pages,
                            int(max_agent_rows or max_rows), pool_pages)
         self.agents, self.heads, self.kv_heads, self.head_dim = agents, heads, kv_heads, head_dim
+        self.device = page_table.get_device()
         self.cap = max_pages * page_tokens
         self._slots = agents * kv_heads * self.cap
         self._ref = ctypes.byref(self.dims)
@@ -137,10 +140,10 @@ class KvPlan:
         _q._check(getattr(load(), name)(self._ref, *args, ctypes.byref(n)), name)
         return n.value
 
-    def _on(self, pool, stream: int | None) -> int:
+    def _on(self, stream: int | None) -> int:
         """The call's stream, of which the allocator is told at its first call."""
         if stream is None:
-            stream = _stream(pool)
+            stream = _raw(self.device)
         if stream not in self._streams:
             device = self.page_table.device
             s = _torch.cuda.ExternalStream(stream, device) if stream else _torch.cuda.default_stream(device)
@@ -164,15 +167,20 @@ class KvPlan:
         return w
 
     def _pool(self, pool) -> int:
-        if pool.dtype is not self._pool_dtype or pool.numel() != self._pool_size or not pool.is_contiguous() or not pool.is_cuda:
-            _refuse("pool", f"a contiguous {self._pool_dtype} CUDA tensor of {self._pool_size} elements")
+        _current(self.device)
+        if pool.dtype is not self._pool_dtype or pool.numel() != self._pool_size or not pool.is_contiguous() or \
+                pool.get_device() != self.device:
+            _refuse("pool", f"a contiguous {self._pool_dtype} CUDA tensor of {self._pool_size} elements on device {self.device}")
         return pool.data_ptr()
+
+    def _vector(self, name, t, dtype, n) -> int:
+        return _vector(name, t, dtype, n, self.device)
 
     def _rows_of(self, name, t, dtype, heads):
         """Address and row stride of [rows, heads, head_dim] with any row stride."""
         s = t.shape
-        if len(s) != 3 or s[1] != heads or s[2] != self.head_dim or t.dtype is not dtype or not t.is_cuda:
-            _refuse(name, f"a {dtype} CUDA tensor [rows, {heads}, {self.head_dim}]")
+        if len(s) != 3 or s[1] != heads or s[2] != self.head_dim or t.dtype is not dtype or t.get_device() != self.device:
+            _refuse(name, f"a {dtype} CUDA tensor [rows, {heads}, {self.head_dim}] on device {self.device}")
         st = t.stride()
         if s[0] > 0 and (st[2] != 1 or (heads > 1 and st[1] != self.head_dim)):
             _refuse(name, "contiguous but for the row stride")
@@ -186,6 +194,7 @@ class KvPlan:
         projection's output are taken in place).  cache_len: int32 [agents], tokens cached
         before the call (not changed).  weight / pos: the slots' arrays, whose new entries become
         0 and row_pos."""
+        at = self._pool(pool)
         kind = _types.get(k.dtype)
         if kind is None:
             _refuse("k", "fp32, fp16 or bf16")
@@ -195,11 +204,11 @@ class KvPlan:
         if v.shape[0] != rows:
             _refuse("v", f"{rows} rows, as k")
         st = self._append(
-            self._ref, self._pool(pool), self._table, _vector("agent_rows", agent_rows, _i32, self.agents + 1),
-            _vector("cache_len", cache_len, _i32, self.agents), kp, ks, vp, vs, kind, rows,
-            0 if weight is None else _vector("weight", weight, _f32, self._slots),
-            0 if pos is None else _vector("pos", pos, _i32, self._slots),
-            0 if row_pos is None else _vector("row_pos", row_pos, _i32, rows), self._err, self._on(pool, stream))
+            self._ref, at, self._table, self._vector("agent_rows", agent_rows, _i32, self.agents + 1),
+            self._vector("cache_len", cache_len, _i32, self.agents), kp, ks, vp, vs, kind, rows,
+            0 if weight is None else self._vector("weight", weight, _f32, self._slots),
+            0 if pos is None else self._vector("pos", pos, _i32, self._slots),
+            0 if row_pos is None else self._vector("row_pos", row_pos, _i32, rows), self._err, self._on(stream))
         if st:
             raise _q.QmmError(st, "qmm_kv_append")
 
@@ -212,21 +221,22 @@ class KvPlan:
         that the row sees; lse: fp32 [rows, heads]; weight_in / weight_out: the slots' accumulated
         weights before and after (weight_in may be weight_out, or None for zeros); scale: None
         for 1 / sqrt(head_dim)."""
+        at = self._pool(pool)
         qp, qs = self._rows_of("q", q, self._q_dtype, self.heads)
         rows = q.shape[0]
         if rows > self.max_rows:
             _refuse("q", f"at most {self.max_rows} rows (the plan's max_rows)")
         kind = _types.get(out.dtype)
-        if kind is None or out.shape != q.shape or not out.is_contiguous() or not out.is_cuda:
-            _refuse("out", f"a contiguous fp32, fp16 or bf16 CUDA tensor [{rows}, {self.heads}, {self.head_dim}]")
-        stream = self._on(pool, stream)
+        if kind is None or out.shape != q.shape or not out.is_contiguous() or out.get_device() != self.device:
+            _refuse("out", f"a contiguous fp32, fp16 or bf16 CUDA tensor [{rows}, {self.heads}, {self.head_dim}] on device {self.device}")
+        stream = self._on(stream)
         ws, ws_bytes, _ = self._space("attend" if weight_out is None else "weights", stream)
         st = self._attend(
-            self._ref, self._pool(pool), self._table, _vector("agent_rows", agent_rows, _i32, self.agents + 1),
-            _vector("row_len", row_len, _i32, rows), qp, qs, rows, self._scale if scale is None else scale, out.data_ptr(), kind,
-            0 if lse is None else _vector("lse", lse, _f32, rows * self.heads),
-            0 if weight_in is None else _vector("weight_in", weight_in, _f32, self._slots),
-            0 if weight_out is None else _vector("weight_out", weight_out, _f32, self._slots), ws, ws_bytes, self._err, stream)
+            self._ref, at, self._table, self._vector("agent_rows", agent_rows, _i32, self.agents + 1),
+            self._vector("row_len", row_len, _i32, rows), qp, qs, rows, self._scale if scale is None else scale, out.data_ptr(), kind,
+            0 if lse is None else self._vector("lse", lse, _f32, rows * self.heads),
+            0 if weight_in is None else self._vector("weight_in", weight_in, _f32, self._slots),
+            0 if weight_out is None else self._vector("weight_out", weight_out, _f32, self._slots), ws, ws_bytes, self._err, stream)
         if st:
             raise _q.QmmError(st, "qmm_kv_attend")
 
@@ -237,15 +247,16 @@ class KvPlan:
         cache_len, keep, len_out: int32 [agents] (keep < 0: no limit); protect_from: int32
         [agents] or None; weight_out and pos_out may be weight and pos.  Slots from len_out on
         are free afterwards."""
-        stream = self._on(pool, stream)
+        at = self._pool(pool)
+        stream = self._on(stream)
         ws, ws_bytes, _ = self._space("evict", stream)
         st = self._evict(
-            self._ref, self._pool(pool), self._table, _vector("cache_len", cache_len, _i32, self.agents),
-            _vector("keep", keep, _i32, self.agents), sink,
-            0 if protect_from is None else _vector("protect_from", protect_from, _i32, self.agents),
-            _vector("weight", weight, _f32, self._slots), _vector("pos", pos, _i32, self._slots),
-            _vector("weight_out", weight_out, _f32, self._slots), _vector("pos_out", pos_out, _i32, self._slots),
-            _vector("len_out", len_out, _i32, self.agents), ws, ws_bytes, self._err, stream)
+            self._ref, at, self._table, self._vector("cache_len", cache_len, _i32, self.agents),
+            self._vector("keep", keep, _i32, self.agents), sink,
+            0 if protect_from is None else self._vector("protect_from", protect_from, _i32, self.agents),
+            self._vector("weight", weight, _f32, self._slots), self._vector("pos", pos, _i32, self._slots),
+            self._vector("weight_out", weight_out, _f32, self._slots), self._vector("pos_out", pos_out, _i32, self._slots),
+            self._vector("len_out", len_out, _i32, self.agents), ws, ws_bytes, self._err, stream)
         if st:
             raise _q.QmmError(st, "qmm_kv_evict")
 
@@ -266,6 +277,8 @@ def logprobs(logits, tokens=None, lse=None, logprob=None, entropy=None, top_inde
     kind = _types.get(logits.dtype)
     if kind is None or logits.dim() != 2 or not logits.is_cuda:
         _refuse("logits", "an fp32, fp16 or bf16 CUDA tensor [m, n]")
+    device = logits.get_device()
+    _current(device)
     m, n = logits.shape
     st = logits.stride()
     if m > 0 and n > 1 and st[1] != 1:
@@ -275,13 +288,13 @@ def logprobs(logits, tokens=None, lse=None, logprob=None, entropy=None, top_inde
     given = top = tp = lp = ip = vp = 0
     if tokens is not None:
         given = tokens.shape[1]
-        tp, lp = _vector("tokens", tokens, _i32, m * given), _vector("logprob", logprob, _f32, m * given)
+        tp, lp = _vector("tokens", tokens, _i32, m * given, device), _vector("logprob", logprob, _f32, m * given, device)
     if top_index is not None:
         top = top_index.shape[1]
-        ip, vp = _vector("top_index", top_index, _i32, m * top), _vector("top_logprob", top_logprob, _f32, m * top)
+        ip, vp = _vector("top_index", top_index, _i32, m * top, device), _vector("top_logprob", top_logprob, _f32, m * top, device)
     status = load().qmm_logprobs(logits.data_ptr(), kind, m, n, st[0] if m > 1 else n, tp, given, top,
-                                 0 if lse is None else _vector("lse", lse, _f32, m),
-                                 0 if entropy is None else _vector("entropy", entropy, _f32, m), lp, ip, vp,
-                                 _stream(logits) if stream is None else stream)
+                                 0 if lse is None else _vector("lse", lse, _f32, m, device),
+                                 0 if entropy is None else _vector("entropy", entropy, _f32, m, device), lp, ip, vp,
+                                 _raw(device) if stream is None else stream)
     if status:
         raise _q.QmmError(status, "qmm_logprobs")
