@@ -287,9 +287,14 @@ def logprobs(logits, tokens=None, lse=None, logprob=None, entropy=None, top_inde
         _refuse("tokens and logprob, top_index and top_logprob", "given together")
     given = top = tp = lp = ip = vp = 0
     if tokens is not None:
+        # (their second dim is the number per row: a transposed pair would pass for one of other rows)
+        if tokens.dim() != 2 or tokens.shape[0] != m or logprob.shape != tokens.shape:
+            _refuse("tokens and logprob", f"[{m}, given], both")
         given = tokens.shape[1]
         tp, lp = _vector("tokens", tokens, _i32, m * given, device), _vector("logprob", logprob, _f32, m * given, device)
     if top_index is not None:
+        if top_index.dim() != 2 or top_index.shape[0] != m or top_logprob.shape != top_index.shape:
+            _refuse("top_index and top_logprob", f"[{m}, top], both")
         top = top_index.shape[1]
         ip, vp = _vector("top_index", top_index, _i32, m * top, device), _vector("top_logprob", top_logprob, _f32, m * top, device)
     status = load().qmm_logprobs(logits.data_ptr(), kind, m, n, st[0] if m > 1 else n, tp, given, top,
