@@ -97,7 +97,7 @@ __device__ __forceinline__ float join_sum(const AttendParams& p, int64_t slot0, 
 // sequence of 118,000 tokens, D = 256, 3 rows of 2 heads: 1,842 chunks a query).  The bits are the same.
 template <int D, int T>
 __global__ void __launch_bounds__(kJoinThreads, 6) attend_join(const AttendParams p, int weight_blocks, int slices) {
-    extern __shared__ float jsm[];
+    extern __shared__ __align__(16) float jsm[];  // (read by float4)
     const int tid = threadIdx.x;
     griddep_wait();  // the split kernel has finished and its partials are visible
     if (static_cast<int>(blockIdx.x) >= weight_blocks) {
