@@ -2,7 +2,7 @@
 //
 // The split kernel (qmm_kv_attend.cuh) leaves, per chunk and query, M_c, l_c and o_c.  A row's
 // result is out = sum_c w_c o_c / sum_c w_c l_c with w_c = 2^(M_c - max M), its lse the logarithm
-// of that denominator, and a token's weight the sum over queries of 2^(x_t - M) / l.
+// of that denominator (and max M), and a token's weight the sum over queries of 2^(x_t - M) / l.
 #include <cudaTypedefs.h>
 
 #include "qmm_kv_attend.cuh"
@@ -95,6 +95,7 @@ __device__ __forceinline__ float join_sum(const AttendParams& p, int64_t slot0, 
 // however many blocks there are.  They are the long ones, so they start first and the others fill
 // in beside them.  The others: one (row, head) each, or 32 dims of one where that makes few blocks (a
 // sequence of 118,000 tokens, D = 256, 3 rows of 2 heads: 1,842 chunks a query).  The bits are the same.
+// (Six blocks an SM leave 40 registers: <256, 1> spills 96 bytes, the other instances none to 28.)
 template <int D, int T>
 __global__ void __launch_bounds__(kJoinThreads, 6) attend_join(const AttendParams p, int weight_blocks, int slices) {
     extern __shared__ __align__(16) float jsm[];  // (read by float4)
@@ -240,10 +241,11 @@ __global__ void __launch_bounds__(kJoinThreads, 6) attend_join(const AttendParam
 
 namespace {
 
-// Tokens per chunk, by the dims alone (so that a row's bits are those of any other call): of 1024 ..
+// Tokens per chunk, by the dims alone (so that a row's bits are those of any other call, and on any GB300, for which
+// the grid is a number here): of 1024 ..
 // a tile, with pages that one warp can hold (32), the one whose rounds of a GB300's grid (608
 // blocks at head dimension 64, 152 at 128, 304 at 256) take the least when all sequences are full, an item being
-// its tiles and kItem tiles' time for its start and end.  At head dimension 64, 61 ragged sequences: 104 us at 1,024, 92 at 512, 93 at 256.  At 128,
+// its tiles and kItem tiles' time for its start and end (an estimate: the pipeline's fill, and the partial).  At head dimension 64, 61 ragged sequences: 104 us at 1,024, 92 at 512, 93 at 256.  At 128,
 // calls with weights at 1,024 and 2,048: 109 and 112 us for a sequence of 131,071 (fp16), 184 and 189 for
 // 8 x 16,000 at 8 rows (bf16), 108 and 115 for 4 x 23,000 (q8_0).
 int32_t chunk_of(const qmm_kv_dims& d) {

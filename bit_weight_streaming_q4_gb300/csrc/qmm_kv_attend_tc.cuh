@@ -32,7 +32,7 @@
 //
 // What it measured (this kernel alone, without weights; in brackets the call, whose join comes after):
 // fp16, one sequence of 131,071, 1 row: 80 us (87), 6.7 TB/s, the bytes.  bf16, 8 x 16,000, 8 rows
-// (48 queries a head): 93 us (107), 5.6 TB/s.  q8_0, 4 x 23,000, 3 rows (18 queries): 80 us (87), 2.5 TB/s.
+// (48 queries a head): 93 us (107), 5.6 TB/s.  q8_0, 4 x 23,000, 3 rows (18 queries): 81 us (87), 2.5 TB/s.
 // The second is bound by the chain from a tile's scores to its probabilities, some 3,500 clocks a tile
 // in a softmax group (by clock readings in a copy of the kernel); q8_0 by the conversion of V as well:
 // without three quarters of it, 66 us for 85.  With weights the scores' way through L2 costs 10 to 33 us.
@@ -55,7 +55,8 @@ constexpr float kFine = 4194304.f;  // 2^22: references below it hold sums with 
                                     // exponent in -7 .. 15 a large score may round away: 2^15)
 constexpr int kVShift = 8;        // q8_0: V's power of two, off again where the outputs are read
 constexpr float kLowScale = 2048.f;  // p's low part is kept times this (its products have columns of their
-                                     // own), so that 22 bits of p count down to 2^-33 of the reference's
+                                     // own), so that p keeps 22 bits down to 2^-23 of the reference's, and 2^-45 of
+                                     // it below
 
 // Q: queries of a tile, of N columns.
 template <int FMT, int N, int Q>
@@ -64,8 +65,8 @@ struct TcGeo {
     static constexpr int groups = N == 48 ? 3 : 2;                 // softmax groups of four warps
     static constexpr int W = Q / groups, B = W % 8 ? W : 8;        // queries of a group, and of a read of tensor memory
     // q8_0, few queries: K and V converted by warps of their own, waits asked for at once and references read
-    // early.  4 x 23,000 tokens with weights: 1 row 84 -> 82 us, 3 rows 98 -> 94.  At 32 and 48 queries, whose
-    // threads have too few registers for it, 5 rows would go from 108 to 125 and 8 from 136 to 158.
+    // early.  4 x 23,000 tokens with weights: 1 row 84 -> 82 us, 3 rows 98 -> 94 (83 and 94 now).  At 32 and 48 queries,
+    // whose threads have too few registers for it, 5 rows would go from 108 to 125 and 8 from 136 to 158 (109 and 139 now).
     static constexpr bool eager = q8 && Q <= 24;
     static constexpr int converters = !q8 ? 0 : eager ? 2 : 1;     // groups of four warps
     static constexpr int threads = 128 * (1 + groups + converters);
@@ -132,12 +133,6 @@ __device__ __forceinline__ bool scales_far_apart(const uint32_t (&w)[4]) {
 __device__ __forceinline__ int p_byte(int token, int col) {
     return (col >> 5) * (kTcTile * 64) + token * 64 + ((((col >> 3) & 3) ^ ((token >> 1) & 3)) << 4) + (col & 7) * 2;
 }
-
-__device__ __forceinline__ uint32_t order_bits(float v) {
-    const uint32_t u = __float_as_uint(v);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float from_order_bits(uint32_t o) { return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o); }
 
 // 8 consecutive columns of the thread's tensor memory lane (to be waited for with tc_wait_ld).
 __device__ __forceinline__ void tmem_load8(uint32_t taddr, float* v) {
@@ -242,8 +237,9 @@ struct alignas(16) ItemRec {
     int q0, nq, minlen, r0;  // first query, queries of the sequence and KV head, the sequence's shortest row and first row
 };
 
-// (512: at most 128 registers, so that with 384 threads a block of the joining kernel, 48 registers by 256
-// threads, fits beside and has begun when the partials are there; without room it cost 2 us a call)
+// (512: at most 128 registers, so that with 384 threads a block of the joining kernel, 40 registers by 256
+// threads, fits beside and has begun when the partials are there; without room it cost 2 us a call.  Spilled at
+// that: 4, 24 and 28 bytes by the 16-bit tiles of 24, 32 and 48 queries, 8 and 28 by q8_0's of 24 and 48.)
 template <int FMT, int N, int Q>
 __global__ void __launch_bounds__((TcGeo<FMT, N, Q>::threads > 512 ? TcGeo<FMT, N, Q>::threads : 512), 1)
     attend_partial_tc(const __grid_constant__ CUtensorMap map, const __grid_constant__ AttendParams p) {

@@ -17,7 +17,7 @@
 // alternatives, 5.9 TB/s; 68 us with 5, whose bound and collection lengthen every segment's
 // chain of barriers); at a few rows that chain and the cluster's two barriers, about 9 us.  Four
 // blocks of 256 threads per SM, 40 elements a thread: 512 threads, or 32 or 24 elements, took
-// 4 to 40 % longer, three blocks 20 %.
+// 4 to 40 % longer, three blocks 20 %.  (Four leave 64 registers, of which it spills 44 bytes.)
 #include <cooperative_groups.h>
 
 #include "qmm_kv.cuh"

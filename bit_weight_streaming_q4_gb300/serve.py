@@ -193,7 +193,7 @@ class KvPlan:
         k, v: fp32, fp16 or bf16 [rows, kv_heads, head_dim], any row stride (columns of the qkv
         projection's output are taken in place).  cache_len: int32 [agents], tokens cached
         before the call (not changed).  weight / pos: the slots' arrays, whose new entries become
-        0 and row_pos."""
+        0 and row_pos.  No other sequence may share the pages that are written to."""
         at = self._pool(pool)
         kind = _types.get(k.dtype)
         if kind is None:
@@ -246,7 +246,8 @@ class KvPlan:
 
         cache_len, keep, len_out: int32 [agents] (keep < 0: no limit); protect_from: int32
         [agents] or None; weight_out and pos_out may be weight and pos.  Slots from len_out on
-        are free afterwards."""
+        are free afterwards.  A sequence that is cut shares none of its pages with another: tokens move
+        into the slots below keep[a]."""
         at = self._pool(pool)
         stream = self._on(stream)
         ws, ws_bytes, _ = self._space("evict", stream)

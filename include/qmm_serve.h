@@ -93,8 +93,14 @@ qmm_status qmm_kv_append(const qmm_kv_dims* dims, void* pool, const int32_t* pag
  *  lse:        fp32 [rows][heads], the logarithm of each softmax's denominator; or null.
  *  weight_in:  or null (zeros); may be weight_out.  weight_out: or null (no weights).
  *  workspace:  16-byte aligned, at least qmm_kv_attend_workspace_bytes bytes, in use until the
- *              call's kernels finish.
- * A row's out and lse are bit-identical whatever the other rows and sequences of the call.
+ *              call's kernels finish.  It is sized by the table, not by the lengths: with weights mostly 4 bytes
+ *              for every slot, KV head and query (max_agent_rows * heads / kv_heads, rounded up to 8).
+ * A row's out and lse are bit-identical whatever the other rows and sequences of the call, as long as the V
+ * that it sees is finite.  An infinity or NaN there makes that element of out infinite or NaN (which of the
+ * two, and the last bits of the row's other elements, depends on whether every row of its sequence sees it);
+ * so may an element of a BF16 pool above 2^110, whose product with a probability leaves fp32.
+ * An entry of the page table outside the pool (error word 2) takes its tokens out of the softmax, and at head
+ * dimension 128 those of up to 128 slots around them.
  * Scores, softmax and sums are fp32; the probabilities enter the product with V as the sum of
  * two 16-bit parts (relative error 2^-22, or 2^-38 of the row's largest one where that is more;
  * 2^-17 with BF16).  With Q8_0 the same holds of a probability times its token's largest V scale,
@@ -116,7 +122,8 @@ qmm_status qmm_kv_attend(const qmm_kv_dims* dims, const void* pool, const int32_
  * +0, a NaN weight is below every other).  Kept tokens in slots below keep[a] stay, and the
  * i-th kept token from slot keep[a] on, in slot order, moves into the i-th slot freed below:
  * sources and destinations never overlap, so the pool is changed in place.  Slots from
- * len_out[a] on are free afterwards; so are the pages that hold only such slots.
+ * len_out[a] on are free afterwards; so are the pages that hold only such slots.  Pages that sequences share
+ * must not hold a slot of one that is cut: tokens move into slots below keep[a], whoever else reads them.
  *  cache_len, keep: int32 [agents].  protect_from: int32 [agents], or null (no recent tokens
  *              are protected).
  *  weight, pos: the slots' arrays.  weight_out, pos_out: the same after the eviction, slots
