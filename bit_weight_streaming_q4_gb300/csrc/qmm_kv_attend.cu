@@ -91,6 +91,31 @@ __device__ __forceinline__ float join_sum(const AttendParams& p, int64_t slot0, 
     return v;
 }
 
+// What an output element is that came out as NaN though its denominator is a number: V is not finite at some slot
+// t < n (a probability's second part times an infinity is NaN, if it is 0).  Every probability is positive: infinity
+// if all that is not finite is infinity of one sign.  (A slow loop, for a result that is no number either way; as a
+// function of its own it costs other calls nothing.)
+__device__ __noinline__ float sum_of_infinities(const AttendParams& p, int format, int d, int a, int g, int n, int dim) {
+    float sum = 0.f;
+    for (int t = 0; t < n; ++t) {
+        const int pg = p.table[static_cast<int64_t>(a) * p.max_pages + (t >> p.page_shift)], s = t & (p.page_tokens - 1);
+        if (pg < 0 || pg >= p.pool_pages) continue;
+        const int64_t rec = static_cast<int64_t>(pg) * p.kv_heads + g;
+        float v;
+        if (format == QMM_KV_Q8_0) {
+            const uint8_t* r = p.pool + rec * kQ8Rec + kQ8Half;
+            v = static_cast<float>(static_cast<int8_t>(r[dim * 64 + s])) *
+                __half2float(*reinterpret_cast<const __half*>(r + 8192 + ((dim >> 5) * 64 + s) * 2));
+        } else {
+            const uint16_t w = reinterpret_cast<const uint16_t*>(p.pool)[((rec * 2 + 1) * p.page_tokens + s) * d + dim];
+            v = format == QMM_KV_BF16 ? __uint_as_float(static_cast<uint32_t>(w) << 16) : __half2float(__ushort_as_half(w));
+        }
+        if (!isfinite(v)) sum += v;
+        if (sum != sum) break;
+    }
+    return sum == 0.f ? __int_as_float(0x7FFFFFFF) : sum;  // (all finite: sums that left fp32)
+}
+
 // The first weight_blocks blocks: T slots a thread of one (sequence, KV head) each, taken in turn by
 // however many blocks there are.  They are the long ones, so they start first and the others fill
 // in beside them.  The others: one (row, head) each, or 32 dims of one where that makes few blocks (a
@@ -132,6 +157,7 @@ __global__ void __launch_bounds__(kJoinThreads, 6) attend_join(const AttendParam
         const bool none = m == kNoMax && l == 0.f;
         if (tid < width) {
             v = none ? 0.f : v / l;
+            if (v != v && l == l) v = sum_of_infinities(p, p.format, D, a, g, min(p.row_len[r], p.info[a].x), slice * 32 + tid);
             const int64_t at = static_cast<int64_t>(block) * D + slice * 32 + tid;
             if (p.out_type == QMM_TYPE_F32) static_cast<float*>(p.out)[at] = v;
             else if (p.out_type == QMM_TYPE_F16) static_cast<__half*>(p.out)[at] = __float2half_rn(v);
@@ -431,6 +457,7 @@ qmm_status qmm_kv_attend(const qmm_kv_dims* dims, const void* pool, const int32_
     p.qp = l.qp;
     p.cap = dims->max_pages * dims->page_tokens;
     p.out_type = out_type;
+    p.format = dims->format;
     p.c2 = scale * 1.4426950408889634f;
     a.head_dim = dims->head_dim;
     a.max_q = dims->max_agent_rows * p.group;

@@ -68,7 +68,7 @@ struct AttendParams {
     int32_t chunk, chunks;      // tokens per chunk, chunks per (sequence, KV head)
     int32_t qp;                 // queries per (sequence, KV head) in the workspace, a multiple of 8
     int32_t cap;                // slots per sequence: max_pages * page_tokens
-    int32_t out_type;
+    int32_t out_type, format;
     float c2;                   // scale * log2(e)
 };
 

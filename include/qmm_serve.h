@@ -96,9 +96,9 @@ qmm_status qmm_kv_append(const qmm_kv_dims* dims, void* pool, const int32_t* pag
  *              call's kernels finish.  It is sized by the table, not by the lengths: with weights mostly 4 bytes
  *              for every slot, KV head and query (max_agent_rows * heads / kv_heads, rounded up to 8).
  * A row's out and lse are bit-identical whatever the other rows and sequences of the call, as long as the V
- * that it sees is finite.  An infinity or NaN there makes that element of out infinite or NaN (which of the
- * two, and the last bits of the row's other elements, depends on whether every row of its sequence sees it);
- * so may an element of a BF16 pool above 2^110, whose product with a probability leaves fp32.
+ * that it sees is finite.  An infinity there makes that element of out infinite (a NaN, or infinities of
+ * both signs: NaN); the last bits of the row's other elements then depend on whether every row of its
+ * sequence sees it.  An element of a BF16 pool above 2^110 may leave fp32 by its product with a probability.
  * An entry of the page table outside the pool (error word 2) takes its tokens out of the softmax, and at head
  * dimension 128 those of up to 128 slots around them.
  * Scores, softmax and sums are fp32; the probabilities enter the product with V as the sum of
