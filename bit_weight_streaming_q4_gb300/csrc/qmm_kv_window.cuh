@@ -1,0 +1,1061 @@
+// Attention with a sliding window over the paged cache: the kernel on the 5th-generation tensor cores.
+//
+// For query (row r of sequence a, head h of KV head g's group) and x_t = scale log2(e) q . k_t:
+//   out = sum_t 2^(x_t - M) v_t / l,   l = sum_t 2^(x_t - M),   M = max_t x_t
+// over the slots t < n with t >= n - window or t < sinks, n = row_len[r].
+// The queries of a sequence and a KV head (rows times heads of the group) lie side by side, 128 of them a tile:
+//   S[query][token] = Q K^T     M = 128 queries, N = the tokens of a tile, K = the dims
+//   O[query][dim]  += P V       M = 128 queries, N = the dims, K = the tokens
+// with S and O in tensor memory.  A softmax thread owns a query: its scores, maximum and sum need no exchange.
+// P goes back over S as the second product's A operand, in 16 bits.
+// An item is a block's work: a sequence, a KV head and
+//   prompts (more than 128 queries a sequence): two tiles of queries, which share each K and V tile;
+//   decode steps: one tile of queries, whose tokens' tiles are dealt to two streams by their parity; the streams
+//     meet at the end through shared memory.
+// Either way two streams take turns on the tensor cores: while one's scores become probabilities, the other's products
+// run.  (Head dimension 256 leaves tensor memory room for one stream; its scores have two buffers instead.)
+// The tiles of an item are those that some of its rows sees: the first ones (sinks), and the window's.  Where few
+// items would leave SMs idle, tokens are cut into chunks at fixed places of a sequence, an item each, whose unnormalised
+// outputs a second kernel joins.  All choices are made by the plan's dims, so a row's bits do not depend on its company.
+//   warp 0      forms the items' records; 16-bit pools: asks for K tiles
+//   warp 1      issues the products
+//   warp 2      16-bit pools: asks for V tiles
+//   warp 3      16-bit pools: zeroes the rows of V that must not count, where some are
+//   warps 4 ..  softmax, four a stream
+//   q8_0: four more convert K (a token a thread), four V (a dim a thread), from memory through registers
+// A query's reference is its first tile's maximum and moves only when a score passes it by more than 2^kSlack; each
+// query decides for itself.
+#pragma once
+
+#include <cuda.h>
+
+#include "qmm_decode.h"
+#include "qmm_kv.cuh"
+
+namespace qmm {
+namespace window {
+
+using namespace qmm::kv;
+
+constexpr float kShift = 9.f;       // p's power of two ..
+constexpr float kSlack = 6.f;       // .. and how far a score may pass its reference: p <= 2^15
+constexpr float kFine = 4194304.f;  // 2^22: a larger reference stands alone (fp32's spacing would swallow the two): p <= 1
+
+struct Params {
+    const uint8_t* pool;
+    const int32_t* table;
+    const int32_t* agent_rows;
+    const int32_t* row_len;
+    const uint16_t* q;
+    void* out;
+    float* lse;
+    float* ml;  // [rows][heads][slots][2]: reference and sum
+    float* o;   // [rows][heads][slots][D]
+    int* err;
+    int64_t q_stride;
+    int32_t max_pages, pool_pages, page_shift, page_tokens, heads, kv_heads, group, agents, rows, max_agent_rows, cap;
+    int32_t window, sinks, out_type, format, head_dim;
+    int32_t chunk;   // tokens per chunk, a multiple of 256; 0: one item has all of a query's tokens and writes its output
+    int32_t slots;   // partials per (row, head)
+    int32_t decode;  // one tile of queries an item, tokens dealt to two streams
+    uint32_t flip;   // sign bits that a negative scale puts on the queries
+    float c2;        // |scale| log2(e), positive
+};
+
+struct Launch {
+    Params p;
+    CUtensorMap map;
+    int device, grid;
+};
+
+template <int FMT, int D>
+struct Geo {
+    static constexpr bool q8 = FMT == QMM_KV_Q8_0;
+    static constexpr int streams = D == 256 ? 1 : 2;
+    static constexpr int TN = D == 256 ? 64 : 128;               // tokens of a tile
+    static constexpr int tile = TN * D * 2;                      // bytes of a tile's K or V in 16 bits
+    static constexpr int k_tile = q8 ? 2 * tile : tile;          // q8_0: K's high and low parts
+    static constexpr int k_slots = D == 64 ? 4 : q8 ? 1 : 2, v_slots = D == 64 ? 4 : 2;
+    static constexpr int q_tile = 128 * D * 2;
+    static constexpr int soft_warps = 4 * streams, conv_warps = q8 ? 8 : 0;
+    static constexpr int threads = 32 * (4 + soft_warps + conv_warps);
+    // tensor memory: S (a buffer per stream, or two), P over it, and O
+    static constexpr int col_o = 256;
+    // shared memory, after aligning to 1024
+    static constexpr int off_v = k_slots * k_tile;
+    static constexpr int off_q = off_v + v_slots * tile;
+    static constexpr int off_ml = off_q + streams * q_tile;      // [128] reference and sum of the second stream
+    static constexpr int off_item = off_ml + 128 * 8;            // [2] of Record
+    static constexpr int off_bar = off_item + 2 * 64;
+    static constexpr int bars = 2 * k_slots + 3 * v_slots + 2 + 2 + 2 + 2 + 2 + 2 + 4;
+    static constexpr int off_misc = off_bar + bars * 8;          // tmp[33], abort, tmem, accumulate[2], miss[4], odd[4][4], zero[2][4]
+    static constexpr int off_seq = (off_misc + 68 * 4 + 15) / 16 * 16;
+    static constexpr int smem(int agents) { return 1024 + off_seq + (agents + 1) * 16; }
+};
+
+// What the roles need to know of an item.
+struct alignas(16) Record {
+    int a, g, q0, nq, r0;          // sequence, KV head, first query, the sequence's queries, its first row
+    int a0, na, b0, nt;            // tiles a0 .. a0 + na - 1, then b0 ..; nt in all
+    int lo, hi, minlen, maxlo;     // first slot of a window, longest and shortest row, the last window's first slot
+    int sink_end, chunk, pad;      // first slots that are visible to the longest row
+};
+__device__ __forceinline__ int tile_at(const Record& it, int i) { return i < it.na ? it.a0 + i : it.b0 + i - it.na; }
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lead) {
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+__device__ __forceinline__ void tma_load_hint(void* smem_dst, const void* tmap, int32_t c0, int32_t c1, uint64_t* bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ uint64_t l2_policy_evict_last() {
+    uint64_t pol;
+    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
+    return pol;
+}
+
+#define QMM_R32(v, c)                                                                                                   \
+    c((v)[0]), c((v)[1]), c((v)[2]), c((v)[3]), c((v)[4]), c((v)[5]), c((v)[6]), c((v)[7]), c((v)[8]), c((v)[9]),         \
+        c((v)[10]), c((v)[11]), c((v)[12]), c((v)[13]), c((v)[14]), c((v)[15]), c((v)[16]), c((v)[17]), c((v)[18]),       \
+        c((v)[19]), c((v)[20]), c((v)[21]), c((v)[22]), c((v)[23]), c((v)[24]), c((v)[25]), c((v)[26]), c((v)[27]),       \
+        c((v)[28]), c((v)[29]), c((v)[30]), c((v)[31])
+// 32 consecutive columns of the thread's tensor memory lane (loads: to be waited for with tc_wait_ld).
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+#define QMM_OUT(x) "=f"(x)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : QMM_R32(v, QMM_OUT)
+        : "r"(taddr)
+        : "memory");
+#undef QMM_OUT
+}
+#define QMM_IN(x) "r"(x)
+#define QMM_INF(x) "f"(x)
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        QMM_R32(v, QMM_IN)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32f(uint32_t taddr, const float* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        QMM_R32(v, QMM_INF)
+        : "memory");
+}
+#undef QMM_IN
+#undef QMM_INF
+#undef QMM_R32
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
+    uint32_t v;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v) : "r"(taddr) : "memory");
+    return v;
+}
+
+template <bool BF>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    uint32_t d;
+    if constexpr (BF) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+    return d;
+}
+__device__ __forceinline__ float wide(uint32_t w, bool bf) {
+    return bf ? __uint_as_float(w << 16) : __half2float(__ushort_as_half(static_cast<uint16_t>(w)));
+}
+// Bytes 0, 1 (sel 0x4140) or 2, 3 (sel 0x4342) of four int8 already XORed with 0x80, as fp16x2, exact.
+__device__ __forceinline__ __half2 i8_to_h2(uint32_t biased, uint32_t sel) {
+    return __hadd2(as_h2(prmt(biased, 0x64646464u, sel)), as_h2(0xE480E480u));
+}
+
+// Whether sequence a can be attended to.
+__device__ __forceinline__ bool sequence_ok(const Params& p, int a) {
+    const int r0 = p.agent_rows[a], r1 = p.agent_rows[a + 1];
+    return r0 >= 0 && r1 >= r0 && r1 <= p.rows && r1 - r0 <= p.max_agent_rows;
+}
+// A row's length, 0 if it is out of range.
+__device__ __forceinline__ int length_of(const Params& p, int r) {
+    const int n = p.row_len[r];
+    return n < 0 || n > p.cap ? 0 : n;
+}
+// Chunks of a row, in its order: those of the first slots, then those of its window that are not among them.
+struct Chunks {
+    int first, from, end;  // 0 .. first - 1 and from .. end - 1
+    __device__ int count() const { return first + max(0, end - from); }
+};
+__device__ __forceinline__ Chunks chunks_of(const Params& p, int n) {
+    Chunks c;
+    c.first = (min(p.sinks, n) + p.chunk - 1) / p.chunk;
+    c.from = max(c.first, max(0, n - p.window) / p.chunk);
+    c.end = (n + p.chunk - 1) / p.chunk;
+    return c;
+}
+
+template <typename F>
+__device__ __forceinline__ void store_out(const Params& p, int64_t at, const float* v, F f) {  // 8 neighbouring elements
+    if (p.out_type == QMM_TYPE_F32) {
+        float* o = static_cast<float*>(p.out) + at;
+        *reinterpret_cast<float4*>(o) = make_float4(f(v[0]), f(v[1]), f(v[2]), f(v[3]));
+        *reinterpret_cast<float4*>(o + 4) = make_float4(f(v[4]), f(v[5]), f(v[6]), f(v[7]));
+    } else {
+        uint4 w;
+        if (p.out_type == QMM_TYPE_F16)
+            w = make_uint4(pack2<false>(f(v[0]), f(v[1])), pack2<false>(f(v[2]), f(v[3])), pack2<false>(f(v[4]), f(v[5])), pack2<false>(f(v[6]), f(v[7])));
+        else
+            w = make_uint4(pack2<true>(f(v[0]), f(v[1])), pack2<true>(f(v[2]), f(v[3])), pack2<true>(f(v[4]), f(v[5])), pack2<true>(f(v[6]), f(v[7])));
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at) = w;
+    }
+}
+
+// The table of sequences, the same in every block: seq[a] = (first item, chunks of the first slots, the window's
+// first chunk, first row), one more entry at the end; returns the number of items.  tmp: 33 ints.
+// QT: queries of an item.  Without chunks also writes the rows that no item has.
+__device__ __forceinline__ int form_table(const Params& p, int4* seq, int* tmp, int qt) {
+    const int tid = threadIdx.x, n_threads = blockDim.x;
+    bool falls = false, gaps = false;
+    for (int a = tid; a <= p.agents; a += n_threads) {
+        const int r0 = p.agent_rows[a], r1 = a < p.agents ? p.agent_rows[a + 1] : r0;
+        const bool ok = a == p.agents || sequence_ok(p, a);
+        seq[a] = make_int4(ok ? 0 : -1, 0, INT32_MAX, r0);
+        falls |= r1 < r0;
+        gaps |= !ok || (a == 0 && r0 > 0) || (a == p.agents && r0 < p.rows);
+    }
+    falls = __syncthreads_or(falls);
+    gaps = __syncthreads_or(gaps || falls);
+    if (falls)
+        for (int a = tid; a <= p.agents; a += n_threads) seq[a].x = -1;
+    if (gaps && blockIdx.x == 0 && tid == 0) atomicOr(p.err, kErrRange);
+    auto find = [&](int r) {
+        int lo = 0, hi = p.agents;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (seq[mid].w <= r) lo = mid;
+            else hi = mid;
+        }
+        return r < seq[lo].w || r >= seq[lo + 1].w ? -1 : lo;
+    };
+    __syncthreads();
+    if (p.chunk) {
+        if (!falls)
+            for (int r = tid; r < p.rows; r += n_threads) {
+                const int a = find(r), n = length_of(p, r);
+                if (a < 0 || n == 0) continue;
+                atomicMax(&seq[a].y, n);
+                atomicMin(&seq[a].z, max(0, n - p.window));
+            }
+    } else if (gaps) {
+        for (int r = blockIdx.x; r < p.rows; r += gridDim.x) {
+            const int a = falls ? -1 : find(r);
+            if (a >= 0 && seq[a].x >= 0) continue;
+            const int size = p.out_type == QMM_TYPE_F32 ? 4 : 2, d = p.head_dim;
+            uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + static_cast<int64_t>(r) * p.heads * d * size);
+            for (int i = tid; i < p.heads * d * size / 4; i += n_threads) o[i] = 0;
+            if (p.lse)
+                for (int h = tid; h < p.heads; h += n_threads) p.lse[static_cast<int64_t>(r) * p.heads + h] = -INFINITY;
+        }
+    }
+    __syncthreads();
+    int total = 0;
+    for (int a0 = 0; a0 < p.agents; a0 += n_threads) {
+        const int a = a0 + tid;
+        int n = 0, first = 0, from = 0;
+        if (a < p.agents) {
+            const int4 s = seq[a];
+            const int nr = seq[a + 1].w - s.w;
+            if (s.x >= 0 && nr > 0) {
+                int chunks = 1;
+                if (p.chunk) {
+                    first = (min(p.sinks, s.y) + p.chunk - 1) / p.chunk;
+                    from = max(first, s.z / p.chunk);
+                    chunks = s.y ? first + max(0, (s.y + p.chunk - 1) / p.chunk - from) : 0;
+                }
+                n = chunks * p.kv_heads * ((nr * p.group + qt - 1) / qt);
+            }
+        }
+        int sum;
+        const int at = block_exclusive(n, tmp, &sum);
+        if (a < p.agents) seq[a].x = total + at, seq[a].y = first, seq[a].z = from;
+        total += sum;
+    }
+    __syncthreads();
+    return total;
+}
+
+// The record of an item, by a warp.
+template <int TN>
+__device__ __forceinline__ Record record_of(const Params& p, const int4* seq, int item, int qt) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = p.agents;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (seq[mid].x <= item) lo = mid;
+        else hi = mid;
+    }
+    const int4 s = seq[lo];
+    Record it;
+    it.a = lo;
+    it.r0 = s.w;
+    it.nq = (seq[lo + 1].w - s.w) * p.group;
+    const int tiles = (it.nq + qt - 1) / qt;
+    int rest = item - s.x;
+    it.q0 = rest % tiles * qt;
+    rest /= tiles;
+    it.g = rest % p.kv_heads;
+    rest /= p.kv_heads;
+    it.chunk = rest < s.y ? rest : s.z + rest - s.y;
+    it.pad = 0;
+    // the item's rows
+    const int ra = it.r0 + it.q0 / p.group, rb = it.r0 + (min(it.q0 + qt, it.nq) - 1) / p.group;
+    int maxlen = 0, minlen = INT32_MAX, minlo = INT32_MAX, maxlo = 0;
+    bool bad = false;
+    for (int r = ra + lane; r <= rb; r += 32) {
+        const int n = length_of(p, r);
+        bad |= n != p.row_len[r];
+        maxlen = max(maxlen, n);
+        minlen = min(minlen, n);
+        if (n > 0) {
+            minlo = min(minlo, max(0, n - p.window));
+            maxlo = max(maxlo, max(0, n - p.window));
+        }
+    }
+    if (bad) atomicOr(p.err, kErrRange);
+    it.hi = __reduce_max_sync(0xffffffffu, maxlen);
+    it.minlen = __reduce_min_sync(0xffffffffu, minlen);
+    it.lo = __reduce_min_sync(0xffffffffu, minlo);
+    it.maxlo = __reduce_max_sync(0xffffffffu, maxlo);
+    it.sink_end = min(p.sinks, it.hi);
+    const int c0 = p.chunk ? it.chunk * (p.chunk / TN) : 0, c1 = p.chunk ? c0 + p.chunk / TN : INT32_MAX;
+    const int end = min((it.hi + TN - 1) / TN, c1);
+    it.a0 = c0;
+    it.na = max(0, min((it.sink_end + TN - 1) / TN, end) - c0);
+    it.b0 = max(it.lo / TN, c0 + it.na);
+    it.nt = it.hi ? it.na + max(0, end - it.b0) : 0;
+    return it;
+}
+
+// Marked tokens of a tile, whose V is not finite, added to the outputs of the queries that see them: p as the products
+// take it, V from memory.  (Rare; a function of its own costs the loop around it no registers.)
+template <int FMT, int D>
+__device__ __noinline__ void add_odd(const Params& p, int a, int g, int t0, const uint32_t* odd, uint32_t ocol, uint32_t pcol, int len,
+                                     int from, int first, bool fresh) {
+    constexpr bool BF = FMT == QMM_KV_BF16;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 8) {
+        uint32_t o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = fresh ? 0u : tmem_ld1(ocol + c + j);
+        tc_wait_ld();
+#pragma unroll 1
+        for (int j = 0; j < Geo<FMT, D>::TN; ++j) {
+            if (!((odd[j >> 5] >> (j & 31)) & 1)) continue;
+            const uint32_t both = tmem_ld1(pcol + j / 2);
+            tc_wait_ld();
+            const float pr = wide(j & 1 ? both >> 16 : both & 0xFFFFu, BF);
+            const int tok = t0 + j, sl = tok & (p.page_tokens - 1);
+            const bool sees = tok < len && (tok >= from || tok < first);
+            const int pg = p.table[static_cast<int64_t>(a) * p.max_pages + (tok >> p.page_shift)];  // (checked: it is not missing)
+            const int64_t rec = static_cast<int64_t>(pg) * p.kv_heads + g;
+#pragma unroll
+            for (int d = 0; d < 8; ++d) {
+                float y;
+                if constexpr (FMT == QMM_KV_Q8_0) {
+                    const uint8_t* b = p.pool + rec * kQ8Rec + kQ8Half;
+                    y = static_cast<float>(static_cast<int8_t>(b[(c + d) * 64 + sl])) *
+                        __half2float(*reinterpret_cast<const __half*>(b + 8192 + (((c + d) >> 5) * 64 + sl) * 2));
+                    y = __half2float(__float2half_rn(y));
+                } else {
+                    y = wide(reinterpret_cast<const uint16_t*>(p.pool)[((rec * 2 + 1) * p.page_tokens + sl) * D + c + d], BF);
+                }
+                if (sees) o[d] = __float_as_uint(fmaf(pr, y, __uint_as_float(o[d])));
+            }
+        }
+        tmem_st8(ocol + c, o);
+    }
+    tc_wait_st();
+}
+
+template <int FMT, int D>
+__global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
+    attend_window_tc(const __grid_constant__ CUtensorMap map, const __grid_constant__ Params p) {
+    using G = Geo<FMT, D>;
+    constexpr bool BF = FMT == QMM_KV_BF16;
+    constexpr int TN = G::TN, NS = G::streams;
+    extern __shared__ uint8_t sm_raw[];
+    griddep_launch_dependents();  // the joining kernel waits for this grid's end before it reads
+    uint8_t* sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
+    float2* ml_sm = reinterpret_cast<float2*>(sm + G::off_ml);
+    Record* item_sm = reinterpret_cast<Record*>(sm + G::off_item);
+    uint64_t* kfull = reinterpret_cast<uint64_t*>(sm + G::off_bar);
+    uint64_t *kempty = kfull + G::k_slots, *vfull = kempty + G::k_slots, *vempty = vfull + G::v_slots, *vready = vempty + G::v_slots;
+    uint64_t *qfull = vready + G::v_slots, *sfull = qfull + 2, *pfull = sfull + 2, *odone = pfull + 2, *ifull = odone + 2, *iempty = ifull + 2;
+    uint64_t *mfree = iempty + 2, *mfull = mfree + 1, *zdone = mfull + 1, *drained = zdone + 1;
+    int* tmp = reinterpret_cast<int*>(sm + G::off_misc);
+    volatile int* abort_flag = tmp + 33;
+    uint32_t* tmem_sm = reinterpret_cast<uint32_t*>(tmp + 34);
+    volatile int* accum_sm = tmp + 35;                                          // [2] O holds something before the first product
+    volatile int* miss_sm = tmp + 37;                                           // [4] a tile's pieces that are outside the pool
+    volatile uint32_t* odd_sm = reinterpret_cast<uint32_t*>(tmp + 41);          // [4][4] tokens that are taken query by query
+    volatile uint32_t* zero_sm = reinterpret_cast<uint32_t*>(tmp + 57);         // [2][4] q8_0: tokens whose V is zero
+    int4* seq = reinterpret_cast<int4*>(sm + G::off_seq);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int qt = NS == 2 && !p.decode ? 256 : 128;
+
+    if (tid == 0) {
+        for (int i = 0; i < G::k_slots; ++i) mbar_init(kfull + i, G::q8 ? 4 : 1), mbar_init(kempty + i, 1);
+        for (int i = 0; i < G::v_slots; ++i) mbar_init(vfull + i, 1), mbar_init(vempty + i, 1), mbar_init(vready + i, G::q8 ? 4 : 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(qfull + i, 4);
+            mbar_init(sfull + i, 1);
+            mbar_init(pfull + i, 4);
+            mbar_init(odone + i, 1);
+            mbar_init(ifull + i, 1);
+            mbar_init(iempty + i, (G::q8 ? 1 + G::conv_warps : 3) + G::soft_warps);
+        }
+        mbar_init(mfree, 4);
+        mbar_init(mfull, 4);
+        mbar_init(zdone, 4);
+        mbar_init(drained, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_sm, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    const int total = form_table(p, seq, tmp, qt);
+    tc_fence_after();
+    const uint32_t tmem = *tmem_sm;
+
+    // A wait of one of the roles, with one answer for the warp.  Once one has run out, everything ends.
+    bool live = true;
+    auto await = [&](uint64_t* b, uint32_t parity) {
+        if (live && !mbar_wait_bounded(b, parity, abort_flag)) {
+            live = false;
+            *abort_flag = 1;
+        }
+        live = __all_sync(0xffffffffu, live);
+    };
+    // the next item's record
+    int k = 0;  // items so far
+    auto next_record = [&]() -> Record {
+        await(ifull + (k & 1), (k >> 1) & 1);
+        const Record it = item_sm[k & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(iempty + (k & 1));
+        ++k;
+        return it;
+    };
+    // whether some row does not see some token of a tile
+    auto edge = [&](const Record& it, int t0) { return !(t0 + TN <= it.minlen && (t0 >= it.maxlo || t0 + TN <= p.sinks)); };
+    // a token that no row of the item sees
+    auto gone = [&](const Record& it, int t) { return t >= it.hi || (t < it.lo && t >= it.sink_end); };
+    constexpr int kPieces = G::q8 ? 2 : TN / 16;
+    const int piece_rows = min(TN, p.page_tokens), piece_shift = 31 - __clz(piece_rows);
+    // lane i: the page of piece i of a tile, -1 if nobody needs it, -2 if it is outside the pool
+    auto page_of = [&](const Record& it, int t0) {
+        int pg = -1;
+        const int t = t0 + lane * piece_rows;
+        if (lane * piece_rows < TN && t < it.hi && (t + piece_rows > it.lo || t < it.sink_end)) {
+            pg = p.table[static_cast<int64_t>(it.a) * p.max_pages + (t >> p.page_shift)];
+            if (pg < 0 || pg >= p.pool_pages) {
+                atomicOr(p.err, kErrPage);
+                pg = -2;
+            }
+        }
+        return pg;
+    };
+
+    // Registers go where the scores are (the shares add up to what the block was launched with, or less:
+    // 256 * 200 + 128 * 104 = 384 * 168; q8_0 256 * 104 + 384 * 88 <= 640 * 96).
+    if (warp < 4) {
+    if constexpr (NS == 2) setmaxnreg_dec<G::q8 ? 88 : 104>();
+    if (warp == 0 || (warp == 2 && !G::q8)) {
+        // ---------------------------------------------------------------- records; K tiles (warp 0), V tiles (warp 2)
+        const int h = warp == 2;
+        constexpr int most = G::k_slots > G::v_slots ? G::k_slots : G::v_slots;
+        const int slots = h ? G::v_slots : G::k_slots;
+        uint64_t* full = h ? vfull : kfull;
+        uint64_t* empty = h ? vempty : kempty;
+        uint8_t* ring = sm + (h ? G::off_v : 0);
+        // (a prompt's tiles are read by other blocks as well)
+        const uint64_t policy = p.decode ? l2_policy_evict_first() : l2_policy_evict_last();
+        int t = 0;
+        for (int item = blockIdx.x; item < total && live; item += gridDim.x) {
+            Record it;
+            if (h) {
+                it = next_record();
+            } else {
+                it = record_of<TN>(p, seq, item, qt);
+                if (k > 1) await(iempty + (k & 1), ((k >> 1) - 1) & 1);
+                if (!live) break;
+                if (lane == 0) {
+                    item_sm[k & 1] = it;
+                    mbar_arrive(ifull + (k & 1));
+                }
+                ++k;
+                if (G::q8) continue;
+            }
+            int next = it.nt > 0 ? page_of(it, tile_at(it, 0) * TN) : -1;
+            for (int i = 0; i < it.nt && live; ++i, ++t) {
+                const int t0 = tile_at(it, i) * TN, mine = next;
+                if (i + 1 < it.nt) next = page_of(it, tile_at(it, i + 1) * TN);
+                const uint32_t there = __ballot_sync(0xffffffffu, mine >= 0), miss = __ballot_sync(0xffffffffu, mine == -2);
+                const int s = t % slots, round = t / slots;
+                if (round > 0) await(empty + s, (round - 1) & 1);
+                if (!live) break;
+                int pg[kPieces];
+#pragma unroll
+                for (int j = 0; j < kPieces; ++j) pg[j] = __shfl_sync(0xffffffffu, mine, j);
+                if (lane == 0) {
+                    fence_proxy_async_smem();  // the slot's generic accesses, before the copies
+                    if (h) miss_sm[s] = static_cast<int>(miss);
+                    uint8_t* dst = ring + s * G::tile;
+                    if (!there) mbar_arrive(full + s);
+                    else mbar_arrive_expect_tx(full + s, __popc(there) * piece_rows * D * 2);
+#pragma unroll
+                    for (int j = 0; j < kPieces; ++j) {
+                        if (j * piece_rows >= TN || pg[j] < 0) continue;
+                        const int y = ((pg[j] * p.kv_heads + it.g) * 2 + h) * p.page_tokens + ((t0 + j * piece_rows) & (p.page_tokens - 1));
+#pragma unroll
+                        for (int x = 0; x < D / 64; ++x)
+                            tma_load_hint(dst + x * TN * 128 + j * piece_rows * 128, &map, 64 * x, y, full + s, policy);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        if (!live && lane == 0 && !G::q8) {
+            // let every copy still in flight land before the block exits: the last of each slot
+            volatile int go_on = 0;
+            for (int i = max(0, t - most); i < t; ++i)
+                if (i >= t - slots) mbar_wait_bounded(full + i % slots, (i / slots) & 1, &go_on, 100000000ull);
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- products
+        constexpr uint32_t kType = BF ? (1u << 7) | (1u << 10) : 0u;
+        constexpr uint32_t kIdescS = idesc_f16_f32(128, TN) | kType;
+        constexpr uint32_t kIdescO = idesc_f16_f32(128, D) | kType | (G::q8 ? 0u : 1u << 16);  // (16-bit pools: V by dims)
+        const uint32_t k0 = smem_u32(sm), v0 = smem_u32(sm + G::off_v), q0 = smem_u32(sm + G::off_q);
+        int t = 0;                 // tiles so far
+        int done[2] = {0, 0};      // products P V of each stream so far
+        int asked[2] = {0, 0};     // scores
+        int pend[2] = {-1, -1};    // the tile whose P V is still to come
+        bool first[2] = {true, true};  // .. and whether it is its item's first
+        // P V of stream s, and V's slot back if this is its last use
+        auto product_o = [&](int s, bool last) {
+            const int n = done[s], x = NS == 2 ? s : n & 1, vs = pend[s] % G::v_slots;
+            await(pfull + x, NS == 2 ? n & 1 : (n >> 1) & 1);
+            await(vready + vs, (pend[s] / G::v_slots) & 1);
+            if (!live) return;
+            tc_fence_after();
+            const uint32_t a = tmem + x * TN, o = tmem + G::col_o + s * D;
+            const uint32_t acc = !first[s] || accum_sm[s] != 0;
+            const uint32_t vb = v0 + vs * G::tile;
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < TN / 16; ++ks) {
+                    const uint64_t b = G::q8 ? smem_desc_sw128(vb) + (((ks >> 2) * (D * 128) + (ks & 3) * 32) >> 4)
+                                             : desc_mn(vb, TN * 128) + ks * (2048 >> 4);
+                    tc_mma_f16_ts(o, a + 8 * ks, b, kIdescO, ks ? 1 : acc);
+                }
+                tc_commit(odone + s);
+                if (last) tc_commit(vempty + vs);
+            }
+            __syncwarp();
+            ++done[s];
+            pend[s] = -1;
+        };
+        auto product_s = [&](int s, int ksl, int qs, bool last) {
+            const int x = NS == 2 ? s : asked[s] & 1;
+            const uint64_t aq = smem_desc_sw128(q0 + qs * G::q_tile), bk = smem_desc_sw128(k0 + ksl * G::k_tile);
+            if (elect_one()) {
+#pragma unroll
+                for (int part = 0; part < (G::q8 ? 2 : 1); ++part)
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        tc_mma_f16_ss(tmem + x * TN, aq + (((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4),
+                                      bk + ((part * G::tile + (ks >> 2) * (TN * 128) + (ks & 3) * 32) >> 4), kIdescS, part + ks > 0);
+                tc_commit(sfull + x);
+                if (last) tc_commit(kempty + ksl);
+            }
+            __syncwarp();
+            ++asked[s];
+        };
+        for (int item = blockIdx.x; item < total && live; item += gridDim.x) {
+            const Record it = next_record();
+            const int n = k - 1;
+            await(qfull, n & 1);
+            if (NS == 2 && !p.decode) await(qfull + 1, n & 1);
+            bool begun[2] = {false, false};
+            for (int i = 0; i < it.nt && live; ++i, ++t) {
+                const int ksl = t % G::k_slots;
+                await(kfull + ksl, (t / G::k_slots) & 1);
+                tc_fence_after();
+                if constexpr (NS == 1) {
+                    if (!live) break;
+                    product_s(0, ksl, 0, true);
+                    if (pend[0] >= 0) product_o(0, true);
+                    pend[0] = t, first[0] = !begun[0], begun[0] = true;
+                } else {
+                    const int from = p.decode ? tile_at(it, i) & 1 : 0, to = p.decode ? from : 1;
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        if (s < from || s > to) continue;
+                        if (pend[s] >= 0) product_o(s, p.decode || s == 1);
+                        if (!live) break;
+                        product_s(s, ksl, p.decode ? 0 : s, s == to);
+                        pend[s] = t, first[s] = !begun[s], begun[s] = true;
+                    }
+                }
+            }
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+                if (pend[s] >= 0 && live) product_o(s, NS == 1 || p.decode || s == 1);
+        }
+        // every product issued has finished before the tensor memory is released
+        if (elect_one()) tc_commit(drained);
+        volatile int go_on = 0;
+        mbar_wait_bounded(drained, 0, &go_on, 10000000000ull);
+        __syncwarp();
+    } else if (warp == 3 && !G::q8) {
+        // ---------------------------------------------------------------- V's rows that must not count
+        // Slots that nobody sees hold anything (and so do those of missing pages): zero.  One that some rows see
+        // and whose V is not finite is marked, to be added query by query, and zero in the product.
+        int t = 0;
+        for (int item = blockIdx.x; item < total && live; item += gridDim.x) {
+            const Record it = next_record();
+            for (int i = 0; i < it.nt && live; ++i, ++t) {
+                const int t0 = tile_at(it, i) * TN, vs = t % G::v_slots;
+                await(vfull + vs, (t / G::v_slots) & 1);
+                if (!live) break;
+                const int miss = miss_sm[vs];
+                if (miss || edge(it, t0)) {
+                    uint8_t* vt = sm + G::off_v + vs * G::tile;
+#pragma unroll 1
+                    for (int j = 0; j < TN / 32; ++j) {
+                        const int row = lane + 32 * j, tok = t0 + row;
+                        bool zero = gone(it, tok) || ((miss >> (row >> piece_shift)) & 1), odd = false;
+                        if (!zero && !(tok < it.minlen && (tok >= it.maxlo || tok < p.sinks))) {
+                            constexpr uint32_t ex = BF ? 0x7F80u : 0x7C00u;
+                            auto bad = [&](uint32_t w) { return (w & ex) == ex || ((w >> 16) & ex) == ex; };
+#pragma unroll 1
+                            for (int x = 0; x < D / 64; ++x)
+#pragma unroll
+                                for (int c = 0; c < 8; ++c) {
+                                    const uint4 v = *reinterpret_cast<const uint4*>(vt + x * TN * 128 + row * 128 + 16 * ((c + lane) & 7));
+                                    odd |= bad(v.x) || bad(v.y) || bad(v.z) || bad(v.w);
+                                }
+                        }
+                        if (zero || odd) {
+#pragma unroll 1
+                            for (int x = 0; x < D / 64; ++x)
+#pragma unroll
+                                for (int c = 0; c < 8; ++c)
+                                    *reinterpret_cast<uint4*>(vt + x * TN * 128 + row * 128 + 16 * ((c + lane) & 7)) = make_uint4(0, 0, 0, 0);
+                        }
+                        const uint32_t word = __ballot_sync(0xffffffffu, odd);
+                        if (lane == 0) odd_sm[vs * 4 + j] = word;
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(vready + vs);
+            }
+        }
+    }
+    } else if (warp < 4 + G::soft_warps) {
+        if constexpr (NS == 2) setmaxnreg_inc<G::q8 ? 104 : 200>();
+        // ---------------------------------------------------------------- softmax: a query per thread
+        const int s = (warp - 4) >> 2, me = tid & 127;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+        const uint32_t ocol = lanes + G::col_o + s * D;
+        int tiles = 0;  // all tiles so far
+        int n = 0;      // the stream's
+        int merges = 0;
+        for (int item = blockIdx.x; item < total && live; item += gridDim.x) {
+            const Record it = next_record();
+            if (!live) break;
+            const int q = it.q0 + (NS == 2 && !p.decode ? 128 * s : 0) + me;
+            const bool valid = q < it.nq;
+            const int r = it.r0 + (valid ? q / p.group : 0), h = it.g * p.group + (valid ? q % p.group : 0);
+            const int len = valid ? length_of(p, r) : 0, from = max(0, len - p.window), first = min(p.sinks, len);
+            if (s == 0 || !p.decode) {  // the query, swizzled as the copies do
+                const uint4* src = reinterpret_cast<const uint4*>(p.q + r * p.q_stride + static_cast<int64_t>(h) * D);
+                uint8_t* dst = sm + G::off_q + s * G::q_tile + me * 128;
+#pragma unroll
+                for (int c0 = 0; c0 < D / 8; c0 += 8) {
+                    uint4 v[8];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) v[c] = valid ? src[c0 + c] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        v[c].x ^= p.flip, v[c].y ^= p.flip, v[c].z ^= p.flip, v[c].w ^= p.flip;
+                        *reinterpret_cast<uint4*>(dst + (c0 >> 3) * (128 * 128) + ((c ^ (me & 7)) << 4)) = v[c];
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(qfull + s);
+            }
+            float l = 0.f, lim = -INFINITY, base = 0.f;  // sum, reference and slack, what comes off the scores
+            bool fresh = true;                           // O holds nothing yet
+            for (int i = 0; i < it.nt; ++i) {
+                const int tile = tile_at(it, i), t0 = tile * TN, tv = tiles + i, vs = tv % G::v_slots;
+                if (NS == 2 && p.decode && (tile & 1) != s) continue;
+                const int x = NS == 2 ? s : n & 1;
+                const uint32_t scol = lanes + x * TN;
+                await(sfull + x, NS == 2 ? n & 1 : (n >> 1) & 1);
+                await(vready + vs, (tv / G::v_slots) & 1);
+                if (!live) break;
+                tc_fence_after();
+                const int miss = miss_sm[vs];
+                const bool some = edge(it, t0);
+                // Scores: all of them in registers, or (q8_0, whose converting warps need registers) 32 at a time, read twice.
+                constexpr int kHeld = G::q8 ? 32 : TN;
+                float v[kHeld];
+                auto masked = [&](int c, float* u) {
+                    if (some || miss) {
+                        const int jl = len - t0 - c, jf = from - t0 - c, js = first - t0 - c;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (!(j < jl && (j >= jf || j < js))) u[j] = -INFINITY;
+                        if (miss) {  // (a piece is 16 tokens at least)
+                            const bool lost[2] = {((miss >> (c >> piece_shift)) & 1) != 0, ((miss >> ((c + 16) >> piece_shift)) & 1) != 0};
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (lost[j >> 4]) u[j] = -INFINITY;
+                        }
+                    }
+                };
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                if constexpr (!G::q8) {
+#pragma unroll
+                    for (int c = 0; c < TN; c += 32) tmem_ld32(scol + c, v + c);
+                    tc_wait_ld();
+                }
+#pragma unroll
+                for (int c = 0; c < TN; c += 32) {
+                    float* u = G::q8 ? v : v + c;
+                    if constexpr (G::q8) {
+                        tmem_ld32(scol + c, u);
+                        tc_wait_ld();
+                    }
+                    masked(c, u);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], u[j]);
+                }
+                const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.c2;  // (a NaN is no maximum)
+                const bool passed = m > lim;
+                if (__any_sync(0xffffffffu, passed)) {
+                    float alpha = 1.f;
+                    if (passed) {
+                        const bool fine = fabsf(m) < kFine;
+                        const float to = fine ? m - kShift : m;
+                        alpha = lim == -INFINITY ? 0.f : ex2(base - to);
+                        base = to;
+                        lim = fine ? m + kSlack : m;
+                        l *= alpha;
+                    }
+                    if (!fresh) {
+                        if (NS == 1) await(odone, (n - 1) & 1);  // (two streams: the scores came after the last product)
+                        if (!live) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            float o[32];
+                            tmem_ld32(ocol + c, o);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) o[j] *= alpha;
+                            tmem_st32f(ocol + c, o);
+                        }
+                    }
+                }
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < TN; c += 32) {
+                    float* u = G::q8 ? v : v + c;
+                    if constexpr (G::q8) {
+                        tmem_ld32(scol + c, u);
+                        tc_wait_ld();
+                        masked(c, u);
+                    }
+                    uint32_t w[16];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float a = ex2(fmaf(u[j], p.c2, -base)), b = ex2(fmaf(u[j + 1], p.c2, -base));
+                        sum[(j & 2)] += a;
+                        sum[(j & 2) + 1] += b;
+                        w[j / 2] = pack2<BF>(a, b);
+                    }
+                    tmem_st16(scol + c / 2, w);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tc_wait_st();
+                // ---- tokens whose V is not finite, to those that see them
+                uint32_t odd = 0;
+                if (some) odd = odd_sm[vs * 4] | odd_sm[vs * 4 + 1] | (TN > 64 ? odd_sm[vs * 4 + 2] | odd_sm[vs * 4 + 3] : 0u);
+                if (odd) {
+                    if (!fresh && NS == 1) await(odone, (n - 1) & 1);
+                    if (!live) break;
+                    tc_fence_after();
+                    add_odd<FMT, D>(p, it.a, it.g, t0, const_cast<const uint32_t*>(odd_sm) + vs * 4, ocol, scol, len, from, first, fresh);
+                }
+                if (fresh && me == 0) accum_sm[s] = odd != 0;
+                fresh = false;
+                ++n;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pfull + x);
+            }
+            tiles += it.nt;
+            if (!live) break;
+            if (!fresh) await(odone + s, (n - 1) & 1);
+            if (!live) break;
+            tc_fence_after();
+
+            // ---- what became of the item
+            float w0 = 1.f, w1 = 0.f;  // the streams' weights
+            const float* stage = reinterpret_cast<const float*>(sm + G::off_q + (warp & 3) * 4096) + lane;  // column c: 16 KB * (c / 32) + 128 * (c % 32)
+            if (NS == 2 && p.decode) {
+                if (s == 1) {
+                    await(mfree, merges & 1);  // (the queries, over which the outputs go, are read)
+                    if (!live) break;
+                    ml_sm[me] = make_float2(base, l);
+                    if (!fresh) {
+                        float* to = const_cast<float*>(stage);
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            float o[32];
+                            tmem_ld32(ocol + c, o);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) to[(c >> 5) * 4096 + j * 32] = o[j];
+                        }
+                        tc_fence_before();
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(mfull);
+                    ++merges;
+                    continue;
+                }
+                if (lane == 0) mbar_arrive(mfree);
+                await(mfull, merges & 1);
+                if (!live) break;
+                ++merges;
+                const float2 other = ml_sm[me];
+                // (a sum of 0: nothing seen, and nothing of the other's outputs counts)
+                const float top = l == 0.f ? other.x : other.y == 0.f ? base : fmaxf(base, other.x);
+                w0 = l == 0.f ? 0.f : ex2(base - top);
+                w1 = other.y == 0.f ? 0.f : ex2(other.x - top);
+                l = l * w0 + other.y * w1;
+                base = top;
+            }
+            int slot = 0;
+            bool write = valid;
+            if (p.chunk && valid) {
+                const Chunks c = chunks_of(p, len);
+                slot = it.chunk < c.first ? it.chunk : c.first + it.chunk - c.from;
+                write = it.chunk < c.first || (it.chunk >= c.from && it.chunk < c.end);
+            }
+            const int64_t at = static_cast<int64_t>(r) * p.heads + h;
+            const float inv = p.chunk ? 1.f : l == 0.f ? 0.f : 1.f / l;
+            const bool none = l == 0.f;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                float o[32];
+                if (!fresh) tmem_ld32(ocol + c, o);
+                tc_wait_ld();
+                if (NS == 2 && p.decode) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = (w0 == 0.f ? 0.f : o[j] * w0) + (w1 == 0.f ? 0.f : stage[(c >> 5) * 4096 + j * 32] * w1);
+                }
+                if (write) {
+                    if (p.chunk) {
+                        float* to = p.o + (at * p.slots + slot) * D + c;
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            *reinterpret_cast<float4*>(to + j) = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8) store_out(p, at * D + c + j, o + j, [&](float y) { return none ? 0.f : y * inv; });
+                    }
+                }
+            }
+            if (write) {
+                if (p.chunk) *reinterpret_cast<float2*>(p.ml + (at * p.slots + slot) * 2) = make_float2(base, l);
+                else if (p.lse) p.lse[at] = none ? -INFINITY : (base + log2f(l)) * 0.6931471805599453f;
+            }
+            tc_fence_before();
+            __syncwarp();
+        }
+        if (!live && lane == 0) atomicOr(p.err, kErrTimeout);
+    } else if constexpr (G::q8) {
+        setmaxnreg_dec<88>();
+        if (warp < 8 + G::soft_warps) {
+            // ---------------------------------------------------------------- K to fp16: a token per thread
+            const int me = tid & 127, slot = me & 63, key = q8_key(slot & 7);
+            int t = 0;
+            for (int item = blockIdx.x; item < total && live; item += gridDim.x) {
+                const Record it = next_record();
+                for (int i = 0; i < it.nt && live; ++i, ++t) {
+                    const int t0 = tile_at(it, i) * TN, ks = t % G::k_slots;
+                    const int pg = __shfl_sync(0xffffffffu, page_of(it, t0), me >> 6);
+                    uint4 row[8];
+                    uint2 sc = make_uint2(0, 0);
+                    if (pg >= 0) {
+                        const uint8_t* b = p.pool + (static_cast<int64_t>(pg) * p.kv_heads + it.g) * kQ8Rec;
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) row[c] = *reinterpret_cast<const uint4*>(b + slot * 128 + 16 * (c ^ key));
+                        sc = *reinterpret_cast<const uint2*>(b + 8192 + slot * 8);
+                    }
+                    if (t >= G::k_slots) await(kempty + ks, (t / G::k_slots - 1) & 1);
+                    if (!live) break;
+                    if (pg >= 0) {
+                        uint8_t* dst = sm + ks * G::k_tile + me * 128;
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {  // eight dims: one 16-byte piece of each part
+                            const uint32_t u0 = ((c & 1) ? row[c >> 1].z : row[c >> 1].x) ^ 0x80808080u;
+                            const uint32_t u1 = ((c & 1) ? row[c >> 1].w : row[c >> 1].y) ^ 0x80808080u;
+                            const uint32_t w = (c >> 3) ? sc.y : sc.x;  // scales of dims 0 .. 63 or 64 .. 127, 32 each
+                            const __half2 d = __half2half2((c >> 2) & 1 ? __high2half(as_h2(w)) : __low2half(as_h2(w)));
+                            const __half2 z[4] = {i8_to_h2(u0, 0x4140u), i8_to_h2(u0, 0x4342u), i8_to_h2(u1, 0x4140u), i8_to_h2(u1, 0x4342u)};
+                            uint32_t hi[4], lo[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const __half2 x = __hmul2(z[j], d);
+                                hi[j] = as_u32(x);
+                                lo[j] = as_u32(__hfma2(z[j], d, __hneg2(x)));
+                            }
+                            const int at = (c >> 3) * (TN * 128) + (((c & 7) ^ (me & 7)) << 4);
+                            *reinterpret_cast<uint4*>(dst + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                            *reinterpret_cast<uint4*>(dst + G::tile + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(kfull + ks);
+                }
+            }
+        } else {
+            // ---------------------------------------------------------------- V to fp16: a dim per thread
+            const int me = tid & 127, w4 = warp & 3;
+            int t = 0, z = 0;
+            for (int item = blockIdx.x; item < total && live; item += gridDim.x) {
+                const Record it = next_record();
+                for (int i = 0; i < it.nt && live; ++i, ++t) {
+                    const int t0 = tile_at(it, i) * TN, vs = t % G::v_slots;
+                    const int pages = page_of(it, t0);
+                    const int pg[2] = {__shfl_sync(0xffffffffu, pages, 0), __shfl_sync(0xffffffffu, pages, 1)};
+                    uint4 row[8];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        row[c] = make_uint4(0, 0, 0, 0);
+                        const int x = pg[c >> 2];
+                        if (x >= 0)
+                            row[c] = *reinterpret_cast<const uint4*>(p.pool + (static_cast<int64_t>(x) * p.kv_heads + it.g) * kQ8Rec + kQ8Half + me * 64 + 16 * (c & 3));
+                    }
+                    if (t >= G::v_slots) await(vempty + vs, (t / G::v_slots - 1) & 1);
+                    if (!live) break;
+                    const int miss = (pg[0] == -2 ? 1 : 0) | (pg[1] == -2 ? 2 : 0);
+                    const bool some = miss || edge(it, t0);
+                    uint32_t zero[4] = {0, 0, 0, 0};
+                    if (some) {  // (by token, as warp 3 does for 16-bit pools; what is not finite is a scale, or too large for fp16)
+                        const int tok = t0 + me, x = pg[me >> 6];
+                        bool none = gone(it, tok) || x < 0, odd = false;
+                        if (!none && !(tok < it.minlen && (tok >= it.maxlo || tok < p.sinks))) {
+                            const uint8_t* b = p.pool + (static_cast<int64_t>(x) * p.kv_heads + it.g) * kQ8Rec + kQ8Half + 8192;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                odd |= (*reinterpret_cast<const uint16_t*>(b + (j * 64 + (me & 63)) * 2) & 0x7FFFu) >= (24u << 10);  // 512
+                        }
+                        const uint32_t who = __ballot_sync(0xffffffffu, odd), all = __ballot_sync(0xffffffffu, none || odd);
+                        if (lane == 0) odd_sm[vs * 4 + w4] = who, zero_sm[(z & 1) * 4 + w4] = all;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(zdone);
+                        await(zdone, z & 1);
+                        if (!live) break;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) zero[j] = zero_sm[(z & 1) * 4 + j];
+                        ++z;
+                    }
+                    if (me == 0) miss_sm[vs] = miss;
+                    uint8_t* dst = sm + G::off_v + vs * G::tile + me * 128;
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {  // eight tokens
+                        const int x = pg[c >> 3];
+                        uint4 sc = make_uint4(0, 0, 0, 0);
+                        if (x >= 0)
+                            sc = *reinterpret_cast<const uint4*>(p.pool + (static_cast<int64_t>(x) * p.kv_heads + it.g) * kQ8Rec + kQ8Half + 8192 + w4 * 128 + 16 * (c & 7));
+                        const uint32_t off = (zero[c >> 2] >> (8 * (c & 3))) & 0xFFu;
+                        uint32_t d[4] = {sc.x, sc.y, sc.z, sc.w};
+                        if (off) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) d[j] &= ((off >> (2 * j)) & 1 ? 0u : 0xFFFFu) | ((off >> (2 * j + 1)) & 1 ? 0u : 0xFFFF0000u);
+                        }
+                        const uint32_t u0 = ((c & 1) ? row[c >> 1].z : row[c >> 1].x) ^ 0x80808080u;
+                        const uint32_t u1 = ((c & 1) ? row[c >> 1].w : row[c >> 1].y) ^ 0x80808080u;
+                        const __half2 zz[4] = {i8_to_h2(u0, 0x4140u), i8_to_h2(u0, 0x4342u), i8_to_h2(u1, 0x4140u), i8_to_h2(u1, 0x4342u)};
+                        uint32_t o[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) o[j] = as_u32(__hmul2(zz[j], as_h2(d[j])));
+                        *reinterpret_cast<uint4*>(dst + (c >> 3) * (D * 128) + (((c & 7) ^ (me & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(vready + vs);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+template <int FMT, int D>
+cudaError_t launch_one(const Launch& a, cudaStream_t s) {
+    using G = Geo<FMT, D>;
+    static_assert(G::smem(kMaxAgents) <= kMaxShared);
+    static Once once;
+    // (the registers that the roles deal out are those of the launch: fewer would leave a role waiting)
+    static const int regs = [] {
+        cudaFuncAttributes f = {};
+        return cudaFuncGetAttributes(&f, attend_window_tc<FMT, D>) == cudaSuccess ? f.numRegs : 0;
+    }();
+    if (G::streams == 2 && regs < (G::q8 ? 96 : 168)) return cudaErrorLaunchOutOfResources;
+    const cudaError_t e = once.allow_shared(attend_window_tc<FMT, D>, a.device);
+    if (e != cudaSuccess) return e;
+    attend_window_tc<FMT, D><<<a.grid, G::threads, G::smem(a.p.agents), s>>>(a.map, a.p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_q8(const Launch& a, cudaStream_t s);
+cudaError_t launch_f16(const Launch& a, int head_dim, cudaStream_t s);
+cudaError_t launch_bf16(const Launch& a, int head_dim, cudaStream_t s);
+
+}  // namespace window
+}  // namespace qmm
