@@ -12,17 +12,19 @@
 //   prompts (more than 128 queries a sequence): two tiles of queries, which share each K and V tile;
 //   decode steps: one tile of queries, whose tokens' tiles are dealt to two streams by their parity; the streams
 //     meet at the end through shared memory.
-// Either way two streams take turns on the tensor cores: while one's scores become probabilities, the other's products
-// run.  (Head dimension 256 leaves tensor memory room for one stream; its scores have two buffers instead.)
+// Either way two streams take turns on the tensor cores (one at head dimension 256, for which tensor memory has no more
+// room).  Tiles have 64 tokens, so that each stream's scores have two buffers: those of the next tile are there when
+// the softmax is done with one, which never waits for a product that waits for it.
 // The tiles of an item are those that some of its rows sees: the first ones (sinks), and the window's.  Where few
 // items would leave SMs idle, tokens are cut into chunks at fixed places of a sequence, an item each, whose unnormalised
 // outputs a second kernel joins.  All choices are made by the plan's dims, so a row's bits do not depend on its company.
-//   warp 0      forms the items' records; 16-bit pools: asks for K tiles
-//   warp 1      issues the products
-//   warp 2      16-bit pools: asks for V tiles
+//   warp 0      forms the items' records; asks for K tiles (q8_0: as they are stored)
+//   warp 1      one thread issues the products
+//   warp 2      asks for V tiles
 //   warp 3      16-bit pools: zeroes the rows of V that must not count, where some are
 //   warps 4 ..  softmax, four a stream
-//   q8_0: four more convert K (a token a thread), four V (a dim a thread), from memory through registers
+//   q8_0: four more convert K (half a token a thread), four V (a dim a thread), both to two fp16 parts whose sum is
+//               quant times scale
 // A query's reference is its first tile's maximum and moves only when a score passes it by more than 2^kSlack; each
 // query decides for itself.
 #pragma once
@@ -55,7 +57,7 @@ struct Params {
     int64_t q_stride;
     int32_t max_pages, pool_pages, page_shift, page_tokens, heads, kv_heads, group, agents, rows, max_agent_rows, cap;
     int32_t window, sinks, out_type, format, head_dim;
-    int32_t chunk;   // tokens per chunk, a multiple of 256; 0: one item has all of a query's tokens and writes its output
+    int32_t chunk;   // tokens per chunk, a multiple of 128; 0: one item has all of a query's tokens and writes its output
     int32_t slots;   // partials per (row, head)
     int32_t decode;  // one tile of queries an item, tokens dealt to two streams
     uint32_t flip;   // sign bits that a negative scale puts on the queries
@@ -72,24 +74,29 @@ template <int FMT, int D>
 struct Geo {
     static constexpr bool q8 = FMT == QMM_KV_Q8_0;
     static constexpr int streams = D == 256 ? 1 : 2;
-    static constexpr int TN = D == 256 ? 64 : 128;               // tokens of a tile
-    static constexpr int tile = TN * D * 2;                      // bytes of a tile's K or V in 16 bits
-    static constexpr int k_tile = q8 ? 2 * tile : tile;          // q8_0: K's high and low parts
-    static constexpr int k_slots = D == 64 ? 4 : q8 ? 1 : 2, v_slots = D == 64 ? 4 : 2;
+    static constexpr int TN = 64;                                // tokens of a tile
+    static constexpr int part = TN * D * 2;                      // bytes of a tile's K or V in 16 bits
+    static constexpr int tile = q8 ? 2 * part : part;            // q8_0: high and low parts
+    static constexpr int k_slots = D == 64 ? 8 : D == 128 && !q8 ? 4 : 2, v_slots = q8 ? 1 : k_slots;
+    static constexpr int info_slots = v_slots < 4 ? 4 : v_slots;  // V tiles of which the softmax is told (see there)
+    static constexpr int raw_slots = q8 ? 2 : 0;                 // pages on their way, K and V
     static constexpr int q_tile = 128 * D * 2;
     static constexpr int soft_warps = 4 * streams, conv_warps = q8 ? 8 : 0;
     static constexpr int threads = 32 * (4 + soft_warps + conv_warps);
-    // tensor memory: S (a buffer per stream, or two), P over it, and O
+    // tensor memory: S (two buffers per stream), P over it, and O
     static constexpr int col_o = 256;
     // shared memory, after aligning to 1024
-    static constexpr int off_v = k_slots * k_tile;
+    static constexpr int off_v = k_slots * tile;
     static constexpr int off_q = off_v + v_slots * tile;
-    static constexpr int off_ml = off_q + streams * q_tile;      // [128] reference and sum of the second stream
+    static constexpr int off_raw = off_q + streams * q_tile;     // K's pages, then V's
+    static constexpr int off_ml = off_raw + 2 * raw_slots * kQ8Half;  // [128] reference and sum of the second stream
     static constexpr int off_item = off_ml + 128 * 8;            // [2] of Record
-    static constexpr int off_bar = off_item + 2 * 64;
-    static constexpr int bars = 2 * k_slots + 3 * v_slots + 2 + 2 + 2 + 2 + 2 + 2 + 4;
-    static constexpr int off_misc = off_bar + bars * 8;          // tmp[33], abort, tmem, accumulate[2], miss[4], odd[4][4], zero[2][4]
-    static constexpr int off_seq = (off_misc + 68 * 4 + 15) / 16 * 16;
+    static constexpr int off_dv = off_item + 2 * 64;             // q8_0: V's scales, zero where a token must not count: [4][64] fp16
+    static constexpr int off_bar = off_dv + (q8 ? 512 : 0);
+    static constexpr int bars = 2 * k_slots + 3 * v_slots + info_slots + 4 * raw_slots + 2 + 4 + 4 + 2 + 2 + 2 + 2 + 3;
+    // tmp[33], abort, tmem, accumulate[2], miss[8] (of V tiles), odd[8][2], miss[16] (of all tiles), raw[2][2]
+    static constexpr int off_misc = (off_bar + bars * 8 + 15) / 16 * 16;
+    static constexpr int off_seq = (off_misc + 84 * 4 + 15) / 16 * 16;
     static constexpr int smem(int agents) { return 1024 + off_seq + (agents + 1) * 16; }
 };
 
@@ -174,6 +181,24 @@ __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
     return v;
 }
 
+// Two fp32 numbers at once.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t r, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 template <bool BF>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     uint32_t d;
@@ -210,22 +235,6 @@ __device__ __forceinline__ Chunks chunks_of(const Params& p, int n) {
     c.from = max(c.first, max(0, n - p.window) / p.chunk);
     c.end = (n + p.chunk - 1) / p.chunk;
     return c;
-}
-
-template <typename F>
-__device__ __forceinline__ void store_out(const Params& p, int64_t at, const float* v, F f) {  // 8 neighbouring elements
-    if (p.out_type == QMM_TYPE_F32) {
-        float* o = static_cast<float*>(p.out) + at;
-        *reinterpret_cast<float4*>(o) = make_float4(f(v[0]), f(v[1]), f(v[2]), f(v[3]));
-        *reinterpret_cast<float4*>(o + 4) = make_float4(f(v[4]), f(v[5]), f(v[6]), f(v[7]));
-    } else {
-        uint4 w;
-        if (p.out_type == QMM_TYPE_F16)
-            w = make_uint4(pack2<false>(f(v[0]), f(v[1])), pack2<false>(f(v[2]), f(v[3])), pack2<false>(f(v[4]), f(v[5])), pack2<false>(f(v[6]), f(v[7])));
-        else
-            w = make_uint4(pack2<true>(f(v[0]), f(v[1])), pack2<true>(f(v[2]), f(v[3])), pack2<true>(f(v[4]), f(v[5])), pack2<true>(f(v[6]), f(v[7])));
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at) = w;
-    }
 }
 
 // The table of sequences, the same in every block: seq[a] = (first item, chunks of the first slots, the window's
@@ -368,7 +377,7 @@ __device__ __noinline__ void add_odd(const Params& p, int a, int g, int t0, cons
         tc_wait_ld();
 #pragma unroll 1
         for (int j = 0; j < Geo<FMT, D>::TN; ++j) {
-            if (!((odd[j >> 5] >> (j & 31)) & 1)) continue;
+            if (!((odd[j & 1] >> (j >> 1)) & 1)) continue;
             const uint32_t both = tmem_ld1(pcol + j / 2);
             tc_wait_ld();
             const float pr = wide(j & 1 ? both >> 16 : both & 0xFFFFu, BF);
@@ -408,15 +417,17 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
     Record* item_sm = reinterpret_cast<Record*>(sm + G::off_item);
     uint64_t* kfull = reinterpret_cast<uint64_t*>(sm + G::off_bar);
     uint64_t *kempty = kfull + G::k_slots, *vfull = kempty + G::k_slots, *vempty = vfull + G::v_slots, *vready = vempty + G::v_slots;
-    uint64_t *qfull = vready + G::v_slots, *sfull = qfull + 2, *pfull = sfull + 2, *odone = pfull + 2, *ifull = odone + 2, *iempty = ifull + 2;
-    uint64_t *mfree = iempty + 2, *mfull = mfree + 1, *zdone = mfull + 1, *drained = zdone + 1;
+    uint64_t *vinfo = vready + G::v_slots, *rfull = vinfo + G::info_slots, *rempty = rfull + 2 * G::raw_slots;  // (K's, then V's)
+    uint64_t *qfull = rempty + 2 * G::raw_slots, *sfull = qfull + 2, *pfull = sfull + 4, *odone = pfull + 4, *ofin = odone + 2;
+    uint64_t *ifull = ofin + 2, *iempty = ifull + 2, *mfree = iempty + 2, *mfull = mfree + 1, *drained = mfull + 1;
     int* tmp = reinterpret_cast<int*>(sm + G::off_misc);
     volatile int* abort_flag = tmp + 33;
     uint32_t* tmem_sm = reinterpret_cast<uint32_t*>(tmp + 34);
     volatile int* accum_sm = tmp + 35;                                          // [2] O holds something before the first product
-    volatile int* miss_sm = tmp + 37;                                           // [4] a tile's pieces that are outside the pool
-    volatile uint32_t* odd_sm = reinterpret_cast<uint32_t*>(tmp + 41);          // [4][4] tokens that are taken query by query
-    volatile uint32_t* zero_sm = reinterpret_cast<uint32_t*>(tmp + 57);         // [2][4] q8_0: tokens whose V is zero
+    volatile int* miss_sm = tmp + 37;                                           // [8] a tile's pieces that are outside the pool
+    volatile uint32_t* odd_sm = reinterpret_cast<uint32_t*>(tmp + 45);          // [8][2] tokens that are taken query by query: even ones, odd ones
+    volatile int* kmiss_sm = tmp + 61;                                          // [16] the same of the last 16 tiles (more than are under way)
+    volatile int* raw_sm = tmp + 77;                                            // q8_0, [2][2]: a page's number, -1 not needed, -2 outside the pool
     int4* seq = reinterpret_cast<int4*>(sm + G::off_seq);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int qt = NS == 2 && !p.decode ? 256 : 128;
@@ -424,17 +435,18 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
     if (tid == 0) {
         for (int i = 0; i < G::k_slots; ++i) mbar_init(kfull + i, G::q8 ? 4 : 1), mbar_init(kempty + i, 1);
         for (int i = 0; i < G::v_slots; ++i) mbar_init(vfull + i, 1), mbar_init(vempty + i, 1), mbar_init(vready + i, G::q8 ? 4 : 1);
+        for (int i = 0; i < G::info_slots; ++i) mbar_init(vinfo + i, G::q8 ? 4 : 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(qfull + i, 4);
-            mbar_init(sfull + i, 1);
-            mbar_init(pfull + i, 4);
             mbar_init(odone + i, 1);
+            mbar_init(ofin + i, 1);
             mbar_init(ifull + i, 1);
-            mbar_init(iempty + i, (G::q8 ? 1 + G::conv_warps : 3) + G::soft_warps);
+            mbar_init(iempty + i, (G::q8 ? 2 + G::conv_warps : 3) + G::soft_warps);
         }
+        for (int i = 0; i < 4; ++i) mbar_init(sfull + i, 1), mbar_init(pfull + i, 4);
+        for (int i = 0; i < 2 * G::raw_slots; ++i) mbar_init(rfull + i, 1), mbar_init(rempty + i, 4);
         mbar_init(mfree, 4);
         mbar_init(mfull, 4);
-        mbar_init(zdone, 4);
         mbar_init(drained, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -471,7 +483,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
     auto edge = [&](const Record& it, int t0) { return !(t0 + TN <= it.minlen && (t0 >= it.maxlo || t0 + TN <= p.sinks)); };
     // a token that no row of the item sees
     auto gone = [&](const Record& it, int t) { return t >= it.hi || (t < it.lo && t >= it.sink_end); };
-    constexpr int kPieces = G::q8 ? 2 : TN / 16;
+    constexpr int kPieces = G::q8 ? 1 : TN / 16;
     const int piece_rows = min(TN, p.page_tokens), piece_shift = 31 - __clz(piece_rows);
     // lane i: the page of piece i of a tile, -1 if nobody needs it, -2 if it is outside the pool
     auto page_of = [&](const Record& it, int t0) {
@@ -488,17 +500,17 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
     };
 
     // Registers go where the scores are (the shares add up to what the block was launched with, or less:
-    // 256 * 200 + 128 * 104 = 384 * 168; q8_0 256 * 104 + 384 * 88 <= 640 * 96).
+    // 256 * 200 + 128 * 104 = 384 * 168; q8_0 256 * 120 + 384 * 80 = 640 * 96).
     if (warp < 4) {
-    if constexpr (NS == 2) setmaxnreg_dec<G::q8 ? 88 : 104>();
-    if (warp == 0 || (warp == 2 && !G::q8)) {
+    if constexpr (NS == 2) setmaxnreg_dec<G::q8 ? 80 : 104>();
+    if (warp == 0 || warp == 2) {
         // ---------------------------------------------------------------- records; K tiles (warp 0), V tiles (warp 2)
         const int h = warp == 2;
-        constexpr int most = G::k_slots > G::v_slots ? G::k_slots : G::v_slots;
-        const int slots = h ? G::v_slots : G::k_slots;
-        uint64_t* full = h ? vfull : kfull;
-        uint64_t* empty = h ? vempty : kempty;
-        uint8_t* ring = sm + (h ? G::off_v : 0);
+        constexpr int kSlots = G::q8 ? G::raw_slots : G::k_slots;
+        static_assert(G::q8 || G::k_slots == G::v_slots);
+        uint64_t* full = G::q8 ? rfull + h * kSlots : h ? vfull : kfull;
+        uint64_t* empty = G::q8 ? rempty + h * kSlots : h ? vempty : kempty;
+        uint8_t* ring = sm + (G::q8 ? G::off_raw + h * kSlots * kQ8Half : h ? G::off_v : 0);
         // (a prompt's tiles are read by other blocks as well)
         const uint64_t policy = p.decode ? l2_policy_evict_first() : l2_policy_evict_last();
         int t = 0;
@@ -515,14 +527,13 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                     mbar_arrive(ifull + (k & 1));
                 }
                 ++k;
-                if (G::q8) continue;
             }
             int next = it.nt > 0 ? page_of(it, tile_at(it, 0) * TN) : -1;
             for (int i = 0; i < it.nt && live; ++i, ++t) {
                 const int t0 = tile_at(it, i) * TN, mine = next;
                 if (i + 1 < it.nt) next = page_of(it, tile_at(it, i + 1) * TN);
                 const uint32_t there = __ballot_sync(0xffffffffu, mine >= 0), miss = __ballot_sync(0xffffffffu, mine == -2);
-                const int s = t % slots, round = t / slots;
+                const int s = t % kSlots, round = t / kSlots;
                 if (round > 0) await(empty + s, (round - 1) & 1);
                 if (!live) break;
                 int pg[kPieces];
@@ -530,114 +541,141 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                 for (int j = 0; j < kPieces; ++j) pg[j] = __shfl_sync(0xffffffffu, mine, j);
                 if (lane == 0) {
                     fence_proxy_async_smem();  // the slot's generic accesses, before the copies
-                    if (h) miss_sm[s] = static_cast<int>(miss);
-                    uint8_t* dst = ring + s * G::tile;
-                    if (!there) mbar_arrive(full + s);
-                    else mbar_arrive_expect_tx(full + s, __popc(there) * piece_rows * D * 2);
+                    if constexpr (G::q8) {
+                        raw_sm[2 * h + s] = mine;
+                        if (mine < 0) {
+                            mbar_arrive(full + s);
+                        } else {
+                            mbar_arrive_expect_tx(full + s, kQ8Half);
+                            bulk_g2s(ring + s * kQ8Half, p.pool + (static_cast<int64_t>(mine) * p.kv_heads + it.g) * kQ8Rec + h * kQ8Half, kQ8Half,
+                                     full + s, policy);
+                        }
+                    } else {
+                        if (h) miss_sm[s] = static_cast<int>(miss);
+                        else kmiss_sm[t & 15] = static_cast<int>(miss);
+                        uint8_t* dst = ring + s * G::tile;
+                        if (!there) mbar_arrive(full + s);
+                        else mbar_arrive_expect_tx(full + s, __popc(there) * piece_rows * D * 2);
 #pragma unroll
-                    for (int j = 0; j < kPieces; ++j) {
-                        if (j * piece_rows >= TN || pg[j] < 0) continue;
-                        const int y = ((pg[j] * p.kv_heads + it.g) * 2 + h) * p.page_tokens + ((t0 + j * piece_rows) & (p.page_tokens - 1));
+                        for (int j = 0; j < kPieces; ++j) {
+                            if (j * piece_rows >= TN || pg[j] < 0) continue;
+                            const int y = ((pg[j] * p.kv_heads + it.g) * 2 + h) * p.page_tokens + ((t0 + j * piece_rows) & (p.page_tokens - 1));
 #pragma unroll
-                        for (int x = 0; x < D / 64; ++x)
-                            tma_load_hint(dst + x * TN * 128 + j * piece_rows * 128, &map, 64 * x, y, full + s, policy);
+                            for (int x = 0; x < D / 64; ++x)
+                                tma_load_hint(dst + x * TN * 128 + j * piece_rows * 128, &map, 64 * x, y, full + s, policy);
+                        }
                     }
                 }
                 __syncwarp();
             }
         }
-        if (!live && lane == 0 && !G::q8) {
+        if (!live && lane == 0) {
             // let every copy still in flight land before the block exits: the last of each slot
             volatile int go_on = 0;
-            for (int i = max(0, t - most); i < t; ++i)
-                if (i >= t - slots) mbar_wait_bounded(full + i % slots, (i / slots) & 1, &go_on, 100000000ull);
+            for (int i = max(0, t - kSlots); i < t; ++i) mbar_wait_bounded(full + i % kSlots, (i / kSlots) & 1, &go_on, 100000000ull);
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- products
         constexpr uint32_t kType = BF ? (1u << 7) | (1u << 10) : 0u;
         constexpr uint32_t kIdescS = idesc_f16_f32(128, TN) | kType;
         constexpr uint32_t kIdescO = idesc_f16_f32(128, D) | kType | (G::q8 ? 0u : 1u << 16);  // (16-bit pools: V by dims)
-        const uint32_t k0 = smem_u32(sm), v0 = smem_u32(sm + G::off_v), q0 = smem_u32(sm + G::off_q);
-        int t = 0;                 // tiles so far
-        int done[2] = {0, 0};      // products P V of each stream so far
-        int asked[2] = {0, 0};     // scores
-        int pend[2] = {-1, -1};    // the tile whose P V is still to come
-        bool first[2] = {true, true};  // .. and whether it is its item's first
-        // P V of stream s, and V's slot back if this is its last use
-        auto product_o = [&](int s, bool last) {
-            const int n = done[s], x = NS == 2 ? s : n & 1, vs = pend[s] % G::v_slots;
-            await(pfull + x, NS == 2 ? n & 1 : (n >> 1) & 1);
-            await(vready + vs, (pend[s] / G::v_slots) & 1);
-            if (!live) return;
-            tc_fence_after();
-            const uint32_t a = tmem + x * TN, o = tmem + G::col_o + s * D;
-            const uint32_t acc = !first[s] || accum_sm[s] != 0;
-            const uint32_t vb = v0 + vs * G::tile;
-            if (elect_one()) {
-#pragma unroll
-                for (int ks = 0; ks < TN / 16; ++ks) {
-                    const uint64_t b = G::q8 ? smem_desc_sw128(vb) + (((ks >> 2) * (D * 128) + (ks & 3) * 32) >> 4)
-                                             : desc_mn(vb, TN * 128) + ks * (2048 >> 4);
-                    tc_mma_f16_ts(o, a + 8 * ks, b, kIdescO, ks ? 1 : acc);
+        const uint64_t kd = smem_desc_sw128(smem_u32(sm)), qd = smem_desc_sw128(smem_u32(sm + G::off_q));
+        const uint64_t vd = G::q8 ? smem_desc_sw128(smem_u32(sm + G::off_v)) : desc_mn(smem_u32(sm + G::off_v), TN * 128);
+        // (one thread for all of it: a wait that is over already then costs some 30 clocks instead of 100, and tcgen05.commit
+        // speaks for the products of its thread)
+        if (elect_one()) {
+            auto wait = [&](uint64_t* b, uint32_t parity) {
+                if (live && !mbar_wait_bounded(b, parity, abort_flag)) {
+                    live = false;
+                    *abort_flag = 1;
                 }
+            };
+            int t = 0;                 // tiles so far
+            int done[2] = {0, 0};      // products P V of each stream so far
+            int asked[2] = {0, 0};     // scores
+            int pend[2] = {-1, -1};    // the tile whose P V is still to come
+            bool first[2] = {true, true};  // .. and whether it is its item's first
+            int both = 0;              // items of two tiles of queries so far
+            // P V of stream s, and V's slot back if this is its last use.  (P is there after its tile's V: the softmax
+            // or warp 3's arrival on vready goes before.)
+            auto product_o = [&](int s, bool last) {
+                const int n = done[s], x = 2 * s + (n & 1), vs = pend[s] % G::v_slots;
+                wait(pfull + x, (n >> 1) & 1);
+                wait(vready + vs, (pend[s] / G::v_slots) & 1);
+                if (!live) return;
+                tc_fence_after();
+                const uint32_t a = tmem + x * TN, o = tmem + G::col_o + s * D;
+                const uint32_t acc = !first[s] || accum_sm[s] != 0;
+                const uint64_t b0 = vd + (vs * G::tile >> 4);
+#pragma unroll
+                for (int part = 0; part < (G::q8 ? 2 : 1); ++part)
+#pragma unroll
+                    for (int ks = 0; ks < TN / 16; ++ks)
+                        tc_mma_f16_ts(o, a + 8 * ks, b0 + (G::q8 ? (part * G::part + ks * 32) >> 4 : ks * (2048 >> 4)), kIdescO, part + ks ? 1 : acc);
                 tc_commit(odone + s);
                 if (last) tc_commit(vempty + vs);
-            }
-            __syncwarp();
-            ++done[s];
-            pend[s] = -1;
-        };
-        auto product_s = [&](int s, int ksl, int qs, bool last) {
-            const int x = NS == 2 ? s : asked[s] & 1;
-            const uint64_t aq = smem_desc_sw128(q0 + qs * G::q_tile), bk = smem_desc_sw128(k0 + ksl * G::k_tile);
-            if (elect_one()) {
+                ++done[s];
+                pend[s] = -1;
+            };
+            auto product_s = [&](int s, int ksl, int qs, bool last) {
+                const int x = 2 * s + (asked[s] & 1);
+                const uint64_t aq = qd + (qs * G::q_tile >> 4), bk = kd + (ksl * G::tile >> 4);
 #pragma unroll
                 for (int part = 0; part < (G::q8 ? 2 : 1); ++part)
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks)
                         tc_mma_f16_ss(tmem + x * TN, aq + (((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4),
-                                      bk + ((part * G::tile + (ks >> 2) * (TN * 128) + (ks & 3) * 32) >> 4), kIdescS, part + ks > 0);
+                                      bk + ((part * G::part + (ks >> 2) * (TN * 128) + (ks & 3) * 32) >> 4), kIdescS, part + ks > 0);
                 tc_commit(sfull + x);
                 if (last) tc_commit(kempty + ksl);
-            }
-            __syncwarp();
-            ++asked[s];
-        };
-        for (int item = blockIdx.x; item < total && live; item += gridDim.x) {
-            const Record it = next_record();
-            const int n = k - 1;
-            await(qfull, n & 1);
-            if (NS == 2 && !p.decode) await(qfull + 1, n & 1);
-            bool begun[2] = {false, false};
-            for (int i = 0; i < it.nt && live; ++i, ++t) {
-                const int ksl = t % G::k_slots;
-                await(kfull + ksl, (t / G::k_slots) & 1);
-                tc_fence_after();
-                if constexpr (NS == 1) {
+                ++asked[s];
+            };
+            for (int item = blockIdx.x; item < total && live; item += gridDim.x, ++k) {
+                wait(ifull + (k & 1), (k >> 1) & 1);
+                if (!live) break;
+                const Record it = item_sm[k & 1];
+                mbar_arrive(iempty + (k & 1));
+                wait(qfull, k & 1);
+                const bool two = NS == 2 && !p.decode && it.nq - it.q0 > 128;
+                if (two) wait(qfull + 1, both++ & 1);
+                int begun[2] = {0, 0};  // the item's tiles by stream
+                for (int i = 0; i < it.nt && live; ++i, ++t) {
+                    const int ksl = t % G::k_slots;
+                    wait(kfull + ksl, (t / G::k_slots) & 1);
                     if (!live) break;
-                    product_s(0, ksl, 0, true);
-                    if (pend[0] >= 0) product_o(0, true);
-                    pend[0] = t, first[0] = !begun[0], begun[0] = true;
-                } else {
-                    const int from = p.decode ? tile_at(it, i) & 1 : 0, to = p.decode ? from : 1;
+                    tc_fence_after();
+                    // the streams that this tile is for: scores first, then the products of their tiles before
+                    const int from = NS == 2 && p.decode ? tile_at(it, i) & 1 : 0, to = two ? 1 : from;
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        if (s < from || s > to) continue;
-                        if (pend[s] >= 0) product_o(s, p.decode || s == 1);
-                        if (!live) break;
-                        product_s(s, ksl, p.decode ? 0 : s, s == to);
-                        pend[s] = t, first[s] = !begun[s], begun[s] = true;
-                    }
+                    for (int s = 0; s < NS; ++s)
+                        if (s >= from && s <= to) {
+                            // S goes over the P before last, whose product has to be over (products of different shapes need
+                            // not keep their order).  Those of earlier items are: their outputs were read before the queries came.
+                            if (begun[s]++ >= 2) wait(odone + s, asked[s] & 1);
+                            if (live) product_s(s, ksl, p.decode ? 0 : s, s == to);
+                        }
+#pragma unroll
+                    for (int s = 0; s < NS; ++s)
+                        if (live && s >= from && s <= to) {
+                            if (NS == 2 && p.decode && pend[1 - s] >= 0 && pend[1 - s] < pend[s]) product_o(1 - s, true);
+                            if (pend[s] >= 0 && live) product_o(s, s == to);
+                            pend[s] = t, first[s] = begun[s] == 1;
+                        }
+                }
+                // what is left, in the tiles' order (V's slots come free in it)
+                const bool swap = NS == 2 && p.decode && pend[1] >= 0 && pend[1] < pend[0];
+                if (swap && live) product_o(1, true);
+#pragma unroll
+                for (int s = 0; s < NS; ++s) {
+                    if (pend[s] >= 0 && live) product_o(s, p.decode || s == (two ? 1 : 0));
+                    if (begun[s] && live) tc_commit(ofin + s);
                 }
             }
-#pragma unroll
-            for (int s = 0; s < NS; ++s)
-                if (pend[s] >= 0 && live) product_o(s, NS == 1 || p.decode || s == 1);
+            // every product issued has finished before the tensor memory is released
+            tc_commit(drained);
+            volatile int go_on = 0;
+            mbar_wait_bounded(drained, 0, &go_on, 10000000000ull);
         }
-        // every product issued has finished before the tensor memory is released
-        if (elect_one()) tc_commit(drained);
-        volatile int go_on = 0;
-        mbar_wait_bounded(drained, 0, &go_on, 10000000000ull);
         __syncwarp();
     } else if (warp == 3 && !G::q8) {
         // ---------------------------------------------------------------- V's rows that must not count
@@ -654,8 +692,8 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                 if (miss || edge(it, t0)) {
                     uint8_t* vt = sm + G::off_v + vs * G::tile;
 #pragma unroll 1
-                    for (int j = 0; j < TN / 32; ++j) {
-                        const int row = lane + 32 * j, tok = t0 + row;
+                    for (int j = 0; j < 2; ++j) {
+                        const int row = 2 * lane + j, tok = t0 + row;
                         bool zero = gone(it, tok) || ((miss >> (row >> piece_shift)) & 1), odd = false;
                         if (!zero && !(tok < it.minlen && (tok >= it.maxlo || tok < p.sinks))) {
                             constexpr uint32_t ex = BF ? 0x7F80u : 0x7C00u;
@@ -676,43 +714,58 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                                     *reinterpret_cast<uint4*>(vt + x * TN * 128 + row * 128 + 16 * ((c + lane) & 7)) = make_uint4(0, 0, 0, 0);
                         }
                         const uint32_t word = __ballot_sync(0xffffffffu, odd);
-                        if (lane == 0) odd_sm[vs * 4 + j] = word;
+                        if (lane == 0) odd_sm[t % G::info_slots * 2 + j] = word;
                     }
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(vready + vs);
+                if (lane == 0) {
+                    mbar_arrive(vready + vs);
+                    mbar_arrive(vinfo + t % G::info_slots);
+                }
             }
         }
     }
     } else if (warp < 4 + G::soft_warps) {
-        if constexpr (NS == 2) setmaxnreg_inc<G::q8 ? 104 : 200>();
+        if constexpr (NS == 2) setmaxnreg_inc<G::q8 ? 120 : 200>();
         // ---------------------------------------------------------------- softmax: a query per thread
         const int s = (warp - 4) >> 2, me = tid & 127;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
         const uint32_t ocol = lanes + G::col_o + s * D;
         int tiles = 0;  // all tiles so far
         int n = 0;      // the stream's
-        int merges = 0;
+        int merges = 0, fins = 0;
         for (int item = blockIdx.x; item < total && live; item += gridDim.x) {
             const Record it = next_record();
             if (!live) break;
-            const int q = it.q0 + (NS == 2 && !p.decode ? 128 * s : 0) + me;
+            const int tiles0 = tiles;
+            tiles += it.nt;
+            const int c0 = it.q0 + (NS == 2 && !p.decode ? 128 * s : 0), q = c0 + me;
+            if (NS == 2 && !p.decode && s == 1 && c0 >= it.nq) continue;  // (the item has one tile of queries)
             const bool valid = q < it.nq;
+            const bool idle = c0 + 32 * (warp & 3) >= it.nq;  // no query of the warp's
             const int r = it.r0 + (valid ? q / p.group : 0), h = it.g * p.group + (valid ? q % p.group : 0);
             const int len = valid ? length_of(p, r) : 0, from = max(0, len - p.window), first = min(p.sinks, len);
-            if (s == 0 || !p.decode) {  // the query, swizzled as the copies do
-                const uint4* src = reinterpret_cast<const uint4*>(p.q + r * p.q_stride + static_cast<int64_t>(h) * D);
-                uint8_t* dst = sm + G::off_q + s * G::q_tile + me * 128;
+            const int64_t at = static_cast<int64_t>(r) * p.heads + h;  // (row, head)
+            if (s == 0 || !p.decode) {  // the queries, swizzled as the copies do: D / 8 lanes a row
+                constexpr int L = D / 8 < 32 ? D / 8 : 32, R = 32 / L;  // lanes of a row, rows at once
+                const int c = lane % L;
+                uint8_t* dst = sm + G::off_q + s * G::q_tile + (c >> 3) * (128 * 128);
+                const int64_t src = r * p.q_stride + static_cast<int64_t>(h) * D;
 #pragma unroll
-                for (int c0 = 0; c0 < D / 8; c0 += 8) {
+                for (int i0 = 0; i0 < 32; i0 += 8 * R) {
                     uint4 v[8];
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) v[c] = valid ? src[c0 + c] : make_uint4(0, 0, 0, 0);
+                    for (int j = 0; j < 8; ++j) {
+                        const int i = i0 + j * R + lane / L;
+                        const int64_t o = __shfl_sync(0xffffffffu, src, i);
+                        v[j] = c0 + 32 * (warp & 3) + i < it.nq ? *reinterpret_cast<const uint4*>(p.q + o + 8 * c) : make_uint4(0, 0, 0, 0);
+                    }
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        v[c].x ^= p.flip, v[c].y ^= p.flip, v[c].z ^= p.flip, v[c].w ^= p.flip;
-                        *reinterpret_cast<uint4*>(dst + (c0 >> 3) * (128 * 128) + ((c ^ (me & 7)) << 4)) = v[c];
+                    for (int j = 0; j < 8; ++j) {
+                        const int row = 32 * (warp & 3) + i0 + j * R + lane / L;
+                        v[j].x ^= p.flip, v[j].y ^= p.flip, v[j].z ^= p.flip, v[j].w ^= p.flip;
+                        *reinterpret_cast<uint4*>(dst + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v[j];
                     }
                 }
                 fence_proxy_async_smem();
@@ -722,50 +775,51 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
             float l = 0.f, lim = -INFINITY, base = 0.f;  // sum, reference and slack, what comes off the scores
             bool fresh = true;                           // O holds nothing yet
             for (int i = 0; i < it.nt; ++i) {
-                const int tile = tile_at(it, i), t0 = tile * TN, tv = tiles + i, vs = tv % G::v_slots;
+                const int tile = tile_at(it, i), t0 = tile * TN, tv = tiles0 + i;
                 if (NS == 2 && p.decode && (tile & 1) != s) continue;
-                const int x = NS == 2 ? s : n & 1;
+                const int x = 2 * s + (n & 1);
                 const uint32_t scol = lanes + x * TN;
-                await(sfull + x, NS == 2 ? n & 1 : (n >> 1) & 1);
-                await(vready + vs, (tv / G::v_slots) & 1);
+                await(sfull + x, (n >> 1) & 1);
                 if (!live) break;
+                if (idle) {  // (its rows of P hold anything: nobody reads what comes of them)
+                    fresh = false;
+                    ++n;
+                    if (lane == 0) mbar_arrive(pfull + x);
+                    continue;
+                }
                 tc_fence_after();
-                const int miss = miss_sm[vs];
                 const bool some = edge(it, t0);
-                // Scores: all of them in registers, or (q8_0, whose converting warps need registers) 32 at a time, read twice.
-                constexpr int kHeld = G::q8 ? 32 : TN;
-                float v[kHeld];
-                auto masked = [&](int c, float* u) {
-                    if (some || miss) {
-                        const int jl = len - t0 - c, jf = from - t0 - c, js = first - t0 - c;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (!(j < jl && (j >= jf || j < js))) u[j] = -INFINITY;
-                        if (miss) {  // (a piece is 16 tokens at least)
-                            const bool lost[2] = {((miss >> (c >> piece_shift)) & 1) != 0, ((miss >> ((c + 16) >> piece_shift)) & 1) != 0};
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (lost[j >> 4]) u[j] = -INFINITY;
-                        }
-                    }
-                };
-                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                if constexpr (!G::q8) {
-#pragma unroll
-                    for (int c = 0; c < TN; c += 32) tmem_ld32(scol + c, v + c);
-                    tc_wait_ld();
+                const int vi = tv % G::info_slots;
+                if (some) {  // which tokens' V is not finite (four tiles before, that barrier's last phase is over for sure)
+                    await(vinfo + vi, (tv / G::info_slots) & 1);
+                    if (!live) break;
                 }
+                float v[TN];
+                tmem_ld32(scol, v);
+                tmem_ld32(scol + 32, v + 32);
+                const int miss = kmiss_sm[tv & 15];
+                tc_wait_ld();
+                if (some || miss) {
+                    const int jl = len - t0, jf = from - t0, js = first - t0;
 #pragma unroll
-                for (int c = 0; c < TN; c += 32) {
-                    float* u = G::q8 ? v : v + c;
-                    if constexpr (G::q8) {
-                        tmem_ld32(scol + c, u);
-                        tc_wait_ld();
+                    for (int j = 0; j < TN; ++j)
+                        if (!(j < jl && (j >= jf || j < js))) v[j] = -INFINITY;
+                    if (miss) {  // (a piece is 16 tokens at least)
+#pragma unroll
+                        for (int c = 0; c < TN; c += 16)
+                            if ((miss >> (c >> piece_shift)) & 1) {
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) v[c + j] = -INFINITY;
+                            }
                     }
-                    masked(c, u);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], u[j]);
                 }
+                float m4[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) m4[j] = fmaxf(v[j], v[j + 4]);
+#pragma unroll
+                for (int j = 8; j < TN; j += 8)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) m4[i] = fmaxf(m4[i], fmaxf(v[j + i], v[j + i + 4]));
                 const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.c2;  // (a NaN is no maximum)
                 const bool passed = m > lim;
                 if (__any_sync(0xffffffffu, passed)) {
@@ -779,7 +833,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                         l *= alpha;
                     }
                     if (!fresh) {
-                        if (NS == 1) await(odone, (n - 1) & 1);  // (two streams: the scores came after the last product)
+                        await(odone + s, (n - 1) & 1);  // (the one before that was over before these scores were asked for)
                         if (!live) break;
                         tc_fence_after();
 #pragma unroll 1
@@ -793,35 +847,33 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                         }
                     }
                 }
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                uint64_t sum[2] = {0, 0};  // pairs of fp32
+                const uint64_t c2 = pair(p.c2, p.c2), off = pair(-base, -base);
 #pragma unroll
                 for (int c = 0; c < TN; c += 32) {
-                    float* u = G::q8 ? v : v + c;
-                    if constexpr (G::q8) {
-                        tmem_ld32(scol + c, u);
-                        tc_wait_ld();
-                        masked(c, u);
-                    }
                     uint32_t w[16];
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
-                        const float a = ex2(fmaf(u[j], p.c2, -base)), b = ex2(fmaf(u[j + 1], p.c2, -base));
-                        sum[(j & 2)] += a;
-                        sum[(j & 2) + 1] += b;
+                        float a, b;
+                        unpair(fma2(pair(v[c + j], v[c + j + 1]), c2, off), a, b);
+                        a = ex2(a), b = ex2(b);
+                        sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], pair(a, b));
                         w[j / 2] = pack2<BF>(a, b);
                     }
                     tmem_st16(scol + c / 2, w);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                float s0, s1;
+                unpair(add2(sum[0], sum[1]), s0, s1);
+                l += s0 + s1;
                 tc_wait_st();
                 // ---- tokens whose V is not finite, to those that see them
                 uint32_t odd = 0;
-                if (some) odd = odd_sm[vs * 4] | odd_sm[vs * 4 + 1] | (TN > 64 ? odd_sm[vs * 4 + 2] | odd_sm[vs * 4 + 3] : 0u);
+                if (some) odd = odd_sm[vi * 2] | odd_sm[vi * 2 + 1];
                 if (odd) {
-                    if (!fresh && NS == 1) await(odone, (n - 1) & 1);
+                    if (!fresh) await(odone + s, (n - 1) & 1);
                     if (!live) break;
                     tc_fence_after();
-                    add_odd<FMT, D>(p, it.a, it.g, t0, const_cast<const uint32_t*>(odd_sm) + vs * 4, ocol, scol, len, from, first, fresh);
+                    add_odd<FMT, D>(p, it.a, it.g, t0, const_cast<const uint32_t*>(odd_sm) + vi * 2, ocol, scol, len, from, first, fresh);
                 }
                 if (fresh && me == 0) accum_sm[s] = odd != 0;
                 fresh = false;
@@ -830,29 +882,29 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(pfull + x);
             }
-            tiles += it.nt;
             if (!live) break;
-            if (!fresh) await(odone + s, (n - 1) & 1);
+            // (the item's last product; odone may be two phases behind here)
+            if (!fresh) await(ofin + s, fins++ & 1);
             if (!live) break;
             tc_fence_after();
 
             // ---- what became of the item
             float w0 = 1.f, w1 = 0.f;  // the streams' weights
-            const float* stage = reinterpret_cast<const float*>(sm + G::off_q + (warp & 3) * 4096) + lane;  // column c: 16 KB * (c / 32) + 128 * (c % 32)
+            // the second stream's outputs, over the queries: column c at 16 KB * (c / 32) + 128 * (c % 32), by warp
+            float* stage = reinterpret_cast<float*>(sm + G::off_q + (warp & 3) * 4096) + lane;
             if (NS == 2 && p.decode) {
                 if (s == 1) {
-                    await(mfree, merges & 1);  // (the queries, over which the outputs go, are read)
+                    await(mfree, merges & 1);  // (the queries are read)
                     if (!live) break;
                     ml_sm[me] = make_float2(base, l);
-                    if (!fresh) {
-                        float* to = const_cast<float*>(stage);
+                    if (!fresh && !idle) {
 #pragma unroll 1
                         for (int c = 0; c < D; c += 32) {
                             float o[32];
                             tmem_ld32(ocol + c, o);
                             tc_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) to[(c >> 5) * 4096 + j * 32] = o[j];
+                            for (int j = 0; j < 32; ++j) stage[(c >> 5) * 4096 + j * 32] = o[j];
                         }
                         tc_fence_before();
                     }
@@ -873,6 +925,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                 l = l * w0 + other.y * w1;
                 base = top;
             }
+            if (idle) continue;
             int slot = 0;
             bool write = valid;
             if (p.chunk && valid) {
@@ -880,67 +933,96 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                 slot = it.chunk < c.first ? it.chunk : c.first + it.chunk - c.from;
                 write = it.chunk < c.first || (it.chunk >= c.from && it.chunk < c.end);
             }
-            const int64_t at = static_cast<int64_t>(r) * p.heads + h;
-            const float inv = p.chunk ? 1.f : l == 0.f ? 0.f : 1.f / l;
-            const bool none = l == 0.f;
+            const bool none = l == 0.f, merge = NS == 2 && p.decode;
+            const float inv = none ? 0.f : p.chunk ? w0 : w0 / l, inv1 = none ? 0.f : p.chunk ? w1 : w1 / l;
+            if (write) {
+                if (p.chunk) *reinterpret_cast<float2*>(p.ml + (at * p.slots + slot) * 2) = make_float2(base, l);
+                else if (p.lse) p.lse[at] = none ? -INFINITY : (base + log2f(l)) * 0.6931471805599453f;
+            }
+            // 32 dims at a time through shared memory, so that lanes side by side write a row's bytes: its 16-byte pieces
+            // go where pieces of the rows around it are in other banks
+            const bool wide32 = p.chunk || p.out_type == QMM_TYPE_F32;
+            uint8_t* turn = sm + G::off_q + (merge ? 0 : s * G::q_tile) + (warp & 3) * 4096;
+            const int64_t dst = write ? (p.chunk ? at * p.slots + slot : at) * D : -1;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 float o[32];
                 if (!fresh) tmem_ld32(ocol + c, o);
                 tc_wait_ld();
-                if (NS == 2 && p.decode) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] = (w0 == 0.f ? 0.f : o[j] * w0) + (w1 == 0.f ? 0.f : stage[(c >> 5) * 4096 + j * 32] * w1);
+                for (int j = 0; j < 32; ++j) {
+                    o[j] = inv == 0.f ? 0.f : o[j] * inv;
+                    if (merge) o[j] += inv1 == 0.f ? 0.f : stage[(c >> 5) * 4096 + j * 32] * inv1;
                 }
-                if (write) {
-                    if (p.chunk) {
-                        float* to = p.o + (at * p.slots + slot) * D + c;
+                __syncwarp();  // (the last piece's rows, and the other stream's outputs here, are read)
+                if (wide32) {
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4)
-                            *reinterpret_cast<float4*>(to + j) = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-                    } else {
+                    for (int j = 0; j < 8; ++j)
+                        *reinterpret_cast<float4*>(turn + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                } else {
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8) store_out(p, at * D + c + j, o + j, [&](float y) { return none ? 0.f : y * inv; });
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            w[i] = p.out_type == QMM_TYPE_F16 ? pack2<false>(o[8 * j + 2 * i], o[8 * j + 2 * i + 1]) : pack2<true>(o[8 * j + 2 * i], o[8 * j + 2 * i + 1]);
+                        *reinterpret_cast<uint4*>(turn + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
-            }
-            if (write) {
-                if (p.chunk) *reinterpret_cast<float2*>(p.ml + (at * p.slots + slot) * 2) = make_float2(base, l);
-                else if (p.lse) p.lse[at] = none ? -INFINITY : (base + log2f(l)) * 0.6931471805599453f;
+                __syncwarp();
+                const int L = wide32 ? 8 : 4;  // lanes of a row
+                const int piece = lane % L;
+#pragma unroll 4
+                for (int i0 = 0; i0 < 32; i0 += 32 / L) {
+                    const int row = i0 + lane / L;
+                    const int64_t to = __shfl_sync(0xffffffffu, dst, row);
+                    const uint4 w = *reinterpret_cast<const uint4*>(turn + row * 128 + ((piece ^ (row & 7)) << 4));
+                    if (to >= 0) {
+                        if (p.chunk) *reinterpret_cast<uint4*>(p.o + to + c + 4 * piece) = w;
+                        else if (wide32) *reinterpret_cast<uint4*>(static_cast<float*>(p.out) + to + c + 4 * piece) = w;
+                        else *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + to + c + 8 * piece) = w;
+                    }
+                }
             }
             tc_fence_before();
             __syncwarp();
         }
         if (!live && lane == 0) atomicOr(p.err, kErrTimeout);
     } else if constexpr (G::q8) {
-        setmaxnreg_dec<88>();
+        setmaxnreg_dec<80>();
+        // A tile is a page.
+        const int me = tid & 127;
+        int t = 0;
         if (warp < 8 + G::soft_warps) {
-            // ---------------------------------------------------------------- K to fp16: a token per thread
-            const int me = tid & 127, slot = me & 63, key = q8_key(slot & 7);
-            int t = 0;
+            // ---------------------------------------------------------------- K to fp16: half a token's dims per thread
+            const int slot = me & 63, half = me >> 6, key = q8_key(slot & 7);
             for (int item = blockIdx.x; item < total && live; item += gridDim.x) {
                 const Record it = next_record();
                 for (int i = 0; i < it.nt && live; ++i, ++t) {
-                    const int t0 = tile_at(it, i) * TN, ks = t % G::k_slots;
-                    const int pg = __shfl_sync(0xffffffffu, page_of(it, t0), me >> 6);
-                    uint4 row[8];
-                    uint2 sc = make_uint2(0, 0);
+                    const int ks = t % G::k_slots, rs = t % G::raw_slots;
+                    await(rfull + rs, (t / G::raw_slots) & 1);
+                    if (!live) break;
+                    const int pg = raw_sm[rs];
+                    uint4 row[4];
+                    uint32_t sc = 0;
                     if (pg >= 0) {
-                        const uint8_t* b = p.pool + (static_cast<int64_t>(pg) * p.kv_heads + it.g) * kQ8Rec;
+                        const uint8_t* b = sm + G::off_raw + rs * kQ8Half;
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) row[c] = *reinterpret_cast<const uint4*>(b + slot * 128 + 16 * (c ^ key));
-                        sc = *reinterpret_cast<const uint2*>(b + 8192 + slot * 8);
+                        for (int c = 0; c < 4; ++c) row[c] = *reinterpret_cast<const uint4*>(b + slot * 128 + 16 * ((4 * half + c) ^ key));
+                        sc = *reinterpret_cast<const uint32_t*>(b + 8192 + slot * 8 + 4 * half);
                     }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(rempty + rs);
                     if (t >= G::k_slots) await(kempty + ks, (t / G::k_slots - 1) & 1);
                     if (!live) break;
+                    if (me == 0) kmiss_sm[t & 15] = pg == -2;
                     if (pg >= 0) {
-                        uint8_t* dst = sm + ks * G::k_tile + me * 128;
+                        uint8_t* dst = sm + ks * G::tile + half * (TN * 128) + slot * 128;
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) {  // eight dims: one 16-byte piece of each part
+                        for (int c = 0; c < 8; ++c) {  // eight dims: one 16-byte piece of each part
                             const uint32_t u0 = ((c & 1) ? row[c >> 1].z : row[c >> 1].x) ^ 0x80808080u;
                             const uint32_t u1 = ((c & 1) ? row[c >> 1].w : row[c >> 1].y) ^ 0x80808080u;
-                            const uint32_t w = (c >> 3) ? sc.y : sc.x;  // scales of dims 0 .. 63 or 64 .. 127, 32 each
-                            const __half2 d = __half2half2((c >> 2) & 1 ? __high2half(as_h2(w)) : __low2half(as_h2(w)));
+                            const __half2 d = __half2half2(c >> 2 ? __high2half(as_h2(sc)) : __low2half(as_h2(sc)));
                             const __half2 z[4] = {i8_to_h2(u0, 0x4140u), i8_to_h2(u0, 0x4342u), i8_to_h2(u1, 0x4140u), i8_to_h2(u1, 0x4342u)};
                             uint32_t hi[4], lo[4];
 #pragma unroll
@@ -949,9 +1031,9 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                                 hi[j] = as_u32(x);
                                 lo[j] = as_u32(__hfma2(z[j], d, __hneg2(x)));
                             }
-                            const int at = (c >> 3) * (TN * 128) + (((c & 7) ^ (me & 7)) << 4);
+                            const int at = (c ^ (slot & 7)) << 4;
                             *reinterpret_cast<uint4*>(dst + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                            *reinterpret_cast<uint4*>(dst + G::tile + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                            *reinterpret_cast<uint4*>(dst + G::part + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                         }
                     }
                     fence_proxy_async_smem();
@@ -961,71 +1043,72 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
             }
         } else {
             // ---------------------------------------------------------------- V to fp16: a dim per thread
-            const int me = tid & 127, w4 = warp & 3;
-            int t = 0, z = 0;
+            // (the order in which a thread takes its four pieces of 16 tokens, c ^ x by lane, keeps both the reads, 64
+            // bytes apart, and the swizzled writes free of bank conflicts)
+            const int w4 = warp & 3, turn = (0x78 >> (2 * ((lane >> 1) & 3))) & 3;  // 0, 2, 3, 1
+            uint8_t* dv = sm + G::off_dv + w4 * 128;
             for (int item = blockIdx.x; item < total && live; item += gridDim.x) {
                 const Record it = next_record();
                 for (int i = 0; i < it.nt && live; ++i, ++t) {
-                    const int t0 = tile_at(it, i) * TN, vs = t % G::v_slots;
-                    const int pages = page_of(it, t0);
-                    const int pg[2] = {__shfl_sync(0xffffffffu, pages, 0), __shfl_sync(0xffffffffu, pages, 1)};
-                    uint4 row[8];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        row[c] = make_uint4(0, 0, 0, 0);
-                        const int x = pg[c >> 2];
-                        if (x >= 0)
-                            row[c] = *reinterpret_cast<const uint4*>(p.pool + (static_cast<int64_t>(x) * p.kv_heads + it.g) * kQ8Rec + kQ8Half + me * 64 + 16 * (c & 3));
-                    }
+                    const int t0 = tile_at(it, i) * TN, vs = t % G::v_slots, rs = t % G::raw_slots;
+                    await(rfull + G::raw_slots + rs, (t / G::raw_slots) & 1);
                     if (t >= G::v_slots) await(vempty + vs, (t / G::v_slots - 1) & 1);
                     if (!live) break;
-                    const int miss = (pg[0] == -2 ? 1 : 0) | (pg[1] == -2 ? 2 : 0);
-                    const bool some = miss || edge(it, t0);
-                    uint32_t zero[4] = {0, 0, 0, 0};
-                    if (some) {  // (by token, as warp 3 does for 16-bit pools; what is not finite is a scale, or too large for fp16)
-                        const int tok = t0 + me, x = pg[me >> 6];
-                        bool none = gone(it, tok) || x < 0, odd = false;
-                        if (!none && !(tok < it.minlen && (tok >= it.maxlo || tok < p.sinks))) {
-                            const uint8_t* b = p.pool + (static_cast<int64_t>(x) * p.kv_heads + it.g) * kQ8Rec + kQ8Half + 8192;
+                    const int pg = raw_sm[2 + rs];
+                    const uint8_t* b = sm + G::off_raw + (G::raw_slots + rs) * kQ8Half;
+                    const uint8_t* scales = b + 8192 + w4 * 128;
+                    if (pg < 0 || edge(it, t0)) {
+                        // Scales of 0 for tokens that must not count, as warp 3 zeroes rows of 16-bit pools (what is not finite
+                        // is a scale, or too large for fp16).  A warp's dims are one block of scales.
+                        uint32_t mine = 0;
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                odd |= (*reinterpret_cast<const uint16_t*>(b + (j * 64 + (me & 63)) * 2) & 0x7FFFu) >= (24u << 10);  // 512
+                        for (int j = 0; j < 2; ++j) {
+                            const int tok = t0 + 2 * lane + j;
+                            const bool none = pg < 0 || gone(it, tok);
+                            bool odd = false;
+                            if (!none && !(tok < it.minlen && (tok >= it.maxlo || tok < p.sinks))) {
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) odd |= (*reinterpret_cast<const uint16_t*>(b + 8192 + c * 128 + 4 * lane + 2 * j) & 0x7FFFu) >= (24u << 10);  // 512
+                            }
+                            const uint32_t who = __ballot_sync(0xffffffffu, odd);
+                            if (w4 == 0 && lane == 0) odd_sm[t % G::info_slots * 2 + j] = who;
+                            if (!none && !odd) mine |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(scales + 4 * lane + 2 * j)) << (16 * j);
                         }
-                        const uint32_t who = __ballot_sync(0xffffffffu, odd), all = __ballot_sync(0xffffffffu, none || odd);
-                        if (lane == 0) odd_sm[vs * 4 + w4] = who, zero_sm[(z & 1) * 4 + w4] = all;
+                        *reinterpret_cast<uint32_t*>(dv + 4 * lane) = mine;
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(zdone);
-                        await(zdone, z & 1);
-                        if (!live) break;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) zero[j] = zero_sm[(z & 1) * 4 + j];
-                        ++z;
+                        scales = dv;
                     }
-                    if (me == 0) miss_sm[vs] = miss;
                     uint8_t* dst = sm + G::off_v + vs * G::tile + me * 128;
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {  // eight tokens
-                        const int x = pg[c >> 3];
-                        uint4 sc = make_uint4(0, 0, 0, 0);
-                        if (x >= 0)
-                            sc = *reinterpret_cast<const uint4*>(p.pool + (static_cast<int64_t>(x) * p.kv_heads + it.g) * kQ8Rec + kQ8Half + 8192 + w4 * 128 + 16 * (c & 7));
-                        const uint32_t off = (zero[c >> 2] >> (8 * (c & 3))) & 0xFFu;
-                        uint32_t d[4] = {sc.x, sc.y, sc.z, sc.w};
-                        if (off) {
+                    for (int c = 0; c < 4; ++c) {
+                        const int cc = c ^ turn;  // 16 tokens
+                        uint4 u = make_uint4(0, 0, 0, 0);
+                        if (pg >= 0) u = *reinterpret_cast<const uint4*>(b + me * 64 + 16 * cc);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) d[j] &= ((off >> (2 * j)) & 1 ? 0u : 0xFFFFu) | ((off >> (2 * j + 1)) & 1 ? 0u : 0xFFFF0000u);
+                        for (int j = 0; j < 2; ++j) {  // eight of them: a 16-byte piece of each part
+                            const uint4 d = *reinterpret_cast<const uint4*>(scales + 32 * cc + 16 * j);
+                            const uint32_t u0 = (j ? u.z : u.x) ^ 0x80808080u, u1 = (j ? u.w : u.y) ^ 0x80808080u;
+                            const __half2 z[4] = {i8_to_h2(u0, 0x4140u), i8_to_h2(u0, 0x4342u), i8_to_h2(u1, 0x4140u), i8_to_h2(u1, 0x4342u)};
+                            const __half2 e[4] = {as_h2(d.x), as_h2(d.y), as_h2(d.z), as_h2(d.w)};
+                            uint32_t hi[4], lo[4];
+#pragma unroll
+                            for (int n = 0; n < 4; ++n) {
+                                const __half2 x = __hmul2(z[n], e[n]);
+                                hi[n] = as_u32(x);
+                                lo[n] = as_u32(__hfma2(z[n], e[n], __hneg2(x)));
+                            }
+                            const int at = ((2 * cc + j) ^ (me & 7)) << 4;
+                            *reinterpret_cast<uint4*>(dst + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                            *reinterpret_cast<uint4*>(dst + G::part + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                         }
-                        const uint32_t u0 = ((c & 1) ? row[c >> 1].z : row[c >> 1].x) ^ 0x80808080u;
-                        const uint32_t u1 = ((c & 1) ? row[c >> 1].w : row[c >> 1].y) ^ 0x80808080u;
-                        const __half2 zz[4] = {i8_to_h2(u0, 0x4140u), i8_to_h2(u0, 0x4342u), i8_to_h2(u1, 0x4140u), i8_to_h2(u1, 0x4342u)};
-                        uint32_t o[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) o[j] = as_u32(__hmul2(zz[j], as_h2(d[j])));
-                        *reinterpret_cast<uint4*>(dst + (c >> 3) * (D * 128) + (((c & 7) ^ (me & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(vready + vs);
+                    if (lane == 0) {
+                        mbar_arrive(vready + vs);
+                        mbar_arrive(vinfo + t % G::info_slots);
+                        mbar_arrive(rempty + G::raw_slots + rs);
+                    }
                 }
             }
         }
