@@ -13,8 +13,10 @@
 //   decode steps: one tile of queries, whose tokens' tiles are dealt to two streams by their parity; the streams
 //     meet at the end through shared memory.
 // Either way two streams take turns on the tensor cores (one at head dimension 256, for which tensor memory has no more
-// room).  Tiles have 64 tokens, so that each stream's scores have two buffers: those of the next tile are there when
-// the softmax is done with one, which never waits for a product that waits for it.
+// room): one's products run while the other's scores become probabilities.  The softmax takes 64 tokens at a time.  16-bit
+// pools at head dimensions 64 and 128 have tiles of two such halves, formed by one product of 128 columns (one of 64 takes
+// as long: it reads as much of Q), and the first half's P V runs under the second's softmax.  Otherwise a tile is
+// one half, and scores have two buffers: the next tile's are there when the softmax is done with one.
 // The tiles of an item are those that some of its rows sees: the first ones (sinks), and the window's.  Where few
 // items would leave SMs idle, tokens are cut into chunks at fixed places of a sequence, an item each, whose unnormalised
 // outputs a second kernel joins.  All choices are made by the plan's dims, so a row's bits do not depend on its company.
@@ -23,8 +25,8 @@
 //   warp 2      asks for V tiles
 //   warp 3      16-bit pools: zeroes the rows of V that must not count, where some are
 //   warps 4 ..  softmax, four a stream
-//   q8_0: four more convert K (half a token a thread), four V (a dim a thread), both to two fp16 parts whose sum is
-//               quant times scale
+//   q8_0: four more convert K (half a token a thread) and V (a dim a thread) to two fp16 parts whose sum is quant
+//               times scale
 // A query's reference is its first tile's maximum and moves only when a score passes it by more than 2^kSlack; each
 // query decides for itself.
 #pragma once
@@ -41,6 +43,7 @@ using namespace qmm::kv;
 
 constexpr float kShift = 9.f;       // p's power of two ..
 constexpr float kSlack = 6.f;       // .. and how far a score may pass its reference: p <= 2^15
+constexpr int kHalf = 64;          // tokens that the softmax takes at a time
 constexpr float kFine = 4194304.f;  // 2^22: a larger reference stands alone (fp32's spacing would swallow the two): p <= 1
 
 struct Params {
@@ -74,16 +77,17 @@ template <int FMT, int D>
 struct Geo {
     static constexpr bool q8 = FMT == QMM_KV_Q8_0;
     static constexpr int streams = D == 256 ? 1 : 2;
-    static constexpr int TN = 64;                                // tokens of a tile
+    static constexpr bool halves = !q8 && D <= 128;              // tiles of two halves, one buffer of scores per stream
+    static constexpr int TN = halves ? 2 * kHalf : kHalf;        // tokens of a tile
     static constexpr int part = TN * D * 2;                      // bytes of a tile's K or V in 16 bits
     static constexpr int tile = q8 ? 2 * part : part;            // q8_0: high and low parts
-    static constexpr int k_slots = D == 64 ? 8 : D == 128 && !q8 ? 4 : 2, v_slots = q8 ? 1 : k_slots;
+    static constexpr int k_slots = D == 64 ? 4 : 2, v_slots = q8 ? 1 : k_slots;
     static constexpr int info_slots = v_slots < 4 ? 4 : v_slots;  // V tiles of which the softmax is told (see there)
     static constexpr int raw_slots = q8 ? 2 : 0;                 // pages on their way, K and V
     static constexpr int q_tile = 128 * D * 2;
-    static constexpr int soft_warps = 4 * streams, conv_warps = q8 ? 8 : 0;
+    static constexpr int soft_warps = 4 * streams, conv_warps = q8 ? 4 : 0;
     static constexpr int threads = 32 * (4 + soft_warps + conv_warps);
-    // tensor memory: S (two buffers per stream), P over it, and O
+    // tensor memory: S (128 columns per stream, two halves or two buffers), P over it, and O
     static constexpr int col_o = 256;
     // shared memory, after aligning to 1024
     static constexpr int off_v = k_slots * tile;
@@ -94,9 +98,9 @@ struct Geo {
     static constexpr int off_dv = off_item + 2 * 64;             // q8_0: V's scales, zero where a token must not count: [4][64] fp16
     static constexpr int off_bar = off_dv + (q8 ? 512 : 0);
     static constexpr int bars = 2 * k_slots + 3 * v_slots + info_slots + 4 * raw_slots + 2 + 4 + 4 + 2 + 2 + 2 + 2 + 3;
-    // tmp[33], abort, tmem, accumulate[2], miss[8] (of V tiles), odd[8][2], miss[16] (of all tiles), raw[2][2]
+    // tmp[33], abort, tmem, accumulate[2], miss[4] (of V tiles), odd[4][4], miss[16] (of all tiles), raw[2][2]
     static constexpr int off_misc = (off_bar + bars * 8 + 15) / 16 * 16;
-    static constexpr int off_seq = (off_misc + 84 * 4 + 15) / 16 * 16;
+    static constexpr int off_seq = (off_misc + 80 * 4 + 15) / 16 * 16;
     static constexpr int smem(int agents) { return 1024 + off_seq + (agents + 1) * 16; }
 };
 
@@ -376,7 +380,7 @@ __device__ __noinline__ void add_odd(const Params& p, int a, int g, int t0, cons
         for (int j = 0; j < 8; ++j) o[j] = fresh ? 0u : tmem_ld1(ocol + c + j);
         tc_wait_ld();
 #pragma unroll 1
-        for (int j = 0; j < Geo<FMT, D>::TN; ++j) {
+        for (int j = 0; j < kHalf; ++j) {
             if (!((odd[j & 1] >> (j >> 1)) & 1)) continue;
             const uint32_t both = tmem_ld1(pcol + j / 2);
             tc_wait_ld();
@@ -424,10 +428,10 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
     volatile int* abort_flag = tmp + 33;
     uint32_t* tmem_sm = reinterpret_cast<uint32_t*>(tmp + 34);
     volatile int* accum_sm = tmp + 35;                                          // [2] O holds something before the first product
-    volatile int* miss_sm = tmp + 37;                                           // [8] a tile's pieces that are outside the pool
-    volatile uint32_t* odd_sm = reinterpret_cast<uint32_t*>(tmp + 45);          // [8][2] tokens that are taken query by query: even ones, odd ones
-    volatile int* kmiss_sm = tmp + 61;                                          // [16] the same of the last 16 tiles (more than are under way)
-    volatile int* raw_sm = tmp + 77;                                            // q8_0, [2][2]: a page's number, -1 not needed, -2 outside the pool
+    volatile int* miss_sm = tmp + 37;                                           // [4] a V tile's pieces that are outside the pool
+    volatile uint32_t* odd_sm = reinterpret_cast<uint32_t*>(tmp + 41);          // [4][4] tokens that are taken query by query: a half's even ones, odd ones
+    volatile int* kmiss_sm = tmp + 57;                                          // [16] miss of the last 16 tiles (more than are under way)
+    volatile int* raw_sm = tmp + 73;                                            // q8_0, [2][2]: a page's number, -1 not needed, -2 outside the pool
     int4* seq = reinterpret_cast<int4*>(sm + G::off_seq);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int qt = NS == 2 && !p.decode ? 256 : 128;
@@ -479,8 +483,8 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
         ++k;
         return it;
     };
-    // whether some row does not see some token of a tile
-    auto edge = [&](const Record& it, int t0) { return !(t0 + TN <= it.minlen && (t0 >= it.maxlo || t0 + TN <= p.sinks)); };
+    // whether some row does not see some token of a half
+    auto edge = [&](const Record& it, int t0) { return !(t0 + kHalf <= it.minlen && (t0 >= it.maxlo || t0 + kHalf <= p.sinks)); };
     // a token that no row of the item sees
     auto gone = [&](const Record& it, int t) { return t >= it.hi || (t < it.lo && t >= it.sink_end); };
     constexpr int kPieces = G::q8 ? 1 : TN / 16;
@@ -500,14 +504,14 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
     };
 
     // Registers go where the scores are (the shares add up to what the block was launched with, or less:
-    // 256 * 200 + 128 * 104 = 384 * 168; q8_0 256 * 120 + 384 * 80 = 640 * 96).
+    // 256 * 200 + 128 * 104 = 384 * 168; q8_0 256 * 168 + 256 * 80 <= 512 * 128).
     if (warp < 4) {
     if constexpr (NS == 2) setmaxnreg_dec<G::q8 ? 80 : 104>();
     if (warp == 0 || warp == 2) {
         // ---------------------------------------------------------------- records; K tiles (warp 0), V tiles (warp 2)
         const int h = warp == 2;
         constexpr int kSlots = G::q8 ? G::raw_slots : G::k_slots;
-        static_assert(G::q8 || G::k_slots == G::v_slots);
+        static_assert(G::info_slots == 4 && (G::q8 || G::k_slots == G::v_slots));
         uint64_t* full = G::q8 ? rfull + h * kSlots : h ? vfull : kfull;
         uint64_t* empty = G::q8 ? rempty + h * kSlots : h ? vempty : kempty;
         uint8_t* ring = sm + (G::q8 ? G::off_raw + h * kSlots * kQ8Half : h ? G::off_v : 0);
@@ -596,35 +600,41 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
             int pend[2] = {-1, -1};    // the tile whose P V is still to come
             bool first[2] = {true, true};  // .. and whether it is its item's first
             int both = 0;              // items of two tiles of queries so far
-            // P V of stream s, and V's slot back if this is its last use.  (P is there after its tile's V: the softmax
-            // or warp 3's arrival on vready goes before.)
-            auto product_o = [&](int s, bool last) {
+            // Products of one thread run in the order in which they are asked for: S may go over a P whose product has been.
+            // P V of a half of stream s's tile; its first use of V waits for it, the last gives V's slot back.
+            auto product_o = [&](int s, int half, bool wait_v, bool last) {
                 const int n = done[s], x = 2 * s + (n & 1), vs = pend[s] % G::v_slots;
                 wait(pfull + x, (n >> 1) & 1);
-                wait(vready + vs, (pend[s] / G::v_slots) & 1);
+                if (wait_v) wait(vready + vs, (pend[s] / G::v_slots) & 1);
                 if (!live) return;
                 tc_fence_after();
-                const uint32_t a = tmem + x * TN, o = tmem + G::col_o + s * D;
+                const uint32_t a = tmem + x * kHalf, o = tmem + G::col_o + s * D;
                 const uint32_t acc = !first[s] || accum_sm[s] != 0;
-                const uint64_t b0 = vd + (vs * G::tile >> 4);
+                const uint64_t b0 = vd + (vs * G::tile >> 4) + half * (kHalf * 128 >> 4);
 #pragma unroll
                 for (int part = 0; part < (G::q8 ? 2 : 1); ++part)
 #pragma unroll
-                    for (int ks = 0; ks < TN / 16; ++ks)
+                    for (int ks = 0; ks < kHalf / 16; ++ks)
                         tc_mma_f16_ts(o, a + 8 * ks, b0 + (G::q8 ? (part * G::part + ks * 32) >> 4 : ks * (2048 >> 4)), kIdescO, part + ks ? 1 : acc);
-                tc_commit(odone + s);
+                if (!G::halves || half == 0) tc_commit(odone + s);
                 if (last) tc_commit(vempty + vs);
+                first[s] = false;
                 ++done[s];
+            };
+            // .. of its whole tile
+            auto product_pv = [&](int s, bool wait_v, bool last) {
+                product_o(s, 0, wait_v, !G::halves && last);
+                if (G::halves && live) product_o(s, 1, false, last);
                 pend[s] = -1;
             };
             auto product_s = [&](int s, int ksl, int qs, bool last) {
-                const int x = 2 * s + (asked[s] & 1);
+                const int x = G::halves ? 2 * s : 2 * s + (asked[s] & 1);
                 const uint64_t aq = qd + (qs * G::q_tile >> 4), bk = kd + (ksl * G::tile >> 4);
 #pragma unroll
                 for (int part = 0; part < (G::q8 ? 2 : 1); ++part)
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks)
-                        tc_mma_f16_ss(tmem + x * TN, aq + (((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4),
+                        tc_mma_f16_ss(tmem + x * kHalf, aq + (((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4),
                                       bk + ((part * G::part + (ks >> 2) * (TN * 128) + (ks & 3) * 32) >> 4), kIdescS, part + ks > 0);
                 tc_commit(sfull + x);
                 if (last) tc_commit(kempty + ksl);
@@ -638,36 +648,35 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                 wait(qfull, k & 1);
                 const bool two = NS == 2 && !p.decode && it.nq - it.q0 > 128;
                 if (two) wait(qfull + 1, both++ & 1);
-                int begun[2] = {0, 0};  // the item's tiles by stream
+                bool begun[2] = {false, false};
                 for (int i = 0; i < it.nt && live; ++i, ++t) {
                     const int ksl = t % G::k_slots;
                     wait(kfull + ksl, (t / G::k_slots) & 1);
                     if (!live) break;
                     tc_fence_after();
-                    // the streams that this tile is for: scores first, then the products of their tiles before
+                    // the streams that this tile is for.  One buffer of scores: the product of its tile before, then its
+                    // scores; two: all scores first
                     const int from = NS == 2 && p.decode ? tile_at(it, i) & 1 : 0, to = two ? 1 : from;
+                    if (!G::halves) {
 #pragma unroll
-                    for (int s = 0; s < NS; ++s)
-                        if (s >= from && s <= to) {
-                            // S goes over the P before last, whose product has to be over (products of different shapes need
-                            // not keep their order).  Those of earlier items are: their outputs were read before the queries came.
-                            if (begun[s]++ >= 2) wait(odone + s, asked[s] & 1);
-                            if (live) product_s(s, ksl, p.decode ? 0 : s, s == to);
-                        }
+                        for (int s = 0; s < NS; ++s)
+                            if (s >= from && s <= to) product_s(s, ksl, p.decode ? 0 : s, s == to);
+                    }
 #pragma unroll
                     for (int s = 0; s < NS; ++s)
                         if (live && s >= from && s <= to) {
-                            if (NS == 2 && p.decode && pend[1 - s] >= 0 && pend[1 - s] < pend[s]) product_o(1 - s, true);
-                            if (pend[s] >= 0 && live) product_o(s, s == to);
-                            pend[s] = t, first[s] = begun[s] == 1;
+                            // (V's slots come free in the tiles' order)
+                            if (NS == 2 && p.decode && pend[1 - s] >= 0 && pend[1 - s] < pend[s]) product_pv(1 - s, true, true);
+                            if (pend[s] >= 0 && live) product_pv(s, s == from, s == to);
+                            if (G::halves && live) product_s(s, ksl, p.decode ? 0 : s, s == to);
+                            pend[s] = t, first[s] = !begun[s], begun[s] = true;
                         }
                 }
-                // what is left, in the tiles' order (V's slots come free in it)
-                const bool swap = NS == 2 && p.decode && pend[1] >= 0 && pend[1] < pend[0];
-                if (swap && live) product_o(1, true);
+                // what is left, in the tiles' order
+                if (NS == 2 && p.decode && pend[1] >= 0 && pend[1] < pend[0] && live) product_pv(1, true, true);
 #pragma unroll
                 for (int s = 0; s < NS; ++s) {
-                    if (pend[s] >= 0 && live) product_o(s, p.decode || s == (two ? 1 : 0));
+                    if (pend[s] >= 0 && live) product_pv(s, s == 0 || p.decode, p.decode || s == (two ? 1 : 0));
                     if (begun[s] && live) tc_commit(ofin + s);
                 }
             }
@@ -689,11 +698,15 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                 await(vfull + vs, (t / G::v_slots) & 1);
                 if (!live) break;
                 const int miss = miss_sm[vs];
-                if (miss || edge(it, t0)) {
+                bool some = false;
+#pragma unroll 1
+                for (int half = 0; half < TN / kHalf; ++half) {
+                    if (!(miss || edge(it, t0 + half * kHalf))) continue;
+                    some = true;
                     uint8_t* vt = sm + G::off_v + vs * G::tile;
 #pragma unroll 1
                     for (int j = 0; j < 2; ++j) {
-                        const int row = 2 * lane + j, tok = t0 + row;
+                        const int row = half * kHalf + 2 * lane + j, tok = t0 + row;
                         bool zero = gone(it, tok) || ((miss >> (row >> piece_shift)) & 1), odd = false;
                         if (!zero && !(tok < it.minlen && (tok >= it.maxlo || tok < p.sinks))) {
                             constexpr uint32_t ex = BF ? 0x7F80u : 0x7C00u;
@@ -714,8 +727,10 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                                     *reinterpret_cast<uint4*>(vt + x * TN * 128 + row * 128 + 16 * ((c + lane) & 7)) = make_uint4(0, 0, 0, 0);
                         }
                         const uint32_t word = __ballot_sync(0xffffffffu, odd);
-                        if (lane == 0) odd_sm[t % G::info_slots * 2 + j] = word;
+                        if (lane == 0) odd_sm[t % G::info_slots * 4 + 2 * half + j] = word;
                     }
+                }
+                if (some) {
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
@@ -727,7 +742,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
         }
     }
     } else if (warp < 4 + G::soft_warps) {
-        if constexpr (NS == 2) setmaxnreg_inc<G::q8 ? 120 : 200>();
+        if constexpr (NS == 2) setmaxnreg_inc<G::q8 ? 168 : 200>();
         // ---------------------------------------------------------------- softmax: a query per thread
         const int s = (warp - 4) >> 2, me = tid & 127;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
@@ -774,12 +789,13 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
             }
             float l = 0.f, lim = -INFINITY, base = 0.f;  // sum, reference and slack, what comes off the scores
             bool fresh = true;                           // O holds nothing yet
-            for (int i = 0; i < it.nt; ++i) {
-                const int tile = tile_at(it, i), t0 = tile * TN, tv = tiles0 + i;
+            for (int ih = 0; ih < it.nt * (TN / kHalf); ++ih) {
+                const int i = G::halves ? ih >> 1 : ih, half = G::halves ? ih & 1 : 0;
+                const int tile = tile_at(it, i), t0 = tile * TN + half * kHalf, tv = tiles0 + i;
                 if (NS == 2 && p.decode && (tile & 1) != s) continue;
                 const int x = 2 * s + (n & 1);
-                const uint32_t scol = lanes + x * TN;
-                await(sfull + x, (n >> 1) & 1);
+                const uint32_t scol = lanes + x * kHalf;
+                if (half == 0) await(sfull + (G::halves ? 2 * s : x), (n >> 1) & 1);
                 if (!live) break;
                 if (idle) {  // (its rows of P hold anything: nobody reads what comes of them)
                     fresh = false;
@@ -794,30 +810,32 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                     await(vinfo + vi, (tv / G::info_slots) & 1);
                     if (!live) break;
                 }
-                float v[TN];
+                float v[kHalf];
                 tmem_ld32(scol, v);
                 tmem_ld32(scol + 32, v + 32);
-                const int miss = kmiss_sm[tv & 15];
+                const int miss = kmiss_sm[tv & 15] >> (half * kHalf >> piece_shift);
                 tc_wait_ld();
                 if (some || miss) {
-                    const int jl = len - t0, jf = from - t0, js = first - t0;
+                    // the tokens that the row sees, as bits; a missing piece is 16 tokens at least
+                    auto below = [](int j) { return j <= 0 ? uint64_t{0} : j >= 64 ? ~uint64_t{0} : (uint64_t{1} << j) - 1; };
+                    uint64_t sees = below(len - t0) & (~below(from - t0) | below(first - t0));
+                    if (miss) {
 #pragma unroll
-                    for (int j = 0; j < TN; ++j)
-                        if (!(j < jl && (j >= jf || j < js))) v[j] = -INFINITY;
-                    if (miss) {  // (a piece is 16 tokens at least)
+                        for (int c = 0; c < kHalf; c += 16)
+                            if ((miss >> (c >> piece_shift)) & 1) sees &= ~(uint64_t{0xFFFF} << c);
+                    }
+                    const uint32_t low = static_cast<uint32_t>(sees), high = static_cast<uint32_t>(sees >> 32);
 #pragma unroll
-                        for (int c = 0; c < TN; c += 16)
-                            if ((miss >> (c >> piece_shift)) & 1) {
-#pragma unroll
-                                for (int j = 0; j < 16; ++j) v[c + j] = -INFINITY;
-                            }
+                    for (int j = 0; j < 32; ++j) {
+                        if (!(low & (1u << j))) v[j] = -INFINITY;
+                        if (!(high & (1u << j))) v[j + 32] = -INFINITY;
                     }
                 }
                 float m4[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) m4[j] = fmaxf(v[j], v[j + 4]);
 #pragma unroll
-                for (int j = 8; j < TN; j += 8)
+                for (int j = 8; j < kHalf; j += 8)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) m4[i] = fmaxf(m4[i], fmaxf(v[j + i], v[j + i + 4]));
                 const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.c2;  // (a NaN is no maximum)
@@ -833,7 +851,8 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                         l *= alpha;
                     }
                     if (!fresh) {
-                        await(odone + s, (n - 1) & 1);  // (the one before that was over before these scores were asked for)
+                        // (the product of the half before; earlier ones were over before these scores were asked for)
+                        if (!G::halves || half == 1) await(odone + s, G::halves ? (n >> 1) & 1 : (n - 1) & 1);
                         if (!live) break;
                         tc_fence_after();
 #pragma unroll 1
@@ -850,7 +869,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                 uint64_t sum[2] = {0, 0};  // pairs of fp32
                 const uint64_t c2 = pair(p.c2, p.c2), off = pair(-base, -base);
 #pragma unroll
-                for (int c = 0; c < TN; c += 32) {
+                for (int c = 0; c < kHalf; c += 32) {
                     uint32_t w[16];
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
@@ -868,12 +887,12 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                 tc_wait_st();
                 // ---- tokens whose V is not finite, to those that see them
                 uint32_t odd = 0;
-                if (some) odd = odd_sm[vi * 2] | odd_sm[vi * 2 + 1];
+                if (some) odd = odd_sm[vi * 4 + 2 * half] | odd_sm[vi * 4 + 2 * half + 1];
                 if (odd) {
-                    if (!fresh) await(odone + s, (n - 1) & 1);
+                    if (!fresh && (!G::halves || half == 1)) await(odone + s, G::halves ? (n >> 1) & 1 : (n - 1) & 1);
                     if (!live) break;
                     tc_fence_after();
-                    add_odd<FMT, D>(p, it.a, it.g, t0, const_cast<const uint32_t*>(odd_sm) + vi * 2, ocol, scol, len, from, first, fresh);
+                    add_odd<FMT, D>(p, it.a, it.g, t0, const_cast<const uint32_t*>(odd_sm) + vi * 4 + 2 * half, ocol, scol, len, from, first, fresh);
                 }
                 if (fresh && me == 0) accum_sm[s] = odd != 0;
                 fresh = false;
@@ -990,126 +1009,142 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
         if (!live && lane == 0) atomicOr(p.err, kErrTimeout);
     } else if constexpr (G::q8) {
         setmaxnreg_dec<80>();
-        // A tile is a page.
-        const int me = tid & 127;
-        int t = 0;
-        if (warp < 8 + G::soft_warps) {
-            // ---------------------------------------------------------------- K to fp16: half a token's dims per thread
-            const int slot = me & 63, half = me >> 6, key = q8_key(slot & 7);
-            for (int item = blockIdx.x; item < total && live; item += gridDim.x) {
-                const Record it = next_record();
-                for (int i = 0; i < it.nt && live; ++i, ++t) {
-                    const int ks = t % G::k_slots, rs = t % G::raw_slots;
-                    await(rfull + rs, (t / G::raw_slots) & 1);
-                    if (!live) break;
-                    const int pg = raw_sm[rs];
-                    uint4 row[4];
-                    uint32_t sc = 0;
-                    if (pg >= 0) {
-                        const uint8_t* b = sm + G::off_raw + rs * kQ8Half;
+        // ---------------------------------------------------------------- q8_0 to fp16; a tile is a page
+        // K goes a tile ahead: V of a tile may wait for a product that comes after the next tile's scores.
+        const int me = tid & 127, slot = me & 63, half = me >> 6, key = q8_key(slot & 7);
+        // (the order in which a thread takes its four pieces of 16 tokens of V, c ^ x by lane, keeps both the reads, 64
+        // bytes apart, and the swizzled writes free of bank conflicts)
+        const int w4 = warp & 3, turn = (0x78 >> (2 * ((lane >> 1) & 3))) & 3;  // 0, 2, 3, 1
+        uint8_t* dv = sm + G::off_dv + w4 * 128;
+        auto convert_k = [&](int t) {  // half a token's dims per thread
+            const int ks = t % G::k_slots, rs = t % G::raw_slots;
+            await(rfull + rs, (t / G::raw_slots) & 1);
+            if (!live) return;
+            const int pg = raw_sm[rs];
+            uint4 row[4];
+            uint32_t sc = 0;
+            if (pg >= 0) {
+                const uint8_t* b = sm + G::off_raw + rs * kQ8Half;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) row[c] = *reinterpret_cast<const uint4*>(b + slot * 128 + 16 * ((4 * half + c) ^ key));
-                        sc = *reinterpret_cast<const uint32_t*>(b + 8192 + slot * 8 + 4 * half);
+                for (int c = 0; c < 4; ++c) row[c] = *reinterpret_cast<const uint4*>(b + slot * 128 + 16 * ((4 * half + c) ^ key));
+                sc = *reinterpret_cast<const uint32_t*>(b + 8192 + slot * 8 + 4 * half);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(rempty + rs);
+            if (t >= G::k_slots) await(kempty + ks, (t / G::k_slots - 1) & 1);
+            if (!live) return;
+            if (me == 0) kmiss_sm[t & 15] = pg == -2;
+            if (pg >= 0) {
+                uint8_t* dst = sm + ks * G::tile + half * (TN * 128) + slot * 128;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {  // eight dims: one 16-byte piece of each part
+                    const uint32_t u0 = ((c & 1) ? row[c >> 1].z : row[c >> 1].x) ^ 0x80808080u;
+                    const uint32_t u1 = ((c & 1) ? row[c >> 1].w : row[c >> 1].y) ^ 0x80808080u;
+                    const __half2 d = __half2half2(c >> 2 ? __high2half(as_h2(sc)) : __low2half(as_h2(sc)));
+                    const __half2 z[4] = {i8_to_h2(u0, 0x4140u), i8_to_h2(u0, 0x4342u), i8_to_h2(u1, 0x4140u), i8_to_h2(u1, 0x4342u)};
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const __half2 x = __hmul2(z[j], d);
+                        hi[j] = as_u32(x);
+                        lo[j] = as_u32(__hfma2(z[j], d, __hneg2(x)));
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(rempty + rs);
-                    if (t >= G::k_slots) await(kempty + ks, (t / G::k_slots - 1) & 1);
-                    if (!live) break;
-                    if (me == 0) kmiss_sm[t & 15] = pg == -2;
-                    if (pg >= 0) {
-                        uint8_t* dst = sm + ks * G::tile + half * (TN * 128) + slot * 128;
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) {  // eight dims: one 16-byte piece of each part
-                            const uint32_t u0 = ((c & 1) ? row[c >> 1].z : row[c >> 1].x) ^ 0x80808080u;
-                            const uint32_t u1 = ((c & 1) ? row[c >> 1].w : row[c >> 1].y) ^ 0x80808080u;
-                            const __half2 d = __half2half2(c >> 2 ? __high2half(as_h2(sc)) : __low2half(as_h2(sc)));
-                            const __half2 z[4] = {i8_to_h2(u0, 0x4140u), i8_to_h2(u0, 0x4342u), i8_to_h2(u1, 0x4140u), i8_to_h2(u1, 0x4342u)};
-                            uint32_t hi[4], lo[4];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const __half2 x = __hmul2(z[j], d);
-                                hi[j] = as_u32(x);
-                                lo[j] = as_u32(__hfma2(z[j], d, __hneg2(x)));
-                            }
-                            const int at = (c ^ (slot & 7)) << 4;
-                            *reinterpret_cast<uint4*>(dst + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                            *reinterpret_cast<uint4*>(dst + G::part + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(kfull + ks);
+                    const int at = (c ^ (slot & 7)) << 4;
+                    *reinterpret_cast<uint4*>(dst + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(dst + G::part + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
             }
-        } else {
-            // ---------------------------------------------------------------- V to fp16: a dim per thread
-            // (the order in which a thread takes its four pieces of 16 tokens, c ^ x by lane, keeps both the reads, 64
-            // bytes apart, and the swizzled writes free of bank conflicts)
-            const int w4 = warp & 3, turn = (0x78 >> (2 * ((lane >> 1) & 3))) & 3;  // 0, 2, 3, 1
-            uint8_t* dv = sm + G::off_dv + w4 * 128;
-            for (int item = blockIdx.x; item < total && live; item += gridDim.x) {
-                const Record it = next_record();
-                for (int i = 0; i < it.nt && live; ++i, ++t) {
-                    const int t0 = tile_at(it, i) * TN, vs = t % G::v_slots, rs = t % G::raw_slots;
-                    await(rfull + G::raw_slots + rs, (t / G::raw_slots) & 1);
-                    if (t >= G::v_slots) await(vempty + vs, (t / G::v_slots - 1) & 1);
-                    if (!live) break;
-                    const int pg = raw_sm[2 + rs];
-                    const uint8_t* b = sm + G::off_raw + (G::raw_slots + rs) * kQ8Half;
-                    const uint8_t* scales = b + 8192 + w4 * 128;
-                    if (pg < 0 || edge(it, t0)) {
-                        // Scales of 0 for tokens that must not count, as warp 3 zeroes rows of 16-bit pools (what is not finite
-                        // is a scale, or too large for fp16).  A warp's dims are one block of scales.
-                        uint32_t mine = 0;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(kfull + ks);
+        };
+        auto convert_v = [&](const Record& it, int t0, int t) {  // a dim per thread
+            const int vs = t % G::v_slots, rs = t % G::raw_slots;
+            await(rfull + G::raw_slots + rs, (t / G::raw_slots) & 1);
+            if (t >= G::v_slots) await(vempty + vs, (t / G::v_slots - 1) & 1);
+            if (!live) return;
+            const int pg = raw_sm[2 + rs];
+            const uint8_t* b = sm + G::off_raw + (G::raw_slots + rs) * kQ8Half;
+            const uint8_t* scales = b + 8192 + w4 * 128;
+            if (pg < 0 || edge(it, t0)) {
+                // Scales of 0 for tokens that must not count, as warp 3 zeroes rows of 16-bit pools (what is not finite
+                // is a scale, or too large for fp16).  A warp's dims are one block of scales.
+                uint32_t mine = 0;
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const int tok = t0 + 2 * lane + j;
-                            const bool none = pg < 0 || gone(it, tok);
-                            bool odd = false;
-                            if (!none && !(tok < it.minlen && (tok >= it.maxlo || tok < p.sinks))) {
+                for (int j = 0; j < 2; ++j) {
+                    const int tok = t0 + 2 * lane + j;
+                    const bool none = pg < 0 || gone(it, tok);
+                    bool odd = false;
+                    if (!none && !(tok < it.minlen && (tok >= it.maxlo || tok < p.sinks))) {
 #pragma unroll
-                                for (int c = 0; c < 4; ++c) odd |= (*reinterpret_cast<const uint16_t*>(b + 8192 + c * 128 + 4 * lane + 2 * j) & 0x7FFFu) >= (24u << 10);  // 512
-                            }
-                            const uint32_t who = __ballot_sync(0xffffffffu, odd);
-                            if (w4 == 0 && lane == 0) odd_sm[t % G::info_slots * 2 + j] = who;
-                            if (!none && !odd) mine |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(scales + 4 * lane + 2 * j)) << (16 * j);
-                        }
-                        *reinterpret_cast<uint32_t*>(dv + 4 * lane) = mine;
-                        __syncwarp();
-                        scales = dv;
+                        for (int c = 0; c < 4; ++c) odd |= (*reinterpret_cast<const uint16_t*>(b + 8192 + c * 128 + 4 * lane + 2 * j) & 0x7FFFu) >= (24u << 10);  // 512
                     }
-                    uint8_t* dst = sm + G::off_v + vs * G::tile + me * 128;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int cc = c ^ turn;  // 16 tokens
-                        uint4 u = make_uint4(0, 0, 0, 0);
-                        if (pg >= 0) u = *reinterpret_cast<const uint4*>(b + me * 64 + 16 * cc);
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {  // eight of them: a 16-byte piece of each part
-                            const uint4 d = *reinterpret_cast<const uint4*>(scales + 32 * cc + 16 * j);
-                            const uint32_t u0 = (j ? u.z : u.x) ^ 0x80808080u, u1 = (j ? u.w : u.y) ^ 0x80808080u;
-                            const __half2 z[4] = {i8_to_h2(u0, 0x4140u), i8_to_h2(u0, 0x4342u), i8_to_h2(u1, 0x4140u), i8_to_h2(u1, 0x4342u)};
-                            const __half2 e[4] = {as_h2(d.x), as_h2(d.y), as_h2(d.z), as_h2(d.w)};
-                            uint32_t hi[4], lo[4];
-#pragma unroll
-                            for (int n = 0; n < 4; ++n) {
-                                const __half2 x = __hmul2(z[n], e[n]);
-                                hi[n] = as_u32(x);
-                                lo[n] = as_u32(__hfma2(z[n], e[n], __hneg2(x)));
-                            }
-                            const int at = ((2 * cc + j) ^ (me & 7)) << 4;
-                            *reinterpret_cast<uint4*>(dst + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                            *reinterpret_cast<uint4*>(dst + G::part + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(vready + vs);
-                        mbar_arrive(vinfo + t % G::info_slots);
-                        mbar_arrive(rempty + G::raw_slots + rs);
-                    }
+                    const uint32_t who = __ballot_sync(0xffffffffu, odd);
+                    if (w4 == 0 && lane == 0) odd_sm[t % G::info_slots * 4 + j] = who;
+                    if (!none && !odd) mine |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(scales + 4 * lane + 2 * j)) << (16 * j);
                 }
+                *reinterpret_cast<uint32_t*>(dv + 4 * lane) = mine;
+                __syncwarp();
+                scales = dv;
+            }
+            uint8_t* dst = sm + G::off_v + vs * G::tile + me * 128;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int cc = c ^ turn;  // 16 tokens
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (pg >= 0) u = *reinterpret_cast<const uint4*>(b + me * 64 + 16 * cc);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {  // eight of them: a 16-byte piece of each part
+                    const uint4 d = *reinterpret_cast<const uint4*>(scales + 32 * cc + 16 * j);
+                    const uint32_t u0 = (j ? u.z : u.x) ^ 0x80808080u, u1 = (j ? u.w : u.y) ^ 0x80808080u;
+                    const __half2 z[4] = {i8_to_h2(u0, 0x4140u), i8_to_h2(u0, 0x4342u), i8_to_h2(u1, 0x4140u), i8_to_h2(u1, 0x4342u)};
+                    const __half2 e[4] = {as_h2(d.x), as_h2(d.y), as_h2(d.z), as_h2(d.w)};
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const __half2 x = __hmul2(z[n], e[n]);
+                        hi[n] = as_u32(x);
+                        lo[n] = as_u32(__hfma2(z[n], e[n], __hneg2(x)));
+                    }
+                    const int at = ((2 * cc + j) ^ (me & 7)) << 4;
+                    *reinterpret_cast<uint4*>(dst + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(dst + G::part + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(vready + vs);
+                mbar_arrive(vinfo + t % G::info_slots);
+                mbar_arrive(rempty + G::raw_slots + rs);
+            }
+        };
+        Record ahead, it;       // K's item and V's
+        int item = blockIdx.x, tk = 0, left = 0;
+        ahead.nt = 0;
+        // the next tile's K, if there is one
+        auto next_k = [&]() -> bool {
+            while (left == 0) {
+                if (item >= total || !live) return false;
+                ahead = next_record();
+                item += gridDim.x;
+                left = live ? ahead.nt : 0;
+            }
+            --left;
+            convert_k(tk++);
+            return live;
+        };
+        bool more = next_k();
+        it = ahead;
+        int i = 0;
+        for (int t = 0; more; ++t) {
+            const bool also = next_k();  // (may have gone on to the next item)
+            if (!live) break;
+            convert_v(it, tile_at(it, i) * TN, t);
+            more = also && live;
+            if (++i == it.nt) {
+                it = ahead;
+                i = 0;
             }
         }
     }
@@ -1129,7 +1164,7 @@ cudaError_t launch_one(const Launch& a, cudaStream_t s) {
         cudaFuncAttributes f = {};
         return cudaFuncGetAttributes(&f, attend_window_tc<FMT, D>) == cudaSuccess ? f.numRegs : 0;
     }();
-    if (G::streams == 2 && regs < (G::q8 ? 96 : 168)) return cudaErrorLaunchOutOfResources;
+    if (G::streams == 2 && regs < (G::q8 ? 128 : 168)) return cudaErrorLaunchOutOfResources;
     const cudaError_t e = once.allow_shared(attend_window_tc<FMT, D>, a.device);
     if (e != cudaSuccess) return e;
     attend_window_tc<FMT, D><<<a.grid, G::threads, G::smem(a.p.agents), s>>>(a.map, a.p);
