@@ -13,17 +13,16 @@
 //   decode steps: one tile of queries, whose tokens' tiles are dealt to two streams by their parity; the streams
 //     meet at the end through shared memory.
 // Either way two streams take turns on the tensor cores (one at head dimension 256, for which tensor memory has no more
-// room): one's products run while the other's scores become probabilities.  The softmax takes 64 tokens at a time.  16-bit
-// pools at head dimensions 64 and 128 have tiles of two such halves, formed by one product of 128 columns (one of 64 takes
-// as long: it reads as much of Q), and the first half's P V runs under the second's softmax.  Otherwise a tile is
-// one half, and scores have two buffers: the next tile's are there when the softmax is done with one.
+// room): one's products run while the other's scores become probabilities.  16-bit pools at head dimensions 64 and 128
+// have tiles of 128 tokens (a product of 64 columns of scores takes as long: it reads as much of Q), whose
+// probabilities go out in two halves, so that the first half's P V runs under the second's exponentials.  Otherwise
+// tiles have 64 tokens, and scores have two buffers: the next tile's are there when the softmax is done with one.
 // The tiles of an item are those that some of its rows sees: the first ones (sinks), and the window's.  Where few
 // items would leave SMs idle, tokens are cut into chunks at fixed places of a sequence, an item each, whose unnormalised
 // outputs a second kernel joins.  All choices are made by the plan's dims, so a row's bits do not depend on its company.
-//   warp 0      forms the items' records; asks for K tiles (q8_0: as they are stored)
-//   warp 1      one thread issues the products
-//   warp 2      asks for V tiles
-//   warp 3      16-bit pools: zeroes the rows of V that must not count, where some are
+//   warp 0      forms the items' records; asks for K and V tiles (q8_0: as they are stored)
+//   warps 1, 3  one thread each issues a stream's products
+//   warp 2      16-bit pools: zeroes the rows of V that must not count, where some are
 //   warps 4 ..  softmax, four a stream
 //   q8_0: four more convert K (half a token a thread) and V (a dim a thread) to two fp16 parts whose sum is quant
 //               times scale
@@ -43,7 +42,7 @@ using namespace qmm::kv;
 
 constexpr float kShift = 9.f;       // p's power of two ..
 constexpr float kSlack = 6.f;       // .. and how far a score may pass its reference: p <= 2^15
-constexpr int kHalf = 64;          // tokens that the softmax takes at a time
+constexpr int kHalf = 64;          // tokens whose probabilities go out at a time
 constexpr float kFine = 4194304.f;  // 2^22: a larger reference stands alone (fp32's spacing would swallow the two): p <= 1
 
 struct Params {
@@ -78,11 +77,14 @@ struct Geo {
     static constexpr bool q8 = FMT == QMM_KV_Q8_0;
     static constexpr int streams = D == 256 ? 1 : 2;
     static constexpr bool halves = !q8 && D <= 128;              // tiles of two halves, one buffer of scores per stream
-    static constexpr int TN = halves ? 2 * kHalf : kHalf;        // tokens of a tile
+    static constexpr int H = halves ? 2 : 1, TN = H * kHalf;     // tokens of a tile
     static constexpr int part = TN * D * 2;                      // bytes of a tile's K or V in 16 bits
     static constexpr int tile = q8 ? 2 * part : part;            // q8_0: high and low parts
     static constexpr int k_slots = D == 64 ? 4 : 2, v_slots = q8 ? 1 : k_slots;
-    static constexpr int info_slots = v_slots < 4 ? 4 : v_slots;  // V tiles of which the softmax is told (see there)
+    // Barriers that say that a tile's K or V is there: more of them than slots, since a stream of a decode step waits only for
+    // tiles of its own, at most three apart.  Then a barrier's phase before the one waited for is over for sure: V's come
+    // in order, and the last own tile's K was asked for after the K of eight tiles before had been used.
+    static constexpr int k_told = 8, v_told = 4;
     static constexpr int raw_slots = q8 ? 2 : 0;                 // pages on their way, K and V
     static constexpr int q_tile = 128 * D * 2;
     static constexpr int soft_warps = 4 * streams, conv_warps = q8 ? 4 : 0;
@@ -97,7 +99,7 @@ struct Geo {
     static constexpr int off_item = off_ml + 128 * 8;            // [2] of Record
     static constexpr int off_dv = off_item + 2 * 64;             // q8_0: V's scales, zero where a token must not count: [4][64] fp16
     static constexpr int off_bar = off_dv + (q8 ? 512 : 0);
-    static constexpr int bars = 2 * k_slots + 3 * v_slots + info_slots + 4 * raw_slots + 2 + 4 + 4 + 2 + 2 + 2 + 2 + 3;
+    static constexpr int bars = k_told + k_slots + 2 * v_slots + v_told + 4 * raw_slots + 2 + 4 + 4 + 2 + 2 + 2 + 2 + 4;
     // tmp[33], abort, tmem, accumulate[2], miss[4] (of V tiles), odd[4][4], miss[16] (of all tiles), raw[2][2]
     static constexpr int off_misc = (off_bar + bars * 8 + 15) / 16 * 16;
     static constexpr int off_seq = (off_misc + 80 * 4 + 15) / 16 * 16;
@@ -130,6 +132,23 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lead) {
     return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
            (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+// A product from descriptors by their low words (the address is in it) and the high ones.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 __device__ __forceinline__ void tma_load_hint(void* smem_dst, const void* tmap, int32_t c0, int32_t c1, uint64_t* bar, uint64_t policy) {
     asm volatile(
@@ -420,8 +439,8 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
     float2* ml_sm = reinterpret_cast<float2*>(sm + G::off_ml);
     Record* item_sm = reinterpret_cast<Record*>(sm + G::off_item);
     uint64_t* kfull = reinterpret_cast<uint64_t*>(sm + G::off_bar);
-    uint64_t *kempty = kfull + G::k_slots, *vfull = kempty + G::k_slots, *vempty = vfull + G::v_slots, *vready = vempty + G::v_slots;
-    uint64_t *vinfo = vready + G::v_slots, *rfull = vinfo + G::info_slots, *rempty = rfull + 2 * G::raw_slots;  // (K's, then V's)
+    uint64_t *kempty = kfull + G::k_told, *vfull = kempty + G::k_slots, *vempty = vfull + G::v_slots, *vready = vempty + G::v_slots;
+    uint64_t *rfull = vready + G::v_told, *rempty = rfull + 2 * G::raw_slots;  // (K's, then V's)
     uint64_t *qfull = rempty + 2 * G::raw_slots, *sfull = qfull + 2, *pfull = sfull + 4, *odone = pfull + 4, *ofin = odone + 2;
     uint64_t *ifull = ofin + 2, *iempty = ifull + 2, *mfree = iempty + 2, *mfull = mfree + 1, *drained = mfull + 1;
     int* tmp = reinterpret_cast<int*>(sm + G::off_misc);
@@ -437,21 +456,24 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
     const int qt = NS == 2 && !p.decode ? 256 : 128;
 
     if (tid == 0) {
-        for (int i = 0; i < G::k_slots; ++i) mbar_init(kfull + i, G::q8 ? 4 : 1), mbar_init(kempty + i, 1);
-        for (int i = 0; i < G::v_slots; ++i) mbar_init(vfull + i, 1), mbar_init(vempty + i, 1), mbar_init(vready + i, G::q8 ? 4 : 1);
-        for (int i = 0; i < G::info_slots; ++i) mbar_init(vinfo + i, G::q8 ? 4 : 1);
+        const int users = NS == 2 && !p.decode ? 2 : 1;  // streams that see a tile
+        for (int i = 0; i < G::k_told; ++i) mbar_init(kfull + i, G::q8 ? 4 : 1);
+        for (int i = 0; i < G::v_told; ++i) mbar_init(vready + i, G::q8 ? 4 : 1);
+        for (int i = 0; i < G::k_slots; ++i) mbar_init(kempty + i, users);
+        for (int i = 0; i < G::v_slots; ++i) mbar_init(vfull + i, 1), mbar_init(vempty + i, users);
         for (int i = 0; i < 2; ++i) {
             mbar_init(qfull + i, 4);
             mbar_init(odone + i, 1);
             mbar_init(ofin + i, 1);
             mbar_init(ifull + i, 1);
-            mbar_init(iempty + i, (G::q8 ? 2 + G::conv_warps : 3) + G::soft_warps);
+            mbar_init(iempty + i, NS + (G::q8 ? G::conv_warps : 1) + G::soft_warps);
         }
         for (int i = 0; i < 4; ++i) mbar_init(sfull + i, 1), mbar_init(pfull + i, 4);
         for (int i = 0; i < 2 * G::raw_slots; ++i) mbar_init(rfull + i, 1), mbar_init(rempty + i, 4);
         mbar_init(mfree, 4);
         mbar_init(mfull, 4);
         mbar_init(drained, 1);
+        mbar_init(drained + 1, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -487,7 +509,6 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
     auto edge = [&](const Record& it, int t0) { return !(t0 + kHalf <= it.minlen && (t0 >= it.maxlo || t0 + kHalf <= p.sinks)); };
     // a token that no row of the item sees
     auto gone = [&](const Record& it, int t) { return t >= it.hi || (t < it.lo && t >= it.sink_end); };
-    constexpr int kPieces = G::q8 ? 1 : TN / 16;
     const int piece_rows = min(TN, p.page_tokens), piece_shift = 31 - __clz(piece_rows);
     // lane i: the page of piece i of a tile, -1 if nobody needs it, -2 if it is outside the pool
     auto page_of = [&](const Record& it, int t0) {
@@ -507,186 +528,181 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
     // 256 * 200 + 128 * 104 = 384 * 168; q8_0 256 * 168 + 256 * 80 <= 512 * 128).
     if (warp < 4) {
     if constexpr (NS == 2) setmaxnreg_dec<G::q8 ? 80 : 104>();
-    if (warp == 0 || warp == 2) {
-        // ---------------------------------------------------------------- records; K tiles (warp 0), V tiles (warp 2)
-        const int h = warp == 2;
+    if (warp == 0) {
+        // ---------------------------------------------------------------- records, K tiles and V tiles
         constexpr int kSlots = G::q8 ? G::raw_slots : G::k_slots;
-        static_assert(G::info_slots == 4 && (G::q8 || G::k_slots == G::v_slots));
-        uint64_t* full = G::q8 ? rfull + h * kSlots : h ? vfull : kfull;
-        uint64_t* empty = G::q8 ? rempty + h * kSlots : h ? vempty : kempty;
-        uint8_t* ring = sm + (G::q8 ? G::off_raw + h * kSlots * kQ8Half : h ? G::off_v : 0);
+        static_assert(G::q8 || G::k_slots == G::v_slots);
+        uint64_t *full[2] = {G::q8 ? rfull : kfull, G::q8 ? rfull + kSlots : vfull};
+        uint64_t *empty[2] = {G::q8 ? rempty : kempty, G::q8 ? rempty + kSlots : vempty};
+        uint8_t* ring[2] = {sm + (G::q8 ? G::off_raw : 0), sm + (G::q8 ? G::off_raw + kSlots * kQ8Half : G::off_v)};
         // (a prompt's tiles are read by other blocks as well)
         const uint64_t policy = p.decode ? l2_policy_evict_first() : l2_policy_evict_last();
-        int t = 0;
-        for (int item = blockIdx.x; item < total && live; item += gridDim.x) {
-            Record it;
-            if (h) {
-                it = next_record();
-            } else {
-                it = record_of<TN>(p, seq, item, qt);
-                if (k > 1) await(iempty + (k & 1), ((k >> 1) - 1) & 1);
-                if (!live) break;
-                if (lane == 0) {
-                    item_sm[k & 1] = it;
-                    mbar_arrive(ifull + (k & 1));
-                }
-                ++k;
+        // Tile t's K (h = 0) or V: lanes by piece.
+        auto ask = [&](int h, int g, int t0, int mine, int t) {
+            const uint32_t there = __ballot_sync(0xffffffffu, mine >= 0);
+            const int miss = static_cast<int>(__ballot_sync(0xffffffffu, mine == -2));
+            const int s = t % kSlots, round = t / kSlots;
+            uint64_t* told = G::q8 || h ? full[h] + s : kfull + t % G::k_told;
+            if (round > 0) await(empty[h] + s, (round - 1) & 1);
+            if (!live) return;
+            if (lane == 0) {
+                if constexpr (G::q8) raw_sm[2 * h + s] = mine;
+                else if (h) miss_sm[s] = miss;
+                else kmiss_sm[t & 15] = miss;
+                if (!there) mbar_arrive(told);
+                else mbar_arrive_expect_tx(told, G::q8 ? kQ8Half : __popc(there) * piece_rows * D * 2);
             }
+            __syncwarp();
+            if (mine < 0) return;
+            fence_proxy_async_smem();  // the slot's generic accesses, before the copies
+            if constexpr (G::q8) {
+                bulk_g2s(ring[h] + s * kQ8Half, p.pool + (static_cast<int64_t>(mine) * p.kv_heads + g) * kQ8Rec + h * kQ8Half, kQ8Half, told, policy);
+            } else {
+                const int y = ((mine * p.kv_heads + g) * 2 + h) * p.page_tokens + ((t0 + lane * piece_rows) & (p.page_tokens - 1));
+#pragma unroll
+                for (int x = 0; x < D / 64; ++x)
+                    tma_load_hint(ring[h] + s * G::tile + x * TN * 128 + lane * piece_rows * 128, &map, 64 * x, y, told, policy);
+            }
+        };
+        // K goes a tile ahead of V
+        int t = 0, v_page = -1, v_t0 = 0, v_g = 0;
+        for (int item = blockIdx.x; item < total && live; item += gridDim.x) {
+            const Record it = record_of<TN>(p, seq, item, qt);
+            if (k > 1) await(iempty + (k & 1), ((k >> 1) - 1) & 1);
+            if (!live) break;
+            if (lane == 0) {
+                item_sm[k & 1] = it;
+                mbar_arrive(ifull + (k & 1));
+            }
+            ++k;
             int next = it.nt > 0 ? page_of(it, tile_at(it, 0) * TN) : -1;
             for (int i = 0; i < it.nt && live; ++i, ++t) {
                 const int t0 = tile_at(it, i) * TN, mine = next;
                 if (i + 1 < it.nt) next = page_of(it, tile_at(it, i + 1) * TN);
-                const uint32_t there = __ballot_sync(0xffffffffu, mine >= 0), miss = __ballot_sync(0xffffffffu, mine == -2);
-                const int s = t % kSlots, round = t / kSlots;
-                if (round > 0) await(empty + s, (round - 1) & 1);
-                if (!live) break;
-                int pg[kPieces];
-#pragma unroll
-                for (int j = 0; j < kPieces; ++j) pg[j] = __shfl_sync(0xffffffffu, mine, j);
-                if (lane == 0) {
-                    fence_proxy_async_smem();  // the slot's generic accesses, before the copies
-                    if constexpr (G::q8) {
-                        raw_sm[2 * h + s] = mine;
-                        if (mine < 0) {
-                            mbar_arrive(full + s);
-                        } else {
-                            mbar_arrive_expect_tx(full + s, kQ8Half);
-                            bulk_g2s(ring + s * kQ8Half, p.pool + (static_cast<int64_t>(mine) * p.kv_heads + it.g) * kQ8Rec + h * kQ8Half, kQ8Half,
-                                     full + s, policy);
-                        }
-                    } else {
-                        if (h) miss_sm[s] = static_cast<int>(miss);
-                        else kmiss_sm[t & 15] = static_cast<int>(miss);
-                        uint8_t* dst = ring + s * G::tile;
-                        if (!there) mbar_arrive(full + s);
-                        else mbar_arrive_expect_tx(full + s, __popc(there) * piece_rows * D * 2);
-#pragma unroll
-                        for (int j = 0; j < kPieces; ++j) {
-                            if (j * piece_rows >= TN || pg[j] < 0) continue;
-                            const int y = ((pg[j] * p.kv_heads + it.g) * 2 + h) * p.page_tokens + ((t0 + j * piece_rows) & (p.page_tokens - 1));
-#pragma unroll
-                            for (int x = 0; x < D / 64; ++x)
-                                tma_load_hint(dst + x * TN * 128 + j * piece_rows * 128, &map, 64 * x, y, full + s, policy);
-                        }
-                    }
-                }
+                if (t > 0) ask(1, v_g, v_t0, v_page, t - 1);  // (whose slot comes free first)
                 __syncwarp();
+                ask(0, it.g, t0, mine, t);
+                __syncwarp();
+                v_page = mine, v_t0 = t0, v_g = it.g;
             }
         }
+        if (t > 0 && live) ask(1, v_g, v_t0, v_page, t - 1);
+        __syncwarp();
         if (!live && lane == 0) {
             // let every copy still in flight land before the block exits: the last of each slot
             volatile int go_on = 0;
-            for (int i = max(0, t - kSlots); i < t; ++i) mbar_wait_bounded(full + i % kSlots, (i / kSlots) & 1, &go_on, 100000000ull);
+            for (int i = max(0, t - kSlots - 1); i <= t; ++i) {
+                mbar_wait_bounded(G::q8 ? rfull + i % kSlots : kfull + i % G::k_told, (G::q8 ? i / kSlots : i / G::k_told) & 1, &go_on, 100000000ull);
+                mbar_wait_bounded(full[1] + i % kSlots, (i / kSlots) & 1, &go_on, 100000000ull);
+            }
         }
-    } else if (warp == 1) {
-        // ---------------------------------------------------------------- products
+    } else if (warp == 1 || (warp == 3 && NS == 2)) {
+        // ---------------------------------------------------------------- a stream's products
+        // One thread: its waits cost 60 clocks where a warp's with a vote take 100, and tcgen05.commit speaks for the products
+        // of its thread.  It is bound by its own instructions (some 4 clocks each), so both streams have one.
         constexpr uint32_t kType = BF ? (1u << 7) | (1u << 10) : 0u;
         constexpr uint32_t kIdescS = idesc_f16_f32(128, TN) | kType;
         constexpr uint32_t kIdescO = idesc_f16_f32(128, D) | kType | (G::q8 ? 0u : 1u << 16);  // (16-bit pools: V by dims)
-        const uint64_t kd = smem_desc_sw128(smem_u32(sm)), qd = smem_desc_sw128(smem_u32(sm + G::off_q));
-        const uint64_t vd = G::q8 ? smem_desc_sw128(smem_u32(sm + G::off_v)) : desc_mn(smem_u32(sm + G::off_v), TN * 128);
-        // (one thread for all of it: a wait that is over already then costs some 30 clocks instead of 100, and tcgen05.commit
-        // speaks for the products of its thread)
+        constexpr uint32_t kHi = static_cast<uint32_t>(uint64_t{1024 >> 4} | uint64_t{1} << 14 | uint64_t{2} << 29);  // of every descriptor here
+        const int s = warp == 3;
         if (elect_one()) {
             auto wait = [&](uint64_t* b, uint32_t parity) {
-                if (live && !mbar_wait_bounded(b, parity, abort_flag)) {
+                if (!mbar_try_wait(b, parity) && !(live && mbar_wait_bounded(b, parity, abort_flag))) {
                     live = false;
                     *abort_flag = 1;
                 }
             };
-            int t = 0;                 // tiles so far
-            int done[2] = {0, 0};      // products P V of each stream so far
-            int asked[2] = {0, 0};     // scores
-            int pend[2] = {-1, -1};    // the tile whose P V is still to come
-            bool first[2] = {true, true};  // .. and whether it is its item's first
-            int both = 0;              // items of two tiles of queries so far
+            const uint32_t qd = static_cast<uint32_t>(smem_desc_sw128(smem_u32(sm + G::off_q + (p.decode ? 0 : s * G::q_tile))));
+            const uint32_t kd = static_cast<uint32_t>(smem_desc_sw128(smem_u32(sm)));
+            const uint32_t vd = static_cast<uint32_t>(G::q8 ? smem_desc_sw128(smem_u32(sm + G::off_v)) : desc_mn(smem_u32(sm + G::off_v), TN * 128));
+            const uint32_t col = tmem + s * 2 * kHalf, o = tmem + G::col_o + s * D;
+            uint64_t *sf = sfull + 2 * s, *pf = pfull + 2 * s;
+            const bool shares = NS == 2 && !p.decode;  // both streams see every tile
+            int t = 0, n = 0, m = 0;  // tiles so far; of this stream: scores asked for, and P V
+            int pend = -1;            // the tile whose P V is still to come
+            uint32_t acc = 0;
             // Products of one thread run in the order in which they are asked for: S may go over a P whose product has been.
-            // P V of a half of stream s's tile; its first use of V waits for it, the last gives V's slot back.
-            auto product_o = [&](int s, int half, bool wait_v, bool last) {
-                const int n = done[s], x = 2 * s + (n & 1), vs = pend[s] % G::v_slots;
-                wait(pfull + x, (n >> 1) & 1);
-                if (wait_v) wait(vready + vs, (pend[s] / G::v_slots) & 1);
-                if (!live) return;
-                tc_fence_after();
-                const uint32_t a = tmem + x * kHalf, o = tmem + G::col_o + s * D;
-                const uint32_t acc = !first[s] || accum_sm[s] != 0;
-                const uint64_t b0 = vd + (vs * G::tile >> 4) + half * (kHalf * 128 >> 4);
+            auto product_pv = [&] {
+                const int vs = pend % G::v_slots;
+                const uint32_t b0 = vd + (vs * G::tile >> 4);
+                wait(vready + pend % G::v_told, (pend / G::v_told) & 1);
 #pragma unroll
-                for (int part = 0; part < (G::q8 ? 2 : 1); ++part)
+                for (int half = 0; half < G::H; ++half) {
+                    const int x = G::halves ? half : m & 1;
+                    wait(pf + x, (G::halves ? m : m >> 1) & 1);
+                    if (!live) return;
+                    tc_fence_after();
+                    if (!acc) acc = accum_sm[s] != 0;
+                    const uint32_t a = col + x * kHalf;
 #pragma unroll
-                    for (int ks = 0; ks < kHalf / 16; ++ks)
-                        tc_mma_f16_ts(o, a + 8 * ks, b0 + (G::q8 ? (part * G::part + ks * 32) >> 4 : ks * (2048 >> 4)), kIdescO, part + ks ? 1 : acc);
-                if (!G::halves || half == 0) tc_commit(odone + s);
-                if (last) tc_commit(vempty + vs);
-                first[s] = false;
-                ++done[s];
+                    for (int part = 0; part < (G::q8 ? 2 : 1); ++part)
+#pragma unroll
+                        for (int ks = 0; ks < kHalf / 16; ++ks) {
+                            mma_ts(o, a + 8 * ks, b0 + ((G::q8 ? part * G::part + ks * 32 : half * kHalf * 128 + ks * 2048) >> 4), kHi, kIdescO, acc);
+                            acc = 1;
+                        }
+                }
+                tc_commit(vempty + vs);
+                if (!G::halves) tc_commit(odone + s);
+                ++m;
+                pend = -1;
             };
-            // .. of its whole tile
-            auto product_pv = [&](int s, bool wait_v, bool last) {
-                product_o(s, 0, wait_v, !G::halves && last);
-                if (G::halves && live) product_o(s, 1, false, last);
-                pend[s] = -1;
-            };
-            auto product_s = [&](int s, int ksl, int qs, bool last) {
-                const int x = G::halves ? 2 * s : 2 * s + (asked[s] & 1);
-                const uint64_t aq = qd + (qs * G::q_tile >> 4), bk = kd + (ksl * G::tile >> 4);
+            auto product_s = [&] {
+                const int ksl = t % G::k_slots, x = G::halves ? 0 : n & 1;
+                const uint32_t bk = kd + (ksl * G::tile >> 4);
 #pragma unroll
                 for (int part = 0; part < (G::q8 ? 2 : 1); ++part)
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks)
-                        tc_mma_f16_ss(tmem + x * kHalf, aq + (((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4),
-                                      bk + ((part * G::part + (ks >> 2) * (TN * 128) + (ks & 3) * 32) >> 4), kIdescS, part + ks > 0);
-                tc_commit(sfull + x);
-                if (last) tc_commit(kempty + ksl);
-                ++asked[s];
+                        mma_ss(col + x * kHalf, qd + (((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4), kHi,
+                               bk + ((part * G::part + (ks >> 2) * (TN * 128) + (ks & 3) * 32) >> 4), kHi, kIdescS, part + ks > 0);
+                tc_commit(sf + x);
+                tc_commit(kempty + ksl);
+                ++n;
             };
+            int both = 0;  // items of this stream's so far
             for (int item = blockIdx.x; item < total && live; item += gridDim.x, ++k) {
                 wait(ifull + (k & 1), (k >> 1) & 1);
                 if (!live) break;
                 const Record it = item_sm[k & 1];
                 mbar_arrive(iempty + (k & 1));
-                wait(qfull, k & 1);
-                const bool two = NS == 2 && !p.decode && it.nq - it.q0 > 128;
-                if (two) wait(qfull + 1, both++ & 1);
-                bool begun[2] = {false, false};
-                for (int i = 0; i < it.nt && live; ++i, ++t) {
-                    const int ksl = t % G::k_slots;
-                    wait(kfull + ksl, (t / G::k_slots) & 1);
+                const int nt = it.nt;
+                if (shares && s == 1 && it.nq - it.q0 <= 128) {  // no queries for this stream: the slots go back without it
+                    for (int i = 0; i < nt && live; ++i, ++t) {
+                        wait(kfull + t % G::k_told, (t / G::k_told) & 1);
+                        wait(vready + t % G::v_told, (t / G::v_told) & 1);
+                        if (!live) break;
+                        mbar_arrive(kempty + t % G::k_slots);
+                        mbar_arrive(vempty + t % G::v_slots);
+                    }
+                    continue;
+                }
+                // (decode steps: the first stream's queries are the second's as well)
+                wait(qfull + (p.decode ? 0 : s), (p.decode ? k : both) & 1);
+                ++both;
+                bool begun = false;
+                for (int i = 0; i < nt && live; ++i, ++t) {
+                    if (NS == 2 && p.decode && (tile_at(it, i) & 1) != s) continue;
+                    if (G::halves && pend >= 0) product_pv();
+                    wait(kfull + t % G::k_told, (t / G::k_told) & 1);
                     if (!live) break;
                     tc_fence_after();
-                    // the streams that this tile is for.  One buffer of scores: the product of its tile before, then its
-                    // scores; two: all scores first
-                    const int from = NS == 2 && p.decode ? tile_at(it, i) & 1 : 0, to = two ? 1 : from;
-                    if (!G::halves) {
-#pragma unroll
-                        for (int s = 0; s < NS; ++s)
-                            if (s >= from && s <= to) product_s(s, ksl, p.decode ? 0 : s, s == to);
-                    }
-#pragma unroll
-                    for (int s = 0; s < NS; ++s)
-                        if (live && s >= from && s <= to) {
-                            // (V's slots come free in the tiles' order)
-                            if (NS == 2 && p.decode && pend[1 - s] >= 0 && pend[1 - s] < pend[s]) product_pv(1 - s, true, true);
-                            if (pend[s] >= 0 && live) product_pv(s, s == from, s == to);
-                            if (G::halves && live) product_s(s, ksl, p.decode ? 0 : s, s == to);
-                            pend[s] = t, first[s] = !begun[s], begun[s] = true;
-                        }
+                    product_s();
+                    if (!G::halves && pend >= 0) product_pv();
+                    if (!begun) acc = 0;
+                    pend = t;
+                    begun = true;
                 }
-                // what is left, in the tiles' order
-                if (NS == 2 && p.decode && pend[1] >= 0 && pend[1] < pend[0] && live) product_pv(1, true, true);
-#pragma unroll
-                for (int s = 0; s < NS; ++s) {
-                    if (pend[s] >= 0 && live) product_pv(s, s == 0 || p.decode, p.decode || s == (two ? 1 : 0));
-                    if (begun[s] && live) tc_commit(ofin + s);
-                }
+                if (pend >= 0 && live) product_pv();
+                if (begun && live) tc_commit(ofin + s);
             }
             // every product issued has finished before the tensor memory is released
-            tc_commit(drained);
+            tc_commit(drained + s);
             volatile int go_on = 0;
-            mbar_wait_bounded(drained, 0, &go_on, 10000000000ull);
+            mbar_wait_bounded(drained + s, 0, &go_on, 10000000000ull);
         }
         __syncwarp();
-    } else if (warp == 3 && !G::q8) {
+    } else if (warp == 2 && !G::q8) {
         // ---------------------------------------------------------------- V's rows that must not count
         // Slots that nobody sees hold anything (and so do those of missing pages): zero.  One that some rows see
         // and whose V is not finite is marked, to be added query by query, and zero in the product.
@@ -698,11 +714,10 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                 await(vfull + vs, (t / G::v_slots) & 1);
                 if (!live) break;
                 const int miss = miss_sm[vs];
-                bool some = false;
+                bool some = miss != 0;
+                for (int half = 0; half < G::H; ++half) some = some || edge(it, t0 + half * kHalf);
 #pragma unroll 1
-                for (int half = 0; half < TN / kHalf; ++half) {
-                    if (!(miss || edge(it, t0 + half * kHalf))) continue;
-                    some = true;
+                for (int half = 0; some && half < G::H; ++half) {
                     uint8_t* vt = sm + G::off_v + vs * G::tile;
 #pragma unroll 1
                     for (int j = 0; j < 2; ++j) {
@@ -727,7 +742,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                                     *reinterpret_cast<uint4*>(vt + x * TN * 128 + row * 128 + 16 * ((c + lane) & 7)) = make_uint4(0, 0, 0, 0);
                         }
                         const uint32_t word = __ballot_sync(0xffffffffu, odd);
-                        if (lane == 0) odd_sm[t % G::info_slots * 4 + 2 * half + j] = word;
+                        if (lane == 0) odd_sm[t % G::v_told * 4 + 2 * half + j] = word;
                     }
                 }
                 if (some) {
@@ -735,8 +750,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                 }
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(vready + vs);
-                    mbar_arrive(vinfo + t % G::info_slots);
+                    mbar_arrive(vready + t % G::v_told);
                 }
             }
         }
@@ -789,56 +803,55 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
             }
             float l = 0.f, lim = -INFINITY, base = 0.f;  // sum, reference and slack, what comes off the scores
             bool fresh = true;                           // O holds nothing yet
-            for (int ih = 0; ih < it.nt * (TN / kHalf); ++ih) {
-                const int i = G::halves ? ih >> 1 : ih, half = G::halves ? ih & 1 : 0;
-                const int tile = tile_at(it, i), t0 = tile * TN + half * kHalf, tv = tiles0 + i;
+            for (int i = 0; i < it.nt; ++i) {
+                const int tile = tile_at(it, i), t0 = tile * TN, tv = tiles0 + i;
                 if (NS == 2 && p.decode && (tile & 1) != s) continue;
-                const int x = 2 * s + (n & 1);
+                const int x = G::halves ? 2 * s : 2 * s + (n & 1);
                 const uint32_t scol = lanes + x * kHalf;
-                if (half == 0) await(sfull + (G::halves ? 2 * s : x), (n >> 1) & 1);
+                await(sfull + x, (G::halves ? n : n >> 1) & 1);
                 if (!live) break;
                 if (idle) {  // (its rows of P hold anything: nobody reads what comes of them)
                     fresh = false;
                     ++n;
-                    if (lane == 0) mbar_arrive(pfull + x);
+                    if (lane < G::H) mbar_arrive(pfull + x + lane);
                     continue;
                 }
                 tc_fence_after();
-                const bool some = edge(it, t0);
-                const int vi = tv % G::info_slots;
-                if (some) {  // which tokens' V is not finite (four tiles before, that barrier's last phase is over for sure)
-                    await(vinfo + vi, (tv / G::info_slots) & 1);
+                const bool some = edge(it, t0) || (G::halves && edge(it, t0 + kHalf));
+                const int vi = tv % G::v_told;
+                if (some) {  // which tokens' V is not finite
+                    await(vready + vi, (tv / G::v_told) & 1);
                     if (!live) break;
                 }
-                float v[kHalf];
-                tmem_ld32(scol, v);
-                tmem_ld32(scol + 32, v + 32);
-                const int miss = kmiss_sm[tv & 15] >> (half * kHalf >> piece_shift);
+                float v[TN];
+#pragma unroll
+                for (int c = 0; c < TN; c += 32) tmem_ld32(scol + c, v + c);
+                const int miss = kmiss_sm[tv & 15];
                 tc_wait_ld();
                 if (some || miss) {
                     // the tokens that the row sees, as bits; a missing piece is 16 tokens at least
-                    auto below = [](int j) { return j <= 0 ? uint64_t{0} : j >= 64 ? ~uint64_t{0} : (uint64_t{1} << j) - 1; };
-                    uint64_t sees = below(len - t0) & (~below(from - t0) | below(first - t0));
-                    if (miss) {
+                    auto below = [](int j) { return j <= 0 ? 0u : j >= 32 ? ~0u : (1u << j) - 1; };
 #pragma unroll
-                        for (int c = 0; c < kHalf; c += 16)
-                            if ((miss >> (c >> piece_shift)) & 1) sees &= ~(uint64_t{0xFFFF} << c);
-                    }
-                    const uint32_t low = static_cast<uint32_t>(sees), high = static_cast<uint32_t>(sees >> 32);
+                    for (int c = 0; c < TN; c += 32) {
+                        uint32_t sees = below(len - t0 - c) & (~below(from - t0 - c) | below(first - t0 - c));
+                        if ((miss >> (c >> piece_shift)) & 1) sees &= 0xFFFF0000u;
+                        if ((miss >> ((c + 16) >> piece_shift)) & 1) sees &= 0xFFFFu;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        if (!(low & (1u << j))) v[j] = -INFINITY;
-                        if (!(high & (1u << j))) v[j + 32] = -INFINITY;
+                        for (int j = 0; j < 32; ++j)
+                            if (!(sees & (1u << j))) v[c + j] = -INFINITY;
                     }
                 }
-                float m4[4];
+                float m8[8];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) m4[j] = fmaxf(v[j], v[j + 4]);
+                for (int j = 0; j < 8; ++j) m8[j] = fmaxf(v[j], fmaxf(v[j + 8], v[j + 16]));
 #pragma unroll
-                for (int j = 8; j < kHalf; j += 8)
+                for (int j = 24; j < TN - 8; j += 16)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) m4[i] = fmaxf(m4[i], fmaxf(v[j + i], v[j + i + 4]));
-                const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.c2;  // (a NaN is no maximum)
+                    for (int i = 0; i < 8; ++i) m8[i] = fmaxf(m8[i], fmaxf(v[j + i], v[j + i + 8]));
+#pragma unroll
+                for (int j = 0; j < 8; ++j) m8[j] = fmaxf(m8[j], v[TN - 8 + j]);
+                // (a NaN is no maximum)
+                const float m = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * p.c2;
                 const bool passed = m > lim;
                 if (__any_sync(0xffffffffu, passed)) {
                     float alpha = 1.f;
@@ -851,8 +864,9 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                         l *= alpha;
                     }
                     if (!fresh) {
-                        // (the product of the half before; earlier ones were over before these scores were asked for)
-                        if (!G::halves || half == 1) await(odone + s, G::halves ? (n >> 1) & 1 : (n - 1) & 1);
+                        // (one buffer of scores: they were asked for after the last product.  Two: the last product may be under way,
+                        // the one before was over before these scores were asked for)
+                        if (!G::halves) await(odone + s, (n - 1) & 1);
                         if (!live) break;
                         tc_fence_after();
 #pragma unroll 1
@@ -866,10 +880,17 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                         }
                     }
                 }
+                // tokens whose V is not finite
+                uint32_t odd = 0;
+                if (some) {
+#pragma unroll
+                    for (int j = 0; j < 2 * G::H; ++j) odd |= odd_sm[vi * 4 + j];
+                }
+                if (fresh && me == 0) accum_sm[s] = odd != 0;
                 uint64_t sum[2] = {0, 0};  // pairs of fp32
                 const uint64_t c2 = pair(p.c2, p.c2), off = pair(-base, -base);
 #pragma unroll
-                for (int c = 0; c < kHalf; c += 32) {
+                for (int c = 0; c < TN; c += 32) {
                     uint32_t w[16];
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
@@ -879,27 +900,35 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                         sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], pair(a, b));
                         w[j / 2] = pack2<BF>(a, b);
                     }
-                    tmem_st16(scol + c / 2, w);
+                    tmem_st16(scol + (c / kHalf) * kHalf + c % kHalf / 2, w);
+                    if (G::halves && c == 32 && !odd) {  // the first half is out
+                        tc_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(pfull + x);
+                    }
                 }
                 float s0, s1;
                 unpair(add2(sum[0], sum[1]), s0, s1);
                 l += s0 + s1;
                 tc_wait_st();
-                // ---- tokens whose V is not finite, to those that see them
-                uint32_t odd = 0;
-                if (some) odd = odd_sm[vi * 4 + 2 * half] | odd_sm[vi * 4 + 2 * half + 1];
-                if (odd) {
-                    if (!fresh && (!G::halves || half == 1)) await(odone + s, G::halves ? (n >> 1) & 1 : (n - 1) & 1);
+                if (odd) {  // to those that see them
+                    if (!fresh && !G::halves) await(odone + s, (n - 1) & 1);
                     if (!live) break;
                     tc_fence_after();
-                    add_odd<FMT, D>(p, it.a, it.g, t0, const_cast<const uint32_t*>(odd_sm) + vi * 4 + 2 * half, ocol, scol, len, from, first, fresh);
+#pragma unroll 1
+                    for (int half = 0; half < G::H; ++half)
+                        add_odd<FMT, D>(p, it.a, it.g, t0 + half * kHalf, const_cast<const uint32_t*>(odd_sm) + vi * 4 + 2 * half, ocol, scol + half * kHalf, len,
+                                        from, first, fresh && half == 0);
                 }
-                if (fresh && me == 0) accum_sm[s] = odd != 0;
                 fresh = false;
                 ++n;
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(pfull + x);
+                if (lane == 0) {
+                    if (G::halves && odd) mbar_arrive(pfull + x);
+                    mbar_arrive(pfull + x + G::H - 1);
+                }
             }
             if (!live) break;
             // (the item's last product; odone may be two phases behind here)
@@ -1056,7 +1085,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(kfull + ks);
+            if (lane == 0) mbar_arrive(kfull + t % G::k_told);
         };
         auto convert_v = [&](const Record& it, int t0, int t) {  // a dim per thread
             const int vs = t % G::v_slots, rs = t % G::raw_slots;
@@ -1067,7 +1096,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
             const uint8_t* b = sm + G::off_raw + (G::raw_slots + rs) * kQ8Half;
             const uint8_t* scales = b + 8192 + w4 * 128;
             if (pg < 0 || edge(it, t0)) {
-                // Scales of 0 for tokens that must not count, as warp 3 zeroes rows of 16-bit pools (what is not finite
+                // Scales of 0 for tokens that must not count, as warp 2 zeroes rows of 16-bit pools (what is not finite
                 // is a scale, or too large for fp16).  A warp's dims are one block of scales.
                 uint32_t mine = 0;
 #pragma unroll
@@ -1080,7 +1109,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                         for (int c = 0; c < 4; ++c) odd |= (*reinterpret_cast<const uint16_t*>(b + 8192 + c * 128 + 4 * lane + 2 * j) & 0x7FFFu) >= (24u << 10);  // 512
                     }
                     const uint32_t who = __ballot_sync(0xffffffffu, odd);
-                    if (w4 == 0 && lane == 0) odd_sm[t % G::info_slots * 4 + j] = who;
+                    if (w4 == 0 && lane == 0) odd_sm[t % G::v_told * 4 + j] = who;
                     if (!none && !odd) mine |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(scales + 4 * lane + 2 * j)) << (16 * j);
                 }
                 *reinterpret_cast<uint32_t*>(dv + 4 * lane) = mine;
@@ -1114,8 +1143,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(vready + vs);
-                mbar_arrive(vinfo + t % G::info_slots);
+                mbar_arrive(vready + t % G::v_told);
                 mbar_arrive(rempty + G::raw_slots + rs);
             }
         };
