@@ -168,7 +168,7 @@ __device__ __forceinline__ uint64_t l2_policy_evict_last() {
         c((v)[10]), c((v)[11]), c((v)[12]), c((v)[13]), c((v)[14]), c((v)[15]), c((v)[16]), c((v)[17]), c((v)[18]),       \
         c((v)[19]), c((v)[20]), c((v)[21]), c((v)[22]), c((v)[23]), c((v)[24]), c((v)[25]), c((v)[26]), c((v)[27]),       \
         c((v)[28]), c((v)[29]), c((v)[30]), c((v)[31])
-// 32 consecutive columns of the thread's tensor memory lane (loads: to be waited for with tc_wait_ld).
+// 32 consecutive columns of the thread's tensor memory lane (to be waited for with tc_wait_ld).
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
 #define QMM_OUT(x) "=f"(x)
     asm volatile(
@@ -179,24 +179,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
         : "memory");
 #undef QMM_OUT
 }
-#define QMM_IN(x) "r"(x)
-#define QMM_INF(x) "f"(x)
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-        QMM_R32(v, QMM_IN)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_st32f(uint32_t taddr, const float* v) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-        QMM_R32(v, QMM_INF)
-        : "memory");
-}
-#undef QMM_IN
-#undef QMM_INF
 #undef QMM_R32
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
     uint32_t v;
@@ -765,22 +747,31 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
         int n = 0;      // the stream's
         int merges = 0, fins = 0;
         for (int item = blockIdx.x; item < total && live; item += gridDim.x) {
-            const Record it = next_record();
+            // (the record stays until the item's end, where what the loop has no registers for is read again)
+            await(ifull + (k & 1), (k >> 1) & 1);
             if (!live) break;
+            const Record it = item_sm[k & 1];
+            auto release = [&] {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(iempty + (k & 1));
+                ++k;
+            };
             const int tiles0 = tiles;
             tiles += it.nt;
             const int c0 = it.q0 + (NS == 2 && !p.decode ? 128 * s : 0), q = c0 + me;
-            if (NS == 2 && !p.decode && s == 1 && c0 >= it.nq) continue;  // (the item has one tile of queries)
-            const bool valid = q < it.nq;
+            if (NS == 2 && !p.decode && s == 1 && c0 >= it.nq) {  // the item has one tile of queries
+                release();
+                continue;
+            }
             const bool idle = c0 + 32 * (warp & 3) >= it.nq;  // no query of the warp's
-            const int r = it.r0 + (valid ? q / p.group : 0), h = it.g * p.group + (valid ? q % p.group : 0);
-            const int len = valid ? length_of(p, r) : 0, from = max(0, len - p.window), first = min(p.sinks, len);
-            const int64_t at = static_cast<int64_t>(r) * p.heads + h;  // (row, head)
+            auto row_of = [&](int q) { return it.r0 + (q < it.nq ? q / p.group : 0); };
+            auto head_of = [&](int q) { return it.g * p.group + (q < it.nq ? q % p.group : 0); };
+            const int len = q < it.nq ? length_of(p, row_of(q)) : 0, from = max(0, len - p.window), first = min(p.sinks, len);
             if (s == 0 || !p.decode) {  // the queries, swizzled as the copies do: D / 8 lanes a row
                 constexpr int L = D / 8 < 32 ? D / 8 : 32, R = 32 / L;  // lanes of a row, rows at once
                 const int c = lane % L;
                 uint8_t* dst = sm + G::off_q + s * G::q_tile + (c >> 3) * (128 * 128);
-                const int64_t src = r * p.q_stride + static_cast<int64_t>(h) * D;
+                const int64_t src = row_of(q) * p.q_stride + static_cast<int64_t>(head_of(q)) * D;
 #pragma unroll
                 for (int i0 = 0; i0 < 32; i0 += 8 * R) {
                     uint4 v[8];
@@ -870,13 +861,13 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                         if (!live) break;
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            float o[32];
-                            tmem_ld32(ocol + c, o);
+                        for (int c = 0; c < D; c += 16) {  // (rare, and the scores hold most registers)
+                            uint32_t o[16];
+                            tmem_ld16(ocol + c, o);
                             tc_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) o[j] *= alpha;
-                            tmem_st32f(ocol + c, o);
+                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                            tmem_st16(ocol + c, o);
                         }
                     }
                 }
@@ -959,6 +950,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(mfull);
                     ++merges;
+                    release();
                     continue;
                 }
                 if (lane == 0) mbar_arrive(mfree);
@@ -973,13 +965,23 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                 l = l * w0 + other.y * w1;
                 base = top;
             }
-            if (idle) continue;
+            if (idle) {
+                release();
+                continue;
+            }
+            const volatile Record& rec = item_sm[k & 1];
+            const int query = rec.q0 + (NS == 2 && !p.decode ? 128 * s : 0) + me, item_chunk = rec.chunk;
+            const bool valid = query < rec.nq;
+            const int row = rec.r0 + (valid ? query / p.group : 0), head = rec.g * p.group + (valid ? query % p.group : 0);
+            const int len2 = valid ? length_of(p, row) : 0;
+            const int64_t at = static_cast<int64_t>(row) * p.heads + head;
+            release();
             int slot = 0;
             bool write = valid;
             if (p.chunk && valid) {
-                const Chunks c = chunks_of(p, len);
-                slot = it.chunk < c.first ? it.chunk : c.first + it.chunk - c.from;
-                write = it.chunk < c.first || (it.chunk >= c.from && it.chunk < c.end);
+                const Chunks c = chunks_of(p, len2);
+                slot = item_chunk < c.first ? item_chunk : c.first + item_chunk - c.from;
+                write = item_chunk < c.first || (item_chunk >= c.from && item_chunk < c.end);
             }
             const bool none = l == 0.f, merge = NS == 2 && p.decode;
             const float inv = none ? 0.f : p.chunk ? w0 : w0 / l, inv1 = none ? 0.f : p.chunk ? w1 : w1 / l;
