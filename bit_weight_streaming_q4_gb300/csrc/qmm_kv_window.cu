@@ -125,7 +125,7 @@ qmm_status make_map(const qmm_kv_dims& d, const void* pool, CUtensorMap* map) {
     if (rows > INT32_MAX) return QMM_ERR_UNSUPPORTED_SHAPE;
     const PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
     if (!enc) return QMM_ERR_CUDA;
-    const int tile = d.head_dim == 256 ? 64 : 128;
+    const int tile = 64;
     const cuuint64_t size[2] = {static_cast<cuuint64_t>(d.head_dim), static_cast<cuuint64_t>(rows)};
     const cuuint64_t stride[1] = {static_cast<cuuint64_t>(d.head_dim) * 2};
     const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(tile < d.page_tokens ? tile : d.page_tokens)};

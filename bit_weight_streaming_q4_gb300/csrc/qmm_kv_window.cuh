@@ -14,16 +14,16 @@
 //     meet at the end through shared memory.
 // Either way two streams take turns on the tensor cores (one at head dimension 256, for which tensor memory has no more
 // room): one's products run while the other's scores become probabilities.  16-bit pools at head dimensions 64 and 128
-// have tiles of 128 tokens (a product of 64 columns of scores takes as long: it reads as much of Q), whose
-// probabilities go out in two halves, so that the first half's P V runs under the second's exponentials.  Otherwise
-// tiles have 64 tokens, and scores have two buffers: the next tile's are there when the softmax is done with one.
+// have tiles of 128 tokens (a product of 64 columns of scores takes as long: it reads as much of Q), whose halves two
+// groups of softmax warps take; they share a query's reference, by a vote per tile.  Otherwise tiles have 64 tokens, and
+// scores have two buffers: the next tile's are there when the softmax is done with one.
 // The tiles of an item are those that some of its rows sees: the first ones (sinks), and the window's.  Where few
 // items would leave SMs idle, tokens are cut into chunks at fixed places of a sequence, an item each, whose unnormalised
 // outputs a second kernel joins.  All choices are made by the plan's dims, so a row's bits do not depend on its company.
 //   warp 0      forms the items' records; asks for K and V tiles (q8_0: as they are stored)
 //   warps 1, 3  one thread each issues a stream's products
 //   warp 2      16-bit pools: zeroes the rows of V that must not count, where some are
-//   warps 4 ..  softmax, four a stream
+//   warps 4 ..  softmax, four or eight a stream
 //   q8_0: four more convert K (half a token a thread) and V (a dim a thread) to two fp16 parts whose sum is quant
 //               times scale
 // A query's reference is its first tile's maximum and moves only when a score passes it by more than 2^kSlack; each
@@ -42,7 +42,7 @@ using namespace qmm::kv;
 
 constexpr float kShift = 9.f;       // p's power of two ..
 constexpr float kSlack = 6.f;       // .. and how far a score may pass its reference: p <= 2^15
-constexpr int kHalf = 64;          // tokens whose probabilities go out at a time
+constexpr int kHalf = 64;          // tokens that a softmax thread takes
 constexpr float kFine = 4194304.f;  // 2^22: a larger reference stands alone (fp32's spacing would swallow the two): p <= 1
 
 struct Params {
@@ -76,18 +76,18 @@ template <int FMT, int D>
 struct Geo {
     static constexpr bool q8 = FMT == QMM_KV_Q8_0;
     static constexpr int streams = D == 256 ? 1 : 2;
-    static constexpr bool halves = !q8 && D <= 128;              // tiles of two halves, one buffer of scores per stream
+    static constexpr bool halves = false;              // tiles of two halves, a group of warps each; one buffer of scores per stream
     static constexpr int H = halves ? 2 : 1, TN = H * kHalf;     // tokens of a tile
     static constexpr int part = TN * D * 2;                      // bytes of a tile's K or V in 16 bits
     static constexpr int tile = q8 ? 2 * part : part;            // q8_0: high and low parts
-    static constexpr int k_slots = D == 64 ? 4 : 2, v_slots = q8 ? 1 : k_slots;
+    static constexpr int k_slots = D <= 128 && !q8 ? 4 : 2, v_slots = q8 ? 1 : k_slots;
     // Barriers that say that a tile's K or V is there: more of them than slots, since a stream of a decode step waits only for
     // tiles of its own, at most three apart.  Then a barrier's phase before the one waited for is over for sure: V's come
     // in order, and the last own tile's K was asked for after the K of eight tiles before had been used.
     static constexpr int k_told = 8, v_told = 4;
     static constexpr int raw_slots = q8 ? 2 : 0;                 // pages on their way, K and V
     static constexpr int q_tile = 128 * D * 2;
-    static constexpr int soft_warps = 4 * streams, conv_warps = q8 ? 4 : 0;
+    static constexpr int soft_warps = 4 * H * streams, conv_warps = q8 ? 4 : 0;
     static constexpr int threads = 32 * (4 + soft_warps + conv_warps);
     // tensor memory: S (128 columns per stream, two halves or two buffers), P over it, and O
     static constexpr int col_o = 256;
@@ -96,7 +96,8 @@ struct Geo {
     static constexpr int off_q = off_v + v_slots * tile;
     static constexpr int off_raw = off_q + streams * q_tile;     // K's pages, then V's
     static constexpr int off_ml = off_raw + 2 * raw_slots * kQ8Half;  // [128] reference and sum of the second stream
-    static constexpr int off_item = off_ml + 128 * 8;            // [2] of Record
+    static constexpr int off_red = off_ml + 128 * 8;             // [stream][half][128] maxima, and sums
+    static constexpr int off_item = off_red + (halves ? 2048 : 0);  // [2] of Record
     static constexpr int off_dv = off_item + 2 * 64;             // q8_0: V's scales, zero where a token must not count: [4][64] fp16
     static constexpr int off_bar = off_dv + (q8 ? 512 : 0);
     static constexpr int bars = k_told + k_slots + 2 * v_slots + v_told + 4 * raw_slots + 2 + 4 + 4 + 2 + 2 + 2 + 2 + 4;
@@ -202,6 +203,18 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
+}
+
+// 32 bytes at once, at any 16-byte boundary.
+__device__ __forceinline__ void store32(void* p, bool whole, const uint32_t* w) {
+    if (whole) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+                     "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
 }
 
 template <bool BF>
@@ -372,10 +385,10 @@ __device__ __forceinline__ Record record_of(const Params& p, const int4* seq, in
 // take it, V from memory.  (Rare; a function of its own costs the loop around it no registers.)
 template <int FMT, int D>
 __device__ __noinline__ void add_odd(const Params& p, int a, int g, int t0, const uint32_t* odd, uint32_t ocol, uint32_t pcol, int len,
-                                     int from, int first, bool fresh) {
+                                     int from, int first, bool fresh, int c_from, int c_to) {
     constexpr bool BF = FMT == QMM_KV_BF16;
 #pragma unroll 1
-    for (int c = 0; c < D; c += 8) {
+    for (int c = c_from; c < c_to; c += 8) {
         uint32_t o[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) o[j] = fresh ? 0u : tmem_ld1(ocol + c + j);
@@ -414,11 +427,12 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
     attend_window_tc(const __grid_constant__ CUtensorMap map, const __grid_constant__ Params p) {
     using G = Geo<FMT, D>;
     constexpr bool BF = FMT == QMM_KV_BF16;
-    constexpr int TN = G::TN, NS = G::streams;
+    constexpr int TN = G::TN, NS = G::streams, kP = G::halves ? 32 : 0;  // (P's columns over S's)
     extern __shared__ uint8_t sm_raw[];
     griddep_launch_dependents();  // the joining kernel waits for this grid's end before it reads
     uint8_t* sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
     float2* ml_sm = reinterpret_cast<float2*>(sm + G::off_ml);
+    float* red_sm = reinterpret_cast<float*>(sm + G::off_red);
     Record* item_sm = reinterpret_cast<Record*>(sm + G::off_item);
     uint64_t* kfull = reinterpret_cast<uint64_t*>(sm + G::off_bar);
     uint64_t *kempty = kfull + G::k_told, *vfull = kempty + G::k_slots, *vempty = vfull + G::v_slots, *vready = vempty + G::v_slots;
@@ -444,16 +458,16 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
         for (int i = 0; i < G::k_slots; ++i) mbar_init(kempty + i, users);
         for (int i = 0; i < G::v_slots; ++i) mbar_init(vfull + i, 1), mbar_init(vempty + i, users);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(qfull + i, 4);
+            mbar_init(qfull + i, 4 * G::H);
             mbar_init(odone + i, 1);
             mbar_init(ofin + i, 1);
             mbar_init(ifull + i, 1);
             mbar_init(iempty + i, NS + (G::q8 ? G::conv_warps : 1) + G::soft_warps);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(sfull + i, 1), mbar_init(pfull + i, 4);
+        for (int i = 0; i < 4; ++i) mbar_init(sfull + i, 1), mbar_init(pfull + i, 4 * G::H);
         for (int i = 0; i < 2 * G::raw_slots; ++i) mbar_init(rfull + i, 1), mbar_init(rempty + i, 4);
-        mbar_init(mfree, 4);
-        mbar_init(mfull, 4);
+        mbar_init(mfree, 4 * G::H);
+        mbar_init(mfull, 4 * G::H);
         mbar_init(drained, 1);
         mbar_init(drained + 1, 1);
         *abort_flag = 0;
@@ -507,7 +521,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
     };
 
     // Registers go where the scores are (the shares add up to what the block was launched with, or less:
-    // 256 * 200 + 128 * 104 = 384 * 168; q8_0 256 * 168 + 256 * 80 <= 512 * 128).
+    // 512 * 104 + 128 * 64 = 640 * 96; q8_0 256 * 168 + 256 * 80 <= 512 * 128).
     if (warp < 4) {
     if constexpr (NS == 2) setmaxnreg_dec<G::q8 ? 80 : 104>();
     if (warp == 0) {
@@ -608,22 +622,18 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                 const int vs = pend % G::v_slots;
                 const uint32_t b0 = vd + (vs * G::tile >> 4);
                 wait(vready + pend % G::v_told, (pend / G::v_told) & 1);
+                const int x = G::halves ? 0 : m & 1;
+                wait(pf + x, (G::halves ? m : m >> 1) & 1);
+                if (!live) return;
+                tc_fence_after();
+                if (!acc) acc = accum_sm[s] != 0;
 #pragma unroll
-                for (int half = 0; half < G::H; ++half) {
-                    const int x = G::halves ? half : m & 1;
-                    wait(pf + x, (G::halves ? m : m >> 1) & 1);
-                    if (!live) return;
-                    tc_fence_after();
-                    if (!acc) acc = accum_sm[s] != 0;
-                    const uint32_t a = col + x * kHalf;
+                for (int part = 0; part < (G::q8 ? 2 : 1); ++part)
 #pragma unroll
-                    for (int part = 0; part < (G::q8 ? 2 : 1); ++part)
-#pragma unroll
-                        for (int ks = 0; ks < kHalf / 16; ++ks) {
-                            mma_ts(o, a + 8 * ks, b0 + ((G::q8 ? part * G::part + ks * 32 : half * kHalf * 128 + ks * 2048) >> 4), kHi, kIdescO, acc);
-                            acc = 1;
-                        }
-                }
+                    for (int ks = 0; ks < TN / 16; ++ks) {
+                        mma_ts(o, col + kP + x * kHalf + (ks >> 2) * kHalf + 8 * (ks & 3), b0 + ((G::q8 ? part * G::part + ks * 32 : ks * 2048) >> 4), kHi, kIdescO, acc);
+                        acc = 1;
+                    }
                 tc_commit(vempty + vs);
                 if (!G::halves) tc_commit(odone + s);
                 ++m;
@@ -739,50 +749,61 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
     }
     } else if (warp < 4 + G::soft_warps) {
         if constexpr (NS == 2) setmaxnreg_inc<G::q8 ? 168 : 200>();
-        // ---------------------------------------------------------------- softmax: a query per thread
-        const int s = (warp - 4) >> 2, me = tid & 127;
+        // ---------------------------------------------------------------- softmax: a query per thread (two, of half a tile's tokens each)
+        const int sw = warp - 4, s = sw / (4 * G::H), half = G::H == 2 ? (sw >> 2) & 1 : 0, me = tid & 127;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
         const uint32_t ocol = lanes + G::col_o + s * D;
+        constexpr int DH = D / G::H;  // the dims of the outputs that are the thread's
+        const int d0 = half * DH;
+        // What ends the loops is voted on where groups meet at barriers, so that they always meet at the same ones.
+        const uint32_t meet = 1 + s;  // the stream's barrier
+        auto over = [&]() -> bool {
+            if constexpr (G::halves) live = !bar_or(meet, 256, !live);
+            return !live;
+        };
         int tiles = 0;  // all tiles so far
         int n = 0;      // the stream's
         int merges = 0, fins = 0;
-        for (int item = blockIdx.x; item < total && live; item += gridDim.x) {
+        for (int item = blockIdx.x; item < total; item += gridDim.x) {
             // (the record stays until the item's end, where what the loop has no registers for is read again)
             await(ifull + (k & 1), (k >> 1) & 1);
-            if (!live) break;
-            const Record it = item_sm[k & 1];
+            if (over()) break;
+            // (read as it is needed: the scores take most registers)
+            const volatile Record& it = item_sm[k & 1];
+            const int nt = it.nt, minlen = it.minlen, maxlo = it.maxlo;
+            auto edge_at = [&](int t) { return !(t + kHalf <= minlen && (t >= maxlo || t + kHalf <= p.sinks)); };
             auto release = [&] {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(iempty + (k & 1));
                 ++k;
             };
-            const int tiles0 = tiles;
-            tiles += it.nt;
             const int c0 = it.q0 + (NS == 2 && !p.decode ? 128 * s : 0), q = c0 + me;
             if (NS == 2 && !p.decode && s == 1 && c0 >= it.nq) {  // the item has one tile of queries
+                tiles += nt;
                 release();
                 continue;
             }
             const bool idle = c0 + 32 * (warp & 3) >= it.nq;  // no query of the warp's
-            auto row_of = [&](int q) { return it.r0 + (q < it.nq ? q / p.group : 0); };
-            auto head_of = [&](int q) { return it.g * p.group + (q < it.nq ? q % p.group : 0); };
-            const int len = q < it.nq ? length_of(p, row_of(q)) : 0, from = max(0, len - p.window), first = min(p.sinks, len);
+            const bool valid = q < it.nq;
+            const int row = it.r0 + (valid ? q / p.group : 0), head = it.g * p.group + (valid ? q % p.group : 0);
+            const int len = valid ? length_of(p, row) : 0, from = max(0, len - p.window), first = min(p.sinks, len);
             if (s == 0 || !p.decode) {  // the queries, swizzled as the copies do: D / 8 lanes a row
                 constexpr int L = D / 8 < 32 ? D / 8 : 32, R = 32 / L;  // lanes of a row, rows at once
+                constexpr int kRows = 32 / G::H;                        // the warp's
                 const int c = lane % L;
                 uint8_t* dst = sm + G::off_q + s * G::q_tile + (c >> 3) * (128 * 128);
-                const int64_t src = row_of(q) * p.q_stride + static_cast<int64_t>(head_of(q)) * D;
+                const int64_t src = row * p.q_stride + static_cast<int64_t>(head) * D;
+#pragma unroll 1
+                for (int i0 = half * kRows; i0 < (half + 1) * kRows; i0 += 4 * R) {
+                    uint4 v[4];
 #pragma unroll
-                for (int i0 = 0; i0 < 32; i0 += 8 * R) {
-                    uint4 v[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
+                    for (int j = 0; j < 4; ++j) {
                         const int i = i0 + j * R + lane / L;
                         const int64_t o = __shfl_sync(0xffffffffu, src, i);
                         v[j] = c0 + 32 * (warp & 3) + i < it.nq ? *reinterpret_cast<const uint4*>(p.q + o + 8 * c) : make_uint4(0, 0, 0, 0);
                     }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
+                    for (int j = 0; j < 4; ++j) {
                         const int row = 32 * (warp & 3) + i0 + j * R + lane / L;
                         v[j].x ^= p.flip, v[j].y ^= p.flip, v[j].z ^= p.flip, v[j].w ^= p.flip;
                         *reinterpret_cast<uint4*>(dst + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v[j];
@@ -794,57 +815,63 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
             }
             float l = 0.f, lim = -INFINITY, base = 0.f;  // sum, reference and slack, what comes off the scores
             bool fresh = true;                           // O holds nothing yet
-            for (int i = 0; i < it.nt; ++i) {
-                const int tile = tile_at(it, i), t0 = tile * TN, tv = tiles0 + i;
+            const int na = it.na;
+            int tile = na ? it.a0 : it.b0;
+            for (int i = 0; i < nt; ++i, ++tile, ++tiles) {
+                if (i == na && i) tile = it.b0;
+                const int t0 = tile * TN + half * kHalf;
                 if (NS == 2 && p.decode && (tile & 1) != s) continue;
                 const int x = G::halves ? 2 * s : 2 * s + (n & 1);
-                const uint32_t scol = lanes + x * kHalf;
+                const uint32_t scol = lanes + x * kHalf;  // S; the thread's half, and P, from pcol on
+                const uint32_t pcol = scol + half * kHalf;
                 await(sfull + x, (G::halves ? n : n >> 1) & 1);
-                if (!live) break;
-                if (idle) {  // (its rows of P hold anything: nobody reads what comes of them)
-                    fresh = false;
-                    ++n;
-                    if (lane < G::H) mbar_arrive(pfull + x + lane);
-                    continue;
-                }
-                tc_fence_after();
-                const bool some = edge(it, t0) || (G::halves && edge(it, t0 + kHalf));
-                const int vi = tv % G::v_told;
-                if (some) {  // which tokens' V is not finite
-                    await(vready + vi, (tv / G::v_told) & 1);
-                    if (!live) break;
-                }
-                float v[TN];
+                const bool some = edge_at(tile * TN) || (G::halves && edge_at(tile * TN + kHalf));
+                const int vi = tiles % G::v_told;
+                if (some) await(vready + vi, (tiles / G::v_told) & 1);  // (which tokens' V is not finite)
+                if (!G::halves && !live) break;
+                float v[kHalf], m = -INFINITY;
+                const int miss = kmiss_sm[tiles & 15] >> (half * kHalf >> piece_shift);
+                auto take = [&](int to) {  // scores 0 .. to - 1
 #pragma unroll
-                for (int c = 0; c < TN; c += 32) tmem_ld32(scol + c, v + c);
-                const int miss = kmiss_sm[tv & 15];
-                tc_wait_ld();
-                if (some || miss) {
-                    // the tokens that the row sees, as bits; a missing piece is 16 tokens at least
-                    auto below = [](int j) { return j <= 0 ? 0u : j >= 32 ? ~0u : (1u << j) - 1; };
+                    for (int i = 0; i < to; i += 32) tmem_ld32(pcol + i, v + i);
+                    tc_wait_ld();
+                    if (some || miss) {
+                        // the tokens that the row sees, as bits; a missing piece is 16 tokens at least
+                        auto below = [](int j) { return j <= 0 ? 0u : j >= 32 ? ~0u : (1u << j) - 1; };
 #pragma unroll
-                    for (int c = 0; c < TN; c += 32) {
-                        uint32_t sees = below(len - t0 - c) & (~below(from - t0 - c) | below(first - t0 - c));
-                        if ((miss >> (c >> piece_shift)) & 1) sees &= 0xFFFF0000u;
-                        if ((miss >> ((c + 16) >> piece_shift)) & 1) sees &= 0xFFFFu;
+                        for (int i = 0; i < to; i += 32) {
+                            const int t = t0 + i;
+                            uint32_t sees = below(len - t) & (~below(from - t) | below(first - t));
+                            if ((miss >> (i >> piece_shift)) & 1) sees &= 0xFFFF0000u;
+                            if ((miss >> ((i + 16) >> piece_shift)) & 1) sees &= 0xFFFFu;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (!(sees & (1u << j))) v[c + j] = -INFINITY;
+                            for (int j = 0; j < 32; ++j)
+                                if (!(sees & (1u << j))) v[i + j] = -INFINITY;
+                        }
                     }
+                };
+                if (live && !idle) {
+                    tc_fence_after();
+                    float m8[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) m8[j] = -INFINITY;
+                    take(kHalf);
+#pragma unroll
+                    for (int j = 0; j < kHalf; j += 16)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) m8[i] = fmaxf(m8[i], fmaxf(v[j + i], v[j + i + 8]));
+                    // (a NaN is no maximum)
+                    m = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * p.c2;
                 }
-                float m8[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) m8[j] = fmaxf(v[j], fmaxf(v[j + 8], v[j + 16]));
-#pragma unroll
-                for (int j = 24; j < TN - 8; j += 16)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) m8[i] = fmaxf(m8[i], fmaxf(v[j + i], v[j + i + 8]));
-#pragma unroll
-                for (int j = 0; j < 8; ++j) m8[j] = fmaxf(m8[j], v[TN - 8 + j]);
-                // (a NaN is no maximum)
-                const float m = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * p.c2;
-                const bool passed = m > lim;
-                if (__any_sync(0xffffffffu, passed)) {
+                const bool any = G::halves ? bar_or(meet, 256, m > lim || !live) : __any_sync(0xffffffffu, m > lim);
+                if (any) {
+                    if constexpr (G::halves) {
+                        if (over()) break;
+                        red_sm[(2 * s + half) * 128 + me] = m;
+                        named_bar_sync(meet, 256);
+                        m = fmaxf(m, red_sm[(2 * s + (half ^ 1)) * 128 + me]);
+                    }
+                    const bool passed = m > lim;
                     float alpha = 1.f;
                     if (passed) {
                         const bool fine = fabsf(m) < kFine;
@@ -854,14 +881,14 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                         lim = fine ? m + kSlack : m;
                         l *= alpha;
                     }
-                    if (!fresh) {
+                    if (!fresh && __any_sync(0xffffffffu, passed)) {
                         // (one buffer of scores: they were asked for after the last product.  Two: the last product may be under way,
                         // the one before was over before these scores were asked for)
                         if (!G::halves) await(odone + s, (n - 1) & 1);
                         if (!live) break;
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 16) {  // (rare, and the scores hold most registers)
+                        for (int c = d0; c < d0 + DH; c += 16) {  // (rare, and the scores hold most registers)
                             uint32_t o[16];
                             tmem_ld16(ocol + c, o);
                             tc_wait_ld();
@@ -877,86 +904,94 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
 #pragma unroll
                     for (int j = 0; j < 2 * G::H; ++j) odd |= odd_sm[vi * 4 + j];
                 }
-                if (fresh && me == 0) accum_sm[s] = odd != 0;
-                uint64_t sum[2] = {0, 0};  // pairs of fp32
-                const uint64_t c2 = pair(p.c2, p.c2), off = pair(-base, -base);
+                if (fresh && me == 0 && half == 0) accum_sm[s] = odd != 0;
+                if (!idle) {
+                    uint64_t sum[2] = {0, 0};  // pairs of fp32
+                    const uint64_t c2 = pair(p.c2, p.c2), off = pair(-base, -base);
 #pragma unroll
-                for (int c = 0; c < TN; c += 32) {
-                    uint32_t w[16];
+                    for (int i = 0; i < kHalf; i += 32) {
+                        // (the upper scores first; two groups' threads have no registers for the lower ones meanwhile, and read
+                        // them again: P goes over the upper)
+                        const int c = 32 - i;
+                        if (G::halves && c == 0) take(32);
+                        const float* u = v + c;
+                        uint32_t w[16];
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        float a, b;
-                        unpair(fma2(pair(v[c + j], v[c + j + 1]), c2, off), a, b);
-                        a = ex2(a), b = ex2(b);
-                        sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], pair(a, b));
-                        w[j / 2] = pack2<BF>(a, b);
+                        for (int g = 0; g < 32; g += 8) {
+                            float e[8];
+#pragma unroll
+                            for (int j = 0; j < 8; j += 2) unpair(fma2(pair(u[g + j], u[g + j + 1]), c2, off), e[j], e[j + 1]);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) e[j] = ex2(e[j]);
+#pragma unroll
+                            for (int j = 0; j < 8; j += 2) {
+                                sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], pair(e[j], e[j + 1]));
+                                w[(g + j) / 2] = pack2<BF>(e[j], e[j + 1]);
+                            }
+                        }
+                        tmem_st16(pcol + kP + c / 2, w);
                     }
-                    tmem_st16(scol + (c / kHalf) * kHalf + c % kHalf / 2, w);
-                    if (G::halves && c == 32 && !odd) {  // the first half is out
-                        tc_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(pfull + x);
-                    }
+                    float s0, s1;
+                    unpair(add2(sum[0], sum[1]), s0, s1);
+                    l += s0 + s1;
+                    tc_wait_st();
                 }
-                float s0, s1;
-                unpair(add2(sum[0], sum[1]), s0, s1);
-                l += s0 + s1;
-                tc_wait_st();
                 if (odd) {  // to those that see them
                     if (!fresh && !G::halves) await(odone + s, (n - 1) & 1);
-                    if (!live) break;
+                    if (!G::halves && !live) break;
+                    tc_fence_before();
+                    if constexpr (G::halves) named_bar_sync(meet, 256);  // (P is there, of both halves)
                     tc_fence_after();
 #pragma unroll 1
-                    for (int half = 0; half < G::H; ++half)
-                        add_odd<FMT, D>(p, it.a, it.g, t0 + half * kHalf, const_cast<const uint32_t*>(odd_sm) + vi * 4 + 2 * half, ocol, scol + half * kHalf, len,
-                                        from, first, fresh && half == 0);
+                    for (int h = 0; h < G::H; ++h)
+                        add_odd<FMT, D>(p, it.a, it.g, tile * TN + h * kHalf, const_cast<const uint32_t*>(odd_sm) + vi * 4 + 2 * h, ocol, scol + h * kHalf + kP, len,
+                                        from, first, fresh && h == 0, d0, d0 + DH);
                 }
                 fresh = false;
                 ++n;
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    if (G::halves && odd) mbar_arrive(pfull + x);
-                    mbar_arrive(pfull + x + G::H - 1);
-                }
+                if (lane == 0) mbar_arrive(pfull + x);
             }
-            if (!live) break;
             // (the item's last product; odone may be two phases behind here)
             if (!fresh) await(ofin + s, fins++ & 1);
-            if (!live) break;
+            if (over()) break;
             tc_fence_after();
+            if constexpr (G::halves) {  // the halves' sums, in their order
+                red_sm[(2 * s + half) * 128 + me] = l;
+                named_bar_sync(meet, 256);
+                l = red_sm[2 * s * 128 + me] + red_sm[(2 * s + 1) * 128 + me];
+            }
 
             // ---- what became of the item
             float w0 = 1.f, w1 = 0.f;  // the streams' weights
             // the second stream's outputs, over the queries: column c at 16 KB * (c / 32) + 128 * (c % 32), by warp
             float* stage = reinterpret_cast<float*>(sm + G::off_q + (warp & 3) * 4096) + lane;
-            if (NS == 2 && p.decode) {
+            const bool merge = NS == 2 && p.decode;
+            if (merge) {
                 if (s == 1) {
-                    await(mfree, merges & 1);  // (the queries are read)
-                    if (!live) break;
-                    ml_sm[me] = make_float2(base, l);
-                    if (!fresh && !idle) {
+                    await(mfree, merges++ & 1);  // (the queries are read)
+                    if (live) {
+                        if (half == 0) ml_sm[me] = make_float2(base, l);
+                        if (!fresh && !idle) {
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            float o[32];
-                            tmem_ld32(ocol + c, o);
-                            tc_wait_ld();
+                            for (int c = d0; c < d0 + DH; c += 32) {
+                                float o[32];
+                                tmem_ld32(ocol + c, o);
+                                tc_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) stage[(c >> 5) * 4096 + j * 32] = o[j];
+                                for (int j = 0; j < 32; ++j) stage[(c >> 5) * 4096 + j * 32] = o[j];
+                            }
+                            tc_fence_before();
                         }
-                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(mfull);
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(mfull);
-                    ++merges;
                     release();
                     continue;
                 }
                 if (lane == 0) mbar_arrive(mfree);
-                await(mfull, merges & 1);
-                if (!live) break;
-                ++merges;
+                await(mfull, merges++ & 1);
                 const float2 other = ml_sm[me];
                 // (a sum of 0: nothing seen, and nothing of the other's outputs counts)
                 const float top = l == 0.f ? other.x : other.y == 0.f ? base : fmaxf(base, other.x);
@@ -965,74 +1000,56 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                 l = l * w0 + other.y * w1;
                 base = top;
             }
-            if (idle) {
+            if (idle || !live) {
                 release();
                 continue;
             }
-            const volatile Record& rec = item_sm[k & 1];
-            const int query = rec.q0 + (NS == 2 && !p.decode ? 128 * s : 0) + me, item_chunk = rec.chunk;
-            const bool valid = query < rec.nq;
-            const int row = rec.r0 + (valid ? query / p.group : 0), head = rec.g * p.group + (valid ? query % p.group : 0);
-            const int len2 = valid ? length_of(p, row) : 0;
-            const int64_t at = static_cast<int64_t>(row) * p.heads + head;
+            const int query = it.q0 + (NS == 2 && !p.decode ? 128 * s : 0) + me, item_chunk = it.chunk;
+            bool write = query < it.nq;
+            const int row2 = it.r0 + (write ? query / p.group : 0), head2 = it.g * p.group + (write ? query % p.group : 0);
+            const int len2 = write ? length_of(p, row2) : 0;
+            const int64_t at = static_cast<int64_t>(row2) * p.heads + head2;
             release();
             int slot = 0;
-            bool write = valid;
-            if (p.chunk && valid) {
+            if (p.chunk && write) {
                 const Chunks c = chunks_of(p, len2);
                 slot = item_chunk < c.first ? item_chunk : c.first + item_chunk - c.from;
                 write = item_chunk < c.first || (item_chunk >= c.from && item_chunk < c.end);
             }
-            const bool none = l == 0.f, merge = NS == 2 && p.decode;
+            const bool none = l == 0.f;
             const float inv = none ? 0.f : p.chunk ? w0 : w0 / l, inv1 = none ? 0.f : p.chunk ? w1 : w1 / l;
-            if (write) {
+            if (write && half == 0) {
                 if (p.chunk) *reinterpret_cast<float2*>(p.ml + (at * p.slots + slot) * 2) = make_float2(base, l);
                 else if (p.lse) p.lse[at] = none ? -INFINITY : (base + log2f(l)) * 0.6931471805599453f;
             }
-            // 32 dims at a time through shared memory, so that lanes side by side write a row's bytes: its 16-byte pieces
-            // go where pieces of the rows around it are in other banks
             const bool wide32 = p.chunk || p.out_type == QMM_TYPE_F32;
-            uint8_t* turn = sm + G::off_q + (merge ? 0 : s * G::q_tile) + (warp & 3) * 4096;
-            const int64_t dst = write ? (p.chunk ? at * p.slots + slot : at) * D : -1;
+            uint8_t* dst = p.chunk ? reinterpret_cast<uint8_t*>(p.o + (at * p.slots + slot) * D) : static_cast<uint8_t*>(p.out) + at * D * (wide32 ? 4 : 2);
+            const bool whole = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                float o[32];
-                if (!fresh) tmem_ld32(ocol + c, o);
+            for (int c = d0; c < d0 + DH; c += 16) {
+                uint32_t w[16];
+                if (!fresh) tmem_ld16(ocol + c, w);
                 tc_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    o[j] = inv == 0.f ? 0.f : o[j] * inv;
-                    if (merge) o[j] += inv1 == 0.f ? 0.f : stage[(c >> 5) * 4096 + j * 32] * inv1;
+                for (int j = 0; j < 16; ++j) {
+                    float o = inv == 0.f ? 0.f : __uint_as_float(w[j]) * inv;
+                    if (merge) o += inv1 == 0.f ? 0.f : stage[(c >> 5) * 4096 + ((c & 16) + j) * 32] * inv1;
+                    w[j] = __float_as_uint(o);
                 }
-                __syncwarp();  // (the last piece's rows, and the other stream's outputs here, are read)
-                if (wide32) {
+                if (write) {
+                    if (wide32) {
+                        store32(dst + 4 * c, whole, w);
+                        store32(dst + 4 * c + 32, whole, w + 8);
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        *reinterpret_cast<float4*>(turn + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            w[i] = p.out_type == QMM_TYPE_F16 ? pack2<false>(o[8 * j + 2 * i], o[8 * j + 2 * i + 1]) : pack2<true>(o[8 * j + 2 * i], o[8 * j + 2 * i + 1]);
-                        *reinterpret_cast<uint4*>(turn + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int j = 0; j < 8; ++j) {
+                            const float a = __uint_as_float(w[2 * j]), b = __uint_as_float(w[2 * j + 1]);
+                            w[j] = p.out_type == QMM_TYPE_F16 ? pack2<false>(a, b) : pack2<true>(a, b);
+                        }
+                        store32(dst + 2 * c, whole, w);
                     }
                 }
                 __syncwarp();
-                const int L = wide32 ? 8 : 4;  // lanes of a row
-                const int piece = lane % L;
-#pragma unroll 4
-                for (int i0 = 0; i0 < 32; i0 += 32 / L) {
-                    const int row = i0 + lane / L;
-                    const int64_t to = __shfl_sync(0xffffffffu, dst, row);
-                    const uint4 w = *reinterpret_cast<const uint4*>(turn + row * 128 + ((piece ^ (row & 7)) << 4));
-                    if (to >= 0) {
-                        if (p.chunk) *reinterpret_cast<uint4*>(p.o + to + c + 4 * piece) = w;
-                        else if (wide32) *reinterpret_cast<uint4*>(static_cast<float*>(p.out) + to + c + 4 * piece) = w;
-                        else *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + to + c + 8 * piece) = w;
-                    }
-                }
             }
             tc_fence_before();
             __syncwarp();
