@@ -77,8 +77,8 @@ struct Layout {
 };
 Layout layout(const qmm_kv_dims& d, int64_t max_rows, int32_t window, int32_t sinks) {
     constexpr int64_t kSms = 152;   // of a GB300
-    constexpr double kItem = 3;     // an item's start and end, in the time of a tile of tokens
-    constexpr double kJoin = 4;     // the second kernel
+    constexpr double kItem = 7;     // an item's start and end, in the time of a tile of tokens: 15,000 and 2,200 clocks
+    constexpr double kJoin = 3;     // the second kernel
     const int64_t cap = int64_t{d.max_pages} * d.page_tokens, q = int64_t{d.max_agent_rows} * (d.heads / d.kv_heads);
     const int64_t tile = 128;
     Layout l = {};
@@ -89,8 +89,8 @@ Layout layout(const qmm_kv_dims& d, int64_t max_rows, int32_t window, int32_t si
     if (span > cap) span = cap;
     auto time = [&](int64_t n, int64_t tokens) { return static_cast<double>((n + kSms - 1) / kSms) * (static_cast<double>((tokens + tile - 1) / tile) + kItem); };
     double least = time(items, span);
-    for (int64_t c = 256; c <= 4096 && c < span; c *= 2) {
-        const double t = time(items * ((span + c - 1) / c), c) + kJoin;
+    for (int64_t c = 256; c <= 8192 && c < span; c += c < 4096 ? 128 : 1024) {
+        const double t = time(items * ((span + c - 1) / c + 1), c) + kJoin;  // (chunks are at fixed places: one more)
         const int64_t slots = ((sinks < cap ? sinks : cap) + c - 1) / c + ((cap + c - 1) / c < (window + c - 1) / c + 1 ? (cap + c - 1) / c : (window + c - 1) / c + 1);
         if (t >= least || max_rows * d.heads * slots > (int64_t{1} << 31) / (4 * d.head_dim)) continue;  // (2 GB of parts at most)
         least = t;

@@ -20,7 +20,7 @@
 // The tiles of an item are those that some of its rows sees: the first ones (sinks), and the window's.  Where few
 // items would leave SMs idle, tokens are cut into chunks at fixed places of a sequence, an item each, whose unnormalised
 // outputs a second kernel joins.  All choices are made by the plan's dims, so a row's bits do not depend on its company.
-//   warp 0      forms the items' records; asks for K and V tiles (q8_0: as they are stored)
+//   warp 0      forms the items' records; asks for K tiles (q8_0: as they are stored), another one for V tiles
 //   warps 1, 3  one thread each issues a stream's products
 //   warp 2      16-bit pools: zeroes the rows of V that must not count, where some are
 //   warps 4 ..  softmax, four or eight a stream
@@ -80,30 +80,31 @@ struct Geo {
     static constexpr int H = halves ? 2 : 1, TN = H * kHalf;     // tokens of a tile
     static constexpr int part = TN * D * 2;                      // bytes of a tile's K or V in 16 bits
     static constexpr int tile = q8 ? 2 * part : part;            // q8_0: high and low parts
-    static constexpr int k_slots = D <= 128 && !q8 ? 4 : 2, v_slots = q8 ? 1 : k_slots;
+    static constexpr int k_slots = D == 64 ? 8 : D == 128 && !q8 ? 4 : 2, v_slots = q8 ? 1 : k_slots;
     // Barriers that say that a tile's K or V is there: more of them than slots, since a stream of a decode step waits only for
     // tiles of its own, at most three apart.  Then a barrier's phase before the one waited for is over for sure: V's come
-    // in order, and the last own tile's K was asked for after the K of eight tiles before had been used.
-    static constexpr int k_told = 8, v_told = 4;
+    // in order, and the last own tile's K was asked for after the K of k_told tiles before had been used.
+    static constexpr int k_told = k_slots <= 4 ? 8 : 16, v_told = v_slots <= 4 ? 4 : 8;
     static constexpr int raw_slots = q8 ? 2 : 0;                 // pages on their way, K and V
     static constexpr int q_tile = 128 * D * 2;
     static constexpr int soft_warps = 4 * H * streams, conv_warps = q8 ? 4 : 0;
-    static constexpr int threads = 32 * (4 + soft_warps + conv_warps);
+    static constexpr int v_warp = q8 ? 2 : streams == 1 ? 3 : 4 + soft_warps;  // asks for V tiles
+    static constexpr int threads = 32 * (4 + soft_warps + (streams == 1 ? 0 : 4));
     // tensor memory: S (128 columns per stream, two halves or two buffers), P over it, and O
     static constexpr int col_o = 256;
     // shared memory, after aligning to 1024
     static constexpr int off_v = k_slots * tile;
     static constexpr int off_q = off_v + v_slots * tile;
     static constexpr int off_raw = off_q + streams * q_tile;     // K's pages, then V's
-    static constexpr int off_ml = off_raw + 2 * raw_slots * kQ8Half;  // [128] reference and sum of the second stream
-    static constexpr int off_red = off_ml + 128 * 8;             // [stream][half][128] maxima, and sums
+    static constexpr int off_ml = off_raw + 2 * raw_slots * kQ8Half;  // [2][128] reference and sum of the streams
+    static constexpr int off_red = off_ml + 256 * 8;             // [stream][half][128] maxima, and sums
     static constexpr int off_item = off_red + (halves ? 2048 : 0);  // [2] of Record
     static constexpr int off_dv = off_item + 2 * 64;             // q8_0: V's scales, zero where a token must not count: [4][64] fp16
     static constexpr int off_bar = off_dv + (q8 ? 512 : 0);
     static constexpr int bars = k_told + k_slots + 2 * v_slots + v_told + 4 * raw_slots + 2 + 4 + 4 + 2 + 2 + 2 + 2 + 4;
-    // tmp[33], abort, tmem, accumulate[2], miss[4] (of V tiles), odd[4][4], miss[16] (of all tiles), raw[2][2]
+    // tmp[33], abort, tmem, accumulate[2], miss[8] (of V tiles), odd[8][4], miss[16] (of all tiles), raw[2][2]
     static constexpr int off_misc = (off_bar + bars * 8 + 15) / 16 * 16;
-    static constexpr int off_seq = (off_misc + 80 * 4 + 15) / 16 * 16;
+    static constexpr int off_seq = (off_misc + 100 * 4 + 15) / 16 * 16;
     static constexpr int smem(int agents) { return 1024 + off_seq + (agents + 1) * 16; }
 };
 
@@ -443,10 +444,10 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
     volatile int* abort_flag = tmp + 33;
     uint32_t* tmem_sm = reinterpret_cast<uint32_t*>(tmp + 34);
     volatile int* accum_sm = tmp + 35;                                          // [2] O holds something before the first product
-    volatile int* miss_sm = tmp + 37;                                           // [4] a V tile's pieces that are outside the pool
-    volatile uint32_t* odd_sm = reinterpret_cast<uint32_t*>(tmp + 41);          // [4][4] tokens that are taken query by query: a half's even ones, odd ones
-    volatile int* kmiss_sm = tmp + 57;                                          // [16] miss of the last 16 tiles (more than are under way)
-    volatile int* raw_sm = tmp + 73;                                            // q8_0, [2][2]: a page's number, -1 not needed, -2 outside the pool
+    volatile int* miss_sm = tmp + 37;                                           // [8] a V tile's pieces that are outside the pool
+    volatile uint32_t* odd_sm = reinterpret_cast<uint32_t*>(tmp + 45);          // [8][4] tokens that are taken query by query: a half's even ones, odd ones
+    volatile int* kmiss_sm = tmp + 77;                                          // [16] miss of the last 16 tiles (more than are under way)
+    volatile int* raw_sm = tmp + 93;                                            // q8_0, [2][2]: a page's number, -1 not needed, -2 outside the pool
     int4* seq = reinterpret_cast<int4*>(sm + G::off_seq);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int qt = NS == 2 && !p.decode ? 256 : 128;
@@ -462,12 +463,12 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
             mbar_init(odone + i, 1);
             mbar_init(ofin + i, 1);
             mbar_init(ifull + i, 1);
-            mbar_init(iempty + i, NS + (G::q8 ? G::conv_warps : 1) + G::soft_warps);
+            mbar_init(iempty + i, 1 + NS + (G::q8 ? G::conv_warps : 1) + G::soft_warps);
         }
         for (int i = 0; i < 4; ++i) mbar_init(sfull + i, 1), mbar_init(pfull + i, 4 * G::H);
         for (int i = 0; i < 2 * G::raw_slots; ++i) mbar_init(rfull + i, 1), mbar_init(rempty + i, 4);
-        mbar_init(mfree, 4 * G::H);
-        mbar_init(mfull, 4 * G::H);
+        mbar_init(mfree, G::soft_warps);
+        mbar_init(mfull, G::soft_warps);
         mbar_init(drained, 1);
         mbar_init(drained + 1, 1);
         *abort_flag = 0;
@@ -521,76 +522,72 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
     };
 
     // Registers go where the scores are (the shares add up to what the block was launched with, or less:
-    // 512 * 104 + 128 * 64 = 640 * 96; q8_0 256 * 168 + 256 * 80 <= 512 * 128).
-    if (warp < 4) {
-    if constexpr (NS == 2) setmaxnreg_dec<G::q8 ? 80 : 104>();
-    if (warp == 0) {
-        // ---------------------------------------------------------------- records, K tiles and V tiles
+    // 256 * 200 + 256 * 56 = 512 * 128).
+    if (warp < 4 || (!G::q8 && warp >= 4 + G::soft_warps)) {
+    if constexpr (NS == 2) setmaxnreg_dec<G::q8 ? 80 : 56>();
+    if (warp == 0 || warp == G::v_warp) {
+        // ---------------------------------------------------------------- records, and K tiles; V tiles
+        const int h = warp == G::v_warp;
         constexpr int kSlots = G::q8 ? G::raw_slots : G::k_slots;
         static_assert(G::q8 || G::k_slots == G::v_slots);
-        uint64_t *full[2] = {G::q8 ? rfull : kfull, G::q8 ? rfull + kSlots : vfull};
-        uint64_t *empty[2] = {G::q8 ? rempty : kempty, G::q8 ? rempty + kSlots : vempty};
-        uint8_t* ring[2] = {sm + (G::q8 ? G::off_raw : 0), sm + (G::q8 ? G::off_raw + kSlots * kQ8Half : G::off_v)};
+        uint64_t* empty = G::q8 ? rempty + h * kSlots : h ? vempty : kempty;
+        uint8_t* ring = sm + (G::q8 ? G::off_raw + h * kSlots * kQ8Half : h ? G::off_v : 0);
+        // the barrier that says that tile t is there
+        auto told = [&](int t) { return G::q8 ? rfull + h * kSlots + t % kSlots : h ? vfull + t % kSlots : kfull + t % G::k_told; };
         // (a prompt's tiles are read by other blocks as well)
         const uint64_t policy = p.decode ? l2_policy_evict_first() : l2_policy_evict_last();
-        // Tile t's K (h = 0) or V: lanes by piece.
-        auto ask = [&](int h, int g, int t0, int mine, int t) {
-            const uint32_t there = __ballot_sync(0xffffffffu, mine >= 0);
-            const int miss = static_cast<int>(__ballot_sync(0xffffffffu, mine == -2));
-            const int s = t % kSlots, round = t / kSlots;
-            uint64_t* told = G::q8 || h ? full[h] + s : kfull + t % G::k_told;
-            if (round > 0) await(empty[h] + s, (round - 1) & 1);
-            if (!live) return;
-            if (lane == 0) {
-                if constexpr (G::q8) raw_sm[2 * h + s] = mine;
-                else if (h) miss_sm[s] = miss;
-                else kmiss_sm[t & 15] = miss;
-                if (!there) mbar_arrive(told);
-                else mbar_arrive_expect_tx(told, G::q8 ? kQ8Half : __popc(there) * piece_rows * D * 2);
-            }
-            __syncwarp();
-            if (mine < 0) return;
-            fence_proxy_async_smem();  // the slot's generic accesses, before the copies
-            if constexpr (G::q8) {
-                bulk_g2s(ring[h] + s * kQ8Half, p.pool + (static_cast<int64_t>(mine) * p.kv_heads + g) * kQ8Rec + h * kQ8Half, kQ8Half, told, policy);
-            } else {
-                const int y = ((mine * p.kv_heads + g) * 2 + h) * p.page_tokens + ((t0 + lane * piece_rows) & (p.page_tokens - 1));
-#pragma unroll
-                for (int x = 0; x < D / 64; ++x)
-                    tma_load_hint(ring[h] + s * G::tile + x * TN * 128 + lane * piece_rows * 128, &map, 64 * x, y, told, policy);
-            }
-        };
-        // K goes a tile ahead of V
-        int t = 0, v_page = -1, v_t0 = 0, v_g = 0;
+        int t = 0;
         for (int item = blockIdx.x; item < total && live; item += gridDim.x) {
-            const Record it = record_of<TN>(p, seq, item, qt);
-            if (k > 1) await(iempty + (k & 1), ((k >> 1) - 1) & 1);
-            if (!live) break;
-            if (lane == 0) {
-                item_sm[k & 1] = it;
-                mbar_arrive(ifull + (k & 1));
+            Record it;
+            if (h) {
+                it = next_record();
+            } else {
+                it = record_of<TN>(p, seq, item, qt);
+                if (k > 1) await(iempty + (k & 1), ((k >> 1) - 1) & 1);
+                if (!live) break;
+                if (lane == 0) {
+                    item_sm[k & 1] = it;
+                    mbar_arrive(ifull + (k & 1));
+                }
+                ++k;
             }
-            ++k;
             int next = it.nt > 0 ? page_of(it, tile_at(it, 0) * TN) : -1;
             for (int i = 0; i < it.nt && live; ++i, ++t) {
-                const int t0 = tile_at(it, i) * TN, mine = next;
+                const int t0 = tile_at(it, i) * TN, mine = next;  // (lanes by piece)
                 if (i + 1 < it.nt) next = page_of(it, tile_at(it, i + 1) * TN);
-                if (t > 0) ask(1, v_g, v_t0, v_page, t - 1);  // (whose slot comes free first)
+                const uint32_t there = __ballot_sync(0xffffffffu, mine >= 0);
+                const int miss = static_cast<int>(__ballot_sync(0xffffffffu, mine == -2));
+                const int s = t % kSlots, round = t / kSlots;
+                if (round > 0) await(empty + s, (round - 1) & 1);
+                if (!live) break;
+                uint64_t* bar = told(t);
+                if (lane == 0) {
+                    if constexpr (G::q8) raw_sm[2 * h + s] = mine;
+                    else if (h) miss_sm[s] = miss;
+                    else kmiss_sm[t & 15] = miss;
+                    if (!there) mbar_arrive(bar);
+                    else mbar_arrive_expect_tx(bar, G::q8 ? kQ8Half : __popc(there) * piece_rows * D * 2);
+                }
                 __syncwarp();
-                ask(0, it.g, t0, mine, t);
+                if (mine >= 0) {
+                    fence_proxy_async_smem();  // the slot's generic accesses, before the copies
+                    if constexpr (G::q8) {
+                        bulk_g2s(ring + s * kQ8Half, p.pool + (static_cast<int64_t>(mine) * p.kv_heads + it.g) * kQ8Rec + h * kQ8Half, kQ8Half, bar, policy);
+                    } else {
+                        const int y = ((mine * p.kv_heads + it.g) * 2 + h) * p.page_tokens + ((t0 + lane * piece_rows) & (p.page_tokens - 1));
+#pragma unroll
+                        for (int x = 0; x < D / 64; ++x)
+                            tma_load_hint(ring + s * G::tile + x * TN * 128 + lane * piece_rows * 128, &map, 64 * x, y, bar, policy);
+                    }
+                }
                 __syncwarp();
-                v_page = mine, v_t0 = t0, v_g = it.g;
             }
         }
-        if (t > 0 && live) ask(1, v_g, v_t0, v_page, t - 1);
-        __syncwarp();
         if (!live && lane == 0) {
             // let every copy still in flight land before the block exits: the last of each slot
             volatile int go_on = 0;
-            for (int i = max(0, t - kSlots - 1); i <= t; ++i) {
-                mbar_wait_bounded(G::q8 ? rfull + i % kSlots : kfull + i % G::k_told, (G::q8 ? i / kSlots : i / G::k_told) & 1, &go_on, 100000000ull);
-                mbar_wait_bounded(full[1] + i % kSlots, (i / kSlots) & 1, &go_on, 100000000ull);
-            }
+            for (int i = max(0, t - kSlots); i <= t; ++i)
+                mbar_wait_bounded(told(i), (i / (!G::q8 && !h ? G::k_told : kSlots)) & 1, &go_on, 100000000ull);
         }
     } else if (warp == 1 || (warp == 3 && NS == 2)) {
         // ---------------------------------------------------------------- a stream's products
@@ -767,6 +764,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
         for (int item = blockIdx.x; item < total; item += gridDim.x) {
             // (the record stays until the item's end, where what the loop has no registers for is read again)
             await(ifull + (k & 1), (k >> 1) & 1);
+            if (NS == 2 && p.decode && merges > 0) await(mfree, (merges - 1) & 1);  // (the last item's outputs are read)
             if (over()) break;
             // (read as it is needed: the scores take most registers)
             const volatile Record& it = item_sm[k & 1];
@@ -787,23 +785,25 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
             const bool valid = q < it.nq;
             const int row = it.r0 + (valid ? q / p.group : 0), head = it.g * p.group + (valid ? q % p.group : 0);
             const int len = valid ? length_of(p, row) : 0, from = max(0, len - p.window), first = min(p.sinks, len);
+            const int nq = it.nq;
             if (s == 0 || !p.decode) {  // the queries, swizzled as the copies do: D / 8 lanes a row
                 constexpr int L = D / 8 < 32 ? D / 8 : 32, R = 32 / L;  // lanes of a row, rows at once
                 constexpr int kRows = 32 / G::H;                        // the warp's
                 const int c = lane % L;
                 uint8_t* dst = sm + G::off_q + s * G::q_tile + (c >> 3) * (128 * 128);
                 const int64_t src = row * p.q_stride + static_cast<int64_t>(head) * D;
+                constexpr int kMost = G::q8 ? 8 : 16, kLoads = kRows / R < kMost ? kRows / R : kMost;  // (on their way at once)
 #pragma unroll 1
-                for (int i0 = half * kRows; i0 < (half + 1) * kRows; i0 += 4 * R) {
-                    uint4 v[4];
+                for (int i0 = half * kRows; i0 < (half + 1) * kRows; i0 += kLoads * R) {
+                    uint4 v[kLoads];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int j = 0; j < kLoads; ++j) {
                         const int i = i0 + j * R + lane / L;
                         const int64_t o = __shfl_sync(0xffffffffu, src, i);
-                        v[j] = c0 + 32 * (warp & 3) + i < it.nq ? *reinterpret_cast<const uint4*>(p.q + o + 8 * c) : make_uint4(0, 0, 0, 0);
+                        v[j] = c0 + 32 * (warp & 3) + i < nq ? *reinterpret_cast<const uint4*>(p.q + o + 8 * c) : make_uint4(0, 0, 0, 0);
                     }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int j = 0; j < kLoads; ++j) {
                         const int row = 32 * (warp & 3) + i0 + j * R + lane / L;
                         v[j].x ^= p.flip, v[j].y ^= p.flip, v[j].z ^= p.flip, v[j].w ^= p.flip;
                         *reinterpret_cast<uint4*>(dst + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v[j];
@@ -965,42 +965,28 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
 
             // ---- what became of the item
             float w0 = 1.f, w1 = 0.f;  // the streams' weights
-            // the second stream's outputs, over the queries: column c at 16 KB * (c / 32) + 128 * (c % 32), by warp
-            float* stage = reinterpret_cast<float*>(sm + G::off_q + (warp & 3) * 4096) + lane;
             const bool merge = NS == 2 && p.decode;
-            if (merge) {
-                if (s == 1) {
-                    await(mfree, merges++ & 1);  // (the queries are read)
-                    if (live) {
-                        if (half == 0) ml_sm[me] = make_float2(base, l);
-                        if (!fresh && !idle) {
-#pragma unroll 1
-                            for (int c = d0; c < d0 + DH; c += 32) {
-                                float o[32];
-                                tmem_ld32(ocol + c, o);
-                                tc_wait_ld();
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) stage[(c >> 5) * 4096 + j * 32] = o[j];
-                            }
-                            tc_fence_before();
-                        }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(mfull);
-                    }
-                    release();
-                    continue;
-                }
-                if (lane == 0) mbar_arrive(mfree);
+            if (merge) {  // the streams' softmaxes have the same lanes of tensor memory: each takes half of both's dims
+                ml_sm[128 * s + me] = make_float2(base, l);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(mfull);
                 await(mfull, merges++ & 1);
-                const float2 other = ml_sm[me];
-                // (a sum of 0: nothing seen, and nothing of the other's outputs counts)
-                const float top = l == 0.f ? other.x : other.y == 0.f ? base : fmaxf(base, other.x);
-                w0 = l == 0.f ? 0.f : ex2(base - top);
-                w1 = other.y == 0.f ? 0.f : ex2(other.x - top);
-                l = l * w0 + other.y * w1;
+                tc_fence_after();
+                const float2 a = ml_sm[me], b = ml_sm[128 + me];
+                // (a sum of 0: nothing seen, and nothing of its outputs counts)
+                const float top = a.y == 0.f ? b.x : b.y == 0.f ? a.x : fmaxf(a.x, b.x);
+                w0 = a.y == 0.f ? 0.f : ex2(a.x - top);
+                w1 = b.y == 0.f ? 0.f : ex2(b.x - top);
+                l = a.y * w0 + b.y * w1;
                 base = top;
             }
+            auto outputs_read = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (merge && lane == 0) mbar_arrive(mfree);
+            };
             if (idle || !live) {
+                outputs_read();
                 release();
                 continue;
             }
@@ -1018,41 +1004,52 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
             }
             const bool none = l == 0.f;
             const float inv = none ? 0.f : p.chunk ? w0 : w0 / l, inv1 = none ? 0.f : p.chunk ? w1 : w1 / l;
-            if (write && half == 0) {
+            const int from_d = merge ? s * (D / 2) : d0, to_d = from_d + (merge ? D / 2 : DH);
+            if (write && from_d == 0) {
                 if (p.chunk) *reinterpret_cast<float2*>(p.ml + (at * p.slots + slot) * 2) = make_float2(base, l);
                 else if (p.lse) p.lse[at] = none ? -INFINITY : (base + log2f(l)) * 0.6931471805599453f;
             }
             const bool wide32 = p.chunk || p.out_type == QMM_TYPE_F32;
             uint8_t* dst = p.chunk ? reinterpret_cast<uint8_t*>(p.o + (at * p.slots + slot) * D) : static_cast<uint8_t*>(p.out) + at * D * (wide32 ? 4 : 2);
             const bool whole = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
+            // 16 dims of both streams at a time, or 32 of the one
 #pragma unroll 1
-            for (int c = d0; c < d0 + DH; c += 16) {
-                uint32_t w[16];
-                if (!fresh) tmem_ld16(ocol + c, w);
+            for (int c = from_d; c < to_d; c += merge ? 16 : 32) {
+                uint32_t w[2][16];
+                const uint32_t first_col = lanes + G::col_o + (merge ? 0 : s * D) + c;
+                if (merge || !fresh) {
+                    tmem_ld16(first_col, w[0]);
+                    tmem_ld16(first_col + (merge ? D : 16), w[1]);
+                }
                 tc_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    float o = inv == 0.f ? 0.f : __uint_as_float(w[j]) * inv;
-                    if (merge) o += inv1 == 0.f ? 0.f : stage[(c >> 5) * 4096 + ((c & 16) + j) * 32] * inv1;
-                    w[j] = __float_as_uint(o);
+                    float o = inv == 0.f ? 0.f : __uint_as_float(w[0][j]) * inv, other = __uint_as_float(w[1][j]);
+                    if (merge) o += inv1 == 0.f ? 0.f : other * inv1;
+                    else other = inv == 0.f ? 0.f : other * inv;
+                    w[0][j] = __float_as_uint(o);
+                    w[1][j] = __float_as_uint(other);
                 }
                 if (write) {
-                    if (wide32) {
-                        store32(dst + 4 * c, whole, w);
-                        store32(dst + 4 * c + 32, whole, w + 8);
-                    } else {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float a = __uint_as_float(w[2 * j]), b = __uint_as_float(w[2 * j + 1]);
-                            w[j] = p.out_type == QMM_TYPE_F16 ? pack2<false>(a, b) : pack2<true>(a, b);
+                    for (int i = 0; i < 2; ++i) {
+                        if (merge && i) continue;
+                        if (wide32) {
+                            store32(dst + 4 * (c + 16 * i), whole, w[i]);
+                            store32(dst + 4 * (c + 16 * i) + 32, whole, w[i] + 8);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const float a = __uint_as_float(w[i][2 * j]), b = __uint_as_float(w[i][2 * j + 1]);
+                                w[i][j] = p.out_type == QMM_TYPE_F16 ? pack2<false>(a, b) : pack2<true>(a, b);
+                            }
+                            store32(dst + 2 * (c + 16 * i), whole, w[i]);
                         }
-                        store32(dst + 2 * c, whole, w);
                     }
                 }
                 __syncwarp();
             }
-            tc_fence_before();
-            __syncwarp();
+            outputs_read();
         }
         if (!live && lane == 0) atomicOr(p.err, kErrTimeout);
     } else if constexpr (G::q8) {
@@ -1211,7 +1208,7 @@ cudaError_t launch_one(const Launch& a, cudaStream_t s) {
         cudaFuncAttributes f = {};
         return cudaFuncGetAttributes(&f, attend_window_tc<FMT, D>) == cudaSuccess ? f.numRegs : 0;
     }();
-    if (G::streams == 2 && regs < (G::q8 ? 128 : 168)) return cudaErrorLaunchOutOfResources;
+    if (G::streams == 2 && regs < 128) return cudaErrorLaunchOutOfResources;
     const cudaError_t e = once.allow_shared(attend_window_tc<FMT, D>, a.device);
     if (e != cudaSuccess) return e;
     attend_window_tc<FMT, D><<<a.grid, G::threads, G::smem(a.p.agents), s>>>(a.map, a.p);
