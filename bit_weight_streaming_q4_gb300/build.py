@@ -19,8 +19,9 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libqmm.so")
 SOURCES = ["qmm_api.cu", "qmm_b1.cu", "qmm_b2.cu", "qmm_noalloc.cu", "qmm_attn.cu",
            "qmm_kv_attend.cu", "qmm_kv_attend_q8.cu", "qmm_kv_attend_f16.cu", "qmm_kv_attend_bf16.cu",
-           "qmm_kv_cache.cu", "qmm_logprobs.cu", "qmm_kv_window.cu", "qmm_kv_window_q8.cu", "qmm_kv_window_f16.cu", "qmm_kv_window_bf16.cu",
-           "qmm_rotate.cu", "qmm_verify.cu"]
+           "qmm_kv_cache.cu", "qmm_logprobs.cu", "qmm_kv_window.cu", "qmm_kv_window_q8.cu",
+           "qmm_kv_window_f16_prompts.cu", "qmm_kv_window_f16_decode.cu", "qmm_kv_window_bf16_prompts.cu",
+           "qmm_kv_window_bf16_decode.cu", "qmm_rotate.cu", "qmm_verify.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

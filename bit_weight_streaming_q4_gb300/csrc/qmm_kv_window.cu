@@ -199,7 +199,7 @@ qmm_status qmm_kv_attend_window(const qmm_kv_dims* dims, const void* pool, const
     p.rows = static_cast<int32_t>(rows), p.max_agent_rows = dims->max_agent_rows, p.cap = dims->max_pages * dims->page_tokens;
     p.window = window < p.cap ? window : p.cap, p.sinks = sinks < p.cap ? sinks : p.cap;
     p.out_type = out_type, p.format = dims->format, p.head_dim = dims->head_dim;
-    p.chunk = l.chunk, p.slots = l.slots, p.decode = l.decode;
+    p.chunk = l.chunk, p.slots = l.slots;
     p.ml = static_cast<float*>(workspace);
     p.o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + l.o);
     // (a scale of 0 leaves every finite score within 2^-126 of 0, and -infinity, which marks what a row does not see, as it is)
@@ -211,9 +211,11 @@ qmm_status qmm_kv_attend_window(const qmm_kv_dims* dims, const void* pool, const
     most *= int64_t{dims->kv_heads} * (l.chunk ? l.slots + dims->max_agent_rows / l.chunk + 1 : 1);
     a.grid = static_cast<int>(most < sms ? most : sms);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = dims->format == QMM_KV_Q8_0  ? launch_q8(a, s)
-                    : dims->format == QMM_KV_F16 ? launch_f16(a, dims->head_dim, s)
-                                                 : launch_bf16(a, dims->head_dim, s);
+    const bool decode = l.decode && dims->head_dim != 256;  // (256: one stream, the same either way)
+    const int hd = dims->head_dim;
+    cudaError_t e = dims->format == QMM_KV_Q8_0  ? launch_q8(a, decode, s)
+                    : dims->format == QMM_KV_F16 ? (decode ? launch_f16_decode(a, hd, s) : launch_f16_prompts(a, hd, s))
+                                                 : (decode ? launch_bf16_decode(a, hd, s) : launch_bf16_prompts(a, hd, s));
     if (e == cudaSuccess && l.chunk)
         e = dims->head_dim == 64 ? launch_join<64>(p, s) : dims->head_dim == 128 ? launch_join<128>(p, s) : launch_join<256>(p, s);
     return e == cudaSuccess ? QMM_OK : QMM_ERR_CUDA;

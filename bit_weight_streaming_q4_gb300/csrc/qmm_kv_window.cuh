@@ -20,7 +20,7 @@
 // The tiles of an item are those that some of its rows sees: the first ones (sinks), and the window's.  Where few
 // items would leave SMs idle, tokens are cut into chunks at fixed places of a sequence, an item each, whose unnormalised
 // outputs a second kernel joins.  All choices are made by the plan's dims, so a row's bits do not depend on its company.
-//   warp 0      forms the items' records; asks for K tiles (q8_0: as they are stored), another one for V tiles
+//   warp 0      forms the items' records; asks for K tiles (q8_0: as they are stored); it or another one asks for V tiles
 //   warps 1, 3  one thread each issues a stream's products
 //   warp 2      16-bit pools: zeroes the rows of V that must not count, where some are
 //   warps 4 ..  softmax, four or eight a stream
@@ -61,7 +61,6 @@ struct Params {
     int32_t window, sinks, out_type, format, head_dim;
     int32_t chunk;   // tokens per chunk, a multiple of 128; 0: one item has all of a query's tokens and writes its output
     int32_t slots;   // partials per (row, head)
-    int32_t decode;  // one tile of queries an item, tokens dealt to two streams
     uint32_t flip;   // sign bits that a negative scale puts on the queries
     float c2;        // |scale| log2(e), positive
 };
@@ -72,7 +71,8 @@ struct Launch {
     int device, grid;
 };
 
-template <int FMT, int D>
+// DEC: decode steps, one tile of queries an item and its tokens dealt to two streams; otherwise prompts.
+template <int FMT, int D, bool DEC>
 struct Geo {
     static constexpr bool q8 = FMT == QMM_KV_Q8_0;
     static constexpr int streams = D == 256 ? 1 : 2;
@@ -88,8 +88,12 @@ struct Geo {
     static constexpr int raw_slots = q8 ? 2 : 0;                 // pages on their way, K and V
     static constexpr int q_tile = 128 * D * 2;
     static constexpr int soft_warps = 4 * H * streams, conv_warps = q8 ? 4 : 0;
-    static constexpr int v_warp = q8 ? 2 : streams == 1 ? 3 : 4 + soft_warps;  // asks for V tiles
-    static constexpr int threads = 32 * (4 + soft_warps + (streams == 1 ? 0 : 4));
+    // The warp that asks for V tiles: one of its own, in decode steps for which it takes four more (which asks faster: 61
+    // ragged sequences at head dimension 64 took 59 us, 71 with one warp for K and V); a prompt's softmax wants their
+    // registers (2,048 rows: 216 us, 230 with them).
+    static constexpr int more_warps = !q8 && streams == 2 && DEC ? 4 : 0;
+    static constexpr int v_warp = q8 ? 2 : streams == 1 ? 3 : DEC ? 4 + soft_warps : 0;
+    static constexpr int threads = 32 * (4 + soft_warps + conv_warps + more_warps);
     // tensor memory: S (128 columns per stream, two halves or two buffers), P over it, and O
     static constexpr int col_o = 256;
     // shared memory, after aligning to 1024
@@ -423,10 +427,10 @@ __device__ __noinline__ void add_odd(const Params& p, int a, int g, int t0, cons
     tc_wait_st();
 }
 
-template <int FMT, int D>
-__global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
+template <int FMT, int D, bool DEC>
+__global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
     attend_window_tc(const __grid_constant__ CUtensorMap map, const __grid_constant__ Params p) {
-    using G = Geo<FMT, D>;
+    using G = Geo<FMT, D, DEC>;
     constexpr bool BF = FMT == QMM_KV_BF16;
     constexpr int TN = G::TN, NS = G::streams, kP = G::halves ? 32 : 0;  // (P's columns over S's)
     extern __shared__ uint8_t sm_raw[];
@@ -450,10 +454,10 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
     volatile int* raw_sm = tmp + 93;                                            // q8_0, [2][2]: a page's number, -1 not needed, -2 outside the pool
     int4* seq = reinterpret_cast<int4*>(sm + G::off_seq);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int qt = NS == 2 && !p.decode ? 256 : 128;
+    constexpr int qt = NS == 2 && !DEC ? 256 : 128;
 
     if (tid == 0) {
-        const int users = NS == 2 && !p.decode ? 2 : 1;  // streams that see a tile
+        const int users = NS == 2 && !DEC ? 2 : 1;  // streams that see a tile
         for (int i = 0; i < G::k_told; ++i) mbar_init(kfull + i, G::q8 ? 4 : 1);
         for (int i = 0; i < G::v_told; ++i) mbar_init(vready + i, G::q8 ? 4 : 1);
         for (int i = 0; i < G::k_slots; ++i) mbar_init(kempty + i, users);
@@ -463,7 +467,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
             mbar_init(odone + i, 1);
             mbar_init(ofin + i, 1);
             mbar_init(ifull + i, 1);
-            mbar_init(iempty + i, 1 + NS + (G::q8 ? G::conv_warps : 1) + G::soft_warps);
+            mbar_init(iempty + i, (G::v_warp != 0) + NS + (G::q8 ? G::conv_warps : 1) + G::soft_warps);
         }
         for (int i = 0; i < 4; ++i) mbar_init(sfull + i, 1), mbar_init(pfull + i, 4 * G::H);
         for (int i = 0; i < 2 * G::raw_slots; ++i) mbar_init(rfull + i, 1), mbar_init(rempty + i, 4);
@@ -522,24 +526,51 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
     };
 
     // Registers go where the scores are (the shares add up to what the block was launched with, or less:
-    // 256 * 200 + 256 * 56 = 512 * 128).
-    if (warp < 4 || (!G::q8 && warp >= 4 + G::soft_warps)) {
-    if constexpr (NS == 2) setmaxnreg_dec<G::q8 ? 80 : 56>();
+    // 256 * 200 + 128 * 104 = 384 * 168, with four more warps 256 * 200 + 256 * 56 = 512 * 128; q8_0 256 * 168 + 256 * 80 <= 512 * 128).
+    if (warp < 4 || (G::more_warps && warp >= 4 + G::soft_warps)) {
+    if constexpr (NS == 2) setmaxnreg_dec<G::q8 ? 80 : G::more_warps ? 56 : 104>();
     if (warp == 0 || warp == G::v_warp) {
         // ---------------------------------------------------------------- records, and K tiles; V tiles
-        const int h = warp == G::v_warp;
         constexpr int kSlots = G::q8 ? G::raw_slots : G::k_slots;
         static_assert(G::q8 || G::k_slots == G::v_slots);
-        uint64_t* empty = G::q8 ? rempty + h * kSlots : h ? vempty : kempty;
-        uint8_t* ring = sm + (G::q8 ? G::off_raw + h * kSlots * kQ8Half : h ? G::off_v : 0);
-        // the barrier that says that tile t is there
-        auto told = [&](int t) { return G::q8 ? rfull + h * kSlots + t % kSlots : h ? vfull + t % kSlots : kfull + t % G::k_told; };
+        const bool does_k = warp == 0, does_v = warp == G::v_warp;
+        // the barrier that says that tile t's K (h = 0) or V is there
+        auto told = [&](int h, int t) { return G::q8 ? rfull + h * kSlots + t % kSlots : h ? vfull + t % kSlots : kfull + t % G::k_told; };
         // (a prompt's tiles are read by other blocks as well)
-        const uint64_t policy = p.decode ? l2_policy_evict_first() : l2_policy_evict_last();
-        int t = 0;
+        const uint64_t policy = DEC ? l2_policy_evict_first() : l2_policy_evict_last();
+        auto ask = [&](int h, int g, int t0, int mine, int t) {  // `mine`: pages, lanes by piece
+            const uint32_t there = __ballot_sync(0xffffffffu, mine >= 0);
+            const int miss = static_cast<int>(__ballot_sync(0xffffffffu, mine == -2));
+            const int s = t % kSlots, round = t / kSlots;
+            if (round > 0) await((G::q8 ? rempty + h * kSlots : h ? vempty : kempty) + s, (round - 1) & 1);
+            if (!live) return;
+            uint64_t* bar = told(h, t);
+            if (lane == 0) {
+                if constexpr (G::q8) raw_sm[2 * h + s] = mine;
+                else if (h) miss_sm[s] = miss;
+                else kmiss_sm[t & 15] = miss;
+                if (!there) mbar_arrive(bar);
+                else mbar_arrive_expect_tx(bar, G::q8 ? kQ8Half : __popc(there) * piece_rows * D * 2);
+            }
+            __syncwarp();
+            if (mine >= 0) {
+                fence_proxy_async_smem();  // the slot's generic accesses, before the copies
+                if constexpr (G::q8) {
+                    bulk_g2s(sm + G::off_raw + (h * kSlots + s) * kQ8Half, p.pool + (static_cast<int64_t>(mine) * p.kv_heads + g) * kQ8Rec + h * kQ8Half,
+                             kQ8Half, bar, policy);
+                } else {
+                    const int y = ((mine * p.kv_heads + g) * 2 + h) * p.page_tokens + ((t0 + lane * piece_rows) & (p.page_tokens - 1));
+#pragma unroll
+                    for (int x = 0; x < D / 64; ++x)
+                        tma_load_hint(sm + (h ? G::off_v : 0) + s * G::tile + x * TN * 128 + lane * piece_rows * 128, &map, 64 * x, y, bar, policy);
+                }
+            }
+            __syncwarp();
+        };
+        int t = 0, v_page = -1, v_t0 = 0, v_g = 0;  // (a warp that asks for both: V a tile behind K, whose slots come free first)
         for (int item = blockIdx.x; item < total && live; item += gridDim.x) {
             Record it;
-            if (h) {
+            if (!does_k) {
                 it = next_record();
             } else {
                 it = record_of<TN>(p, seq, item, qt);
@@ -553,41 +584,24 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
             }
             int next = it.nt > 0 ? page_of(it, tile_at(it, 0) * TN) : -1;
             for (int i = 0; i < it.nt && live; ++i, ++t) {
-                const int t0 = tile_at(it, i) * TN, mine = next;  // (lanes by piece)
+                const int t0 = tile_at(it, i) * TN, mine = next;
                 if (i + 1 < it.nt) next = page_of(it, tile_at(it, i + 1) * TN);
-                const uint32_t there = __ballot_sync(0xffffffffu, mine >= 0);
-                const int miss = static_cast<int>(__ballot_sync(0xffffffffu, mine == -2));
-                const int s = t % kSlots, round = t / kSlots;
-                if (round > 0) await(empty + s, (round - 1) & 1);
-                if (!live) break;
-                uint64_t* bar = told(t);
-                if (lane == 0) {
-                    if constexpr (G::q8) raw_sm[2 * h + s] = mine;
-                    else if (h) miss_sm[s] = miss;
-                    else kmiss_sm[t & 15] = miss;
-                    if (!there) mbar_arrive(bar);
-                    else mbar_arrive_expect_tx(bar, G::q8 ? kQ8Half : __popc(there) * piece_rows * D * 2);
+                if (does_k && does_v) {
+                    if (t > 0) ask(1, v_g, v_t0, v_page, t - 1);
+                    ask(0, it.g, t0, mine, t);
+                    v_page = mine, v_t0 = t0, v_g = it.g;
+                } else {
+                    ask(does_v, it.g, t0, mine, t);
                 }
-                __syncwarp();
-                if (mine >= 0) {
-                    fence_proxy_async_smem();  // the slot's generic accesses, before the copies
-                    if constexpr (G::q8) {
-                        bulk_g2s(ring + s * kQ8Half, p.pool + (static_cast<int64_t>(mine) * p.kv_heads + it.g) * kQ8Rec + h * kQ8Half, kQ8Half, bar, policy);
-                    } else {
-                        const int y = ((mine * p.kv_heads + it.g) * 2 + h) * p.page_tokens + ((t0 + lane * piece_rows) & (p.page_tokens - 1));
-#pragma unroll
-                        for (int x = 0; x < D / 64; ++x)
-                            tma_load_hint(ring + s * G::tile + x * TN * 128 + lane * piece_rows * 128, &map, 64 * x, y, bar, policy);
-                    }
-                }
-                __syncwarp();
             }
         }
+        if (does_k && does_v && t > 0 && live) ask(1, v_g, v_t0, v_page, t - 1);
         if (!live && lane == 0) {
             // let every copy still in flight land before the block exits: the last of each slot
             volatile int go_on = 0;
-            for (int i = max(0, t - kSlots); i <= t; ++i)
-                mbar_wait_bounded(told(i), (i / (!G::q8 && !h ? G::k_told : kSlots)) & 1, &go_on, 100000000ull);
+            for (int h = does_k ? 0 : 1; h <= (does_v ? 1 : 0); ++h)
+                for (int i = max(0, t - kSlots - 1); i <= t; ++i)
+                    mbar_wait_bounded(told(h, i), (i / (!G::q8 && !h ? G::k_told : kSlots)) & 1, &go_on, 100000000ull);
         }
     } else if (warp == 1 || (warp == 3 && NS == 2)) {
         // ---------------------------------------------------------------- a stream's products
@@ -605,12 +619,12 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                     *abort_flag = 1;
                 }
             };
-            const uint32_t qd = static_cast<uint32_t>(smem_desc_sw128(smem_u32(sm + G::off_q + (p.decode ? 0 : s * G::q_tile))));
+            const uint32_t qd = static_cast<uint32_t>(smem_desc_sw128(smem_u32(sm + G::off_q + (DEC ? 0 : s * G::q_tile))));
             const uint32_t kd = static_cast<uint32_t>(smem_desc_sw128(smem_u32(sm)));
             const uint32_t vd = static_cast<uint32_t>(G::q8 ? smem_desc_sw128(smem_u32(sm + G::off_v)) : desc_mn(smem_u32(sm + G::off_v), TN * 128));
             const uint32_t col = tmem + s * 2 * kHalf, o = tmem + G::col_o + s * D;
             uint64_t *sf = sfull + 2 * s, *pf = pfull + 2 * s;
-            const bool shares = NS == 2 && !p.decode;  // both streams see every tile
+            const bool shares = NS == 2 && !DEC;  // both streams see every tile
             int t = 0, n = 0, m = 0;  // tiles so far; of this stream: scores asked for, and P V
             int pend = -1;            // the tile whose P V is still to come
             uint32_t acc = 0;
@@ -667,11 +681,11 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                     continue;
                 }
                 // (decode steps: the first stream's queries are the second's as well)
-                wait(qfull + (p.decode ? 0 : s), (p.decode ? k : both) & 1);
+                wait(qfull + (DEC ? 0 : s), (DEC ? k : both) & 1);
                 ++both;
                 bool begun = false;
                 for (int i = 0; i < nt && live; ++i, ++t) {
-                    if (NS == 2 && p.decode && (tile_at(it, i) & 1) != s) continue;
+                    if (NS == 2 && DEC && (tile_at(it, i) & 1) != s) continue;
                     if (G::halves && pend >= 0) product_pv();
                     wait(kfull + t % G::k_told, (t / G::k_told) & 1);
                     if (!live) break;
@@ -764,7 +778,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
         for (int item = blockIdx.x; item < total; item += gridDim.x) {
             // (the record stays until the item's end, where what the loop has no registers for is read again)
             await(ifull + (k & 1), (k >> 1) & 1);
-            if (NS == 2 && p.decode && merges > 0) await(mfree, (merges - 1) & 1);  // (the last item's outputs are read)
+            if (NS == 2 && DEC && merges > 0) await(mfree, (merges - 1) & 1);  // (the last item's outputs are read)
             if (over()) break;
             // (read as it is needed: the scores take most registers)
             const volatile Record& it = item_sm[k & 1];
@@ -775,8 +789,8 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                 if (lane == 0) mbar_arrive(iempty + (k & 1));
                 ++k;
             };
-            const int c0 = it.q0 + (NS == 2 && !p.decode ? 128 * s : 0), q = c0 + me;
-            if (NS == 2 && !p.decode && s == 1 && c0 >= it.nq) {  // the item has one tile of queries
+            const int c0 = it.q0 + (NS == 2 && !DEC ? 128 * s : 0), q = c0 + me;
+            if (NS == 2 && !DEC && s == 1 && c0 >= it.nq) {  // the item has one tile of queries
                 tiles += nt;
                 release();
                 continue;
@@ -786,7 +800,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
             const int row = it.r0 + (valid ? q / p.group : 0), head = it.g * p.group + (valid ? q % p.group : 0);
             const int len = valid ? length_of(p, row) : 0, from = max(0, len - p.window), first = min(p.sinks, len);
             const int nq = it.nq;
-            if (s == 0 || !p.decode) {  // the queries, swizzled as the copies do: D / 8 lanes a row
+            if (s == 0 || !DEC) {  // the queries, swizzled as the copies do: D / 8 lanes a row
                 constexpr int L = D / 8 < 32 ? D / 8 : 32, R = 32 / L;  // lanes of a row, rows at once
                 constexpr int kRows = 32 / G::H;                        // the warp's
                 const int c = lane % L;
@@ -820,7 +834,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
             for (int i = 0; i < nt; ++i, ++tile, ++tiles) {
                 if (i == na && i) tile = it.b0;
                 const int t0 = tile * TN + half * kHalf;
-                if (NS == 2 && p.decode && (tile & 1) != s) continue;
+                if (NS == 2 && DEC && (tile & 1) != s) continue;
                 const int x = G::halves ? 2 * s : 2 * s + (n & 1);
                 const uint32_t scol = lanes + x * kHalf;  // S; the thread's half, and P, from pcol on
                 const uint32_t pcol = scol + half * kHalf;
@@ -965,7 +979,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
 
             // ---- what became of the item
             float w0 = 1.f, w1 = 0.f;  // the streams' weights
-            const bool merge = NS == 2 && p.decode;
+            const bool merge = NS == 2 && DEC;
             if (merge) {  // the streams' softmaxes have the same lanes of tensor memory: each takes half of both's dims
                 ml_sm[128 * s + me] = make_float2(base, l);
                 __syncwarp();
@@ -990,7 +1004,7 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
                 release();
                 continue;
             }
-            const int query = it.q0 + (NS == 2 && !p.decode ? 128 * s : 0) + me, item_chunk = it.chunk;
+            const int query = it.q0 + (NS == 2 && !DEC ? 128 * s : 0) + me, item_chunk = it.chunk;
             bool write = query < it.nq;
             const int row2 = it.r0 + (write ? query / p.group : 0), head2 = it.g * p.group + (write ? query % p.group : 0);
             const int len2 = write ? length_of(p, row2) : 0;
@@ -1198,26 +1212,28 @@ __global__ void __launch_bounds__(Geo<FMT, D>::threads, 1)
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-template <int FMT, int D>
+template <int FMT, int D, bool DEC>
 cudaError_t launch_one(const Launch& a, cudaStream_t s) {
-    using G = Geo<FMT, D>;
+    using G = Geo<FMT, D, DEC>;
     static_assert(G::smem(kMaxAgents) <= kMaxShared);
     static Once once;
     // (the registers that the roles deal out are those of the launch: fewer would leave a role waiting)
     static const int regs = [] {
         cudaFuncAttributes f = {};
-        return cudaFuncGetAttributes(&f, attend_window_tc<FMT, D>) == cudaSuccess ? f.numRegs : 0;
+        return cudaFuncGetAttributes(&f, attend_window_tc<FMT, D, DEC>) == cudaSuccess ? f.numRegs : 0;
     }();
-    if (G::streams == 2 && regs < 128) return cudaErrorLaunchOutOfResources;
-    const cudaError_t e = once.allow_shared(attend_window_tc<FMT, D>, a.device);
+    if (G::streams == 2 && regs < (G::threads == 512 ? 128 : 168)) return cudaErrorLaunchOutOfResources;
+    const cudaError_t e = once.allow_shared(attend_window_tc<FMT, D, DEC>, a.device);
     if (e != cudaSuccess) return e;
-    attend_window_tc<FMT, D><<<a.grid, G::threads, G::smem(a.p.agents), s>>>(a.map, a.p);
+    attend_window_tc<FMT, D, DEC><<<a.grid, G::threads, G::smem(a.p.agents), s>>>(a.map, a.p);
     return cudaGetLastError();
 }
 
-cudaError_t launch_q8(const Launch& a, cudaStream_t s);
-cudaError_t launch_f16(const Launch& a, int head_dim, cudaStream_t s);
-cudaError_t launch_bf16(const Launch& a, int head_dim, cudaStream_t s);
+cudaError_t launch_q8(const Launch& a, bool decode, cudaStream_t s);
+cudaError_t launch_f16_prompts(const Launch& a, int head_dim, cudaStream_t s);
+cudaError_t launch_f16_decode(const Launch& a, int head_dim, cudaStream_t s);
+cudaError_t launch_bf16_prompts(const Launch& a, int head_dim, cudaStream_t s);
+cudaError_t launch_bf16_decode(const Launch& a, int head_dim, cudaStream_t s);
 
 }  // namespace window
 }  // namespace qmm

@@ -1,0 +1,10 @@
+// Attention with a sliding window: the kernels for decode steps over the bf16 pools.
+#include "qmm_kv_window.cuh"
+
+namespace qmm {
+namespace window {
+cudaError_t launch_bf16_decode(const Launch& a, int head_dim, cudaStream_t s) {
+    return head_dim == 64 ? launch_one<QMM_KV_BF16, 64, true>(a, s) : launch_one<QMM_KV_BF16, 128, true>(a, s);
+}
+}  // namespace window
+}  // namespace qmm
