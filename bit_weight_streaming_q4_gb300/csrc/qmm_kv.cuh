@@ -84,6 +84,15 @@ public:
         if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
         return e;
     }
+    // clusters of up to 16 blocks
+    template <typename K>
+    cudaError_t allow_cluster(K kernel, int dev) {
+        const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t{1} << dev : 0;
+        if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+        return e;
+    }
 };
 
 // Exclusive prefix of `v` over the block's threads (blockDim.x a multiple of 32, at most 1024)

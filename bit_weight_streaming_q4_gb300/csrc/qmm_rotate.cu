@@ -1,18 +1,18 @@
 // Norms of queries and keys with the position rotation, in one pass over the qkv matmul's output.
 //
-// A warp takes a head: a lane holds D / 32 neighbouring dims, the sum of squares is a butterfly, and a
-// dim's partner of the rotation is in the same lane (interleaved pairs) or in another one (halves),
-// from which a shuffle brings it.  Cosine and sine of a row's rot_dim / 2 angles are formed once per block, for all
-// of its heads.  An angle is pos * f turns, f = inv_freq / 2 pi as a 64-bit fraction of a turn: the
-// product modulo 2^64 drops whole turns exactly, for any position, in integers (64-bit floating point
-// runs at 1/64 of fp32's rate here; one multiplication per angle is left of it).
+// D / 16 lanes take a head, a lane two pieces of 8 neighbouring dims each: those of the first and of the second half that
+// turn together (or, interleaved, any two), so that a rotation stays in a lane and a head's sum of squares takes
+// log2(D / 16) shuffles.  (A warp a head, with shuffles for both, took 115 us for the case below.)  Cosine and sine of a
+// row's rot_dim / 2 angles are formed once per block, for all of its heads.  An angle is pos * f turns, f = inv_freq / 2 pi as
+// a 64-bit fraction of a turn: the product modulo 2^64 drops whole turns exactly, for any position, in integers
+// (64-bit floating point runs at 1/64 of fp32's rate here; one multiplication per angle is left of it).
 #include "qmm_decode.h"
 #include "qmm_kv.cuh"
 
 namespace qmm {
 namespace rotate {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 
 struct Params {
@@ -28,7 +28,8 @@ struct Params {
     int64_t q_stride, k_stride, q_out_stride, k_out_stride, rows;
     int32_t heads, kv_heads, half, axes, interleaved;  // half: rot_dim / 2
     int32_t q_type, k_type;
-    int32_t vec;    // inputs can be read, and outputs written, by a lane's dims at once
+    int32_t vec;    // inputs can be read, and outputs written, 16 bytes at a time
+    int32_t weight_vec;  // .. and the weights
     int32_t parts;  // blocks that share a row's heads
     float eps;
 };
@@ -37,20 +38,21 @@ __device__ __forceinline__ float as_f32(float v) { return v; }
 __device__ __forceinline__ float as_f32(__half v) { return __half2float(v); }
 __device__ __forceinline__ float as_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-template <typename T, int E>
-struct alignas(sizeof(T) * E <= 16 ? sizeof(T) * E : 16) Pack {
-    T v[E];
-};
-
-template <typename T, int E>
-__device__ __forceinline__ void load(const T* p, bool vec, float (&x)[E]) {
+// Eight neighbouring elements.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, bool vec, float (&x)[8]) {
     if (vec) {
-        const Pack<T, E> w = *reinterpret_cast<const Pack<T, E>*>(p);
+        constexpr int N = 8 * sizeof(T) / 16;
+        uint4 w[N];
 #pragma unroll
-        for (int i = 0; i < E; ++i) x[i] = as_f32(w.v[i]);
+        for (int i = 0; i < N; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+        T v[8];
+        memcpy(v, w, sizeof(v));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = as_f32(v[i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i) x[i] = as_f32(p[i]);
+        for (int i = 0; i < 8; ++i) x[i] = as_f32(p[i]);
     }
 }
 
@@ -58,97 +60,117 @@ __device__ __forceinline__ void to(float& d, float v) { d = v; }
 __device__ __forceinline__ void to(__half& d, float v) { d = __float2half_rn(v); }
 __device__ __forceinline__ void to(__nv_bfloat16& d, float v) { d = __float2bfloat16_rn(v); }
 
-template <typename T, int E>
-__device__ __forceinline__ void store(T* p, bool vec, const float (&x)[E]) {
-    Pack<T, E> w;
+template <typename T>
+__device__ __forceinline__ void store8(T* p, bool vec, const float (&x)[8]) {
+    T v[8];
 #pragma unroll
-    for (int i = 0; i < E; ++i) to(w.v[i], x[i]);
+    for (int i = 0; i < 8; ++i) to(v[i], x[i]);
     if (vec) {
-        *reinterpret_cast<Pack<T, E>*>(p) = w;
+        constexpr int N = 8 * sizeof(T) / 16;
+        uint4 w[N];
+        memcpy(w, v, sizeof(v));
+#pragma unroll
+        for (int i = 0; i < N; ++i) reinterpret_cast<uint4*>(p)[i] = w[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i) p[i] = w.v[i];
+        for (int i = 0; i < 8; ++i) p[i] = v[i];
     }
 }
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) rotate_kernel(const Params p) {
-    constexpr int E = D / 32;
-    __shared__ float2 turn[D / 2];  // cos, sin
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int L = D / 16;             // lanes of a head
+    constexpr int kHeads = 32 / L;        // heads that a warp takes at a time
+    __shared__ float2 turn[D / 2];        // cos, sin
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, i = lane % L;
     const int64_t row = blockIdx.x / p.parts;
     const int part = static_cast<int>(blockIdx.x % p.parts);
-    const int all = p.heads + p.kv_heads;
+    const int all = p.heads + p.kv_heads, eighth = p.half / 8;
+    // the lane's pieces: dims a0 .. a0 + 7 and b0 .. b0 + 7
+    const bool turns = p.interleaved ? false : i < eighth;
+    const int a0 = 8 * (turns ? i : p.interleaved ? 2 * i : 2 * eighth + 2 * (i - eighth)), b0 = turns ? a0 + p.half : a0 + 8;
+    const int first = (part * kWarps + warp) * kHeads + lane / L, step = p.parts * kWarps * kHeads;
     auto source = [&](int h) {
         const bool is_q = h < p.heads;
         const int64_t at = is_q ? row * p.q_stride + static_cast<int64_t>(h) * D : row * p.k_stride + static_cast<int64_t>(h - p.heads) * D;
-        return static_cast<const T*>(is_q ? p.q : p.k) + at + lane * E;
+        return static_cast<const T*>(is_q ? p.q : p.k) + at;
     };
-    const int first = part * kWarps + warp, step = p.parts * kWarps;
-    float x[E];
-    if (first < all) load<T, E>(source(first), p.vec, x);  // (on its way while the angles are formed)
-    if (tid < p.half) {
-        const int ax = p.axis ? p.axis[tid] : 0;
+    float xa[8], xb[8];
+    auto fetch = [&](int h) {
+        if (h >= all) return;
+        const T* src = source(h);
+        load8(src + a0, p.vec, xa);
+        load8(src + b0, p.vec, xb);
+    };
+    fetch(first);  // (on its way while the angles are formed)
+    for (int f = tid; f < p.half; f += kThreads) {
+        const int ax = p.axis ? p.axis[f] : 0;
         const int32_t at = p.pos[static_cast<int64_t>(ax >= 0 && ax < p.axes ? ax : 0) * p.rows + row];
-        const double f = static_cast<double>(p.inv_freq[tid]) * 0.15915494309189535;  // 1 / 2 pi: turns per position
-        const double part_of_turn = f - floor(f);
+        const double per = static_cast<double>(p.inv_freq[f]) * 0.15915494309189535;  // 1 / 2 pi: turns per position
+        const double part_of_turn = per - floor(per);
         const uint64_t u = static_cast<uint64_t>(part_of_turn * 18446744073709551616.0) * static_cast<uint64_t>(static_cast<int64_t>(at));
         // the nearest of the turns, as half turns in -1 .. 1
         float c, s;
         sincospif(static_cast<float>(static_cast<int32_t>(u >> 32)) * 4.656612873077393e-10f, &s, &c);
-        if (!isfinite(f)) c = s = __int_as_float(0x7FFFFFFF);
-        turn[tid] = make_float2(c, s);
+        if (!isfinite(per)) c = s = __int_as_float(0x7FFFFFFF);
+        turn[f] = make_float2(c, s);
     }
     __syncthreads();
-    for (int h = first; h < all; h += step) {
+    // the angles of the lane's pairs: dims (a0 + j, b0 + j), or interleaved (a0 + 2 j, a0 + 2 j + 1), then those of b0
+    float c[8], s[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int f = p.interleaved ? (j < 4 ? a0 / 2 + j : b0 / 2 + j - 4) : a0 + j;
+        const float2 t = (p.interleaved ? f < p.half : turns) ? turn[f] : make_float2(1.f, 0.f);
+        c[j] = t.x, s[j] = t.y;
+    }
+    for (int h0 = first - lane / L; h0 < all; h0 += step) {  // (the same for the warp: its lanes meet in shuffles)
+        const int h = h0 + lane / L;
         const bool is_q = h < p.heads;
-        float y[E];
+        float ya[8], yb[8];
 #pragma unroll
-        for (int i = 0; i < E; ++i) y[i] = x[i];
-        if (h + step < all) load<T, E>(source(h + step), p.vec, x);
+        for (int j = 0; j < 8; ++j) ya[j] = xa[j], yb[j] = xb[j];
+        fetch(h + step);
         const float* weight = is_q ? p.q_weight : p.k_weight;
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum = fmaf(ya[j], ya[j], fmaf(yb[j], yb[j], sum));
+#pragma unroll
+        for (int k = L / 2; k >= 1; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+        if (h >= all) continue;
         if (weight) {
-            float sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < E; ++i) sum = fmaf(y[i], y[i], sum);
-#pragma unroll
-            for (int k = 16; k >= 1; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
             const float r = rsqrtf(sum * (1.f / D) + p.eps);
+            float wa[8], wb[8];
+            load8(weight + a0, p.weight_vec, wa);
+            load8(weight + b0, p.weight_vec, wb);
 #pragma unroll
-            for (int i = 0; i < E; ++i) y[i] = y[i] * r * weight[lane * E + i];
+            for (int j = 0; j < 8; ++j) ya[j] = ya[j] * r * wa[j], yb[j] = yb[j] * r * wb[j];
         }
-        const int d0 = lane * E;
-        float out[E];
         if (p.interleaved) {
+            const bool turns_a = a0 < 2 * p.half, turns_b = b0 < 2 * p.half;  // (of 16 dims that turn, both do)
 #pragma unroll
-            for (int i = 0; i < E; i += 2) {
-                out[i] = y[i], out[i + 1] = y[i + 1];
-                if (d0 + i < 2 * p.half) {
-                    const float2 t = turn[(d0 + i) >> 1];
-                    out[i] = y[i] * t.x - y[i + 1] * t.y;
-                    out[i + 1] = y[i] * t.y + y[i + 1] * t.x;
-                }
+            for (int j = 0; j < 4; ++j) {
+                const float u = ya[2 * j], v = ya[2 * j + 1], x = yb[2 * j], y = yb[2 * j + 1];
+                if (turns_a) ya[2 * j] = u * c[j] - v * s[j], ya[2 * j + 1] = u * s[j] + v * c[j];
+                if (turns_b) yb[2 * j] = x * c[j + 4] - y * s[j + 4], yb[2 * j + 1] = x * s[j + 4] + y * c[j + 4];
             }
-        } else {
-            // (half is a multiple of 8, and so of E: a lane's dims are all of the first half, of the second, or neither)
-            const bool low = d0 < p.half, in = d0 < 2 * p.half;
-            const int other = in ? lane + (low ? p.half : -p.half) / E : lane;
+        } else if (turns) {
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const float z = __shfl_sync(0xffffffffu, y[i], other);
-                out[i] = y[i];
-                if (in) {
-                    const float2 t = turn[low ? d0 + i : d0 + i - p.half];
-                    out[i] = y[i] * t.x + (low ? -z : z) * t.y;
-                }
+            for (int j = 0; j < 8; ++j) {
+                const float u = ya[j], v = yb[j];
+                ya[j] = u * c[j] - v * s[j], yb[j] = u * s[j] + v * c[j];
             }
         }
         void* base = is_q ? p.q_out : p.k_out;
-        const int64_t at = (is_q ? row * p.q_out_stride + static_cast<int64_t>(h) * D : row * p.k_out_stride + static_cast<int64_t>(h - p.heads) * D) + d0;
+        const int64_t at = is_q ? row * p.q_out_stride + static_cast<int64_t>(h) * D : row * p.k_out_stride + static_cast<int64_t>(h - p.heads) * D;
         const int type = is_q ? p.q_type : p.k_type;
-        if (type == QMM_TYPE_F32) store<float, E>(static_cast<float*>(base) + at, p.vec, out);
-        else if (type == QMM_TYPE_F16) store<__half, E>(static_cast<__half*>(base) + at, p.vec, out);
-        else store<__nv_bfloat16, E>(static_cast<__nv_bfloat16*>(base) + at, p.vec, out);
+        auto store = [&](auto* out) {
+            store8(out + at + a0, p.vec, ya);
+            store8(out + at + b0, p.vec, yb);
+        };
+        if (type == QMM_TYPE_F32) store(static_cast<float*>(base));
+        else if (type == QMM_TYPE_F16) store(static_cast<__half*>(base));
+        else store(static_cast<__nv_bfloat16*>(base));
     }
 }
 
@@ -203,10 +225,11 @@ extern "C" qmm_status qmm_rotate(const qmm_rotate_dims* d, const void* q, int64_
     auto whole = [&](const void* a, int64_t stride, int32_t type) { return aligned(a, 16) && stride * size(type) % 16 == 0; };
     p.vec = (!d->heads || (whole(q, q_stride, d->in_type) && whole(q_out, q_out_stride, d->q_type))) &&
             (!d->kv_heads || (whole(k, k_stride, d->in_type) && whole(k_out, k_out_stride, d->k_type)));
-    // a block per row, or more of them where that leaves SMs without one, down to a head per warp
-    const int all = d->heads + d->kv_heads, most = (all + kWarps - 1) / kWarps;
+    p.weight_vec = aligned(q_weight, 16) && aligned(k_weight, 16);
+    // a block per row, or more of them where that leaves SMs without one, down to a round of heads per warp
+    const int all = d->heads + d->kv_heads, round = kWarps * 32 / (d->head_dim / 16), most = (all + round - 1) / round;
     p.parts = 1;
-    while (p.parts < most && rows * p.parts < 2 * sms) ++p.parts;
+    while (p.parts < most && rows * p.parts < 4 * sms) ++p.parts;
     if (rows > INT32_MAX / p.parts) return QMM_ERR_UNSUPPORTED_SHAPE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = d->in_type == QMM_TYPE_F32   ? launch<float>(p, d->head_dim, s)

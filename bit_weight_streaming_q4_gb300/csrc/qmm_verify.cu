@@ -25,9 +25,15 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kPer = 32;                 // columns per thread and segment
 constexpr int kSeg = kThreads * kPer;
 constexpr int kSteps = kPer / 4;         // a thread's columns are kSteps runs of 4
-constexpr int kRanks = 8;                // blocks per sequence of the second kernel
+constexpr int kChoose = 512;             // threads of the second kernel ..
+constexpr int kChooseWarps = kChoose / 32;
+constexpr int kMaxRanks = 16;            // .. and blocks per sequence
+constexpr int kStep = 4 * kChoose;       // columns that one of its blocks takes at a time
+constexpr int kSpan = 4;                 // steps whose loads are on their way at once
+constexpr int kKept = 32;                // rows of a sequence whose joined numbers are kept for the choice
 constexpr int kMaxColumns = 1 << 19;
 constexpr int kMaxSegs = kMaxColumns / kSeg;
+constexpr int kMaxSteps = kMaxColumns / kStep / 8 + 1;  // of a block (8 blocks a sequence at least)
 constexpr int kShift = 44;               // weights count 2^-44
 
 struct alignas(16) Stat {
@@ -51,7 +57,8 @@ struct Params {
     int* err;
     int64_t stride, draft_stride;
     int32_t rows, n, segs, agents;
-    int32_t vec, draft_vec;  // rows can be read 16 bytes at a time
+    int32_t vec, draft_vec;  // rows can be read four columns at a time
+    int32_t ranks;           // blocks per sequence of the second kernel, 8 or 16
 };
 
 __device__ __forceinline__ float as_f32(float v) { return v; }
@@ -150,17 +157,6 @@ __device__ __forceinline__ void load4(const T* row, bool vec, int col, int n, fl
     }
 }
 
-// The sequence that holds row r, or -1.  agent_rows does not fall.
-__device__ __forceinline__ int sequence_of(const Params& p, int r) {
-    int lo = 0, hi = p.agents;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.agent_rows[mid] <= r) lo = mid;
-        else hi = mid;
-    }
-    return p.agent_rows[lo] <= r && r < p.agent_rows[lo + 1] ? lo : -1;
-}
-
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 3) verify_stats(const Params p) {
     __shared__ Table table;
@@ -178,10 +174,15 @@ __global__ void __launch_bounds__(kThreads, 3) verify_stats(const Params p) {
     float x[kSteps][4];
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) load4<T>(base, vec, seg * kSeg + (i * kThreads + tid) * 4, p.n, x[i]);
-    if (tid == 0) {
-        const int a = sequence_of(p, row);
-        first_sm = a < 0 || (draft && p.agent_rows[a] == row);  // (a row that nobody asks for)
-        scale_sm = a < 0 ? Two{0.f, 0.f} : scale_of(p, a);
+    if (tid == 0) first_sm = 1;
+    __syncthreads();
+    // the row's sequence (where agent_rows falls there may be several: nobody asks for what comes of it)
+    for (int a = tid; a < p.agents; a += kThreads) {
+        const int r0 = p.agent_rows[a];
+        if (r0 <= row && row < p.agent_rows[a + 1] && !(draft && r0 == row)) {
+            scale_sm = scale_of(p, a);
+            first_sm = 0;
+        }
     }
     fill(table);
     // ---- the largest, its lowest column, and whether something is no number
@@ -281,20 +282,22 @@ struct Choice {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) verify_choose(const Params p) {
+__global__ void __launch_bounds__(kChoose) verify_choose(const Params p) {
     __shared__ Table table;
     __shared__ Choice choice;
+    __shared__ Joined kept[2][kKept];          // target rows, draft rows
     __shared__ int refused;                    // lowest refused draft
-    __shared__ uint64_t share[kRanks];         // the blocks' sums (each block's own copy)
-    __shared__ uint64_t part[kSteps * kWarps];
-    __shared__ int found;
+    __shared__ uint64_t share[kMaxRanks];      // the blocks' sums (each block's own copy)
+    __shared__ uint64_t part[kMaxSteps * kChooseWarps];
     cg::cluster_group cluster = cg::this_cluster();
-    const int rank = static_cast<int>(cluster.block_rank()), a = blockIdx.x / kRanks;
+    const int rank = static_cast<int>(cluster.block_rank()), ranks = p.ranks, a = blockIdx.x / ranks;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     bool falls = false;
-    for (int i = tid; i < p.agents; i += kThreads) falls |= p.agent_rows[i + 1] < p.agent_rows[i];
+    for (int i = tid; i < p.agents; i += kChoose) falls |= p.agent_rows[i + 1] < p.agent_rows[i];
     fill(table);
     const int r0 = p.agent_rows[a], r1 = p.agent_rows[a + 1];
+    const Two scale = scale_of(p, a);
+    const float sample = p.sample_u[a];
     if (tid == 0) refused = INT32_MAX;
     falls = __syncthreads_or(falls);
     griddep_wait();  // the first kernel's numbers are there
@@ -304,15 +307,20 @@ __global__ void __launch_bounds__(kThreads) verify_choose(const Params p) {
         if (tid == 0 && rank == 0) p.accepted[a] = 0, p.token[a] = -1;
         return;  // (the whole cluster)
     }
-    const Two scale = scale_of(p, a);
     const bool greedy = scale.hi == 0.f;
     const T* logits = static_cast<const T*>(p.logits);
     const T* drafts = static_cast<const T*>(p.draft);
     // ---- the drafts: a warp each
-    for (int r = r0 + 1 + warp; r < r1; r += kWarps) {
-        const Joined tp = join(p, false, r - 1, scale, table);
+    for (int r = r0 + 1 + warp; r < r1; r += kChooseWarps) {
         const int x = p.tokens[r];
         const bool in = x >= 0 && x < p.n;
+        // (what the joins do not need is asked for before them)
+        const float xp = in ? as_f32(logits[(r - 1) * p.stride + x]) : 0.f, xq = in && drafts ? as_f32(drafts[r * p.draft_stride + x]) : 0.f;
+        const float u = p.accept_u[r];
+        const Joined tp = join(p, false, r - 1, scale, table);
+        Joined tq = tp;
+        if (drafts && !greedy) tq = join(p, true, r, scale, table);
+        if (lane == 0 && r - r0 <= kKept) kept[0][r - r0 - 1] = tp, kept[1][r - r0 - 1] = tq;
         bool yes = false;
         float prob = 0.f;
         if (tp.odd) {
@@ -322,21 +330,16 @@ __global__ void __launch_bounds__(kThreads) verify_choose(const Params p) {
             prob = yes ? 1.f : 0.f;
         } else {
             double wq = 1, zq = 1;
-            bool none = false;
-            if (drafts) {
-                const Joined tq = join(p, true, r, scale, table);
-                none = tq.odd || tq.m == -INFINITY;
-                if (in && !none) {
-                    wq = weight_of(as_f32(drafts[r * p.draft_stride + x]), tq.m, scale, table);
-                    zq = static_cast<double>(tq.z);
-                }
+            const bool none = drafts && (tq.odd || tq.m == -INFINITY);
+            if (drafts && in && !none) {
+                wq = weight_of(xq, tq.m, scale, table);
+                zq = static_cast<double>(tq.z);
             }
             if (none) {
                 prob = __int_as_float(0x7FFFFFFF);
             } else if (in && tp.m > -INFINITY) {
-                const double wp = weight_of(as_f32(logits[(r - 1) * p.stride + x]), tp.m, scale, table);
-                const double zp = static_cast<double>(tp.z);
-                yes = static_cast<double>(p.accept_u[r]) * (wq * zp) < wp * zq;
+                const double wp = weight_of(xp, tp.m, scale, table), zp = static_cast<double>(tp.z);
+                yes = static_cast<double>(u) * (wq * zp) < wp * zq;
                 prob = wp * zq >= wq * zp ? (wp > 0 ? 1.f : 0.f) : static_cast<float>(wp * zq / (wq * zp));
             }
         }
@@ -355,11 +358,12 @@ __global__ void __launch_bounds__(kThreads) verify_choose(const Params p) {
         c.taken = c.row - r0;
         c.how = kPlain;
         c.column = -1;
-        c.p = join(p, false, c.row, scale, table);
+        const bool have = no != INT32_MAX && no - r0 <= kKept;
+        c.p = have ? kept[0][no - r0 - 1] : join(p, false, c.row, scale, table);
         c.q = c.p;
         if (no != INT32_MAX && !greedy) {
             if (drafts) {
-                c.q = join(p, true, no, scale, table);
+                c.q = have ? kept[1][no - r0 - 1] : join(p, true, no, scale, table);
                 if (!c.q.odd && c.q.m > -INFINITY) c.how = kLess;
             } else {
                 c.column = p.tokens[no];
@@ -392,39 +396,41 @@ __global__ void __launch_bounds__(kThreads) verify_choose(const Params p) {
         }
         return w;
     };
-    auto run = [&](int seg, int i, uint64_t (&w)[4]) -> uint64_t {  // four columns and their sum
-        const int col = seg * kSeg + (i * kThreads + tid) * 4;
-        float x[4], y[4] = {};
-        load4<T>(prow, p.vec, col, p.n, x);
-        if (how == kLess) load4<T>(qrow, p.draft_vec, col, p.n, y);
-        uint64_t sum = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sum += w[j] = left(x[j], y[j], col + j);
-        return sum;
-    };
-    // segments of this block: neighbouring ones
-    const int per = (p.segs + kRanks - 1) / kRanks;
-    const int seg0 = min(p.segs, rank * per), seg1 = min(p.segs, seg0 + per);
+    // this block's columns: neighbouring steps; a thread has four neighbouring columns of each
+    const int steps = (p.n + kStep - 1) / kStep, per = (steps + ranks - 1) / ranks;
+    const int step0 = min(steps, rank * per), step1 = min(steps, step0 + per);
     uint64_t total = 0, before = 0, mine = 0;
     for (;;) {
-        uint64_t sum = 0;
-        for (int seg = seg0; seg < seg1; ++seg)
-            for (int i = 0; i < kSteps; ++i) {
-                uint64_t w[4];
-                sum += run(seg, i, w);
+        for (int s0 = step0; s0 < step1; s0 += kSpan) {
+            float x[kSpan][4], y[kSpan][4];
+#pragma unroll
+            for (int i = 0; i < kSpan; ++i) {
+                const int col = s0 + i < step1 ? (s0 + i) * kStep + 4 * tid : p.n;
+                load4<T>(prow, p.vec, col, p.n, x[i]);
+                if (how == kLess) load4<T>(qrow, p.draft_vec, col, p.n, y[i]);
             }
 #pragma unroll
-        for (int k = 16; k >= 1; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-        if (lane == 0) part[warp] = sum;
+            for (int i = 0; i < kSpan; ++i) {
+                if (s0 + i >= step1) break;
+                uint64_t sum = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sum += left(x[i][j], how == kLess ? y[i][j] : 0.f, (s0 + i) * kStep + 4 * tid + j);
+#pragma unroll
+                for (int k = 16; k >= 1; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+                if (lane == 0) part[(s0 + i - step0) * kChooseWarps + warp] = sum;
+            }
+        }
         __syncthreads();
-        if (tid < kRanks) {
-            mine = 0;
-            for (int w = 0; w < kWarps; ++w) mine += part[w];
-            *cluster.map_shared_rank(&share[rank], tid) = mine;
+        if (warp == 0) {
+            uint64_t sum = 0;
+            for (int i = lane; i < (step1 - step0) * kChooseWarps; i += 32) sum += part[i];
+#pragma unroll
+            for (int k = 16; k >= 1; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+            if (lane < ranks) *cluster.map_shared_rank(&share[rank], lane) = sum;
         }
         cluster.sync();
         total = before = 0;
-        for (int i = 0; i < kRanks; ++i) {
+        for (int i = 0; i < ranks; ++i) {
             if (i < rank) before += share[i];
             total += share[i];
         }
@@ -433,69 +439,71 @@ __global__ void __launch_bounds__(kThreads) verify_choose(const Params p) {
         how = kPlain;  // (p and q alike but for their roundings)
         cluster.sync();
     }
-    cluster.sync();  // (nobody leaves while others write to it)
-    // ---- the lowest column whose running sum passes u * total
-    const double u = fmin(fmax(static_cast<double>(p.sample_u[a]), 0.0), 1.0);
+    // ---- the lowest column whose running sum passes u * total  (nobody writes to another block any more)
+    const double u = fmin(fmax(static_cast<double>(sample), 0.0), 1.0);
     uint64_t target = __double2ull_rd(u * static_cast<double>(total));
     if (target >= total) target = total - 1;
-    if (target < before || target >= before + mine) return;
-    uint64_t rest = target - before;
-    for (int seg = seg0; seg < seg1; ++seg) {
-        for (int i = 0; i < kSteps; ++i) {
-            uint64_t w[4];
-            uint64_t sum = run(seg, i, w);
+    if (warp > 0 || target < before || target >= before + mine) return;
+    // the part in which it falls: part[step][warp] is in the columns' order; a lane takes neighbouring ones
+    const uint64_t rest = target - before;
+    const int parts = (step1 - step0) * kChooseWarps, each = (parts + 31) / 32;
+    uint64_t sum = 0;
+    for (int i = lane * each; i < min(parts, (lane + 1) * each); ++i) sum += part[i];
+    uint64_t up = sum;
 #pragma unroll
-            for (int k = 16; k >= 1; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-            if (lane == 0) part[i * kWarps + warp] = sum;
-        }
-        if (tid == 0) found = -1;
-        __syncthreads();
-        uint64_t all = 0, at = 0;  // running sums over (run, warp), which is the columns' order
-        int hit = -1;
-        for (int i = 0; i < kSteps * kWarps; ++i) {
-            const uint64_t v = part[i];
-            if (hit < 0 && rest < all + v) hit = i, at = all;
-            all += v;
-        }
-        if (hit >= 0 && hit % kWarps == warp) {
-            uint64_t w[4];
-            uint64_t sum = run(seg, hit / kWarps, w), up = sum;
+    for (int k = 1; k < 32; k <<= 1) {
+        const uint64_t o = __shfl_up_sync(0xffffffffu, up, k);
+        if (lane >= k) up += o;
+    }
+    int hit = -1;
+    uint64_t low = up - sum;
+    if (rest >= low && rest < up) {
+        hit = lane * each;
+        while (rest >= low + part[hit]) low += part[hit++];
+    }
+    const int who = __ffs(__ballot_sync(0xffffffffu, hit >= 0)) - 1;  // (the parts' sums reach past rest: one lane has it)
+    hit = __shfl_sync(0xffffffffu, hit, who);
+    low = __shfl_sync(0xffffffffu, low, who);
+    // its 128 columns once more
+    const int col = (step0 + hit / kChooseWarps) * kStep + (hit % kChooseWarps) * 128 + 4 * lane;
+    float x[4], y[4] = {};
+    load4<T>(prow, p.vec, col, p.n, x);
+    if (how == kLess) load4<T>(qrow, p.draft_vec, col, p.n, y);
+    uint64_t w[4];
+    sum = 0;
 #pragma unroll
-            for (int k = 1; k < 32; k <<= 1) {
-                const uint64_t o = __shfl_up_sync(0xffffffffu, up, k);
-                if (lane >= k) up += o;
-            }
-            uint64_t low = at + up - sum;
-            if (rest >= low && rest < low + sum) {
-                int j = 0;
-                while (rest >= low + w[j]) low += w[j++];
-                found = seg * kSeg + ((hit / kWarps) * kThreads + tid) * 4 + j;
-            }
-        }
-        __syncthreads();
-        if (found >= 0) {
-            if (tid == 0) p.accepted[a] = c.taken, p.token[a] = found;
-            return;
-        }
-        rest -= all;
-        __syncthreads();
+    for (int j = 0; j < 4; ++j) sum += w[j] = left(x[j], y[j], col + j);
+    up = sum;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+        const uint64_t o = __shfl_up_sync(0xffffffffu, up, k);
+        if (lane >= k) up += o;
+    }
+    low += up - sum;
+    if (rest >= low && rest < low + sum) {
+        int j = 0;
+        while (rest >= low + w[j]) low += w[j++];
+        p.accepted[a] = c.taken, p.token[a] = col + j;
     }
 }
 
 template <typename T>
-cudaError_t launch(const Params& p, cudaStream_t s) {
+cudaError_t launch(const Params& p, int dev, cudaStream_t s) {
+    static kv::Once once;
+    const cudaError_t o = once.allow_cluster(verify_choose<T>, dev);
+    if (o != cudaSuccess) return o;
     if (p.rows > 0) {
         verify_stats<T><<<dim3(p.segs, p.rows, p.draft ? 2 : 1), kThreads, 0, s>>>(p);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.agents) * kRanks);
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3(static_cast<unsigned>(p.agents) * p.ranks);
+    cfg.blockDim = dim3(kChoose);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kRanks;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(p.ranks);
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
@@ -551,10 +559,12 @@ qmm_status qmm_verify(const void* logits, int32_t type, int64_t stride, int64_t 
     p.rows = static_cast<int32_t>(rows), p.n = static_cast<int32_t>(n), p.segs = static_cast<int32_t>(segments(n)), p.agents = agents;
     p.vec = aligned(logits, 4 * size) && stride % 4 == 0;
     p.draft_vec = aligned(draft_logits, 4 * size) && draft_stride % 4 == 0;
+    // blocks per sequence: 16 where that leaves no SM with two, and there are columns for them
+    p.ranks = int64_t{agents} * kMaxRanks <= sms && n > 8 * kStep ? kMaxRanks : 8;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = type == QMM_TYPE_F32   ? launch<float>(p, s)
-                          : type == QMM_TYPE_F16 ? launch<__half>(p, s)
-                                                 : launch<__nv_bfloat16>(p, s);
+    const cudaError_t e = type == QMM_TYPE_F32   ? launch<float>(p, dev, s)
+                          : type == QMM_TYPE_F16 ? launch<__half>(p, dev, s)
+                                                 : launch<__nv_bfloat16>(p, dev, s);
     return e == cudaSuccess ? QMM_OK : QMM_ERR_CUDA;
 }
 
