@@ -81,20 +81,56 @@ __device__ __forceinline__ Two scale_of(const Params& p, int a) {
     return two_of(1.4426950408889634074 / static_cast<double>(fminf(t, 1.2676506e30f)));
 }
 
-// 2^(i / 64) for i = 0 .. 63, as 2^44ths and as a pair.
+// 2^(i / 64) for i = 0 .. 63, as 2^44ths and as a pair.  (Rounded from 60 digits; formed on the device, whose 64-bit
+// floating point is slow, they took some microseconds a block.)
+struct alignas(16) Power {
+    uint64_t fix;
+    Two two;
+};
+__device__ const Power kPowers[64] = {
+    {17592186044416ull, {0x1.0000000000000p+0f, 0x0.0p+0f}}, {17783752390528ull, {0x1.02c9a40000000p+0f, -0x1.887fa00000000p-28f}},
+    {17977404757381ull, {0x1.059b0e0000000p+0f, -0x1.9d4f520000000p-25f}}, {18173165860252ull, {0x1.0874520000000p+0f, -0x1.e2990e0000000p-26f}},
+    {18371058661769ull, {0x1.0b55860000000p+0f, 0x1.9f31220000000p-25f}}, {18571106374610ull, {0x1.0e3ec40000000p+0f, -0x1.a585cc0000000p-25f}},
+    {18773332464219ull, {0x1.11301e0000000p+0f, -0x1.fdb4960000000p-25f}}, {18977760651566ull, {0x1.1429aa0000000p+0f, 0x1.d525bc0000000p-25f}},
+    {19184414915921ull, {0x1.172b840000000p+0f, -0x1.c157420000000p-27f}}, {19393319497675ull, {0x1.1a35be0000000p+0f, 0x1.6df96e0000000p-25f}},
+    {19604498901178ull, {0x1.1d48740000000p+0f, -0x1.d2e8ca0000000p-25f}}, {19817977897613ull, {0x1.2063b80000000p+0f, 0x1.0c519a0000000p-25f}},
+    {20033781527906ull, {0x1.2387a60000000p+0f, 0x1.ceac480000000p-25f}}, {20251935105661ull, {0x1.26b4560000000p+0f, 0x1.789f380000000p-26f}},
+    {20472464220127ull, {0x1.29e9e00000000p+0f, -0x1.5c04240000000p-25f}}, {20695394739203ull, {0x1.2d285a0000000p+0f, 0x1.b900c20000000p-26f}},
+    {20920752812471ull, {0x1.306fe00000000p+0f, 0x1.4636e20000000p-25f}}, {21148564874263ull, {0x1.33c08c0000000p+0f, -0x1.b37d200000000p-25f}},
+    {21378857646762ull, {0x1.371a740000000p+0f, -0x1.18aac60000000p-25f}}, {21611658143136ull, {0x1.3a7db40000000p+0f, -0x1.634c020000000p-25f}},
+    {21846993670708ull, {0x1.3dea640000000p+0f, 0x1.8246840000000p-25f}}, {22084891834158ull, {0x1.4160a20000000p+0f, 0x1.f72e2a0000000p-28f}},
+    {22325380538761ull, {0x1.44e0860000000p+0f, 0x1.8624b40000000p-30f}}, {22568487993661ull, {0x1.486a2c0000000p+0f, -0x1.47d8660000000p-25f}},
+    {22814242715178ull, {0x1.4bfdae0000000p+0f, -0x1.593abc0000000p-25f}}, {23062673530157ull, {0x1.4f9b280000000p+0f, -0x1.2c5a6c0000000p-25f}},
+    {23313809579344ull, {0x1.5342b60000000p+0f, -0x1.2c56100000000p-25f}}, {23567680320808ull, {0x1.56f4740000000p+0f, -0x1.295b040000000p-25f}},
+    {23824315533396ull, {0x1.5ab07e0000000p+0f, -0x1.5bd5ec0000000p-27f}}, {24083745320225ull, {0x1.5e76f20000000p+0f, -0x1.4a5bd60000000p-25f}},
+    {24346000112214ull, {0x1.6247ec0000000p+0f, -0x1.f8b5500000000p-25f}}, {24611110671650ull, {0x1.6623880000000p+0f, 0x1.2a91120000000p-27f}},
+    {24879108095804ull, {0x1.6a09e60000000p+0f, 0x1.9fcef40000000p-26f}}, {25150023820570ull, {0x1.6dfb240000000p+0f, -0x1.cd72e80000000p-27f}},
+    {25423889624159ull, {0x1.71f75e0000000p+0f, 0x1.1d8bee0000000p-25f}}, {25700737630824ull, {0x1.75feb60000000p+0f, -0x1.37b3060000000p-25f}},
+    {25980600314626ull, {0x1.7a11480000000p+0f, -0x1.829fd00000000p-25f}}, {26263510503246ull, {0x1.7e2f340000000p+0f, -0x1.2616340000000p-25f}},
+    {26549501381838ull, {0x1.82589a0000000p+0f, -0x1.accc7c0000000p-26f}}, {26838606496915ull, {0x1.868d9a0000000p+0f, -0x1.2edb440000000p-26f}},
+    {27130859760289ull, {0x1.8ace540000000p+0f, 0x1.15506e0000000p-27f}}, {27426295453047ull, {0x1.8f1aea0000000p+0f, -0x1.baa2320000000p-26f}},
+    {27724948229574ull, {0x1.93737c0000000p+0f, -0x1.e647440000000p-25f}}, {28026853121614ull, {0x1.97d82a0000000p+0f, -0x1.0d8d840000000p-31f}},
+    {28332045542385ull, {0x1.9c49180000000p+0f, 0x1.51f8480000000p-27f}}, {28640561290725ull, {0x1.a0c6680000000p+0f, -0x1.2886a60000000p-26f}},
+    {28952436555301ull, {0x1.a5503c0000000p+0f, -0x1.b83b540000000p-25f}}, {29267707918846ull, {0x1.a9e6b60000000p+0f, -0x1.50c0480000000p-25f}},
+    {29586412362452ull, {0x1.ae89fa0000000p+0f, -0x1.a94b140000000p-26f}}, {29908587269910ull, {0x1.b33a2c0000000p+0f, -0x1.ec3a820000000p-26f}},
+    {30234270432094ull, {0x1.b7f7700000000p+0f, -0x1.a094380000000p-25f}}, {30563500051394ull, {0x1.bcc1ea0000000p+0f, -0x1.f687c60000000p-25f}},
+    {30896314746195ull, {0x1.c199be0000000p+0f, -0x1.3d56b20000000p-27f}}, {31232753555409ull, {0x1.c67f120000000p+0f, 0x1.cafa2a0000000p-25f}},
+    {31572855943056ull, {0x1.cb720e0000000p+0f, -0x1.8837cc0000000p-27f}}, {31916661802889ull, {0x1.d072d40000000p+0f, 0x1.40f1300000000p-25f}},
+    {32264211463077ull, {0x1.d5818e0000000p+0f, -0x1.822dbc0000000p-27f}}, {32615545690931ull, {0x1.da9e600000000p+0f, 0x1.ed99420000000p-27f}},
+    {32970705697691ull, {0x1.dfc9740000000p+0f, -0x1.908c940000000p-25f}}, {33329733143360ull, {0x1.e502ee0000000p+0f, 0x1.e2cffe0000000p-26f}},
+    {33692670141585ull, {0x1.ea4afa0000000p+0f, 0x1.52486c0000000p-27f}}, {34059559264602ull, {0x1.efa1be0000000p+0f, 0x1.cc2b440000000p-25f}},
+    {34430443548229ull, {0x1.f507660000000p+0f, -0x1.246eb00000000p-26f}}, {34805366496913ull, {0x1.fa7c180000000p+0f, 0x1.9e90d80000000p-28f}},
+};
 struct Table {
-    uint64_t fix[64];
-    Two two[64];
+    Power at[64];
 };
 __device__ __forceinline__ void fill(Table& t) {
-    if (threadIdx.x < 64) {
-        const double v = exp2(threadIdx.x / 64.0);
-        t.fix[threadIdx.x] = static_cast<uint64_t>(__double2ll_rn(v * 17592186044416.0));
-        t.two[threadIdx.x] = two_of(v);
-    }
+    if (threadIdx.x < 64) reinterpret_cast<uint4*>(t.at)[threadIdx.x] = reinterpret_cast<const uint4*>(kPowers)[threadIdx.x];
 }
 
-__device__ __forceinline__ int whole(float v) { return __float_as_int(v + 12582912.f) - 0x4B400000; }  // nearest, |v| < 2^22
+// v + kRound, |v| < 2^22, is rounded to a whole number, which is in its low bits (and less kRound again, as a float).
+constexpr float kRound = 12582912.f;  // 3 * 2^22
+__device__ __forceinline__ int low_bits(float sum) { return __float_as_int(sum) - 0x4B400000; }
 
 // 2^((x - m) scale) = w 2^(-44 - k), x <= m, m finite; false where it is below 2^least.  The exponent is a pair: x - m
 // without error, times the scale's pair; its 64ths come from the table and 2^r of what is left, |r| <= 2^-7, from its
@@ -105,18 +141,20 @@ __device__ __forceinline__ bool power(float x, float m, Two scale, const Table& 
     const float ph = s * scale.hi;
     if (!(ph >= least)) return false;  // (and x = -infinity)
     const float pl = fmaf(s, scale.hi, -ph) + fmaf(s, scale.lo, e * scale.hi);
-    const int n = whole(ph * 64.f);
+    const float near = fmaf(ph, 64.f, kRound);
+    const int n = low_bits(near);
     // (what is left is 0 or a step of ph at least, and pl half a step at most: the sum of the two is exact as a pair)
-    const float rest = fmaf(static_cast<float>(n), -0.015625f, ph), rh = rest + pl, rl = pl - (rh - rest);
+    const float rest = fmaf(near - kRound, -0.015625f, ph), rh = rest + pl, rl = pl - (rh - rest);
     constexpr float kHi = 0.693147182464599609375f, kLo = -1.9046542999577680e-9f;  // ln 2
     const float uh = rh * kHi, ul = fmaf(rh, kHi, -uh) + fmaf(rh, kLo, rl * kHi);
     const float q = uh * uh * fmaf(uh, fmaf(uh, fmaf(uh, 1.f / 120, 1.f / 24), 1.f / 6), 0.5f);
     const float vh = uh + q, vl = ul + (q - (vh - uh));  // (|q| < |uh|)
-    const Two f = t.two[n & 63];
+    const Power power = t.at[n & 63];
+    const Two f = power.two;
     const float wh = f.hi * vh, wl = fmaf(f.hi, vh, -wh) + fmaf(f.hi, vl, f.lo * vh);
-    const int h = whole(wh * 16777216.f);  // 2^24ths
-    const int l = whole((fmaf(static_cast<float>(h), -5.9604644775390625e-8f, wh) + wl) * 17592186044416.f);
-    w = static_cast<int64_t>(t.fix[n & 63]) + (static_cast<int64_t>(h) << (kShift - 24)) + l;
+    const float high = fmaf(wh, 16777216.f, kRound);  // 2^24ths
+    const int l = low_bits(fmaf(fmaf(high - kRound, -5.9604644775390625e-8f, wh) + wl, 17592186044416.f, kRound));
+    w = static_cast<int64_t>(power.fix) + (static_cast<int64_t>(low_bits(high)) << (kShift - 24)) + l;
     k = -(n >> 6);
     return true;
 }
@@ -285,6 +323,8 @@ template <typename T>
 __global__ void __launch_bounds__(kChoose) verify_choose(const Params p) {
     __shared__ Table table;
     __shared__ Choice choice;
+    __shared__ Two scale_sm;
+    __shared__ uint64_t share_of[2];           // 2^106 / Z, of p and q
     __shared__ Joined kept[2][kKept];          // target rows, draft rows
     __shared__ int refused;                    // lowest refused draft
     __shared__ uint64_t share[kMaxRanks];      // the blocks' sums (each block's own copy)
@@ -296,9 +336,8 @@ __global__ void __launch_bounds__(kChoose) verify_choose(const Params p) {
     for (int i = tid; i < p.agents; i += kChoose) falls |= p.agent_rows[i + 1] < p.agent_rows[i];
     fill(table);
     const int r0 = p.agent_rows[a], r1 = p.agent_rows[a + 1];
-    const Two scale = scale_of(p, a);
     const float sample = p.sample_u[a];
-    if (tid == 0) refused = INT32_MAX;
+    if (tid == 0) refused = INT32_MAX, scale_sm = scale_of(p, a);  // (64-bit arithmetic by one thread: it is slow)
     falls = __syncthreads_or(falls);
     griddep_wait();  // the first kernel's numbers are there
     const bool bad = falls || r0 < 0 || r1 > p.rows;
@@ -307,6 +346,7 @@ __global__ void __launch_bounds__(kChoose) verify_choose(const Params p) {
         if (tid == 0 && rank == 0) p.accepted[a] = 0, p.token[a] = -1;
         return;  // (the whole cluster)
     }
+    const Two scale = scale_sm;
     const bool greedy = scale.hi == 0.f;
     const T* logits = static_cast<const T*>(p.logits);
     const T* drafts = static_cast<const T*>(p.draft);
@@ -340,7 +380,7 @@ __global__ void __launch_bounds__(kChoose) verify_choose(const Params p) {
             } else if (in && tp.m > -INFINITY) {
                 const double wp = weight_of(xp, tp.m, scale, table), zp = static_cast<double>(tp.z);
                 yes = static_cast<double>(u) * (wq * zp) < wp * zq;
-                prob = wp * zq >= wq * zp ? (wp > 0 ? 1.f : 0.f) : static_cast<float>(wp * zq / (wq * zp));
+                if (p.prob && rank == 0) prob = wp * zq >= wq * zp ? (wp > 0 ? 1.f : 0.f) : static_cast<float>(wp * zq / (wq * zp));
             }
         }
         if (lane == 0) {
@@ -370,6 +410,10 @@ __global__ void __launch_bounds__(kChoose) verify_choose(const Params p) {
                 c.how = kWithout;
             }
         }
+        if (lane < 2) {  // the columns' shares of 2^60: weight times 2^60 / Z, p's and q's alike
+            const Joined& of = lane ? c.q : c.p;
+            if (of.z) share_of[lane] = __double2ull_rn(4.0 * 1152921504606846976.0 * (17592186044416.0 / static_cast<double>(of.z)));
+        }
         if (lane == 0) choice = c;
     }
     __syncthreads();
@@ -379,9 +423,7 @@ __global__ void __launch_bounds__(kChoose) verify_choose(const Params p) {
         if (rank == 0 && tid == 0) p.accepted[a] = c.taken, p.token[a] = nothing ? -1 : c.p.best;
         return;
     }
-    // The columns' shares of 2^60: weight times 2^60 / Z, p's and q's alike.
-    const uint64_t fp = __double2ull_rn(4.0 * 1152921504606846976.0 * (17592186044416.0 / static_cast<double>(c.p.z)));
-    const uint64_t fq = __double2ull_rn(4.0 * 1152921504606846976.0 * (17592186044416.0 / static_cast<double>(c.q.z)));
+    const uint64_t fp = share_of[0], fq = share_of[1];
     const T* prow = logits + c.row * p.stride;
     const T* qrow = drafts ? drafts + (c.row + 1) * p.draft_stride : nullptr;
     int how = c.how;
@@ -440,10 +482,11 @@ __global__ void __launch_bounds__(kChoose) verify_choose(const Params p) {
         cluster.sync();
     }
     // ---- the lowest column whose running sum passes u * total  (nobody writes to another block any more)
+    if (warp > 0) return;
     const double u = fmin(fmax(static_cast<double>(sample), 0.0), 1.0);
     uint64_t target = __double2ull_rd(u * static_cast<double>(total));
     if (target >= total) target = total - 1;
-    if (warp > 0 || target < before || target >= before + mine) return;
+    if (target < before || target >= before + mine) return;
     // the part in which it falls: part[step][warp] is in the columns' order; a lane takes neighbouring ones
     const uint64_t rest = target - before;
     const int parts = (step1 - step0) * kChooseWarps, each = (parts + 31) / 32;
