@@ -292,6 +292,7 @@ __device__ __forceinline__ int form_table(const Params& p, int4* seq, int* tmp, 
         if (!falls)
             for (int r = tid; r < p.rows; r += n_threads) {
                 const int a = find(r), n = length_of(p, r);
+                if (n != p.row_len[r] && blockIdx.x == 0) atomicOr(p.err, kErrRange);  // (its sequence may have no item to say so)
                 if (a < 0 || n == 0) continue;
                 atomicMax(&seq[a].y, n);
                 atomicMin(&seq[a].z, max(0, n - p.window));
