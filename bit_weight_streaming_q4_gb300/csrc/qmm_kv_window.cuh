@@ -80,7 +80,7 @@ struct Geo {
     static constexpr int H = halves ? 2 : 1, TN = H * kHalf;     // tokens of a tile
     static constexpr int part = TN * D * 2;                      // bytes of a tile's K or V in 16 bits
     static constexpr int tile = q8 ? 2 * part : part;            // q8_0: high and low parts
-    static constexpr int k_slots = D == 64 ? 8 : D == 128 && !q8 ? 4 : 2, v_slots = q8 ? 1 : k_slots;
+    static constexpr int k_slots = D == 64 ? 8 : D == 128 && !q8 ? 4 : 2, v_slots = q8 && !DEC ? 1 : k_slots;
     // Barriers that say that a tile's K or V is there: more of them than slots, since a stream of a decode step waits only for
     // tiles of its own, at most three apart.  Then a barrier's phase before the one waited for is over for sure: V's come
     // in order, and the last own tile's K was asked for after the K of k_told tiles before had been used.
@@ -99,7 +99,7 @@ struct Geo {
     // shared memory, after aligning to 1024
     static constexpr int off_v = k_slots * tile;
     static constexpr int off_q = off_v + v_slots * tile;
-    static constexpr int off_raw = off_q + streams * q_tile;     // K's pages, then V's
+    static constexpr int off_raw = off_q + (DEC ? 1 : streams) * q_tile;  // K's pages, then V's
     static constexpr int off_ml = off_raw + 2 * raw_slots * kQ8Half;  // [2][128] reference and sum of the streams
     static constexpr int off_red = off_ml + 256 * 8;             // [stream][half][128] maxima, and sums
     static constexpr int off_item = off_red + (halves ? 2048 : 0);  // [2] of Record
