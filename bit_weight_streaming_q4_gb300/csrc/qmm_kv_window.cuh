@@ -10,20 +10,18 @@
 // P goes back over S as the second product's A operand, in 16 bits.
 // An item is a block's work: a sequence, a KV head and
 //   prompts (more than 128 queries a sequence): two tiles of queries, which share each K and V tile;
-//   decode steps: one tile of queries, whose tokens' tiles are dealt to two streams by their parity; the streams
-//     meet at the end through shared memory.
+//   decode steps: one tile of queries, whose tokens' tiles are dealt to two streams by their parity; each stream's
+//     softmax weighs both outputs at the end, for half of the dims.
 // Either way two streams take turns on the tensor cores (one at head dimension 256, for which tensor memory has no more
-// room): one's products run while the other's scores become probabilities.  16-bit pools at head dimensions 64 and 128
-// have tiles of 128 tokens (a product of 64 columns of scores takes as long: it reads as much of Q), whose halves two
-// groups of softmax warps take; they share a query's reference, by a vote per tile.  Otherwise tiles have 64 tokens, and
-// scores have two buffers: the next tile's are there when the softmax is done with one.
+// room): one's products run while the other's scores become probabilities.  Tiles have 64 tokens, and scores two buffers:
+// the next tile's are there when the softmax is done with one.
 // The tiles of an item are those that some of its rows sees: the first ones (sinks), and the window's.  Where few
 // items would leave SMs idle, tokens are cut into chunks at fixed places of a sequence, an item each, whose unnormalised
 // outputs a second kernel joins.  All choices are made by the plan's dims, so a row's bits do not depend on its company.
 //   warp 0      forms the items' records; asks for K tiles (q8_0: as they are stored); it or another one asks for V tiles
 //   warps 1, 3  one thread each issues a stream's products
 //   warp 2      16-bit pools: zeroes the rows of V that must not count, where some are
-//   warps 4 ..  softmax, four or eight a stream
+//   warps 4 ..  softmax, four a stream
 //   q8_0: four more convert K (half a token a thread) and V (a dim a thread) to two fp16 parts whose sum is quant
 //               times scale
 // A query's reference is its first tile's maximum and moves only when a score passes it by more than 2^kSlack; each
@@ -42,7 +40,7 @@ using namespace qmm::kv;
 
 constexpr float kShift = 9.f;       // p's power of two ..
 constexpr float kSlack = 6.f;       // .. and how far a score may pass its reference: p <= 2^15
-constexpr int kHalf = 64;          // tokens that a softmax thread takes
+constexpr int kTile = 64;           // tokens of a tile
 constexpr float kFine = 4194304.f;  // 2^22: a larger reference stands alone (fp32's spacing would swallow the two): p <= 1
 
 struct Params {
@@ -76,9 +74,7 @@ template <int FMT, int D, bool DEC>
 struct Geo {
     static constexpr bool q8 = FMT == QMM_KV_Q8_0;
     static constexpr int streams = D == 256 ? 1 : 2;
-    static constexpr bool halves = false;              // tiles of two halves, a group of warps each; one buffer of scores per stream
-    static constexpr int H = halves ? 2 : 1, TN = H * kHalf;     // tokens of a tile
-    static constexpr int part = TN * D * 2;                      // bytes of a tile's K or V in 16 bits
+    static constexpr int part = kTile * D * 2;                   // bytes of a tile's K or V in 16 bits
     static constexpr int tile = q8 ? 2 * part : part;            // q8_0: high and low parts
     static constexpr int k_slots = D == 64 ? 8 : D == 128 && !q8 ? 4 : 2, v_slots = q8 && !DEC ? 1 : k_slots;
     // Barriers that say that a tile's K or V is there: more of them than slots, since a stream of a decode step waits only for
@@ -87,28 +83,27 @@ struct Geo {
     static constexpr int k_told = k_slots <= 4 ? 8 : 16, v_told = v_slots <= 4 ? 4 : 8;
     static constexpr int raw_slots = q8 ? 2 : 0;                 // pages on their way, K and V
     static constexpr int q_tile = 128 * D * 2;
-    static constexpr int soft_warps = 4 * H * streams, conv_warps = q8 ? 4 : 0;
+    static constexpr int soft_warps = 4 * streams, conv_warps = q8 ? 4 : 0;
     // The warp that asks for V tiles: one of its own, in decode steps for which it takes four more (which asks faster: 61
     // ragged sequences at head dimension 64 took 59 us, 71 with one warp for K and V); a prompt's softmax wants their
     // registers (2,048 rows: 216 us, 230 with them).
     static constexpr int more_warps = !q8 && streams == 2 && DEC ? 4 : 0;
     static constexpr int v_warp = q8 ? 2 : streams == 1 ? 3 : DEC ? 4 + soft_warps : 0;
     static constexpr int threads = 32 * (4 + soft_warps + conv_warps + more_warps);
-    // tensor memory: S (128 columns per stream, two halves or two buffers), P over it, and O
+    // tensor memory: S (two buffers a stream), P over it, and O
     static constexpr int col_o = 256;
     // shared memory, after aligning to 1024
     static constexpr int off_v = k_slots * tile;
     static constexpr int off_q = off_v + v_slots * tile;
     static constexpr int off_raw = off_q + (DEC ? 1 : streams) * q_tile;  // K's pages, then V's
     static constexpr int off_ml = off_raw + 2 * raw_slots * kQ8Half;  // [2][128] reference and sum of the streams
-    static constexpr int off_red = off_ml + 256 * 8;             // [stream][half][128] maxima, and sums
-    static constexpr int off_item = off_red + (halves ? 2048 : 0);  // [2] of Record
+    static constexpr int off_item = off_ml + 256 * 8;            // [2] of Record
     static constexpr int off_dv = off_item + 2 * 64;             // q8_0: V's scales, zero where a token must not count: [4][64] fp16
     static constexpr int off_bar = off_dv + (q8 ? 512 : 0);
     static constexpr int bars = k_told + k_slots + 2 * v_slots + v_told + 4 * raw_slots + 2 + 4 + 4 + 2 + 2 + 2 + 2 + 4;
-    // tmp[33], abort, tmem, accumulate[2], miss[8] (of V tiles), odd[8][4], miss[16] (of all tiles), raw[2][2]
+    // tmp[33], abort, tmem, accumulate[2], miss[8] (of V tiles), odd[8][2], miss[16] (of all tiles), raw[2][2]
     static constexpr int off_misc = (off_bar + bars * 8 + 15) / 16 * 16;
-    static constexpr int off_seq = (off_misc + 100 * 4 + 15) / 16 * 16;
+    static constexpr int off_seq = (off_misc + 81 * 4 + 15) / 16 * 16;
     static constexpr int smem(int agents) { return 1024 + off_seq + (agents + 1) * 16; }
 };
 
@@ -336,7 +331,6 @@ __device__ __forceinline__ int form_table(const Params& p, int4* seq, int* tmp, 
 }
 
 // The record of an item, by a warp.
-template <int TN>
 __device__ __forceinline__ Record record_of(const Params& p, const int4* seq, int item, int qt) {
     const int lane = threadIdx.x & 31;
     int lo = 0, hi = p.agents;
@@ -378,11 +372,11 @@ __device__ __forceinline__ Record record_of(const Params& p, const int4* seq, in
     it.lo = __reduce_min_sync(0xffffffffu, minlo);
     it.maxlo = __reduce_max_sync(0xffffffffu, maxlo);
     it.sink_end = min(p.sinks, it.hi);
-    const int c0 = p.chunk ? it.chunk * (p.chunk / TN) : 0, c1 = p.chunk ? c0 + p.chunk / TN : INT32_MAX;
-    const int end = min((it.hi + TN - 1) / TN, c1);
+    const int c0 = p.chunk ? it.chunk * (p.chunk / kTile) : 0, c1 = p.chunk ? c0 + p.chunk / kTile : INT32_MAX;
+    const int end = min((it.hi + kTile - 1) / kTile, c1);
     it.a0 = c0;
-    it.na = max(0, min((it.sink_end + TN - 1) / TN, end) - c0);
-    it.b0 = max(it.lo / TN, c0 + it.na);
+    it.na = max(0, min((it.sink_end + kTile - 1) / kTile, end) - c0);
+    it.b0 = max(it.lo / kTile, c0 + it.na);
     it.nt = it.hi ? it.na + max(0, end - it.b0) : 0;
     return it;
 }
@@ -391,16 +385,16 @@ __device__ __forceinline__ Record record_of(const Params& p, const int4* seq, in
 // take it, V from memory.  (Rare; a function of its own costs the loop around it no registers.)
 template <int FMT, int D>
 __device__ __noinline__ void add_odd(const Params& p, int a, int g, int t0, const uint32_t* odd, uint32_t ocol, uint32_t pcol, int len,
-                                     int from, int first, bool fresh, int c_from, int c_to) {
+                                     int from, int first, bool fresh) {
     constexpr bool BF = FMT == QMM_KV_BF16;
 #pragma unroll 1
-    for (int c = c_from; c < c_to; c += 8) {
+    for (int c = 0; c < D; c += 8) {
         uint32_t o[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) o[j] = fresh ? 0u : tmem_ld1(ocol + c + j);
         tc_wait_ld();
 #pragma unroll 1
-        for (int j = 0; j < kHalf; ++j) {
+        for (int j = 0; j < kTile; ++j) {
             if (!((odd[j & 1] >> (j >> 1)) & 1)) continue;
             const uint32_t both = tmem_ld1(pcol + j / 2);
             tc_wait_ld();
@@ -416,7 +410,8 @@ __device__ __noinline__ void add_odd(const Params& p, int a, int g, int t0, cons
                     const uint8_t* b = p.pool + rec * kQ8Rec + kQ8Half;
                     y = static_cast<float>(static_cast<int8_t>(b[(c + d) * 64 + sl])) *
                         __half2float(*reinterpret_cast<const __half*>(b + 8192 + (((c + d) >> 5) * 64 + sl) * 2));
-                    y = __half2float(__float2half_rn(y));
+                    const float hi = __half2float(__float2half_rn(y));  // (the two parts that the products take)
+                    y = hi + __half2float(__float2half_rn(y - hi));
                 } else {
                     y = wide(reinterpret_cast<const uint16_t*>(p.pool)[((rec * 2 + 1) * p.page_tokens + sl) * D + c + d], BF);
                 }
@@ -433,12 +428,11 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
     attend_window_tc(const __grid_constant__ CUtensorMap map, const __grid_constant__ Params p) {
     using G = Geo<FMT, D, DEC>;
     constexpr bool BF = FMT == QMM_KV_BF16;
-    constexpr int TN = G::TN, NS = G::streams, kP = G::halves ? 32 : 0;  // (P's columns over S's)
+    constexpr int NS = G::streams;
     extern __shared__ uint8_t sm_raw[];
     griddep_launch_dependents();  // the joining kernel waits for this grid's end before it reads
     uint8_t* sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
     float2* ml_sm = reinterpret_cast<float2*>(sm + G::off_ml);
-    float* red_sm = reinterpret_cast<float*>(sm + G::off_red);
     Record* item_sm = reinterpret_cast<Record*>(sm + G::off_item);
     uint64_t* kfull = reinterpret_cast<uint64_t*>(sm + G::off_bar);
     uint64_t *kempty = kfull + G::k_told, *vfull = kempty + G::k_slots, *vempty = vfull + G::v_slots, *vready = vempty + G::v_slots;
@@ -450,9 +444,9 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
     uint32_t* tmem_sm = reinterpret_cast<uint32_t*>(tmp + 34);
     volatile int* accum_sm = tmp + 35;                                          // [2] O holds something before the first product
     volatile int* miss_sm = tmp + 37;                                           // [8] a V tile's pieces that are outside the pool
-    volatile uint32_t* odd_sm = reinterpret_cast<uint32_t*>(tmp + 45);          // [8][4] tokens that are taken query by query: a half's even ones, odd ones
-    volatile int* kmiss_sm = tmp + 77;                                          // [16] miss of the last 16 tiles (more than are under way)
-    volatile int* raw_sm = tmp + 93;                                            // q8_0, [2][2]: a page's number, -1 not needed, -2 outside the pool
+    volatile uint32_t* odd_sm = reinterpret_cast<uint32_t*>(tmp + 45);          // [8][2] tokens that are taken query by query: even ones, odd ones
+    volatile int* kmiss_sm = tmp + 61;                                          // [16] miss of the last 16 tiles (more than are under way)
+    volatile int* raw_sm = tmp + 77;                                            // q8_0, [2][2]: a page's number, -1 not needed, -2 outside the pool
     int4* seq = reinterpret_cast<int4*>(sm + G::off_seq);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int qt = NS == 2 && !DEC ? 256 : 128;
@@ -464,13 +458,13 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
         for (int i = 0; i < G::k_slots; ++i) mbar_init(kempty + i, users);
         for (int i = 0; i < G::v_slots; ++i) mbar_init(vfull + i, 1), mbar_init(vempty + i, users);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(qfull + i, 4 * G::H);
+            mbar_init(qfull + i, 4);
             mbar_init(odone + i, 1);
             mbar_init(ofin + i, 1);
             mbar_init(ifull + i, 1);
             mbar_init(iempty + i, (G::v_warp != 0) + NS + (G::q8 ? G::conv_warps : 1) + G::soft_warps);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(sfull + i, 1), mbar_init(pfull + i, 4 * G::H);
+        for (int i = 0; i < 4; ++i) mbar_init(sfull + i, 1), mbar_init(pfull + i, 4);
         for (int i = 0; i < 2 * G::raw_slots; ++i) mbar_init(rfull + i, 1), mbar_init(rempty + i, 4);
         mbar_init(mfree, G::soft_warps);
         mbar_init(mfull, G::soft_warps);
@@ -507,16 +501,16 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
         ++k;
         return it;
     };
-    // whether some row does not see some token of a half
-    auto edge = [&](const Record& it, int t0) { return !(t0 + kHalf <= it.minlen && (t0 >= it.maxlo || t0 + kHalf <= p.sinks)); };
+    // whether some row does not see some token of a tile
+    auto edge = [&](const Record& it, int t0) { return !(t0 + kTile <= it.minlen && (t0 >= it.maxlo || t0 + kTile <= p.sinks)); };
     // a token that no row of the item sees
     auto gone = [&](const Record& it, int t) { return t >= it.hi || (t < it.lo && t >= it.sink_end); };
-    const int piece_rows = min(TN, p.page_tokens), piece_shift = 31 - __clz(piece_rows);
+    const int piece_rows = min(kTile, p.page_tokens), piece_shift = 31 - __clz(piece_rows);
     // lane i: the page of piece i of a tile, -1 if nobody needs it, -2 if it is outside the pool
     auto page_of = [&](const Record& it, int t0) {
         int pg = -1;
         const int t = t0 + lane * piece_rows;
-        if (lane * piece_rows < TN && t < it.hi && (t + piece_rows > it.lo || t < it.sink_end)) {
+        if (lane * piece_rows < kTile && t < it.hi && (t + piece_rows > it.lo || t < it.sink_end)) {
             pg = p.table[static_cast<int64_t>(it.a) * p.max_pages + (t >> p.page_shift)];
             if (pg < 0 || pg >= p.pool_pages) {
                 atomicOr(p.err, kErrPage);
@@ -563,7 +557,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
                     const int y = ((mine * p.kv_heads + g) * 2 + h) * p.page_tokens + ((t0 + lane * piece_rows) & (p.page_tokens - 1));
 #pragma unroll
                     for (int x = 0; x < D / 64; ++x)
-                        tma_load_hint(sm + (h ? G::off_v : 0) + s * G::tile + x * TN * 128 + lane * piece_rows * 128, &map, 64 * x, y, bar, policy);
+                        tma_load_hint(sm + (h ? G::off_v : 0) + s * G::tile + x * kTile * 128 + lane * piece_rows * 128, &map, 64 * x, y, bar, policy);
                 }
             }
             __syncwarp();
@@ -574,7 +568,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
             if (!does_k) {
                 it = next_record();
             } else {
-                it = record_of<TN>(p, seq, item, qt);
+                it = record_of(p, seq, item, qt);
                 if (k > 1) await(iempty + (k & 1), ((k >> 1) - 1) & 1);
                 if (!live) break;
                 if (lane == 0) {
@@ -583,10 +577,10 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
                 }
                 ++k;
             }
-            int next = it.nt > 0 ? page_of(it, tile_at(it, 0) * TN) : -1;
+            int next = it.nt > 0 ? page_of(it, tile_at(it, 0) * kTile) : -1;
             for (int i = 0; i < it.nt && live; ++i, ++t) {
-                const int t0 = tile_at(it, i) * TN, mine = next;
-                if (i + 1 < it.nt) next = page_of(it, tile_at(it, i + 1) * TN);
+                const int t0 = tile_at(it, i) * kTile, mine = next;
+                if (i + 1 < it.nt) next = page_of(it, tile_at(it, i + 1) * kTile);
                 if (does_k && does_v) {
                     if (t > 0) ask(1, v_g, v_t0, v_page, t - 1);
                     ask(0, it.g, t0, mine, t);
@@ -609,7 +603,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
         // One thread: its waits cost 60 clocks where a warp's with a vote take 100, and tcgen05.commit speaks for the products
         // of its thread.  It is bound by its own instructions (some 4 clocks each), so both streams have one.
         constexpr uint32_t kType = BF ? (1u << 7) | (1u << 10) : 0u;
-        constexpr uint32_t kIdescS = idesc_f16_f32(128, TN) | kType;
+        constexpr uint32_t kIdescS = idesc_f16_f32(128, kTile) | kType;
         constexpr uint32_t kIdescO = idesc_f16_f32(128, D) | kType | (G::q8 ? 0u : 1u << 16);  // (16-bit pools: V by dims)
         constexpr uint32_t kHi = static_cast<uint32_t>(uint64_t{1024 >> 4} | uint64_t{1} << 14 | uint64_t{2} << 29);  // of every descriptor here
         const int s = warp == 3;
@@ -622,8 +616,8 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
             };
             const uint32_t qd = static_cast<uint32_t>(smem_desc_sw128(smem_u32(sm + G::off_q + (DEC ? 0 : s * G::q_tile))));
             const uint32_t kd = static_cast<uint32_t>(smem_desc_sw128(smem_u32(sm)));
-            const uint32_t vd = static_cast<uint32_t>(G::q8 ? smem_desc_sw128(smem_u32(sm + G::off_v)) : desc_mn(smem_u32(sm + G::off_v), TN * 128));
-            const uint32_t col = tmem + s * 2 * kHalf, o = tmem + G::col_o + s * D;
+            const uint32_t vd = static_cast<uint32_t>(G::q8 ? smem_desc_sw128(smem_u32(sm + G::off_v)) : desc_mn(smem_u32(sm + G::off_v), kTile * 128));
+            const uint32_t col = tmem + s * 2 * kTile, o = tmem + G::col_o + s * D;
             uint64_t *sf = sfull + 2 * s, *pf = pfull + 2 * s;
             const bool shares = NS == 2 && !DEC;  // both streams see every tile
             int t = 0, n = 0, m = 0;  // tiles so far; of this stream: scores asked for, and P V
@@ -634,32 +628,32 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
                 const int vs = pend % G::v_slots;
                 const uint32_t b0 = vd + (vs * G::tile >> 4);
                 wait(vready + pend % G::v_told, (pend / G::v_told) & 1);
-                const int x = G::halves ? 0 : m & 1;
-                wait(pf + x, (G::halves ? m : m >> 1) & 1);
+                const int x = m & 1;
+                wait(pf + x, (m >> 1) & 1);
                 if (!live) return;
                 tc_fence_after();
                 if (!acc) acc = accum_sm[s] != 0;
 #pragma unroll
                 for (int part = 0; part < (G::q8 ? 2 : 1); ++part)
 #pragma unroll
-                    for (int ks = 0; ks < TN / 16; ++ks) {
-                        mma_ts(o, col + kP + x * kHalf + (ks >> 2) * kHalf + 8 * (ks & 3), b0 + ((G::q8 ? part * G::part + ks * 32 : ks * 2048) >> 4), kHi, kIdescO, acc);
+                    for (int ks = 0; ks < kTile / 16; ++ks) {
+                        mma_ts(o, col + x * kTile + 8 * ks, b0 + ((G::q8 ? part * G::part + ks * 32 : ks * 2048) >> 4), kHi, kIdescO, acc);
                         acc = 1;
                     }
                 tc_commit(vempty + vs);
-                if (!G::halves) tc_commit(odone + s);
+                tc_commit(odone + s);
                 ++m;
                 pend = -1;
             };
             auto product_s = [&] {
-                const int ksl = t % G::k_slots, x = G::halves ? 0 : n & 1;
+                const int ksl = t % G::k_slots, x = n & 1;
                 const uint32_t bk = kd + (ksl * G::tile >> 4);
 #pragma unroll
                 for (int part = 0; part < (G::q8 ? 2 : 1); ++part)
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks)
-                        mma_ss(col + x * kHalf, qd + (((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4), kHi,
-                               bk + ((part * G::part + (ks >> 2) * (TN * 128) + (ks & 3) * 32) >> 4), kHi, kIdescS, part + ks > 0);
+                        mma_ss(col + x * kTile, qd + (((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4), kHi,
+                               bk + ((part * G::part + (ks >> 2) * (kTile * 128) + (ks & 3) * 32) >> 4), kHi, kIdescS, part + ks > 0);
                 tc_commit(sf + x);
                 tc_commit(kempty + ksl);
                 ++n;
@@ -687,12 +681,11 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
                 bool begun = false;
                 for (int i = 0; i < nt && live; ++i, ++t) {
                     if (NS == 2 && DEC && (tile_at(it, i) & 1) != s) continue;
-                    if (G::halves && pend >= 0) product_pv();
                     wait(kfull + t % G::k_told, (t / G::k_told) & 1);
                     if (!live) break;
                     tc_fence_after();
                     product_s();
-                    if (!G::halves && pend >= 0) product_pv();
+                    if (pend >= 0) product_pv();
                     if (!begun) acc = 0;
                     pend = t;
                     begun = true;
@@ -714,18 +707,15 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
         for (int item = blockIdx.x; item < total && live; item += gridDim.x) {
             const Record it = next_record();
             for (int i = 0; i < it.nt && live; ++i, ++t) {
-                const int t0 = tile_at(it, i) * TN, vs = t % G::v_slots;
+                const int t0 = tile_at(it, i) * kTile, vs = t % G::v_slots;
                 await(vfull + vs, (t / G::v_slots) & 1);
                 if (!live) break;
                 const int miss = miss_sm[vs];
-                bool some = miss != 0;
-                for (int half = 0; half < G::H; ++half) some = some || edge(it, t0 + half * kHalf);
-#pragma unroll 1
-                for (int half = 0; some && half < G::H; ++half) {
+                if (miss != 0 || edge(it, t0)) {
                     uint8_t* vt = sm + G::off_v + vs * G::tile;
 #pragma unroll 1
                     for (int j = 0; j < 2; ++j) {
-                        const int row = half * kHalf + 2 * lane + j, tok = t0 + row;
+                        const int row = 2 * lane + j, tok = t0 + row;
                         bool zero = gone(it, tok) || ((miss >> (row >> piece_shift)) & 1), odd = false;
                         if (!zero && !(tok < it.minlen && (tok >= it.maxlo || tok < p.sinks))) {
                             constexpr uint32_t ex = BF ? 0x7F80u : 0x7C00u;
@@ -734,7 +724,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
                             for (int x = 0; x < D / 64; ++x)
 #pragma unroll
                                 for (int c = 0; c < 8; ++c) {
-                                    const uint4 v = *reinterpret_cast<const uint4*>(vt + x * TN * 128 + row * 128 + 16 * ((c + lane) & 7));
+                                    const uint4 v = *reinterpret_cast<const uint4*>(vt + x * kTile * 128 + row * 128 + 16 * ((c + lane) & 7));
                                     odd |= bad(v.x) || bad(v.y) || bad(v.z) || bad(v.w);
                                 }
                         }
@@ -743,36 +733,24 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
                             for (int x = 0; x < D / 64; ++x)
 #pragma unroll
                                 for (int c = 0; c < 8; ++c)
-                                    *reinterpret_cast<uint4*>(vt + x * TN * 128 + row * 128 + 16 * ((c + lane) & 7)) = make_uint4(0, 0, 0, 0);
+                                    *reinterpret_cast<uint4*>(vt + x * kTile * 128 + row * 128 + 16 * ((c + lane) & 7)) = make_uint4(0, 0, 0, 0);
                         }
                         const uint32_t word = __ballot_sync(0xffffffffu, odd);
-                        if (lane == 0) odd_sm[t % G::v_told * 4 + 2 * half + j] = word;
+                        if (lane == 0) odd_sm[t % G::v_told * 2 + j] = word;
                     }
-                }
-                if (some) {
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(vready + t % G::v_told);
-                }
+                if (lane == 0) mbar_arrive(vready + t % G::v_told);
             }
         }
     }
     } else if (warp < 4 + G::soft_warps) {
         if constexpr (NS == 2) setmaxnreg_inc<G::q8 ? 168 : 200>();
-        // ---------------------------------------------------------------- softmax: a query per thread (two, of half a tile's tokens each)
-        const int sw = warp - 4, s = sw / (4 * G::H), half = G::H == 2 ? (sw >> 2) & 1 : 0, me = tid & 127;
+        // ---------------------------------------------------------------- softmax: a query per thread
+        const int s = (warp - 4) >> 2, me = tid & 127;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
         const uint32_t ocol = lanes + G::col_o + s * D;
-        constexpr int DH = D / G::H;  // the dims of the outputs that are the thread's
-        const int d0 = half * DH;
-        // What ends the loops is voted on where groups meet at barriers, so that they always meet at the same ones.
-        const uint32_t meet = 1 + s;  // the stream's barrier
-        auto over = [&]() -> bool {
-            if constexpr (G::halves) live = !bar_or(meet, 256, !live);
-            return !live;
-        };
         int tiles = 0;  // all tiles so far
         int n = 0;      // the stream's
         int merges = 0, fins = 0;
@@ -780,11 +758,11 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
             // (the record stays until the item's end, where what the loop has no registers for is read again)
             await(ifull + (k & 1), (k >> 1) & 1);
             if (NS == 2 && DEC && merges > 0) await(mfree, (merges - 1) & 1);  // (the last item's outputs are read)
-            if (over()) break;
+            if (!live) break;
             // (read as it is needed: the scores take most registers)
             const volatile Record& it = item_sm[k & 1];
             const int nt = it.nt, minlen = it.minlen, maxlo = it.maxlo;
-            auto edge_at = [&](int t) { return !(t + kHalf <= minlen && (t >= maxlo || t + kHalf <= p.sinks)); };
+            auto edge_at = [&](int t) { return !(t + kTile <= minlen && (t >= maxlo || t + kTile <= p.sinks)); };
             auto release = [&] {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(iempty + (k & 1));
@@ -803,13 +781,12 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
             const int nq = it.nq;
             if (s == 0 || !DEC) {  // the queries, swizzled as the copies do: D / 8 lanes a row
                 constexpr int L = D / 8 < 32 ? D / 8 : 32, R = 32 / L;  // lanes of a row, rows at once
-                constexpr int kRows = 32 / G::H;                        // the warp's
                 const int c = lane % L;
                 uint8_t* dst = sm + G::off_q + s * G::q_tile + (c >> 3) * (128 * 128);
                 const int64_t src = row * p.q_stride + static_cast<int64_t>(head) * D;
-                constexpr int kMost = G::q8 ? 8 : 16, kLoads = kRows / R < kMost ? kRows / R : kMost;  // (on their way at once)
+                constexpr int kMost = G::q8 ? 8 : 16, kLoads = 32 / R < kMost ? 32 / R : kMost;  // (on their way at once)
 #pragma unroll 1
-                for (int i0 = half * kRows; i0 < (half + 1) * kRows; i0 += kLoads * R) {
+                for (int i0 = 0; i0 < 32; i0 += kLoads * R) {
                     uint4 v[kLoads];
 #pragma unroll
                     for (int j = 0; j < kLoads; ++j) {
@@ -834,27 +811,27 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
             int tile = na ? it.a0 : it.b0;
             for (int i = 0; i < nt; ++i, ++tile, ++tiles) {
                 if (i == na && i) tile = it.b0;
-                const int t0 = tile * TN + half * kHalf;
+                const int t0 = tile * kTile;
                 if (NS == 2 && DEC && (tile & 1) != s) continue;
-                const int x = G::halves ? 2 * s : 2 * s + (n & 1);
-                const uint32_t scol = lanes + x * kHalf;  // S; the thread's half, and P, from pcol on
-                const uint32_t pcol = scol + half * kHalf;
-                await(sfull + x, (G::halves ? n : n >> 1) & 1);
-                const bool some = edge_at(tile * TN) || (G::halves && edge_at(tile * TN + kHalf));
+                const int x = 2 * s + (n & 1);
+                const uint32_t scol = lanes + x * kTile;  // S, and P over it
+                await(sfull + x, (n >> 1) & 1);
+                const bool some = edge_at(t0);
                 const int vi = tiles % G::v_told;
                 if (some) await(vready + vi, (tiles / G::v_told) & 1);  // (which tokens' V is not finite)
-                if (!G::halves && !live) break;
-                float v[kHalf], m = -INFINITY;
-                const int miss = kmiss_sm[tiles & 15] >> (half * kHalf >> piece_shift);
-                auto take = [&](int to) {  // scores 0 .. to - 1
+                if (!live) break;
+                float v[kTile], m = -INFINITY;
+                const int miss = kmiss_sm[tiles & 15];
+                if (!idle) {
+                    tc_fence_after();
 #pragma unroll
-                    for (int i = 0; i < to; i += 32) tmem_ld32(pcol + i, v + i);
+                    for (int i = 0; i < kTile; i += 32) tmem_ld32(scol + i, v + i);
                     tc_wait_ld();
                     if (some || miss) {
                         // the tokens that the row sees, as bits; a missing piece is 16 tokens at least
                         auto below = [](int j) { return j <= 0 ? 0u : j >= 32 ? ~0u : (1u << j) - 1; };
 #pragma unroll
-                        for (int i = 0; i < to; i += 32) {
+                        for (int i = 0; i < kTile; i += 32) {
                             const int t = t0 + i;
                             uint32_t sees = below(len - t) & (~below(from - t) | below(first - t));
                             if ((miss >> (i >> piece_shift)) & 1) sees &= 0xFFFF0000u;
@@ -864,28 +841,17 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
                                 if (!(sees & (1u << j))) v[i + j] = -INFINITY;
                         }
                     }
-                };
-                if (live && !idle) {
-                    tc_fence_after();
                     float m8[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) m8[j] = -INFINITY;
-                    take(kHalf);
 #pragma unroll
-                    for (int j = 0; j < kHalf; j += 16)
+                    for (int j = 0; j < kTile; j += 16)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) m8[i] = fmaxf(m8[i], fmaxf(v[j + i], v[j + i + 8]));
                     // (a NaN is no maximum)
                     m = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * p.c2;
                 }
-                const bool any = G::halves ? bar_or(meet, 256, m > lim || !live) : __any_sync(0xffffffffu, m > lim);
-                if (any) {
-                    if constexpr (G::halves) {
-                        if (over()) break;
-                        red_sm[(2 * s + half) * 128 + me] = m;
-                        named_bar_sync(meet, 256);
-                        m = fmaxf(m, red_sm[(2 * s + (half ^ 1)) * 128 + me]);
-                    }
+                if (__any_sync(0xffffffffu, m > lim)) {
                     const bool passed = m > lim;
                     float alpha = 1.f;
                     if (passed) {
@@ -896,14 +862,13 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
                         lim = fine ? m + kSlack : m;
                         l *= alpha;
                     }
-                    if (!fresh && __any_sync(0xffffffffu, passed)) {
-                        // (one buffer of scores: they were asked for after the last product.  Two: the last product may be under way,
-                        // the one before was over before these scores were asked for)
-                        if (!G::halves) await(odone + s, (n - 1) & 1);
+                    if (!fresh) {
+                        // (the last product may be under way; the one before was over before these scores were asked for)
+                        await(odone + s, (n - 1) & 1);
                         if (!live) break;
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c = d0; c < d0 + DH; c += 16) {  // (rare, and the scores hold most registers)
+                        for (int c = 0; c < D; c += 16) {  // (rare, and the scores hold most registers)
                             uint32_t o[16];
                             tmem_ld16(ocol + c, o);
                             tc_wait_ld();
@@ -917,18 +882,15 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
                 uint32_t odd = 0;
                 if (some) {
 #pragma unroll
-                    for (int j = 0; j < 2 * G::H; ++j) odd |= odd_sm[vi * 4 + j];
+                    for (int j = 0; j < 2; ++j) odd |= odd_sm[vi * 2 + j];
                 }
-                if (fresh && me == 0 && half == 0) accum_sm[s] = odd != 0;
+                if (fresh && me == 0) accum_sm[s] = odd != 0;
                 if (!idle) {
                     uint64_t sum[2] = {0, 0};  // pairs of fp32
                     const uint64_t c2 = pair(p.c2, p.c2), off = pair(-base, -base);
 #pragma unroll
-                    for (int i = 0; i < kHalf; i += 32) {
-                        // (the upper scores first; two groups' threads have no registers for the lower ones meanwhile, and read
-                        // them again: P goes over the upper)
-                        const int c = 32 - i;
-                        if (G::halves && c == 0) take(32);
+                    for (int i = 0; i < kTile; i += 32) {
+                        const int c = 32 - i;  // (the upper scores first)
                         const float* u = v + c;
                         uint32_t w[16];
 #pragma unroll
@@ -944,7 +906,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
                                 w[(g + j) / 2] = pack2<BF>(e[j], e[j + 1]);
                             }
                         }
-                        tmem_st16(pcol + kP + c / 2, w);
+                        tmem_st16(scol + c / 2, w);
                     }
                     float s0, s1;
                     unpair(add2(sum[0], sum[1]), s0, s1);
@@ -952,15 +914,11 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
                     tc_wait_st();
                 }
                 if (odd) {  // to those that see them
-                    if (!fresh && !G::halves) await(odone + s, (n - 1) & 1);
-                    if (!G::halves && !live) break;
+                    if (!fresh) await(odone + s, (n - 1) & 1);
+                    if (!live) break;
                     tc_fence_before();
-                    if constexpr (G::halves) named_bar_sync(meet, 256);  // (P is there, of both halves)
                     tc_fence_after();
-#pragma unroll 1
-                    for (int h = 0; h < G::H; ++h)
-                        add_odd<FMT, D>(p, it.a, it.g, tile * TN + h * kHalf, const_cast<const uint32_t*>(odd_sm) + vi * 4 + 2 * h, ocol, scol + h * kHalf + kP, len,
-                                        from, first, fresh && h == 0, d0, d0 + DH);
+                    add_odd<FMT, D>(p, it.a, it.g, t0, const_cast<const uint32_t*>(odd_sm) + vi * 2, ocol, scol, len, from, first, fresh);
                 }
                 fresh = false;
                 ++n;
@@ -970,13 +928,8 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
             }
             // (the item's last product; odone may be two phases behind here)
             if (!fresh) await(ofin + s, fins++ & 1);
-            if (over()) break;
+            if (!live) break;
             tc_fence_after();
-            if constexpr (G::halves) {  // the halves' sums, in their order
-                red_sm[(2 * s + half) * 128 + me] = l;
-                named_bar_sync(meet, 256);
-                l = red_sm[2 * s * 128 + me] + red_sm[(2 * s + 1) * 128 + me];
-            }
 
             // ---- what became of the item
             float w0 = 1.f, w1 = 0.f;  // the streams' weights
@@ -1019,7 +972,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
             }
             const bool none = l == 0.f;
             const float inv = none ? 0.f : p.chunk ? w0 : w0 / l, inv1 = none ? 0.f : p.chunk ? w1 : w1 / l;
-            const int from_d = merge ? s * (D / 2) : d0, to_d = from_d + (merge ? D / 2 : DH);
+            const int from_d = merge ? s * (D / 2) : 0, to_d = from_d + (merge ? D / 2 : D);
             if (write && from_d == 0) {
                 if (p.chunk) *reinterpret_cast<float2*>(p.ml + (at * p.slots + slot) * 2) = make_float2(base, l);
                 else if (p.lse) p.lse[at] = none ? -INFINITY : (base + log2f(l)) * 0.6931471805599453f;
@@ -1095,7 +1048,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
             if (!live) return;
             if (me == 0) kmiss_sm[t & 15] = pg == -2;
             if (pg >= 0) {
-                uint8_t* dst = sm + ks * G::tile + half * (TN * 128) + slot * 128;
+                uint8_t* dst = sm + ks * G::tile + half * (kTile * 128) + slot * 128;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {  // eight dims: one 16-byte piece of each part
                     const uint32_t u0 = ((c & 1) ? row[c >> 1].z : row[c >> 1].x) ^ 0x80808080u;
@@ -1140,7 +1093,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
                         for (int c = 0; c < 4; ++c) odd |= (*reinterpret_cast<const uint16_t*>(b + 8192 + c * 128 + 4 * lane + 2 * j) & 0x7FFFu) >= (24u << 10);  // 512
                     }
                     const uint32_t who = __ballot_sync(0xffffffffu, odd);
-                    if (w4 == 0 && lane == 0) odd_sm[t % G::v_told * 4 + j] = who;
+                    if (w4 == 0 && lane == 0) odd_sm[t % G::v_told * 2 + j] = who;
                     if (!none && !odd) mine |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(scales + 4 * lane + 2 * j)) << (16 * j);
                 }
                 *reinterpret_cast<uint32_t*>(dv + 4 * lane) = mine;
@@ -1199,7 +1152,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
         for (int t = 0; more; ++t) {
             const bool also = next_k();  // (may have gone on to the next item)
             if (!live) break;
-            convert_v(it, tile_at(it, i) * TN, t);
+            convert_v(it, tile_at(it, i) * kTile, t);
             more = also && live;
             if (++i == it.nt) {
                 it = ahead;

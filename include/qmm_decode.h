@@ -71,14 +71,14 @@ qmm_status qmm_rotate(const qmm_rotate_dims* dims, const void* q, int64_t q_stri
  *  workspace:  16-byte aligned, at least qmm_kv_window_workspace_bytes bytes for the same dims, max_rows,
  *              window and sinks, in use until the call's kernels finish.  It may be null where that is 0.
  * A row's out and lse are bit-identical whatever the other rows and sequences of the call, as long as the V
- * that they see is finite (Q8_0: its scales below 512).  What lies in slots that a row does not see has no effect on it, NaN and infinity
- * included; a row that sees a score that is NaN has NaN throughout, and an element of V that is not finite
+ * that they see is finite (Q8_0: its scales below 512).  What lies in slots that a row does not see has no effect on
+ * it, NaN and infinity included; a row that sees a score that is NaN has NaN throughout, and an element of V that is not finite
  * makes that element of out not finite (infinite or NaN) for the rows that see it.
  * A page table entry outside the pool (error word 2) takes its page's tokens out of the softmax.
  * Scores, softmax and sums are fp32.  A probability enters the product with V rounded once to the pool's 16-bit
- * type (Q8_0: fp16), relative to the row's largest one; Q8_0's K enters the scores as the sum of two fp16 parts
- * (quant times scale without error, down to 2^-25), its V rounded once to fp16.  An element of a Q8_0 pool is at
- * most 65,504 in magnitude: a larger one of V is infinite, one of K makes the rows that see it NaN.
+ * type (Q8_0: fp16), relative to the row's largest one; Q8_0's K and V are sums of two fp16 parts (quant times scale
+ * without error, down to 2^-25).  An element of a Q8_0 pool is at most 65,504 in magnitude: a larger one of V counts
+ * as not finite, one of K makes the rows that see it NaN.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, SCRATCH_TOO_SMALL, NO_DEVICE, CUDA.
  */
 qmm_status qmm_kv_window_workspace_bytes(const qmm_kv_dims* dims, int64_t max_rows, int32_t window, int32_t sinks,
