@@ -70,7 +70,9 @@ qmm_status check(const qmm_kv_dims* d, int64_t max_rows, int32_t window, int32_t
     return QMM_OK;
 }
 
-// How a plan's calls are laid out, by its dims alone (so that a row's bits are those of any other call).
+// How a plan's calls are laid out, by its dims alone (so that a row's bits are those of any other call).  Tokens are cut
+// into the chunks whose rounds of items take least time by this estimate, or not at all: 4 sequences of 23,000 with a window
+// of 4,096 at q8_0, 3 rows each, take 44 us in chunks of 1,408, 93 as 32 whole windows.
 struct Layout {
     int32_t decode, qt, chunk, slots;
     int64_t o, bytes;

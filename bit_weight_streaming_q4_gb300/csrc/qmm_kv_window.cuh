@@ -26,6 +26,22 @@
 //               times scale
 // A query's reference is its first tile's maximum and moves only when a score passes it by more than 2^kSlack; each
 // query decides for itself.
+//
+// What bounds it (times as a loop of calls, window of 4,096 and 48 query heads over 8 unless given):
+//   prompts, fp16, 2,048 rows at the end of 23,000 tokens, 206 GFLOP: 217 us, 950 TFLOP/s, 0.49 of a library matmul's rate.
+//     A score product of 64 columns takes the tensor cores as long as one of 128 (it reads as much of Q): 1,520 clocks of
+//     products per tile and two streams, of the 1,770 that a tile takes; the rest are the items' starts and ends, of which
+//     384 items on 152 blocks make 2.53 rounds.
+//   decode steps, q8_0, 4 x 23,000 tokens, 3 rows, 35 MB: 44 us (one slot of converted V: 55).  The conversion's chain, 600
+//     clocks for a tile's K and 1,150 for its V with the waits for their slots.  Both are two fp16 parts; one for V
+//     would halve its products but lose 2^-11 of V.
+//   decode steps, bf16, 61 ragged sequences to 4,099, 32 heads over 8 of 64, window 1,024, 113 MB: 57 us, 2.0 TB/s.  A tile's
+//     chain of roles and an item's start and end (15,000 clocks, the time of 7 tiles).
+//   prompts, q8_0, 4 x 524 rows, window 1,024: 132 us; bf16, 3 x 777 rows, 8 heads over 2 of 256, no window: 51 us.
+// Measured and not taken, for the fp16 prompt: tiles of 128 tokens with one product of 128 columns, whose halves two
+// threads take (242 us: one buffer of scores); those threads with a vote on the reference (255 to 263); streams that take
+// strict turns (255); 64 scores of a thread kept across the two passes (386: registers spill); V tiles asked for by a warp
+// of its own (230).
 #pragma once
 
 #include <cuda.h>

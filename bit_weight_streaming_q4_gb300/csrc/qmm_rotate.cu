@@ -6,6 +6,9 @@
 // row's rot_dim / 2 angles are formed once per block, for all of its heads.  An angle is pos * f turns, f = inv_freq / 2 pi as
 // a 64-bit fraction of a turn: the product modulo 2^64 drops whole turns exactly, for any position, in integers
 // (64-bit floating point runs at 1/64 of fp32's rate here; one multiplication per angle is left of it).
+// What bounds it: the bytes.  8,191 rows of 48 + 8 heads of 128 with norms, fp32 to fp16, 352 MB: 64 us, 5.5 TB/s, 0.83 of a
+// plain copy's rate.  2,345 rows of 16 + 2 heads of 256, bf16, 64 dims of them turned by three axes, 43 MB: 20 us, of which
+// the bytes are 6.5; the rest is a block's chain (angles, a barrier, three rounds of heads).  12 rows: 4.4 us, a launch.
 #include "qmm_decode.h"
 #include "qmm_kv.cuh"
 

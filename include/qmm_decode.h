@@ -40,7 +40,8 @@ typedef struct {
  *              (k_stride) elements: columns of a wider matrix are taken in place.  Aligned to
  *              their element; 16-byte aligned rows are read faster.
  *  q_weight, k_weight: fp32 [head_dim], or null (that one is not normalised).
- *  pos:        int32 [axes][rows].  Any value: the angle is formed exactly in 64-bit turns.
+ *  pos:        int32 [axes][rows].  Any value: an angle's whole turns drop out without error, and what is left
+ *              is off by 2^-52 of the angle and 2^-31 of a turn at most, and by fp32's rounding before cosine and sine.
  *  inv_freq:   fp32 [rot_dim / 2].   axis: int32 [rot_dim / 2], 0 .. axes - 1 (others count as 0), or null (all 0).
  *  q_out, k_out: [rows][heads][head_dim], [rows][kv_heads][head_dim], row r at r * q_out_stride
  *              (k_out_stride) elements.  An output may be its input, at the same stride and type;
