@@ -271,9 +271,12 @@ __device__ __forceinline__ Chunks chunks_of(const Params& p, int n) {
     return c;
 }
 
-// The table of sequences, the same in every block: seq[a] = (first item, chunks of the first slots, the window's
-// first chunk, first row), one more entry at the end; returns the number of items.  tmp: 33 ints.
-// QT: queries of an item.  Without chunks also writes the rows that no item has.
+// The table of sequences, the same in every block, one more entry at the end; returns the number of items.  With chunks
+// seq[a] = (first item, chunks of the first slots, the window's first chunk, first row).  Without, entries are (first
+// item, rows, sequence, first row); where blocks have several items, longer sequences come first, and blocks take items
+// there and back (following()), so that the last round has the shortest: 61 ragged sequences of up to 4,099 tokens, 488 items, took
+// 57 us in the order of the call.  (The ranks are counted, a thread a sequence, up to as many as the block has threads.)
+// tmp: 33 ints.  qt: queries of an item.  Without chunks also writes the rows that no item has.
 __device__ __forceinline__ int form_table(const Params& p, int4* seq, int* tmp, int qt) {
     const int tid = threadIdx.x, n_threads = blockDim.x;
     bool falls = false, gaps = false;
@@ -339,8 +342,42 @@ __device__ __forceinline__ int form_table(const Params& p, int4* seq, int* tmp, 
         }
         int sum;
         const int at = block_exclusive(n, tmp, &sum);
-        if (a < p.agents) seq[a].x = total + at, seq[a].y = first, seq[a].z = from;
+        if (a < p.agents) {
+            if (p.chunk) seq[a].x = total + at, seq[a].y = first, seq[a].z = from;
+            else seq[a].x = total + at, seq[a].y = n, seq[a].z = a;
+        }
         total += sum;
+    }
+    if (tid == 0) seq[p.agents].x = total;
+    __syncthreads();
+    if (p.chunk) return total;
+    const bool order = total > static_cast<int>(gridDim.x) && p.agents <= n_threads;
+    auto rows_of = [&](int a) { return seq[a + 1].w - seq[a].w; };
+    if (order) {
+        int4 mine = make_int4(0, 0, tid, 0);
+        int at = 0;
+        if (tid < p.agents) {
+            mine = seq[tid];
+            const int nr = rows_of(tid), n = mine.y ? length_of(p, mine.w + nr - 1) : 0;  // (the last row is the longest, as a rule)
+            mine.x = min(n, p.window + p.sinks);
+            mine.y = nr;
+        }
+        __syncthreads();
+        if (tid < p.agents) seq[tid].x = mine.x;
+        __syncthreads();
+        int rank = 0;
+        if (tid < p.agents) {
+            for (int b = 0; b < p.agents; ++b) {
+                const int2 s = *reinterpret_cast<const int2*>(seq + b);  // (its tokens, its items)
+                const bool before = s.x > mine.x || (s.x == mine.x && b < tid);
+                rank += before;
+                at += before ? s.y : 0;
+            }
+        }
+        __syncthreads();
+        if (tid < p.agents) seq[rank] = make_int4(at, mine.y, tid, mine.w);
+    } else {
+        for (int a = tid; a < p.agents; a += n_threads) seq[a].y = rows_of(a);
     }
     __syncthreads();
     return total;
@@ -357,16 +394,16 @@ __device__ __forceinline__ Record record_of(const Params& p, const int4* seq, in
     }
     const int4 s = seq[lo];
     Record it;
-    it.a = lo;
+    it.a = p.chunk ? lo : s.z;
     it.r0 = s.w;
-    it.nq = (seq[lo + 1].w - s.w) * p.group;
+    it.nq = (p.chunk ? seq[lo + 1].w - s.w : s.y) * p.group;
     const int tiles = (it.nq + qt - 1) / qt;
     int rest = item - s.x;
     it.q0 = rest % tiles * qt;
     rest /= tiles;
     it.g = rest % p.kv_heads;
     rest /= p.kv_heads;
-    it.chunk = rest < s.y ? rest : s.z + rest - s.y;
+    it.chunk = p.chunk ? (rest < s.y ? rest : s.z + rest - s.y) : 0;
     it.pad = 0;
     // the item's rows
     const int ra = it.r0 + it.q0 / p.group, rb = it.r0 + (min(it.q0 + qt, it.nq) - 1) / p.group;
@@ -507,8 +544,10 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
         }
         live = __all_sync(0xffffffffu, live);
     };
-    // the next item's record
     int k = 0;  // items so far
+    // the block's next item, k being the items up to this one: there and back in the table's order, or with chunks in turns
+    auto following = [&](int item) { return p.chunk ? item + static_cast<int>(gridDim.x) : 2 * k * static_cast<int>(gridDim.x) - 1 - item; };
+    // the next item's record
     auto next_record = [&]() -> Record {
         await(ifull + (k & 1), (k >> 1) & 1);
         const Record it = item_sm[k & 1];
@@ -579,7 +618,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
             __syncwarp();
         };
         int t = 0, v_page = -1, v_t0 = 0, v_g = 0;  // (a warp that asks for both: V a tile behind K, whose slots come free first)
-        for (int item = blockIdx.x; item < total && live; item += gridDim.x) {
+        for (int item = blockIdx.x; item < total && live; item = following(item)) {
             Record it;
             if (!does_k) {
                 it = next_record();
@@ -675,7 +714,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
                 ++n;
             };
             int both = 0;  // items of this stream's so far
-            for (int item = blockIdx.x; item < total && live; item += gridDim.x, ++k) {
+            for (int item = blockIdx.x; item < total && live; ++k, item = following(item)) {
                 wait(ifull + (k & 1), (k >> 1) & 1);
                 if (!live) break;
                 const Record it = item_sm[k & 1];
@@ -720,7 +759,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
         // Slots that nobody sees hold anything (and so do those of missing pages): zero.  One that some rows see
         // and whose V is not finite is marked, to be added query by query, and zero in the product.
         int t = 0;
-        for (int item = blockIdx.x; item < total && live; item += gridDim.x) {
+        for (int item = blockIdx.x; item < total && live; item = following(item)) {
             const Record it = next_record();
             for (int i = 0; i < it.nt && live; ++i, ++t) {
                 const int t0 = tile_at(it, i) * kTile, vs = t % G::v_slots;
@@ -770,7 +809,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
         int tiles = 0;  // all tiles so far
         int n = 0;      // the stream's
         int merges = 0, fins = 0;
-        for (int item = blockIdx.x; item < total; item += gridDim.x) {
+        for (int item = blockIdx.x; item < total; item = following(item)) {
             // (the record stays until the item's end, where what the loop has no registers for is read again)
             await(ifull + (k & 1), (k >> 1) & 1);
             if (NS == 2 && DEC && merges > 0) await(mfree, (merges - 1) & 1);  // (the last item's outputs are read)
@@ -1155,7 +1194,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
             while (left == 0) {
                 if (item >= total || !live) return false;
                 ahead = next_record();
-                item += gridDim.x;
+                item = following(item);
                 left = live ? ahead.nt : 0;
             }
             --left;
