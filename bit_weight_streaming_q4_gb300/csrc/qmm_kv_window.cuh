@@ -617,7 +617,14 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
             }
             __syncwarp();
         };
-        int t = 0, v_page = -1, v_t0 = 0, v_g = 0;  // (a warp that asks for both: V a tile behind K, whose slots come free first)
+        // (a warp that asks for both: V a tile behind K, whose slots come free first, but not behind an item without tiles,
+        // since the record after that takes the place of one that waits for this V)
+        int t = 0, v_page = -1, v_t0 = 0, v_g = 0;
+        bool behind = false;
+        auto ask_behind = [&] {
+            if (behind && live) ask(1, v_g, v_t0, v_page, t - 1);
+            behind = false;
+        };
         for (int item = blockIdx.x; item < total && live; item = following(item)) {
             Record it;
             if (!does_k) {
@@ -632,20 +639,22 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
                 }
                 ++k;
             }
+            if (does_k && does_v && it.nt == 0) ask_behind();
             int next = it.nt > 0 ? page_of(it, tile_at(it, 0) * kTile) : -1;
             for (int i = 0; i < it.nt && live; ++i, ++t) {
                 const int t0 = tile_at(it, i) * kTile, mine = next;
                 if (i + 1 < it.nt) next = page_of(it, tile_at(it, i + 1) * kTile);
                 if (does_k && does_v) {
-                    if (t > 0) ask(1, v_g, v_t0, v_page, t - 1);
+                    ask_behind();
                     ask(0, it.g, t0, mine, t);
                     v_page = mine, v_t0 = t0, v_g = it.g;
+                    behind = true;
                 } else {
                     ask(does_v, it.g, t0, mine, t);
                 }
             }
         }
-        if (does_k && does_v && t > 0 && live) ask(1, v_g, v_t0, v_page, t - 1);
+        ask_behind();
         if (!live && lane == 0) {
             // let every copy still in flight land before the block exits: the last of each slot
             volatile int go_on = 0;
@@ -1186,34 +1195,20 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
                 mbar_arrive(rempty + G::raw_slots + rs);
             }
         };
-        Record ahead, it;       // K's item and V's
-        int item = blockIdx.x, tk = 0, left = 0;
-        ahead.nt = 0;
-        // the next tile's K, if there is one
-        auto next_k = [&]() -> bool {
-            while (left == 0) {
-                if (item >= total || !live) return false;
-                ahead = next_record();
-                item = following(item);
-                left = live ? ahead.nt : 0;
+        Record it;  // V's item
+        int tk = 0, tv = 0, v_t0 = 0;
+        for (int item = blockIdx.x; item < total && live; item = following(item)) {
+            const Record now = next_record();
+            for (int i = 0; i < now.nt && live; ++i) {
+                convert_k(tk++);
+                if (tv + 1 < tk && live) convert_v(it, v_t0, tv++);
+                if (i == 0) it = now;
+                v_t0 = tile_at(now, i) * kTile;
             }
-            --left;
-            convert_k(tk++);
-            return live;
-        };
-        bool more = next_k();
-        it = ahead;
-        int i = 0;
-        for (int t = 0; more; ++t) {
-            const bool also = next_k();  // (may have gone on to the next item)
-            if (!live) break;
-            convert_v(it, tile_at(it, i) * kTile, t);
-            more = also && live;
-            if (++i == it.nt) {
-                it = ahead;
-                i = 0;
-            }
+            // (the record after one without tiles takes the place of one that waits for this V)
+            if (now.nt == 0 && tv < tk && live) convert_v(it, v_t0, tv++);
         }
+        if (tv < tk && live) convert_v(it, v_t0, tv++);
     }
     tc_fence_before();
     __syncthreads();

@@ -102,3 +102,88 @@ def test_bad_lengths_where_tokens_are_cut_into_chunks():
                 assert bool((out[r] == 0).all()) and bool((lse[r] == -float("inf")).all())
             else:
                 assert t.equal(out[r], want[r])
+
+
+@pytest.mark.parametrize("fmt,dim,page", [("f16", 64, 16), ("q8_0", 128, 64)])
+def test_more_sequences_than_threads(fmt, dim, page):
+    rng = np.random.default_rng(3)
+    large(fmt, dim, page, rng.integers(0, 130, 950).tolist(), rng.integers(0, 3, 950).tolist(), 4, 2, 60, 2, 35)
+
+
+@pytest.mark.parametrize("fmt,dim", [("q8_0", 128), ("bf16", 64), ("f16", 256)])
+def test_order_of_sequences_changes_no_bits(fmt, dim):
+    """320 items and more: rows of a sequence in any order of lengths, alone, among others, and beside a sequence with
+    too many rows, one with a bad length and rows of none."""
+    t = torch_cuda()
+    rng = np.random.default_rng(4)
+    lens = rng.integers(3, 700, 40).tolist()
+    c = Cache(fmt, lens, 8, dim, 64, seed=36)
+    pool = c.pool.cuda()
+    i32 = lambda v: t.tensor(v, dtype=t.int32, device="cuda")  # noqa: E731
+    row_len = np.array([[int(x) for x in rng.integers(1, n + 1, 3)] for n in lens])  # three rows each
+    q = queries(c, 123, 16).cuda()
+
+    def call(agent_rows, lengths, rows):
+        plan = c.plan(16, 123, 3)
+        out, lse = t.full((rows, 16, dim), 7.0, device="cuda"), t.full((rows, 16), 7.0, device="cuda")
+        plan.attend_window(pool, i32(agent_rows), i32(lengths), q[:rows], out, window=200, sinks=3, lse=lse)
+        return out, lse, plan.error()
+
+    every = [3 * a for a in range(41)]
+    out, lse, err = call(every, row_len.reshape(-1).tolist(), 120)
+    assert err == 0 and bool(t.isfinite(lse).all())
+    for a in (0, 17, 39):  # alone, its rows where they were
+        o, s, err = call([3 * a if b <= a else 3 * a + 3 for b in range(41)], row_len.reshape(-1).tolist(), 120)
+        assert err == 4  # (the other rows are no sequence's)
+        assert t.equal(o[3 * a:3 * a + 3], out[3 * a:3 * a + 3]) and t.equal(s[3 * a:3 * a + 3], lse[3 * a:3 * a + 3])
+        assert bool((o[:3 * a] == 0).all()) and bool((o[3 * a + 3:] == 0).all())
+    # sequence 5 loses its rows to sequence 4, which then has six; a row of sequence 9 is longer than the table; three rows are no sequence's
+    bad = every.copy()
+    bad[5] = 18
+    lengths = row_len.reshape(-1).tolist() + [5, 5, 5]
+    lengths[28] = c.cap + 1
+    o, s, err = call(bad, lengths, 123)
+    assert err == 4
+    for r in range(123):
+        if 12 <= r < 18 or r == 28 or r >= 120:
+            assert bool((o[r] == 0).all()) and bool((s[r] == -float("inf")).all())
+        else:
+            assert t.equal(o[r], out[r]) and t.equal(s[r], lse[r]), r
+
+
+@pytest.mark.parametrize("fmt,dim", [("q8_0", 128), ("f16", 64), ("f16", 128), ("bf16", 256)])
+@pytest.mark.parametrize("agents,rows", [(80, 2), (950, 1), (12, 400)])
+def test_items_without_tokens(fmt, dim, agents, rows):
+    """Blocks whose items have no token in turn, between others: rows of length 0 (whole sequences, or runs of rows)."""
+    t = torch_cuda()
+    rng = np.random.default_rng(5)
+    kvh, heads, cap = 4, 8, 128
+    c = Cache(fmt, [cap] * agents, kvh, dim, 64, seed=37)
+    i32 = lambda v: t.tensor(v, dtype=t.int32, device="cuda")  # noqa: E731
+    n = agents * rows
+    ar = [rows * a for a in range(agents + 1)]
+    lens = rng.integers(1, cap + 1, (agents, rows))
+    q = queries(c, n, heads).cuda()
+    pool = c.pool.cuda()
+
+    def call(lengths):
+        plan = c.plan(heads, n, rows)
+        out, lse = t.full((n, heads, dim), 7.0, device="cuda"), t.full((n, heads), 7.0, device="cuda")
+        plan.attend_window(pool, i32(ar), i32(lengths.reshape(-1).tolist()), q, out, window=100, sinks=3, lse=lse)
+        assert plan.error() == 0
+        return out, lse
+
+    out, lse = call(lens)
+    for empty in (rng.random(agents) < 0.5, rng.random(agents) < 0.95, np.arange(agents) % 2 == 0, np.arange(agents) >= agents // 2):
+        some = lens.copy()
+        if rows > 2:  # runs of rows
+            for a in range(agents):
+                at = int(rng.integers(0, rows))
+                some[a, :at] = 0 if empty[a] else some[a, :at]
+                some[a, at:] = some[a, at:] if empty[a] else 0
+        else:
+            some[empty] = 0
+        o, s = call(some)
+        none = torch.from_numpy(some.reshape(-1) == 0).cuda()
+        assert bool((o[none] == 0).all()) and bool((s[none] == -float("inf")).all())
+        assert t.equal(o[~none], out[~none]) and t.equal(s[~none], lse[~none])
