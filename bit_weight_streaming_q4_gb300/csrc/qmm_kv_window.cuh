@@ -1195,20 +1195,32 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
                 mbar_arrive(rempty + G::raw_slots + rs);
             }
         };
-        Record it;  // V's item
-        int tk = 0, tv = 0, v_t0 = 0;
-        for (int item = blockIdx.x; item < total && live; item = following(item)) {
-            const Record now = next_record();
-            for (int i = 0; i < now.nt && live; ++i) {
-                convert_k(tk++);
-                if (tv + 1 < tk && live) convert_v(it, v_t0, tv++);
-                if (i == 0) it = now;
-                v_t0 = tile_at(now, i) * kTile;
+        Record ahead, it;  // K's item and V's
+        ahead.nt = it.nt = 0;
+        int item = blockIdx.x, tk = 0, tv = 0, left = 0, i = 0;
+        for (;;) {
+            if (left == 0 && item < total) {
+                ahead = next_record();
+                item = following(item);
+                left = live ? ahead.nt : 0;
             }
-            // (the record after one without tiles takes the place of one that waits for this V)
-            if (now.nt == 0 && tv < tk && live) convert_v(it, v_t0, tv++);
+            const bool also = left > 0;  // a tile's K before the V of the one before it
+            if (also) {
+                convert_k(tk++);
+                --left;
+            }
+            if (!live) break;
+            if (tv + also < tk) {  // (without a K too: the record after an item without tiles takes the place of one that waits for this V)
+                convert_v(it, tile_at(it, i) * kTile, tv++);
+                ++i;
+            } else if (!also && item >= total) {
+                break;
+            }
+            if (i == it.nt) {
+                it = ahead;
+                i = 0;
+            }
         }
-        if (tv < tk && live) convert_v(it, v_t0, tv++);
     }
     tc_fence_before();
     __syncthreads();
