@@ -72,14 +72,14 @@ qmm_status check(const qmm_kv_dims* d, int64_t max_rows, int32_t window, int32_t
 
 // How a plan's calls are laid out, by its dims alone (so that a row's bits are those of any other call).  Tokens are cut
 // into the chunks whose rounds of items take least time by this estimate, or not at all: 4 sequences of 23,000 with a window
-// of 4,096 at q8_0, 3 rows each, take 44 us in chunks of 1,408, 93 as 32 whole windows.
+// of 4,096 at q8_0, 3 rows each, take 45 us in chunks of 1,408, 93 as 32 whole windows.
 struct Layout {
     int32_t decode, qt, chunk, slots;
     int64_t o, bytes;
 };
 Layout layout(const qmm_kv_dims& d, int64_t max_rows, int32_t window, int32_t sinks) {
     constexpr int64_t kSms = 152;   // of a GB300
-    constexpr double kItem = 7;     // an item's start and end, in the time of a tile of tokens: 15,000 and 2,200 clocks
+    constexpr double kItem = 7;     // an item's start and end, in the time of a tile of tokens: 15,000 and 2,200 clocks (2 to 20 choose alike there)
     constexpr double kJoin = 3;     // the second kernel
     const int64_t cap = int64_t{d.max_pages} * d.page_tokens, q = int64_t{d.max_agent_rows} * (d.heads / d.kv_heads);
     const int64_t tile = 128;

@@ -32,12 +32,12 @@
 //     A score product of 64 columns takes the tensor cores as long as one of 128 (it reads as much of Q): 1,520 clocks of
 //     products per tile and two streams, of the 1,770 that a tile takes; the rest are the items' starts and ends, of which
 //     384 items on 152 blocks make 2.53 rounds.
-//   decode steps, q8_0, 4 x 23,000 tokens, 3 rows, 35 MB: 44 us (one slot of converted V: 55).  The conversion's chain, 600
+//   decode steps, q8_0, 4 x 23,000 tokens, 3 rows, 35 MB: 45 us (one slot of converted V: 55).  The conversion's chain, 600
 //     clocks for a tile's K and 1,150 for its V with the waits for their slots.  Both are two fp16 parts; one for V
 //     would halve its products but lose 2^-11 of V.
-//   decode steps, bf16, 61 ragged sequences to 4,099, 32 heads over 8 of 64, window 1,024, 113 MB: 57 us, 2.0 TB/s.  A tile's
-//     chain of roles and an item's start and end (15,000 clocks, the time of 7 tiles).
-//   prompts, q8_0, 4 x 524 rows, window 1,024: 132 us; bf16, 3 x 777 rows, 8 heads over 2 of 256, no window: 51 us.
+//   decode steps, bf16, 61 ragged sequences to 4,099, 32 heads over 8 of 64, window 1,024, 113 MB: 47 us, 2.4 TB/s.  A tile's
+//     chain of roles (2,100 clocks a stream) and an item's start and end (6,000 of its 24,000 clocks, 16,000 for the first).
+//   prompts, q8_0, 4 x 524 rows, window 1,024: 136 us; bf16, 3 x 777 rows, 8 heads over 2 of 256, no window: 51 us.
 // Measured and not taken, for the fp16 prompt: tiles of 128 tokens with one product of 128 columns, whose halves two
 // threads take (242 us: one buffer of scores); those threads with a vote on the reference (255 to 263); streams that take
 // strict turns (255); 64 scores of a thread kept across the two passes (386: registers spill); V tiles asked for by a warp
@@ -273,9 +273,10 @@ __device__ __forceinline__ Chunks chunks_of(const Params& p, int n) {
 
 // The table of sequences, the same in every block, one more entry at the end; returns the number of items.  With chunks
 // seq[a] = (first item, chunks of the first slots, the window's first chunk, first row).  Without, entries are (first
-// item, rows, sequence, first row); where blocks have several items, longer sequences come first, and blocks take items
-// there and back (following()), so that the last round has the shortest: 61 ragged sequences of up to 4,099 tokens, 488 items, took
-// 57 us in the order of the call.  (The ranks are counted, a thread a sequence, up to as many as the block has threads.)
+// item, rows, sequence, first row); where blocks have several items, longer sequences come first, and in decode steps
+// blocks take items there and back (following()), so that the last round has the shortest: 61 ragged sequences of up to
+// 4,099 tokens, 488 items, take 47 us, 57 in the order of the call.  (The ranks are counted, a thread a sequence, up to as
+// many as the block has threads.)
 // tmp: 33 ints.  qt: queries of an item.  Without chunks also writes the rows that no item has.
 __device__ __forceinline__ int form_table(const Params& p, int4* seq, int* tmp, int qt) {
     const int tid = threadIdx.x, n_threads = blockDim.x;
@@ -545,8 +546,9 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
         live = __all_sync(0xffffffffu, live);
     };
     int k = 0;  // items so far
-    // the block's next item, k being the items up to this one: there and back in the table's order, or with chunks in turns
-    auto following = [&](int item) { return p.chunk ? item + static_cast<int>(gridDim.x) : 2 * k * static_cast<int>(gridDim.x) - 1 - item; };
+    // the block's next item, k being the items up to this one: there and back in the table's order; in turns for chunks and
+    // prompts, whose items differ less (4 x 524 rows of q8_0: 136 us, 139 there and back)
+    auto following = [&](int item) { return p.chunk || !DEC ? item + static_cast<int>(gridDim.x) : 2 * k * static_cast<int>(gridDim.x) - 1 - item; };
     // the next item's record
     auto next_record = [&]() -> Record {
         await(ifull + (k & 1), (k >> 1) & 1);
