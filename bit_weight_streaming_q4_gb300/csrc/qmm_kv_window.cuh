@@ -57,7 +57,11 @@ using namespace qmm::kv;
 constexpr float kShift = 9.f;       // p's power of two ..
 constexpr float kSlack = 6.f;       // .. and how far a score may pass its reference: p <= 2^15
 constexpr int kTile = 64;           // tokens of a tile
-constexpr float kFine = 4194304.f;  // 2^22: a larger reference stands alone (fp32's spacing would swallow the two): p <= 1
+// From 2^22 on fp32's spacing swallows the two, and the product of a score and the scale is off by more than an exponent can
+// be (16 from 2^28 on: p would leave 16 bits).  A reference past it is kept as the score that it is, which comes off before the
+// scale: the largest one's exponent is 0, and p <= 1.  Below, an exponent is the unrounded product less the reference, which is
+// off by 1/8 at most.
+constexpr float kFine = 4194304.f;
 
 struct Params {
     const uint8_t* pool;
@@ -871,7 +875,11 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(qfull + s);
             }
-            float l = 0.f, lim = -INFINITY, base = 0.f;  // sum, reference and slack, what comes off the scores
+            // Sum, reference and slack, what is added to the scaled scores.  A reference past kFine: ref is the score that it is,
+            // shift 0, and lim stays -infinity, so that each tile goes the way of one that moves its reference, where ref comes off
+            // the scores (others do not pay for the case: 217 us for the 2,048-row prompt either way, 229 with a test in each tile).
+            float l = 0.f, lim = -INFINITY, shift = 0.f, ref = 0.f;
+            auto level = [&] { return ref != 0.f ? ref * p.c2 : -shift; };  // what the exponents are relative to
             bool fresh = true;                           // O holds nothing yet
             const int na = it.na;
             int tile = na ? it.a0 : it.b0;
@@ -886,7 +894,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
                 const int vi = tiles % G::v_told;
                 if (some) await(vready + vi, (tiles / G::v_told) & 1);  // (which tokens' V is not finite)
                 if (!live) break;
-                float v[kTile], m = -INFINITY;
+                float v[kTile], top = -INFINITY, m = -INFINITY;  // scores, the largest, and the same times the scale
                 const int miss = kmiss_sm[tiles & 15];
                 if (!idle) {
                     tc_fence_after();
@@ -915,18 +923,24 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) m8[i] = fmaxf(m8[i], fmaxf(v[j + i], v[j + i + 8]));
                     // (a NaN is no maximum)
-                    m = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))) * p.c2;
+                    top = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
+                    m = top * p.c2;
                 }
                 if (__any_sync(0xffffffffu, m > lim)) {
-                    const bool passed = m > lim;
+                    const bool passed = ref != 0.f ? top > ref : m > lim;
                     float alpha = 1.f;
                     if (passed) {
-                        const bool fine = fabsf(m) < kFine;
-                        const float to = fine ? m - kShift : m;
-                        alpha = lim == -INFINITY ? 0.f : ex2(base - to);
-                        base = to;
-                        lim = fine ? m + kSlack : m;
+                        const bool fine = fabsf(m) < kFine, had = lim > -INFINITY || ref != 0.f;
+                        alpha = had ? ex2(level() - (fine ? m - kShift : m)) : 0.f;
+                        shift = fine ? kShift - m : 0.f;
+                        ref = fine ? 0.f : top;
+                        lim = fine ? m + kSlack : -INFINITY;
                         l *= alpha;
+                    }
+                    if (__any_sync(0xffffffffu, ref != 0.f)) {
+                        const uint64_t r2 = pair(-ref, -ref);
+#pragma unroll
+                        for (int j = 0; j < kTile; j += 2) unpair(add2(pair(v[j], v[j + 1]), r2), v[j], v[j + 1]);
                     }
                     if (!fresh) {
                         // (the last product may be under way; the one before was over before these scores were asked for)
@@ -953,7 +967,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
                 if (fresh && me == 0) accum_sm[s] = odd != 0;
                 if (!idle) {
                     uint64_t sum[2] = {0, 0};  // pairs of fp32
-                    const uint64_t c2 = pair(p.c2, p.c2), off = pair(-base, -base);
+                    const uint64_t c2 = pair(p.c2, p.c2), off = pair(shift, shift);
 #pragma unroll
                     for (int i = 0; i < kTile; i += 32) {
                         const int c = 32 - i;  // (the upper scores first)
@@ -998,6 +1012,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
             tc_fence_after();
 
             // ---- what became of the item
+            float base = level();
             float w0 = 1.f, w1 = 0.f;  // the streams' weights
             const bool merge = NS == 2 && DEC;
             if (merge) {  // the streams' softmaxes have the same lanes of tensor memory: each takes half of both's dims
