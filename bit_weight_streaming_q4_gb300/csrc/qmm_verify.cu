@@ -17,6 +17,8 @@
 // fp32's rate here: with powers in fp64 4 x 3 rows took 76 us.
 #include <cooperative_groups.h>
 
+#include <utility>
+
 #include "qmm_decode.h"
 #include "qmm_kv.cuh"
 
@@ -335,6 +337,8 @@ __global__ void __launch_bounds__(kChoose) verify_choose(const Params p) {
     __shared__ uint64_t share[kMaxRanks];      // the blocks' sums (each block's own copy)
     __shared__ uint64_t part[kMaxSteps * kChooseWarps];
     cg::cluster_group cluster = cg::this_cluster();
+    // (the other blocks' shared memory is there once they have started: said here, waited for behind the drafts)
+    cg::cluster_group::arrival_token started = cluster.barrier_arrive();
     const int rank = static_cast<int>(cluster.block_rank()), ranks = p.ranks, a = blockIdx.x / ranks;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     bool falls = false;
@@ -348,6 +352,7 @@ __global__ void __launch_bounds__(kChoose) verify_choose(const Params p) {
     const bool bad = falls || r0 < 0 || r1 > p.rows;
     if (bad && tid == 0 && rank == 0) atomicOr(p.err, kv::kErrRange);
     if (bad || r1 <= r0) {
+        cluster.barrier_wait(std::move(started));
         if (tid == 0 && rank == 0) p.accepted[a] = 0, p.token[a] = -1;
         return;  // (the whole cluster)
     }
@@ -422,6 +427,7 @@ __global__ void __launch_bounds__(kChoose) verify_choose(const Params p) {
         if (lane == 0) choice = c;
     }
     __syncthreads();
+    cluster.barrier_wait(std::move(started));
     const Choice c = choice;
     const bool nothing = c.p.odd || c.p.m == -INFINITY;
     if (greedy || nothing) {
