@@ -209,26 +209,37 @@ __global__ void __launch_bounds__(kThreads, 3) verify_stats(const Params p) {
     __shared__ float max_sm[kWarps];
     __shared__ int best_sm[kWarps];
     __shared__ uint64_t sum_sm[kWarps];
-    __shared__ int first_sm;
+    __shared__ int counts_sm;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     griddep_launch_dependents();
     const int seg = blockIdx.x, row = blockIdx.y;
     const bool draft = blockIdx.z == 1;
     const T* base = draft ? static_cast<const T*>(p.draft) + row * p.draft_stride : static_cast<const T*>(p.logits) + row * p.stride;
     const bool vec = draft ? p.draft_vec : p.vec;
+    if (tid == 0) counts_sm = 0;
+    __syncthreads();
+    // the row's sequence (where agent_rows falls there may be several: nobody asks for what comes of it)
+    auto find = [&] {
+        for (int a = tid; a < p.agents; a += kThreads) {
+            const int r0 = p.agent_rows[a];
+            if (r0 <= row && row < p.agent_rows[a + 1] && !(draft && r0 == row)) {
+                const Two scale = scale_of(p, a);
+                scale_sm = scale;
+                counts_sm = !draft || scale.hi != 0.f;
+            }
+        }
+    };
+    // A draft row that does not count (a sequence's first, a greedy one's, one of no sequence) is not read: it may not be there.
+    // A target row is, so it is asked for before its sequence is known.
+    if (draft) {
+        find();
+        __syncthreads();
+        if (!counts_sm) return;
+    }
     float x[kSteps][4];
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) load4<T>(base, vec, seg * kSeg + (i * kThreads + tid) * 4, p.n, x[i]);
-    if (tid == 0) first_sm = 1;
-    __syncthreads();
-    // the row's sequence (where agent_rows falls there may be several: nobody asks for what comes of it)
-    for (int a = tid; a < p.agents; a += kThreads) {
-        const int r0 = p.agent_rows[a];
-        if (r0 <= row && row < p.agent_rows[a + 1] && !(draft && r0 == row)) {
-            scale_sm = scale_of(p, a);
-            first_sm = 0;
-        }
-    }
+    if (!draft) find();
     fill(table);
     // ---- the largest, its lowest column, and whether something is no number
     float m = -INFINITY;
@@ -244,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 3) verify_stats(const Params p) {
     for (int k = 16; k >= 1; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
     if (lane == 0) max_sm[warp] = m;
     odd = __syncthreads_or(odd);
-    if (first_sm) return;
+    if (!counts_sm) return;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) m = fmaxf(m, max_sm[w]);
     const Two scale = scale_sm;
@@ -365,7 +376,7 @@ __global__ void __launch_bounds__(kChoose) verify_choose(const Params p) {
         const int x = p.tokens[r];
         const bool in = x >= 0 && x < p.n;
         // (what the joins do not need is asked for before them)
-        const float xp = in ? as_f32(logits[(r - 1) * p.stride + x]) : 0.f, xq = in && drafts ? as_f32(drafts[r * p.draft_stride + x]) : 0.f;
+        const float xp = in ? as_f32(logits[(r - 1) * p.stride + x]) : 0.f, xq = in && drafts && !greedy ? as_f32(drafts[r * p.draft_stride + x]) : 0.f;
         const float u = p.accept_u[r];
         const Joined tp = join(p, false, r - 1, scale, table);
         Joined tq = tp;

@@ -101,8 +101,8 @@ qmm_status qmm_kv_attend_window(const qmm_kv_dims* dims, const void* pool, const
  * column whose running sum passes sample_u times the sum of all.  So accepted tokens and the next one
  * are distributed as p, whatever q is.
  *  logits:      [rows][n] of `type`, row r at r * stride elements (the lm_head's y); aligned to its element.
- *  draft_logits: the same with draft_stride (a sequence's first row is not read), or null: every q is
- *               1 at its draft (drafts looked up in the text).
+ *  draft_logits: the same with draft_stride (a sequence's first row, the rows of a greedy one and rows of no
+ *               sequence are not read), or null: every q is 1 at its draft (drafts looked up in the text).
  *  agent_rows:  int32 [agents + 1], non-decreasing.  If it falls, or a sequence's rows are not within
  *               0 .. rows, *err_word |= 4 and the sequences concerned (if it falls: all) are as ones without rows.
  *  temperature: fp32 [agents], or null (1).  0 (or less than 2^-100, or NaN) is greedy: a draft is taken if it
