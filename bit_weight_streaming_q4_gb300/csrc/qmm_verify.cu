@@ -573,7 +573,8 @@ cudaError_t launch(const Params& p, int dev, cudaStream_t s) {
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    // (without rows there is no first kernel, and what is read before the wait may come from the caller's kernel before)
+    cfg.numAttrs = p.rows > 0 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, verify_choose<T>, p);
 }
 
