@@ -567,16 +567,14 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
     // a token that no row of the item sees
     auto gone = [&](const Record& it, int t) { return t >= it.hi || (t < it.lo && t >= it.sink_end); };
     const int piece_rows = min(kTile, p.page_tokens), piece_shift = 31 - __clz(piece_rows);
-    // lane i: the page of piece i of a tile, -1 if nobody needs it, -2 if it is outside the pool
+    // lane i: the page of piece i of a tile, -1 if nobody needs it, -2 if it is outside the pool: an error if some row sees it,
+    // which the row's softmax finds (between windows that lie apart entries may hold anything)
     auto page_of = [&](const Record& it, int t0) {
         int pg = -1;
         const int t = t0 + lane * piece_rows;
         if (lane * piece_rows < kTile && t < it.hi && (t + piece_rows > it.lo || t < it.sink_end)) {
             pg = p.table[static_cast<int64_t>(it.a) * p.max_pages + (t >> p.page_shift)];
-            if (pg < 0 || pg >= p.pool_pages) {
-                atomicOr(p.err, kErrPage);
-                pg = -2;
-            }
+            if (pg < 0 || pg >= p.pool_pages) pg = -2;
         }
         return pg;
     };
@@ -904,16 +902,20 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
                     if (some || miss) {
                         // the tokens that the row sees, as bits; a missing piece is 16 tokens at least
                         auto below = [](int j) { return j <= 0 ? 0u : j >= 32 ? ~0u : (1u << j) - 1; };
+                        uint32_t lost = 0;  // .. and those among them whose page is missing
 #pragma unroll
                         for (int i = 0; i < kTile; i += 32) {
                             const int t = t0 + i;
                             uint32_t sees = below(len - t) & (~below(from - t) | below(first - t));
+                            const uint32_t all = sees;
                             if ((miss >> (i >> piece_shift)) & 1) sees &= 0xFFFF0000u;
                             if ((miss >> ((i + 16) >> piece_shift)) & 1) sees &= 0xFFFFu;
+                            lost |= sees ^ all;
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
                                 if (!(sees & (1u << j))) v[i + j] = -INFINITY;
                         }
+                        if (lost) atomicOr(p.err, kErrPage);
                     }
                     float m8[8];
 #pragma unroll

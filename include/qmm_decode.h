@@ -61,7 +61,8 @@ qmm_status qmm_rotate(const qmm_rotate_dims* dims, const void* q, int64_t q_stri
  *     t < n  with  t >= n - window  or  t < sinks.
  * Slots are taken in their order, so this is for caches that are not cut by qmm_kv_evict.  A window of
  * at least max_pages * page_tokens leaves every slot below row_len visible: causal attention of a
- * prompt's rows.  Pages that no row sees are not read, and their page table entries may hold anything.
+ * prompt's rows.  Page table entries of pages that no row sees may hold anything, also between the windows of rows
+ * that lie apart, and set no error; such pages are read there if their entries are in the pool, without effect.
  *  dims:       as for qmm_kv_attend, but max_agent_rows bounds a sequence's rows up to 2^24 / (heads / kv_heads).
  *  max_rows:   upper bound on rows; sizes the workspace.
  *  window >= 1, sinks >= 0.
