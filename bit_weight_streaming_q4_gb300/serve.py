@@ -87,6 +87,9 @@ def _setup():
     _torch = torch
 
 
+_NO_SPACE = (0, 0, None)
+
+
 def _refuse(name, what):
     raise ValueError(f"{name}: {what}")
 
@@ -113,7 +116,7 @@ class KvPlan:
     call, so that layers can share a plan: a uint8 tensor of pool_pages * kv_heads * 17,408 bytes,
     or a 16-bit one of pool_pages * kv_heads * 2 * page_tokens * head_dim elements.
     max_rows / max_agent_rows bound the rows of an attend call, and those of one sequence.
-    Calls of one plan share its workspace: those on different streams have to be ordered by the caller.
+    Calls of one plan share its workspace, whatever their windows: those on different streams have to be ordered by the caller.
     A workspace is allocated at the first call that needs it, as memory of that call's stream, and
     goes back to the allocator behind the work of every stream that calls went to; a stream that is
     handed to a call has to outlive the plan."""
@@ -142,7 +145,7 @@ class KvPlan:
         # (a copy from the host: it is there, on any stream, when the constructor returns)
         self.error_word = _torch.tensor([0], dtype=_i32, device=page_table.device)
         self._err, self._table = self.error_word.data_ptr(), page_table.data_ptr()
-        self._workspace = {}
+        self._workspace, self._windows, self._need = {}, [], {}
         self._streams = {}  # handles of the calls' streams, and the streams as torch knows them
         lib = load()
         self._append, self._attend, self._evict = lib.qmm_kv_append, lib.qmm_kv_attend, lib.qmm_kv_evict
@@ -161,27 +164,44 @@ class KvPlan:
         if stream not in self._streams:
             device = self.page_table.device
             s = _torch.cuda.ExternalStream(stream, device) if stream else _torch.cuda.default_stream(device)
-            for t in [self.error_word] + [w[2] for w in self._workspace.values()]:
+            for t in [self.error_word] + [w[2] for w in (*self._workspace.values(), *self._windows)]:
                 t.record_stream(s)
             self._streams[stream] = s
         return stream
 
     def _space(self, kind: str | tuple, stream: int):
-        """Address and bytes of a kind of call's workspace, allocated for the stream of its first use and kept."""
-        w = self._workspace.get(kind)
-        if w is None:
-            if kind == "evict":
-                n = self._bytes("qmm_kv_evict_workspace_bytes")
-            elif type(kind) is tuple:  # (each window has its own: what a captured graph was given stays)
-                n = self._bytes("qmm_kv_window_workspace_bytes", self.max_rows, *kind[1:])
-            else:
-                n = self._bytes("qmm_kv_attend_workspace_bytes", int(kind == "weights"))
-            # (not for torch's current stream, whose pending work may still use the block that it gets)
-            with _torch.cuda.stream(self._streams[stream]):
-                t = _torch.empty(n, dtype=_torch.uint8, device=self.page_table.device)
-            for s in self._streams.values():
-                t.record_stream(s)
-            w = self._workspace[kind] = (t.data_ptr(), n, t)
+        """Address and bytes of a kind of call's workspace, allocated for the stream of its first use and kept.
+
+        Windows, ("window", window, sinks), share one.  Where it is too small for a call, one of at least twice its size is
+        added, and those before stay, since a captured graph may have been given them: together they hold less than four
+        times what the largest call needs, whatever the number of windows."""
+        windows = type(kind) is tuple
+        if windows:
+            n = self._need.get(kind)
+            if n is None:
+                if len(self._need) == 1024:
+                    self._need.clear()
+                n = self._need[kind] = self._bytes("qmm_kv_window_workspace_bytes", self.max_rows, *kind[1:])
+            w = self._windows[-1] if self._windows else _NO_SPACE
+            if n <= w[1]:
+                return w
+            n = max(n, 2 * w[1])
+        else:
+            w = self._workspace.get(kind)
+            if w is not None:
+                return w
+            n = self._bytes("qmm_kv_evict_workspace_bytes") if kind == "evict" else \
+                self._bytes("qmm_kv_attend_workspace_bytes", int(kind == "weights"))
+        # (not for torch's current stream, whose pending work may still use the block that it gets)
+        with _torch.cuda.stream(self._streams[stream]):
+            t = _torch.empty(n, dtype=_torch.uint8, device=self.page_table.device)
+        for s in self._streams.values():
+            t.record_stream(s)
+        w = (t.data_ptr(), n, t)
+        if windows:
+            self._windows.append(w)
+        else:
+            self._workspace[kind] = w
         return w
 
     def _pool(self, pool) -> int:
