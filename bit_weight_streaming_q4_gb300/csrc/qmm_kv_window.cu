@@ -204,10 +204,11 @@ qmm_status qmm_kv_attend_window(const qmm_kv_dims* dims, const void* pool, const
     p.chunk = l.chunk, p.slots = l.slots;
     p.ml = static_cast<float*>(workspace);
     p.o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + l.o);
-    // (a scale of 0 leaves every finite score within 2^-126 of 0, and -infinity, which marks what a row does not see, as it is)
+    // (fp32's smallest number for a scale of 0: it leaves every finite score within 2^-21 of 0, and -infinity, which marks what a row
+    // does not see, as it is)
     p.flip = scale < 0.f ? 0x80008000u : 0u;
     p.c2 = fabsf(scale) * 1.4426950408889634f;
-    if (p.c2 == 0.f) p.c2 = 1.17549435e-38f;
+    if (p.c2 == 0.f) p.c2 = 1.40129846e-45f;
     // blocks: one per SM, as far as there can be items
     int64_t most = (rows * p.group + l.qt - 1) / l.qt + (dims->agents < rows ? dims->agents : rows);
     most *= int64_t{dims->kv_heads} * (l.chunk ? l.slots + dims->max_agent_rows / l.chunk + 1 : 1);
