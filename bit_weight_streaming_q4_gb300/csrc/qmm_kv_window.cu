@@ -200,7 +200,7 @@ qmm_status qmm_kv_attend_window(const qmm_kv_dims* dims, const void* pool, const
     p.heads = dims->heads, p.kv_heads = dims->kv_heads, p.group = dims->heads / dims->kv_heads, p.agents = dims->agents;
     p.rows = static_cast<int32_t>(rows), p.max_agent_rows = dims->max_agent_rows, p.cap = dims->max_pages * dims->page_tokens;
     p.window = window < p.cap ? window : p.cap, p.sinks = sinks < p.cap ? sinks : p.cap;
-    p.out_type = out_type, p.format = dims->format, p.head_dim = dims->head_dim;
+    p.out_type = out_type, p.head_dim = dims->head_dim;
     p.chunk = l.chunk, p.slots = l.slots;
     p.ml = static_cast<float*>(workspace);
     p.o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + l.o);

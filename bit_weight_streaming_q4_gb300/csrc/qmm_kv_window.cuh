@@ -24,8 +24,8 @@
 //   warps 4 ..  softmax, four a stream
 //   q8_0: four more convert K (half a token a thread) and V (a dim a thread) to two fp16 parts whose sum is quant
 //               times scale
-// A query's reference is its first tile's maximum and moves only when a score passes it by more than 2^kSlack; each
-// query decides for itself.
+// A query's reference is its first tile's maximum and moves only when a score passes it by more than 2^kSlack (past kFine: when
+// one passes it); each query decides for itself.
 //
 // What bounds it (times as a loop of calls, window of 4,096 and 48 query heads over 8 unless given):
 //   prompts, fp16, 2,048 rows at the end of 23,000 tokens, 206 GFLOP: 217 us, 950 TFLOP/s, 0.49 of a library matmul's rate.
@@ -37,7 +37,9 @@
 //     would halve its products but lose 2^-11 of V.
 //   decode steps, bf16, 61 ragged sequences to 4,099, 32 heads over 8 of 64, window 1,024, 113 MB: 47 us, 2.4 TB/s.  A tile's
 //     chain of roles (2,100 clocks a stream) and an item's start and end (6,000 of its 24,000 clocks, 16,000 for the first).
-//   prompts, q8_0, 4 x 524 rows, window 1,024: 136 us; bf16, 3 x 777 rows, 8 heads over 2 of 256, no window: 51 us.
+//   prompts, q8_0, 4 x 524 rows, window 1,024: 138 us; bf16, 3 x 777 rows, 8 heads over 2 of 256, no window: 52 us.  The
+//     first: conversion, and warps that wait for instructions (code that does not run, in the softmax's loop or in other roles,
+//     cost it up to 5 %).
 // Measured and not taken, for the fp16 prompt: tiles of 128 tokens with one product of 128 columns, whose halves two
 // threads take (242 us: one buffer of scores); those threads with a vote on the reference (255 to 263); streams that take
 // strict turns (255); 64 scores of a thread kept across the two passes (386: registers spill); V tiles asked for by a warp
@@ -76,7 +78,7 @@ struct Params {
     int* err;
     int64_t q_stride;
     int32_t max_pages, pool_pages, page_shift, page_tokens, heads, kv_heads, group, agents, rows, max_agent_rows, cap;
-    int32_t window, sinks, out_type, format, head_dim;
+    int32_t window, sinks, out_type, head_dim;
     int32_t chunk;   // tokens per chunk, a multiple of 128; 0: one item has all of a query's tokens and writes its output
     int32_t slots;   // partials per (row, head)
     uint32_t flip;   // sign bits that a negative scale puts on the queries
@@ -551,7 +553,7 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
     };
     int k = 0;  // items so far
     // the block's next item, k being the items up to this one: there and back in the table's order; in turns for chunks and
-    // prompts, whose items differ less (4 x 524 rows of q8_0: 136 us, 139 there and back)
+    // prompts, whose items differ less (4 x 524 rows of q8_0: 2 % more there and back)
     auto following = [&](int item) { return p.chunk || !DEC ? item + static_cast<int>(gridDim.x) : 2 * k * static_cast<int>(gridDim.x) - 1 - item; };
     // the next item's record
     auto next_record = [&]() -> Record {
@@ -985,6 +987,8 @@ __global__ void __launch_bounds__(Geo<FMT, D, DEC>::threads, 1)
 #pragma unroll
                             for (int j = 0; j < 8; j += 2) {
                                 sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], pair(e[j], e[j + 1]));
+                                // (one rounding to 16 bits, 2^-11 or bf16's 2^-8 of a probability, as V's own elements have: a second part
+                                // would double the second product, half of the tensor cores' time in prompts; the sum is of fp32)
                                 w[(g + j) / 2] = pack2<BF>(e[j], e[j + 1]);
                             }
                         }

@@ -11,7 +11,7 @@
 //     the blocks exchange their sums, and the one in whose share the number falls looks for the column.
 // What bounds it: instructions in the first kernel, some 60 for a weight (its power of two as a pair of fp32 from a table
 // of 64 and a series, the pair's 46 bits made an integer), so that 8 sequences of 8 rows of 151,936 fp32 logits with a draft
-// model's, 73 MB, take 73 us where the bytes alone would take 11; latencies in the second, about 15 us whatever the size (the
+// model's, 73 MB, take 70 us where the bytes alone would take 11; latencies in the second, about 15 us whatever the size (the
 // rows' numbers, the joins, the row's share again, an exchange in the cluster, the search).  4 x 3 rows: 34 us; 33 x 5 rows of
 // 32,001 bf16 logits without a draft model: 33 us.  64-bit floating point and conversions of integers run at 1/64 and 1/8 of
 // fp32's rate here: with powers in fp64 4 x 3 rows took 76 us.

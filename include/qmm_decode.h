@@ -63,7 +63,10 @@ qmm_status qmm_rotate(const qmm_rotate_dims* dims, const void* q, int64_t q_stri
  * at least max_pages * page_tokens leaves every slot below row_len visible: causal attention of a
  * prompt's rows.  Page table entries of pages that no row sees may hold anything, also between the windows of rows
  * that lie apart, and set no error; such pages are read there if their entries are in the pool, without effect.
- *  dims:       as for qmm_kv_attend, but max_agent_rows bounds a sequence's rows up to 2^24 / (heads / kv_heads).
+ *  dims:       as for qmm_kv_attend, but max_agent_rows bounds a sequence's rows up to 2^24 / (heads / kv_heads).  The
+ *              kernel follows from them, not from a call's rows: at most 128 rows times heads / kv_heads are a decode step's.
+ *              Decode steps called with a prompt's max_agent_rows are right but slower (Q8_0, 4 sequences of 23,000, 3 rows:
+ *              94 us with a max_agent_rows of 524, 45 with 3): a program that does both has dims for each.
  *  max_rows:   upper bound on rows; sizes the workspace.
  *  window >= 1, sinks >= 0.
  *  agent_rows, row_len, q, q_stride, out, out_type, lse, err_word: as for qmm_kv_attend.  Rows of no
@@ -77,8 +80,8 @@ qmm_status qmm_rotate(const qmm_rotate_dims* dims, const void* q, int64_t q_stri
  * it, NaN and infinity included; a row that sees a score that is NaN has NaN throughout, and an element of V that is not finite
  * makes that element of out not finite (infinite or NaN) for the rows that see it.
  * A page table entry outside the pool (error word 2) takes its page's tokens out of the softmax.
- * Scores, softmax and sums are fp32.  A probability enters the product with V rounded once to the pool's 16-bit
- * type (Q8_0: fp16), relative to the row's largest one; Q8_0's K and V are sums of two fp16 parts (quant times scale
+ * Scores, softmax and sums are fp32, whatever the scores' size.  A probability enters the product with V rounded once to the
+ * pool's 16-bit type (Q8_0: fp16), relative to the row's largest one (qmm_kv_attend keeps two parts of it); Q8_0's K and V are sums of two fp16 parts (quant times scale
  * without error, down to 2^-25).  An element of a Q8_0 pool is at most 65,504 in magnitude: a larger one of V counts
  * as not finite, one of K makes the rows that see it NaN.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, SCRATCH_TOO_SMALL, NO_DEVICE, CUDA.
