@@ -118,10 +118,12 @@ qmm_status qmm_kv_attend_window(const qmm_kv_dims* dims, const void* pool, const
  *               Rows of no sequence are left as they are.
  * -infinity is a column of probability 0.  A row of logits with a NaN, with +infinity or with nothing but
  * -infinity has no distribution: its draft is refused (prob NaN, 0 for the last kind), and a next token from it is -1.  A row of
- * draft_logits without one: the draft is refused (prob NaN), and the next token is drawn from p.  A draft outside
- * 0 .. n - 1 is refused (prob 0).  A sequence without rows: accepted 0, token -1.
+ * draft_logits without one: the draft is refused (prob NaN, whatever its row of logits), and the next token is drawn from p.
+ * A draft outside 0 .. n - 1 is refused (prob 0).  A sequence without rows: accepted 0, token -1.
  * Probabilities are formed to 2^-38 and summed exactly in 64-bit fixed point (a column of less than 2^-45 of the
- * row's largest counts as 0), so what is drawn does not depend on the order of a sum.  n is at most 2^19.
+ * row's largest counts as 0), so what is drawn does not depend on the order of a sum.  Where that leaves nothing of
+ * max(p - q, 0), the next token is drawn from p.  A draft is judged by all the bits of its p and q, down to 2^-1000 of the row's
+ * largest, below which they count as 0.  n is at most 2^19.
  *  workspace:   16-byte aligned, at least qmm_verify_workspace_bytes bytes, in use until the call's kernels finish.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, SCRATCH_TOO_SMALL, NO_DEVICE, CUDA.
  */
