@@ -31,7 +31,7 @@ def many_bits(fmt, rows, heads, dim):
 def check_ties(fmt, dim, sign, rows, heads, n, at, power, window=None, sinks=0, chunks=None):
     c = Cache(fmt, (n,), 1, dim, seed=40)
     for t in range(n):
-        set_key(c, t, {1: 384.0 if t > 1 else 448.0, -1: -4096.0 if t > 1 else -3072.0}[sign])
+        set_key(c, t, {1: 384.0 if t > 1 else 448.0, -1: -4096.0 if t > 1 else -2560.0}[sign])
     for t in at:
         set_key(c, t, sign * 1024.0)
     k, v = c.values()

@@ -19,7 +19,7 @@ def setup(seed):
 
 
 def test_windows_that_grow():
-    """A window of its own for each step: before, an allocation each, kept as long as the plan."""
+    """A window of its own for each step: hundreds under one plan."""
     t, c, plan, args, q, out = setup(60)
     windows = list(range(300, 20000, 61))
     need = max(plan._bytes("qmm_kv_window_workspace_bytes", 2, w, s) for w in windows for s in (0, 3))
